@@ -211,6 +211,39 @@ int swiftkv_decode_step(swiftkv_model* m, const int32_t* tokens, const int32_t* 
                         int batch, const swiftkv_kv_pages* kv, float* logits,
                         int32_t* next_tokens, swiftkv_stream stream);
 
+/* How swiftkv_sample draws. Each setting is a device array with one value per row, or NULL and
+ * one value for all rows in the *_all field. Order and meaning, with w_i = exp((l_i - max l) / T):
+ *   temperature T <= 0 or NaN: the argmax, lowest id on ties (u and the rest are not used)
+ *   top_k    the first k ids by (logit descending, id ascending); <= 0 or >= vocab: off
+ *   top_p    of those, the ids with less than top_p of their mass before them in that order
+ *            (the first always stays); >= 1 or NaN: off
+ *   min_p    of those, the ids with w_i >= min_p (the largest w is 1; above 1 counts as 1);
+ *            <= 0 or NaN: off */
+typedef struct {
+  const float* temperature;
+  const int32_t* top_k;
+  const float* top_p;
+  const float* min_p;
+  float temperature_all;
+  int32_t top_k_all;
+  float top_p_all;
+  float min_p_all;
+} swiftkv_sampling;
+
+/* Draws one token per row of logits, next to the greedy choice of swiftkv_decode_step: the
+ * lowest kept id whose running sum of kept weights, ids ascending, exceeds u times their total.
+ *   logits  device float [rows][ld], the first `vocab` of each row (ld >= vocab, any alignment of
+ *           4 bytes); NaN counts as -inf, and a row without any logit above -inf gives id 0
+ *   u       device float [rows] in [0, 1): the caller's random numbers (below 0 or NaN: 0; from 1
+ *           on: the largest float below 1)
+ *   tokens  device int32 [rows]
+ * Weights are 44-bit fixed-point numbers, within 2^-40 of their value, and every sum is exact, so
+ * a row's token depends on nothing but its own logits, settings and u. Needs no model and no
+ * workspace: calls on several streams may overlap, and a call can be captured into a CUDA graph
+ * (the arrays are read at each replay). vocab up to 360448, else SWIFTKV_EUNSUPPORTED. */
+int swiftkv_sample(const float* logits, int rows, int vocab, long long ld, const swiftkv_sampling* settings,
+                   const float* u, int32_t* tokens, swiftkv_stream stream);
+
 /* Reads (synchronously) the device status word; clears it when clear != 0.
  * Returns the swiftkv_status_bits that are set, or a negative swiftkv_error. */
 int swiftkv_status(swiftkv_model* m, int clear);

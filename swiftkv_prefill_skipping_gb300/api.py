@@ -231,3 +231,44 @@ def decode_step(model: Model, tokens: torch.Tensor, seq_lens: Sequence[int], kv:
     B.check(B.lib().swiftkv_decode_step(model.handle, tokens.data_ptr(), sl.ctypes.data, Bsz, C.byref(kv.pages),
                                         logits.data_ptr(), nxt.data_ptr(), _stream(stream)))
     return logits, nxt
+
+
+def _need(cond: bool, msg: str) -> None:
+    if not cond:
+        raise ValueError(msg)
+
+
+def sample(logits: torch.Tensor, u: torch.Tensor, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0,
+           out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """One token id (int32) per row of float32 logits [P, V] (rows may be strided), drawn with the
+    uniform numbers u [P] in [0, 1). temperature, top_k, top_p and min_p are numbers, or one value
+    per row as tensors on the same device (float32; top_k int32); temperature <= 0 takes the argmax,
+    top_k <= 0, top_p >= 1 and min_p <= 0 are off. Enqueued without synchronising."""
+    _need(logits.dim() == 2 and logits.dtype == torch.float32 and logits.is_cuda, "logits: float32 CUDA [P, V]")
+    P, V = logits.shape
+    _need(V >= 1, "logits need at least one column")
+    _need(V == 1 or logits.stride(1) == 1, "logits: the columns of a row must be contiguous")
+    ld = logits.stride(0) if P > 1 else max(V, logits.stride(0))
+    _need(ld >= V, "logits: rows must not overlap")
+    dev = logits.device
+
+    def rows(t, dtype, name):
+        _need(t.device == dev and t.dtype == dtype and t.shape == (P,) and t.is_contiguous(),
+              f"{name}: contiguous {dtype} [{P}] on {dev}")
+        return t.data_ptr()
+
+    s = B.Sampling()
+    for name, value, dtype in (("temperature", temperature, torch.float32), ("top_k", top_k, torch.int32),
+                               ("top_p", top_p, torch.float32), ("min_p", min_p, torch.float32)):
+        if isinstance(value, torch.Tensor):
+            setattr(s, name, rows(value, dtype, name))
+        else:
+            setattr(s, name + "_all", int(value) if dtype == torch.int32 else float(value))
+    if out is None:
+        out = torch.empty((P,), dtype=torch.int32, device=dev)
+    rows(out, torch.int32, "out")
+    st = stream if stream is not None else torch.cuda.current_stream(dev)
+    with torch.cuda.device(dev):
+        B.check(B.lib().swiftkv_sample(logits.data_ptr(), P, V, ld, C.byref(s), rows(u, torch.float32, "u"),
+                                       out.data_ptr(), st.cuda_stream))
+    return out

@@ -26,7 +26,7 @@ STATUS_TIMEOUT = 4
 # every symbol include/swiftkv.h declares
 EXPORTS = ("swiftkv_cache_count", "swiftkv_model_create", "swiftkv_load_layer", "swiftkv_load_globals",
            "swiftkv_load_weights", "swiftkv_prefill", "swiftkv_prefill_host", "swiftkv_forward",
-           "swiftkv_decode_step",
+           "swiftkv_decode_step", "swiftkv_sample",
            "swiftkv_status", "swiftkv_memory", "swiftkv_set_gemm_impl", "swiftkv_set_attention_impl",
            "swiftkv_set_norm_fusion", "swiftkv_set_rows_impl", "swiftkv_gemm_bf16",
            "swiftkv_gemm_skinny_noalloc", "swiftkv_selftest_wait_timeout",
@@ -65,6 +65,12 @@ class KVPages(C.Structure):
                 ("k_scale", C.POINTER(C.c_void_p)), ("v_scale", C.POINTER(C.c_void_p))]
 
 
+class Sampling(C.Structure):
+    _fields_ = [("temperature", C.c_void_p), ("top_k", C.c_void_p), ("top_p", C.c_void_p), ("min_p", C.c_void_p),
+                ("temperature_all", C.c_float), ("top_k_all", C.c_int), ("top_p_all", C.c_float),
+                ("min_p_all", C.c_float)]
+
+
 class ProfileEntry(C.Structure):
     _fields_ = [("name", C.c_char * 32), ("calls", C.c_int), ("kernels", C.c_int), ("ms", C.c_double),
                 ("flops", C.c_double), ("bytes", C.c_double)]
@@ -88,6 +94,7 @@ def lib(path: str | None = None):
             L.swiftkv_prefill_host.argtypes = [vp, vp, vp, i, i, i, C.POINTER(KVPages), vp, vp]
             L.swiftkv_forward.argtypes = [vp, vp, vp, vp, i, i, i, C.POINTER(KVPages), vp, vp]
             L.swiftkv_decode_step.argtypes = [vp, vp, vp, i, C.POINTER(KVPages), vp, vp, vp]
+            L.swiftkv_sample.argtypes = [vp, i, i, C.c_longlong, C.POINTER(Sampling), vp, vp, vp]
             L.swiftkv_status.argtypes = [vp, i]
             L.swiftkv_memory.argtypes = [vp, C.POINTER(sz), C.POINTER(sz)]
             L.swiftkv_set_gemm_impl.argtypes = [vp, i]
