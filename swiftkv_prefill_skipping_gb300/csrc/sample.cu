@@ -39,7 +39,7 @@ constexpr int ST = 512;            // threads per CTA
 constexpr int SWARPS = ST / 32;
 constexpr int NB = 1024;           // histogram bins
 constexpr int TAB = 256;           // 2^(j / TAB) table
-constexpr int FX = 44;             // fixed-point weights: w * 2^FX
+constexpr int FX = 44;             // fixed-point weights: w * 2^FX (360448 of them, times 2^(1/256), stay below 2^63)
 constexpr int kMaxSlice = 45056;   // floats of a row one CTA holds (176 KB)
 constexpr int kMaxVocab = 8 * kMaxSlice;
 
@@ -77,22 +77,19 @@ __device__ constexpr Pow2Table kPow2 = Pow2Table();
 
 // Shared-memory state of one CTA (ahead of its slice); the cluster's other CTAs read it.
 struct alignas(16) Share {  // the slice behind it is written 16 bytes at a time
-  u64 mass[NB];                 // this CTA's bin masses
+  u64 mass[NB];                 // this CTA's bins
   u64 tab[TAB];
-  unsigned limb[3][NB];         // 16-bit limbs of the bin masses while they are summed
-  unsigned cnt[NB];             // bin counts
+  unsigned limb[3][NB];         // 16-bit limbs of the bins while they are summed
   u64 warp_mass[SWARPS];
-  unsigned warp_cnt[SWARPS];
   float red_f[SWARPS];
   unsigned red_a[SWARPS], red_b[SWARPS];
-  // exchanged between the CTAs
+  // read by the cluster's other CTAs
   float x_max;
-  unsigned x_idx, x_kmin, x_kmax, x_ties;
+  unsigned x_kmin, x_kmax, x_ties;
   u64 x_mass;
-  // rank 0's decisions
+  // the bin that a search found
   int d_bin;
-  u64 d_before_mass;
-  unsigned d_before_cnt, d_in_cnt;
+  u64 d_before;
 };
 
 __device__ __forceinline__ unsigned cluster_rank() {
@@ -103,6 +100,7 @@ __device__ __forceinline__ unsigned cluster_rank() {
 __device__ __forceinline__ void cluster_barrier() {
   asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+// The same shared variable in CTA `rank` of the cluster.
 template <typename T>
 __device__ __forceinline__ uint32_t remote(const T* p, unsigned rank) {
   uint32_t r;
@@ -113,9 +111,6 @@ __device__ __forceinline__ unsigned ld_remote(const unsigned* p, unsigned rank) 
   unsigned v;
   asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(remote(p, rank)) : "memory");
   return v;
-}
-__device__ __forceinline__ int ld_remote(const int* p, unsigned rank) {
-  return (int)ld_remote(reinterpret_cast<const unsigned*>(p), rank);
 }
 __device__ __forceinline__ float ld_remote(const float* p, unsigned rank) {
   return __uint_as_float(ld_remote(reinterpret_cast<const unsigned*>(p), rank));
@@ -136,88 +131,99 @@ __device__ __forceinline__ float value_of(unsigned key) {
   return __uint_as_float(key & 0x80000000u ? key & 0x7fffffffu : ~key);
 }
 
-// The row's exponent scale log2(e) / T as a pair of floats.
+// How a row's logits become exponents: c = log2(e) / T as a pair of floats, and a reference
+// exponent near m c on the 1/256 grid. All weights of a row are scaled by the one factor
+// 2^(m c - ref), which no comparison sees. Far from zero (|m c| > 256, tiny temperatures) l c
+// would lose too many bits, and l - m is taken first (`diff`, ref = 0).
 struct Scale {
-  float m, ch, cl;
+  float m, ch, cl, ref;
+  bool diff;
 };
 
-// round(2^FX * exp((l - m) / T)). The exponent t = (l - m) * c is kept as th + tl: l - m by a
-// two-sum, the product by fused multiply-adds; |error of t| < 2^-42. th = k / 256 + r with
-// |r| <= 2^-9, and 2^r - 1 = L r + (L r)^2 / 2 + ... (L = ln 2, Taylor terms up to the
-// fourth), its leading term again as a pair. Scaled by 2^40 the sum fits 32 bits; the table
-// entry times it is a 64-bit product, shifted into place and rounded to nearest (truncation
-// would bias the sum of 10^5 small weights by 2^-28).
+// w * 2^FX for w = 2^((l - m) c) up to the row's common factor, within 2^-40 of it. l c is a
+// pair p + lo; p = ref + k / 256 + r with |r| <= 2^-9, exactly; 2^(r + lo) - 1 is its Taylor
+// series in L (r + lo), L = ln 2, to the fourth term, the leading one again as a pair. Scaled by
+// 2^40 it fits 32 bits; the table entry times it is a 64-bit product, shifted into place. The
+// shift drops bits and sets the lowest one, the middle of what was dropped, so that 10^5 small
+// weights carry no bias.
 __device__ __forceinline__ u64 weight_fx(float l, const Scale& s, const u64* tab) {
-  if (l == s.m) return 1ull << FX;
-  const float dh = l - s.m;
-  const float th = dh * s.ch;
-  if (!(th > -(float)(FX + 1))) return 0;  // also l = -inf
-  const float bb = dh - l;
-  const float dl = (l - (dh - bb)) - (s.m + bb);  // l - m = dh + dl exactly
-  float tl = fmaf(dh, s.ch, -th);
-  tl = fmaf(dh, s.cl, tl);
-  tl = fmaf(dl, s.ch, tl);
+  float p, lo;
+  if (s.diff) {
+    if (l == s.m) return 1ull << FX;
+    const float dh = l - s.m, bb = dh - l;
+    const float dl = (l - (dh - bb)) - (s.m + bb);  // l - m = dh + dl exactly
+    p = dh * s.ch;
+    lo = fmaf(dl, s.ch, fmaf(dh, s.cl, fmaf(dh, s.ch, -p)));
+  } else {
+    p = l * s.ch;
+    lo = fmaf(l, s.cl, fmaf(l, s.ch, -p));
+  }
+  const float d = p - s.ref;
+  if (!(d > -(float)(FX + 1))) return 0;  // also l = -inf (c may be 0 or infinite)
   const float magic = 12582912.f;  // 1.5 * 2^23: rounds to an integer held in the low bits
-  const float kf = fmaf(th, 256.f, magic);
+  const float kf = fmaf(d, 256.f, magic);
   const int k = __float_as_int(kf) - 0x4b400000;
-  const float r = fmaf(kf - magic, -1.f / 256.f, th);
+  const float r = p - fmaf(kf - magic, 1.f / 256.f, s.ref);
   constexpr float S40 = 1099511627776.f;
   constexpr double L = 0.69314718055994530942;
   constexpr float Lh = (float)L * S40;
   constexpr float Ll = (float)(L - (double)(float)L) * S40;
   constexpr float C2 = (float)(L * L / 2 * S40), C3 = (float)(L * L * L / 6 * S40), C4 = (float)(L * L * L * L / 24 * S40);
-  const float qh = r * Lh;
-  float ql = fmaf(r, Lh, -qh);
-  ql = fmaf(r, Ll, ql);
-  ql = fmaf(tl, Lh, ql);
-  ql = fmaf(tl * r, 2.f * C2, ql);
-  ql = fmaf(fmaf(fmaf(C4, r, C3), r, C2), r * r, ql);
+  const float qh = r * Lh, rs = r + lo;
+  float ql = fmaf(lo, Lh, fmaf(r, Ll, fmaf(r, Lh, -qh)));
+  ql = fmaf(fmaf(fmaf(C4, rs, C3), rs, C2), rs * rs, ql);
   const int q = __float2int_rn(qh) + __float2int_rn(ql);
-  const u64 t = tab[k & (TAB - 1)];                       // 2^(j / 256) * 2^44
-  const int t31 = (int)((t + (1u << 13)) >> 14);          // ... * 2^30 (below 2^31)
-  const long long x = (long long)t + (((long long)t31 * q) >> 26);  // 2^30 * 2^40 / 2^26 = 2^44
-  const int n = -(k >> 8);                                // 0 .. FX + 1
-  return (((u64)x << 1 >> n) + 1) >> 1;
+  const u64 t = tab[k & (TAB - 1)];               // 2^(j / 256) * 2^FX, below 2^46
+  const int t30 = (int)(t >> (FX - 30));          // 30 bits of it and one before the point
+  const u64 x = t + (u64)(((long long)t30 * q) >> (70 - FX));
+  return (x >> -(k >> 8)) | 1ull;                 // k <= 1, so the shift is 0 .. FX + 1
 }
 
-// Per-CTA sum and count over all threads.
-__device__ __forceinline__ u64 block_sum(u64 v, u64* tmp) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  if ((threadIdx.x & 31) == 0) tmp[threadIdx.x >> 5] = v;
-  __syncthreads();
-  u64 s = 0;
-#pragma unroll
-  for (int i = 0; i < SWARPS; ++i) s += tmp[i];
-  __syncthreads();
-  return s;
-}
-
-// ceil(f * w) for a float 0 <= f < 1 (or 1): f is mant * 2^-sh exactly.
-__device__ __forceinline__ u64 ceil_mul(float f, u64 w) {
-  if (!(f > 0.f)) return 0;
-  if (f >= 1.f) return w;
+// floor(f * w) for a float 0 <= f < 1 and whether that is exact: f = mant * 2^-sh.
+__device__ __forceinline__ u64 floor_mul(float f, u64 w, bool* exact = nullptr) {
   const unsigned b = __float_as_uint(f);
   const int e = (int)(b >> 23);
   const u64 mant = e ? (b & 0x7fffffu) | 0x800000u : b & 0x7fffffu;
-  const int sh = 150 - (e ? e : 1);  // f = mant * 2^-sh, sh >= 24
-  const u64 lo = mant * w, hi = __umul64hi(mant, w);
-  if (sh >= 128) return (lo | hi) != 0;
-  const u64 up_lo = sh >= 64 ? ~0ull : (1ull << sh) - 1, up_hi = sh > 64 ? (sh >= 128 ? ~0ull : (1ull << (sh - 64)) - 1) : 0;
-  u64 a = lo + up_lo;
-  u64 c = hi + up_hi + (a < lo);
-  if (sh == 64) return c;
-  return sh > 64 ? c >> (sh - 64) : (a >> sh) | (c << (64 - sh));
+  const int sh = 150 - (e ? e : 1);  // at least 24
+  const u64 lo = mant * w, hi = __umul64hi(mant, w);  // below 2^87
+  u64 q, rest;
+  if (sh < 64) {
+    q = (lo >> sh) | (hi << (64 - sh));
+    rest = lo & ((1ull << sh) - 1);
+  } else {
+    const int s = min(sh - 64, 63);
+    q = hi >> s;
+    rest = lo | (hi & ((1ull << s) - 1));
+  }
+  if (exact) *exact = rest == 0;
+  return q;
+}
+__device__ __forceinline__ u64 ceil_mul(float f, u64 w) {
+  if (!(f > 0.f)) return 0;
+  bool exact;
+  const u64 q = floor_mul(f, w, &exact);
+  return exact ? q : q + 1;
 }
 
-// The prefix of the order that ends at (and includes `ties` ids of) key `key`.
+// The prefix of the order that ends with the first `ties` ids of key `key`.
 struct Prefix {
   unsigned key, ties;
-  __device__ __forceinline__ bool shorter(const Prefix& o) const { return key > o.key || (key == o.key && ties < o.ties); }
+  __device__ __forceinline__ bool shorter(const Prefix& o) const {
+    return key > o.key || (key == o.key && ties < o.ties);
+  }
+  // Whether the lane's element (of 32 in ascending order; all lanes call) belongs to it; t0
+  // counts the elements at `key` seen so far.
+  __device__ __forceinline__ bool keeps(bool in, unsigned k, unsigned& t0, int lane) const {
+    if (ties == UINT_MAX) return in && k >= key;
+    const unsigned eq = __ballot_sync(0xffffffffu, in && k == key);
+    const bool keep = in && (k > key || (k == key && t0 + __popc(eq & ((1u << lane) - 1)) < ties));
+    t0 += __popc(eq);
+    return keep;
+  }
 };
 
 template <int C>
-__global__ void __launch_bounds__(ST) sample_kernel(const SampleParams p) {
+__global__ void __launch_bounds__(ST, 2) sample_kernel(const SampleParams p) {
   extern __shared__ __align__(16) unsigned char smem[];
   Share& sh = *reinterpret_cast<Share*>(smem);
   float* row = reinterpret_cast<float*>(smem + sizeof(Share));
@@ -227,68 +233,61 @@ __global__ void __launch_bounds__(ST) sample_kernel(const SampleParams p) {
   const int base = (int)rank * p.slice;
   const int n = max(0, min(p.slice, p.V - base));  // this CTA's ids: [base, base + n)
   const float* src = p.logits + (long long)r * p.ld + base;
+  auto sync_all = [&]() {
+    if (C > 1) cluster_barrier();
+    else __syncthreads();
+  };
 
   griddep_launch_dependents();
   for (int i = tid; i < TAB; i += ST) sh.tab[i] = kPow2.v[i];
   griddep_wait();
-  // ---- the slice, its maximum and that one's lowest id
+  // ---- the slice and its maximum (NaN becomes -inf)
   float mx = -INFINITY;
-  int mi = INT_MAX;
-  auto take = [&](float v, int i) {
-    v = v != v ? -INFINITY : v;
-    if (v > mx || mi == INT_MAX) {  // ids ascend within a thread
-      mx = v;
-      mi = i;
-    }
-    return v;
-  };
   if (p.vec) {
     const int n4 = n >> 2;
-#pragma unroll 4
+#pragma unroll 8
     for (int i = tid; i < n4; i += ST) {
       float4 v = __ldcs(reinterpret_cast<const float4*>(src) + i);
-      v.x = take(v.x, 4 * i);
-      v.y = take(v.y, 4 * i + 1);
-      v.z = take(v.z, 4 * i + 2);
-      v.w = take(v.w, 4 * i + 3);
+      v.x = fmaxf(v.x, -INFINITY);
+      v.y = fmaxf(v.y, -INFINITY);
+      v.z = fmaxf(v.z, -INFINITY);
+      v.w = fmaxf(v.w, -INFINITY);
+      mx = fmaxf(fmaxf(mx, fmaxf(v.x, v.y)), fmaxf(v.z, v.w));
       *reinterpret_cast<float4*>(row + 4 * i) = v;
     }
-    for (int i = 4 * n4 + tid; i < n; i += ST) row[i] = take(src[i], i);
+    for (int i = 4 * n4 + tid; i < n; i += ST) mx = fmaxf(mx, row[i] = fmaxf(src[i], -INFINITY));
   } else {
-#pragma unroll 4
-    for (int i = tid; i < n; i += ST) row[i] = take(__ldcs(src + i), i);
+#pragma unroll 8
+    for (int i = tid; i < n; i += ST) mx = fmaxf(mx, row[i] = fmaxf(__ldcs(src + i), -INFINITY));
   }
-  unsigned gi = mi == INT_MAX ? UINT_MAX : (unsigned)(base + mi);
-  auto better = [&](float v, unsigned i) {
-    if (i != UINT_MAX && (gi == UINT_MAX || v > mx || (v == mx && i < gi))) {
-      mx = v;
-      gi = i;
-    }
-  };
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const float v2 = __shfl_xor_sync(0xffffffffu, mx, o);
-    const unsigned i2 = __shfl_xor_sync(0xffffffffu, gi, o);
-    better(v2, i2);
-  }
-  if (lane == 0) {
-    sh.red_f[warp] = mx;
-    sh.red_a[warp] = gi;
-  }
+  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  if (lane == 0) sh.red_f[warp] = mx;
   __syncthreads();
-  for (int w = 0; w < SWARPS; ++w) better(sh.red_f[w], sh.red_a[w]);
+#pragma unroll
+  for (int w = 0; w < SWARPS; ++w) mx = fmaxf(mx, sh.red_f[w]);
   if (C > 1) {
-    if (tid == 0) {
-      sh.x_max = mx;
-      sh.x_idx = gi;
-    }
+    if (tid == 0) sh.x_max = mx;
     cluster_barrier();
-    for (unsigned c = 0; c < (unsigned)C; ++c) better(ld_remote(&sh.x_max, c), ld_remote(&sh.x_idx, c));
+#pragma unroll
+    for (unsigned c = 0; c < (unsigned)C; ++c) mx = fmaxf(mx, ld_remote(&sh.x_max, c));
   }
   const float T = p.temperature ? p.temperature[r] : p.temperature_all;
-  if (!(T > 0.f) || mx == -INFINITY) {  // greedy; a row with no finite logit gives id 0
-    if (rank == 0 && tid == 0) p.tokens[r] = mx == -INFINITY ? 0 : (int)gi;
-    if (C > 1) cluster_barrier();  // no CTA leaves while another may read its x_max
+  if (!(T > 0.f) || mx == -INFINITY) {  // greedy; a row with no logit above -inf gives id 0
+    unsigned at = UINT_MAX;
+    for (int i = tid; i < n; i += ST)
+      if (row[i] == mx) at = min(at, (unsigned)(base + i));
+    at = __reduce_min_sync(0xffffffffu, at);
+    if (lane == 0) sh.red_a[warp] = at;
+    __syncthreads();
+    for (int w = 0; w < SWARPS; ++w) at = min(at, sh.red_a[w]);
+    if (C > 1) {
+      if (tid == 0) sh.x_kmin = at;
+      cluster_barrier();
+      for (unsigned c = 0; c < (unsigned)C; ++c) at = min(at, ld_remote(&sh.x_kmin, c));
+    }
+    if (rank == 0 && tid == 0) p.tokens[r] = (int)at;
+    if (C > 1) cluster_barrier();  // no CTA leaves while another may read its x_kmin
     return;
   }
   const int tk = p.top_k ? p.top_k[r] : p.top_k_all;
@@ -299,92 +298,90 @@ __global__ void __launch_bounds__(ST) sample_kernel(const SampleParams p) {
   Scale sc;
   sc.m = mx;
   {
-    const double c = 1.4426950408889634074 / (double)T;
+    const double c = 1.4426950408889634074 / (double)T, mc = (double)mx * c;
     sc.ch = (float)c;
     sc.cl = isinf(sc.ch) ? 0.f : (float)(c - (double)sc.ch);
+    sc.diff = !(fabs(mc) <= 256.0);
+    sc.ref = sc.diff ? 0.f : (float)(rint(mc * 256.0) * (1.0 / 256.0));
   }
+  // Warp w owns the slice's segment [s0, s1), ids ascending. Filters compact the segments in
+  // place (lower positions only), so later passes read what is left.
+  const int seg = ((n + SWARPS - 1) / SWARPS + 31) & ~31;
+  const int s0 = min(n, warp * seg);
+  int s1 = min(n, s0 + seg);
+
   // linear bins over the range where weights are not zero; the last bin takes the rest
   const float bin_scale = fminf(sc.ch * ((float)(NB - 1) / (float)(FX + 1)), FLT_MAX);
   auto bin_of = [&](float l) {
-    const float b = (sc.m - l) * bin_scale;  // NaN (l = m = inf, or 0 * inf): bin 0
-    return b >= (float)(NB - 1) ? NB - 1 : (b > 0.f ? (int)b : 0);
+    const float b = (mx - l) * bin_scale;  // NaN (l = m = inf, or inf * 0): bin 0
+    return (int)fminf(b > 0.f ? b : 0.f, (float)(NB - 1));
   };
   auto add_mass = [&](int b, u64 w) {
-    atomicAdd(&sh.limb[0][b], (unsigned)(w & 0xffffu));
-    atomicAdd(&sh.limb[1][b], (unsigned)((w >> 16) & 0xffffu));
-    atomicAdd(&sh.limb[2][b], (unsigned)(w >> 32));
+    const unsigned lo = (unsigned)w, hi = (unsigned)(w >> 32);
+    atomicAdd(&sh.limb[0][b], lo & 0xffffu);
+    if (lo >> 16) atomicAdd(&sh.limb[1][b], lo >> 16);
+    if (hi) atomicAdd(&sh.limb[2][b], hi);
   };
   auto clear = [&]() {
-    for (int b = tid; b < NB; b += ST) {
-      sh.cnt[b] = 0;
-      sh.limb[0][b] = sh.limb[1][b] = sh.limb[2][b] = 0;
-    }
+    for (int b = tid; b < NB; b += ST) sh.limb[0][b] = sh.limb[1][b] = sh.limb[2][b] = 0;
     __syncthreads();
   };
-  auto publish = [&](bool mass) {  // limbs -> 64-bit masses, visible to the cluster
+  // this CTA's bins as 64-bit masses (or counts, in the first limb), visible to the cluster
+  auto publish = [&]() {
     __syncthreads();
-    if (mass)
-      for (int b = tid; b < NB; b += ST)
-        sh.mass[b] = (u64)sh.limb[0][b] + ((u64)sh.limb[1][b] << 16) + ((u64)sh.limb[2][b] << 32);
-    if (C > 1) cluster_barrier(); else __syncthreads();
+    for (int b = tid; b < NB; b += ST)
+      sh.mass[b] = (u64)sh.limb[0][b] + ((u64)sh.limb[1][b] << 16) + ((u64)sh.limb[2][b] << 32);
+    sync_all();
   };
-  // Rank-independent scan: every CTA sums the cluster's bins (thread t: bins 2t, 2t + 1) and
-  // finds the first bin, in descending order of the logits, at which the running count or mass
-  // reaches `want`. Fills sh.d_* and returns with the block synchronised.
-  auto find = [&](bool by_mass, bool with_mass, u64 want, u64 before_mass, unsigned before_cnt) {
+  // Every CTA sums the cluster's bins (thread t: bins 2t, 2t + 1) and finds the first bin, in
+  // descending order of the logits, at which the running sum reaches `want`; sums above it are
+  // returned in `before`. fraction >= 0: want is that part of all the bins (at least 1).
+  auto find = [&](u64& want, float fraction, u64& before) -> int {
     u64 ms[2] = {0, 0};
-    unsigned ct[2] = {0, 0};
+#pragma unroll
     for (unsigned c = 0; c < (unsigned)C; ++c)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        if (with_mass) ms[e] += ld_remote(&sh.mass[2 * tid + e], c);
-        ct[e] += ld_remote(&sh.cnt[2 * tid + e], c);
-      }
+      for (int e = 0; e < 2; ++e) ms[e] += ld_remote(&sh.mass[2 * tid + e], c);
     u64 im = ms[0] + ms[1];
-    unsigned ic = ct[0] + ct[1];
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const u64 m2 = __shfl_up_sync(0xffffffffu, im, o);
-      const unsigned c2 = __shfl_up_sync(0xffffffffu, ic, o);
-      if (lane >= o) {
-        im += m2;
-        ic += c2;
-      }
+      if (lane >= o) im += m2;
     }
-    if (lane == 31) {
-      sh.warp_mass[warp] = im;
-      sh.warp_cnt[warp] = ic;
-    }
-    if (tid == 0) sh.d_bin = -1;
+    if (lane == 31) sh.warp_mass[warp] = im;
+    if (tid == 0) sh.d_bin = 0;
     __syncthreads();
-    for (int w = 0; w < warp; ++w) {
-      im += sh.warp_mass[w];
-      ic += sh.warp_cnt[w];
+    u64 bm = before + im - ms[0] - ms[1], all = 0;
+#pragma unroll
+    for (int w = 0; w < SWARPS; ++w) {
+      const u64 x = sh.warp_mass[w];
+      if (w < warp) bm += x;
+      all += x;
     }
-    u64 bm = before_mass + im - ms[0] - ms[1];
-    unsigned bc = before_cnt + ic - ct[0] - ct[1];
+    if (fraction >= 0.f) {
+      const u64 c = ceil_mul(fraction, all);
+      want = c > 0 ? c : 1;
+    }
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      // by count: the bin with bc < want <= bc + ct; by mass: bm < want <= bm + ms
-      const u64 b0 = by_mass ? bm : (u64)bc, b1 = by_mass ? bm + ms[e] : (u64)(bc + ct[e]);
-      if (b0 < want && want <= b1) {
+      if (bm < want && want <= bm + ms[e]) {
         sh.d_bin = 2 * tid + e;
-        sh.d_before_mass = bm;
-        sh.d_before_cnt = bc;
-        sh.d_in_cnt = ct[e];
+        sh.d_before = bm;
       }
       bm += ms[e];
-      bc += ct[e];
     }
-    if (C > 1) cluster_barrier(); else __syncthreads();  // also: nobody still reads the bins
+    sync_all();  // also: nobody still reads the bins
+    before = sh.d_before;
+    return sh.d_bin;
   };
-  // Smallest and largest key of the cluster's elements in the open interval test `in`.
+  // Smallest and largest key of the cluster's elements that pass `in`.
   auto key_range = [&](auto in, unsigned& lo, unsigned& hi) {
     unsigned a = UINT_MAX, b = 0;
-    for (int i = tid; i < n; i += ST) {
+#pragma unroll 4
+    for (int i = s0 + lane; i < s1; i += 32) {
       const float l = row[i];
+      const unsigned k = key_of(l);
       if (in(l)) {
-        const unsigned k = key_of(l);
         a = min(a, k);
         b = max(b, k);
       }
@@ -410,219 +407,199 @@ __global__ void __launch_bounds__(ST) sample_kernel(const SampleParams p) {
         a = min(a, ld_remote(&sh.x_kmin, c));
         b = max(b, ld_remote(&sh.x_kmax, c));
       }
-      cluster_barrier();
-    } else {
-      __syncthreads();
     }
+    sync_all();
     lo = a;
     hi = b;
   };
-  // Refines "the threshold lies in bin `bin` of the first histogram" to one key. On return
-  // lo is that key, before_* what lies above it and in_cnt how many elements equal it.
-  auto refine = [&](bool by_mass, bool with_mass, u64 want, int bin, u64& before_mass, unsigned& before_cnt,
-                    unsigned& in_cnt) -> unsigned {
+  // "The threshold lies in bin `bin` of a first histogram" to one key; `before` becomes the
+  // count or mass above that key.
+  auto refine = [&](bool by_mass, u64 want, int bin, u64& before) -> unsigned {
     unsigned lo, hi;
     key_range([&](float l) { return bin_of(l) == bin; }, lo, hi);
-    for (int it = 0; it < 5 && lo != hi; ++it) {  // ten bits of the key a round
-      const unsigned span = hi - lo;
-      const int s = max(0, 32 - __clz(span) - 10);  // span >> s < NB
+    for (int it = 0; it < 5 && lo < hi; ++it) {  // ten bits of the key a round
+      const int s = max(0, 22 - __clz(hi - lo));  // (hi - lo) >> s < NB
       clear();
-      for (int i = tid; i < n; i += ST) {
+#pragma unroll 4
+      for (int i = s0 + lane; i < s1; i += 32) {
         const unsigned k = key_of(row[i]);
         if (k >= lo && k <= hi) {
           const int b = (int)((hi - k) >> s);
-          atomicAdd(&sh.cnt[b], 1u);
-          if (with_mass) add_mass(b, weight_fx(row[i], sc, sh.tab));
+          if (by_mass) add_mass(b, weight_fx(row[i], sc, sh.tab));
+          else atomicAdd(&sh.limb[0][b], 1u);
         }
       }
-      publish(with_mass);
-      find(by_mass, with_mass, want, before_mass, before_cnt);
-      const unsigned b = (unsigned)sh.d_bin;
-      before_mass = sh.d_before_mass;
-      before_cnt = sh.d_before_cnt;
-      in_cnt = sh.d_in_cnt;
-      const unsigned nh = hi - (b << s);
-      lo = max(lo, nh - ((1u << s) - 1));
-      hi = nh;
-      __syncthreads();
+      publish();
+      const unsigned b = (unsigned)find(want, -1.f, before);
+      hi -= b << s;
+      lo = max(lo, hi - ((1u << s) - 1));
+      __syncthreads();  // everyone has read the decision
     }
     return lo;
   };
 
   Prefix pre;
   pre.key = 0;
-  pre.ties = UINT_MAX;  // everything
-  if (use_k || use_p) {
+  pre.ties = UINT_MAX;    // everything
+  unsigned tie_base = 0;  // elements at pre.key with lower ids than this warp's segment
+  // Keeps what belongs to the prefix, each warp's segment in place.
+  auto compact = [&]() {
+    if (pre.ties != UINT_MAX) {
+      unsigned t = 0;
+      for (int i = s0 + lane; i < s1; i += 32) t += key_of(row[i]) == pre.key;
+      t = __reduce_add_sync(0xffffffffu, t);
+      if (lane == 0) sh.red_a[warp] = t;
+      __syncthreads();
+      unsigned all = 0;
+      tie_base = 0;
+      for (int w = 0; w < SWARPS; ++w) {
+        if (w < warp) tie_base += sh.red_a[w];
+        all += sh.red_a[w];
+      }
+      if (C > 1) {
+        if (tid == 0) sh.x_ties = all;
+        cluster_barrier();
+        for (unsigned c = 0; c + 1 <= rank; ++c) tie_base += ld_remote(&sh.x_ties, c);
+      }
+      sync_all();
+    }
+    unsigned t0 = tie_base;
+    int out = s0;
+    for (int i = s0; i < s1; i += 32) {
+      const bool in = i + lane < s1;
+      const float l = in ? row[i + lane] : 0.f;
+      const bool keep = pre.keeps(in, key_of(l), t0, lane);
+      const unsigned kept = __ballot_sync(0xffffffffu, keep);
+      if (keep) row[out + __popc(kept & ((1u << lane) - 1))] = l;
+      out += __popc(kept);
+      __syncwarp();
+    }
+    s1 = out;
+  };
+
+  if (use_k) {
     clear();
-    for (int i = tid; i < n; i += ST) {
+#pragma unroll 4
+    for (int i = s0 + lane; i < s1; i += 32) atomicAdd(&sh.limb[0][bin_of(row[i])], 1u);
+    publish();
+    u64 want = (u64)tk, before = 0;
+    const int bin = find(want, -1.f, before);
+    pre.key = refine(false, want, bin, before);
+    pre.ties = (unsigned)(want - before);
+    compact();
+  }
+  if (use_p) {
+    // elements with less than top_p of the mass before them: the last one kept is the one at
+    // which the running mass reaches it, and the first of the order is always kept
+    clear();
+#pragma unroll 4
+    for (int i = s0 + lane; i < s1; i += 32) {
       const float l = row[i];
-      const int b = bin_of(l);
-      atomicAdd(&sh.cnt[b], 1u);
-      if (use_p) {
-        const u64 w = weight_fx(l, sc, sh.tab);
-        if (w) add_mass(b, w);
-      }
+      const u64 w = weight_fx(l, sc, sh.tab);
+      if (w) add_mass(bin_of(l), w);
     }
-    publish(use_p);
-    u64 total = 0, bm;  // bm, bc, ic: mass and count before the threshold's bin, count inside it
-    unsigned bc, ic;
-    if (use_k) {
-      find(false, use_p, (u64)tk, 0, 0);
-      const int bin = sh.d_bin;
-      bm = sh.d_before_mass;
-      bc = sh.d_before_cnt;
-      ic = sh.d_in_cnt;
-      pre.key = refine(false, use_p, (u64)tk, bin, bm, bc, ic);
-      pre.ties = (unsigned)tk - bc;
-    }
-    if (use_k && use_p) {
-      // mass of the top k; the top-p search starts from a histogram of those alone
-      total = bm + (u64)pre.ties * weight_fx(value_of(pre.key), sc, sh.tab);
-      clear();
-      for (int i = tid; i < n; i += ST) {
-        const float l = row[i];
-        if (key_of(l) >= pre.key) {
-          const int b = bin_of(l);
-          atomicAdd(&sh.cnt[b], 1u);
-          add_mass(b, weight_fx(l, sc, sh.tab));
-        }
-      }
-      publish(true);
-    } else if (use_p) {
-      u64 t = 0;
-      for (unsigned c = 0; c < (unsigned)C; ++c)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) t += ld_remote(&sh.mass[2 * tid + e], c);
-      total = block_sum(t, sh.warp_mass);
-    }
-    if (use_p) {
-      // elements with less than top_p of the mass before them: the last one kept is the one at
-      // which the running mass reaches it, and the first of the order is always kept
-      const u64 c = ceil_mul(tp, total), want = c > 0 ? c : 1;
-      find(true, true, want, 0, 0);
-      const int bin = sh.d_bin;
-      bm = sh.d_before_mass;
-      bc = sh.d_before_cnt;
-      ic = sh.d_in_cnt;
-      Prefix pp;
-      pp.key = refine(true, true, want, bin, bm, bc, ic);
-      const u64 w = weight_fx(value_of(pp.key), sc, sh.tab);
-      const u64 ties = w ? (want - bm + w - 1) / w : UINT_MAX;
-      pp.ties = ties > UINT_MAX ? UINT_MAX : (unsigned)ties;
-      if (pp.shorter(pre)) pre = pp;
-    }
+    publish();
+    u64 want = 0, before = 0;
+    const int bin = find(want, tp, before);
+    Prefix pp;
+    pp.key = refine(true, want, bin, before);
+    const u64 w = weight_fx(value_of(pp.key), sc, sh.tab);
+    const u64 ties = w ? (want - before + w - 1) / w : UINT_MAX;
+    pp.ties = ties > UINT_MAX ? UINT_MAX : (unsigned)ties;
+    if (pp.shorter(pre)) pre = pp;
   }
   if (mp > 0.f) {
-    // w >= min_p  <=>  l >= m + T ln(min_p)
-    const double thr = (double)mx + (double)T * log((double)fminf(mp, 1.f));
-    const float tf = mp >= 1.f ? mx : __double2float_ru(thr);
-    // an infinite product (T = inf) leaves everything; NaN cannot arise for mx > -inf, T > 0
+    // w >= min_p  <=>  l >= m + T ln(min_p); an infinite product leaves everything
+    const float tf = mp >= 1.f ? mx : __double2float_ru((double)mx + (double)T * log((double)mp));
     const unsigned key = key_of(tf);
     if (key > pre.key) {
       pre.key = key;
       pre.ties = UINT_MAX;
     }
   }
+  if (use_p || mp > 0.f) compact();
 
-  // ---- ids in ascending order: warp w of CTA c owns a contiguous segment
-  const int seg = ((n + SWARPS - 1) / SWARPS + 31) & ~31;
-  const int s0 = min(n, warp * seg), s1 = min(n, s0 + seg);
-  unsigned tie_base = 0;  // equal-key ids before this warp's segment
-  if (pre.ties != UINT_MAX) {
-    unsigned t = 0;
-    for (int i = s0 + lane; i < s1; i += 32) t += key_of(row[i]) == pre.key;
-    t = __reduce_add_sync(0xffffffffu, t);
-    if (lane == 0) sh.red_a[warp] = t;
-    __syncthreads();
-    unsigned all = 0;
-    for (int w = 0; w < SWARPS; ++w) {
-      if (w < warp) tie_base += sh.red_a[w];
-      all += sh.red_a[w];
-    }
-    if (C > 1) {
-      if (tid == 0) sh.x_ties = all;
-      cluster_barrier();
-      for (unsigned c = 0; c < rank; ++c) tie_base += ld_remote(&sh.x_ties, c);
-    }
-  }
-  // kept weight of id i (all lanes call; t0: ties seen so far in this segment)
-  auto kept = [&](int i, unsigned& t0) -> u64 {
-    const bool in = i < s1;
-    const float l = in ? row[i] : 0.f;
-    const unsigned k = in ? key_of(l) : 0u;
-    bool keep = in && k > pre.key;
-    if (pre.ties == UINT_MAX) {
-      keep = in && k >= pre.key;
-    } else {
-      const unsigned eq = __ballot_sync(0xffffffffu, in && k == pre.key);
-      if (in && k == pre.key) keep = t0 + __popc(eq & ((1u << lane) - 1)) < pre.ties;
-      t0 += __popc(eq);
-    }
-    return keep ? weight_fx(l, sc, sh.tab) : 0ull;
-  };
+  // ---- the draw: running sums over the kept ids in ascending order
   u64 sum = 0;
-  {
-    unsigned t0 = tie_base;
-    for (int i = s0; i < s1; i += 32) sum += kept(i + lane, t0);
-  }
+#pragma unroll 4
+  for (int i = s0 + lane; i < s1; i += 32) sum += weight_fx(row[i], sc, sh.tab);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  __syncthreads();  // warp_mass of an earlier search has been read
   if (lane == 0) sh.warp_mass[warp] = sum;
   __syncthreads();
   u64 before = 0, total = 0;
+#pragma unroll
   for (int w = 0; w < SWARPS; ++w) {
-    if (w < warp) before += sh.warp_mass[w];
-    total += sh.warp_mass[w];
+    const u64 x = sh.warp_mass[w];
+    if (w < warp) before += x;
+    total += x;
   }
   if (C > 1) {
     if (tid == 0) sh.x_mass = total;
     cluster_barrier();
-    const u64 mine = total;
     total = 0;
+#pragma unroll
     for (unsigned c = 0; c < (unsigned)C; ++c) {
-      const u64 x = c == rank ? mine : ld_remote(&sh.x_mass, c);
-      if (c < rank) before += x;
+      const u64 x = ld_remote(&sh.x_mass, c);
+      if (c + 1 <= rank) before += x;
       total += x;
     }
   }
-  // the first id whose running sum exceeds u * total; sums are whole, so "exceeds the real
-  // number u * total" is "is at least floor(u * total) + 1"
+  // sums are whole numbers, so "exceeds the real number u * total" is "is at least
+  // floor(u * total) + 1"
   float u = p.u[r];
-  u = u >= 0.f ? fminf(u, 0.99999994f) : 0.f;
-  const u64 up = ceil_mul(u, total);
-  u64 target;
-  {
-    // ceil(u * total) equals the product exactly when the product is whole
-    const unsigned b = __float_as_uint(u);
-    const int e = (int)(b >> 23);
-    const u64 mant = u > 0.f ? (e ? (b & 0x7fffffu) | 0x800000u : b & 0x7fffffu) : 0;
-    const int s = 150 - (e ? e : 1);
-    const u64 lo = mant * total, hi = __umul64hi(mant, total);
-    bool whole;
-    if (s >= 128) whole = (lo | hi) == 0;
-    else if (s > 64) whole = lo == 0 && (hi & ((1ull << (s - 64)) - 1)) == 0;
-    else if (s == 64) whole = lo == 0;
-    else whole = (lo & ((1ull << s) - 1)) == 0;
-    target = whole ? up + 1 : up;
-  }
+  u = u > 0.f ? fminf(u, 0.99999994f) : 0.f;  // NaN and -0 too
+  const u64 target = floor_mul(u, total) + 1;
   if (before < target && target <= before + sum) {  // one warp of the cluster
-    unsigned t0 = tie_base;
-    u64 run = before;
-    for (int i = s0; i < s1; i += 32) {
-      const u64 w = kept(i + lane, t0);
-      u64 inc = w;
+    // lane j sums a contiguous share; then the warp looks into the share that holds the target
+    const int each = (s1 - s0 + 31) / 32;
+    const int b0 = min(s1, s0 + lane * each), b1 = min(s1, b0 + each);
+    u64 mine = 0;
+#pragma unroll 4
+    for (int i = b0; i < b1; ++i) mine += weight_fx(row[i], sc, sh.tab);
+    auto scan = [&](u64 v) {
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const u64 x = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += x;
+        const u64 x = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += x;
       }
-      const unsigned hit = __ballot_sync(0xffffffffu, run + inc >= target);
+      return v;
+    };
+    const u64 upto = before + scan(mine);
+    const int who = __ffs(__ballot_sync(0xffffffffu, upto >= target)) - 1;
+    u64 run = __shfl_sync(0xffffffffu, upto - mine, who);
+    const int c0 = __shfl_sync(0xffffffffu, b0, who), c1 = __shfl_sync(0xffffffffu, b1, who);
+    int at = c0;
+    for (int i = c0; i < c1; i += 32) {
+      const u64 inc = run + scan(i + lane < c1 ? weight_fx(row[i + lane], sc, sh.tab) : 0ull);
+      const unsigned hit = __ballot_sync(0xffffffffu, inc >= target);
       if (hit) {
-        if (lane == 0) p.tokens[r] = base + i + __ffs(hit) - 1;
+        at = i + __ffs(hit) - 1;
         break;
       }
-      run += __shfl_sync(0xffffffffu, inc, 31);
+      run = __shfl_sync(0xffffffffu, inc, 31);
     }
+    int id = at;
+    if (pre.key || pre.ties != UINT_MAX) {
+      // the segment was compacted: its (at - s0)-th kept element, counted in the logits again
+      int left = at - s0;
+      unsigned t0 = tie_base;
+      const int e1 = min(n, s0 + seg);
+      for (int i = s0; i < e1; i += 32) {
+        const bool in = i + lane < e1;
+        const float l = in ? fmaxf(src[i + lane], -INFINITY) : 0.f;
+        unsigned kept = __ballot_sync(0xffffffffu, pre.keeps(in, key_of(l), t0, lane));
+        const int c = __popc(kept);
+        if (left < c) {
+          for (; left > 0; --left) kept &= kept - 1;
+          id = i + __ffs(kept) - 1;
+          break;
+        }
+        left -= c;
+      }
+    }
+    if (lane == 0) p.tokens[r] = base + id;
   }
   if (C > 1) cluster_barrier();  // shared memory stays until every CTA has read it
 }
