@@ -7,6 +7,7 @@ libswiftkv.so. Every call checks the library's return code and raises
 from __future__ import annotations
 
 import ctypes as C
+from contextlib import nullcontext
 from dataclasses import dataclass
 from typing import Optional, Sequence
 
@@ -19,6 +20,15 @@ from . import binding as B
 def _stream(stream) -> int:
     s = stream if stream is not None else torch.cuda.current_stream()
     return s.cuda_stream
+
+
+def _stream_of(dev: torch.device, stream) -> int:
+    return (stream if stream is not None else torch.cuda.current_stream(dev)).cuda_stream
+
+
+def _on(dev: torch.device):
+    """Makes dev the current device for a call, at no cost where it already is."""
+    return nullcontext() if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
 
 
 def _ptr(a) -> Optional[int]:
@@ -238,6 +248,9 @@ def _need(cond: bool, msg: str) -> None:
         raise ValueError(msg)
 
 
+_SAMPLING = (("temperature", torch.float32), ("top_k", torch.int32), ("top_p", torch.float32), ("min_p", torch.float32))
+
+
 def sample(logits: torch.Tensor, u: torch.Tensor, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0,
            out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """One token id (int32) per row of float32 logits [P, V] (rows may be strided), drawn with the
@@ -246,29 +259,30 @@ def sample(logits: torch.Tensor, u: torch.Tensor, temperature=1.0, top_k=0, top_
     top_k <= 0, top_p >= 1 and min_p <= 0 are off. Enqueued without synchronising."""
     _need(logits.dim() == 2 and logits.dtype == torch.float32 and logits.is_cuda, "logits: float32 CUDA [P, V]")
     P, V = logits.shape
+    ld, step = logits.stride()
     _need(V >= 1, "logits need at least one column")
-    _need(V == 1 or logits.stride(1) == 1, "logits: the columns of a row must be contiguous")
-    ld = logits.stride(0) if P > 1 else max(V, logits.stride(0))
+    _need(V == 1 or step == 1, "logits: the columns of a row must be contiguous")
+    if P <= 1:
+        ld = V
     _need(ld >= V, "logits: rows must not overlap")
     dev = logits.device
 
     def rows(t, dtype, name):
-        _need(t.device == dev and t.dtype == dtype and t.shape == (P,) and t.is_contiguous(),
-              f"{name}: contiguous {dtype} [{P}] on {dev}")
+        if not (t.dtype == dtype and t.dim() == 1 and t.shape[0] == P and t.is_contiguous() and t.device == dev):
+            raise ValueError(f"{name}: contiguous {dtype} [{P}] on {dev}")
         return t.data_ptr()
 
-    s = B.Sampling()
-    for name, value, dtype in (("temperature", temperature, torch.float32), ("top_k", top_k, torch.int32),
-                               ("top_p", top_p, torch.float32), ("min_p", min_p, torch.float32)):
+    s = B.Sampling(None, None, None, None, 1.0, 0, 1.0, 0.0)
+    for (name, dtype), value in zip(_SAMPLING, (temperature, top_k, top_p, min_p)):
         if isinstance(value, torch.Tensor):
             setattr(s, name, rows(value, dtype, name))
         else:
             setattr(s, name + "_all", int(value) if dtype == torch.int32 else float(value))
     if out is None:
         out = torch.empty((P,), dtype=torch.int32, device=dev)
-    rows(out, torch.int32, "out")
-    st = stream if stream is not None else torch.cuda.current_stream(dev)
-    with torch.cuda.device(dev):
+    else:
+        rows(out, torch.int32, "out")
+    with _on(dev):
         B.check(B.lib().swiftkv_sample(logits.data_ptr(), P, V, ld, C.byref(s), rows(u, torch.float32, "u"),
-                                       out.data_ptr(), st.cuda_stream))
+                                       out.data_ptr(), _stream_of(dev, stream)))
     return out

@@ -79,6 +79,8 @@ class ProfileEntry(C.Structure):
 def lib(path: str | None = None):
     """Builds (if stale) and opens libswiftkv.so."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             so = path or _build.build()

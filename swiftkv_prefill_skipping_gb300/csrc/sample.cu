@@ -81,14 +81,15 @@ struct alignas(16) Share {  // the slice behind it is written 16 bytes at a time
   u64 tab[TAB];
   unsigned limb[3][NB];         // 16-bit limbs of the bins while they are summed
   u64 warp_mass[SWARPS];
+  u64 sums[NB];                 // the cluster's sums of the bins this CTA scans
   float red_f[SWARPS];
   unsigned red_a[SWARPS], red_b[SWARPS];
   // read by the cluster's other CTAs
   float x_max;
   unsigned x_kmin, x_kmax, x_ties;
-  u64 x_mass;
+  u64 x_mass, x_sum;
   // the bin that a search found
-  int d_bin;
+  unsigned d_bin;
   u64 d_before;
 };
 
@@ -333,46 +334,76 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const SampleParams p) {
       sh.mass[b] = (u64)sh.limb[0][b] + ((u64)sh.limb[1][b] << 16) + ((u64)sh.limb[2][b] << 32);
     sync_all();
   };
-  // Every CTA sums the cluster's bins (thread t: bins 2t, 2t + 1) and finds the first bin, in
-  // descending order of the logits, at which the running sum reaches `want`; sums above it are
-  // returned in `before`. fraction >= 0: want is that part of all the bins (at least 1).
+  // The first bin, in descending order of the logits, at which the cluster's running sum reaches
+  // `want`; the sum above it is returned in `before`. fraction >= 0: want is that part of all the
+  // bins (at least 1). Each CTA sums its NB / C bins over the cluster's copies, so a bin crosses
+  // between CTAs once (all CTAs reading all bins took 3 us a search), and only the totals and the
+  // decision are exchanged after that.
   auto find = [&](u64& want, float fraction, u64& before) -> int {
-    u64 ms[2] = {0, 0};
+    constexpr int BPC = NB / C;
+    constexpr int PER = ST >= BPC ? ST / BPC : 1;  // threads per bin, each with C / PER copies
 #pragma unroll
-    for (unsigned c = 0; c < (unsigned)C; ++c)
+    for (int b = tid / PER; b < BPC; b += ST / PER) {
+      u64 x = 0;
 #pragma unroll
-      for (int e = 0; e < 2; ++e) ms[e] += ld_remote(&sh.mass[2 * tid + e], c);
-    u64 im = ms[0] + ms[1];
+      for (int c = 0; c < C / PER; ++c) x += ld_remote(&sh.mass[rank * BPC + b], (tid % PER) * (C / PER) + c);
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const u64 m2 = __shfl_up_sync(0xffffffffu, im, o);
-      if (lane >= o) im += m2;
+      for (int o = 1; o < PER; o <<= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+      if (tid % PER == 0) sh.sums[b] = x;
     }
-    if (lane == 31) sh.warp_mass[warp] = im;
-    if (tid == 0) sh.d_bin = 0;
     __syncthreads();
-    u64 bm = before + im - ms[0] - ms[1], all = 0;
+    constexpr int PL = BPC / 32;  // bins per lane of the scanning warp
+    u64 upto = 0;                 // of warp 0's lanes: their bins and all before, in this CTA
+    u64 mine = 0;
+    if (warp == 0) {
+#pragma unroll 4
+      for (int e = 0; e < PL; ++e) mine += sh.sums[lane * PL + e];
+      upto = mine;
 #pragma unroll
-    for (int w = 0; w < SWARPS; ++w) {
-      const u64 x = sh.warp_mass[w];
-      if (w < warp) bm += x;
-      all += x;
+      for (int o = 1; o < 32; o <<= 1) {
+        const u64 x = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += x;
+      }
+      if (lane == 31) sh.x_sum = upto;
+    }
+    sync_all();
+    u64 tot[C], all = 0;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      tot[c] = ld_remote(&sh.x_sum, c);
+      all += tot[c];
     }
     if (fraction >= 0.f) {
       const u64 c = ceil_mul(fraction, all);
       want = c > 0 ? c : 1;
     }
+    unsigned owner = 0;
+    u64 bm = before, first = before;
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      if (bm < want && want <= bm + ms[e]) {
-        sh.d_bin = 2 * tid + e;
-        sh.d_before = bm;
+    for (int c = 0; c < C; ++c) {
+      if (bm < want && want <= bm + tot[c]) {
+        owner = c;
+        first = bm;
       }
-      bm += ms[e];
+      bm += tot[c];
     }
-    sync_all();  // also: nobody still reads the bins
-    before = sh.d_before;
-    return sh.d_bin;
+    if (rank == owner && warp == 0) {
+      u64 x = first + upto - mine;
+      if (lane == 0) sh.d_bin = 0;
+      __syncwarp();
+      if (x < want && want <= x + mine)
+        for (int e = 0; e < PL; ++e) {
+          const u64 v = sh.sums[lane * PL + e];
+          if (x < want && want <= x + v) {
+            sh.d_bin = (unsigned)(rank * BPC + lane * PL + e);
+            sh.d_before = x;
+          }
+          x += v;
+        }
+    }
+    sync_all();
+    before = ld_remote(&sh.d_before, owner);
+    return (int)ld_remote(&sh.d_bin, owner);
   };
   // Smallest and largest key of the cluster's elements that pass `in`.
   auto key_range = [&](auto in, unsigned& lo, unsigned& hi) {
@@ -433,7 +464,6 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const SampleParams p) {
       const unsigned b = (unsigned)find(want, -1.f, before);
       hi -= b << s;
       lo = max(lo, hi - ((1u << s) - 1));
-      __syncthreads();  // everyone has read the decision
     }
     return lo;
   };
@@ -525,7 +555,6 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const SampleParams p) {
   for (int i = s0 + lane; i < s1; i += 32) sum += weight_fx(row[i], sc, sh.tab);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  __syncthreads();  // warp_mass of an earlier search has been read
   if (lane == 0) sh.warp_mass[warp] = sum;
   __syncthreads();
   u64 before = 0, total = 0;
