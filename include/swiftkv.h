@@ -211,6 +211,65 @@ int swiftkv_decode_step(swiftkv_model* m, const int32_t* tokens, const int32_t* 
                         int batch, const swiftkv_kv_pages* kv, float* logits,
                         int32_t* next_tokens, swiftkv_stream stream);
 
+/* ---- operators over the paged cache -------------------------------------------------------
+ * They take a model for its shape, its status word and its workspace; its weights need not be
+ * loaded. As every call on a model, calls that share one must be ordered on the GPU (one stream,
+ * or events between streams), graph replays among them. They can be captured into a CUDA graph:
+ * host arrays are read at the call and stay fixed in the graph, and a call whose workspace would
+ * have to grow is refused during a capture (SWIFTKV_ESTATE) - make one like it before. The model's
+ * device need not be the current one. num_seqs == 0 and chunks of no tokens are allowed.
+ *
+ * Visibility: chunk row i of sequence s sits at position p = ctx_lens[s] + i and sees the cached
+ * keys j <= p if window == 0; else those with j > p - window (the last `window` of them, its own
+ * among them) or j < sinks (the first tokens, which stay visible). Pages that no row of a chunk
+ * sees a key of are not read, whatever their block-table entry, and cached rows that no row sees
+ * may hold anything, NaN included. Visible rows must be finite. A needed entry outside
+ * [0, num_pages) sets SWIFTKV_STATUS_BAD_PAGE and leaves the rows that see it undefined. */
+
+/* Attention of a ragged batch of new tokens over cache `cache`, whose rows (the new tokens' own
+ * included) are already written:
+ *   out[i][h] = sum_j softmax_j(q[i][h] . k_j / sqrt(d_head)) v_j,   h reads KV head h / (n_q/n_kv)
+ *   q    device bf16 [T] rows of n_q*d_head, ldq elements apart (a multiple of 8; 16-byte aligned),
+ *        rotated already; T = cu_seqlens[num_seqs]
+ *   cu_seqlens, ctx_lens  HOST int32, as for swiftkv_forward
+ *   out  device bf16, rows ldo apart (same rules); must not overlap q
+ *   lse  device float [n_q][T] or NULL: natural log of sum_j exp(q . k_j / sqrt(d_head))
+ * Chunks of at most 4 rows run on the key-split kernel, longer ones in query tiles: tcgen05 for
+ * d_head 128 (mma.sync under swiftkv_set_attention_impl(m, 1)), mma.sync for d_head 64. */
+int swiftkv_attend(swiftkv_model* m, int cache, const void* q, int ldq, const int32_t* cu_seqlens,
+                   const int32_t* ctx_lens, int num_seqs, const swiftkv_kv_pages* kv, int window, int sinks,
+                   void* out, int ldo, float* lse, swiftkv_stream stream);
+
+/* Attention weight that each cached key received from the chunks' rows, per KV head: for every key
+ * that some row sees
+ *   scores[page][head][row] = decay * scores[page][head][row]
+ *       + sum over the rows that see it and the group's query heads of exp(q . k / sqrt(d_head) - lse)
+ * and every other entry stays as it is (decay 0 does not read the old value).
+ *   q, lse  as swiftkv_attend took and wrote them
+ *   scores  device float [num_pages][n_kv][16], the layout of the FP8 scale pools; 16-byte aligned
+ * Sequences of one call must not share pages they see. */
+int swiftkv_attention_weights(swiftkv_model* m, int cache, const void* q, int ldq, const float* lse,
+                              const int32_t* cu_seqlens, const int32_t* ctx_lens, int num_seqs,
+                              const swiftkv_kv_pages* kv, int window, int sinks, float decay, float* scores,
+                              swiftkv_stream stream);
+
+/* Shrinks each sequence to at most `keep` keys in cache `cache`, or in every cache (-1), for each
+ * KV head on its own: the first `sinks` and the last `recent` keys stay, and of the others those
+ * with the largest scores (ties: the earlier key; NaN ranks last). The kept keys move, in order, to
+ * rows 0.. of the destination, with their scores and FP8 scales; all other rows stay as they are.
+ * Sequence s then holds min(seq_lens[s], keep) keys; a shorter one keeps them all.
+ *   scores     HOST array [num_caches] of device float pools (those of the caches named are used)
+ *   seq_lens   HOST int32 [num_seqs]: keys held now
+ *   dst_block_table  device int32 [num_seqs][dst_max_pages], or NULL: in place. Its pages must not
+ *              be pages of any sequence's first seq_lens[s] keys; source pages are only read then,
+ *              so they may be shared (a common prefix). In place, no two sequences may share pages.
+ *   kept       device int32 [caches][num_seqs][n_kv][keep]: former indices, ascending, -1 behind them
+ * A block-table entry outside the pools among those a sequence needs sets SWIFTKV_STATUS_BAD_PAGE,
+ * leaves that sequence's rows as they are and its `kept` at -1. */
+int swiftkv_evict(swiftkv_model* m, int cache, const swiftkv_kv_pages* kv, float* const* scores,
+                  const int32_t* seq_lens, int num_seqs, int keep, int sinks, int recent,
+                  const int32_t* dst_block_table, int dst_max_pages, int32_t* kept, swiftkv_stream stream);
+
 /* How swiftkv_sample draws. Each setting is a device array with one value per row, or NULL and
  * one value for all rows in the *_all field. Order and meaning, with w_i = exp((l_i - max l) / T):
  *   temperature T <= 0 or NaN: the argmax, lowest id on ties (u and the rest are not used)

@@ -248,6 +248,112 @@ def _need(cond: bool, msg: str) -> None:
         raise ValueError(msg)
 
 
+def _chunks(cu_seqlens, ctx_lens, kv: KVCache):
+    """Host int32 arrays of a ragged batch, checked against the block table: (cu, ctx, P, T)."""
+    cu = np.ascontiguousarray(cu_seqlens, dtype=np.int32)
+    ctx = None if ctx_lens is None else np.ascontiguousarray(ctx_lens, dtype=np.int32)
+    P = len(cu) - 1
+    _need(cu.ndim == 1 and P >= 0, "cu_seqlens: [P + 1]")
+    _need(ctx is None or ctx.shape == (P,), f"ctx_lens: {P} entries")
+    _need(P <= kv.block_table.shape[0], f"{P} chunks, but the block table has {kv.block_table.shape[0]} rows")
+    return cu, ctx, P, int(cu[P])
+
+
+def _rows_of(t: torch.Tensor, T: int, model: Model, dev, name: str) -> int:
+    """Row stride of bf16 rows [T, n_q, d_h] (or [T, n_q * d_h]) whose heads are contiguous."""
+    s = model.shape
+    ok = t.dtype == torch.bfloat16 and t.device == dev and t.shape[0] == T and (
+        t.dim() == 3 and t.shape[1:] == (s.n_q, s.d_h) and t.stride(2) == 1 and (s.n_q == 1 or t.stride(1) == s.d_h)
+        or t.dim() == 2 and t.shape[1] == s.n_q * s.d_h and t.stride(1) == 1)
+    if not ok:
+        raise ValueError(f"{name}: bfloat16 [{T}, {s.n_q}, {s.d_h}] on {dev}, the heads of a row contiguous")
+    return t.stride(0) if T > 1 else s.n_q * s.d_h
+
+
+def attend(model: Model, q: torch.Tensor, cu_seqlens: Sequence[int], ctx_lens: Optional[Sequence[int]], kv: KVCache,
+           cache: int = 0, window: int = 0, sinks: int = 0, out: Optional[torch.Tensor] = None,
+           lse: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Attention of chunks of new tokens, q [T, n_q, d_h] bf16, over one cache of kv that already
+    holds their keys and values. Chunk s follows ctx_lens[s] cached tokens (None: none). A token at
+    position p sees positions <= p; with window > 0 only those above p - window, and the first
+    `sinks`. Returns out [T, n_q, d_h] bf16; lse (float32 [n_q, T]), if given, receives each row's
+    log-sum-exp, which attention_weights takes."""
+    cu, ctx, P, T = _chunks(cu_seqlens, ctx_lens, kv)
+    dev = kv.k.device
+    ldq = _rows_of(q, T, model, dev, "q")
+    if out is None:
+        out = torch.empty((T, model.shape.n_q, model.shape.d_h), dtype=torch.bfloat16, device=dev)
+    ldo = _rows_of(out, T, model, dev, "out")
+    if lse is not None:
+        _need(lse.dtype == torch.float32 and lse.device == dev and lse.shape == (model.shape.n_q, T) and
+              lse.is_contiguous(), f"lse: contiguous float32 [{model.shape.n_q}, {T}] on {dev}")
+    B.check(B.lib().swiftkv_attend(model.handle, cache, q.data_ptr(), ldq, cu.ctypes.data,
+                                   None if ctx is None else ctx.ctypes.data, P, C.byref(kv.pages), window, sinks,
+                                   out.data_ptr(), ldo, None if lse is None else lse.data_ptr(),
+                                   _stream_of(dev, stream)))
+    return out
+
+
+def attention_weights(model: Model, q: torch.Tensor, lse: torch.Tensor, cu_seqlens: Sequence[int],
+                      ctx_lens: Optional[Sequence[int]], kv: KVCache, scores: torch.Tensor, cache: int = 0,
+                      window: int = 0, sinks: int = 0, decay: float = 1.0, stream=None) -> torch.Tensor:
+    """Adds the attention weight that each cached key received from these tokens, summed over them
+    and the query heads of its KV head, to scores (float32 [num_pages, n_kv, 16], one per key of the
+    cache): scores = decay * scores + weight for every key some token sees, the others unchanged.
+    q and lse are those of the attend call before. Returns scores."""
+    cu, ctx, P, T = _chunks(cu_seqlens, ctx_lens, kv)
+    dev, s = kv.k.device, model.shape
+    ldq = _rows_of(q, T, model, dev, "q")
+    _need(lse.dtype == torch.float32 and lse.device == dev and lse.shape == (s.n_q, T) and lse.is_contiguous(),
+          f"lse: contiguous float32 [{s.n_q}, {T}] on {dev}")
+    _need(scores.dtype == torch.float32 and scores.device == dev and scores.shape == (kv.num_pages, s.n_kv, 16) and
+          scores.is_contiguous(), f"scores: contiguous float32 [{kv.num_pages}, {s.n_kv}, 16] on {dev}")
+    B.check(B.lib().swiftkv_attention_weights(model.handle, cache, q.data_ptr(), ldq, lse.data_ptr(), cu.ctypes.data,
+                                              None if ctx is None else ctx.ctypes.data, P, C.byref(kv.pages), window,
+                                              sinks, decay, scores.data_ptr(), _stream_of(dev, stream)))
+    return scores
+
+
+def evict(model: Model, kv: KVCache, scores: torch.Tensor, seq_lens: Sequence[int], keep: int, sinks: int = 0,
+          recent: int = 0, cache: Optional[int] = None, dst_block_table: Optional[torch.Tensor] = None,
+          kept: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Shrinks each sequence to at most `keep` keys, per cache and KV head: the first `sinks`, the
+    last `recent`, and of the others those with the largest scores (float32 [num_caches, num_pages,
+    n_kv, 16]; with `cache`, that cache's [num_pages, n_kv, 16]), ties to the earlier key. Kept rows
+    move in order to rows 0.. of the sequence's own pages, or of dst_block_table's (int32 [P, n],
+    pages no sequence uses now; the source is then only read). Returns kept, the former indices
+    [caches, P, n_kv, keep] int32, -1 behind a shorter list; sequence s then holds
+    min(seq_lens[s], keep) keys."""
+    sl = np.ascontiguousarray(seq_lens, dtype=np.int32)
+    P, dev, s = len(sl), kv.k.device, model.shape
+    _need(P <= kv.block_table.shape[0], f"{P} sequences, but the block table has {kv.block_table.shape[0]} rows")
+    _need(keep >= 1, "keep must be at least 1")
+    pool = (kv.num_pages, s.n_kv, 16)
+    n = kv.num_caches if cache is None else 1
+    _need(cache is None or 0 <= cache < kv.num_caches, f"cache {cache} of {kv.num_caches}")
+    _need(scores.dtype == torch.float32 and scores.device == dev and scores.is_contiguous() and
+          scores.shape == (pool if cache is not None else (n,) + pool),
+          f"scores: contiguous float32 {pool if cache is not None else (n,) + pool} on {dev}")
+    if dst_block_table is not None:
+        _need(dst_block_table.dtype == torch.int32 and dst_block_table.device == dev and dst_block_table.dim() == 2 and
+              dst_block_table.shape[0] >= P and dst_block_table.is_contiguous(),
+              f"dst_block_table: contiguous int32 [{P}, pages] on {dev}")
+    if kept is None:
+        kept = torch.empty((n, P, s.n_kv, keep), dtype=torch.int32, device=dev)
+    else:
+        _need(kept.dtype == torch.int32 and kept.device == dev and kept.shape == (n, P, s.n_kv, keep) and
+              kept.is_contiguous(), f"kept: contiguous int32 {(n, P, s.n_kv, keep)} on {dev}")
+    base, step, first = scores.data_ptr(), 4 * kv.num_pages * s.n_kv * 16, cache or 0
+    ptrs = (C.c_void_p * kv.num_caches)()
+    for c in range(n):
+        ptrs[first + c] = base + c * step
+    dst = dst_block_table
+    B.check(B.lib().swiftkv_evict(model.handle, -1 if cache is None else cache, C.byref(kv.pages), ptrs,
+                                  sl.ctypes.data, P, keep, sinks, recent, None if dst is None else dst.data_ptr(),
+                                  0 if dst is None else dst.shape[1], kept.data_ptr(), _stream_of(dev, stream)))
+    return kept
+
+
 _SAMPLING = (("temperature", torch.float32), ("top_k", torch.int32), ("top_p", torch.float32), ("min_p", torch.float32))
 
 

@@ -41,12 +41,15 @@ struct Sp {
   static constexpr int SMEM = SW * SSTAGES * STAGE * 2;
 };
 
-template <int D>
+// EXT (AttnExt): units list visible keys only and may start inside a page, qpos is indexed by item,
+// rows of a page outside the unit are staged as zeros, and the row's log-sum-exp is written.
+template <int D, bool EXT>
 __global__ void __launch_bounds__(SW * 32, 1) attn_split_kernel(
     const bf16* __restrict__ q, int ldq, const bf16* __restrict__ kpool, const bf16* __restrict__ vpool,
     const int* __restrict__ bt, int max_pages, int num_pages, const int* __restrict__ qpos,
     const int* __restrict__ rows, const int* __restrict__ seqs, const int* __restrict__ units, int num_units,
-    int n_q, int n_kv, bf16* __restrict__ out, int ldo, float* __restrict__ part, float scale_log2) {
+    const int* __restrict__ ubeg, int n_q, int n_kv, bf16* __restrict__ out, int ldo, float* __restrict__ part,
+    float scale_log2, const AttnExt ext) {
   using S = Sp<D>;
   constexpr int CH = D / 8;  // 16-byte chunks per row
   extern __shared__ __align__(128) unsigned char smem[];
@@ -60,7 +63,7 @@ __global__ void __launch_bounds__(SW * 32, 1) attn_split_kernel(
 
   auto swz = [](int row, int ch) { return row * D + ((ch ^ (row & 7)) * 8); };
   struct Geo {
-    int r, kvh, k_begin, k_end, p_begin, npages, nkeys;
+    int b, r, kvh, k_begin, k_end, p_begin, npages, nkeys;
     const int* btrow;
   };
   auto geo = [&](int v) {
@@ -68,9 +71,10 @@ __global__ void __launch_bounds__(SW * 32, 1) attn_split_kernel(
     const int u = v / n_kv;
     g.kvh = v - u * n_kv;
     const int b = units[3 * u];
+    g.b = b;
     g.r = rows ? rows[b] : b;
     const int sq = seqs ? seqs[b] : b;
-    g.nkeys = qpos[g.r] + 1;
+    g.nkeys = qpos[EXT ? b : g.r] + 1;
     g.k_begin = units[3 * u + 1];
     g.k_end = min(g.nkeys, g.k_begin + units[3 * u + 2]);
     g.p_begin = g.k_begin / kPageSize;
@@ -88,12 +92,15 @@ __global__ void __launch_bounds__(SW * 32, 1) attn_split_kernel(
       bf16* st = ring + lslot * S::STAGE;
       const int page = lg.btrow[lg.p_begin + lp];
       const bool ok = page >= 0 && page < num_pages;
+      if (EXT && !ok && lane == 0) atomicOr(ext.status, kStatusBadPage);
       const size_t base = ok ? ((size_t)page * n_kv + lg.kvh) * S::PAGE : 0;
 #pragma unroll
       for (int c = lane; c < kPageSize * CH; c += 32) {
         const int row = c / CH, ch = c % CH;
-        cp_async16(smem_u32(st + swz(row, ch)), kpool + base + row * D + ch * 8, ok ? 16 : 0);
-        cp_async16(smem_u32(st + S::PAGE + swz(row, ch)), vpool + base + row * D + ch * 8, ok ? 16 : 0);
+        const int key = (lg.p_begin + lp) * kPageSize + row;
+        const int bytes = ok && (!EXT || (key >= lg.k_begin && key < lg.k_end)) ? 16 : 0;
+        cp_async16(smem_u32(st + swz(row, ch)), kpool + base + row * D + ch * 8, bytes);
+        cp_async16(smem_u32(st + S::PAGE + swz(row, ch)), vpool + base + row * D + ch * 8, bytes);
       }
       if (lp == 0) {  // the unit's query heads ride with its first page
         const bf16* qsrc = q + (size_t)lg.r * ldq + (size_t)lg.kvh * G * D;
@@ -236,10 +243,12 @@ __global__ void __launch_bounds__(SW * 32, 1) attn_split_kernel(
       float s0 = l0;
 #pragma unroll
       for (int off = 1; off <= 2; off <<= 1) s0 += __shfl_xor_sync(0xffffffffu, s0, off);
-      const bool whole = cg.k_begin == 0 && cg.k_end == cg.nkeys;
+      const bool whole = EXT ? ubeg[cg.b + 1] - ubeg[cg.b] == 1 : cg.k_begin == 0 && cg.k_end == cg.nkeys;
       const int u = cv / n_kv;
       if (whole) {
         const float i0 = s0 > 0.f ? 1.f / s0 : 0.f;
+        if (EXT && ext.lse && g0 < G && (lane & 3) == 0)
+          ext.lse[(size_t)(cg.kvh * G + g0) * ext.ldl + cg.r] = (m0 + log2f(s0)) * 0.69314718055994531f;
         bf16* orow = out + (size_t)cg.r * ldo + (size_t)cg.kvh * G * D;
 #pragma unroll
         for (int n = 0; n < D / 8; ++n) {
@@ -287,13 +296,13 @@ struct Sp8 {
   static constexpr int CHB = D / 16;                  // 16-byte chunks per code row
 };
 
-template <int D>
+template <int D, bool EXT>
 __global__ void __launch_bounds__(SW * 32, 1) attn_split_fp8_kernel(
     const bf16* __restrict__ q, int ldq, const uint8_t* __restrict__ kpool, const uint8_t* __restrict__ vpool,
     const float* __restrict__ kscale, const float* __restrict__ vscale, const int* __restrict__ bt, int max_pages,
     int num_pages, const int* __restrict__ qpos, const int* __restrict__ rows, const int* __restrict__ seqs,
-    const int* __restrict__ units, int num_units, int n_q, int n_kv, bf16* __restrict__ out, int ldo,
-    float* __restrict__ part, float scale_log2) {
+    const int* __restrict__ units, int num_units, const int* __restrict__ ubeg, int n_q, int n_kv,
+    bf16* __restrict__ out, int ldo, float* __restrict__ part, float scale_log2, const AttnExt ext) {
   using S = Sp8<D>;
   extern __shared__ __align__(128) unsigned char smem[];
   griddep_launch_dependents();
@@ -311,7 +320,7 @@ __global__ void __launch_bounds__(SW * 32, 1) attn_split_fp8_kernel(
   };
   auto swzq = [](int row, int ch) { return row * D + ((ch ^ (row & 7)) * 8); };  // bf16 elements
   struct Geo {
-    int r, kvh, k_begin, k_end, p_begin, npages, nkeys;
+    int b, r, kvh, k_begin, k_end, p_begin, npages, nkeys;
     const int* btrow;
   };
   auto geo = [&](int v) {
@@ -319,9 +328,10 @@ __global__ void __launch_bounds__(SW * 32, 1) attn_split_fp8_kernel(
     const int u = v / n_kv;
     g.kvh = v - u * n_kv;
     const int b = units[3 * u];
+    g.b = b;
     g.r = rows ? rows[b] : b;
     const int sq = seqs ? seqs[b] : b;
-    g.nkeys = qpos[g.r] + 1;
+    g.nkeys = qpos[EXT ? b : g.r] + 1;
     g.k_begin = units[3 * u + 1];
     g.k_end = min(g.nkeys, g.k_begin + units[3 * u + 2]);
     g.p_begin = g.k_begin / kPageSize;
@@ -338,12 +348,15 @@ __global__ void __launch_bounds__(SW * 32, 1) attn_split_fp8_kernel(
       unsigned char* st = ring + lslot * S::STAGE;
       const int page = lg.btrow[lg.p_begin + lp];
       const bool ok = page >= 0 && page < num_pages;
+      if (EXT && !ok && lane == 0) atomicOr(ext.status, kStatusBadPage);
       const size_t blk = ok ? (size_t)page * n_kv + lg.kvh : 0;
 #pragma unroll
       for (int c = lane; c < kPageSize * S::CHB; c += 32) {
         const int row = c / S::CHB, ch = c % S::CHB;
-        cp_async16(smem_u32(st + swzb(row, ch)), kpool + blk * S::CODES + row * D + ch * 16, ok ? 16 : 0);
-        cp_async16(smem_u32(st + S::CODES + swzb(row, ch)), vpool + blk * S::CODES + row * D + ch * 16, ok ? 16 : 0);
+        const int key = (lg.p_begin + lp) * kPageSize + row;
+        const int bytes = ok && (!EXT || (key >= lg.k_begin && key < lg.k_end)) ? 16 : 0;
+        cp_async16(smem_u32(st + swzb(row, ch)), kpool + blk * S::CODES + row * D + ch * 16, bytes);
+        cp_async16(smem_u32(st + S::CODES + swzb(row, ch)), vpool + blk * S::CODES + row * D + ch * 16, bytes);
       }
       if (lane < 8) {  // 16 K scales, then 16 V scales
         const float* sp = (lane < 4 ? kscale : vscale) + blk * kPageSize + (lane & 3) * 4;
@@ -475,7 +488,7 @@ __global__ void __launch_bounds__(SW * 32, 1) attn_split_fp8_kernel(
       for (int e = 0; e < 2; ++e) {
         const float p = exp2f(sc[t][e] - m0);
         ps0 += p;
-        pv[t][e] = p * (sv[8 * t + 2 * qd + e] * isref);
+        pv[t][e] = EXT && p == 0.f ? 0.f : p * (sv[8 * t + 2 * qd + e] * isref);  // a masked key's scale may be NaN
       }
     l0 += ps0;
     uint32_t pa[4];
@@ -507,11 +520,13 @@ __global__ void __launch_bounds__(SW * 32, 1) attn_split_fp8_kernel(
       float s0 = l0;
 #pragma unroll
       for (int off = 1; off <= 2; off <<= 1) s0 += __shfl_xor_sync(0xffffffffu, s0, off);
-      const bool whole = cg.k_begin == 0 && cg.k_end == cg.nkeys;
+      const bool whole = EXT ? ubeg[cg.b + 1] - ubeg[cg.b] == 1 : cg.k_begin == 0 && cg.k_end == cg.nkeys;
       const int u = cv / n_kv;
       if (g0 < G) {
         if (whole) {
           const float f = s0 > 0.f ? sref / s0 : 0.f;
+          if (EXT && ext.lse && qd == 0)
+            ext.lse[(size_t)(cg.kvh * G + g0) * ext.ldl + cg.r] = (m0 + log2f(s0)) * 0.69314718055994531f;
           bf16* orow = out + (size_t)cg.r * ldo + (size_t)(cg.kvh * G + g0) * D;
 #pragma unroll
           for (int c = 0; c < D / 16; ++c) {
@@ -548,7 +563,8 @@ template <int D>
 __global__ void __launch_bounds__(CMB_THREADS) attn_split_combine(const int* __restrict__ rows,
                                                                   const int* __restrict__ ubeg, int n_q, int n_kv,
                                                                   const float* __restrict__ part,
-                                                                  bf16* __restrict__ out, int ldo) {
+                                                                  bf16* __restrict__ out, int ldo,
+                                                                  float* __restrict__ lse, int ldl) {
   __shared__ float s_w[CMB_MAX_W];
   __shared__ float s_mx[SMAXG], s_den[SMAXG];
   griddep_launch_dependents();
@@ -583,6 +599,7 @@ __global__ void __launch_bounds__(CMB_THREADS) attn_split_combine(const int* __r
     if (lane == 0) {
       s_mx[g] = mx;
       s_den[g] = den;
+      if (lse) lse[(size_t)(kvh * G + g) * ldl + r] = (mx + log2f(den)) * 0.69314718055994531f;
     }
   }
   __syncthreads();
@@ -607,50 +624,50 @@ __global__ void __launch_bounds__(CMB_THREADS) attn_split_combine(const int* __r
   }
 }
 
-template <int D>
+template <int D, bool EXT>
 cudaError_t split_d(const bf16* q, int ldq, const bf16* k_pool, const bf16* v_pool, const int* bt, int max_pages,
                     int num_pages, const int* qpos, const int* rows, const int* seqs, const SplitPlan& plan,
-                    int n_q, int n_kv, bf16* out, int ldo, int num_sms, cudaStream_t stream) {
+                    int n_q, int n_kv, bf16* out, int ldo, int num_sms, cudaStream_t stream, const AttnExt& ext) {
   constexpr int smem = Sp<D>::SMEM;
   static_assert(smem <= 227 * 1024, "rings must fit in shared memory");
   static PerDeviceOnce smem_attr;
   {
-    cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void*>(attn_split_kernel<D>), smem, smem_attr);
+    cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void*>(attn_split_kernel<D, EXT>), smem, smem_attr);
     if (e != cudaSuccess) return e;
   }
   const float scale_log2 = 1.4426950408889634f / sqrtf((float)D);
   const int total = plan.num_units * n_kv;
   const int ctas = std::min((total + SW - 1) / SW, num_sms);
-  cudaError_t e = launch_pdl(attn_split_kernel<D>, dim3(ctas), dim3(SW * 32), smem, stream, q, ldq, k_pool, v_pool,
-                             bt, max_pages, num_pages, qpos, rows, seqs, (const int*)plan.units, plan.num_units, n_q,
-                             n_kv, out, ldo, plan.part, scale_log2);
+  cudaError_t e = launch_pdl(attn_split_kernel<D, EXT>, dim3(ctas), dim3(SW * 32), smem, stream, q, ldq, k_pool, v_pool,
+                             bt, max_pages, num_pages, qpos, rows, seqs, (const int*)plan.units, plan.num_units,
+                             (const int*)plan.ubeg, n_q, n_kv, out, ldo, plan.part, scale_log2, ext);
   if (e != cudaSuccess || !plan.any_split) return e;
   return launch_pdl(attn_split_combine<D>, dim3(plan.num_items, n_kv), dim3(CMB_THREADS), 0, stream, rows,
-                    (const int*)plan.ubeg, n_q, n_kv, (const float*)plan.part, out, ldo);
+                    (const int*)plan.ubeg, n_q, n_kv, (const float*)plan.part, out, ldo, ext.lse, ext.ldl);
 }
 
-template <int D>
+template <int D, bool EXT>
 cudaError_t split_fp8_d(const bf16* q, int ldq, const uint8_t* k8, const uint8_t* v8, const float* ks,
                         const float* vs, const int* bt, int max_pages, int num_pages, const int* qpos,
                         const int* rows, const int* seqs, const SplitPlan& plan, int n_q, int n_kv, bf16* out,
-                        int ldo, int num_sms, cudaStream_t stream) {
+                        int ldo, int num_sms, cudaStream_t stream, const AttnExt& ext) {
   constexpr int smem = Sp8<D>::SMEM;
   static_assert(smem <= 227 * 1024, "rings must fit in shared memory");
   static_assert(Sp8<D>::STAGE % 16 == 0, "ring slots must keep 16-byte alignment");
   static PerDeviceOnce smem_attr;
   {
-    cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void*>(attn_split_fp8_kernel<D>), smem, smem_attr);
+    cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void*>(attn_split_fp8_kernel<D, EXT>), smem, smem_attr);
     if (e != cudaSuccess) return e;
   }
   const float scale_log2 = 1.4426950408889634f / sqrtf((float)D);
   const int total = plan.num_units * n_kv;
   const int ctas = std::min((total + SW - 1) / SW, num_sms);
-  cudaError_t e = launch_pdl(attn_split_fp8_kernel<D>, dim3(ctas), dim3(SW * 32), smem, stream, q, ldq, k8, v8, ks,
+  cudaError_t e = launch_pdl(attn_split_fp8_kernel<D, EXT>, dim3(ctas), dim3(SW * 32), smem, stream, q, ldq, k8, v8, ks,
                              vs, bt, max_pages, num_pages, qpos, rows, seqs, (const int*)plan.units, plan.num_units,
-                             n_q, n_kv, out, ldo, plan.part, scale_log2);
+                             (const int*)plan.ubeg, n_q, n_kv, out, ldo, plan.part, scale_log2, ext);
   if (e != cudaSuccess || !plan.any_split) return e;
   return launch_pdl(attn_split_combine<D>, dim3(plan.num_items, n_kv), dim3(CMB_THREADS), 0, stream, rows,
-                    (const int*)plan.ubeg, n_q, n_kv, (const float*)plan.part, out, ldo);
+                    (const int*)plan.ubeg, n_q, n_kv, (const float*)plan.part, out, ldo, ext.lse, ext.ldl);
 }
 
 }  // namespace
@@ -659,15 +676,16 @@ cudaError_t launch_attention_decode_split_fp8(const bf16* q, int ldq, const uint
                                               const float* k_scale, const float* v_scale, const int* block_table,
                                               int max_pages, int num_pages, const int* qpos, const int* rows,
                                               const int* seqs, const SplitPlan& plan, int n_q, int n_kv, int d_head,
-                                              bf16* out, int ldo, int num_sms, cudaStream_t stream) {
+                                              bf16* out, int ldo, int num_sms, cudaStream_t stream,
+                                              const AttnExt* ext) {
   if (plan.num_units <= 0) return cudaSuccess;
   if (n_q % n_kv || n_q / n_kv > SMAXG) return cudaErrorNotSupported;
-  if (d_head == 128)
-    return split_fp8_d<128>(q, ldq, k8, v8, k_scale, v_scale, block_table, max_pages, num_pages, qpos, rows, seqs,
-                            plan, n_q, n_kv, out, ldo, num_sms, stream);
-  if (d_head == 64)
-    return split_fp8_d<64>(q, ldq, k8, v8, k_scale, v_scale, block_table, max_pages, num_pages, qpos, rows, seqs,
-                           plan, n_q, n_kv, out, ldo, num_sms, stream);
+  auto run = [&](auto kernel) {
+    return kernel(q, ldq, k8, v8, k_scale, v_scale, block_table, max_pages, num_pages, qpos, rows, seqs, plan, n_q,
+                  n_kv, out, ldo, num_sms, stream, ext ? *ext : AttnExt());
+  };
+  if (d_head == 128) return ext ? run(split_fp8_d<128, true>) : run(split_fp8_d<128, false>);
+  if (d_head == 64) return ext ? run(split_fp8_d<64, true>) : run(split_fp8_d<64, false>);
   return cudaErrorNotSupported;
 }
 
@@ -687,21 +705,46 @@ void split_plan_host(const int* nkeys, int items, std::vector<int>* units, std::
   }
 }
 
+void split_plan_host_window(const int* qpos, int items, int window, int sinks, std::vector<int>* units,
+                            std::vector<int>* ubeg) {
+  units->clear();
+  ubeg->assign(1, 0);
+  for (int b = 0; b < items; ++b) {
+    const int end = qpos[b] + 1, w0 = window_begin(qpos[b], window);
+    const int s1 = window > 0 && w0 > 0 ? std::min(sinks, w0) : 0;  // keys [0, s1) and [w0, end)
+    const int first = s1 == w0 ? 0 : w0;                            // sinks that reach the window join it
+    const int split = split_keys_for(end - first + (first ? s1 : 0));
+    auto range = [&](int k0, int k1) {
+      while (k0 < k1) {  // units end on multiples of the split, so that only a range's first is ragged
+        const int e = std::min(k1, (k0 / split + 1) * split);
+        units->push_back(b);
+        units->push_back(k0);
+        units->push_back(e - k0);
+        k0 = e;
+      }
+    };
+    if (first) range(0, s1);
+    range(first, end);
+    ubeg->push_back((int)(units->size() / 3));
+  }
+}
+
 size_t split_part_floats(int num_units, int n_q, int d_head) { return (size_t)num_units * n_q * (d_head + 2); }
 
 cudaError_t launch_attention_decode_split(const bf16* q, int ldq, const bf16* k_pool, const bf16* v_pool,
                                           const int* block_table, int max_pages, int num_pages, const int* qpos,
                                           const int* rows, const int* seqs, const SplitPlan& plan, int n_q,
-                                          int n_kv, int d_head, bf16* out, int ldo, int num_sms, cudaStream_t stream) {
+                                          int n_kv, int d_head, bf16* out, int ldo, int num_sms, cudaStream_t stream,
+                                          const AttnExt* ext) {
   if (plan.num_units <= 0) return cudaSuccess;
   // a group of more than 8 query heads takes the one-CTA-per-row kernel
   if (n_q % n_kv || n_q / n_kv > SMAXG) return cudaErrorNotSupported;
-  if (d_head == 128)
-    return split_d<128>(q, ldq, k_pool, v_pool, block_table, max_pages, num_pages, qpos, rows, seqs, plan, n_q,
-                        n_kv, out, ldo, num_sms, stream);
-  if (d_head == 64)
-    return split_d<64>(q, ldq, k_pool, v_pool, block_table, max_pages, num_pages, qpos, rows, seqs, plan, n_q,
-                       n_kv, out, ldo, num_sms, stream);
+  auto run = [&](auto kernel) {
+    return kernel(q, ldq, k_pool, v_pool, block_table, max_pages, num_pages, qpos, rows, seqs, plan, n_q, n_kv, out,
+                  ldo, num_sms, stream, ext ? *ext : AttnExt());
+  };
+  if (d_head == 128) return ext ? run(split_d<128, true>) : run(split_d<128, false>);
+  if (d_head == 64) return ext ? run(split_d<64, true>) : run(split_d<64, false>);
   return cudaErrorNotSupported;
 }
 

@@ -1,0 +1,293 @@
+// Eviction from the paged cache by accumulated attention weight. Per (cache, sequence, KV head)
+// with n keys: the first `sinks` and the last `recent` stay, and of the others those with the
+// largest scores (ties: lower index first; NaN ranks last), `keep` in all; the kept keys move, in
+// order, to rows 0 .. of the destination pages, K, V, FP8 scales and scores alike.
+//
+// evict_select_kernel: one CTA per list. Scores become order-preserving 32-bit keys in shared
+// memory (protected keys the largest); four rounds of 256-bin histograms find the keep-th largest
+// key, and one ordered pass writes the kept indices, ties by index. The floats of a kept key (its
+// score, FP8 scales) move here.
+// evict_move_kernel: the bound, HBM: kept rows are read once and written once. To other pages, CTAs
+// split the kept list freely. In place every destination row lies at or below its source, so a CTA
+// walks one list in order: a chunk is loaded whole before any of it is written, and the next chunk
+// is loaded before that, which only reads rows that no earlier write reaches. Rows of a list are
+// cut into 64-byte columns, each its own CTA, so that one sequence still fills the GPU.
+#include <climits>
+
+#include "common.cuh"
+#include "pdl.cuh"
+#include "serving.h"
+
+namespace skv {
+
+namespace {
+
+constexpr int ET = 512;               // threads of the selection
+constexpr int EWARPS = ET / 32;
+constexpr int kSelectSmemKeys = 49152;  // lists up to this long keep their keys in shared memory
+
+// Order-preserving map of scores; NaN is the least, and only protected keys are UINT_MAX.
+__device__ __forceinline__ unsigned score_key(float x) {
+  if (x != x) return 0;
+  const unsigned b = __float_as_uint(x + 0.f);
+  return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+
+struct List {
+  int c, s, h, n;  // cache (within the call), sequence, KV head, keys
+};
+__device__ __forceinline__ List list_at(const EvictArgs& a, int i) {
+  List l;
+  l.h = i % a.n_kv;
+  l.s = i / a.n_kv % a.P;
+  l.c = i / a.n_kv / a.P;
+  l.n = a.lens[l.s];
+  return l;
+}
+// Row index (page, head, slot) of key j of a list in the pools, -1 on a page outside them.
+__device__ __forceinline__ long long row_of(const int* bt, int width, int num_pages, int n_kv, const List& l, int j) {
+  const int page = bt[(size_t)l.s * width + (j >> 4)];
+  if (page < 0 || page >= num_pages) return -1;
+  return ((long long)page * n_kv + l.h) * kPageSize + (j & 15);
+}
+
+__global__ void __launch_bounds__(ET) evict_select_kernel(const EvictArgs a, int in_smem) {
+  extern __shared__ unsigned keys[];  // [n] when in_smem
+  __shared__ unsigned hist[256];
+  __shared__ unsigned s_key, s_left;
+  __shared__ int s_cnt[2][EWARPS];
+  griddep_launch_dependents();
+  griddep_wait();
+  const List l = list_at(a, blockIdx.x);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const float* scores = a.scores[a.first_cache + l.c];
+  int* kept = a.kept + (size_t)blockIdx.x * a.keep;
+  const int n = l.n;
+  auto key_at = [&](int j) -> unsigned {
+    if (j < a.sinks || j >= n - a.recent) return UINT_MAX;
+    const long long r = row_of(a.src_bt, a.src_pages, a.num_pages, a.n_kv, l, j);
+    return r < 0 ? 0u : score_key(scores[r]);
+  };
+  // an entry outside the pool: the status says so, and the list is left as it is
+  int bad = 0;
+  const int out_pages = (min(n, a.keep) + kPageSize - 1) / kPageSize;
+  for (int p = tid; p < (n + kPageSize - 1) / kPageSize; p += ET) {
+    const int page = a.src_bt[(size_t)l.s * a.src_pages + p];
+    bad |= page < 0 || page >= a.num_pages;
+  }
+  for (int p = tid; p < out_pages; p += ET) {
+    const int page = a.dst_bt[(size_t)l.s * a.dst_pages + p];
+    bad |= page < 0 || page >= a.num_pages;
+  }
+  if (__syncthreads_or(bad)) {
+    if (tid == 0) atomicOr(a.status, kStatusBadPage);
+    for (int i = tid; i < a.keep; i += ET) kept[i] = -1;
+    return;
+  }
+  if (n <= a.keep) {
+    for (int i = tid; i < a.keep; i += ET) kept[i] = i < n ? i : -1;
+  } else {
+    if (in_smem) {
+      for (int j = tid; j < n; j += ET) keys[j] = key_at(j);
+      __syncthreads();
+    }
+    auto key = [&](int j) { return in_smem ? keys[j] : key_at(j); };
+    // the keep-th largest key, eight bits a round
+    unsigned prefix = 0, left = (unsigned)a.keep;
+    for (int shift = 24; shift >= 0; shift -= 8) {
+      for (int b = tid; b < 256; b += ET) hist[b] = 0;
+      __syncthreads();
+      const unsigned mask = shift == 24 ? 0u : ~0u << (shift + 8);
+      for (int j0 = 0; j0 < n; j0 += ET) {
+        const int j = j0 + tid;
+        const unsigned k = j < n ? key(j) : 0u;
+        const bool in = j < n && (k & mask) == prefix;
+        const unsigned b = (k >> shift) & 255u;
+        // scores share their leading bits: one add per distinct bin of the warp
+        const unsigned peers = __match_any_sync(0xffffffffu, in ? b : 256u);
+        if (in && (peers & ((1u << lane) - 1)) == 0) atomicAdd(&hist[b], (unsigned)__popc(peers));
+      }
+      __syncthreads();
+      if (warp == 0) {  // lane: bins 255 - 8 lane .. down
+        unsigned c = 0;
+        for (int e = 0; e < 8; ++e) c += hist[255 - 8 * lane - e];
+        unsigned upto = c;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const unsigned x = __shfl_up_sync(0xffffffffu, upto, o);
+          if (lane >= o) upto += x;
+        }
+        unsigned before = upto - c;
+        for (int e = 0; e < 8; ++e) {
+          const unsigned v = hist[255 - 8 * lane - e];
+          if (before < left && left <= before + v) {
+            s_key = prefix | ((unsigned)(255 - 8 * lane - e) << shift);
+            s_left = left - before;
+          }
+          before += v;
+        }
+      }
+      __syncthreads();
+      prefix = s_key;
+      left = s_left;
+    }
+    // ordered pass: everything above the key, and the first `left` at it
+    int above = 0, ties = 0;  // before this round
+    for (int j0 = 0; j0 < n; j0 += ET) {
+      const int j = j0 + tid, par = (j0 / ET) & 1;
+      const unsigned k = j < n ? key(j) : 0u;
+      const unsigned gt = __ballot_sync(0xffffffffu, j < n && k > prefix);
+      const unsigned eq = __ballot_sync(0xffffffffu, j < n && k == prefix);
+      if (lane == 0) s_cnt[par][warp] = __popc(gt) | __popc(eq) << 16;
+      __syncthreads();
+      int g0 = 0, e0 = 0, gs = 0, es = 0;
+#pragma unroll
+      for (int w = 0; w < EWARPS; ++w) {
+        const int c = s_cnt[par][w];
+        if (w < warp) {
+          g0 += c & 0xffff;
+          e0 += c >> 16;
+        }
+        gs += c & 0xffff;
+        es += c >> 16;
+      }
+      const unsigned below = (1u << lane) - 1;
+      const int my_gt = above + g0 + __popc(gt & below), my_eq = ties + e0 + __popc(eq & below);
+      const bool is_gt = gt >> lane & 1, is_eq = eq >> lane & 1;
+      if (is_gt || (is_eq && my_eq < (int)left)) kept[my_gt + min(my_eq, (int)left)] = j;
+      above += gs;
+      ties += es;
+    }
+  }
+  __syncthreads();  // kept, written by this CTA, is read below
+  // the kept keys' floats; a round is read whole before it is written (in place, rows move down)
+  const int m = min(n, a.keep);
+  const int c = a.first_cache + l.c;
+  float* arrays[3] = {a.scores[c], a.ks ? a.ks[c] : nullptr, a.vs ? a.vs[c] : nullptr};
+  for (int i0 = 0; i0 < m; i0 += ET) {
+    const int i = i0 + tid;
+    float v[3];
+    long long to = -1;
+    if (i < m) {
+      const long long from = row_of(a.src_bt, a.src_pages, a.num_pages, a.n_kv, l, kept[i]);
+      to = row_of(a.dst_bt, a.dst_pages, a.num_pages, a.n_kv, l, i);
+#pragma unroll
+      for (int t = 0; t < 3; ++t)
+        if (arrays[t]) v[t] = arrays[t][from];
+    }
+    __syncthreads();
+    if (to >= 0)
+#pragma unroll
+      for (int t = 0; t < 3; ++t)
+        if (arrays[t]) arrays[t][to] = v[t];
+  }
+}
+
+constexpr int MT = 256;  // threads of the move
+
+// To other pages: CTA (list, part of the kept list); K and V of a row by neighbouring threads.
+constexpr int kPartBytes = 32768;
+__global__ void __launch_bounds__(MT) evict_copy_kernel(const EvictArgs a, int parts) {
+  griddep_launch_dependents();
+  griddep_wait();
+  const int li = blockIdx.x / parts, part = blockIdx.x - li * parts;
+  const List l = list_at(a, li);
+  const int* kept = a.kept + (size_t)li * a.keep;
+  const int vecs = a.row_bytes / 16, rows = kPartBytes / a.row_bytes;
+  const int i0 = part * rows, i1 = min(min(l.n, a.keep), i0 + rows);
+  unsigned char* k = a.k[a.first_cache + l.c];
+  unsigned char* v = a.v[a.first_cache + l.c];
+  const int count = (i1 - i0) * vecs;
+  constexpr int U = 4;
+  for (int e0 = threadIdx.x; e0 < count; e0 += MT * U) {
+    uint4 x[U], y[U];
+    long long to[U];
+#pragma unroll
+    for (int t = 0; t < U; ++t) {
+      const int e = e0 + t * MT;
+      to[t] = -1;
+      if (e < count) {
+        const int i = i0 + e / vecs, src = kept[i];
+        if (src >= 0) {
+          const size_t off = (size_t)row_of(a.src_bt, a.src_pages, a.num_pages, a.n_kv, l, src) * a.row_bytes + e % vecs * 16;
+          x[t] = __ldcs(reinterpret_cast<const uint4*>(k + off));
+          y[t] = __ldcs(reinterpret_cast<const uint4*>(v + off));
+          to[t] = row_of(a.dst_bt, a.dst_pages, a.num_pages, a.n_kv, l, i) * a.row_bytes + e % vecs * 16;
+        }
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < U; ++t)
+      if (to[t] >= 0) {
+        *reinterpret_cast<uint4*>(k + to[t]) = x[t];
+        *reinterpret_cast<uint4*>(v + to[t]) = y[t];
+      }
+  }
+}
+
+// In place: CTA (list, K or V, 64-byte column). 4 threads a row, 64 U rows a chunk, the next chunk
+// loaded before the current one is written.
+__global__ void __launch_bounds__(MT) evict_shift_kernel(const EvictArgs a, int cols) {
+  griddep_launch_dependents();
+  griddep_wait();
+  constexpr int U = 8, RPC = MT / 4 * U;
+  const int col = blockIdx.x % cols, sel = blockIdx.x / cols % 2, li = blockIdx.x / cols / 2;
+  const List l = list_at(a, li);
+  const int* kept = a.kept + (size_t)li * a.keep;
+  const int m = min(l.n, a.keep);
+  unsigned char* pool = (sel ? a.v : a.k)[a.first_cache + l.c];
+  const size_t at = col * 64 + threadIdx.x % 4 * 16;  // this thread's 16 bytes of a row
+  uint4 x[U], y[U];
+  auto row_off = [&](const int* bt, int width, int j) {
+    return (size_t)row_of(bt, width, a.num_pages, a.n_kv, l, j) * a.row_bytes + at;
+  };
+  // chunk c of the list: kept rows that move (src > i; a row at its place stays untouched)
+  auto load = [&](int c, uint4* v) {
+#pragma unroll
+    for (int t = 0; t < U; ++t) {
+      const int i = c * RPC + t * (MT / 4) + threadIdx.x / 4;
+      const int src = i < m ? kept[i] : -1;
+      if (src > i) v[t] = *reinterpret_cast<const uint4*>(pool + row_off(a.src_bt, a.src_pages, src));
+    }
+  };
+  auto store = [&](int c, const uint4* v) {
+#pragma unroll
+    for (int t = 0; t < U; ++t) {
+      const int i = c * RPC + t * (MT / 4) + threadIdx.x / 4;
+      const int src = i < m ? kept[i] : -1;
+      if (src > i) *reinterpret_cast<uint4*>(pool + row_off(a.dst_bt, a.dst_pages, i)) = v[t];
+    }
+  };
+  const int chunks = (m + RPC - 1) / RPC;
+  if (chunks > 0) load(0, x);
+  for (int c = 0; c < chunks; c += 2) {
+    if (c + 1 < chunks) load(c + 1, y);
+    __syncthreads();  // every thread holds its rows of chunk c
+    store(c, x);
+    if (c + 1 >= chunks) break;
+    if (c + 2 < chunks) load(c + 2, x);
+    __syncthreads();
+    store(c + 1, y);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_evict(const EvictArgs& a, int max_len, cudaStream_t s) {
+  const long long lists = (long long)a.num_caches * a.P * a.n_kv;
+  const int parts = (int)(((long long)a.keep * a.row_bytes + kPartBytes - 1) / kPartBytes);
+  const int cols = a.row_bytes / 64;
+  const long long ctas = a.in_place ? lists * 2 * cols : lists * parts;
+  if (lists <= 0) return cudaSuccess;
+  if (ctas > INT_MAX || a.row_bytes % 64) return cudaErrorNotSupported;
+  static PerDeviceOnce once;
+  cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void*>(evict_select_kernel), kSelectSmemKeys * 4, once);
+  if (e != cudaSuccess) return e;
+  const int in_smem = max_len <= kSelectSmemKeys;
+  e = launch_pdl(evict_select_kernel, dim3((unsigned)lists), dim3(ET), in_smem ? (size_t)max_len * 4 : 0, s, a, in_smem);
+  if (e != cudaSuccess) return e;
+  if (a.in_place) return launch_pdl(evict_shift_kernel, dim3((unsigned)ctas), dim3(MT), 0, s, a, cols);
+  return launch_pdl(evict_copy_kernel, dim3((unsigned)ctas), dim3(MT), 0, s, a, parts);
+}
+
+}  // namespace skv

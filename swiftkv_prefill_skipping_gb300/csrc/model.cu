@@ -14,13 +14,14 @@
 #include <nvtx3/nvToolsExt.h>
 
 #include "launch.h"
+#include "model_state.h"
 #include "swiftkv.h"
 
 using namespace skv;
 
-namespace {
+namespace skv {
 
-thread_local std::string g_err;
+static thread_local std::string g_err;
 
 int fail(int code, const char* fmt, ...) {
   char buf[512];
@@ -31,31 +32,31 @@ int fail(int code, const char* fmt, ...) {
   g_err = buf;
   return code;
 }
+int set_error(int code, const char* msg) { return fail(code, "%s", msg); }
 
-#define CK(call)                                                                              \
-  do {                                                                                        \
-    cudaError_t e_ = (call);                                                                  \
-    if (e_ != cudaSuccess) return fail(SWIFTKV_ECUDA, "%s: %s", #call, cudaGetErrorString(e_)); \
-  } while (0)
+int check_kv(const swiftkv_model* m, const swiftkv_kv_pages* kv) {
+  if (!kv || !kv->k_pool || !kv->v_pool || !kv->block_table) return fail(SWIFTKV_EINVAL, "null kv pages");
+  if (kv->num_caches != m->C) return fail(SWIFTKV_EINVAL, "num_caches %d != %d", kv->num_caches, m->C);
+  if (kv->page_size != kPageSize) return fail(SWIFTKV_EINVAL, "page_size must be 16");
+  if (kv->num_pages < 1 || kv->max_pages_per_seq < 1) return fail(SWIFTKV_EINVAL, "empty page pool");
+  for (int c = 0; c < m->C; ++c)
+    if (!kv->k_pool[c] || !kv->v_pool[c]) return fail(SWIFTKV_EINVAL, "null pool pointer for cache %d", c);
+  if (kv->kv_dtype != 0 && kv->kv_dtype != 1) return fail(SWIFTKV_EINVAL, "kv_dtype %d", kv->kv_dtype);
+  if (kv->kv_dtype == 1) {
+    if (!kv->k_scale || !kv->v_scale) return fail(SWIFTKV_EINVAL, "fp8 cache without scale pools");
+    for (int c = 0; c < m->C; ++c)
+      if (!kv->k_scale[c] || !kv->v_scale[c]) return fail(SWIFTKV_EINVAL, "null scale pool for cache %d", c);
+    if (m->cfg.n_q / m->cfg.n_kv > 8)
+      return fail(SWIFTKV_EUNSUPPORTED, "fp8 cache needs at most 8 query heads per KV head");
+  }
+  return SWIFTKV_OK;
+}
 
-#define RET(x)                 \
-  do {                         \
-    int r_ = (x);              \
-    if (r_ != SWIFTKV_OK) return r_; \
-  } while (0)
+}  // namespace skv
+
+namespace {
 
 constexpr int kRopeLen = 32768;
-
-struct LayerW {
-  float* g_attn = nullptr;
-  float* g_mlp = nullptr;
-  bf16* wqkv = nullptr;  // full layer: [Nq + 2 Nkv][d]; skipped layer: W_Q only [Nq][d]
-  float* bqkv = nullptr;
-  bf16* wo = nullptr;    // [d][Nq]
-  bf16* wgu = nullptr;   // [2 Fp][d], gate/up interleaved in 64-row blocks
-  bf16* wd = nullptr;    // [d][Fp]
-  bool loaded = false;
-};
 
 struct Workspace {
   int *cu, *tiles, *pools, *positions, *slots, *last_idx, *last_pos, *tokens, *ctx, *srow, *sseq, *dint;
@@ -81,47 +82,6 @@ struct PhaseRange {
 size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 }  // namespace
-
-namespace skv {
-int set_error(int code, const char* msg) { return fail(code, "%s", msg); }
-}  // namespace skv
-
-struct swiftkv_model {
-  swiftkv_model_config cfg;
-  int l, g, C, G;
-  int Nq, Nkv, Fp, Nwide;
-  int device, num_sms;
-  std::vector<LayerW> layers;
-  bf16 *embed = nullptr, *lm_head = nullptr;
-  float* g_final = nullptr;
-  bf16* w_wide = nullptr;
-  float* b_wide = nullptr;
-  float2* rope_tab = nullptr;
-  float* inv_freq = nullptr;
-  int* status = nullptr;
-  std::vector<void*> allocs;
-  size_t weight_bytes = 0;
-  char* ws = nullptr;
-  size_t ws_bytes = 0;
-  bool globals_loaded = false;
-  int gemm_impl = 0;  // 0 tcgen05 CTA pairs, 1 mma.sync tiles, 2 tcgen05 single CTA (GEMMs with > 64 rows)
-  int attn_impl = 0;  // 0 tcgen05 when d_head == 128, 1 mma.sync
-  bool norm_fusion = false;  // prompt rows: RMSNorm in the tcgen05 GEMM epilogues (else its own pass)
-  int rows_impl = 1;  // tail / decode rows after attention: 0 one chained launch, 1 a launch per GEMM / norm
-  unsigned* chain_count = nullptr;  // grid-barrier arrivals of the chained launches (device)
-  unsigned chain_base = 0;          // ... and their count so far (host)
-  // profiling (swiftkv_profile_begin/end)
-  bool prof_on = false;
-  struct Rec {
-    std::string name;
-    cudaEvent_t a, b;
-    int kernels;
-    double flops, bytes;
-  };
-  std::vector<Rec> recs;
-  std::vector<cudaEvent_t> ev_pool;
-  size_t ev_used = 0;
-};
 
 namespace {
 
@@ -685,24 +645,6 @@ int check_ready(const swiftkv_model* m) {
   if (!m->globals_loaded) return fail(SWIFTKV_ESTATE, "globals not loaded");
   for (int j = 0; j < m->cfg.L; ++j)
     if (!m->layers[j].loaded) return fail(SWIFTKV_ESTATE, "layer %d not loaded", j);
-  return SWIFTKV_OK;
-}
-
-int check_kv(const swiftkv_model* m, const swiftkv_kv_pages* kv) {
-  if (!kv || !kv->k_pool || !kv->v_pool || !kv->block_table) return fail(SWIFTKV_EINVAL, "null kv pages");
-  if (kv->num_caches != m->C) return fail(SWIFTKV_EINVAL, "num_caches %d != %d", kv->num_caches, m->C);
-  if (kv->page_size != kPageSize) return fail(SWIFTKV_EINVAL, "page_size must be 16");
-  if (kv->num_pages < 1 || kv->max_pages_per_seq < 1) return fail(SWIFTKV_EINVAL, "empty page pool");
-  for (int c = 0; c < m->C; ++c)
-    if (!kv->k_pool[c] || !kv->v_pool[c]) return fail(SWIFTKV_EINVAL, "null pool pointer for cache %d", c);
-  if (kv->kv_dtype != 0 && kv->kv_dtype != 1) return fail(SWIFTKV_EINVAL, "kv_dtype %d", kv->kv_dtype);
-  if (kv->kv_dtype == 1) {
-    if (!kv->k_scale || !kv->v_scale) return fail(SWIFTKV_EINVAL, "fp8 cache without scale pools");
-    for (int c = 0; c < m->C; ++c)
-      if (!kv->k_scale[c] || !kv->v_scale[c]) return fail(SWIFTKV_EINVAL, "null scale pool for cache %d", c);
-    if (m->cfg.n_q / m->cfg.n_kv > 8)
-      return fail(SWIFTKV_EUNSUPPORTED, "fp8 cache needs at most 8 query heads per KV head");
-  }
   return SWIFTKV_OK;
 }
 

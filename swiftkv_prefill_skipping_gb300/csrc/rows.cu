@@ -317,6 +317,21 @@ __global__ void kv_quantize_kernel(const bf16* __restrict__ stage, int ld, int M
   }
 }
 
+// 16 e4m3 codes as bf16 values (exact).
+__device__ __forceinline__ void expand_codes16(uint4 raw, uint32_t* o) {
+  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+#pragma unroll
+    for (int hh = 0; hh < 2; ++hh) {
+      const uint32_t h = f16x2_from_e4m3x2((w[i] >> (16 * hh)) & 0xffffu);
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+      __nv_bfloat162 b2 = __floats2bfloat162_rn(f.x, f.y);
+      o[2 * i + hh] = *reinterpret_cast<uint32_t*>(&b2);
+    }
+  }
+}
+
 // Expands whole (page, all heads) blocks of one cache's uint8 code pools into bf16 pools of
 // the same layout (exact: e4m3 values are bf16 values; the attention applies the scales):
 // item i = (sequence, page index) pairs; 16 codes per thread-step.
@@ -332,21 +347,65 @@ __global__ void kv_dequant_pages_kernel(const int* __restrict__ items, const int
     const int kvsel = c >= per_page / 16;
     const int e = (c - kvsel * (per_page / 16)) * 16;  // element within the page
     const uint4 raw = *reinterpret_cast<const uint4*>((kvsel ? v8 : k8) + base + e);
-    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
     uint32_t o[8];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-#pragma unroll
-      for (int hh = 0; hh < 2; ++hh) {
-        const uint32_t h = f16x2_from_e4m3x2((w[i] >> (16 * hh)) & 0xffffu);
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-        __nv_bfloat162 b2 = __floats2bfloat162_rn(f.x, f.y);
-        o[2 * i + hh] = *reinterpret_cast<uint32_t*>(&b2);
-      }
-    }
+    expand_codes16(raw, o);
     bf16* dst = (kvsel ? sv : sk) + base + e;
     *reinterpret_cast<uint4*>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
     *reinterpret_cast<uint4*>(dst + 8) = make_uint4(o[4], o[5], o[6], o[7]);
+  }
+}
+
+// Item i = (sequence, page index) becomes page i of the expansion.
+__global__ void kv_expand_seen_kernel(const int* __restrict__ items, const KVPool8 src, int max_pages, int num_pages,
+                                      const int* __restrict__ cu, const int* __restrict__ ctx, int n_kv, int dh,
+                                      int window, int sinks, const KVExpansion dst, int* status) {
+  const int i = blockIdx.x, s = items[2 * i], pidx = items[2 * i + 1];
+  const int page = src.block_table[(size_t)s * max_pages + pidx];
+  const bool ok = page >= 0 && page < num_pages;
+  if (threadIdx.x == 0) {
+    dst.block_table[(size_t)s * max_pages + pidx] = i;
+    if (!ok) atomicOr(status, kStatusBadPage);
+  }
+  const TailPages t = tail_pages(ctx[s], cu[s + 1] - cu[s], window, sinks);
+  const int rows = n_kv * kPageSize, per_page = rows * dh;
+  const size_t from = ok ? (size_t)page * per_page : 0, to = (size_t)i * per_page;
+  for (int c = threadIdx.x; c < 2 * per_page / 16; c += blockDim.x) {
+    const int kvsel = c >= per_page / 16;
+    if (kvsel && !dst.v) break;  // K alone
+    const int e = (c - kvsel * (per_page / 16)) * 16;
+    uint32_t o[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    if (ok && t.seen(pidx * kPageSize + e / dh % kPageSize))
+      expand_codes16(*reinterpret_cast<const uint4*>((kvsel ? src.v : src.k) + from + e), o);
+    bf16* d = (kvsel ? dst.v : dst.k) + to + e;
+    *reinterpret_cast<uint4*>(d) = make_uint4(o[0], o[1], o[2], o[3]);
+    *reinterpret_cast<uint4*>(d + 8) = make_uint4(o[4], o[5], o[6], o[7]);
+  }
+  for (int c = threadIdx.x; c < 2 * rows; c += blockDim.x) {
+    const int kvsel = c >= rows, e = c - kvsel * rows;
+    if (kvsel && !dst.v) break;
+    const bool seen = ok && t.seen(pidx * kPageSize + e % kPageSize);
+    (kvsel ? dst.v_scale : dst.k_scale)[(size_t)i * rows + e] =
+        seen ? (kvsel ? src.v_scale : src.k_scale)[(size_t)page * rows + e] : 0.f;
+  }
+}
+
+__global__ void v_tail_kernel(const bf16* __restrict__ v_pool, const int* __restrict__ bt, int max_pages, int num_pages,
+                              const int* __restrict__ cu, const int* __restrict__ ctx, int n_kv, int dh, int window,
+                              int sinks, bf16* __restrict__ out) {
+  const int s = blockIdx.x, slot = blockIdx.y;
+  const int n = cu[s + 1] - cu[s];
+  if (n < 1) return;
+  const TailPages t = tail_pages(ctx ? ctx[s] : 0, n, window, sinks);
+  const int pidx = t.page[slot];
+  if (pidx < 0) return;
+  const int page = bt[(size_t)s * max_pages + pidx];
+  const bool ok = page >= 0 && page < num_pages;
+  const int per_page = n_kv * kPageSize * dh;
+  bf16* dst = out + ((size_t)s * kTailSlots + slot) * per_page;
+  for (int e = threadIdx.x * 8; e < per_page; e += blockDim.x * 8) {
+    const bool seen = ok && t.seen(pidx * kPageSize + e / dh % kPageSize);
+    *reinterpret_cast<uint4*>(dst + e) =
+        seen ? *reinterpret_cast<const uint4*>(v_pool + (size_t)page * per_page + e) : make_uint4(0, 0, 0, 0);
   }
 }
 
@@ -375,6 +434,24 @@ cudaError_t launch_kv_dequant_pages(const int* items, int num_items, const int* 
   if (num_items <= 0) return cudaSuccess;
   kv_dequant_pages_kernel<<<num_items, 256, 0, stream>>>(items, block_table, max_pages, num_pages, n_kv, d_head, k8,
                                                           v8, sk, sv);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_kv_expand_seen(const int* items, int num_items, const KVPool8& src, int max_pages, int num_pages,
+                                  const int* cu, const int* ctx, int n_kv, int d_head, int window, int sinks,
+                                  const KVExpansion& dst, int* status, cudaStream_t stream) {
+  if (num_items <= 0) return cudaSuccess;
+  kv_expand_seen_kernel<<<num_items, 256, 0, stream>>>(items, src, max_pages, num_pages, cu, ctx, n_kv, d_head, window,
+                                                       sinks, dst, status);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_v_tail(const bf16* v_pool, const int* block_table, int max_pages, int num_pages, const int* cu,
+                          const int* ctx, int P, int n_kv, int d_head, int window, int sinks, bf16* out,
+                          cudaStream_t stream) {
+  if (P <= 0) return cudaSuccess;
+  v_tail_kernel<<<dim3(P, kTailSlots), 256, 0, stream>>>(v_pool, block_table, max_pages, num_pages, cu, ctx, n_kv,
+                                                         d_head, window, sinks, out);
   return cudaGetLastError();
 }
 
