@@ -13,7 +13,7 @@
 // (sequence, KV head); the tile stays in shared memory while 128-row query tiles of every head of
 // the group stream past it. The transposed product gives each of the 128 epilogue threads one
 // key: it reads its row of S from TMEM, adds exp2(s c - lse_column) over the columns, and keeps
-// the key's sum in a register for the whole item; no score leaves the SM. Two warpgroups take
+// the key's sum in a register for the whole item; no score leaves the SM. Three warpgroups take
 // alternate tiles, so one reads TMEM and computes exponentials (the bound: one per score) while
 // the tensor core fills the next of four accumulators.
 #include <cuda.h>
@@ -234,7 +234,8 @@ constexpr int BK = 128;        // keys per item
 constexpr int BQ = 128;        // query rows per tile
 constexpr int QST = 4;         // query tiles in flight
 constexpr int SBUF = 4;        // S accumulators (128 TMEM columns each)
-constexpr int WT = 320;        // TMA, MMA, 2 x 4 epilogue warps
+constexpr int WGS = 3;         // epilogue warpgroups
+constexpr int WT = 64 + WGS * 128;  // TMA, MMA, epilogue warps
 constexpr int EPI0 = 2;
 
 struct WCtrl {
@@ -242,13 +243,27 @@ struct WCtrl {
   uint32_t tmem_base;
   int abort;
   int pend_k[2], pend_q[QST];
-  alignas(16) float lse[2][2][BQ];  // [warpgroup][parity], read 16 bytes at a time
-  float comb[2][BK];     // warpgroup 1's sums, by item parity
+  alignas(16) float lse[WGS][2][BQ];  // [warpgroup][parity], read 16 bytes at a time
+  float comb[2][WGS - 1][BK];  // the other warpgroups' sums, by item parity
 };
 
 template <int D>
 constexpr int w_smem() {
   return 1024 + 2 * BK * D * 2 + QST * BQ * D * 2 + (int)sizeof(WCtrl);
+}
+
+// d[0 .. 1] = (x0, x1) * c + (l0, l1) and acc[0 .. 1] += (p0, p1), each one packed fp32 instruction.
+__device__ __forceinline__ void fma2(float* d, uint32_t x0, uint32_t x1, float c, float l0, float l1) {
+  asm("{\n .reg .b64 a, b, e, f;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %4};\n mov.b64 e, {%5, %6};\n"
+      " fma.rn.f32x2 f, a, b, e;\n mov.b64 {%0, %1}, f;\n}\n"
+      : "=f"(d[0]), "=f"(d[1])
+      : "r"(x0), "r"(x1), "f"(c), "f"(l0), "f"(l1));
+}
+__device__ __forceinline__ void add2(float* acc, float p0, float p1) {
+  asm("{\n .reg .b64 a, b;\n mov.b64 a, {%0, %1};\n mov.b64 b, {%2, %3};\n add.rn.f32x2 a, a, b;\n"
+      " mov.b64 {%0, %1}, a;\n}\n"
+      : "+f"(acc[0]), "+f"(acc[1])
+      : "f"(p0), "f"(p1));
 }
 
 struct WItem {
@@ -427,20 +442,29 @@ __global__ void __launch_bounds__(WT, 1) weights_tc_kernel(const __grid_constant
       float c = scale_log2;
       if (kscale) c *= page >= 0 && page < pages_k ? kscale[((size_t)page * a.n_kv + I.kvh) * kPageSize + (key & 15)] : 0.f;
       const int tiles_here = (I.qt1 - I.qt0) * G;
-      float acc[4] = {0.f, 0.f, 0.f, 0.f};
-      // the lse of this thread's column of tile t
-      auto lse_of = [&](int t) -> float {
-        if (t >= tiles_here) return INFINITY;
-        const int row = (I.qt0 + t / G) * BQ + r;
-        return row < I.n ? a.lse[(size_t)(I.kvh * G + t % G) * a.ldl + I.seq0 + row] * kLog2e : INFINITY;
+      float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      // tiles alternate between the warpgroups over all items; (qt, h): tile t's rows and head
+      int t = (int)((wg + WGS - g % WGS) % WGS), qt = I.qt0, h = t;
+      auto settle = [&]() {
+        while (h >= G) {
+          h -= G;
+          ++qt;
+        }
       };
-      int t = (int)((g & 1) == wg ? 0 : 1);  // tiles alternate between the warpgroups over all items
-      float next = lse_of(t);
-      for (; t < tiles_here; t += 2, ++turn) {
+      settle();
+      auto lse_here = [&]() -> float {  // of this thread's column, negated, in log2
+        const int row = qt * BQ + r;
+        return qt < I.qt1 && row < I.n ? -a.lse[(size_t)(I.kvh * G + h) * a.ldl + I.seq0 + row] * kLog2e : -INFINITY;
+      };
+      float next = lse_here();
+      for (; t < tiles_here; t += WGS, ++turn) {
         float* lse = ctl->lse[wg][turn & 1];
         lse[r] = next;
         wg_sync();  // written; and everyone has left the buffer of two turns ago
-        next = lse_of(t + 2);
+        const int q0 = qt * BQ;
+        h += WGS;
+        settle();
+        next = lse_here();
         const long long gt = g + t;
         const int sb = (int)(gt % SBUF);
         // after an expired wait the loops run on without work, so that every thread still meets
@@ -451,47 +475,63 @@ __global__ void __launch_bounds__(WT, 1) weights_tc_kernel(const __grid_constant
           continue;
         }
         tc_fence_after();
-        const int q0 = (I.qt0 + t / G) * BQ;
         // no key of the tile hidden from any row, and no row past the chunk
         const bool interior = I.key0 + BK - 1 <= I.c0 + q0 && q0 + BQ <= I.n &&
                               (a.window <= 0 || I.key0 > I.c0 + q0 + BQ - 1 - a.window || I.key0 + BK <= a.sinks);
+        // columns of this tile whose rows see the key: [lo, lo + span)
+        const int first = max(0, key - I.c0 - q0);
+        long long last = min(BQ, I.n - q0);
+        if (a.window > 0 && key >= a.sinks) last = min(last, (long long)key + a.window - I.c0 - q0);
+        const unsigned lo = (unsigned)first, span = last > first ? (unsigned)(last - first) : 0u;
+        // two groups of 32 columns in registers; a group is loaded as soon as one has been summed,
+        // so that the accumulator is free when half of it has been
+        uint32_t v[2][32];
+        tmem_ld32_async(tmem + lane_off + sb * BQ, v[0]);
+        tmem_ld32_async(tmem + lane_off + sb * BQ + 32, v[1]);
+        tmem_wait32(v[0]);
+        tmem_wait32(v[1]);
 #pragma unroll
         for (int cb = 0; cb < BQ; cb += 32) {
-          float v[32];
-          tmem_ld32(tmem + lane_off + sb * BQ + cb, v);
-          if (cb + 32 == BQ) {
+          uint32_t* x = v[(cb / 32) & 1];
+          if (cb == 64) {
+            tmem_wait32(v[0]);
+            tmem_wait32(v[1]);
             tc_fence_before();
             mbar_arrive(bar(ctl->s_empty[sb]));  // S has been read: the accumulator may be refilled
           }
           if (interior) {
+            float e[32];  // two columns an instruction, all exponents before the exponentials
 #pragma unroll
             for (int i = 0; i < 32; i += 4) {
               const float4 l = *reinterpret_cast<const float4*>(lse + cb + i);
-              acc[0] += ex2_approx(fmaf(v[i], c, -l.x));
-              acc[1] += ex2_approx(fmaf(v[i + 1], c, -l.y));
-              acc[2] += ex2_approx(fmaf(v[i + 2], c, -l.z));
-              acc[3] += ex2_approx(fmaf(v[i + 3], c, -l.w));
+              fma2(e + i, x[i], x[i + 1], c, l.x, l.y);
+              fma2(e + i + 2, x[i + 2], x[i + 3], c, l.z, l.w);
             }
+#pragma unroll
+            for (int i = 0; i < 32; ++i) e[i] = ex2_approx(e[i]);
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) add2(acc + (i & 7), e[i], e[i + 1]);
           } else {
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
-              const int row = q0 + cb + i;
-              const bool in = row < I.n && attn_visible(key, I.c0 + row, a.window, a.sinks);
-              acc[i & 3] += in ? ex2_approx(fmaf(v[i], c, -lse[cb + i])) : 0.f;
+              const float e = fmaf(__uint_as_float(x[i]), c, lse[cb + i]);
+              acc[i & 7] += ex2_approx((unsigned)(cb + i) - lo < span ? e : -INFINITY);
             }
           }
+          if (cb < 64) tmem_ld32_async(tmem + lane_off + sb * BQ + cb + 64, x);
         }
       }
       g += tiles_here;
-      const float sum = (acc[0] + acc[1]) + (acc[2] + acc[3]);
-      float* comb = ctl->comb[it & 1];
-      if (wg == 1) comb[r] = sum;
-      asm volatile("bar.sync 3, 256;" ::: "memory");
+      const float sum = ((acc[0] + acc[1]) + (acc[2] + acc[3])) + ((acc[4] + acc[5]) + (acc[6] + acc[7]));
+      if (wg > 0) ctl->comb[it & 1][wg - 1][r] = sum;
+      asm volatile("bar.sync %0, %1;" ::"n"(1 + WGS), "n"(WGS * 128) : "memory");
       if (wg == 0 && seen && ok) {
         const int own = a.bt[(size_t)I.s * a.max_pages + (key >> 4)];
         if (own >= 0 && own < a.num_pages) {
           float* dst = a.scores + ((size_t)own * a.n_kv + I.kvh) * kPageSize + (key & 15);
-          const float w = sum + comb[r];
+          float w = sum;
+#pragma unroll
+          for (int i = 0; i + 1 < WGS; ++i) w += ctl->comb[it & 1][i][r];
           *dst = a.decay != 0.f ? fmaf(a.decay, *dst, w) : w;
         } else {
           atomicOr(a.status, kStatusBadPage);

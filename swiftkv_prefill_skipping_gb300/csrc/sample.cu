@@ -23,6 +23,7 @@
 #include <cfloat>
 #include <climits>
 #include <cmath>
+#include <type_traits>
 
 #include "common.cuh"
 #include "launch.h"
@@ -42,6 +43,7 @@ constexpr int TAB = 256;           // 2^(j / TAB) table
 constexpr int FX = 44;             // fixed-point weights: w * 2^FX (360448 of them, times 2^(1/256), stay below 2^63)
 constexpr int kMaxSlice = 45056;   // floats of a row one CTA holds (176 KB)
 constexpr int kMaxVocab = 8 * kMaxSlice;
+constexpr int MAXCHUNK = kMaxSlice / SWARPS / 32 + 1;  // 32-element chunks of a warp's segment
 
 struct SampleParams {
   const float* logits;
@@ -82,6 +84,15 @@ struct alignas(16) Share {  // the slice behind it is written 16 bytes at a time
   unsigned limb[3][NB];         // 16-bit limbs of the bins while they are summed
   u64 warp_mass[SWARPS];
   u64 sums[NB];                 // the cluster's sums of the bins this CTA scans
+  // the row's settings
+  double set_tlog;
+  float set_t, set_p, set_m, set_u, set_ch, set_cl;
+  int set_k;
+  // the search for the drawn id: masses, or kept and tied elements, of 32-element chunks
+  u64 chunk_mass[MAXCHUNK];
+  unsigned chunk_gt[MAXCHUNK], chunk_eq[MAXCHUNK];
+  int len[SWARPS];
+  int pos;
   float red_f[SWARPS];
   unsigned red_a[SWARPS], red_b[SWARPS];
   // read by the cluster's other CTAs
@@ -147,10 +158,11 @@ struct Scale {
 // 2^40 it fits 32 bits; the table entry times it is a 64-bit product, shifted into place. The
 // shift drops bits and sets the lowest one, the middle of what was dropped, so that 10^5 small
 // weights carry no bias.
-__device__ __forceinline__ u64 weight_fx(float l, const Scale& s, const u64* tab) {
+// No branches, so that a thread's loop runs several weights at once.
+template <bool DIFF>
+__device__ __forceinline__ u64 weight_of(float l, const Scale& s, const u64* tab) {
   float p, lo;
-  if (s.diff) {
-    if (l == s.m) return 1ull << FX;
+  if (DIFF) {
     const float dh = l - s.m, bb = dh - l;
     const float dl = (l - (dh - bb)) - (s.m + bb);  // l - m = dh + dl exactly
     p = dh * s.ch;
@@ -160,9 +172,9 @@ __device__ __forceinline__ u64 weight_fx(float l, const Scale& s, const u64* tab
     lo = fmaf(l, s.cl, fmaf(l, s.ch, -p));
   }
   const float d = p - s.ref;
-  if (!(d > -(float)(FX + 1))) return 0;  // also l = -inf (c may be 0 or infinite)
+  const bool none = !(d > -(float)(FX + 1));  // also l = -inf (c may be 0 or infinite)
   const float magic = 12582912.f;  // 1.5 * 2^23: rounds to an integer held in the low bits
-  const float kf = fmaf(d, 256.f, magic);
+  const float kf = fmaf(none ? 0.f : d, 256.f, magic);
   const int k = __float_as_int(kf) - 0x4b400000;
   const float r = p - fmaf(kf - magic, 1.f / 256.f, s.ref);
   constexpr float S40 = 1099511627776.f;
@@ -177,7 +189,12 @@ __device__ __forceinline__ u64 weight_fx(float l, const Scale& s, const u64* tab
   const u64 t = tab[k & (TAB - 1)];               // 2^(j / 256) * 2^FX, below 2^46
   const int t30 = (int)(t >> (FX - 30));          // 30 bits of it and one before the point
   const u64 x = t + (u64)(((long long)t30 * q) >> (70 - FX));
-  return (x >> -(k >> 8)) | 1ull;                 // k <= 1, so the shift is 0 .. FX + 1
+  u64 w = (x >> -(k >> 8)) | 1ull;                // k <= 1, so the shift is 0 .. FX + 1
+  if (DIFF && l == s.m) w = 1ull << FX;           // c may be infinite
+  return none && !(DIFF && l == s.m) ? 0 : w;
+}
+__device__ __forceinline__ u64 weight_fx(float l, const Scale& s, const u64* tab) {
+  return s.diff ? weight_of<true>(l, s, tab) : weight_of<false>(l, s, tab);
 }
 
 // floor(f * w) for a float 0 <= f < 1 and whether that is exact: f = mant * 2^-sh.
@@ -242,6 +259,21 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const SampleParams p) {
   griddep_launch_dependents();
   for (int i = tid; i < TAB; i += ST) sh.tab[i] = kPow2.v[i];
   griddep_wait();
+  if (tid == ST - 1) {
+    // the row's settings, while the others load: what needs 64 bits is computed once (double
+    // arithmetic of all threads took longer than the load)
+    const float t = p.temperature ? p.temperature[r] : p.temperature_all;
+    const float mp = p.min_p ? p.min_p[r] : p.min_p_all;
+    sh.set_t = t;
+    sh.set_k = p.top_k ? p.top_k[r] : p.top_k_all;
+    sh.set_p = p.top_p ? p.top_p[r] : p.top_p_all;
+    sh.set_m = mp;
+    sh.set_u = p.u[r];
+    const double c = 1.4426950408889634074 / (double)t;
+    sh.set_ch = (float)c;
+    sh.set_cl = isinf(sh.set_ch) ? 0.f : (float)(c - (double)sh.set_ch);
+    sh.set_tlog = mp > 0.f && mp < 1.f ? (double)t * log((double)mp) : 0.0;
+  }
   // ---- the slice and its maximum (NaN becomes -inf)
   float mx = -INFINITY;
   if (p.vec) {
@@ -273,7 +305,7 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const SampleParams p) {
 #pragma unroll
     for (unsigned c = 0; c < (unsigned)C; ++c) mx = fmaxf(mx, ld_remote(&sh.x_max, c));
   }
-  const float T = p.temperature ? p.temperature[r] : p.temperature_all;
+  const float T = sh.set_t;
   if (!(T > 0.f) || mx == -INFINITY) {  // greedy; a row with no logit above -inf gives id 0
     unsigned at = UINT_MAX;
     for (int i = tid; i < n; i += ST)
@@ -291,20 +323,16 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const SampleParams p) {
     if (C > 1) cluster_barrier();  // no CTA leaves while another may read its x_kmin
     return;
   }
-  const int tk = p.top_k ? p.top_k[r] : p.top_k_all;
-  const float tp = p.top_p ? p.top_p[r] : p.top_p_all;
-  const float mp = p.min_p ? p.min_p[r] : p.min_p_all;
+  const int tk = sh.set_k;
+  const float tp = sh.set_p, mp = sh.set_m;
   const bool use_k = tk > 0 && tk < p.V;
   const bool use_p = tp < 1.f;  // NaN: off
   Scale sc;
   sc.m = mx;
-  {
-    const double c = 1.4426950408889634074 / (double)T, mc = (double)mx * c;
-    sc.ch = (float)c;
-    sc.cl = isinf(sc.ch) ? 0.f : (float)(c - (double)sc.ch);
-    sc.diff = !(fabs(mc) <= 256.0);
-    sc.ref = sc.diff ? 0.f : (float)(rint(mc * 256.0) * (1.0 / 256.0));
-  }
+  sc.ch = sh.set_ch;
+  sc.cl = sh.set_cl;
+  sc.diff = !(fabsf(mx * sc.ch) <= 256.f);
+  sc.ref = sc.diff ? 0.f : rintf(mx * sc.ch * 256.f) * (1.f / 256.f);
   // Warp w owns the slice's segment [s0, s1), ids ascending. Filters compact the segments in
   // place (lower positions only), so later passes read what is left.
   const int seg = ((n + SWARPS - 1) / SWARPS + 31) & ~31;
@@ -322,6 +350,16 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const SampleParams p) {
     atomicAdd(&sh.limb[0][b], lo & 0xffffu);
     if (lo >> 16) atomicAdd(&sh.limb[1][b], lo >> 16);
     if (hi) atomicAdd(&sh.limb[2][b], hi);
+  };
+  // f(row element, weight function) over this warp's elements, the kind of scale hoisted out
+  auto each = [&](auto f) {
+    auto go = [&](auto kind) {
+      auto weight = [&](float l) { return weight_of<decltype(kind)::value>(l, sc, sh.tab); };
+#pragma unroll 4
+      for (int i = s0 + lane; i < s1; i += 32) f(row[i], weight);
+    };
+    if (sc.diff) go(std::true_type());
+    else go(std::false_type());
   };
   auto clear = [&]() {
     for (int b = tid; b < NB; b += ST) sh.limb[0][b] = sh.limb[1][b] = sh.limb[2][b] = 0;
@@ -451,12 +489,12 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const SampleParams p) {
     for (int it = 0; it < 5 && lo < hi; ++it) {  // ten bits of the key a round
       const int s = max(0, 22 - __clz(hi - lo));  // (hi - lo) >> s < NB
       clear();
-#pragma unroll 4
       for (int i = s0 + lane; i < s1; i += 32) {
-        const unsigned k = key_of(row[i]);
+        const float l = row[i];
+        const unsigned k = key_of(l);
         if (k >= lo && k <= hi) {
           const int b = (int)((hi - k) >> s);
-          if (by_mass) add_mass(b, weight_fx(row[i], sc, sh.tab));
+          if (by_mass) add_mass(b, weight_fx(l, sc, sh.tab));
           else atomicAdd(&sh.limb[0][b], 1u);
         }
       }
@@ -466,6 +504,26 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const SampleParams p) {
       lo = max(lo, hi - ((1u << s) - 1));
     }
     return lo;
+  };
+
+  // Keeps the elements that pass `keep` (all lanes call it), each warp's segment in place.
+  auto squeeze = [&](auto keep) {
+    int out = s0;
+    for (int i0 = s0; i0 < s1; i0 += 128) {
+      float l[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) l[e] = i0 + 32 * e + lane < s1 ? row[i0 + 32 * e + lane] : 0.f;
+      __syncwarp();  // read before lower positions are written
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const bool k = keep(i0 + 32 * e + lane < s1, l[e]);
+        const unsigned kept = __ballot_sync(0xffffffffu, k);
+        if (k) row[out + __popc(kept & ((1u << lane) - 1))] = l[e];
+        out += __popc(kept);
+      }
+      __syncwarp();
+    }
+    s1 = out;
   };
 
   Prefix pre;
@@ -494,17 +552,11 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const SampleParams p) {
       sync_all();
     }
     unsigned t0 = tie_base;
-    int out = s0;
-    for (int i = s0; i < s1; i += 32) {
-      const bool in = i + lane < s1;
-      const float l = in ? row[i + lane] : 0.f;
-      const bool keep = pre.keeps(in, key_of(l), t0, lane);
-      const unsigned kept = __ballot_sync(0xffffffffu, keep);
-      if (keep) row[out + __popc(kept & ((1u << lane) - 1))] = l;
-      out += __popc(kept);
-      __syncwarp();
-    }
-    s1 = out;
+    squeeze([&](bool in, float l) { return pre.keeps(in, key_of(l), t0, lane); });
+  };
+  // Drops what lies below the threshold's bin of a first histogram, before that bin is refined.
+  auto drop_below = [&](int bin) {
+    squeeze([&](bool in, float l) { return in && bin_of(l) <= bin; });
   };
 
   if (use_k) {
@@ -514,6 +566,7 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const SampleParams p) {
     publish();
     u64 want = (u64)tk, before = 0;
     const int bin = find(want, -1.f, before);
+    drop_below(bin);
     pre.key = refine(false, want, bin, before);
     pre.ties = (unsigned)(want - before);
     compact();
@@ -522,15 +575,14 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const SampleParams p) {
     // elements with less than top_p of the mass before them: the last one kept is the one at
     // which the running mass reaches it, and the first of the order is always kept
     clear();
-#pragma unroll 4
-    for (int i = s0 + lane; i < s1; i += 32) {
-      const float l = row[i];
-      const u64 w = weight_fx(l, sc, sh.tab);
+    each([&](float l, auto weight) {
+      const u64 w = weight(l);
       if (w) add_mass(bin_of(l), w);
-    }
+    });
     publish();
     u64 want = 0, before = 0;
     const int bin = find(want, tp, before);
+    drop_below(bin);
     Prefix pp;
     pp.key = refine(true, want, bin, before);
     const u64 w = weight_fx(value_of(pp.key), sc, sh.tab);
@@ -540,7 +592,7 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const SampleParams p) {
   }
   if (mp > 0.f) {
     // w >= min_p  <=>  l >= m + T ln(min_p); an infinite product leaves everything
-    const float tf = mp >= 1.f ? mx : __double2float_ru((double)mx + (double)T * log((double)mp));
+    const float tf = mp >= 1.f ? mx : __double2float_ru((double)mx + sh.set_tlog);
     const unsigned key = key_of(tf);
     if (key > pre.key) {
       pre.key = key;
@@ -551,21 +603,20 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const SampleParams p) {
 
   // ---- the draw: running sums over the kept ids in ascending order
   u64 sum = 0;
-#pragma unroll 4
-  for (int i = s0 + lane; i < s1; i += 32) sum += weight_fx(row[i], sc, sh.tab);
+  each([&](float l, auto weight) { sum += weight(l); });
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  if (lane == 0) sh.warp_mass[warp] = sum;
-  __syncthreads();
-  u64 before = 0, total = 0;
-#pragma unroll
-  for (int w = 0; w < SWARPS; ++w) {
-    const u64 x = sh.warp_mass[w];
-    if (w < warp) before += x;
-    total += x;
+  if (lane == 0) {
+    sh.warp_mass[warp] = sum;
+    sh.len[warp] = s1 - s0;
   }
+  __syncthreads();
+  u64 mine = 0;
+#pragma unroll
+  for (int w = 0; w < SWARPS; ++w) mine += sh.warp_mass[w];
+  u64 before = 0, total = mine;
   if (C > 1) {
-    if (tid == 0) sh.x_mass = total;
+    if (tid == 0) sh.x_mass = mine;
     cluster_barrier();
     total = 0;
 #pragma unroll
@@ -574,63 +625,105 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const SampleParams p) {
       if (c + 1 <= rank) before += x;
       total += x;
     }
+    cluster_barrier();  // the last remote read: from here on every CTA is on its own
   }
   // sums are whole numbers, so "exceeds the real number u * total" is "is at least
   // floor(u * total) + 1"
-  float u = p.u[r];
+  float u = sh.set_u;
   u = u > 0.f ? fminf(u, 0.99999994f) : 0.f;  // NaN and -0 too
   const u64 target = floor_mul(u, total) + 1;
-  if (before < target && target <= before + sum) {  // one warp of the cluster
-    // lane j sums a contiguous share; then the warp looks into the share that holds the target
-    const int each = (s1 - s0 + 31) / 32;
-    const int b0 = min(s1, s0 + lane * each), b1 = min(s1, b0 + each);
-    u64 mine = 0;
-#pragma unroll 4
-    for (int i = b0; i < b1; ++i) mine += weight_fx(row[i], sc, sh.tab);
-    auto scan = [&](u64 v) {
+  if (!(before < target && target <= before + mine)) return;
+  // The id is in this CTA's slice: the warps share the segment that holds it, a chunk of 32 at a
+  // time, and warp 0 picks the chunk and the element.
+  int win = 0;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const u64 x = __shfl_up_sync(0xffffffffu, v, o);
-        if (lane >= o) v += x;
-      }
-      return v;
-    };
-    const u64 upto = before + scan(mine);
-    const int who = __ffs(__ballot_sync(0xffffffffu, upto >= target)) - 1;
-    u64 run = __shfl_sync(0xffffffffu, upto - mine, who);
-    const int c0 = __shfl_sync(0xffffffffu, b0, who), c1 = __shfl_sync(0xffffffffu, b1, who);
-    int at = c0;
-    for (int i = c0; i < c1; i += 32) {
-      const u64 inc = run + scan(i + lane < c1 ? weight_fx(row[i + lane], sc, sh.tab) : 0ull);
-      const unsigned hit = __ballot_sync(0xffffffffu, inc >= target);
+  for (int w = 0; w < SWARPS - 1; ++w) {
+    const u64 x = sh.warp_mass[w];
+    if (win == w && before + x < target) {
+      before += x;
+      win = w + 1;
+    }
+  }
+  const int w0 = min(n, win * seg), w1 = w0 + sh.len[win];
+  const int chunks = (w1 - w0 + 31) / 32;
+  for (int c = warp; c < chunks; c += SWARPS) {
+    const int i = w0 + 32 * c + lane;
+    u64 x = i < w1 ? weight_fx(row[i], sc, sh.tab) : 0ull;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    if (lane == 0) sh.chunk_mass[c] = x;
+  }
+  __syncthreads();
+  auto scan = [&](u64 v) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const u64 x = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += x;
+    }
+    return v;
+  };
+  const bool whole = pre.key == 0 && pre.ties == UINT_MAX;  // nothing was dropped
+  if (warp == 0) {
+    int c = 0;
+    for (int c0 = 0; c0 < chunks; c0 += 32) {
+      const u64 upto = before + scan(c0 + lane < chunks ? sh.chunk_mass[c0 + lane] : 0ull);
+      const unsigned hit = __ballot_sync(0xffffffffu, upto >= target);
       if (hit) {
-        at = i + __ffs(hit) - 1;
+        c = c0 + __ffs(hit) - 1;
+        if (c > c0) before = __shfl_sync(0xffffffffu, upto, c - c0 - 1);
         break;
       }
-      run = __shfl_sync(0xffffffffu, inc, 31);
+      before = __shfl_sync(0xffffffffu, upto, 31);
     }
-    int id = at;
-    if (pre.key || pre.ties != UINT_MAX) {
-      // the segment was compacted: its (at - s0)-th kept element, counted in the logits again
-      int left = at - s0;
-      unsigned t0 = tie_base;
-      const int e1 = min(n, s0 + seg);
-      for (int i = s0; i < e1; i += 32) {
-        const bool in = i + lane < e1;
-        const float l = in ? fmaxf(src[i + lane], -INFINITY) : 0.f;
-        unsigned kept = __ballot_sync(0xffffffffu, pre.keeps(in, key_of(l), t0, lane));
-        const int c = __popc(kept);
-        if (left < c) {
-          for (; left > 0; --left) kept &= kept - 1;
-          id = i + __ffs(kept) - 1;
-          break;
-        }
-        left -= c;
-      }
+    const int i = w0 + 32 * c + lane;
+    const u64 upto = before + scan(i < w1 ? weight_fx(row[i], sc, sh.tab) : 0ull);
+    const unsigned hit = __ballot_sync(0xffffffffu, upto >= target);
+    const int at = 32 * c + __ffs(hit) - 1;  // within the segment's kept elements
+    if (lane == 0) {
+      if (whole) p.tokens[r] = base + w0 + at;
+      sh.pos = at;
     }
-    if (lane == 0) p.tokens[r] = base + id;
   }
-  if (C > 1) cluster_barrier();  // shared memory stays until every CTA has read it
+  if (whole) return;
+  // the segment was compacted: its pos-th kept element, counted in the logits again
+  const int e1 = min(n, win * seg + seg), all = (e1 - w0 + 31) / 32;
+  auto key_in = [&](int c) {
+    const int i = w0 + 32 * c + lane;
+    return i < e1 ? key_of(fmaxf(src[i], -INFINITY)) : 0u;  // 0: below every key
+  };
+  for (int c = warp; c < all; c += SWARPS) {
+    const unsigned k = key_in(c);
+    const unsigned gt = __ballot_sync(0xffffffffu, k > pre.key), eq = __ballot_sync(0xffffffffu, k == pre.key && k);
+    if (lane == 0) {
+      sh.chunk_gt[c] = __popc(gt);
+      sh.chunk_eq[c] = __popc(eq);
+    }
+  }
+  if (lane == 0 && warp == win) sh.red_a[0] = tie_base;  // ties before this segment
+  __syncthreads();
+  if (warp == 0) {
+    unsigned ties = sh.red_a[0];
+    int left = sh.pos;
+    for (int c0 = 0; c0 < all; c0 += 32) {
+      const bool in = c0 + lane < all;
+      const unsigned gt = in ? sh.chunk_gt[c0 + lane] : 0u, eq = in ? sh.chunk_eq[c0 + lane] : 0u;
+      const unsigned eq_to = (unsigned)scan(eq) + ties;  // ties up to and with the lane's chunk
+      const unsigned kept_to = (unsigned)scan(gt + min(eq_to, pre.ties) - min(eq_to - eq, pre.ties));
+      const unsigned hit = __ballot_sync(0xffffffffu, kept_to > (unsigned)left);
+      if (hit) {
+        const int who = __ffs(hit) - 1;
+        const unsigned skip = who ? __shfl_sync(0xffffffffu, kept_to, who - 1) : 0u;
+        unsigned t0 = who ? __shfl_sync(0xffffffffu, eq_to, who - 1) : ties;
+        const int i = w0 + 32 * (c0 + who) + lane;
+        unsigned kept = __ballot_sync(0xffffffffu, pre.keeps(i < e1, key_in(c0 + who), t0, lane));
+        for (left -= (int)skip; left > 0; --left) kept &= kept - 1;
+        if (lane == 0) p.tokens[r] = base + w0 + 32 * (c0 + who) + __ffs(kept) - 1;
+        break;
+      }
+      left -= (int)__shfl_sync(0xffffffffu, kept_to, 31);
+      ties = __shfl_sync(0xffffffffu, eq_to, 31);
+    }
+  }
 }
 
 template <int C>
