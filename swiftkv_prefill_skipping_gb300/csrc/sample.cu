@@ -85,7 +85,6 @@ struct alignas(16) Share {  // the slice behind it is written 16 bytes at a time
   u64 warp_mass[SWARPS];
   u64 sums[NB];                 // the cluster's sums of the bins this CTA scans
   // the row's settings
-  double set_tlog;
   float set_t, set_p, set_m, set_u, set_ch, set_cl;
   int set_k;
   // the search for the drawn id: masses, or kept and tied elements, of 32-element chunks
@@ -97,7 +96,8 @@ struct alignas(16) Share {  // the slice behind it is written 16 bytes at a time
   unsigned red_a[SWARPS], red_b[SWARPS];
   // read by the cluster's other CTAs
   float x_max;
-  unsigned x_kmin, x_kmax, x_ties;
+  unsigned x_kmin, x_ties;
+  unsigned x_key;  // of this CTA alone: min-p's smallest key
   u64 x_mass, x_sum;
   // the bin that a search found
   unsigned d_bin;
@@ -257,41 +257,55 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const SampleParams p) {
   };
 
   griddep_launch_dependents();
-  for (int i = tid; i < TAB; i += ST) sh.tab[i] = kPow2.v[i];
+  static_assert(TAB <= ST, "one table entry a thread");
+  const u64 entry = tid < TAB ? kPow2.v[tid] : 0;
   griddep_wait();
-  if (tid == ST - 1) {
-    // the row's settings, while the others load: what needs 64 bits is computed once (double
-    // arithmetic of all threads took longer than the load)
-    const float t = p.temperature ? p.temperature[r] : p.temperature_all;
-    const float mp = p.min_p ? p.min_p[r] : p.min_p_all;
-    sh.set_t = t;
-    sh.set_k = p.top_k ? p.top_k[r] : p.top_k_all;
-    sh.set_p = p.top_p ? p.top_p[r] : p.top_p_all;
-    sh.set_m = mp;
-    sh.set_u = p.u[r];
-    const double c = 1.4426950408889634074 / (double)t;
-    sh.set_ch = (float)c;
-    sh.set_cl = isinf(sh.set_ch) ? 0.f : (float)(c - (double)sh.set_ch);
-    sh.set_tlog = mp > 0.f && mp < 1.f ? (double)t * log((double)mp) : 0.0;
-  }
-  // ---- the slice and its maximum (NaN becomes -inf)
+  // ---- the slice and its maximum (NaN becomes -inf): all loads of a round before their use
   float mx = -INFINITY;
+  constexpr int LD = 8;
   if (p.vec) {
     const int n4 = n >> 2;
-#pragma unroll 8
-    for (int i = tid; i < n4; i += ST) {
-      float4 v = __ldcs(reinterpret_cast<const float4*>(src) + i);
-      v.x = fmaxf(v.x, -INFINITY);
-      v.y = fmaxf(v.y, -INFINITY);
-      v.z = fmaxf(v.z, -INFINITY);
-      v.w = fmaxf(v.w, -INFINITY);
-      mx = fmaxf(fmaxf(mx, fmaxf(v.x, v.y)), fmaxf(v.z, v.w));
-      *reinterpret_cast<float4*>(row + 4 * i) = v;
+    for (int i0 = tid; i0 < n4; i0 += LD * ST) {
+      float4 v[LD];
+#pragma unroll
+      for (int e = 0; e < LD; ++e)
+        if (i0 + e * ST < n4) v[e] = __ldcs(reinterpret_cast<const float4*>(src) + i0 + e * ST);
+#pragma unroll
+      for (int e = 0; e < LD; ++e) {
+        if (i0 + e * ST >= n4) break;
+        float4 x = v[e];
+        x.x = fmaxf(x.x, -INFINITY);
+        x.y = fmaxf(x.y, -INFINITY);
+        x.z = fmaxf(x.z, -INFINITY);
+        x.w = fmaxf(x.w, -INFINITY);
+        mx = fmaxf(fmaxf(mx, fmaxf(x.x, x.y)), fmaxf(x.z, x.w));
+        *reinterpret_cast<float4*>(row + 4 * (i0 + e * ST)) = x;
+      }
     }
     for (int i = 4 * n4 + tid; i < n; i += ST) mx = fmaxf(mx, row[i] = fmaxf(src[i], -INFINITY));
   } else {
-#pragma unroll 8
-    for (int i = tid; i < n; i += ST) mx = fmaxf(mx, row[i] = fmaxf(__ldcs(src + i), -INFINITY));
+    for (int i0 = tid; i0 < n; i0 += 2 * LD * ST) {
+      float v[2 * LD];
+#pragma unroll
+      for (int e = 0; e < 2 * LD; ++e)
+        if (i0 + e * ST < n) v[e] = __ldcs(src + i0 + e * ST);
+#pragma unroll
+      for (int e = 0; e < 2 * LD; ++e)
+        if (i0 + e * ST < n) mx = fmaxf(mx, row[i0 + e * ST] = fmaxf(v[e], -INFINITY));
+    }
+  }
+  if (tid < TAB) sh.tab[tid] = entry;
+  if (tid == ST - 1) {
+    const float t = p.temperature ? p.temperature[r] : p.temperature_all;
+    sh.set_t = t;
+    sh.set_k = p.top_k ? p.top_k[r] : p.top_k_all;
+    sh.set_p = p.top_p ? p.top_p[r] : p.top_p_all;
+    sh.set_m = p.min_p ? p.min_p[r] : p.min_p_all;
+    sh.set_u = p.u[r];
+    // log2(e) / T as a pair: the quotient and what its product with T leaves
+    const float c = 1.442695041f / t;
+    sh.set_ch = c;
+    sh.set_cl = c > 0.f && c < INFINITY ? (fmaf(-c, t, 1.442695041f) + 1.925963033e-8f) / t : 0.f;
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
@@ -391,18 +405,13 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const SampleParams p) {
     }
     __syncthreads();
     constexpr int PL = BPC / 32;  // bins per lane of the scanning warp
-    u64 upto = 0;                 // of warp 0's lanes: their bins and all before, in this CTA
-    u64 mine = 0;
     if (warp == 0) {
-#pragma unroll 4
-      for (int e = 0; e < PL; ++e) mine += sh.sums[lane * PL + e];
-      upto = mine;
+      u64 x = 0;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const u64 x = __shfl_up_sync(0xffffffffu, upto, o);
-        if (lane >= o) upto += x;
-      }
-      if (lane == 31) sh.x_sum = upto;
+      for (int e = 0; e < PL; ++e) x += sh.sums[lane * PL + e];
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+      if (lane == 0) sh.x_sum = x;
     }
     sync_all();
     u64 tot[C], all = 0;
@@ -425,74 +434,50 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const SampleParams p) {
       }
       bm += tot[c];
     }
-    if (rank == owner && warp == 0) {
-      u64 x = first + upto - mine;
+    // every CTA looks into the owner's bins itself: cheaper than a third barrier
+    if (warp == 0) {
+      u64 own = 0;
+#pragma unroll 8
+      for (int e = 0; e < PL; ++e) own += ld_remote(&sh.sums[lane * PL + e], owner);
+      u64 x = own;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const u64 y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      x = first + x - own;
       if (lane == 0) sh.d_bin = 0;
       __syncwarp();
-      if (x < want && want <= x + mine)
+      if (x < want && want <= x + own)  // one lane
         for (int e = 0; e < PL; ++e) {
-          const u64 v = sh.sums[lane * PL + e];
-          if (x < want && want <= x + v) {
-            sh.d_bin = (unsigned)(rank * BPC + lane * PL + e);
+          const u64 v = ld_remote(&sh.sums[lane * PL + e], owner);
+          if (want <= x + v) {
+            sh.d_bin = (unsigned)(owner * BPC + lane * PL + e);
             sh.d_before = x;
+            break;
           }
           x += v;
         }
     }
-    sync_all();
-    before = ld_remote(&sh.d_before, owner);
-    return (int)ld_remote(&sh.d_bin, owner);
-  };
-  // Smallest and largest key of the cluster's elements that pass `in`.
-  auto key_range = [&](auto in, unsigned& lo, unsigned& hi) {
-    unsigned a = UINT_MAX, b = 0;
-#pragma unroll 4
-    for (int i = s0 + lane; i < s1; i += 32) {
-      const float l = row[i];
-      const unsigned k = key_of(l);
-      if (in(l)) {
-        a = min(a, k);
-        b = max(b, k);
-      }
-    }
-    a = __reduce_min_sync(0xffffffffu, a);
-    b = __reduce_max_sync(0xffffffffu, b);
-    if (lane == 0) {
-      sh.red_a[warp] = a;
-      sh.red_b[warp] = b;
-    }
     __syncthreads();
-    for (int w = 0; w < SWARPS; ++w) {
-      a = min(a, sh.red_a[w]);
-      b = max(b, sh.red_b[w]);
-    }
-    if (C > 1) {
-      if (tid == 0) {
-        sh.x_kmin = a;
-        sh.x_kmax = b;
-      }
-      cluster_barrier();
-      for (unsigned c = 0; c < (unsigned)C; ++c) {
-        a = min(a, ld_remote(&sh.x_kmin, c));
-        b = max(b, ld_remote(&sh.x_kmax, c));
-      }
-    }
-    sync_all();
-    lo = a;
-    hi = b;
+    before = sh.d_before;
+    return (int)sh.d_bin;
   };
   // "The threshold lies in bin `bin` of a first histogram" to one key; `before` becomes the
   // count or mass above that key.
   auto refine = [&](bool by_mass, u64 want, int bin, u64& before) -> unsigned {
-    unsigned lo, hi;
-    key_range([&](float l) { return bin_of(l) == bin; }, lo, hi);
+    // keys that can fall into the bin: its ends, moved out by more than bin_of can round
+    const float width = 1.f / bin_scale, slack = 4e-6f * ((float)(bin + 1) * width + fabsf(mx));
+    const float top = mx - (float)bin * width + slack, low = mx - (float)(bin + 1) * width - slack;
+    unsigned hi = top < mx ? key_of(top) : key_of(mx);
+    unsigned lo = bin < NB - 1 && low > -FLT_MAX ? key_of(low) : 0u;  // NaN and infinite ends: everything
     for (int it = 0; it < 5 && lo < hi; ++it) {  // ten bits of the key a round
       const int s = max(0, 22 - __clz(hi - lo));  // (hi - lo) >> s < NB
       clear();
       for (int i = s0 + lane; i < s1; i += 32) {
         const float l = row[i];
         const unsigned k = key_of(l);
-        if (k >= lo && k <= hi) {
+        if (k >= lo && k <= hi && bin_of(l) == bin) {
           const int b = (int)((hi - k) >> s);
           if (by_mass) add_mass(b, weight_fx(l, sc, sh.tab));
           else atomicAdd(&sh.limb[0][b], 1u);
@@ -591,9 +576,27 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const SampleParams p) {
     if (pp.shorter(pre)) pre = pp;
   }
   if (mp > 0.f) {
-    // w >= min_p  <=>  l >= m + T ln(min_p); an infinite product leaves everything
-    const float tf = mp >= 1.f ? mx : __double2float_ru((double)mx + sh.set_tlog);
-    const unsigned key = key_of(tf);
+    // the smallest key, up to the maximum's, whose weight is min_p of the maximum's: weights grow
+    // with the key, and a warp tries 32 keys a round
+    unsigned lo = 0, hi = key_of(mx);
+    if (mp >= 1.f) lo = hi;
+    if (warp == 0) {
+      const u64 least = ceil_mul(fminf(mp, 1.f), weight_fx(mx, sc, sh.tab));
+      for (int shift = 27; shift > -5; shift -= 5) {
+        const unsigned step = shift > 0 ? 1u << shift : 1u, off = step * (unsigned)lane;
+        const unsigned cand = off < hi - lo ? lo + off : hi;
+        const float x = cand < 0x007fffffu ? -INFINITY : value_of(cand);  // smaller keys are NaN patterns
+        const unsigned ok = __ballot_sync(0xffffffffu, weight_fx(x, sc, sh.tab) >= least);
+        const int f = ok ? __ffs(ok) - 1 : 31;
+        const unsigned c0 = __shfl_sync(0xffffffffu, cand, max(f - 1, 0)), c1 = __shfl_sync(0xffffffffu, cand, f);
+        if (ok && f > 0) lo = min(c0 + 1, c1);
+        if (!ok) lo = min(c1 + 1, hi);
+        if (ok) hi = c1;
+      }
+      if (lane == 0) sh.x_key = lo;
+    }
+    __syncthreads();
+    const unsigned key = sh.x_key;
     if (key > pre.key) {
       pre.key = key;
       pre.ties = UINT_MAX;
