@@ -258,7 +258,8 @@ int swiftkv_attention_weights(swiftkv_model* m, int cache, const void* q, int ld
  * with the largest scores (ties: the earlier key; NaN ranks last). The kept keys move, in order, to
  * rows 0.. of the destination, with their scores and FP8 scales; all other rows stay as they are.
  * Sequence s then holds min(seq_lens[s], keep) keys; a shorter one keeps them all.
- *   scores     HOST array [num_caches] of device float pools (those of the caches named are used)
+ *   scores     HOST array [num_caches] of device float pools, 16-byte aligned (those of the caches
+ *              named are used)
  *   seq_lens   HOST int32 [num_seqs]: keys held now
  *   dst_block_table  device int32 [num_seqs][dst_max_pages], or NULL: in place. Its pages must not
  *              be pages of any sequence's first seq_lens[s] keys; source pages are only read then,

@@ -30,15 +30,18 @@ namespace skv {
 
 namespace {
 
-constexpr int SW = 7;        // warps per CTA (one CTA per SM; 3 ring slots of 10 KB each fit 7)
+constexpr int SW = kSplitWarps;  // warps per CTA (one CTA per SM; 3 ring slots of 10 KB each fit 7)
 constexpr int SSTAGES = 3;   // ring slots per warp
 constexpr int SMAXG = 8;     // query heads per KV head (rows 0..7 of the mma A operand)
 
-template <int D>
+// EXT reads Q from global memory when a unit begins and gives the room to another ring slot: with
+// long units a warp waits for Q once, and more pages in flight are worth more.
+template <int D, bool EXT = false>
 struct Sp {
   static constexpr int PAGE = kPageSize * D;      // elements of one (page, head) K or V block
-  static constexpr int STAGE = 2 * PAGE + SMAXG * D;  // K, V, and the unit's Q when the page is its first
-  static constexpr int SMEM = SW * SSTAGES * STAGE * 2;
+  static constexpr int SLOTS = EXT ? 4 : SSTAGES;
+  static constexpr int STAGE = 2 * PAGE + (EXT ? 0 : SMAXG * D);  // K, V, and the unit's Q when the page is its first
+  static constexpr int SMEM = SW * SLOTS * STAGE * 2;
 };
 
 // EXT (AttnExt): units list visible keys only and may start inside a page, qpos is indexed by item,
@@ -50,16 +53,16 @@ __global__ void __launch_bounds__(SW * 32, 1) attn_split_kernel(
     const int* __restrict__ rows, const int* __restrict__ seqs, const int* __restrict__ units, int num_units,
     const int* __restrict__ ubeg, int n_q, int n_kv, bf16* __restrict__ out, int ldo, float* __restrict__ part,
     float scale_log2, const AttnExt ext) {
-  using S = Sp<D>;
+  using S = Sp<D, EXT>;
   constexpr int CH = D / 8;  // 16-byte chunks per row
   extern __shared__ __align__(128) unsigned char smem[];
   griddep_launch_dependents();  // a programmatic dependent may start as these blocks leave
   griddep_wait();               // itself launched as one: q and the cache rows are fresh
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  bf16* ring = reinterpret_cast<bf16*>(smem) + (size_t)warp * SSTAGES * S::STAGE;
+  bf16* ring = reinterpret_cast<bf16*>(smem) + (size_t)warp * S::SLOTS * S::STAGE;
   const int G = n_q / n_kv;
   const int total = num_units * n_kv;              // work items v = unit * n_kv + head
-  const int gw = blockIdx.x * SW + warp, nw = gridDim.x * SW;
+  const int gw = EXT ? warp * gridDim.x + blockIdx.x : blockIdx.x * SW + warp, nw = gridDim.x * SW;
 
   auto swz = [](int row, int ch) { return row * D + ((ch ^ (row & 7)) * 8); };
   struct Geo {
@@ -83,7 +86,7 @@ __global__ void __launch_bounds__(SW * 32, 1) attn_split_kernel(
     return g;
   };
 
-  // loader: walks this warp's (work item, page) sequence SSTAGES - 1 pages ahead of the compute
+  // loader: walks this warp's (work item, page) sequence S::SLOTS - 1 pages ahead of the compute
   int lv = gw, lp = 0, lslot = 0;
   Geo lg;
   if (lv < total) lg = geo(lv);
@@ -102,14 +105,14 @@ __global__ void __launch_bounds__(SW * 32, 1) attn_split_kernel(
         cp_async16(smem_u32(st + swz(row, ch)), kpool + base + row * D + ch * 8, bytes);
         cp_async16(smem_u32(st + S::PAGE + swz(row, ch)), vpool + base + row * D + ch * 8, bytes);
       }
-      if (lp == 0) {  // the unit's query heads ride with its first page
+      if (!EXT && lp == 0) {  // the unit's query heads ride with its first page
         const bf16* qsrc = q + (size_t)lg.r * ldq + (size_t)lg.kvh * G * D;
         for (int c = lane; c < G * CH; c += 32) {
           const int row = c / CH, ch = c % CH;
           cp_async16(smem_u32(st + 2 * S::PAGE + swz(row, ch)), qsrc + row * D + ch * 8, 16);
         }
       }
-      if (++lslot == SSTAGES) lslot = 0;
+      if (++lslot == S::SLOTS) lslot = 0;
       if (++lp == lg.npages) {
         lp = 0;
         lv += nw;
@@ -126,13 +129,13 @@ __global__ void __launch_bounds__(SW * 32, 1) attn_split_kernel(
   float m0 = -FLT_MAX, l0 = 0.f;
 
 #pragma unroll
-  for (int i = 0; i < SSTAGES - 1; ++i) issue();
+  for (int i = 0; i < S::SLOTS - 1; ++i) issue();
   int cv = gw, cp = 0, cslot = 0;
   Geo cg;
   if (cv < total) cg = geo(cv);
   while (cv < total) {
     issue();
-    cp_async_wait<SSTAGES - 1>();
+    cp_async_wait<S::SLOTS - 1>();
     __syncwarp();
     bf16* st = ring + cslot * S::STAGE;
     const bf16* kb = st;
@@ -143,7 +146,9 @@ __global__ void __launch_bounds__(SW * 32, 1) attn_split_kernel(
       for (int ks = 0; ks < D / 16; ++ks) {
         const int c = ks * 16 + qc;
         auto qat = [&](int g, int col) -> uint32_t {  // g < 8
-          return g < G ? *reinterpret_cast<const uint32_t*>(qs + swz(g, col / 8) + (col & 7)) : 0u;
+          if (g >= G) return 0u;
+          if (EXT) return *reinterpret_cast<const uint32_t*>(q + (size_t)cg.r * ldq + (size_t)(cg.kvh * G + g) * D + col);
+          return *reinterpret_cast<const uint32_t*>(qs + swz(g, col / 8) + (col & 7));
         };
         qf[ks][0] = qat(g0, c);
         qf[ks][1] = 0u;
@@ -236,7 +241,7 @@ __global__ void __launch_bounds__(SW * 32, 1) attn_split_kernel(
       mma_bf16_16816(o[2 * dp + 1], pl, b1);
     }
     __syncwarp();  // the slot is refilled by a later issue()
-    if (++cslot == SSTAGES) cslot = 0;
+    if (++cslot == S::SLOTS) cslot = 0;
 
     if (++cp == cg.npages) {
       // unit done: the whole row -> output; one split of it -> (max, sum, unnormalised O)
@@ -287,12 +292,13 @@ __global__ void __launch_bounds__(SW * 32, 1) attn_split_kernel(
 // when it grows, like the softmax max), and O * S_ref is the unnormalised output.
 constexpr int SSTAGES8 = 3;
 
-template <int D>
+template <int D, bool EXT = false>
 struct Sp8 {
   static constexpr int CODES = kPageSize * D;        // bytes of one (page, head) K or V block
-  static constexpr int QB = SMAXG * D * 2;            // bytes of the unit's query rows (bf16)
+  static constexpr int QB = EXT ? 0 : SMAXG * D * 2;  // bytes of the unit's query rows (bf16)
+  static constexpr int SLOTS = EXT ? 7 : SSTAGES8;
   static constexpr int STAGE = 2 * CODES + 2 * kPageSize * 4 + QB;
-  static constexpr int SMEM = SW * SSTAGES8 * STAGE;
+  static constexpr int SMEM = SW * SLOTS * STAGE;
   static constexpr int CHB = D / 16;                  // 16-byte chunks per code row
 };
 
@@ -303,15 +309,15 @@ __global__ void __launch_bounds__(SW * 32, 1) attn_split_fp8_kernel(
     int num_pages, const int* __restrict__ qpos, const int* __restrict__ rows, const int* __restrict__ seqs,
     const int* __restrict__ units, int num_units, const int* __restrict__ ubeg, int n_q, int n_kv,
     bf16* __restrict__ out, int ldo, float* __restrict__ part, float scale_log2, const AttnExt ext) {
-  using S = Sp8<D>;
+  using S = Sp8<D, EXT>;
   extern __shared__ __align__(128) unsigned char smem[];
   griddep_launch_dependents();
   griddep_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  unsigned char* ring = smem + (size_t)warp * SSTAGES8 * S::STAGE;
+  unsigned char* ring = smem + (size_t)warp * S::SLOTS * S::STAGE;
   const int G = n_q / n_kv;
   const int total = num_units * n_kv;
-  const int gw = blockIdx.x * SW + warp, nw = gridDim.x * SW;
+  const int gw = EXT ? warp * gridDim.x + blockIdx.x : blockIdx.x * SW + warp, nw = gridDim.x * SW;
 
   // code rows of D bytes, 16-byte chunks XOR-swizzled so 8 rows of one chunk hit 8 bank groups
   auto swzb = [](int row, int ch) {
@@ -362,7 +368,7 @@ __global__ void __launch_bounds__(SW * 32, 1) attn_split_fp8_kernel(
         const float* sp = (lane < 4 ? kscale : vscale) + blk * kPageSize + (lane & 3) * 4;
         cp_async16(smem_u32(st + 2 * S::CODES + lane * 16), sp, ok ? 16 : 0);
       }
-      if (lp == 0) {
+      if (!EXT && lp == 0) {
         const bf16* qsrc = q + (size_t)lg.r * ldq + (size_t)lg.kvh * G * D;
         bf16* qs = reinterpret_cast<bf16*>(st + 2 * S::CODES + 2 * kPageSize * 4);
         for (int c = lane; c < G * (D / 8); c += 32) {
@@ -370,7 +376,7 @@ __global__ void __launch_bounds__(SW * 32, 1) attn_split_fp8_kernel(
           cp_async16(smem_u32(qs + swzq(row, ch)), qsrc + row * D + ch * 8, 16);
         }
       }
-      if (++lslot == SSTAGES8) lslot = 0;
+      if (++lslot == S::SLOTS) lslot = 0;
       if (++lp == lg.npages) {
         lp = 0;
         lv += nw;
@@ -386,13 +392,13 @@ __global__ void __launch_bounds__(SW * 32, 1) attn_split_fp8_kernel(
   float m0 = -FLT_MAX, l0 = 0.f, sref = 0.f;
 
 #pragma unroll
-  for (int i = 0; i < SSTAGES8 - 1; ++i) issue();
+  for (int i = 0; i < S::SLOTS - 1; ++i) issue();
   int cv = gw, cp = 0, cslot = 0;
   Geo cg;
   if (cv < total) cg = geo(cv);
   while (cv < total) {
     issue();
-    cp_async_wait<SSTAGES8 - 1>();
+    cp_async_wait<S::SLOTS - 1>();
     __syncwarp();
     const unsigned char* st = ring + cslot * S::STAGE;
     const float* sk = reinterpret_cast<const float*>(st + 2 * S::CODES);
@@ -403,7 +409,9 @@ __global__ void __launch_bounds__(SW * 32, 1) attn_split_fp8_kernel(
       for (int ks = 0; ks < D / 16; ++ks) {
         uint32_t lo = 0u, hi = 0u;
         if (g0 < G) {
-          const uint2 w = *reinterpret_cast<const uint2*>(qs + swzq(g0, 2 * ks + (qd >> 1)) + 4 * (qd & 1));
+          const uint2 w = *reinterpret_cast<const uint2*>(
+              EXT ? q + (size_t)cg.r * ldq + (size_t)(cg.kvh * G + g0) * D + ks * 16 + 4 * qd
+                  : qs + swzq(g0, 2 * ks + (qd >> 1)) + 4 * (qd & 1));
           const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w.x));
           const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w.y));
           lo = pack_f16(a.x, a.y);
@@ -514,7 +522,7 @@ __global__ void __launch_bounds__(SW * 32, 1) attn_split_fp8_kernel(
       }
     }
     __syncwarp();
-    if (++cslot == SSTAGES8) cslot = 0;
+    if (++cslot == S::SLOTS) cslot = 0;
 
     if (++cp == cg.npages) {
       float s0 = l0;
@@ -563,8 +571,7 @@ template <int D>
 __global__ void __launch_bounds__(CMB_THREADS) attn_split_combine(const int* __restrict__ rows,
                                                                   const int* __restrict__ ubeg, int n_q, int n_kv,
                                                                   const float* __restrict__ part,
-                                                                  bf16* __restrict__ out, int ldo,
-                                                                  float* __restrict__ lse, int ldl) {
+                                                                  bf16* __restrict__ out, int ldo) {
   __shared__ float s_w[CMB_MAX_W];
   __shared__ float s_mx[SMAXG], s_den[SMAXG];
   griddep_launch_dependents();
@@ -599,7 +606,6 @@ __global__ void __launch_bounds__(CMB_THREADS) attn_split_combine(const int* __r
     if (lane == 0) {
       s_mx[g] = mx;
       s_den[g] = den;
-      if (lse) lse[(size_t)(kvh * G + g) * ldl + r] = (mx + log2f(den)) * 0.69314718055994531f;
     }
   }
   __syncthreads();
@@ -624,11 +630,90 @@ __global__ void __launch_bounds__(CMB_THREADS) attn_split_combine(const int* __r
   }
 }
 
+// The same for EXT, one warp per (item, query head): a lane owns D / 32 neighbouring dimensions,
+// lanes share out the splits' maxima and sums, and a batch of partial rows is in flight before the
+// first is used, so a merge of a few splits takes one trip to memory (the CTA-wide one takes three:
+// 6 against 3 us for 24 rows of 40 heads).
+constexpr int CMB_WARPS = 4;
+
+template <int D>
+__global__ void __launch_bounds__(CMB_WARPS * 32) attn_split_merge(const int* __restrict__ rows,
+                                                                   const int* __restrict__ ubeg, int items, int n_q,
+                                                                   int n_kv, const float* __restrict__ part,
+                                                                   bf16* __restrict__ out, int ldo,
+                                                                   float* __restrict__ lse, int ldl) {
+  griddep_launch_dependents();
+  griddep_wait();
+  const long long w = (long long)blockIdx.x * CMB_WARPS + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (w >= (long long)items * n_q) return;
+  const int b = (int)(w / n_q), h = (int)(w - (long long)b * n_q);
+  const int G = n_q / n_kv, kvh = h / G, g = h - kvh * G;
+  const int u0 = ubeg[b], ns = ubeg[b + 1] - u0;
+  if (ns <= 1) return;  // written by its only unit
+  const size_t step = (size_t)n_q * (D + 2);
+  const float* p = part + ((size_t)u0 * n_kv + kvh) * G * (D + 2) + (size_t)g * (D + 2);
+  constexpr int E = D / 32, B = 8;
+  float o[E], m = -INFINITY, den = 0.f;
+#pragma unroll
+  for (int e = 0; e < E; ++e) o[e] = 0.f;
+  for (int i0 = 0; i0 < ns; i0 += B) {
+    float v[B][E], pm = -INFINITY, pl = 0.f;
+    if (lane < B && i0 + lane < ns) {
+      const float2 ml = *reinterpret_cast<const float2*>(p + (i0 + lane) * step);
+      pm = ml.x;
+      pl = ml.y;
+    }
+#pragma unroll
+    for (int i = 0; i < B; ++i)
+#pragma unroll
+      for (int e = 0; e < E; e += 2) {
+        float2 x = make_float2(0.f, 0.f);
+        if (i0 + i < ns) x = *reinterpret_cast<const float2*>(p + (i0 + i) * step + 2 + lane * E + e);
+        v[i][e] = x.x;
+        v[i][e + 1] = x.y;
+      }
+    float mx = pm;
+#pragma unroll
+    for (int off = 4; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+    mx = fmaxf(m, __shfl_sync(0xffffffffu, mx, 0));
+    const float keep = exp2f(m - mx), wt = exp2f(pm - mx);
+    m = mx;
+    float l = pl * wt;
+#pragma unroll
+    for (int off = 4; off > 0; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
+    den = den * keep + __shfl_sync(0xffffffffu, l, 0);
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] *= keep;
+#pragma unroll
+    for (int i = 0; i < B; ++i) {
+      const float wi = __shfl_sync(0xffffffffu, wt, i);
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] = fmaf(v[i][e], wi, o[e]);
+    }
+  }
+  const int r = rows[b];
+  const float inv = 1.f / den;
+  bf16* dst = out + (size_t)r * ldo + (size_t)h * D + lane * E;
+#pragma unroll
+  for (int e = 0; e < E; e += 2) *reinterpret_cast<uint32_t*>(dst + e) = pack_bf16(o[e] * inv, o[e + 1] * inv);
+  if (lse && lane == 0) lse[(size_t)h * ldl + r] = (m + log2f(den)) * 0.69314718055994531f;
+}
+
+template <int D>
+cudaError_t launch_merge(const SplitPlan& plan, const int* rows, int n_q, int n_kv, bf16* out, int ldo,
+                         const AttnExt& ext, cudaStream_t stream) {
+  const long long warps = (long long)plan.num_items * n_q;
+  return launch_pdl(attn_split_merge<D>, dim3((unsigned)((warps + CMB_WARPS - 1) / CMB_WARPS)), dim3(CMB_WARPS * 32), 0,
+                    stream, rows, (const int*)plan.ubeg, plan.num_items, n_q, n_kv, (const float*)plan.part, out, ldo,
+                    ext.lse, ext.ldl);
+}
+
 template <int D, bool EXT>
 cudaError_t split_d(const bf16* q, int ldq, const bf16* k_pool, const bf16* v_pool, const int* bt, int max_pages,
                     int num_pages, const int* qpos, const int* rows, const int* seqs, const SplitPlan& plan,
                     int n_q, int n_kv, bf16* out, int ldo, int num_sms, cudaStream_t stream, const AttnExt& ext) {
-  constexpr int smem = Sp<D>::SMEM;
+  constexpr int smem = Sp<D, EXT>::SMEM;
   static_assert(smem <= 227 * 1024, "rings must fit in shared memory");
   static PerDeviceOnce smem_attr;
   {
@@ -637,13 +722,14 @@ cudaError_t split_d(const bf16* q, int ldq, const bf16* k_pool, const bf16* v_po
   }
   const float scale_log2 = 1.4426950408889634f / sqrtf((float)D);
   const int total = plan.num_units * n_kv;
-  const int ctas = std::min((total + SW - 1) / SW, num_sms);
+  const int ctas = EXT ? std::min(total, num_sms) : std::min((total + SW - 1) / SW, num_sms);
   cudaError_t e = launch_pdl(attn_split_kernel<D, EXT>, dim3(ctas), dim3(SW * 32), smem, stream, q, ldq, k_pool, v_pool,
                              bt, max_pages, num_pages, qpos, rows, seqs, (const int*)plan.units, plan.num_units,
                              (const int*)plan.ubeg, n_q, n_kv, out, ldo, plan.part, scale_log2, ext);
   if (e != cudaSuccess || !plan.any_split) return e;
+  if (EXT) return launch_merge<D>(plan, rows, n_q, n_kv, out, ldo, ext, stream);
   return launch_pdl(attn_split_combine<D>, dim3(plan.num_items, n_kv), dim3(CMB_THREADS), 0, stream, rows,
-                    (const int*)plan.ubeg, n_q, n_kv, (const float*)plan.part, out, ldo, ext.lse, ext.ldl);
+                    (const int*)plan.ubeg, n_q, n_kv, (const float*)plan.part, out, ldo);
 }
 
 template <int D, bool EXT>
@@ -651,9 +737,9 @@ cudaError_t split_fp8_d(const bf16* q, int ldq, const uint8_t* k8, const uint8_t
                         const float* vs, const int* bt, int max_pages, int num_pages, const int* qpos,
                         const int* rows, const int* seqs, const SplitPlan& plan, int n_q, int n_kv, bf16* out,
                         int ldo, int num_sms, cudaStream_t stream, const AttnExt& ext) {
-  constexpr int smem = Sp8<D>::SMEM;
+  constexpr int smem = Sp8<D, EXT>::SMEM;
   static_assert(smem <= 227 * 1024, "rings must fit in shared memory");
-  static_assert(Sp8<D>::STAGE % 16 == 0, "ring slots must keep 16-byte alignment");
+  static_assert(Sp8<D, EXT>::STAGE % 16 == 0, "ring slots must keep 16-byte alignment");
   static PerDeviceOnce smem_attr;
   {
     cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void*>(attn_split_fp8_kernel<D, EXT>), smem, smem_attr);
@@ -661,13 +747,14 @@ cudaError_t split_fp8_d(const bf16* q, int ldq, const uint8_t* k8, const uint8_t
   }
   const float scale_log2 = 1.4426950408889634f / sqrtf((float)D);
   const int total = plan.num_units * n_kv;
-  const int ctas = std::min((total + SW - 1) / SW, num_sms);
+  const int ctas = EXT ? std::min(total, num_sms) : std::min((total + SW - 1) / SW, num_sms);
   cudaError_t e = launch_pdl(attn_split_fp8_kernel<D, EXT>, dim3(ctas), dim3(SW * 32), smem, stream, q, ldq, k8, v8, ks,
                              vs, bt, max_pages, num_pages, qpos, rows, seqs, (const int*)plan.units, plan.num_units,
                              (const int*)plan.ubeg, n_q, n_kv, out, ldo, plan.part, scale_log2, ext);
   if (e != cudaSuccess || !plan.any_split) return e;
+  if (EXT) return launch_merge<D>(plan, rows, n_q, n_kv, out, ldo, ext, stream);
   return launch_pdl(attn_split_combine<D>, dim3(plan.num_items, n_kv), dim3(CMB_THREADS), 0, stream, rows,
-                    (const int*)plan.ubeg, n_q, n_kv, (const float*)plan.part, out, ldo, ext.lse, ext.ldl);
+                    (const int*)plan.ubeg, n_q, n_kv, (const float*)plan.part, out, ldo);
 }
 
 }  // namespace
@@ -701,30 +788,6 @@ void split_plan_host(const int* nkeys, int items, std::vector<int>* units, std::
       units->push_back(k0);
       units->push_back(split);
     }
-    ubeg->push_back((int)(units->size() / 3));
-  }
-}
-
-void split_plan_host_window(const int* qpos, int items, int window, int sinks, std::vector<int>* units,
-                            std::vector<int>* ubeg) {
-  units->clear();
-  ubeg->assign(1, 0);
-  for (int b = 0; b < items; ++b) {
-    const int end = qpos[b] + 1, w0 = window_begin(qpos[b], window);
-    const int s1 = window > 0 && w0 > 0 ? std::min(sinks, w0) : 0;  // keys [0, s1) and [w0, end)
-    const int first = s1 == w0 ? 0 : w0;                            // sinks that reach the window join it
-    const int split = split_keys_for(end - first + (first ? s1 : 0));
-    auto range = [&](int k0, int k1) {
-      while (k0 < k1) {  // units end on multiples of the split, so that only a range's first is ragged
-        const int e = std::min(k1, (k0 / split + 1) * split);
-        units->push_back(b);
-        units->push_back(k0);
-        units->push_back(e - k0);
-        k0 = e;
-      }
-    };
-    if (first) range(0, s1);
-    range(first, end);
     ubeg->push_back((int)(units->size() / 3));
   }
 }

@@ -35,7 +35,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 
 // ---------------------------------------------------------------------------- few rows
 
-constexpr int RW = 12;      // warps per CTA, one CTA per SM
+constexpr int RW = kWeightWarps;  // warps per CTA, one CTA per SM
 constexpr int RSTAGES = 4;  // ring slots per warp
 
 template <int D, bool FP8>
@@ -60,7 +60,7 @@ __global__ void __launch_bounds__(RW * 32, 1) weights_rows_kernel(const WeightsA
   unsigned char* ring = smem + (size_t)warp * RSTAGES * S::STAGE;
   const int G = a.n_q / a.n_kv;
   const long long total = (long long)num_units * a.n_kv;
-  const long long gw = (long long)blockIdx.x * RW + warp, nw = (long long)gridDim.x * RW;
+  const long long gw = (long long)warp * gridDim.x + blockIdx.x, nw = (long long)gridDim.x * RW;
   constexpr int RB = D * (FP8 ? 1 : 2), CH = RB / 16;  // bytes and 16-byte chunks of a key
   // chunks XOR-swizzled so that 8 rows of one chunk fall into 8 bank groups (rows of 64 bytes
   // come in pairs per 128)
@@ -575,7 +575,7 @@ cudaError_t rows_launch(const WeightsArgs& a, const bf16* k, const uint8_t* k8, 
   cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void*>(weights_rows_kernel<D, FP8, NT>), smem, once);
   if (e != cudaSuccess) return e;
   const long long total = (long long)num_units * a.n_kv;
-  const int ctas = (int)(total + RW - 1 < (long long)num_sms * RW ? (total + RW - 1) / RW : num_sms);
+  const int ctas = (int)(total < num_sms ? total : num_sms);
   return launch_pdl(weights_rows_kernel<D, FP8, NT>, dim3(ctas), dim3(RW * 32), smem, s, a, k, k8, ks, units, num_units,
                     kLog2e / sqrtf((float)D));
 }

@@ -51,10 +51,16 @@ __device__ __forceinline__ long long row_of(const int* bt, int width, int num_pa
   return ((long long)page * n_kv + l.h) * kPageSize + (j & 15);
 }
 
+// Digits of a key, most significant first: 11 + 11 + 10 bits. Scores crowd into few exponents, and
+// two more bits a digit than a byte spread their first histogram over enough bins to need no
+// aggregation within the warp.
+constexpr int EBINS = 2048;
+__device__ __forceinline__ int digit_shift(int d) { return d == 0 ? 21 : d == 1 ? 10 : 0; }
+
 __global__ void __launch_bounds__(ET) evict_select_kernel(const EvictArgs a, int in_smem) {
-  extern __shared__ unsigned keys[];  // [n] when in_smem
-  __shared__ unsigned hist[256];
-  __shared__ unsigned s_key, s_left;
+  extern __shared__ __align__(16) unsigned keys[];  // [n rounded up to pages] when in_smem
+  __shared__ unsigned hist[EBINS];
+  __shared__ unsigned s_sum[EWARPS], s_key, s_left;
   __shared__ int s_cnt[2][EWARPS];
   griddep_launch_dependents();
   griddep_wait();
@@ -62,19 +68,12 @@ __global__ void __launch_bounds__(ET) evict_select_kernel(const EvictArgs a, int
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const float* scores = a.scores[a.first_cache + l.c];
   int* kept = a.kept + (size_t)blockIdx.x * a.keep;
-  const int n = l.n;
-  auto key_at = [&](int j) -> unsigned {
-    if (j < a.sinks || j >= n - a.recent) return UINT_MAX;
-    const long long r = row_of(a.src_bt, a.src_pages, a.num_pages, a.n_kv, l, j);
-    return r < 0 ? 0u : score_key(scores[r]);
-  };
+  const int n = l.n, pages = (n + kPageSize - 1) / kPageSize;
+  const int* bt = a.src_bt + (size_t)l.s * a.src_pages;
   // an entry outside the pool: the status says so, and the list is left as it is
   int bad = 0;
   const int out_pages = (min(n, a.keep) + kPageSize - 1) / kPageSize;
-  for (int p = tid; p < (n + kPageSize - 1) / kPageSize; p += ET) {
-    const int page = a.src_bt[(size_t)l.s * a.src_pages + p];
-    bad |= page < 0 || page >= a.num_pages;
-  }
+  for (int p = tid; p < pages; p += ET) bad |= bt[p] < 0 || bt[p] >= a.num_pages;
   for (int p = tid; p < out_pages; p += ET) {
     const int page = a.dst_bt[(size_t)l.s * a.dst_pages + p];
     bad |= page < 0 || page >= a.num_pages;
@@ -84,47 +83,74 @@ __global__ void __launch_bounds__(ET) evict_select_kernel(const EvictArgs a, int
     for (int i = tid; i < a.keep; i += ET) kept[i] = -1;
     return;
   }
+  // keys of rows 4 q .. 4 q + 3 (a quarter of a page); rows behind the list: 0, never counted
+  auto quad = [&](int q) -> uint4 {
+    const float4 v = *reinterpret_cast<const float4*>(
+        scores + ((size_t)bt[q >> 2] * a.n_kv + l.h) * kPageSize + (q & 3) * 4);
+    const float f[4] = {v.x, v.y, v.z, v.w};
+    unsigned k[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int j = 4 * q + e;
+      k[e] = j >= n ? 0u : j < a.sinks || j >= n - a.recent ? UINT_MAX : score_key(f[e]);
+    }
+    return make_uint4(k[0], k[1], k[2], k[3]);
+  };
   if (n <= a.keep) {
     for (int i = tid; i < a.keep; i += ET) kept[i] = i < n ? i : -1;
   } else {
+    const int quads = pages * 4;
     if (in_smem) {
-      for (int j = tid; j < n; j += ET) keys[j] = key_at(j);
-      __syncthreads();
+      constexpr int U = 4;
+      for (int q0 = tid; q0 < quads; q0 += ET * U) {
+        uint4 v[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (q0 + u * ET < quads) v[u] = quad(q0 + u * ET);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (q0 + u * ET < quads) reinterpret_cast<uint4*>(keys)[q0 + u * ET] = v[u];
+      }
     }
-    auto key = [&](int j) { return in_smem ? keys[j] : key_at(j); };
-    // the keep-th largest key, eight bits a round
+    auto key4 = [&](int q) { return in_smem ? reinterpret_cast<const uint4*>(keys)[q] : quad(q); };
+    // the keep-th largest key, a digit a round
     unsigned prefix = 0, left = (unsigned)a.keep;
-    for (int shift = 24; shift >= 0; shift -= 8) {
-      for (int b = tid; b < 256; b += ET) hist[b] = 0;
+    for (int d = 0; d < 3; ++d) {
+      const int shift = digit_shift(d), bits = d == 2 ? 10 : 11;
+      for (int b = tid; b < EBINS; b += ET) hist[b] = 0;
       __syncthreads();
-      const unsigned mask = shift == 24 ? 0u : ~0u << (shift + 8);
-      for (int j0 = 0; j0 < n; j0 += ET) {
-        const int j = j0 + tid;
-        const unsigned k = j < n ? key(j) : 0u;
-        const bool in = j < n && (k & mask) == prefix;
-        const unsigned b = (k >> shift) & 255u;
-        // scores share their leading bits: one add per distinct bin of the warp
-        const unsigned peers = __match_any_sync(0xffffffffu, in ? b : 256u);
-        if (in && (peers & ((1u << lane) - 1)) == 0) atomicAdd(&hist[b], (unsigned)__popc(peers));
+      const unsigned mask = d == 0 ? 0u : ~0u << (shift + bits);
+      for (int q = tid; q < quads; q += ET) {
+        const uint4 v = key4(q);
+        const unsigned k[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if ((k[e] & mask) == prefix && 4 * q + e < n) atomicAdd(&hist[(k[e] >> shift) & ((1u << bits) - 1)], 1u);
       }
       __syncthreads();
-      if (warp == 0) {  // lane: bins 255 - 8 lane .. down
-        unsigned c = 0;
-        for (int e = 0; e < 8; ++e) c += hist[255 - 8 * lane - e];
-        unsigned upto = c;
+      // descending: thread t owns bins top - 4 t .. top - 4 t - 3
+      constexpr int PER = EBINS / ET;
+      unsigned c[PER], mine = 0;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const unsigned x = __shfl_up_sync(0xffffffffu, upto, o);
-          if (lane >= o) upto += x;
-        }
-        unsigned before = upto - c;
-        for (int e = 0; e < 8; ++e) {
-          const unsigned v = hist[255 - 8 * lane - e];
-          if (before < left && left <= before + v) {
-            s_key = prefix | ((unsigned)(255 - 8 * lane - e) << shift);
+      for (int e = 0; e < PER; ++e) mine += c[e] = hist[EBINS - 1 - PER * tid - e];
+      unsigned upto = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const unsigned x = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += x;
+      }
+      if (lane == 31) s_sum[warp] = upto;
+      __syncthreads();
+      for (int w = 0; w < warp; ++w) upto += s_sum[w];
+      unsigned before = upto - mine;
+      if (before < left && left <= upto) {
+#pragma unroll
+        for (int e = 0; e < PER; ++e) {
+          if (before < left && left <= before + c[e]) {
+            s_key = prefix | ((unsigned)(EBINS - 1 - PER * tid - e) << shift);
             s_left = left - before;
           }
-          before += v;
+          before += c[e];
         }
       }
       __syncthreads();
@@ -133,30 +159,43 @@ __global__ void __launch_bounds__(ET) evict_select_kernel(const EvictArgs a, int
     }
     // ordered pass: everything above the key, and the first `left` at it
     int above = 0, ties = 0;  // before this round
-    for (int j0 = 0; j0 < n; j0 += ET) {
-      const int j = j0 + tid, par = (j0 / ET) & 1;
-      const unsigned k = j < n ? key(j) : 0u;
-      const unsigned gt = __ballot_sync(0xffffffffu, j < n && k > prefix);
-      const unsigned eq = __ballot_sync(0xffffffffu, j < n && k == prefix);
-      if (lane == 0) s_cnt[par][warp] = __popc(gt) | __popc(eq) << 16;
+    for (int q0 = 0; q0 < quads; q0 += ET) {
+      const int q = q0 + tid, par = (q0 / ET) & 1;
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (q < quads) v = key4(q);
+      const unsigned k[4] = {v.x, v.y, v.z, v.w};
+      unsigned gt = 0, eq = 0;  // of the thread's four keys
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const bool in = q < quads && 4 * q + e < n;
+        gt |= (unsigned)(in && k[e] > prefix) << e;
+        eq |= (unsigned)(in && k[e] == prefix) << e;
+      }
+      int both = __popc(gt) | __popc(eq) << 16, upto = both;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += x;
+      }
+      if (lane == 31) s_cnt[par][warp] = upto;
       __syncthreads();
-      int g0 = 0, e0 = 0, gs = 0, es = 0;
+      int first = upto - both, all = 0;
 #pragma unroll
       for (int w = 0; w < EWARPS; ++w) {
         const int c = s_cnt[par][w];
-        if (w < warp) {
-          g0 += c & 0xffff;
-          e0 += c >> 16;
-        }
-        gs += c & 0xffff;
-        es += c >> 16;
+        if (w < warp) first += c;
+        all += c;
       }
-      const unsigned below = (1u << lane) - 1;
-      const int my_gt = above + g0 + __popc(gt & below), my_eq = ties + e0 + __popc(eq & below);
-      const bool is_gt = gt >> lane & 1, is_eq = eq >> lane & 1;
-      if (is_gt || (is_eq && my_eq < (int)left)) kept[my_gt + min(my_eq, (int)left)] = j;
-      above += gs;
-      ties += es;
+      int g = above + (first & 0xffff), t = ties + (first >> 16);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const bool is_gt = gt >> e & 1, is_eq = eq >> e & 1;
+        if (is_gt || (is_eq && t < (int)left)) kept[g + min(t, (int)left)] = 4 * q + e;
+        g += is_gt;
+        t += is_eq;
+      }
+      above += all & 0xffff;
+      ties += all >> 16;
     }
   }
   __syncthreads();  // kept, written by this CTA, is read below
@@ -164,22 +203,29 @@ __global__ void __launch_bounds__(ET) evict_select_kernel(const EvictArgs a, int
   const int m = min(n, a.keep);
   const int c = a.first_cache + l.c;
   float* arrays[3] = {a.scores[c], a.ks ? a.ks[c] : nullptr, a.vs ? a.vs[c] : nullptr};
-  for (int i0 = 0; i0 < m; i0 += ET) {
-    const int i = i0 + tid;
-    float v[3];
-    long long to = -1;
-    if (i < m) {
-      const long long from = row_of(a.src_bt, a.src_pages, a.num_pages, a.n_kv, l, kept[i]);
-      to = row_of(a.dst_bt, a.dst_pages, a.num_pages, a.n_kv, l, i);
+  constexpr int U = 4;
+  for (int i0 = 0; i0 < m; i0 += ET * U) {
+    float v[U][3];
+    long long to[U];
 #pragma unroll
-      for (int t = 0; t < 3; ++t)
-        if (arrays[t]) v[t] = arrays[t][from];
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + u * ET + tid;
+      to[u] = -1;
+      if (i < m) {
+        const long long from = row_of(a.src_bt, a.src_pages, a.num_pages, a.n_kv, l, kept[i]);
+        to[u] = row_of(a.dst_bt, a.dst_pages, a.num_pages, a.n_kv, l, i);
+#pragma unroll
+        for (int t = 0; t < 3; ++t)
+          if (arrays[t]) v[u][t] = arrays[t][from];
+      }
     }
     __syncthreads();
-    if (to >= 0)
 #pragma unroll
-      for (int t = 0; t < 3; ++t)
-        if (arrays[t]) arrays[t][to] = v[t];
+    for (int u = 0; u < U; ++u)
+      if (to[u] >= 0)
+#pragma unroll
+        for (int t = 0; t < 3; ++t)
+          if (arrays[t]) arrays[t][to[u]] = v[u][t];
   }
 }
 
@@ -284,7 +330,7 @@ cudaError_t launch_evict(const EvictArgs& a, int max_len, cudaStream_t s) {
   cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void*>(evict_select_kernel), kSelectSmemKeys * 4, once);
   if (e != cudaSuccess) return e;
   const int in_smem = max_len <= kSelectSmemKeys;
-  e = launch_pdl(evict_select_kernel, dim3((unsigned)lists), dim3(ET), in_smem ? (size_t)max_len * 4 : 0, s, a, in_smem);
+  e = launch_pdl(evict_select_kernel, dim3((unsigned)lists), dim3(ET), in_smem ? (size_t)(max_len + 15) / 16 * 64 : 0, s, a, in_smem);
   if (e != cudaSuccess) return e;
   if (a.in_place) return launch_pdl(evict_shift_kernel, dim3((unsigned)ctas), dim3(MT), 0, s, a, cols);
   return launch_pdl(evict_copy_kernel, dim3((unsigned)ctas), dim3(MT), 0, s, a, parts);

@@ -268,8 +268,7 @@ cudaError_t launch_attention_decode_split(const bf16* q, int ldq, const bf16* k_
                                           const int* rows, const int* seqs, const SplitPlan& plan, int n_q,
                                           int n_kv, int d_head, bf16* out, int ldo, int num_sms,
                                           cudaStream_t stream, const AttnExt* ext = nullptr);
-// With ext, units hold visible keys only (split_plan_host_window) and may start inside a page.
-void split_plan_host_window(const int* qpos, int items, int window, int sinks, std::vector<int>* units,
-                            std::vector<int>* ubeg);
+// With ext, units hold visible keys only, may start inside a page, and qpos is indexed by item.
+constexpr int kSplitWarps = 7;  // warps per SM that walk units
 
 }  // namespace skv

@@ -55,6 +55,48 @@ Ranges seen_ranges(int c0, int n, int window, int sinks) {
   return r;
 }
 
+int pages_of(int k0, int k1) { return k1 > k0 ? (k1 - 1) / kPageSize - k0 / kPageSize + 1 : 0; }
+
+// Cuts the items' key ranges into units (item, first key, keys) of whole pages and about the same
+// length, so that each of `warps` warps gets one per KV head: units of a fixed 128 or 256 keys left
+// the last round of warps half empty (attention of 24 rows of ~1100 keys, 40 / 8 heads: 22 against
+// 25 us; 16 windows of 4100 FP8 keys: 60 against 83 us). The rounding of a row split this way
+// depends on the call it is part of. ubeg [items + 1]: each item's first unit.
+constexpr int kMinUnitPages = 4;   // below this a unit's partial result costs more than it spreads
+constexpr int kMaxUnitPages = 64;  // with more items than warps: the last round stays short
+void cut_units(const std::vector<int>& item_ids, const std::vector<Ranges>& seen, int n_kv, long long warps,
+               std::vector<int>* units, std::vector<int>* ubeg) {
+  auto count = [&](int len) {
+    long long n = 0;
+    for (const Ranges& r : seen)
+      for (int i = 0; i < r.n; ++i) n += (pages_of(r.k0[i], r.k1[i]) + len - 1) / len;
+    return n;
+  };
+  const long long budget = std::max(1LL, warps / n_kv);
+  int lo = kMinUnitPages, hi = kMinUnitPages;
+  for (const Ranges& r : seen)
+    for (int i = 0; i < r.n; ++i) hi = std::max(hi, pages_of(r.k0[i], r.k1[i]));
+  if (count(hi) > budget) lo = hi = std::min(hi, kMaxUnitPages);
+  while (lo < hi) {  // the shortest length that fits the budget
+    const int mid = (lo + hi) / 2;
+    if (count(mid) <= budget) hi = mid;
+    else lo = mid + 1;
+  }
+  if (ubeg) ubeg->assign(1, 0);
+  for (size_t b = 0; b < seen.size(); ++b) {
+    for (int i = 0; i < seen[b].n; ++i) {
+      const int k0 = seen[b].k0[i], k1 = seen[b].k1[i], p0 = k0 / kPageSize;
+      const long long np = pages_of(k0, k1), nu = (np + lo - 1) / lo;
+      for (long long u = 0; u < nu; ++u) {
+        const int a = std::max(k0, (p0 + (int)(np * u / nu)) * kPageSize);
+        const int e = (int)std::min<long long>(k1, (p0 + np * (u + 1) / nu) * kPageSize);
+        units->insert(units->end(), {item_ids[b], a, e - a});
+      }
+    }
+    if (ubeg) ubeg->push_back((int)(units->size() / 3));
+  }
+}
+
 // (sequence, page) pairs of the pages some row of the chunk sees.
 void list_pages(int s, int c0, int n, int window, int sinks, std::vector<int>* out) {
   const Ranges r = seen_ranges(c0, n, window, sinks);
@@ -169,8 +211,13 @@ int AttendPlan::make(const swiftkv_model* m, const int32_t* cu, const int32_t* c
     return b.window > 0 ? std::min((long long)p, (long long)b.window + b.sinks + tile_rows) : (long long)p;
   };
   std::stable_sort(tiles.begin(), tiles.end(), [&](int x, int y) { return keys_of(x) > keys_of(y); });
-  std::vector<int> units, ubeg;
-  if (!rows.empty()) split_plan_host_window(pos.data(), (int)pos.size(), b.window, b.sinks, &units, &ubeg);
+  std::vector<int> units, ubeg, items(rows.size());
+  std::vector<Ranges> seen(rows.size());
+  for (size_t i = 0; i < rows.size(); ++i) {
+    items[i] = (int)i;
+    seen[i] = seen_ranges(pos[i], 1, b.window, b.sinks);
+  }
+  if (!rows.empty()) cut_units(items, seen, c.n_kv, (long long)m->num_sms * kSplitWarps, &units, &ubeg);
   num_tiles = (int)tiles.size();
   num_rows = (int)rows.size();
   num_units = (int)units.size() / 3;
@@ -280,7 +327,8 @@ int WeightsPlan::make(const swiftkv_model* m, const int32_t* cu, const int32_t* 
   RET(check_batch(m, cu, ctx, P, kv, window, sinks, &b));
   const auto& c = m->cfg;
   const int G = c.n_q / c.n_kv;
-  std::vector<int> cuv(cu, cu + P + 1), ctxv(P, 0), units, tiles, exp_items;
+  std::vector<int> cuv(cu, cu + P + 1), ctxv(P, 0), ids, units, tiles, exp_items;
+  std::vector<Ranges> seen;
   std::vector<std::pair<long long, std::pair<int, int>>> heavy;  // (rows that see the tile, (sequence, tile))
   for (int i = 0; i < P; ++i) {
     const int n = cu[i + 1] - cu[i], c0 = ctx ? ctx[i] : 0;
@@ -288,13 +336,9 @@ int WeightsPlan::make(const swiftkv_model* m, const int32_t* cu, const int32_t* 
     const Ranges r = seen_ranges(c0, n, b.window, b.sinks);
     if (n * (long long)G <= kWeightCols) {
       max_cols = std::max(max_cols, n * G);
-      for (int k = 0; k < r.n; ++k) {
-        const int split = split_keys_for(r.k1[k] - r.k0[k]);
-        for (int k0 = r.k0[k]; k0 < r.k1[k];) {
-          const int k1 = std::min(r.k1[k], (k0 / split + 1) * split);
-          units.insert(units.end(), {i, k0, k1 - k0});
-          k0 = k1;
-        }
+      if (r.n > 0) {
+        ids.push_back(i);
+        seen.push_back(r);
       }
       continue;
     }
@@ -310,6 +354,7 @@ int WeightsPlan::make(const swiftkv_model* m, const int32_t* cu, const int32_t* 
       }
     if (b.fp8) list_pages(i, c0, n, b.window, b.sinks, &exp_items);
   }
+  if (!ids.empty()) cut_units(ids, seen, c.n_kv, (long long)m->num_sms * kWeightWarps, &units, nullptr);
   std::stable_sort(heavy.begin(), heavy.end(), [](const auto& x, const auto& y) { return x.first > y.first; });
   for (const auto& h : heavy) {
     tiles.push_back(h.second.first);
@@ -470,7 +515,7 @@ int swiftkv_evict(swiftkv_model* m, int cache, const swiftkv_kv_pages* kv, float
   if (!scores || !seq_lens || !kept) return fail(SWIFTKV_EINVAL, "null scores / seq_lens / kept");
   const int first = cache < 0 ? 0 : cache, C = cache < 0 ? m->C : 1;
   for (int c = first; c < first + C; ++c)
-    if (!scores[c] || (reinterpret_cast<uintptr_t>(scores[c]) & 3))
+    if (!scores[c] || (reinterpret_cast<uintptr_t>(scores[c]) & 15))
       return fail(SWIFTKV_EINVAL, "null or misaligned score pool for cache %d", c);
   if (keep < 1 || sinks < 0 || recent < 0 || (long long)sinks + recent > keep)
     return fail(SWIFTKV_EINVAL, "need keep >= 1, sinks >= 0, recent >= 0 and sinks + recent <= keep");

@@ -95,6 +95,7 @@ struct WeightsArgs {
 // Chunks of few rows (rows x group <= kWeightCols): units [3 * num_units] = (sequence, first key,
 // keys), one warp per unit and KV head at a time. FP8 cache: codes and scales of K.
 constexpr int kWeightCols = 32;
+constexpr int kWeightWarps = 12;  // warps per SM that walk units
 cudaError_t launch_weights_rows(const WeightsArgs& a, const bf16* k, const uint8_t* k8, const float* k_scale, int d_head,
                                 int max_cols, const int* units, int num_units, int num_sms, cudaStream_t s);
 // Longer chunks on tcgen05: tiles [2 * num_tiles] = (sequence, 128-key tile), heaviest first. FP8:
