@@ -30,43 +30,37 @@ namespace skv {
 
 namespace {
 
-constexpr int SW = kSplitWarps;  // warps per CTA (one CTA per SM; 3 ring slots of 10 KB each fit 7)
+constexpr int SW = 7;        // warps per CTA (one CTA per SM; 3 ring slots of 10 KB each fit 7)
 constexpr int SSTAGES = 3;   // ring slots per warp
 constexpr int SMAXG = 8;     // query heads per KV head (rows 0..7 of the mma A operand)
 
-// EXT reads Q from global memory when a unit begins and gives the room to another ring slot: with
-// long units a warp waits for Q once, and more pages in flight are worth more.
-template <int D, bool EXT = false>
+template <int D>
 struct Sp {
   static constexpr int PAGE = kPageSize * D;      // elements of one (page, head) K or V block
-  static constexpr int SLOTS = EXT ? 4 : SSTAGES;
-  static constexpr int STAGE = 2 * PAGE + (EXT ? 0 : SMAXG * D);  // K, V, and the unit's Q when the page is its first
-  static constexpr int SMEM = SW * SLOTS * STAGE * 2;
+  static constexpr int STAGE = 2 * PAGE + SMAXG * D;  // K, V, and the unit's Q when the page is its first
+  static constexpr int SMEM = SW * SSTAGES * STAGE * 2;
 };
 
-// EXT (AttnExt): units list visible keys only and may start inside a page, qpos is indexed by item,
-// rows of a page outside the unit are staged as zeros, and the row's log-sum-exp is written.
-template <int D, bool EXT>
+template <int D>
 __global__ void __launch_bounds__(SW * 32, 1) attn_split_kernel(
     const bf16* __restrict__ q, int ldq, const bf16* __restrict__ kpool, const bf16* __restrict__ vpool,
     const int* __restrict__ bt, int max_pages, int num_pages, const int* __restrict__ qpos,
     const int* __restrict__ rows, const int* __restrict__ seqs, const int* __restrict__ units, int num_units,
-    const int* __restrict__ ubeg, int n_q, int n_kv, bf16* __restrict__ out, int ldo, float* __restrict__ part,
-    float scale_log2, const AttnExt ext) {
-  using S = Sp<D, EXT>;
+    int n_q, int n_kv, bf16* __restrict__ out, int ldo, float* __restrict__ part, float scale_log2) {
+  using S = Sp<D>;
   constexpr int CH = D / 8;  // 16-byte chunks per row
   extern __shared__ __align__(128) unsigned char smem[];
   griddep_launch_dependents();  // a programmatic dependent may start as these blocks leave
   griddep_wait();               // itself launched as one: q and the cache rows are fresh
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  bf16* ring = reinterpret_cast<bf16*>(smem) + (size_t)warp * S::SLOTS * S::STAGE;
+  bf16* ring = reinterpret_cast<bf16*>(smem) + (size_t)warp * SSTAGES * S::STAGE;
   const int G = n_q / n_kv;
   const int total = num_units * n_kv;              // work items v = unit * n_kv + head
-  const int gw = EXT ? warp * gridDim.x + blockIdx.x : blockIdx.x * SW + warp, nw = gridDim.x * SW;
+  const int gw = blockIdx.x * SW + warp, nw = gridDim.x * SW;
 
   auto swz = [](int row, int ch) { return row * D + ((ch ^ (row & 7)) * 8); };
   struct Geo {
-    int b, r, kvh, k_begin, k_end, p_begin, npages, nkeys;
+    int r, kvh, k_begin, k_end, p_begin, npages, nkeys;
     const int* btrow;
   };
   auto geo = [&](int v) {
@@ -74,10 +68,9 @@ __global__ void __launch_bounds__(SW * 32, 1) attn_split_kernel(
     const int u = v / n_kv;
     g.kvh = v - u * n_kv;
     const int b = units[3 * u];
-    g.b = b;
     g.r = rows ? rows[b] : b;
     const int sq = seqs ? seqs[b] : b;
-    g.nkeys = qpos[EXT ? b : g.r] + 1;
+    g.nkeys = qpos[g.r] + 1;
     g.k_begin = units[3 * u + 1];
     g.k_end = min(g.nkeys, g.k_begin + units[3 * u + 2]);
     g.p_begin = g.k_begin / kPageSize;
@@ -86,7 +79,7 @@ __global__ void __launch_bounds__(SW * 32, 1) attn_split_kernel(
     return g;
   };
 
-  // loader: walks this warp's (work item, page) sequence S::SLOTS - 1 pages ahead of the compute
+  // loader: walks this warp's (work item, page) sequence SSTAGES - 1 pages ahead of the compute
   int lv = gw, lp = 0, lslot = 0;
   Geo lg;
   if (lv < total) lg = geo(lv);
@@ -95,24 +88,21 @@ __global__ void __launch_bounds__(SW * 32, 1) attn_split_kernel(
       bf16* st = ring + lslot * S::STAGE;
       const int page = lg.btrow[lg.p_begin + lp];
       const bool ok = page >= 0 && page < num_pages;
-      if (EXT && !ok && lane == 0) atomicOr(ext.status, kStatusBadPage);
       const size_t base = ok ? ((size_t)page * n_kv + lg.kvh) * S::PAGE : 0;
 #pragma unroll
       for (int c = lane; c < kPageSize * CH; c += 32) {
         const int row = c / CH, ch = c % CH;
-        const int key = (lg.p_begin + lp) * kPageSize + row;
-        const int bytes = ok && (!EXT || (key >= lg.k_begin && key < lg.k_end)) ? 16 : 0;
-        cp_async16(smem_u32(st + swz(row, ch)), kpool + base + row * D + ch * 8, bytes);
-        cp_async16(smem_u32(st + S::PAGE + swz(row, ch)), vpool + base + row * D + ch * 8, bytes);
+        cp_async16(smem_u32(st + swz(row, ch)), kpool + base + row * D + ch * 8, ok ? 16 : 0);
+        cp_async16(smem_u32(st + S::PAGE + swz(row, ch)), vpool + base + row * D + ch * 8, ok ? 16 : 0);
       }
-      if (!EXT && lp == 0) {  // the unit's query heads ride with its first page
+      if (lp == 0) {  // the unit's query heads ride with its first page
         const bf16* qsrc = q + (size_t)lg.r * ldq + (size_t)lg.kvh * G * D;
         for (int c = lane; c < G * CH; c += 32) {
           const int row = c / CH, ch = c % CH;
           cp_async16(smem_u32(st + 2 * S::PAGE + swz(row, ch)), qsrc + row * D + ch * 8, 16);
         }
       }
-      if (++lslot == S::SLOTS) lslot = 0;
+      if (++lslot == SSTAGES) lslot = 0;
       if (++lp == lg.npages) {
         lp = 0;
         lv += nw;
@@ -129,13 +119,13 @@ __global__ void __launch_bounds__(SW * 32, 1) attn_split_kernel(
   float m0 = -FLT_MAX, l0 = 0.f;
 
 #pragma unroll
-  for (int i = 0; i < S::SLOTS - 1; ++i) issue();
+  for (int i = 0; i < SSTAGES - 1; ++i) issue();
   int cv = gw, cp = 0, cslot = 0;
   Geo cg;
   if (cv < total) cg = geo(cv);
   while (cv < total) {
     issue();
-    cp_async_wait<S::SLOTS - 1>();
+    cp_async_wait<SSTAGES - 1>();
     __syncwarp();
     bf16* st = ring + cslot * S::STAGE;
     const bf16* kb = st;
@@ -146,9 +136,7 @@ __global__ void __launch_bounds__(SW * 32, 1) attn_split_kernel(
       for (int ks = 0; ks < D / 16; ++ks) {
         const int c = ks * 16 + qc;
         auto qat = [&](int g, int col) -> uint32_t {  // g < 8
-          if (g >= G) return 0u;
-          if (EXT) return *reinterpret_cast<const uint32_t*>(q + (size_t)cg.r * ldq + (size_t)(cg.kvh * G + g) * D + col);
-          return *reinterpret_cast<const uint32_t*>(qs + swz(g, col / 8) + (col & 7));
+          return g < G ? *reinterpret_cast<const uint32_t*>(qs + swz(g, col / 8) + (col & 7)) : 0u;
         };
         qf[ks][0] = qat(g0, c);
         qf[ks][1] = 0u;
@@ -241,19 +229,17 @@ __global__ void __launch_bounds__(SW * 32, 1) attn_split_kernel(
       mma_bf16_16816(o[2 * dp + 1], pl, b1);
     }
     __syncwarp();  // the slot is refilled by a later issue()
-    if (++cslot == S::SLOTS) cslot = 0;
+    if (++cslot == SSTAGES) cslot = 0;
 
     if (++cp == cg.npages) {
       // unit done: the whole row -> output; one split of it -> (max, sum, unnormalised O)
       float s0 = l0;
 #pragma unroll
       for (int off = 1; off <= 2; off <<= 1) s0 += __shfl_xor_sync(0xffffffffu, s0, off);
-      const bool whole = EXT ? ubeg[cg.b + 1] - ubeg[cg.b] == 1 : cg.k_begin == 0 && cg.k_end == cg.nkeys;
+      const bool whole = cg.k_begin == 0 && cg.k_end == cg.nkeys;
       const int u = cv / n_kv;
       if (whole) {
         const float i0 = s0 > 0.f ? 1.f / s0 : 0.f;
-        if (EXT && ext.lse && g0 < G && (lane & 3) == 0)
-          ext.lse[(size_t)(cg.kvh * G + g0) * ext.ldl + cg.r] = (m0 + log2f(s0)) * 0.69314718055994531f;
         bf16* orow = out + (size_t)cg.r * ldo + (size_t)cg.kvh * G * D;
 #pragma unroll
         for (int n = 0; n < D / 8; ++n) {
@@ -292,32 +278,31 @@ __global__ void __launch_bounds__(SW * 32, 1) attn_split_kernel(
 // when it grows, like the softmax max), and O * S_ref is the unnormalised output.
 constexpr int SSTAGES8 = 3;
 
-template <int D, bool EXT = false>
+template <int D>
 struct Sp8 {
   static constexpr int CODES = kPageSize * D;        // bytes of one (page, head) K or V block
-  static constexpr int QB = EXT ? 0 : SMAXG * D * 2;  // bytes of the unit's query rows (bf16)
-  static constexpr int SLOTS = EXT ? 7 : SSTAGES8;
+  static constexpr int QB = SMAXG * D * 2;            // bytes of the unit's query rows (bf16)
   static constexpr int STAGE = 2 * CODES + 2 * kPageSize * 4 + QB;
-  static constexpr int SMEM = SW * SLOTS * STAGE;
+  static constexpr int SMEM = SW * SSTAGES8 * STAGE;
   static constexpr int CHB = D / 16;                  // 16-byte chunks per code row
 };
 
-template <int D, bool EXT>
+template <int D>
 __global__ void __launch_bounds__(SW * 32, 1) attn_split_fp8_kernel(
     const bf16* __restrict__ q, int ldq, const uint8_t* __restrict__ kpool, const uint8_t* __restrict__ vpool,
     const float* __restrict__ kscale, const float* __restrict__ vscale, const int* __restrict__ bt, int max_pages,
     int num_pages, const int* __restrict__ qpos, const int* __restrict__ rows, const int* __restrict__ seqs,
-    const int* __restrict__ units, int num_units, const int* __restrict__ ubeg, int n_q, int n_kv,
-    bf16* __restrict__ out, int ldo, float* __restrict__ part, float scale_log2, const AttnExt ext) {
-  using S = Sp8<D, EXT>;
+    const int* __restrict__ units, int num_units, int n_q, int n_kv, bf16* __restrict__ out, int ldo,
+    float* __restrict__ part, float scale_log2) {
+  using S = Sp8<D>;
   extern __shared__ __align__(128) unsigned char smem[];
   griddep_launch_dependents();
   griddep_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  unsigned char* ring = smem + (size_t)warp * S::SLOTS * S::STAGE;
+  unsigned char* ring = smem + (size_t)warp * SSTAGES8 * S::STAGE;
   const int G = n_q / n_kv;
   const int total = num_units * n_kv;
-  const int gw = EXT ? warp * gridDim.x + blockIdx.x : blockIdx.x * SW + warp, nw = gridDim.x * SW;
+  const int gw = blockIdx.x * SW + warp, nw = gridDim.x * SW;
 
   // code rows of D bytes, 16-byte chunks XOR-swizzled so 8 rows of one chunk hit 8 bank groups
   auto swzb = [](int row, int ch) {
@@ -326,7 +311,7 @@ __global__ void __launch_bounds__(SW * 32, 1) attn_split_fp8_kernel(
   };
   auto swzq = [](int row, int ch) { return row * D + ((ch ^ (row & 7)) * 8); };  // bf16 elements
   struct Geo {
-    int b, r, kvh, k_begin, k_end, p_begin, npages, nkeys;
+    int r, kvh, k_begin, k_end, p_begin, npages, nkeys;
     const int* btrow;
   };
   auto geo = [&](int v) {
@@ -334,10 +319,9 @@ __global__ void __launch_bounds__(SW * 32, 1) attn_split_fp8_kernel(
     const int u = v / n_kv;
     g.kvh = v - u * n_kv;
     const int b = units[3 * u];
-    g.b = b;
     g.r = rows ? rows[b] : b;
     const int sq = seqs ? seqs[b] : b;
-    g.nkeys = qpos[EXT ? b : g.r] + 1;
+    g.nkeys = qpos[g.r] + 1;
     g.k_begin = units[3 * u + 1];
     g.k_end = min(g.nkeys, g.k_begin + units[3 * u + 2]);
     g.p_begin = g.k_begin / kPageSize;
@@ -354,21 +338,18 @@ __global__ void __launch_bounds__(SW * 32, 1) attn_split_fp8_kernel(
       unsigned char* st = ring + lslot * S::STAGE;
       const int page = lg.btrow[lg.p_begin + lp];
       const bool ok = page >= 0 && page < num_pages;
-      if (EXT && !ok && lane == 0) atomicOr(ext.status, kStatusBadPage);
       const size_t blk = ok ? (size_t)page * n_kv + lg.kvh : 0;
 #pragma unroll
       for (int c = lane; c < kPageSize * S::CHB; c += 32) {
         const int row = c / S::CHB, ch = c % S::CHB;
-        const int key = (lg.p_begin + lp) * kPageSize + row;
-        const int bytes = ok && (!EXT || (key >= lg.k_begin && key < lg.k_end)) ? 16 : 0;
-        cp_async16(smem_u32(st + swzb(row, ch)), kpool + blk * S::CODES + row * D + ch * 16, bytes);
-        cp_async16(smem_u32(st + S::CODES + swzb(row, ch)), vpool + blk * S::CODES + row * D + ch * 16, bytes);
+        cp_async16(smem_u32(st + swzb(row, ch)), kpool + blk * S::CODES + row * D + ch * 16, ok ? 16 : 0);
+        cp_async16(smem_u32(st + S::CODES + swzb(row, ch)), vpool + blk * S::CODES + row * D + ch * 16, ok ? 16 : 0);
       }
       if (lane < 8) {  // 16 K scales, then 16 V scales
         const float* sp = (lane < 4 ? kscale : vscale) + blk * kPageSize + (lane & 3) * 4;
         cp_async16(smem_u32(st + 2 * S::CODES + lane * 16), sp, ok ? 16 : 0);
       }
-      if (!EXT && lp == 0) {
+      if (lp == 0) {
         const bf16* qsrc = q + (size_t)lg.r * ldq + (size_t)lg.kvh * G * D;
         bf16* qs = reinterpret_cast<bf16*>(st + 2 * S::CODES + 2 * kPageSize * 4);
         for (int c = lane; c < G * (D / 8); c += 32) {
@@ -376,7 +357,7 @@ __global__ void __launch_bounds__(SW * 32, 1) attn_split_fp8_kernel(
           cp_async16(smem_u32(qs + swzq(row, ch)), qsrc + row * D + ch * 8, 16);
         }
       }
-      if (++lslot == S::SLOTS) lslot = 0;
+      if (++lslot == SSTAGES8) lslot = 0;
       if (++lp == lg.npages) {
         lp = 0;
         lv += nw;
@@ -392,13 +373,13 @@ __global__ void __launch_bounds__(SW * 32, 1) attn_split_fp8_kernel(
   float m0 = -FLT_MAX, l0 = 0.f, sref = 0.f;
 
 #pragma unroll
-  for (int i = 0; i < S::SLOTS - 1; ++i) issue();
+  for (int i = 0; i < SSTAGES8 - 1; ++i) issue();
   int cv = gw, cp = 0, cslot = 0;
   Geo cg;
   if (cv < total) cg = geo(cv);
   while (cv < total) {
     issue();
-    cp_async_wait<S::SLOTS - 1>();
+    cp_async_wait<SSTAGES8 - 1>();
     __syncwarp();
     const unsigned char* st = ring + cslot * S::STAGE;
     const float* sk = reinterpret_cast<const float*>(st + 2 * S::CODES);
@@ -409,9 +390,7 @@ __global__ void __launch_bounds__(SW * 32, 1) attn_split_fp8_kernel(
       for (int ks = 0; ks < D / 16; ++ks) {
         uint32_t lo = 0u, hi = 0u;
         if (g0 < G) {
-          const uint2 w = *reinterpret_cast<const uint2*>(
-              EXT ? q + (size_t)cg.r * ldq + (size_t)(cg.kvh * G + g0) * D + ks * 16 + 4 * qd
-                  : qs + swzq(g0, 2 * ks + (qd >> 1)) + 4 * (qd & 1));
+          const uint2 w = *reinterpret_cast<const uint2*>(qs + swzq(g0, 2 * ks + (qd >> 1)) + 4 * (qd & 1));
           const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w.x));
           const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w.y));
           lo = pack_f16(a.x, a.y);
@@ -496,7 +475,7 @@ __global__ void __launch_bounds__(SW * 32, 1) attn_split_fp8_kernel(
       for (int e = 0; e < 2; ++e) {
         const float p = exp2f(sc[t][e] - m0);
         ps0 += p;
-        pv[t][e] = EXT && p == 0.f ? 0.f : p * (sv[8 * t + 2 * qd + e] * isref);  // a masked key's scale may be NaN
+        pv[t][e] = p * (sv[8 * t + 2 * qd + e] * isref);
       }
     l0 += ps0;
     uint32_t pa[4];
@@ -522,19 +501,17 @@ __global__ void __launch_bounds__(SW * 32, 1) attn_split_fp8_kernel(
       }
     }
     __syncwarp();
-    if (++cslot == S::SLOTS) cslot = 0;
+    if (++cslot == SSTAGES8) cslot = 0;
 
     if (++cp == cg.npages) {
       float s0 = l0;
 #pragma unroll
       for (int off = 1; off <= 2; off <<= 1) s0 += __shfl_xor_sync(0xffffffffu, s0, off);
-      const bool whole = EXT ? ubeg[cg.b + 1] - ubeg[cg.b] == 1 : cg.k_begin == 0 && cg.k_end == cg.nkeys;
+      const bool whole = cg.k_begin == 0 && cg.k_end == cg.nkeys;
       const int u = cv / n_kv;
       if (g0 < G) {
         if (whole) {
           const float f = s0 > 0.f ? sref / s0 : 0.f;
-          if (EXT && ext.lse && qd == 0)
-            ext.lse[(size_t)(cg.kvh * G + g0) * ext.ldl + cg.r] = (m0 + log2f(s0)) * 0.69314718055994531f;
           bf16* orow = out + (size_t)cg.r * ldo + (size_t)(cg.kvh * G + g0) * D;
 #pragma unroll
           for (int c = 0; c < D / 16; ++c) {
@@ -630,129 +607,48 @@ __global__ void __launch_bounds__(CMB_THREADS) attn_split_combine(const int* __r
   }
 }
 
-// The same for EXT, one warp per (item, query head): a lane owns D / 32 neighbouring dimensions,
-// lanes share out the splits' maxima and sums, and a batch of partial rows is in flight before the
-// first is used, so a merge of a few splits takes one trip to memory (the CTA-wide one takes three:
-// 6 against 3 us for 24 rows of 40 heads).
-constexpr int CMB_WARPS = 4;
-
 template <int D>
-__global__ void __launch_bounds__(CMB_WARPS * 32) attn_split_merge(const int* __restrict__ rows,
-                                                                   const int* __restrict__ ubeg, int items, int n_q,
-                                                                   int n_kv, const float* __restrict__ part,
-                                                                   bf16* __restrict__ out, int ldo,
-                                                                   float* __restrict__ lse, int ldl) {
-  griddep_launch_dependents();
-  griddep_wait();
-  const long long w = (long long)blockIdx.x * CMB_WARPS + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  if (w >= (long long)items * n_q) return;
-  const int b = (int)(w / n_q), h = (int)(w - (long long)b * n_q);
-  const int G = n_q / n_kv, kvh = h / G, g = h - kvh * G;
-  const int u0 = ubeg[b], ns = ubeg[b + 1] - u0;
-  if (ns <= 1) return;  // written by its only unit
-  const size_t step = (size_t)n_q * (D + 2);
-  const float* p = part + ((size_t)u0 * n_kv + kvh) * G * (D + 2) + (size_t)g * (D + 2);
-  constexpr int E = D / 32, B = 8;
-  float o[E], m = -INFINITY, den = 0.f;
-#pragma unroll
-  for (int e = 0; e < E; ++e) o[e] = 0.f;
-  for (int i0 = 0; i0 < ns; i0 += B) {
-    float v[B][E], pm = -INFINITY, pl = 0.f;
-    if (lane < B && i0 + lane < ns) {
-      const float2 ml = *reinterpret_cast<const float2*>(p + (i0 + lane) * step);
-      pm = ml.x;
-      pl = ml.y;
-    }
-#pragma unroll
-    for (int i = 0; i < B; ++i)
-#pragma unroll
-      for (int e = 0; e < E; e += 2) {
-        float2 x = make_float2(0.f, 0.f);
-        if (i0 + i < ns) x = *reinterpret_cast<const float2*>(p + (i0 + i) * step + 2 + lane * E + e);
-        v[i][e] = x.x;
-        v[i][e + 1] = x.y;
-      }
-    float mx = pm;
-#pragma unroll
-    for (int off = 4; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-    mx = fmaxf(m, __shfl_sync(0xffffffffu, mx, 0));
-    const float keep = exp2f(m - mx), wt = exp2f(pm - mx);
-    m = mx;
-    float l = pl * wt;
-#pragma unroll
-    for (int off = 4; off > 0; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
-    den = den * keep + __shfl_sync(0xffffffffu, l, 0);
-#pragma unroll
-    for (int e = 0; e < E; ++e) o[e] *= keep;
-#pragma unroll
-    for (int i = 0; i < B; ++i) {
-      const float wi = __shfl_sync(0xffffffffu, wt, i);
-#pragma unroll
-      for (int e = 0; e < E; ++e) o[e] = fmaf(v[i][e], wi, o[e]);
-    }
-  }
-  const int r = rows[b];
-  const float inv = 1.f / den;
-  bf16* dst = out + (size_t)r * ldo + (size_t)h * D + lane * E;
-#pragma unroll
-  for (int e = 0; e < E; e += 2) *reinterpret_cast<uint32_t*>(dst + e) = pack_bf16(o[e] * inv, o[e + 1] * inv);
-  if (lse && lane == 0) lse[(size_t)h * ldl + r] = (m + log2f(den)) * 0.69314718055994531f;
-}
-
-template <int D>
-cudaError_t launch_merge(const SplitPlan& plan, const int* rows, int n_q, int n_kv, bf16* out, int ldo,
-                         const AttnExt& ext, cudaStream_t stream) {
-  const long long warps = (long long)plan.num_items * n_q;
-  return launch_pdl(attn_split_merge<D>, dim3((unsigned)((warps + CMB_WARPS - 1) / CMB_WARPS)), dim3(CMB_WARPS * 32), 0,
-                    stream, rows, (const int*)plan.ubeg, plan.num_items, n_q, n_kv, (const float*)plan.part, out, ldo,
-                    ext.lse, ext.ldl);
-}
-
-template <int D, bool EXT>
 cudaError_t split_d(const bf16* q, int ldq, const bf16* k_pool, const bf16* v_pool, const int* bt, int max_pages,
                     int num_pages, const int* qpos, const int* rows, const int* seqs, const SplitPlan& plan,
-                    int n_q, int n_kv, bf16* out, int ldo, int num_sms, cudaStream_t stream, const AttnExt& ext) {
-  constexpr int smem = Sp<D, EXT>::SMEM;
+                    int n_q, int n_kv, bf16* out, int ldo, int num_sms, cudaStream_t stream) {
+  constexpr int smem = Sp<D>::SMEM;
   static_assert(smem <= 227 * 1024, "rings must fit in shared memory");
   static PerDeviceOnce smem_attr;
   {
-    cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void*>(attn_split_kernel<D, EXT>), smem, smem_attr);
+    cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void*>(attn_split_kernel<D>), smem, smem_attr);
     if (e != cudaSuccess) return e;
   }
   const float scale_log2 = 1.4426950408889634f / sqrtf((float)D);
   const int total = plan.num_units * n_kv;
-  const int ctas = EXT ? std::min(total, num_sms) : std::min((total + SW - 1) / SW, num_sms);
-  cudaError_t e = launch_pdl(attn_split_kernel<D, EXT>, dim3(ctas), dim3(SW * 32), smem, stream, q, ldq, k_pool, v_pool,
-                             bt, max_pages, num_pages, qpos, rows, seqs, (const int*)plan.units, plan.num_units,
-                             (const int*)plan.ubeg, n_q, n_kv, out, ldo, plan.part, scale_log2, ext);
+  const int ctas = std::min((total + SW - 1) / SW, num_sms);
+  cudaError_t e = launch_pdl(attn_split_kernel<D>, dim3(ctas), dim3(SW * 32), smem, stream, q, ldq, k_pool, v_pool,
+                             bt, max_pages, num_pages, qpos, rows, seqs, (const int*)plan.units, plan.num_units, n_q,
+                             n_kv, out, ldo, plan.part, scale_log2);
   if (e != cudaSuccess || !plan.any_split) return e;
-  if (EXT) return launch_merge<D>(plan, rows, n_q, n_kv, out, ldo, ext, stream);
   return launch_pdl(attn_split_combine<D>, dim3(plan.num_items, n_kv), dim3(CMB_THREADS), 0, stream, rows,
                     (const int*)plan.ubeg, n_q, n_kv, (const float*)plan.part, out, ldo);
 }
 
-template <int D, bool EXT>
+template <int D>
 cudaError_t split_fp8_d(const bf16* q, int ldq, const uint8_t* k8, const uint8_t* v8, const float* ks,
                         const float* vs, const int* bt, int max_pages, int num_pages, const int* qpos,
                         const int* rows, const int* seqs, const SplitPlan& plan, int n_q, int n_kv, bf16* out,
-                        int ldo, int num_sms, cudaStream_t stream, const AttnExt& ext) {
-  constexpr int smem = Sp8<D, EXT>::SMEM;
+                        int ldo, int num_sms, cudaStream_t stream) {
+  constexpr int smem = Sp8<D>::SMEM;
   static_assert(smem <= 227 * 1024, "rings must fit in shared memory");
-  static_assert(Sp8<D, EXT>::STAGE % 16 == 0, "ring slots must keep 16-byte alignment");
+  static_assert(Sp8<D>::STAGE % 16 == 0, "ring slots must keep 16-byte alignment");
   static PerDeviceOnce smem_attr;
   {
-    cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void*>(attn_split_fp8_kernel<D, EXT>), smem, smem_attr);
+    cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void*>(attn_split_fp8_kernel<D>), smem, smem_attr);
     if (e != cudaSuccess) return e;
   }
   const float scale_log2 = 1.4426950408889634f / sqrtf((float)D);
   const int total = plan.num_units * n_kv;
-  const int ctas = EXT ? std::min(total, num_sms) : std::min((total + SW - 1) / SW, num_sms);
-  cudaError_t e = launch_pdl(attn_split_fp8_kernel<D, EXT>, dim3(ctas), dim3(SW * 32), smem, stream, q, ldq, k8, v8, ks,
+  const int ctas = std::min((total + SW - 1) / SW, num_sms);
+  cudaError_t e = launch_pdl(attn_split_fp8_kernel<D>, dim3(ctas), dim3(SW * 32), smem, stream, q, ldq, k8, v8, ks,
                              vs, bt, max_pages, num_pages, qpos, rows, seqs, (const int*)plan.units, plan.num_units,
-                             (const int*)plan.ubeg, n_q, n_kv, out, ldo, plan.part, scale_log2, ext);
+                             n_q, n_kv, out, ldo, plan.part, scale_log2);
   if (e != cudaSuccess || !plan.any_split) return e;
-  if (EXT) return launch_merge<D>(plan, rows, n_q, n_kv, out, ldo, ext, stream);
   return launch_pdl(attn_split_combine<D>, dim3(plan.num_items, n_kv), dim3(CMB_THREADS), 0, stream, rows,
                     (const int*)plan.ubeg, n_q, n_kv, (const float*)plan.part, out, ldo);
 }
@@ -763,16 +659,15 @@ cudaError_t launch_attention_decode_split_fp8(const bf16* q, int ldq, const uint
                                               const float* k_scale, const float* v_scale, const int* block_table,
                                               int max_pages, int num_pages, const int* qpos, const int* rows,
                                               const int* seqs, const SplitPlan& plan, int n_q, int n_kv, int d_head,
-                                              bf16* out, int ldo, int num_sms, cudaStream_t stream,
-                                              const AttnExt* ext) {
+                                              bf16* out, int ldo, int num_sms, cudaStream_t stream) {
   if (plan.num_units <= 0) return cudaSuccess;
   if (n_q % n_kv || n_q / n_kv > SMAXG) return cudaErrorNotSupported;
-  auto run = [&](auto kernel) {
-    return kernel(q, ldq, k8, v8, k_scale, v_scale, block_table, max_pages, num_pages, qpos, rows, seqs, plan, n_q,
-                  n_kv, out, ldo, num_sms, stream, ext ? *ext : AttnExt());
-  };
-  if (d_head == 128) return ext ? run(split_fp8_d<128, true>) : run(split_fp8_d<128, false>);
-  if (d_head == 64) return ext ? run(split_fp8_d<64, true>) : run(split_fp8_d<64, false>);
+  if (d_head == 128)
+    return split_fp8_d<128>(q, ldq, k8, v8, k_scale, v_scale, block_table, max_pages, num_pages, qpos, rows, seqs,
+                            plan, n_q, n_kv, out, ldo, num_sms, stream);
+  if (d_head == 64)
+    return split_fp8_d<64>(q, ldq, k8, v8, k_scale, v_scale, block_table, max_pages, num_pages, qpos, rows, seqs,
+                           plan, n_q, n_kv, out, ldo, num_sms, stream);
   return cudaErrorNotSupported;
 }
 
@@ -797,17 +692,16 @@ size_t split_part_floats(int num_units, int n_q, int d_head) { return (size_t)nu
 cudaError_t launch_attention_decode_split(const bf16* q, int ldq, const bf16* k_pool, const bf16* v_pool,
                                           const int* block_table, int max_pages, int num_pages, const int* qpos,
                                           const int* rows, const int* seqs, const SplitPlan& plan, int n_q,
-                                          int n_kv, int d_head, bf16* out, int ldo, int num_sms, cudaStream_t stream,
-                                          const AttnExt* ext) {
+                                          int n_kv, int d_head, bf16* out, int ldo, int num_sms, cudaStream_t stream) {
   if (plan.num_units <= 0) return cudaSuccess;
   // a group of more than 8 query heads takes the one-CTA-per-row kernel
   if (n_q % n_kv || n_q / n_kv > SMAXG) return cudaErrorNotSupported;
-  auto run = [&](auto kernel) {
-    return kernel(q, ldq, k_pool, v_pool, block_table, max_pages, num_pages, qpos, rows, seqs, plan, n_q, n_kv, out,
-                  ldo, num_sms, stream, ext ? *ext : AttnExt());
-  };
-  if (d_head == 128) return ext ? run(split_d<128, true>) : run(split_d<128, false>);
-  if (d_head == 64) return ext ? run(split_d<64, true>) : run(split_d<64, false>);
+  if (d_head == 128)
+    return split_d<128>(q, ldq, k_pool, v_pool, block_table, max_pages, num_pages, qpos, rows, seqs, plan, n_q,
+                        n_kv, out, ldo, num_sms, stream);
+  if (d_head == 64)
+    return split_d<64>(q, ldq, k_pool, v_pool, block_table, max_pages, num_pages, qpos, rows, seqs, plan, n_q,
+                       n_kv, out, ldo, num_sms, stream);
   return cudaErrorNotSupported;
 }
 

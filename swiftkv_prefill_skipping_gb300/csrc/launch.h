@@ -261,14 +261,11 @@ cudaError_t launch_attention_decode_split_fp8(const bf16* q, int ldq, const uint
                                               const float* k_scale, const float* v_scale, const int* block_table,
                                               int max_pages, int num_pages, const int* qpos, const int* rows,
                                               const int* seqs, const SplitPlan& plan, int n_q, int n_kv, int d_head,
-                                              bf16* out, int ldo, int num_sms, cudaStream_t stream,
-                                              const AttnExt* ext = nullptr);
+                                              bf16* out, int ldo, int num_sms, cudaStream_t stream);
 cudaError_t launch_attention_decode_split(const bf16* q, int ldq, const bf16* k_pool, const bf16* v_pool,
                                           const int* block_table, int max_pages, int num_pages, const int* qpos,
                                           const int* rows, const int* seqs, const SplitPlan& plan, int n_q,
                                           int n_kv, int d_head, bf16* out, int ldo, int num_sms,
-                                          cudaStream_t stream, const AttnExt* ext = nullptr);
-// With ext, units hold visible keys only, may start inside a page, and qpos is indexed by item.
-constexpr int kSplitWarps = 7;  // warps per SM that walk units
+                                          cudaStream_t stream);
 
 }  // namespace skv

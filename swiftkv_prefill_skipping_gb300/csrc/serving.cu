@@ -11,8 +11,8 @@ namespace skv {
 
 namespace {
 
-// Chunks of at most this many rows are attended one row at a time by the key-split kernel; a
-// 128-row query tile would be nearly empty (the serving forward's rule).
+// Chunks of at most this many rows go to the row kernel, split along their keys; a 128-row query
+// tile would be nearly empty (the serving forward's rule).
 constexpr int kRowChunk = 4;
 
 int check_batch(const swiftkv_model* m, const int32_t* cu, const int32_t* ctx, int P, const swiftkv_kv_pages* kv,
@@ -190,15 +190,19 @@ int AttendPlan::make(const swiftkv_model* m, const int32_t* cu, const int32_t* c
   tc = m->attn_impl != 1 && c.d_head == 128;
   head_pairs = tc && (c.n_q / c.n_kv) % 2 == 0;
   const int tile_rows = tc ? (head_pairs ? 128 : 256) : 64;
-  std::vector<int> cuv(cu, cu + P + 1), ctxv(P, 0), tiles, rows, seqs, pos, exp_items;
+  std::vector<int> cuv(cu, cu + P + 1), ctxv(P, 0), tiles, items, ids, exp_items;
+  std::vector<Ranges> seen;
+  const int G = c.n_q / c.n_kv, group = kRowsCols / G;  // rows of an item of the row kernel
   for (int i = 0; i < P; ++i) {
     const int n = cu[i + 1] - cu[i], c0 = ctx ? ctx[i] : 0;
     ctxv[i] = c0;
     if (n <= kRowChunk) {
-      for (int r = 0; r < n; ++r) {
-        rows.push_back(cu[i] + r);
-        seqs.push_back(i);
-        pos.push_back(c0 + r);
+      for (int r = 0; r < n; r += group) {
+        const int rows = std::min(group, n - r);
+        ids.push_back((int)ids.size());
+        items.insert(items.end(), {cu[i] + r, rows, i, c0 + r});
+        seen.push_back(seen_ranges(c0 + r, rows, b.window, b.sinks));
+        max_cols = std::max(max_cols, rows * G);
       }
       continue;
     }
@@ -211,15 +215,11 @@ int AttendPlan::make(const swiftkv_model* m, const int32_t* cu, const int32_t* c
     return b.window > 0 ? std::min((long long)p, (long long)b.window + b.sinks + tile_rows) : (long long)p;
   };
   std::stable_sort(tiles.begin(), tiles.end(), [&](int x, int y) { return keys_of(x) > keys_of(y); });
-  std::vector<int> units, ubeg, items(rows.size());
-  std::vector<Ranges> seen(rows.size());
-  for (size_t i = 0; i < rows.size(); ++i) {
-    items[i] = (int)i;
-    seen[i] = seen_ranges(pos[i], 1, b.window, b.sinks);
-  }
-  if (!rows.empty()) cut_units(items, seen, c.n_kv, (long long)m->num_sms * kSplitWarps, &units, &ubeg);
+  std::vector<int> units, ubeg;
+  if (!ids.empty())
+    cut_units(ids, seen, c.n_kv, (long long)m->num_sms * (b.fp8 ? kRowsWarps8 : kRowsWarps), &units, &ubeg);
   num_tiles = (int)tiles.size();
-  num_rows = (int)rows.size();
+  num_items = (int)ids.size();
   num_units = (int)units.size() / 3;
   num_exp = (int)exp_items.size() / 2;
   if ((long long)num_units * c.n_kv >= (1LL << 31) || (long long)num_tiles * c.n_q >= (1LL << 31))
@@ -227,9 +227,7 @@ int AttendPlan::make(const swiftkv_model* m, const int32_t* cu, const int32_t* c
   o_cu = put(&ints, cuv);
   o_ctx = put(&ints, ctxv);
   o_tiles = put(&ints, tiles);
-  o_rows = put(&ints, rows);
-  o_seqs = put(&ints, seqs);
-  o_pos = put(&ints, pos);
+  o_items = put(&ints, items);
   o_units = put(&ints, units);
   o_ubeg = put(&ints, ubeg);
   o_exp = put(&ints, exp_items);
@@ -240,7 +238,7 @@ int AttendPlan::make(const swiftkv_model* m, const int32_t* cu, const int32_t* c
 void AttendPlan::place(const swiftkv_model* m, Arena* a) {
   const auto& c = m->cfg;
   dev = a->take<int>(ints.size());
-  part = a->take<float>(num_units > num_rows ? split_part_floats(num_units, c.n_q, c.d_head) : 0);
+  part = a->take<float>(num_units > num_items ? (size_t)num_units * c.n_kv * max_cols * (c.d_head + 4) : 0);
   v_tail = nullptr;
   if (tc && num_tiles > 0 && !b.fp8)
     v_tail = a->take<bf16>((size_t)b.P * kTailSlots * c.n_kv * kPageSize * c.d_head);
@@ -290,26 +288,30 @@ int AttendPlan::run(swiftkv_model* m, const swiftkv_kv_pages* kv, int c, const b
       e = launch_attention_prefill(q, ldq, k, v, ks, vs, bt, b.max_pages, pages, cu, ctx, dev + o_tiles, num_tiles,
                                    g.n_q, g.n_kv, g.d_head, out, ldo, s, &ext);
   }
-  if (e == cudaSuccess && num_rows > 0) {
-    SplitPlan sp;
-    sp.units = dev + o_units;
-    sp.ubeg = dev + o_ubeg;
-    sp.num_units = num_units;
-    sp.num_items = num_rows;
-    sp.any_split = num_units > num_rows;
-    sp.part = part;
-    if (b.fp8)
-      e = launch_attention_decode_split_fp8(q, ldq, static_cast<const uint8_t*>(kv->k_pool[c]),
-                                            static_cast<const uint8_t*>(kv->v_pool[c]),
-                                            static_cast<const float*>(kv->k_scale[c]),
-                                            static_cast<const float*>(kv->v_scale[c]), kv->block_table, b.max_pages,
-                                            kv->num_pages, dev + o_pos, dev + o_rows, dev + o_seqs, sp, g.n_q, g.n_kv,
-                                            g.d_head, out, ldo, m->num_sms, s, &ext);
-    else
-      e = launch_attention_decode_split(q, ldq, static_cast<const bf16*>(kv->k_pool[c]),
-                                        static_cast<const bf16*>(kv->v_pool[c]), kv->block_table, b.max_pages,
-                                        kv->num_pages, dev + o_pos, dev + o_rows, dev + o_seqs, sp, g.n_q, g.n_kv,
-                                        g.d_head, out, ldo, m->num_sms, s, &ext);
+  if (e == cudaSuccess && num_items > 0) {
+    RowsArgs r;
+    r.q = q;
+    r.ldq = ldq;
+    r.bt = kv->block_table;
+    r.max_pages = b.max_pages;
+    r.num_pages = kv->num_pages;
+    r.items = dev + o_items;
+    r.units = dev + o_units;
+    r.ubeg = dev + o_ubeg;
+    r.num_units = num_units;
+    r.max_cols = max_cols;
+    r.n_q = g.n_q;
+    r.n_kv = g.n_kv;
+    r.window = b.window;
+    r.sinks = b.sinks;
+    r.out = out;
+    r.ldo = ldo;
+    r.lse = lse;
+    r.ldl = ldl;
+    r.part = part;
+    r.status = m->status;
+    e = launch_attn_rows(r, kv->k_pool[c], kv->v_pool[c], b.fp8 ? static_cast<const float*>(kv->k_scale[c]) : nullptr,
+                         b.fp8 ? static_cast<const float*>(kv->v_scale[c]) : nullptr, g.d_head, num_items, m->num_sms, s);
   }
   if (e != cudaSuccess)
     return fail(e == cudaErrorNotSupported ? SWIFTKV_EUNSUPPORTED : SWIFTKV_ECUDA, "attention: %s", cudaGetErrorString(e));
@@ -317,7 +319,7 @@ int AttendPlan::run(swiftkv_model* m, const swiftkv_kv_pages* kv, int c, const b
 }
 
 int AttendPlan::kernels() const {
-  return (num_tiles > 0 ? 1 + (b.fp8 || tc) : 0) + (num_rows > 0 ? 1 + (num_units > num_rows) : 0);
+  return (num_tiles > 0 ? 1 + (b.fp8 || tc) : 0) + (num_items > 0 ? 1 + (num_units > num_items) : 0);
 }
 
 // ---------------------------------------------------------------------------- attention weights

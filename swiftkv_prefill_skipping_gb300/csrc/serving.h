@@ -38,8 +38,8 @@ struct AttendPlan {
   bool tc = false, head_pairs = false;
   // host lists, and their places in one device upload
   std::vector<int> ints;
-  int o_cu = 0, o_ctx = 0, o_tiles = 0, o_rows = 0, o_seqs = 0, o_pos = 0, o_units = 0, o_ubeg = 0, o_exp = 0;
-  int num_tiles = 0, num_rows = 0, num_units = 0, num_exp = 0;
+  int o_cu = 0, o_ctx = 0, o_tiles = 0, o_items = 0, o_units = 0, o_ubeg = 0, o_exp = 0;
+  int num_tiles = 0, num_items = 0, max_cols = 0, num_units = 0, num_exp = 0;
   // device
   int* dev = nullptr;
   float* part = nullptr;
@@ -77,7 +77,30 @@ struct WeightsPlan {
   int kernels() const;
 };
 
-// ---- kernels (attn_weights.cu, evict.cu) ---------------------------------------------------
+// ---- kernels (attn_rows.cu, attn_weights.cu, evict.cu) --------------------------------------
+// Rows of short chunks: items [4 * n] = (first row, rows, sequence, first position), rows x group <=
+// kRowsCols; units [3 * num_units] = (item, first key, keys) of keys some row sees, item-major; ubeg
+// [n + 1]; part: num_units * n_kv * max_cols records of d_head + 4 floats (several units an item).
+constexpr int kRowsCols = 16;
+constexpr int kRowsWarps = 8, kRowsWarps8 = 12;  // warps per SM that walk units: bf16, FP8
+struct RowsArgs {
+  const bf16* q;
+  int ldq;
+  const int* bt;
+  int max_pages, num_pages;
+  const int *items, *units, *ubeg;
+  int num_units, max_cols;
+  int n_q, n_kv;
+  int window, sinks;
+  bf16* out;
+  int ldo;
+  float* lse;
+  int ldl;
+  float* part;
+  int* status;
+};
+cudaError_t launch_attn_rows(const RowsArgs& a, const void* k, const void* v, const float* k_scale, const float* v_scale,
+                             int d_head, int num_items, int num_sms, cudaStream_t s);
 struct WeightsArgs {
   const bf16* q;
   int ldq, T;
