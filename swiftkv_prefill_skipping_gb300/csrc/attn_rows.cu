@@ -17,7 +17,7 @@
 // running maximum may lag behind by 2^8 before O is rescaled, so no reduction over the keys is
 // needed while it holds.
 //
-// bf16: P enters P V as two bf16 parts (about 17 bits). FP8: K and V codes enter as f16 (exact), the
+// bf16: P enters P V as two bf16 parts (about 17 bits). FP8: K and V codes enter as f16 (exact, times 2^-8), the
 // key's scale multiplies the score in float32, and the value's scale rides on P against a
 // reference, P' = p s_v / S_ref in f16; O and S_ref are rescaled when a scale exceeds 128 S_ref.
 //
@@ -47,10 +47,24 @@ struct Rg {
   static_assert(SLOTS >= 2 && SMEM <= 227 * 1024, "ring");
 };
 
+__device__ __forceinline__ float ex2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   uint32_t y;
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
+}
+
+// Four e4m3 codes as two f16 pairs, each value times 2^-8 (exactly: the exponent fields differ by 8
+// and f16's subnormals cover e4m3's): the even and the odd bytes. Cheaper than two conversions and
+// the moves that line their inputs up, and part of it runs on the multiply pipe.
+constexpr float kCodeScale = 256.f;
+__device__ __forceinline__ void unpack4(uint32_t r, uint32_t& even, uint32_t& odd) {
+  even = ((r * 128u) & 0x3f803f80u) | ((r * 256u) & 0x80008000u);
+  odd = ((r >> 1) & 0x3f803f80u) | (r & 0x80008000u);
 }
 
 // NT: columns in groups of 8.
@@ -87,6 +101,10 @@ __global__ void __launch_bounds__(Rg<D, FP8>::WARPS * 32, 1) attn_rows_kernel(
     g.npages = (g.k1 + kPageSize - 1) / kPageSize - g.p0;
     return g;
   };
+  constexpr int NC = kPageSize * CH / 32;  // 16-byte chunks of a page per lane
+  int at[NC];                              // their places in a slot
+#pragma unroll
+  for (int i = 0; i < NC; ++i) at[i] = swz((lane + 32 * i) / CH, (lane + 32 * i) % CH);
   long long lv = gw;
   int lp = 0, lslot = 0;
   Geo lg;
@@ -98,12 +116,21 @@ __global__ void __launch_bounds__(Rg<D, FP8>::WARPS * 32, 1) attn_rows_kernel(
       const bool ok = page >= 0 && page < a.num_pages;
       const size_t blk = ok ? (size_t)page * a.n_kv + lg.kvh : 0;
       const int key0 = (lg.p0 + lp) * kPageSize;
+      const unsigned char *kp = kpool + blk * S::PAGE + lane * 16, *vp = vpool + blk * S::PAGE + lane * 16;
+      const uint32_t to = smem_u32(st);
+      if (ok && key0 >= lg.k0 && key0 + kPageSize <= lg.k1) {
 #pragma unroll
-      for (int c = lane; c < kPageSize * CH; c += 32) {
-        const int row = c / CH, ch = c % CH, key = key0 + row;
-        const int bytes = ok && key >= lg.k0 && key < lg.k1 ? 16 : 0;  // rows outside the unit become zeros
-        cp_async16(smem_u32(st + swz(row, ch)), kpool + blk * S::PAGE + c * 16, bytes);
-        cp_async16(smem_u32(st + S::PAGE + swz(row, ch)), vpool + blk * S::PAGE + c * 16, bytes);
+        for (int i = 0; i < NC; ++i) {
+          cp_async16(to + at[i], kp + i * 512, 16);
+          cp_async16(to + S::PAGE + at[i], vp + i * 512, 16);
+        }
+      } else {  // rows outside the unit become zeros
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+          const int key = key0 + (lane + 32 * i) / CH, bytes = ok && key >= lg.k0 && key < lg.k1 ? 16 : 0;
+          cp_async16(to + at[i], kp + i * 512, bytes);
+          cp_async16(to + S::PAGE + at[i], vp + i * 512, bytes);
+        }
       }
       if (FP8 && lane < 8)  // 16 K scales, then 16 V scales
         cp_async16(smem_u32(st + 2 * S::PAGE + lane * 16), (lane < 4 ? kscale : vscale) + blk * kPageSize + (lane & 3) * 4,
@@ -153,12 +180,12 @@ __global__ void __launch_bounds__(Rg<D, FP8>::WARPS * 32, 1) attn_rows_kernel(
         const bf16* src = a.q + (size_t)(row0 + (in ? cb / G : 0)) * a.ldq + (cg.kvh * G + (in ? cb % G : 0)) * D;
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
-          if (FP8) {  // f16, dims 16 ks + 4 qd .. + 3: the order in which K's codes arrive
+          if (FP8) {  // f16, dims 16 ks + 4 qd + {0, 2} and {1, 3}: the order in which K's codes arrive
             const uint2 w = in ? *reinterpret_cast<const uint2*>(src + ks * 16 + 4 * qd) : make_uint2(0u, 0u);
             const float2 x = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w.x));
             const float2 y = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w.y));
-            qf[t][ks][0] = pack_f16(x.x, x.y);
-            qf[t][ks][1] = pack_f16(y.x, y.y);
+            qf[t][ks][0] = pack_f16(x.x, y.x);
+            qf[t][ks][1] = pack_f16(x.y, y.y);
           } else {
             qf[t][ks][0] = in ? *reinterpret_cast<const uint32_t*>(src + ks * 16 + 2 * qd) : 0u;
             qf[t][ks][1] = in ? *reinterpret_cast<const uint32_t*>(src + ks * 16 + 8 + 2 * qd) : 0u;
@@ -196,10 +223,8 @@ __global__ void __launch_bounds__(Rg<D, FP8>::WARPS * 32, 1) attn_rows_kernel(
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           uint32_t ka[4];
-          ka[0] = f16x2_from_e4m3x2(r[2 * h] & 0xffffu);
-          ka[1] = f16x2_from_e4m3x2(r[2 * h + 1] & 0xffffu);
-          ka[2] = f16x2_from_e4m3x2(r[2 * h] >> 16);
-          ka[3] = f16x2_from_e4m3x2(r[2 * h + 1] >> 16);
+          unpack4(r[2 * h], ka[0], ka[2]);
+          unpack4(r[2 * h + 1], ka[1], ka[3]);
 #pragma unroll
           for (int t = 0; t < NT; ++t) mma_f16_16816(s[t][h], ka, qf[t][ks + h]);
         }
@@ -215,7 +240,8 @@ __global__ void __launch_bounds__(Rg<D, FP8>::WARPS * 32, 1) attn_rows_kernel(
     }
     const int key0 = (cg.p0 + cp) * kPageSize;
     const float* sc = reinterpret_cast<const float*>(st + 2 * S::PAGE);  // FP8: 16 key, 16 value scales
-    const float c_lo = FP8 ? scale_log2 * sc[g0] : scale_log2, c_hi = FP8 ? scale_log2 * sc[g0 + 8] : scale_log2;
+    const float c_lo = FP8 ? kCodeScale * scale_log2 * sc[g0] : scale_log2;
+    const float c_hi = FP8 ? kCodeScale * scale_log2 * sc[g0 + 8] : scale_log2;
     // every key of the page visible to every column
     const bool inside = *reinterpret_cast<const int*>(st + S::STAGE - 16) && key0 >= cg.k0 && key0 + kPageSize <= cg.k1 &&
                         key0 + kPageSize - 1 <= pos_lo &&
@@ -284,7 +310,7 @@ __global__ void __launch_bounds__(Rg<D, FP8>::WARPS * 32, 1) attn_rows_kernel(
     for (int t = 0; t < NT; ++t) {
       float p[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) p[e] = z[t][e] == -INFINITY ? 0.f : exp2f(z[t][e] - m[t][e & 1]);
+      for (int e = 0; e < 4; ++e) p[e] = ex2_approx(z[t][e] - (m[t][e & 1] == -INFINITY ? 0.f : m[t][e & 1]));
       l[t][0] += p[0] + p[2];
       l[t][1] += p[1] + p[3];
       if (FP8) {
@@ -311,10 +337,8 @@ __global__ void __launch_bounds__(Rg<D, FP8>::WARPS * 32, 1) attn_rows_kernel(
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           uint32_t va[4];
-          va[0] = f16x2_from_e4m3x2(__byte_perm(r[2 * h], 0, 0x0020));
-          va[1] = f16x2_from_e4m3x2(__byte_perm(r[2 * h], 0, 0x0031));
-          va[2] = f16x2_from_e4m3x2(__byte_perm(r[2 * h + 1], 0, 0x0020));
-          va[3] = f16x2_from_e4m3x2(__byte_perm(r[2 * h + 1], 0, 0x0031));
+          unpack4(r[2 * h], va[0], va[1]);
+          unpack4(r[2 * h + 1], va[2], va[3]);
 #pragma unroll
           for (int t = 0; t < NT; ++t) mma_f16_16816(o[t][c + h], va, ph[t]);
         }
@@ -350,7 +374,7 @@ __global__ void __launch_bounds__(Rg<D, FP8>::WARPS * 32, 1) attn_rows_kernel(
           // dims this thread holds of tile i: bf16 16 i + g0 and + 8; FP8 16 i + 2 g0 and + 1
           if (whole) {
             const int row = row0 + col / G, h = cg.kvh * G + col % G;
-            const float f = (FP8 ? sref : 1.f) / sum;
+            const float f = (FP8 ? kCodeScale * sref : 1.f) / sum;
             if (a.lse && g0 == 0) a.lse[(size_t)h * a.ldl + row] = (m[t][e] + log2f(sum)) * kLn2;
             bf16* dst = a.out + (size_t)row * a.ldo + (size_t)h * D;
 #pragma unroll
@@ -369,7 +393,7 @@ __global__ void __launch_bounds__(Rg<D, FP8>::WARPS * 32, 1) attn_rows_kernel(
             for (int i = 0; i < D / 16; ++i) {
               if (FP8) {
                 *reinterpret_cast<float2*>(pp + 4 + 16 * i + 2 * g0) =
-                    make_float2(o[t][i][e] * sref, o[t][i][2 + e] * sref);
+                    make_float2(o[t][i][e] * (kCodeScale * sref), o[t][i][2 + e] * (kCodeScale * sref));
               } else {
                 pp[4 + 16 * i + g0] = o[t][i][e];
                 pp[4 + 16 * i + 8 + g0] = o[t][i][2 + e];
