@@ -22,7 +22,13 @@ def _stream(stream) -> int:
     return s.cuda_stream
 
 
+# the current stream's handle without a Stream object around it, where PyTorch offers that
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream_of(dev: torch.device, stream) -> int:
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(dev.index)
     return (stream if stream is not None else torch.cuda.current_stream(dev)).cuda_stream
 
 
@@ -146,12 +152,16 @@ class KVCache:
             self._ks = (C.c_void_p * n)(*[self.k_scale[c].data_ptr() for c in range(n)])
             self._vs = (C.c_void_p * n)(*[self.v_scale[c].data_ptr() for c in range(n)])
         self.num_caches = n
-        self.pages = self._pages(self.block_table)
+        self._set_pages(self._pages(self.block_table))
 
     def _pages(self, block_table: torch.Tensor) -> B.KVPages:
         ptr = lambda a: C.cast(a, C.POINTER(C.c_void_p)) if a is not None else None  # noqa: E731
         return B.KVPages(ptr(self._kp), ptr(self._vp), self.num_caches, self.num_pages, 16, block_table.data_ptr(),
                          block_table.shape[1], 1 if self.dtype == "fp8" else 0, ptr(self._ks), ptr(self._vs))
+
+    def _set_pages(self, pages: B.KVPages) -> None:
+        self.pages, self.pages_ref = pages, C.byref(pages)
+        self.num_rows = self.block_table.shape[0]
 
     def view(self, rows: Sequence[int]) -> "KVCache":
         """The same pools with block table rows `rows` (in that order): a batch that holds
@@ -160,7 +170,7 @@ class KVCache:
         out.__dict__.update(self.__dict__)
         out.block_table = self.block_table[torch.as_tensor(list(rows), dtype=torch.long,
                                                            device=self.block_table.device)].contiguous()
-        out.pages = out._pages(out.block_table)
+        out._set_pages(out._pages(out.block_table))
         return out
 
     def _rows(self, pool: torch.Tensor, s: int, n: int) -> torch.Tensor:
@@ -243,31 +253,34 @@ def decode_step(model: Model, tokens: torch.Tensor, seq_lens: Sequence[int], kv:
     return logits, nxt
 
 
-def _need(cond: bool, msg: str) -> None:
-    if not cond:
-        raise ValueError(msg)
-
-
 def _chunks(cu_seqlens, ctx_lens, kv: KVCache):
     """Host int32 arrays of a ragged batch, checked against the block table: (cu, ctx, P, T)."""
     cu = np.ascontiguousarray(cu_seqlens, dtype=np.int32)
     ctx = None if ctx_lens is None else np.ascontiguousarray(ctx_lens, dtype=np.int32)
-    P = len(cu) - 1
-    _need(cu.ndim == 1 and P >= 0, "cu_seqlens: [P + 1]")
-    _need(ctx is None or ctx.shape == (P,), f"ctx_lens: {P} entries")
-    _need(P <= kv.block_table.shape[0], f"{P} chunks, but the block table has {kv.block_table.shape[0]} rows")
+    P = cu.shape[0] - 1 if cu.ndim == 1 else -1
+    if P < 0 or (ctx is not None and ctx.shape != (P,)):
+        raise ValueError("cu_seqlens: [P + 1], ctx_lens: [P]")
+    if P > kv.num_rows:
+        raise ValueError(f"{P} chunks, but the block table has {kv.num_rows} rows")
     return cu, ctx, P, int(cu[P])
 
 
 def _rows_of(t: torch.Tensor, T: int, model: Model, dev, name: str) -> int:
     """Row stride of bf16 rows [T, n_q, d_h] (or [T, n_q * d_h]) whose heads are contiguous."""
-    s = model.shape
-    ok = t.dtype == torch.bfloat16 and t.device == dev and t.shape[0] == T and (
-        t.dim() == 3 and t.shape[1:] == (s.n_q, s.d_h) and t.stride(2) == 1 and (s.n_q == 1 or t.stride(1) == s.d_h)
-        or t.dim() == 2 and t.shape[1] == s.n_q * s.d_h and t.stride(1) == 1)
-    if not ok:
+    s, shape, stride = model.shape, t.shape, t.stride()
+    if t.dtype != torch.bfloat16 or t.device != dev or shape[0] != T or not (
+            len(shape) == 3 and shape[1] == s.n_q and shape[2] == s.d_h and stride[2] == 1 and
+            (s.n_q == 1 or stride[1] == s.d_h) or
+            len(shape) == 2 and shape[1] == s.n_q * s.d_h and stride[1] == 1):
         raise ValueError(f"{name}: bfloat16 [{T}, {s.n_q}, {s.d_h}] on {dev}, the heads of a row contiguous")
-    return t.stride(0) if T > 1 else s.n_q * s.d_h
+    return stride[0] if T > 1 else s.n_q * s.d_h
+
+
+def _flat(t: torch.Tensor, dtype, shape: tuple, dev, name: str) -> int:
+    """Address of a contiguous tensor of this type and shape on dev."""
+    if t.dtype != dtype or tuple(t.shape) != shape or t.device != dev or not t.is_contiguous():
+        raise ValueError(f"{name}: contiguous {dtype} {list(shape)} on {dev}")
+    return t.data_ptr()
 
 
 def attend(model: Model, q: torch.Tensor, cu_seqlens: Sequence[int], ctx_lens: Optional[Sequence[int]], kv: KVCache,
@@ -284,13 +297,9 @@ def attend(model: Model, q: torch.Tensor, cu_seqlens: Sequence[int], ctx_lens: O
     if out is None:
         out = torch.empty((T, model.shape.n_q, model.shape.d_h), dtype=torch.bfloat16, device=dev)
     ldo = _rows_of(out, T, model, dev, "out")
-    if lse is not None:
-        _need(lse.dtype == torch.float32 and lse.device == dev and lse.shape == (model.shape.n_q, T) and
-              lse.is_contiguous(), f"lse: contiguous float32 [{model.shape.n_q}, {T}] on {dev}")
-    B.check(B.lib().swiftkv_attend(model.handle, cache, q.data_ptr(), ldq, cu.ctypes.data,
-                                   None if ctx is None else ctx.ctypes.data, P, C.byref(kv.pages), window, sinks,
-                                   out.data_ptr(), ldo, None if lse is None else lse.data_ptr(),
-                                   _stream_of(dev, stream)))
+    lp = None if lse is None else _flat(lse, torch.float32, (model.shape.n_q, T), dev, "lse")
+    B.check(B.lib().swiftkv_attend(model.handle, cache, q.data_ptr(), ldq, B.host(cu), B.host(ctx), P, kv.pages_ref,
+                                   window, sinks, out.data_ptr(), ldo, lp, _stream_of(dev, stream)))
     return out
 
 
@@ -304,13 +313,10 @@ def attention_weights(model: Model, q: torch.Tensor, lse: torch.Tensor, cu_seqle
     cu, ctx, P, T = _chunks(cu_seqlens, ctx_lens, kv)
     dev, s = kv.k.device, model.shape
     ldq = _rows_of(q, T, model, dev, "q")
-    _need(lse.dtype == torch.float32 and lse.device == dev and lse.shape == (s.n_q, T) and lse.is_contiguous(),
-          f"lse: contiguous float32 [{s.n_q}, {T}] on {dev}")
-    _need(scores.dtype == torch.float32 and scores.device == dev and scores.shape == (kv.num_pages, s.n_kv, 16) and
-          scores.is_contiguous(), f"scores: contiguous float32 [{kv.num_pages}, {s.n_kv}, 16] on {dev}")
-    B.check(B.lib().swiftkv_attention_weights(model.handle, cache, q.data_ptr(), ldq, lse.data_ptr(), cu.ctypes.data,
-                                              None if ctx is None else ctx.ctypes.data, P, C.byref(kv.pages), window,
-                                              sinks, decay, scores.data_ptr(), _stream_of(dev, stream)))
+    lp = _flat(lse, torch.float32, (s.n_q, T), dev, "lse")
+    sp = _flat(scores, torch.float32, (kv.num_pages, s.n_kv, 16), dev, "scores")
+    B.check(B.lib().swiftkv_attention_weights(model.handle, cache, q.data_ptr(), ldq, lp, B.host(cu), B.host(ctx), P,
+                                              kv.pages_ref, window, sinks, decay, sp, _stream_of(dev, stream)))
     return scores
 
 
@@ -325,32 +331,29 @@ def evict(model: Model, kv: KVCache, scores: torch.Tensor, seq_lens: Sequence[in
     [caches, P, n_kv, keep] int32, -1 behind a shorter list; sequence s then holds
     min(seq_lens[s], keep) keys."""
     sl = np.ascontiguousarray(seq_lens, dtype=np.int32)
-    P, dev, s = len(sl), kv.k.device, model.shape
-    _need(P <= kv.block_table.shape[0], f"{P} sequences, but the block table has {kv.block_table.shape[0]} rows")
-    _need(keep >= 1, "keep must be at least 1")
+    P, dev, s = sl.shape[0], kv.k.device, model.shape
+    if P > kv.num_rows:
+        raise ValueError(f"{P} sequences, but the block table has {kv.num_rows} rows")
+    if keep < 1 or (cache is not None and not 0 <= cache < kv.num_caches):
+        raise ValueError(f"keep {keep}, cache {cache} of {kv.num_caches}")
     pool = (kv.num_pages, s.n_kv, 16)
     n = kv.num_caches if cache is None else 1
-    _need(cache is None or 0 <= cache < kv.num_caches, f"cache {cache} of {kv.num_caches}")
-    _need(scores.dtype == torch.float32 and scores.device == dev and scores.is_contiguous() and
-          scores.shape == (pool if cache is not None else (n,) + pool),
-          f"scores: contiguous float32 {pool if cache is not None else (n,) + pool} on {dev}")
+    base = _flat(scores, torch.float32, pool if cache is not None else (n,) + pool, dev, "scores")
+    dst, width = None, 0
     if dst_block_table is not None:
-        _need(dst_block_table.dtype == torch.int32 and dst_block_table.device == dev and dst_block_table.dim() == 2 and
-              dst_block_table.shape[0] >= P and dst_block_table.is_contiguous(),
-              f"dst_block_table: contiguous int32 [{P}, pages] on {dev}")
+        width = dst_block_table.shape[-1]
+        if dst_block_table.dim() != 2 or dst_block_table.shape[0] < P:
+            raise ValueError(f"dst_block_table: int32 [{P}, pages]")
+        dst = _flat(dst_block_table, torch.int32, tuple(dst_block_table.shape), dev, "dst_block_table")
     if kept is None:
         kept = torch.empty((n, P, s.n_kv, keep), dtype=torch.int32, device=dev)
-    else:
-        _need(kept.dtype == torch.int32 and kept.device == dev and kept.shape == (n, P, s.n_kv, keep) and
-              kept.is_contiguous(), f"kept: contiguous int32 {(n, P, s.n_kv, keep)} on {dev}")
-    base, step, first = scores.data_ptr(), 4 * kv.num_pages * s.n_kv * 16, cache or 0
+    kp = _flat(kept, torch.int32, (n, P, s.n_kv, keep), dev, "kept")
+    step, first = 4 * kv.num_pages * s.n_kv * 16, cache or 0
     ptrs = (C.c_void_p * kv.num_caches)()
     for c in range(n):
         ptrs[first + c] = base + c * step
-    dst = dst_block_table
-    B.check(B.lib().swiftkv_evict(model.handle, -1 if cache is None else cache, C.byref(kv.pages), ptrs,
-                                  sl.ctypes.data, P, keep, sinks, recent, None if dst is None else dst.data_ptr(),
-                                  0 if dst is None else dst.shape[1], kept.data_ptr(), _stream_of(dev, stream)))
+    B.check(B.lib().swiftkv_evict(model.handle, -1 if cache is None else cache, kv.pages_ref, ptrs, B.host(sl), P, keep,
+                                  sinks, recent, dst, width, kp, _stream_of(dev, stream)))
     return kept
 
 
@@ -363,32 +366,22 @@ def sample(logits: torch.Tensor, u: torch.Tensor, temperature=1.0, top_k=0, top_
     uniform numbers u [P] in [0, 1). temperature, top_k, top_p and min_p are numbers, or one value
     per row as tensors on the same device (float32; top_k int32); temperature <= 0 takes the argmax,
     top_k <= 0, top_p >= 1 and min_p <= 0 are off. Enqueued without synchronising."""
-    _need(logits.dim() == 2 and logits.dtype == torch.float32 and logits.is_cuda, "logits: float32 CUDA [P, V]")
-    P, V = logits.shape
-    ld, step = logits.stride()
-    _need(V >= 1, "logits need at least one column")
-    _need(V == 1 or step == 1, "logits: the columns of a row must be contiguous")
+    if logits.dim() != 2 or logits.dtype != torch.float32 or not logits.is_cuda:
+        raise ValueError("logits: float32 CUDA [P, V]")
+    (P, V), (ld, step), dev = logits.shape, logits.stride(), logits.device
     if P <= 1:
         ld = V
-    _need(ld >= V, "logits: rows must not overlap")
-    dev = logits.device
-
-    def rows(t, dtype, name):
-        if not (t.dtype == dtype and t.dim() == 1 and t.shape[0] == P and t.is_contiguous() and t.device == dev):
-            raise ValueError(f"{name}: contiguous {dtype} [{P}] on {dev}")
-        return t.data_ptr()
-
-    s = B.Sampling(None, None, None, None, 1.0, 0, 1.0, 0.0)
+    if V < 1 or (V > 1 and step != 1) or ld < V:
+        raise ValueError("logits: at least one column, contiguous within a row, rows that do not overlap")
+    s, vec = B.Sampling(None, None, None, None, 1.0, 0, 1.0, 0.0), (P,)
     for (name, dtype), value in zip(_SAMPLING, (temperature, top_k, top_p, min_p)):
         if isinstance(value, torch.Tensor):
-            setattr(s, name, rows(value, dtype, name))
+            setattr(s, name, _flat(value, dtype, vec, dev, name))
         else:
             setattr(s, name + "_all", int(value) if dtype == torch.int32 else float(value))
     if out is None:
-        out = torch.empty((P,), dtype=torch.int32, device=dev)
-    else:
-        rows(out, torch.int32, "out")
+        out = torch.empty(vec, dtype=torch.int32, device=dev)
     with _on(dev):
-        B.check(B.lib().swiftkv_sample(logits.data_ptr(), P, V, ld, C.byref(s), rows(u, torch.float32, "u"),
-                                       out.data_ptr(), _stream_of(dev, stream)))
+        B.check(B.lib().swiftkv_sample(logits.data_ptr(), P, V, ld, C.byref(s), _flat(u, torch.float32, vec, dev, "u"),
+                                       _flat(out, torch.int32, vec, dev, "out"), _stream_of(dev, stream)))
     return out

@@ -120,6 +120,11 @@ def lib(path: str | None = None):
     return _lib
 
 
+def host(a) -> int | None:
+    """Address of a NumPy array's data (None for None); the array must outlive the call."""
+    return None if a is None else a.__array_interface__["data"][0]
+
+
 def check(code: int) -> int:
     if code < 0:
         raise SwiftKVError(code, lib().swiftkv_last_error().decode())

@@ -70,12 +70,15 @@ __device__ __forceinline__ void unpack4(uint32_t r, uint32_t& even, uint32_t& od
 // NT: columns in groups of 8.
 template <int D, bool FP8, int NT>
 __global__ void __launch_bounds__(Rg<D, FP8>::WARPS * 32, 1) attn_rows_kernel(
-    const RowsArgs a, const unsigned char* __restrict__ kpool, const unsigned char* __restrict__ vpool,
-    const float* __restrict__ kscale, const float* __restrict__ vscale, float scale_log2) {
+    const RowsArgs a, const __grid_constant__ InlineInts inl, const unsigned char* __restrict__ kpool,
+    const unsigned char* __restrict__ vpool, const float* __restrict__ kscale, const float* __restrict__ vscale,
+    float scale_log2) {
   using S = Rg<D, FP8>;
   extern __shared__ __align__(128) unsigned char smem[];
   griddep_launch_dependents();
   griddep_wait();
+  const int* const lists = list_base(a.lists, inl);
+  const int *items = lists + a.o_items, *units = lists + a.o_units, *ubeg = lists + a.o_ubeg;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   unsigned char* ring = smem + (size_t)warp * S::SLOTS * S::STAGE;
   const int G = a.n_q / a.n_kv;
@@ -93,10 +96,10 @@ __global__ void __launch_bounds__(Rg<D, FP8>::WARPS * 32, 1) attn_rows_kernel(
     Geo g;
     const int u = (int)(v / a.n_kv);
     g.kvh = (int)(v - (long long)u * a.n_kv);
-    g.item = a.units[3 * u];
-    g.k0 = a.units[3 * u + 1];
-    g.k1 = g.k0 + a.units[3 * u + 2];
-    g.seq = a.items[4 * g.item + 2];
+    g.item = units[3 * u];
+    g.k0 = units[3 * u + 1];
+    g.k1 = g.k0 + units[3 * u + 2];
+    g.seq = items[4 * g.item + 2];
     g.p0 = g.k0 / kPageSize;
     g.npages = (g.k1 + kPageSize - 1) / kPageSize - g.p0;
     return g;
@@ -168,7 +171,7 @@ __global__ void __launch_bounds__(Rg<D, FP8>::WARPS * 32, 1) attn_rows_kernel(
     __syncwarp();
     const unsigned char* st = ring + cslot * S::STAGE;
     if (cp == 0) {  // a new unit: Q as B operands straight from memory, fresh softmax state
-      const int* it = a.items + 4 * cg.item;
+      const int* it = items + 4 * cg.item;
       row0 = it[0];
       cols = it[1] * G;
       pos_lo = it[3];
@@ -360,7 +363,7 @@ __global__ void __launch_bounds__(Rg<D, FP8>::WARPS * 32, 1) attn_rows_kernel(
     if (++cslot == S::SLOTS) cslot = 0;
 
     if (++cp == cg.npages) {
-      const bool whole = a.ubeg[cg.item + 1] - a.ubeg[cg.item] == 1;
+      const bool whole = ubeg[cg.item + 1] - ubeg[cg.item] == 1;
       const int u = (int)(cv / a.n_kv);
 #pragma unroll
       for (int t = 0; t < NT; ++t)
@@ -415,16 +418,19 @@ __global__ void __launch_bounds__(Rg<D, FP8>::WARPS * 32, 1) attn_rows_kernel(
 constexpr int MERGE_WARPS = 4;
 
 template <int D>
-__global__ void __launch_bounds__(MERGE_WARPS * 32) attn_rows_merge(const RowsArgs a, int num_items) {
+__global__ void __launch_bounds__(MERGE_WARPS * 32) attn_rows_merge(const RowsArgs a, const __grid_constant__ InlineInts inl,
+                                                                     int num_items) {
   griddep_launch_dependents();
   griddep_wait();
+  const int* const lists = list_base(a.lists, inl);
+  const int *items = lists + a.o_items, *ubeg = lists + a.o_ubeg;
   const int G = a.n_q / a.n_kv, per = a.n_kv * a.max_cols;
   const long long w = (long long)blockIdx.x * MERGE_WARPS + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
   if (w >= (long long)num_items * per) return;
   const int b = (int)(w / per), kvh = (int)(w % per) / a.max_cols, col = (int)(w % a.max_cols);
-  const int u0 = a.ubeg[b], ns = a.ubeg[b + 1] - u0;
-  if (ns <= 1 || col >= a.items[4 * b + 1] * G) return;  // written by its only unit / no such column
+  const int u0 = ubeg[b], ns = ubeg[b + 1] - u0;
+  if (ns <= 1 || col >= items[4 * b + 1] * G) return;  // written by its only unit / no such column
   const size_t step = (size_t)per * (D + 4);
   const float* p = a.part + (((size_t)u0 * a.n_kv + kvh) * a.max_cols + col) * (D + 4);
   constexpr int E = D / 32, B = 8;
@@ -467,7 +473,7 @@ __global__ void __launch_bounds__(MERGE_WARPS * 32) attn_rows_merge(const RowsAr
       for (int e = 0; e < E; ++e) o[e] = fmaf(v[i][e], wi, o[e]);
     }
   }
-  const int row = a.items[4 * b] + col / G, h = kvh * G + col % G;
+  const int row = items[4 * b] + col / G, h = kvh * G + col % G;
   const float inv = 1.f / den;
   bf16* dst = a.out + (size_t)row * a.ldo + (size_t)h * D + lane * E;
 #pragma unroll
@@ -476,7 +482,7 @@ __global__ void __launch_bounds__(MERGE_WARPS * 32) attn_rows_merge(const RowsAr
 }
 
 template <int D, bool FP8, int NT>
-cudaError_t launch_nt(const RowsArgs& a, const void* k, const void* v, const float* ks, const float* vs, int num_items,
+cudaError_t launch_nt(const RowsArgs& a, const InlineInts& inl, const void* k, const void* v, const float* ks, const float* vs, int num_items,
                       int num_sms, cudaStream_t s) {
   using S = Rg<D, FP8>;
   static PerDeviceOnce once;
@@ -484,32 +490,32 @@ cudaError_t launch_nt(const RowsArgs& a, const void* k, const void* v, const flo
   if (e != cudaSuccess) return e;
   const long long total = (long long)a.num_units * a.n_kv;
   e = launch_pdl(attn_rows_kernel<D, FP8, NT>, dim3((unsigned)(total < num_sms ? total : num_sms)), dim3(S::WARPS * 32),
-                 S::SMEM, s, a, static_cast<const unsigned char*>(k), static_cast<const unsigned char*>(v), ks, vs,
+                 S::SMEM, s, a, inl, static_cast<const unsigned char*>(k), static_cast<const unsigned char*>(v), ks, vs,
                  1.4426950408889634f / sqrtf((float)D));
   if (e != cudaSuccess || a.num_units == num_items) return e;
   const long long warps = (long long)num_items * a.n_kv * a.max_cols;
   return launch_pdl(attn_rows_merge<D>, dim3((unsigned)((warps + MERGE_WARPS - 1) / MERGE_WARPS)), dim3(MERGE_WARPS * 32),
-                    0, s, a, num_items);
+                    0, s, a, inl, num_items);
 }
 
 template <int D, bool FP8>
-cudaError_t launch_cols(const RowsArgs& a, const void* k, const void* v, const float* ks, const float* vs, int num_items,
+cudaError_t launch_cols(const RowsArgs& a, const InlineInts& inl, const void* k, const void* v, const float* ks, const float* vs, int num_items,
                         int num_sms, cudaStream_t s) {
-  return a.max_cols <= 8 ? launch_nt<D, FP8, 1>(a, k, v, ks, vs, num_items, num_sms, s)
-                         : launch_nt<D, FP8, 2>(a, k, v, ks, vs, num_items, num_sms, s);
+  return a.max_cols <= 8 ? launch_nt<D, FP8, 1>(a, inl, k, v, ks, vs, num_items, num_sms, s)
+                         : launch_nt<D, FP8, 2>(a, inl, k, v, ks, vs, num_items, num_sms, s);
 }
 
 }  // namespace
 
-cudaError_t launch_attn_rows(const RowsArgs& a, const void* k, const void* v, const float* ks, const float* vs, int d_head,
+cudaError_t launch_attn_rows(const RowsArgs& a, const InlineInts& inl, const void* k, const void* v, const float* ks, const float* vs, int d_head,
                              int num_items, int num_sms, cudaStream_t s) {
   if (a.max_cols > kRowsCols || (!ks != !vs)) return cudaErrorNotSupported;
   if (d_head == 128)
-    return ks ? launch_cols<128, true>(a, k, v, ks, vs, num_items, num_sms, s)
-              : launch_cols<128, false>(a, k, v, ks, vs, num_items, num_sms, s);
+    return ks ? launch_cols<128, true>(a, inl, k, v, ks, vs, num_items, num_sms, s)
+              : launch_cols<128, false>(a, inl, k, v, ks, vs, num_items, num_sms, s);
   if (d_head == 64)
-    return ks ? launch_cols<64, true>(a, k, v, ks, vs, num_items, num_sms, s)
-              : launch_cols<64, false>(a, k, v, ks, vs, num_items, num_sms, s);
+    return ks ? launch_cols<64, true>(a, inl, k, v, ks, vs, num_items, num_sms, s)
+              : launch_cols<64, false>(a, inl, k, v, ks, vs, num_items, num_sms, s);
   return cudaErrorNotSupported;
 }
 

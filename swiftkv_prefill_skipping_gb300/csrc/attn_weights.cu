@@ -47,15 +47,18 @@ struct Rp {
 
 // NT: columns in groups of 8 (rows x heads of a chunk, at most 8 NT).
 template <int D, bool FP8, int NT>
-__global__ void __launch_bounds__(RW * 32, 1) weights_rows_kernel(const WeightsArgs a, const bf16* __restrict__ kpool,
+__global__ void __launch_bounds__(RW * 32, 1) weights_rows_kernel(const WeightsArgs a,
+                                                                  const __grid_constant__ InlineInts inl,
+                                                                  const bf16* __restrict__ kpool,
                                                                   const uint8_t* __restrict__ k8,
-                                                                  const float* __restrict__ kscale,
-                                                                  const int* __restrict__ units, int num_units,
+                                                                  const float* __restrict__ kscale, int num_units,
                                                                   float scale_log2) {
   using S = Rp<D, FP8>;
   extern __shared__ __align__(128) unsigned char smem[];
   griddep_launch_dependents();
   griddep_wait();
+  const int* const lists = list_base(a.lists, inl);
+  const int *units = lists + a.o_units, *cu = lists + a.o_cu, *ctx = lists + a.o_ctx;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   unsigned char* ring = smem + (size_t)warp * RSTAGES * S::STAGE;
   const int G = a.n_q / a.n_kv;
@@ -128,7 +131,7 @@ __global__ void __launch_bounds__(RW * 32, 1) weights_rows_kernel(const WeightsA
     if (cp == 0) {
       // the chunk's rows x heads as B columns (column c: row c / G, head c % G of the group), read
       // once per unit; columns past them weigh nothing
-      const int seq0 = a.cu[cg.s], M = (a.cu[cg.s + 1] - seq0) * G, c0 = a.ctx[cg.s];
+      const int seq0 = cu[cg.s], M = (cu[cg.s + 1] - seq0) * G, c0 = ctx[cg.s];
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         const int cb = t * 8 + g0;
@@ -279,9 +282,10 @@ __device__ __forceinline__ bool w_item(long long it, const int* __restrict__ til
   I.kvh = (int)(w - (long long)t * a.n_kv);
   I.s = tiles[2 * t];
   I.key0 = tiles[2 * t + 1] * BK;
-  I.seq0 = a.cu[I.s];
-  I.n = a.cu[I.s + 1] - I.seq0;
-  I.c0 = a.ctx[I.s];
+  const int *cu = a.lists + a.o_cu, *ctx = a.lists + a.o_ctx;
+  I.seq0 = cu[I.s];
+  I.n = cu[I.s + 1] - I.seq0;
+  I.c0 = ctx[I.s];
   I.nk = I.c0 + I.n;
   // rows that see some key of the tile
   const int lo = max(0, I.key0 - I.c0);
@@ -567,7 +571,7 @@ __global__ void __launch_bounds__(WT, 1) weights_tc_kernel(const __grid_constant
 }
 
 template <int D, bool FP8, int NT>
-cudaError_t rows_launch(const WeightsArgs& a, const bf16* k, const uint8_t* k8, const float* ks, const int* units,
+cudaError_t rows_launch(const WeightsArgs& a, const InlineInts& inl, const bf16* k, const uint8_t* k8, const float* ks,
                         int num_units, int num_sms, cudaStream_t s) {
   constexpr int smem = Rp<D, FP8>::SMEM;
   static_assert(smem <= 227 * 1024, "rings must fit in shared memory");
@@ -576,16 +580,16 @@ cudaError_t rows_launch(const WeightsArgs& a, const bf16* k, const uint8_t* k8, 
   if (e != cudaSuccess) return e;
   const long long total = (long long)num_units * a.n_kv;
   const int ctas = (int)(total < num_sms ? total : num_sms);
-  return launch_pdl(weights_rows_kernel<D, FP8, NT>, dim3(ctas), dim3(RW * 32), smem, s, a, k, k8, ks, units, num_units,
+  return launch_pdl(weights_rows_kernel<D, FP8, NT>, dim3(ctas), dim3(RW * 32), smem, s, a, inl, k, k8, ks, num_units,
                     kLog2e / sqrtf((float)D));
 }
 
 template <int D, bool FP8>
-cudaError_t rows_cols(const WeightsArgs& a, const bf16* k, const uint8_t* k8, const float* ks, int max_cols,
-                      const int* units, int num_units, int num_sms, cudaStream_t s) {
-  if (max_cols <= 8) return rows_launch<D, FP8, 1>(a, k, k8, ks, units, num_units, num_sms, s);
-  if (max_cols <= 16) return rows_launch<D, FP8, 2>(a, k, k8, ks, units, num_units, num_sms, s);
-  return rows_launch<D, FP8, 4>(a, k, k8, ks, units, num_units, num_sms, s);
+cudaError_t rows_cols(const WeightsArgs& a, const InlineInts& inl, const bf16* k, const uint8_t* k8, const float* ks,
+                      int max_cols, int num_units, int num_sms, cudaStream_t s) {
+  if (max_cols <= 8) return rows_launch<D, FP8, 1>(a, inl, k, k8, ks, num_units, num_sms, s);
+  if (max_cols <= 16) return rows_launch<D, FP8, 2>(a, inl, k, k8, ks, num_units, num_sms, s);
+  return rows_launch<D, FP8, 4>(a, inl, k, k8, ks, num_units, num_sms, s);
 }
 
 template <int D>
@@ -608,15 +612,15 @@ cudaError_t tc_launch(const WeightsArgs& a, const bf16* k, const float* ks, cons
 
 }  // namespace
 
-cudaError_t launch_weights_rows(const WeightsArgs& a, const bf16* k, const uint8_t* k8, const float* ks, int d_head,
-                                int max_cols, const int* units, int num_units, int num_sms, cudaStream_t s) {
+cudaError_t launch_weights_rows(const WeightsArgs& a, const InlineInts& inl, const bf16* k, const uint8_t* k8,
+                                const float* ks, int d_head, int max_cols, int num_units, int num_sms, cudaStream_t s) {
   if (max_cols > kWeightCols) return cudaErrorNotSupported;
   if (d_head == 128)
-    return k8 ? rows_cols<128, true>(a, k, k8, ks, max_cols, units, num_units, num_sms, s)
-              : rows_cols<128, false>(a, k, k8, ks, max_cols, units, num_units, num_sms, s);
+    return k8 ? rows_cols<128, true>(a, inl, k, k8, ks, max_cols, num_units, num_sms, s)
+              : rows_cols<128, false>(a, inl, k, k8, ks, max_cols, num_units, num_sms, s);
   if (d_head == 64)
-    return k8 ? rows_cols<64, true>(a, k, k8, ks, max_cols, units, num_units, num_sms, s)
-              : rows_cols<64, false>(a, k, k8, ks, max_cols, units, num_units, num_sms, s);
+    return k8 ? rows_cols<64, true>(a, inl, k, k8, ks, max_cols, num_units, num_sms, s)
+              : rows_cols<64, false>(a, inl, k, k8, ks, max_cols, num_units, num_sms, s);
   return cudaErrorNotSupported;
 }
 

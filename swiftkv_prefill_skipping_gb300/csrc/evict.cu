@@ -36,12 +36,25 @@ __device__ __forceinline__ unsigned score_key(float x) {
 struct List {
   int c, s, h, n;  // cache (within the call), sequence, KV head, keys
 };
-__device__ __forceinline__ List list_at(const EvictArgs& a, int i) {
+// The lengths and pool pointers of a call.
+struct Pools {
+  const int* lens;
+  void* const* ptrs;
+  int n;  // caches of the model
+  __device__ __forceinline__ Pools(const EvictArgs& a, const InlineInts& inl)
+      : lens(list_base(a.lists, inl)), ptrs(reinterpret_cast<void* const*>(lens + a.o_ptrs)), n(a.num_ptrs) {}
+  __device__ __forceinline__ unsigned char* k(int c) const { return static_cast<unsigned char*>(ptrs[c]); }
+  __device__ __forceinline__ unsigned char* v(int c) const { return static_cast<unsigned char*>(ptrs[n + c]); }
+  __device__ __forceinline__ float* scores(int c) const { return static_cast<float*>(ptrs[2 * n + c]); }
+  __device__ __forceinline__ float* ks(int c) const { return static_cast<float*>(ptrs[3 * n + c]); }
+  __device__ __forceinline__ float* vs(int c) const { return static_cast<float*>(ptrs[4 * n + c]); }
+};
+__device__ __forceinline__ List list_at(const EvictArgs& a, const Pools& pools, int i) {
   List l;
   l.h = i % a.n_kv;
   l.s = i / a.n_kv % a.P;
   l.c = i / a.n_kv / a.P;
-  l.n = a.lens[l.s];
+  l.n = pools.lens[l.s];
   return l;
 }
 // Row index (page, head, slot) of key j of a list in the pools, -1 on a page outside them.
@@ -57,16 +70,18 @@ __device__ __forceinline__ long long row_of(const int* bt, int width, int num_pa
 constexpr int EBINS = 2048;
 __device__ __forceinline__ int digit_shift(int d) { return d == 0 ? 21 : d == 1 ? 10 : 0; }
 
-__global__ void __launch_bounds__(ET) evict_select_kernel(const EvictArgs a, int in_smem) {
+__global__ void __launch_bounds__(ET) evict_select_kernel(const EvictArgs a, const __grid_constant__ InlineInts inl,
+                                                          int in_smem) {
   extern __shared__ __align__(16) unsigned keys[];  // [n rounded up to pages] when in_smem
   __shared__ unsigned hist[EBINS];
   __shared__ unsigned s_sum[EWARPS], s_key, s_left;
   __shared__ int s_cnt[2][EWARPS];
   griddep_launch_dependents();
   griddep_wait();
-  const List l = list_at(a, blockIdx.x);
+  const Pools pools(a, inl);
+  const List l = list_at(a, pools, blockIdx.x);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const float* scores = a.scores[a.first_cache + l.c];
+  const float* scores = pools.scores(a.first_cache + l.c);
   int* kept = a.kept + (size_t)blockIdx.x * a.keep;
   const int n = l.n, pages = (n + kPageSize - 1) / kPageSize;
   const int* bt = a.src_bt + (size_t)l.s * a.src_pages;
@@ -202,7 +217,7 @@ __global__ void __launch_bounds__(ET) evict_select_kernel(const EvictArgs a, int
   // the kept keys' floats; a round is read whole before it is written (in place, rows move down)
   const int m = min(n, a.keep);
   const int c = a.first_cache + l.c;
-  float* arrays[3] = {a.scores[c], a.ks ? a.ks[c] : nullptr, a.vs ? a.vs[c] : nullptr};
+  float* arrays[3] = {pools.scores(c), a.fp8 ? pools.ks(c) : nullptr, a.fp8 ? pools.vs(c) : nullptr};
   constexpr int U = 4;
   for (int i0 = 0; i0 < m; i0 += ET * U) {
     float v[U][3];
@@ -233,16 +248,17 @@ constexpr int MT = 256;  // threads of the move
 
 // To other pages: CTA (list, part of the kept list); K and V of a row by neighbouring threads.
 constexpr int kPartBytes = 32768;
-__global__ void __launch_bounds__(MT) evict_copy_kernel(const EvictArgs a, int parts) {
+__global__ void __launch_bounds__(MT) evict_copy_kernel(const EvictArgs a, const __grid_constant__ InlineInts inl, int parts) {
   griddep_launch_dependents();
   griddep_wait();
   const int li = blockIdx.x / parts, part = blockIdx.x - li * parts;
-  const List l = list_at(a, li);
+  const Pools pools(a, inl);
+  const List l = list_at(a, pools, li);
   const int* kept = a.kept + (size_t)li * a.keep;
   const int vecs = a.row_bytes / 16, rows = kPartBytes / a.row_bytes;
   const int i0 = part * rows, i1 = min(min(l.n, a.keep), i0 + rows);
-  unsigned char* k = a.k[a.first_cache + l.c];
-  unsigned char* v = a.v[a.first_cache + l.c];
+  unsigned char* k = pools.k(a.first_cache + l.c);
+  unsigned char* v = pools.v(a.first_cache + l.c);
   const int count = (i1 - i0) * vecs;
   constexpr int U = 4;
   for (int e0 = threadIdx.x; e0 < count; e0 += MT * U) {
@@ -273,15 +289,16 @@ __global__ void __launch_bounds__(MT) evict_copy_kernel(const EvictArgs a, int p
 
 // In place: CTA (list, K or V, 64-byte column). 4 threads a row, 64 U rows a chunk, the next chunk
 // loaded before the current one is written.
-__global__ void __launch_bounds__(MT) evict_shift_kernel(const EvictArgs a, int cols) {
+__global__ void __launch_bounds__(MT) evict_shift_kernel(const EvictArgs a, const __grid_constant__ InlineInts inl, int cols) {
   griddep_launch_dependents();
   griddep_wait();
   constexpr int U = 8, RPC = MT / 4 * U;
   const int col = blockIdx.x % cols, sel = blockIdx.x / cols % 2, li = blockIdx.x / cols / 2;
-  const List l = list_at(a, li);
+  const Pools pools(a, inl);
+  const List l = list_at(a, pools, li);
   const int* kept = a.kept + (size_t)li * a.keep;
   const int m = min(l.n, a.keep);
-  unsigned char* pool = (sel ? a.v : a.k)[a.first_cache + l.c];
+  unsigned char* pool = sel ? pools.v(a.first_cache + l.c) : pools.k(a.first_cache + l.c);
   const size_t at = col * 64 + threadIdx.x % 4 * 16;  // this thread's 16 bytes of a row
   uint4 x[U], y[U];
   auto row_off = [&](const int* bt, int width, int j) {
@@ -319,7 +336,7 @@ __global__ void __launch_bounds__(MT) evict_shift_kernel(const EvictArgs a, int 
 
 }  // namespace
 
-cudaError_t launch_evict(const EvictArgs& a, int max_len, cudaStream_t s) {
+cudaError_t launch_evict(const EvictArgs& a, const InlineInts& inl, int max_len, cudaStream_t s) {
   const long long lists = (long long)a.num_caches * a.P * a.n_kv;
   const int parts = (int)(((long long)a.keep * a.row_bytes + kPartBytes - 1) / kPartBytes);
   const int cols = a.row_bytes / 64;
@@ -330,10 +347,10 @@ cudaError_t launch_evict(const EvictArgs& a, int max_len, cudaStream_t s) {
   cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void*>(evict_select_kernel), kSelectSmemKeys * 4, once);
   if (e != cudaSuccess) return e;
   const int in_smem = max_len <= kSelectSmemKeys;
-  e = launch_pdl(evict_select_kernel, dim3((unsigned)lists), dim3(ET), in_smem ? (size_t)(max_len + 15) / 16 * 64 : 0, s, a, in_smem);
+  e = launch_pdl(evict_select_kernel, dim3((unsigned)lists), dim3(ET), in_smem ? (size_t)(max_len + 15) / 16 * 64 : 0, s, a, inl, in_smem);
   if (e != cudaSuccess) return e;
-  if (a.in_place) return launch_pdl(evict_shift_kernel, dim3((unsigned)ctas), dim3(MT), 0, s, a, cols);
-  return launch_pdl(evict_copy_kernel, dim3((unsigned)ctas), dim3(MT), 0, s, a, parts);
+  if (a.in_place) return launch_pdl(evict_shift_kernel, dim3((unsigned)ctas), dim3(MT), 0, s, a, inl, cols);
+  return launch_pdl(evict_copy_kernel, dim3((unsigned)ctas), dim3(MT), 0, s, a, inl, parts);
 }
 
 }  // namespace skv

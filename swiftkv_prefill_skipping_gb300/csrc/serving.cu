@@ -134,6 +134,13 @@ int put(std::vector<int>* ints, const std::vector<int>& v) {
   return at;
 }
 
+// The lists for the kernels' parameters (nothing of them where they were uploaded).
+InlineInts inline_of(const std::vector<int>& ints, const int* dev) {
+  InlineInts r;
+  if (!dev) memcpy(r.v, ints.data(), ints.size() * 4);
+  return r;
+}
+
 void place_expansion(const swiftkv_model* m, Arena* a, int pages, const Batch& b, bool with_v, KVExpansion* e) {
   if (pages <= 0) return;
   const size_t rows = (size_t)pages * m->cfg.n_kv * kPageSize;
@@ -237,7 +244,7 @@ int AttendPlan::make(const swiftkv_model* m, const int32_t* cu, const int32_t* c
 
 void AttendPlan::place(const swiftkv_model* m, Arena* a) {
   const auto& c = m->cfg;
-  dev = a->take<int>(ints.size());
+  dev = num_tiles > 0 || ints.size() > kInlineInts ? a->take<int>(ints.size()) : nullptr;
   part = a->take<float>(num_units > num_items ? (size_t)num_units * c.n_kv * max_cols * (c.d_head + 4) : 0);
   v_tail = nullptr;
   if (tc && num_tiles > 0 && !b.fp8)
@@ -246,7 +253,7 @@ void AttendPlan::place(const swiftkv_model* m, Arena* a) {
 }
 
 int AttendPlan::upload(cudaStream_t s) const {
-  CK(upload_ints(dev, ints.data(), (int)ints.size(), s));
+  if (dev) CK(upload_ints(dev, ints.data(), (int)ints.size(), s));
   return SWIFTKV_OK;
 }
 
@@ -295,9 +302,10 @@ int AttendPlan::run(swiftkv_model* m, const swiftkv_kv_pages* kv, int c, const b
     r.bt = kv->block_table;
     r.max_pages = b.max_pages;
     r.num_pages = kv->num_pages;
-    r.items = dev + o_items;
-    r.units = dev + o_units;
-    r.ubeg = dev + o_ubeg;
+    r.lists = dev;
+    r.o_items = o_items;
+    r.o_units = o_units;
+    r.o_ubeg = o_ubeg;
     r.num_units = num_units;
     r.max_cols = max_cols;
     r.n_q = g.n_q;
@@ -310,7 +318,7 @@ int AttendPlan::run(swiftkv_model* m, const swiftkv_kv_pages* kv, int c, const b
     r.ldl = ldl;
     r.part = part;
     r.status = m->status;
-    e = launch_attn_rows(r, kv->k_pool[c], kv->v_pool[c], b.fp8 ? static_cast<const float*>(kv->k_scale[c]) : nullptr,
+    e = launch_attn_rows(r, inline_of(ints, dev), kv->k_pool[c], kv->v_pool[c], b.fp8 ? static_cast<const float*>(kv->k_scale[c]) : nullptr,
                          b.fp8 ? static_cast<const float*>(kv->v_scale[c]) : nullptr, g.d_head, num_items, m->num_sms, s);
   }
   if (e != cudaSuccess)
@@ -377,12 +385,12 @@ int WeightsPlan::make(const swiftkv_model* m, const int32_t* cu, const int32_t* 
 }
 
 void WeightsPlan::place(const swiftkv_model* m, Arena* a) {
-  dev = a->take<int>(ints.size());
+  dev = num_tiles > 0 || ints.size() > kInlineInts ? a->take<int>(ints.size()) : nullptr;
   place_expansion(m, a, num_exp, b, false, &exp);
 }
 
 int WeightsPlan::upload(cudaStream_t s) const {
-  CK(upload_ints(dev, ints.data(), (int)ints.size(), s));
+  if (dev) CK(upload_ints(dev, ints.data(), (int)ints.size(), s));
   return SWIFTKV_OK;
 }
 
@@ -398,8 +406,10 @@ int WeightsPlan::run(swiftkv_model* m, const swiftkv_kv_pages* kv, int c, const 
   a.bt = kv->block_table;
   a.max_pages = b.max_pages;
   a.num_pages = kv->num_pages;
-  a.cu = dev + o_cu;
-  a.ctx = dev + o_ctx;
+  a.lists = dev;
+  a.o_cu = o_cu;
+  a.o_ctx = o_ctx;
+  a.o_units = o_units;
   a.window = b.window;
   a.sinks = b.sinks;
   a.n_q = g.n_q;
@@ -409,13 +419,13 @@ int WeightsPlan::run(swiftkv_model* m, const swiftkv_kv_pages* kv, int c, const 
   a.status = m->status;
   cudaError_t e = cudaSuccess;
   if (num_units > 0)
-    e = launch_weights_rows(a, b.fp8 ? nullptr : static_cast<const bf16*>(kv->k_pool[c]),
+    e = launch_weights_rows(a, inline_of(ints, dev), b.fp8 ? nullptr : static_cast<const bf16*>(kv->k_pool[c]),
                             b.fp8 ? static_cast<const uint8_t*>(kv->k_pool[c]) : nullptr,
                             b.fp8 ? static_cast<const float*>(kv->k_scale[c]) : nullptr, g.d_head, max_cols,
-                            dev + o_units, num_units, m->num_sms, s);
+                            num_units, m->num_sms, s);
   if (e == cudaSuccess && num_tiles > 0) {
     if (b.fp8) {
-      RET(expand(m, kv, c, b, dev + o_exp, num_exp, a.cu, a.ctx, exp, s));
+      RET(expand(m, kv, c, b, dev + o_exp, num_exp, dev + o_cu, dev + o_ctx, exp, s));
       e = launch_weights_tc(a, exp.k, exp.k_scale, exp.block_table, num_exp, g.d_head, dev + o_tiles, num_tiles,
                             m->num_sms, s);
     } else {
@@ -538,7 +548,7 @@ int swiftkv_evict(swiftkv_model* m, int cache, const swiftkv_kv_pages* kv, float
   }
   OnDevice on_device(m);
   cudaStream_t s = (cudaStream_t)stream;
-  // lengths and the caches' pool pointers in one upload
+  // lengths and the caches' pool pointers in one list
   const bool fp8 = kv->kv_dtype == 1;
   std::vector<int> ints(seq_lens, seq_lens + P);
   if (ints.size() % 2) ints.push_back(0);
@@ -551,13 +561,18 @@ int swiftkv_evict(swiftkv_model* m, int cache, const swiftkv_kv_pages* kv, float
   for (int c = 0; fp8 && c < m->C; ++c) ptrs.push_back(kv->v_scale[c]);
   ints.resize(at + 2 * ptrs.size());
   memcpy(ints.data() + at, ptrs.data(), ptrs.size() * 8);
-  Arena arena;
-  RET(reserve(m, ints.size() * 4, s, &arena));
-  int* dev = arena.take<int>(ints.size());
-  CK(upload_ints(dev, ints.data(), (int)ints.size(), s));
-  unsigned char* const* pools = reinterpret_cast<unsigned char* const*>(dev + at);
+  int* dev = nullptr;
+  if (ints.size() > kInlineInts) {
+    Arena arena;
+    RET(reserve(m, ints.size() * 4, s, &arena));
+    dev = arena.take<int>(ints.size());
+    CK(upload_ints(dev, ints.data(), (int)ints.size(), s));
+  }
   EvictArgs a;
-  a.lens = dev;
+  a.lists = dev;
+  a.o_ptrs = (int)at;
+  a.num_ptrs = m->C;
+  a.fp8 = fp8;
   a.P = P;
   a.first_cache = first;
   a.num_caches = C;
@@ -571,15 +586,10 @@ int swiftkv_evict(swiftkv_model* m, int cache, const swiftkv_kv_pages* kv, float
   a.keep = keep;
   a.sinks = sinks;
   a.recent = recent;
-  a.k = pools;
-  a.v = pools + m->C;
-  a.scores = reinterpret_cast<float* const*>(pools + 2 * m->C);
-  a.ks = fp8 ? reinterpret_cast<float* const*>(pools + 3 * m->C) : nullptr;
-  a.vs = fp8 ? reinterpret_cast<float* const*>(pools + 4 * m->C) : nullptr;
   a.kept = kept;
   a.status = m->status;
   a.in_place = !dst_block_table;
-  const cudaError_t e = launch_evict(a, longest, s);
+  const cudaError_t e = launch_evict(a, inline_of(ints, dev), longest, s);
   if (e != cudaSuccess)
     return fail(e == cudaErrorNotSupported ? SWIFTKV_EUNSUPPORTED : SWIFTKV_ECUDA, "evict: %s", cudaGetErrorString(e));
   return SWIFTKV_OK;

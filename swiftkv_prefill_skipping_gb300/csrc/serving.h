@@ -10,6 +10,15 @@
 
 namespace skv {
 
+// Host lists of a small call travel in the kernels' parameters instead of an upload of their own
+// (which costs a launch: 2 us of a 26 us decode attention, a third of a tiny one). A kernel that may
+// get them so reads its lists at list_base(dev, inl) + offset.
+constexpr int kInlineInts = 1000;
+struct alignas(16) InlineInts {
+  int v[kInlineInts];
+};
+__device__ __forceinline__ const int* list_base(const int* dev, const InlineInts& inl) { return dev ? dev : inl.v; }
+
 // Bump allocator over the model's operator workspace: sized by a first pass without a base.
 struct Arena {
   char* base = nullptr;
@@ -40,7 +49,7 @@ struct AttendPlan {
   std::vector<int> ints;
   int o_cu = 0, o_ctx = 0, o_tiles = 0, o_items = 0, o_units = 0, o_ubeg = 0, o_exp = 0;
   int num_tiles = 0, num_items = 0, max_cols = 0, num_units = 0, num_exp = 0;
-  // device
+  // device (lists: null where the kernels take them inline)
   int* dev = nullptr;
   float* part = nullptr;
   bf16* v_tail = nullptr;
@@ -88,7 +97,8 @@ struct RowsArgs {
   int ldq;
   const int* bt;
   int max_pages, num_pages;
-  const int *items, *units, *ubeg;
+  const int* lists;  // null: inline
+  int o_items, o_units, o_ubeg;
   int num_units, max_cols;
   int n_q, n_kv;
   int window, sinks;
@@ -99,7 +109,7 @@ struct RowsArgs {
   float* part;
   int* status;
 };
-cudaError_t launch_attn_rows(const RowsArgs& a, const void* k, const void* v, const float* k_scale, const float* v_scale,
+cudaError_t launch_attn_rows(const RowsArgs& a, const InlineInts& inl, const void* k, const void* v, const float* k_scale, const float* v_scale,
                              int d_head, int num_items, int num_sms, cudaStream_t s);
 struct WeightsArgs {
   const bf16* q;
@@ -108,7 +118,8 @@ struct WeightsArgs {
   int ldl;
   const int* bt;
   int max_pages, num_pages;
-  const int *cu, *ctx;
+  const int* lists;  // null: inline (rows kernel only)
+  int o_cu, o_ctx, o_units;
   int window, sinks;
   int n_q, n_kv;
   float decay;
@@ -119,27 +130,28 @@ struct WeightsArgs {
 // keys), one warp per unit and KV head at a time. FP8 cache: codes and scales of K.
 constexpr int kWeightCols = 32;
 constexpr int kWeightWarps = 12;  // warps per SM that walk units
-cudaError_t launch_weights_rows(const WeightsArgs& a, const bf16* k, const uint8_t* k8, const float* k_scale, int d_head,
-                                int max_cols, const int* units, int num_units, int num_sms, cudaStream_t s);
+cudaError_t launch_weights_rows(const WeightsArgs& a, const InlineInts& inl, const bf16* k, const uint8_t* k8,
+                                const float* k_scale, int d_head, int max_cols, int num_units, int num_sms,
+                                cudaStream_t s);
 // Longer chunks on tcgen05: tiles [2 * num_tiles] = (sequence, 128-key tile), heaviest first. FP8:
 // k / k_scale are an expansion (pages named by a.bt's counterpart `bt_k` of the same shape).
 cudaError_t launch_weights_tc(const WeightsArgs& a, const bf16* k, const float* k_scale, const int* bt_k, int pages_k,
                               int d_head, const int* tiles, int num_tiles, int num_sms, cudaStream_t s);
 
 struct EvictArgs {
-  const int* lens;          // [P] keys each sequence holds
+  const int* lists;         // null: inline; [0, P): keys each sequence holds, then at o_ptrs the
+  int o_ptrs, num_ptrs;     // pools of all num_ptrs caches: K, V, scores and, for FP8, both scales
   int P, first_cache, num_caches;
   int n_kv, row_bytes;      // bytes of one K or V row
   const int *src_bt, *dst_bt;
   int src_pages, dst_pages; // pages per block-table row
   int num_pages;
   int keep, sinks, recent;
-  unsigned char* const *k, *const *v;  // device arrays over all caches
-  float* const *ks, *const *vs, *const *scores;  // ks / vs null for bf16
+  bool fp8;
   int* kept;                // [num_caches][P][n_kv][keep]
   int* status;
   bool in_place;
 };
-cudaError_t launch_evict(const EvictArgs& a, int max_len, cudaStream_t s);
+cudaError_t launch_evict(const EvictArgs& a, const InlineInts& inl, int max_len, cudaStream_t s);
 
 }  // namespace skv
