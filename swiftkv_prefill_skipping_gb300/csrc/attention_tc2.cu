@@ -454,12 +454,25 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc2_kernel(
         bool interior = key0 + BKV - 1 <= I.c0 + q0 && key0 + BKV <= I.nk;  // no key masked in any row
         if (EXT)
           interior = interior && (ext.window <= 0 || key0 > I.c0 + q0 + BQ - 1 - ext.window || key0 + BKV <= ext.sinks);
-        if (!interior) {
+        if (EXT && !interior) {
+          // the block's visible keys as 64 bits: [first, last] of the window, and the sinks
+          const int last = min(qpos, I.nk - 1) - key0, first = window_begin(qpos, ext.window) - key0;
+          unsigned long long in = 0;
+          if (last >= 0) {
+            in = last >= BKV - 1 ? ~0ull : (2ull << last) - 1;
+            const int sink = ext.window > 0 ? ext.sinks - key0 : 0;
+            if (first > 0)
+              in &= (first >= BKV ? 0ull : ~0ull << first) | (sink <= 0 ? 0ull : sink >= BKV ? ~0ull : (1ull << sink) - 1);
+          }
+          const uint32_t in0 = (uint32_t)in, in1 = (uint32_t)(in >> 32);
+#pragma unroll
+          for (int i = 0; i < BKV; ++i)
+            if (!((i < 32 ? in0 : in1) >> (i & 31) & 1u)) sc[i] = -INFINITY;
+        } else if (!interior) {
 #pragma unroll
           for (int i = 0; i < BKV; ++i) {
             const int key = key0 + i;
-            const bool in = EXT ? attn_visible(key, qpos, ext.window, ext.sinks) : key <= qpos;
-            if (!in || key >= I.nk) sc[i] = -INFINITY;
+            if (key > qpos || key >= I.nk) sc[i] = -INFINITY;
           }
         }
         // row max and row sum over 8 independent partials (short dependency chains), combined
