@@ -23,14 +23,13 @@ namespace {
 
 constexpr int ABQ = 64, ABKV = 64, ATHREADS = 128;
 
-// EXT: window, sinks and the row's log-sum-exp (AttnExt).
-template <int D, bool EXT>
+template <int D>
 __global__ void __launch_bounds__(ATHREADS) attn_prefill_kernel(
     const bf16* __restrict__ q, int ldq, const bf16* __restrict__ kpool, const bf16* __restrict__ vpool,
     const float* __restrict__ kscale, const float* __restrict__ vscale,
     const int* __restrict__ bt, int max_pages, int num_pages, const int* __restrict__ cu,
     const int* __restrict__ ctx, const int* __restrict__ tiles, int n_q, int n_kv, bf16* __restrict__ out, int ldo,
-    float scale_log2, const AttnExt ext) {
+    float scale_log2) {
   constexpr int CH = D / 8;  // 16-byte chunks per row
   __shared__ float s_scale[2][2][ABKV];  // FP8 cache: [buffer][key, value][key of the block]
   const bool fp8 = kscale != nullptr;
@@ -58,24 +57,19 @@ __global__ void __launch_bounds__(ATHREADS) attn_prefill_kernel(
     cp_async16(smem_u32(sQ + swz(r, ch)), src, ok ? 16 : 0);
   }
 
-  // keys that some row of the tile may see: [0, sinks) and [w0, ..)
-  const int w0 = EXT ? window_begin(c0 + q0, ext.window) : 0;
-  const int wsinks = EXT && ext.window > 0 ? ext.sinks : 0;
-  auto needed = [&](int key) { return !EXT || key >= w0 || key < wsinks; };  // others are staged as zeros
   auto load_kv = [&](int buf, int kb) {
     for (int c = tid; c < ABKV * CH; c += ATHREADS) {
       int r = c / CH, ch = c % CH;
       int key = kb * ABKV + r;
-      int page = key < nk && needed(key) ? bt[(size_t)s * max_pages + (key >> 4)] : -1;
+      int page = key < nk ? bt[(size_t)s * max_pages + (key >> 4)] : -1;
       bool ok = page >= 0 && page < num_pages;
-      if (EXT && !ok && ch == 0 && key < nk && needed(key)) atomicOr(ext.status, kStatusBadPage);
       size_t off = ok ? (((size_t)page * n_kv + kvh) * kPageSize + (key & 15)) * D + ch * 8 : 0;
       cp_async16(smem_u32(sK + buf * ABKV * D + swz(r, ch)), kpool + off, ok ? 16 : 0);
       cp_async16(smem_u32(sV + buf * ABKV * D + swz(r, ch)), vpool + off, ok ? 16 : 0);
     }
     if (fp8 && tid < ABKV) {  // this block's scales (keys past the chunk or off the pool: 1)
       const int key = kb * ABKV + tid;
-      const int page = key < nk && needed(key) ? bt[(size_t)s * max_pages + (key >> 4)] : -1;
+      const int page = key < nk ? bt[(size_t)s * max_pages + (key >> 4)] : -1;
       const bool ok = page >= 0 && page < num_pages;
       const size_t si = ((size_t)page * n_kv + kvh) * kPageSize + (key & 15);
       s_scale[buf][0][tid] = ok ? kscale[si] : 1.f;
@@ -84,12 +78,8 @@ __global__ void __launch_bounds__(ATHREADS) attn_prefill_kernel(
   };
 
   const int kv_end = min(nk, c0 + q0 + ABQ);  // keys needed: [0, kv_end)
-  const int nend = (kv_end + ABKV - 1) / ABKV;
-  // blocks read: the sinks', then those from the first row's window on
-  const int nsink = min(nend, (wsinks + ABKV - 1) / ABKV), nwin = max(nsink, w0 / ABKV);
-  const int nkv = nsink + max(0, nend - nwin);
-  auto block = [&](int i) { return !EXT || i < nsink ? i : nwin + i - nsink; };
-  load_kv(0, block(0));
+  const int nkv = (kv_end + ABKV - 1) / ABKV;
+  load_kv(0, 0);
   cp_async_commit();
 
   uint32_t qf[D / 16][4];
@@ -103,13 +93,12 @@ __global__ void __launch_bounds__(ATHREADS) attn_prefill_kernel(
   const int qa = q0 + ra, qb = qa + 8;            // rows within the chunk
   const int pa_ = c0 + qa, pb_ = c0 + qb;          // their positions
 
-  for (int it = 0; it < nkv; ++it) {
-    const int kb = block(it);
-    if (it + 1 < nkv) load_kv((it + 1) & 1, block(it + 1));
+  for (int kb = 0; kb < nkv; ++kb) {
+    if (kb + 1 < nkv) load_kv((kb + 1) & 1, kb + 1);
     cp_async_commit();
     cp_async_wait<1>();
     __syncthreads();
-    if (it == 0) {
+    if (kb == 0) {
 #pragma unroll
       for (int ks = 0; ks < D / 16; ++ks) {
         int row = warp * 16 + (lane & 15);
@@ -117,10 +106,10 @@ __global__ void __launch_bounds__(ATHREADS) attn_prefill_kernel(
         ldmatrix_x4(smem_u32(sQ + swz(row, ch)), qf[ks][0], qf[ks][1], qf[ks][2], qf[ks][3]);
       }
     }
-    const bf16* kb_s = sK + (it & 1) * ABKV * D;
-    const bf16* vb_s = sV + (it & 1) * ABKV * D;
-    const float* ksc = s_scale[it & 1][0];
-    const float* vsc = s_scale[it & 1][1];
+    const bf16* kb_s = sK + (kb & 1) * ABKV * D;
+    const bf16* vb_s = sV + (kb & 1) * ABKV * D;
+    const float* ksc = s_scale[kb & 1][0];
+    const float* vsc = s_scale[kb & 1][1];
     float sc[ABKV / 8][4];
 #pragma unroll
     for (int i = 0; i < ABKV / 8; ++i)
@@ -147,10 +136,8 @@ __global__ void __launch_bounds__(ATHREADS) attn_prefill_kernel(
       for (int e = 0; e < 2; ++e) {
         int k = key + e;
         const float ks = fp8 ? ksc[k - kb * ABKV] : 1.f;  // FP8: the key's scale
-        const bool ina = EXT ? k < nk && attn_visible(k, pa_, ext.window, ext.sinks) : k <= pa_ && k < nk;
-        const bool inb = EXT ? k < nk && attn_visible(k, pb_, ext.window, ext.sinks) : k <= pb_ && k < nk;
-        float va = ina ? sc[nb][e] * ks * scale_log2 : -INFINITY;
-        float vb = inb ? sc[nb][2 + e] * ks * scale_log2 : -INFINITY;
+        float va = (k <= pa_ && k < nk) ? sc[nb][e] * ks * scale_log2 : -INFINITY;
+        float vb = (k <= pb_ && k < nk) ? sc[nb][2 + e] * ks * scale_log2 : -INFINITY;
         sc[nb][e] = va;
         sc[nb][2 + e] = vb;
         mx_a = fmaxf(mx_a, va);
@@ -226,11 +213,6 @@ __global__ void __launch_bounds__(ATHREADS) attn_prefill_kernel(
     l_b += __shfl_xor_sync(0xffffffffu, l_b, off);
   }
   const float ia = 1.f / l_a, ib = 1.f / l_b;
-  if (EXT && ext.lse && (lane & 3) == 0) {
-    float* lrow = ext.lse + (size_t)h * ext.ldl + seq0;
-    if (qa < n) lrow[qa] = (m_a + log2f(l_a)) * 0.69314718055994531f;
-    if (qb < n) lrow[qb] = (m_b + log2f(l_b)) * 0.69314718055994531f;
-  }
 #pragma unroll
   for (int db = 0; db < D / 8; ++db) {
     int col = h * D + db * 8 + 2 * (lane & 3);
@@ -392,22 +374,21 @@ __global__ void __launch_bounds__(DTHREADS) attn_decode_kernel(
   }
 }
 
-template <int D, bool EXT>
+template <int D>
 cudaError_t prefill_d(const bf16* q, int ldq, const bf16* k_pool, const bf16* v_pool, const float* k_scale,
                       const float* v_scale, const int* bt, int max_pages, int num_pages, const int* cu,
                       const int* ctx, const int* tiles, int num_tiles, int n_q, int n_kv, bf16* out, int ldo,
-                      cudaStream_t stream, const AttnExt& ext) {
+                      cudaStream_t stream) {
   constexpr int smem = (ABQ + 4 * ABKV) * D * 2;
   static PerDeviceOnce smem_attr;
   {
-    cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void*>(attn_prefill_kernel<D, EXT>), smem, smem_attr);
+    cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void*>(attn_prefill_kernel<D>), smem, smem_attr);
     if (e != cudaSuccess) return e;
   }
   const float scale_log2 = 1.4426950408889634f / sqrtf((float)D);
   dim3 grid(num_tiles, n_q);
-  attn_prefill_kernel<D, EXT><<<grid, ATHREADS, smem, stream>>>(q, ldq, k_pool, v_pool, k_scale, v_scale, bt,
-                                                                max_pages, num_pages, cu, ctx, tiles, n_q, n_kv, out,
-                                                                ldo, scale_log2, ext);
+  attn_prefill_kernel<D><<<grid, ATHREADS, smem, stream>>>(q, ldq, k_pool, v_pool, k_scale, v_scale, bt, max_pages,
+                                                          num_pages, cu, ctx, tiles, n_q, n_kv, out, ldo, scale_log2);
   return cudaGetLastError();
 }
 
@@ -417,16 +398,15 @@ cudaError_t launch_attention_prefill(const bf16* q, int ldq, const bf16* k_pool,
                                      const float* k_scale, const float* v_scale,
                                      const int* block_table, int max_pages, int num_pages,
                                      const int* cu, const int* ctx, const int* tiles, int num_tiles, int n_q,
-                                     int n_kv, int d_head, bf16* out, int ldo, cudaStream_t stream,
-                                     const AttnExt* ext) {
+                                     int n_kv, int d_head, bf16* out, int ldo, cudaStream_t stream) {
   if (num_tiles <= 0) return cudaSuccess;
   if (!k_scale != !v_scale) return cudaErrorNotSupported;
-  auto run = [&](auto kernel) {
-    return kernel(q, ldq, k_pool, v_pool, k_scale, v_scale, block_table, max_pages, num_pages, cu, ctx, tiles,
-                  num_tiles, n_q, n_kv, out, ldo, stream, ext ? *ext : AttnExt());
-  };
-  if (d_head == 128) return ext ? run(prefill_d<128, true>) : run(prefill_d<128, false>);
-  if (d_head == 64) return ext ? run(prefill_d<64, true>) : run(prefill_d<64, false>);
+  if (d_head == 128)
+    return prefill_d<128>(q, ldq, k_pool, v_pool, k_scale, v_scale, block_table, max_pages, num_pages, cu, ctx,
+                          tiles, num_tiles, n_q, n_kv, out, ldo, stream);
+  if (d_head == 64)
+    return prefill_d<64>(q, ldq, k_pool, v_pool, k_scale, v_scale, block_table, max_pages, num_pages, cu, ctx,
+                         tiles, num_tiles, n_q, n_kv, out, ldo, stream);
   return cudaErrorNotSupported;
 }
 

@@ -40,13 +40,6 @@
 // (float32) before the split, so K and V enter as code x scale without a bf16 rounding of
 // the product. All mbarrier waits are bounded; on a timeout the CTA flags kStatusTimeout,
 // drains its own TMA copies and MMAs, frees TMEM and exits.
-//
-// EXT instances take a sliding window and sinks, and write each row's log-sum-exp (AttnExt). An
-// item then walks the blocks of the sinks and those from its first row's window on; the blocks
-// form one ascending list, so tile A's are still a prefix of it. A row may see nothing of a block
-// (its window begins later): its scores are all -inf and its running max stays where it is. Pages
-// without a visible key are not loaded, and pages of V that the chunk sees in part come from
-// zero-padded copies (launch_v_tail).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -96,24 +89,16 @@ constexpr uint32_t IDESC_O = make_idesc(BQ, D, false, true);  // P (TMEM) x V (M
 // One work item: tile A (query head h, rows q0a..) and tile B (head hb, rows q0b..) of one chunk.
 struct Item {
   int s, h, hb, seq0, n, c0, nk, q0a, q0b, nblk_a, nblk_b, nblk;
-  int nsink, nwin;  // EXT: list entries below nsink are blocks of the sinks, the rest start at block nwin
   bool has_b;
 };
-
-// Keys of list entry j start at block_of(I, j) * BKV.
-template <bool EXT>
-__device__ __forceinline__ int block_of(const Item& I, int j) {
-  return !EXT || j < I.nsink ? j : I.nwin + j - I.nsink;
-}
 
 // This CTA's it-th item. Items are (tile, head) or (tile, head pair) pairs, tile-major over the
 // tile list (sorted heaviest first), so consecutive items share their K/V rows in L2; CTA c
 // takes item c of every round of gridDim.x items, counted from the other end in odd rounds, so
 // every CTA gets a similar total. False past the last item.
-template <bool EXT>
 __device__ __forceinline__ bool item_at(int it, const int* __restrict__ tiles, int n_items, int n_q,
                                         const int* __restrict__ cu, const int* __restrict__ ctx, Item& I,
-                                        bool head_pairs, const AttnExt& ext) {
+                                        bool head_pairs) {
   const int G = gridDim.x, c = blockIdx.x;
   const long long w = (long long)it * G + ((it & 1) ? (G - 1 - c) : c);
   if (w >= n_items) return false;
@@ -142,26 +127,16 @@ __device__ __forceinline__ bool item_at(int it, const int* __restrict__ tiles, i
   }
   I.nblk_a = (min(I.nk, I.c0 + I.q0a + BQ) + BKV - 1) / BKV;
   I.nblk_b = I.has_b ? (min(I.nk, I.c0 + I.q0b + BQ) + BKV - 1) / BKV : 0;
-  if (EXT) {
-    const int end = I.has_b ? I.nblk_b : I.nblk_a, w0 = window_begin(I.c0 + I.q0a, ext.window);
-    I.nsink = w0 > 0 ? min(end, (min(ext.sinks, w0) + BKV - 1) / BKV) : 0;
-    I.nwin = max(I.nsink, w0 / BKV);
-    auto entries = [&](int last) { return min(I.nsink, last) + max(0, last - I.nwin); };
-    I.nblk_a = entries(I.nblk_a);
-    I.nblk_b = entries(I.nblk_b);
-  }
   I.nblk = I.has_b ? I.nblk_b : I.nblk_a;  // blocks loaded (tile B's range covers tile A's)
   return true;
 }
 
-template <bool EXT>
 __global__ void __launch_bounds__(THREADS, 1) attn_tc2_kernel(
     const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-    const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmTail, const float* __restrict__ kscale, const float* __restrict__ vscale,
+    const __grid_constant__ CUtensorMap tmV, const float* __restrict__ kscale, const float* __restrict__ vscale,
     const int* __restrict__ bt, int max_pages, int num_pages, const int* __restrict__ cu,
     const int* __restrict__ ctx, const int* __restrict__ tiles, int n_items, int n_q, int n_kv,
-    bf16* __restrict__ out, int ldo, float scale_log2, int* status, bool head_pairs,
-    const __grid_constant__ AttnExt ext) {
+    bf16* __restrict__ out, int ldo, float scale_log2, int* status, bool head_pairs) {
   extern __shared__ unsigned char smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   unsigned char* smem = smem_raw + ((1024 - (raw & 1023)) & 1023);
@@ -219,19 +194,15 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc2_kernel(
       // Page ids of block j of item X, read from the block table one block ahead of that
       // block's copies, so the reads' latency hides behind the copies of the block before
       auto block_pages = [&](const Item& X, int j, int* pg) {
-        const int w0 = EXT ? window_begin(X.c0 + X.q0a, ext.window) : 0;
 #pragma unroll
         for (int p = 0; p < BKV / kPageSize; ++p) {
-          const int key = block_of<EXT>(X, j) * BKV + p * kPageSize;
-          bool read = key < X.nk;
-          if (EXT) read = read && (key + kPageSize > w0 || key < ext.sinks);
-          pg[p] = read ? bt[(size_t)X.s * max_pages + (key >> 4)] : -1;
-          if (EXT && read && (pg[p] < 0 || pg[p] >= num_pages)) atomicOr(status, kStatusBadPage);
+          const int key = j * BKV + p * kPageSize;
+          pg[p] = key < X.nk ? bt[(size_t)X.s * max_pages + (key >> 4)] : -1;
         }
       };
       int kv_i = 0;  // K/V blocks loaded so far (all items): ring stage and phase
       bool ok = true;
-      bool have = item_at<EXT>(0, tiles, n_items, n_q, cu, ctx, I, head_pairs, ext);
+      bool have = item_at(0, tiles, n_items, n_q, cu, ctx, I, head_pairs);
       int pg[BKV / kPageSize], pgn[BKV / kPageSize];
 #pragma unroll
       for (int p = 0; p < BKV / kPageSize; ++p) pg[p] = pgn[p] = -1;
@@ -250,10 +221,8 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc2_kernel(
           tma_load_2d(sQ + t * Q_BYTES, &tmQ, hq * D, row, bar(ctl->q_full));
           tma_load_2d(sQ + t * Q_BYTES + Q_BYTES / 2, &tmQ, hq * D + 64, row, bar(ctl->q_full));
         }
-        TailPages tail;
-        if (EXT) tail = tail_pages(I.c0, I.n, ext.window, ext.sinks);
         Item N;
-        const bool have_next = item_at<EXT>(it + 1, tiles, n_items, n_q, cu, ctx, N, head_pairs, ext);
+        const bool have_next = item_at(it + 1, tiles, n_items, n_q, cu, ctx, N, head_pairs);
         for (int j = 0; j < I.nblk; ++j, ++kv_i) {
           const int stage = kv_i % KV_STAGES;
           const uint32_t phase = (uint32_t)((kv_i / KV_STAGES) & 1);
@@ -275,21 +244,10 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc2_kernel(
             const bool valid = page >= 0 && page < num_pages;
             // a page outside the pool reads rows past the tensor's end: TMA fills zeros
             const int row = valid ? (page * n_kv + kvh) * kPageSize : pool_rows;
-            const CUtensorMap* vmap = &tmV;
-            int vrow = row;
-            if (EXT && ext.v_tail && valid) {
-              const int pidx = block_of<EXT>(I, j) * (BKV / kPageSize) + p;
-#pragma unroll
-              for (int t = 0; t < kTailSlots; ++t)
-                if (pidx == tail.page[t]) {
-                  vmap = &tmTail;
-                  vrow = ((I.s * kTailSlots + t) * n_kv + kvh) * kPageSize;
-                }
-            }
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
               tma_load_2d(sk + hf * KV_HALF + p * 2048, &tmK, hf * 64, row, bar(ctl->kv_full[stage]));
-              tma_load_2d(sv + hf * KV_HALF + p * 2048, vmap, hf * 64, vrow, bar(ctl->kv_full[stage]));
+              tma_load_2d(sv + hf * KV_HALF + p * 2048, &tmV, hf * 64, row, bar(ctl->kv_full[stage]));
             }
             if (fp8) {  // the page's 16 key and 16 value scales (page 0's for a page outside the pool)
               const size_t srow = valid ? (size_t)row : (size_t)kvh * kPageSize;
@@ -322,7 +280,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc2_kernel(
       const int t = warp - 1;
       int kv_base = 0, sp = 0, oi = 0;
       bool ok = true;
-      for (int it = 0; ok && item_at<EXT>(it, tiles, n_items, n_q, cu, ctx, I, head_pairs, ext); ++it) {
+      for (int it = 0; ok && item_at(it, tiles, n_items, n_q, cu, ctx, I, head_pairs); ++it) {
         const int nb = t ? I.nblk_b : I.nblk_a;  // blocks this tile reads (0: no tile B)
         // Releases block j's K/V stage for a block this tile does not read. The arrival counts
         // toward that block's phase only once the block has been loaded (kv_full), so it can
@@ -421,7 +379,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc2_kernel(
     int sp = 0;   // S/P blocks of this tile over all items
     int kvb = 0;  // K/V blocks over all items (ring stage of block j: (kvb + j) % KV_STAGES)
     bool ok = true;
-    for (int it = 0; ok && item_at<EXT>(it, tiles, n_items, n_q, cu, ctx, I, head_pairs, ext); kvb += I.nblk, ++it) {
+    for (int it = 0; ok && item_at(it, tiles, n_items, n_q, cu, ctx, I, head_pairs); kvb += I.nblk, ++it) {
       if (t == 1 && !I.has_b) continue;
       const int nb = t ? I.nblk_b : I.nblk_a;
       const int q0 = t ? I.q0b : I.q0a;
@@ -450,28 +408,11 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc2_kernel(
 #pragma unroll
           for (int i = 0; i < BKV; ++i) sc[i] *= kvs[i];
         }
-        const int key0 = block_of<EXT>(I, j) * BKV;
-        bool interior = key0 + BKV - 1 <= I.c0 + q0 && key0 + BKV <= I.nk;  // no key masked in any row
-        if (EXT)
-          interior = interior && (ext.window <= 0 || key0 > I.c0 + q0 + BQ - 1 - ext.window || key0 + BKV <= ext.sinks);
-        if (EXT && !interior) {
-          // the block's visible keys as 64 bits: [first, last] of the window, and the sinks
-          const int last = min(qpos, I.nk - 1) - key0, first = window_begin(qpos, ext.window) - key0;
-          unsigned long long in = 0;
-          if (last >= 0) {
-            in = last >= BKV - 1 ? ~0ull : (2ull << last) - 1;
-            const int sink = ext.window > 0 ? ext.sinks - key0 : 0;
-            if (first > 0)
-              in &= (first >= BKV ? 0ull : ~0ull << first) | (sink <= 0 ? 0ull : sink >= BKV ? ~0ull : (1ull << sink) - 1);
-          }
-          const uint32_t in0 = (uint32_t)in, in1 = (uint32_t)(in >> 32);
-#pragma unroll
-          for (int i = 0; i < BKV; ++i)
-            if (!((i < 32 ? in0 : in1) >> (i & 31) & 1u)) sc[i] = -INFINITY;
-        } else if (!interior) {
+        const bool interior = (j + 1) * BKV - 1 <= I.c0 + q0 && (j + 1) * BKV <= I.nk;  // no key masked in any row
+        if (!interior) {
 #pragma unroll
           for (int i = 0; i < BKV; ++i) {
-            const int key = key0 + i;
+            const int key = j * BKV + i;
             if (key > qpos || key >= I.nk) sc[i] = -INFINITY;
           }
         }
@@ -509,7 +450,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc2_kernel(
           l *= factor;
           m = mn;
         }
-        const float mneg = EXT && m == -INFINITY ? 0.f : -m;  // a row that has seen nothing yet: P = 0
+        const float mneg = -m;
         float ps[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) ps[k] = 0.f;
@@ -536,8 +477,6 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc2_kernel(
       if (ok) {
         tc_fence_after();
         const float inv = 1.f / l;
-        if (EXT && ext.lse && qrow < I.n)
-          ext.lse[(size_t)(t ? I.hb : I.h) * ext.ldl + I.seq0 + qrow] = (m + log2f(l)) * 0.69314718055994531f;
         bf16* dst = out + (size_t)(I.seq0 + min(qrow, I.n - 1)) * ldo + (t ? I.hb : I.h) * D;
 #pragma unroll
         for (int c = 0; c < D; c += 32) {
@@ -597,35 +536,30 @@ cudaError_t launch_attention_prefill_tc2(const bf16* q, int ldq, int T, const bf
                                          const int* block_table, int max_pages, int num_pages, const int* cu,
                                          const int* ctx, const int* tiles, int num_tiles, int n_q, int n_kv,
                                          int d_head, bf16* out, int ldo, int num_sms, int* status,
-                                         cudaStream_t stream, bool head_pairs, const AttnExt* ext) {
+                                         cudaStream_t stream, bool head_pairs) {
   if (num_tiles <= 0) return cudaSuccess;
   // a head pair shares its KV head only when the group size is even
   if (head_pairs && (n_kv < 1 || n_q % n_kv || (n_q / n_kv) % 2)) return cudaErrorNotSupported;
   if (d_head != D || (reinterpret_cast<uintptr_t>(q) & 15) || ldq % 8 || num_sms < 1 || (!k_scale != !v_scale) ||
       (reinterpret_cast<uintptr_t>(k_scale) & 15) || (reinterpret_cast<uintptr_t>(v_scale) & 15))
     return cudaErrorNotSupported;
-  CUtensorMap mq, mk, mv, mt;
+  CUtensorMap mq, mk, mv;
   const int pool_rows = num_pages * n_kv * kPageSize;
   if (!tma_map_bf16_2d(&mq, q, T, n_q * D, ldq, 64, BQ, true) ||
       !tma_map_bf16_2d(&mk, k_pool, pool_rows, D, D, 64, kPageSize, true) ||
       !tma_map_bf16_2d(&mv, v_pool, pool_rows, D, D, 64, kPageSize, true))
     return cudaErrorNotSupported;
-  mt = mv;
-  if (ext && ext->v_tail && !tma_map_bf16_2d(&mt, ext->v_tail, ext->tail_seqs * kTailSlots * n_kv * kPageSize, D, D, 64,
-                                             kPageSize, true))
-    return cudaErrorNotSupported;
+  static PerDeviceOnce smem_attr;
+  {
+    cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void*>(attn_tc2_kernel), SMEM_BYTES, smem_attr);
+    if (e != cudaSuccess) return e;
+  }
   const float scale_log2 = 1.4426950408889634f / sqrtf((float)D);
   const int n_items = num_tiles * (head_pairs ? n_q / 2 : n_q);
-  auto run = [&](auto kernel, PerDeviceOnce& smem_attr) {
-    cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void*>(kernel), SMEM_BYTES, smem_attr);
-    if (e != cudaSuccess) return e;
-    kernel<<<n_items < num_sms ? n_items : num_sms, THREADS, SMEM_BYTES, stream>>>(
-        mq, mk, mv, mt, k_scale, v_scale, block_table, max_pages, num_pages, cu, ctx, tiles, n_items, n_q, n_kv, out,
-        ldo, scale_log2, status, head_pairs, ext ? *ext : AttnExt());
-    return cudaGetLastError();
-  };
-  static PerDeviceOnce plain, extended;
-  return ext ? run(attn_tc2_kernel<true>, extended) : run(attn_tc2_kernel<false>, plain);
+  attn_tc2_kernel<<<n_items < num_sms ? n_items : num_sms, THREADS, SMEM_BYTES, stream>>>(
+      mq, mk, mv, k_scale, v_scale, block_table, max_pages, num_pages, cu, ctx, tiles, n_items, n_q, n_kv, out, ldo,
+      scale_log2, status, head_pairs);
+  return cudaGetLastError();
 }
 
 }  // namespace skv

@@ -141,64 +141,6 @@ cudaError_t launch_argmax(const float* logits, int rows, int V, int* out, cudaSt
 cudaError_t launch_scale_columns(bf16* W, int rows, int K, const float* gamma, cudaStream_t stream);
 
 // ---- attention ---------------------------------------------------------------------------
-// What attention over the paged cache may be given beyond causal visibility. A row at position p
-// sees key j <= p when window == 0 or j > p - window or j < sinks. Pages that hold no visible key
-// are not read, whatever their block-table entry; an entry outside the pool that is needed sets
-// kStatusBadPage. Cached rows past a sequence's end may hold anything, NaN included.
-struct AttnExt {
-  int window = 0, sinks = 0;
-  float* lse = nullptr;       // [n_q][ldl]: natural log of each row's sum of exp(score); may be null
-  int ldl = 0;
-  const bf16* v_tail = nullptr;  // tcgen05 kernel, bf16 cache: launch_v_tail's copies ...
-  int tail_seqs = 0;             // ... of this many sequences
-  int* status = nullptr;
-};
-// First key, past the sinks, that a row at position p sees.
-__host__ __device__ __forceinline__ int window_begin(int p, int window) { return window > 0 && p >= window ? p - window + 1 : 0; }
-__host__ __device__ __forceinline__ bool attn_visible(int key, int p, int window, int sinks) {
-  return key <= p && (window <= 0 || key > p - window || key < sinks);
-}
-// Copies of the pages of V that a chunk sees in part, with the rows that none of its rows sees (past
-// the sequence's end, before the first row's window, between the sinks and it) zero: out
-// [P][kTailSlots][n_kv][16][d_head], slot 0 the last page, 1 the window's first, 2 the sinks' last.
-// The tensor core multiplies whole pages, and a NaN in such a row would reach every output
-// through 0 * NaN.
-constexpr int kTailSlots = 3;
-struct TailPages {
-  int page[kTailSlots];  // page index within the sequence, -1: none
-  int first, end, sinks;
-  __host__ __device__ bool seen(int key) const { return key < end && (key >= first || key < sinks); }
-};
-__host__ __device__ __forceinline__ TailPages tail_pages(int c0, int n, int window, int sinks) {
-  TailPages t;
-  t.end = c0 + n;
-  t.first = window_begin(c0, window);
-  t.sinks = window > 0 && sinks < t.first ? sinks : t.first;
-  t.page[0] = t.end % kPageSize ? t.end / kPageSize : -1;
-  t.page[1] = t.first % kPageSize ? t.first / kPageSize : -1;
-  t.page[2] = t.first > 0 && t.sinks % kPageSize ? t.sinks / kPageSize : -1;
-  return t;
-}
-cudaError_t launch_v_tail(const bf16* v_pool, const int* block_table, int max_pages, int num_pages, const int* cu,
-                          const int* ctx, int P, int n_kv, int d_head, int window, int sinks, bf16* out,
-                          cudaStream_t stream);
-// One FP8 cache, and a dense bf16 copy of the pages a call needs (codes as bf16 values, scales
-// beside them, rows that no row of the sequence's chunk sees as zeros): item i = (sequence, page
-// index) becomes page i, which `dst.block_table`, of the same shape as src's, then names. Dense
-// and per sequence, so that sequences may share pages and the copy is no larger than what is read.
-struct KVPool8 {
-  const uint8_t *k, *v;
-  const float *k_scale, *v_scale;
-  const int* block_table;
-};
-struct KVExpansion {
-  bf16 *k, *v;
-  float *k_scale, *v_scale;
-  int* block_table;
-};
-cudaError_t launch_kv_expand_seen(const int* items, int num_items, const KVPool8& src, int max_pages, int num_pages,
-                                  const int* cu, const int* ctx, int n_kv, int d_head, int window, int sinks,
-                                  const KVExpansion& dst, int* status, cudaStream_t stream);
 // Varlen causal GQA attention of packed prompt chunks against their own paged K/V.
 // tiles: [num_tiles] (seq << 16 | q_tile) 64-row query tiles; cu: [P+1] device; ctx: [P]
 // device or nullptr: cached tokens before each chunk (row i at position ctx[s] + i sees
@@ -210,8 +152,7 @@ cudaError_t launch_attention_prefill(const bf16* q, int ldq, const bf16* k_pool,
                                      const float* k_scale, const float* v_scale,
                                      const int* block_table, int max_pages, int num_pages,
                                      const int* cu, const int* ctx, const int* tiles, int num_tiles, int n_q,
-                                     int n_kv, int d_head, bf16* out, int ldo, cudaStream_t stream,
-                                     const AttnExt* ext = nullptr);
+                                     int n_kv, int d_head, bf16* out, int ldo, cudaStream_t stream);
 // Same on tcgen05 with two 128-row query tiles per CTA sharing every K/V block (d_head 128
 // only), heaviest tiles first. head_pairs (n_q / n_kv even): tiles are 128-row tiles
 // (seq << 16 | tile) and an item is one tile for two query heads of one KV head; otherwise
@@ -221,7 +162,7 @@ cudaError_t launch_attention_prefill_tc2(const bf16* q, int ldq, int T, const bf
                                          const float* k_scale, const float* v_scale, const int* block_table, int max_pages, int num_pages, const int* cu,
                                          const int* ctx, const int* tiles, int num_tiles, int n_q, int n_kv,
                                          int d_head, bf16* out, int ldo, int num_sms, int* status,
-                                         cudaStream_t stream, bool head_pairs, const AttnExt* ext = nullptr);
+                                         cudaStream_t stream, bool head_pairs);
 // Same on tcgen05 (d_head 128 only; cudaErrorNotSupported otherwise). tiles are 128-row tiles;
 // T = rows of q. status receives kStatusTimeout if a bounded wait expires.
 cudaError_t launch_attention_prefill_tc(const bf16* q, int ldq, int T, const bf16* k_pool, const bf16* v_pool,

@@ -10,6 +10,7 @@
 #include "common.cuh"
 #include "launch.h"
 #include "pdl.cuh"
+#include "serving.h"
 
 namespace skv {
 

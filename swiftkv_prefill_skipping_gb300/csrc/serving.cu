@@ -194,9 +194,8 @@ int AttendPlan::make(const swiftkv_model* m, const int32_t* cu, const int32_t* c
                      int window, int sinks) {
   RET(check_batch(m, cu, ctx, P, kv, window, sinks, &b));
   const auto& c = m->cfg;
-  tc = m->attn_impl != 1 && c.d_head == 128;
-  head_pairs = tc && (c.n_q / c.n_kv) % 2 == 0;
-  const int tile_rows = tc ? (head_pairs ? 128 : 256) : 64;
+  head_pairs = (c.n_q / c.n_kv) % 2 == 0;
+  const int tile_rows = head_pairs ? 128 : 256;
   std::vector<int> cuv(cu, cu + P + 1), ctxv(P, 0), tiles, items, ids, exp_items;
   std::vector<Ranges> seen;
   const int G = c.n_q / c.n_kv, group = kRowsCols / G;  // rows of an item of the row kernel
@@ -247,7 +246,7 @@ void AttendPlan::place(const swiftkv_model* m, Arena* a) {
   dev = num_tiles > 0 || ints.size() > kInlineInts ? a->take<int>(ints.size()) : nullptr;
   part = a->take<float>(num_units > num_items ? (size_t)num_units * c.n_kv * max_cols * (c.d_head + 4) : 0);
   v_tail = nullptr;
-  if (tc && num_tiles > 0 && !b.fp8)
+  if (num_tiles > 0 && !b.fp8)
     v_tail = a->take<bf16>((size_t)b.P * kTailSlots * c.n_kv * kPageSize * c.d_head);
   place_expansion(m, a, num_exp, b, true, &exp);
 }
@@ -260,40 +259,44 @@ int AttendPlan::upload(cudaStream_t s) const {
 int AttendPlan::run(swiftkv_model* m, const swiftkv_kv_pages* kv, int c, const bf16* q, int ldq, bf16* out, int ldo,
                     float* lse, int ldl, cudaStream_t s) const {
   const auto& g = m->cfg;
-  AttnExt ext;
-  ext.window = b.window;
-  ext.sinks = b.sinks;
-  ext.lse = lse;
-  ext.ldl = ldl;
-  ext.status = m->status;
-  const int *cu = dev + o_cu, *ctx = dev + o_ctx;
   cudaError_t e = cudaSuccess;
   if (num_tiles > 0) {
+    ChunkArgs t;
     const bf16* k = static_cast<const bf16*>(kv->k_pool[c]);
     const bf16* v = static_cast<const bf16*>(kv->v_pool[c]);
-    const float *ks = nullptr, *vs = nullptr;
-    const int* bt = kv->block_table;
-    int pages = kv->num_pages;
+    t.k_scale = t.v_scale = nullptr;
+    t.bt = kv->block_table;
+    t.num_pages = kv->num_pages;
+    t.v_tail = nullptr;
+    t.tail_seqs = b.P;
+    t.cu = dev + o_cu;
+    t.ctx = dev + o_ctx;
     if (b.fp8) {
-      RET(expand(m, kv, c, b, dev + o_exp, num_exp, cu, ctx, exp, s));
+      RET(expand(m, kv, c, b, dev + o_exp, num_exp, t.cu, t.ctx, exp, s));
       k = exp.k;
       v = exp.v;
-      ks = exp.k_scale;
-      vs = exp.v_scale;
-      bt = exp.block_table;
-      pages = num_exp;
-    } else if (tc) {
-      CK(launch_v_tail(v, bt, b.max_pages, pages, cu, ctx, b.P, g.n_kv, g.d_head, b.window, b.sinks, v_tail, s));
-      ext.v_tail = v_tail;
-      ext.tail_seqs = b.P;
+      t.k_scale = exp.k_scale;
+      t.v_scale = exp.v_scale;
+      t.bt = exp.block_table;
+      t.num_pages = num_exp;
+    } else {
+      CK(launch_v_tail(v, t.bt, b.max_pages, t.num_pages, t.cu, t.ctx, b.P, g.n_kv, g.d_head, b.window, b.sinks, v_tail, s));
+      t.v_tail = v_tail;
     }
-    if (tc)
-      e = launch_attention_prefill_tc2(q, ldq, b.T, k, v, ks, vs, bt, b.max_pages, pages, cu, ctx, dev + o_tiles,
-                                       num_tiles, g.n_q, g.n_kv, g.d_head, out, ldo, m->num_sms, m->status, s,
-                                       head_pairs, &ext);
-    else
-      e = launch_attention_prefill(q, ldq, k, v, ks, vs, bt, b.max_pages, pages, cu, ctx, dev + o_tiles, num_tiles,
-                                   g.n_q, g.n_kv, g.d_head, out, ldo, s, &ext);
+    t.max_pages = b.max_pages;
+    t.tiles = dev + o_tiles;
+    t.num_items = num_tiles * (head_pairs ? g.n_q / 2 : g.n_q);
+    t.head_pairs = head_pairs;
+    t.n_q = g.n_q;
+    t.n_kv = g.n_kv;
+    t.window = b.window;
+    t.sinks = b.sinks;
+    t.out = out;
+    t.ldo = ldo;
+    t.lse = lse;
+    t.ldl = ldl;
+    t.status = m->status;
+    e = launch_attn_chunk(t, q, ldq, b.T, k, v, g.d_head, m->num_sms, s);
   }
   if (e == cudaSuccess && num_items > 0) {
     RowsArgs r;
@@ -327,7 +330,7 @@ int AttendPlan::run(swiftkv_model* m, const swiftkv_kv_pages* kv, int c, const b
 }
 
 int AttendPlan::kernels() const {
-  return (num_tiles > 0 ? 1 + (b.fp8 || tc) : 0) + (num_items > 0 ? 1 + (num_units > num_items) : 0);
+  return (num_tiles > 0 ? 2 : 0) + (num_items > 0 ? 1 + (num_units > num_items) : 0);
 }
 
 // ---------------------------------------------------------------------------- attention weights

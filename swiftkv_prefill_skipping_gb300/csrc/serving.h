@@ -10,6 +10,56 @@
 
 namespace skv {
 
+// A row at position p sees key j <= p when window == 0 or j > p - window or j < sinks. Pages that
+// hold no visible key are not read, whatever their block-table entry; an entry outside the pool that
+// is needed sets kStatusBadPage. Cached rows that no row sees may hold anything, NaN included.
+// First key, past the sinks, that a row at position p sees.
+__host__ __device__ __forceinline__ int window_begin(int p, int window) { return window > 0 && p >= window ? p - window + 1 : 0; }
+__host__ __device__ __forceinline__ bool attn_visible(int key, int p, int window, int sinks) {
+  return key <= p && (window <= 0 || key > p - window || key < sinks);
+}
+// Copies of the pages of V that a chunk sees in part, with the rows that none of its rows sees (past
+// the sequence's end, before the first row's window, between the sinks and it) zero: out
+// [P][kTailSlots][n_kv][16][d_head], slot 0 the last page, 1 the window's first, 2 the sinks' last.
+// The tensor core multiplies whole pages, and a NaN in such a row would reach every output
+// through 0 * NaN.
+constexpr int kTailSlots = 3;
+struct TailPages {
+  int page[kTailSlots];  // page index within the sequence, -1: none
+  int first, end, sinks;
+  __host__ __device__ bool seen(int key) const { return key < end && (key >= first || key < sinks); }
+};
+__host__ __device__ __forceinline__ TailPages tail_pages(int c0, int n, int window, int sinks) {
+  TailPages t;
+  t.end = c0 + n;
+  t.first = window_begin(c0, window);
+  t.sinks = window > 0 && sinks < t.first ? sinks : t.first;
+  t.page[0] = t.end % kPageSize ? t.end / kPageSize : -1;
+  t.page[1] = t.first % kPageSize ? t.first / kPageSize : -1;
+  t.page[2] = t.first > 0 && t.sinks % kPageSize ? t.sinks / kPageSize : -1;
+  return t;
+}
+cudaError_t launch_v_tail(const bf16* v_pool, const int* block_table, int max_pages, int num_pages, const int* cu,
+                          const int* ctx, int P, int n_kv, int d_head, int window, int sinks, bf16* out,
+                          cudaStream_t stream);
+// One FP8 cache, and a dense bf16 copy of the pages a call needs (codes as bf16 values, scales
+// beside them, rows that no row of the sequence's chunk sees as zeros): item i = (sequence, page
+// index) becomes page i, which `dst.block_table`, of the same shape as src's, then names. Dense
+// and per sequence, so that sequences may share pages and the copy is no larger than what is read.
+struct KVPool8 {
+  const uint8_t *k, *v;
+  const float *k_scale, *v_scale;
+  const int* block_table;
+};
+struct KVExpansion {
+  bf16 *k, *v;
+  float *k_scale, *v_scale;
+  int* block_table;
+};
+cudaError_t launch_kv_expand_seen(const int* items, int num_items, const KVPool8& src, int max_pages, int num_pages,
+                                  const int* cu, const int* ctx, int n_kv, int d_head, int window, int sinks,
+                                  const KVExpansion& dst, int* status, cudaStream_t stream);
+
 // Host lists of a small call travel in the kernels' parameters instead of an upload of their own
 // (which costs a launch: 2 us of a 26 us decode attention, a third of a tiny one). A kernel that may
 // get them so reads its lists at list_base(dev, inl) + offset.
@@ -44,7 +94,7 @@ struct Batch {
 
 struct AttendPlan {
   Batch b;
-  bool tc = false, head_pairs = false;
+  bool head_pairs = false;
   // host lists, and their places in one device upload
   std::vector<int> ints;
   int o_cu = 0, o_ctx = 0, o_tiles = 0, o_items = 0, o_units = 0, o_ubeg = 0, o_exp = 0;
@@ -86,7 +136,29 @@ struct WeightsPlan {
   int kernels() const;
 };
 
-// ---- kernels (attn_rows.cu, attn_weights.cu, evict.cu) --------------------------------------
+// ---- kernels (attn_chunk.cu, attn_rows.cu, attn_weights.cu, evict.cu) --------------------------------------
+// Query tiles of longer chunks: tiles (seq << 16 | tile), heaviest first, of 128 rows (head_pairs:
+// an item is a tile for two query heads of one KV head, num_items = tiles * n_q / 2) or of 256 rows
+// (an item is a tile for one head, num_items = tiles * n_q).
+struct ChunkArgs {
+  const float *k_scale, *v_scale;  // FP8: the expansion's scales; else null
+  const int* bt;
+  int max_pages, num_pages;
+  const int *cu, *ctx, *tiles;
+  int num_items;
+  bool head_pairs;
+  int n_q, n_kv;
+  int window, sinks;
+  bf16* out;
+  int ldo;
+  float* lse;              // [n_q][ldl] or null
+  int ldl;
+  const bf16* v_tail;      // bf16 cache: launch_v_tail's copies of tail_seqs sequences
+  int tail_seqs;
+  int* status;
+};
+cudaError_t launch_attn_chunk(const ChunkArgs& a, const bf16* q, int ldq, int T, const bf16* k, const bf16* v, int d_head,
+                              int num_sms, cudaStream_t s);
 // Rows of short chunks: items [4 * n] = (first row, rows, sequence, first position), rows x group <=
 // kRowsCols; units [3 * num_units] = (item, first key, keys) of keys some row sees, item-major; ubeg
 // [n + 1]; part: num_units * n_kv * max_cols records of d_head + 4 floats (several units an item).
