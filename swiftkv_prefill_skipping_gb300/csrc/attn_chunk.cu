@@ -8,19 +8,22 @@
 // position, one ascending list of which tile A needs a prefix. Persistent: one CTA per SM walks its
 // share of the items, heaviest first, alternate rounds reversed.
 //
-// A block is 128 keys. Per tile and block: S = Q K^T (tensor memory, 128 columns), softmax, P over S
-// as bf16, O += P V. Both tiles' S and O fill the 512 columns of tensor memory exactly, so a tile's
-// S has one buffer, and the tiles take turns: while the softmax warps of one work (one thread per
-// row), the tensor core runs the other's two products. Against 64-key blocks with two S buffers
-// (attention_tc2.cu) that halves the number of hand-overs between tensor core and softmax, whose
-// latency is what bounds that kernel. P is rounded once to bf16
+// A block is 80 keys at d_head 128 and 128 keys at 64: per tile, tensor memory then holds the scores S
+// of one block, the weights P of another (bf16, two a column) and O, and both tiles fill its 512
+// columns almost exactly. Because P does not lie over S, S of the next block is issued as soon as
+// the softmax warps have read this block's into registers, and the softmax of one block runs while the
+// tensor core computes the scores of the next and O += P V of the one before. With P over S
+// (128-key blocks) each of the three hand-overs between tensor core and softmax, some 500 cycles, stood
+// in a tile's chain: 691 us for 4 x ~1960 rows after 0 - 6048 keys and 32 heads, 605 of them with
+// the softmax left out. P is rounded once to bf16
 // (at most 2^-8 of a weight and so 2^-8 of sum p |v| in the output, which is itself rounded to bf16
 // with 2^-8 of its value); a second product with the remainders would add half of the tensor work.
 // Row sums use the unrounded weights, in float32.
 //
-// 12 warps: 0 TMA, 1 and 2 the tiles' MMAs, 3 idle, 4-7 and 8-11 softmax of tile A and B with the
-// registers that the first four give up. All mbarrier waits are bounded; when one expires the CTA
-// flags kStatusTimeout, drains its copies and MMAs, frees tensor memory and exits.
+// 12 warps: 0 loads Q and K and 3 loads V by TMA, each with the page ids of a block read one block
+// ahead; 1 and 2 issue the tiles' MMAs; 4-7 and 8-11 are the softmax of tile A and B, one thread per
+// row, with the registers that the first four give up. All mbarrier waits are bounded; when one expires
+// the CTA flags kStatusTimeout, drains its copies and MMAs, frees tensor memory and exits.
 //
 // Pages without a visible key are not loaded (zeros instead), and pages of V that the chunk sees in
 // part come from zero-padded copies (launch_v_tail). FP8: K and V are an expansion to bf16 codes;
@@ -40,41 +43,49 @@ namespace {
 using namespace tc;
 
 constexpr int BQ = 128;                // query rows per tile
-constexpr int BKV = 128;               // keys per block
-constexpr int PAGES = BKV / kPageSize;
-constexpr int ST = 2;                  // K and V stages
 constexpr int THREADS = 384;
 constexpr int REGS_ISSUE = 72, REGS_SOFTMAX = 216;  // 72 + 2 x 216 = 3 x 168, the registers at launch
-constexpr int O_COL = 256;             // tensor memory: S_A 0, S_B 128, O_A 256, O_B 384
 constexpr float kLag = 8.f;            // log2 headroom of the running maximum
 constexpr float kLn2 = 0.69314718055994531f;
 
-struct Ctrl {
-  uint64_t q_full, q_empty, k_full[ST], k_empty[ST], v_full[ST], v_empty[ST];
-  uint64_t s_full[2], p_full[2], pv_done[2], o_empty[2], fin[2];
-  uint32_t tmem_base;
-  int abort;
-  int pend[1 + 2 * ST];                // phases of copies in flight: Q, K stages, V stages
-  alignas(16) float scale[ST][2][BKV];  // FP8: key scales, value scales
-};
-
 template <int D>
 struct Cfg {
+  static constexpr int BKV = D == 128 ? 80 : 128;  // keys per block
+  static constexpr int PAGES = BKV / kPageSize;
+  static constexpr int KST = 3, VST = 3;           // K and V stages
   static constexpr int HALVES = D / 64;
-  static constexpr int HALF = 128 * 128;          // 128 rows x 64 dims
-  static constexpr int TILE = HALVES * HALF;      // Q tile, K block or V block
-  static constexpr int SMEM = 1024 + (2 + 2 * ST) * TILE + (int)sizeof(Ctrl);
+  static constexpr int Q_HALF = BQ * 128, KV_HALF = BKV * 128;  // rows x 64 dims
+  static constexpr int Q_TILE = HALVES * Q_HALF, KV_TILE = HALVES * KV_HALF;
+  // tensor memory columns of a tile: S, P (half as many), O
+  static constexpr int COLS = 256, P_COL = BKV, O_COL = COLS - D;
+  static_assert(P_COL + BKV / 2 <= O_COL && BKV % 16 == 0, "two tiles in 512 columns");
   static constexpr uint32_t IDESC_S = make_idesc(BQ, BKV, false, false);  // Q (K-major) x K (K-major)
   static constexpr uint32_t IDESC_O = make_idesc(BQ, D, false, true);     // P (tensor memory) x V (MN-major)
 };
 
+template <int D>
+struct Ctrl {
+  using C = Cfg<D>;
+  uint64_t q_full, q_empty, k_full[C::KST], k_empty[C::KST], v_full[C::VST], v_empty[C::VST];
+  uint64_t s_full[2], s_empty[2], p_full[2], pv_done[2], o_empty[2], fin[2];
+  uint32_t tmem_base;
+  int abort;
+  int pend[1 + C::KST + C::VST];                  // phases of copies in flight: Q, K stages, V stages
+  alignas(16) float scale[C::VST][2][C::BKV];      // FP8: key scales, value scales
+};
+template <int D>
+constexpr int smem_bytes() {
+  return 1024 + 2 * Cfg<D>::Q_TILE + (Cfg<D>::KST + Cfg<D>::VST) * Cfg<D>::KV_TILE + (int)sizeof(Ctrl<D>);
+}
+
 struct Item {
   int s, h, hb, seq0, n, c0, nk, q0a, q0b, nblk_a, nblk_b, nblk, nsink, nwin;
   bool has_b;
-  // first key of list entry j
-  __device__ __forceinline__ int key0(int j) const { return (j < nsink ? j : nwin + j - nsink) * BKV; }
+  // block of list entry j
+  __device__ __forceinline__ int block(int j) const { return j < nsink ? j : nwin + j - nsink; }
 };
 
+template <int BKV>
 __device__ __forceinline__ bool item_at(int it, const ChunkArgs& a, Item& I) {
   const int G = gridDim.x, c = blockIdx.x;
   const long long w = (long long)it * G + ((it & 1) ? (G - 1 - c) : c);
@@ -110,6 +121,40 @@ __device__ __forceinline__ bool item_at(int it, const ChunkArgs& a, Item& I) {
   return true;
 }
 
+// 16 columns of this thread's tensor-memory lane; a load's registers hold values after tmem_wait16
+__device__ __forceinline__ void tmem_ld16_async(uint32_t addr, float* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]),
+        "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15])
+      : "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait16(float* r) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;\n"
+               : "+f"(r[0]), "+f"(r[1]), "+f"(r[2]), "+f"(r[3]), "+f"(r[4]), "+f"(r[5]), "+f"(r[6]), "+f"(r[7]), "+f"(r[8]),
+                 "+f"(r[9]), "+f"(r[10]), "+f"(r[11]), "+f"(r[12]), "+f"(r[13]), "+f"(r[14]), "+f"(r[15])
+               :
+               : "memory");
+}
+template <int N>
+__device__ __forceinline__ void tmem_ld_row(uint32_t addr, float* x) {
+#pragma unroll
+  for (int c = 0; c < N; c += 16) tmem_ld16_async(addr + c, x + c);
+#pragma unroll
+  for (int c = 0; c < N; c += 16) tmem_wait16(x + c);
+}
+// N (a multiple of 8) 32-bit columns, complete on return
+template <int N>
+__device__ __forceinline__ void tmem_st_row(uint32_t addr, const uint32_t* r) {
+#pragma unroll
+  for (int c = 0; c < N; c += 8)
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"r"(addr + c), "r"(r[c]),
+                 "r"(r[c + 1]), "r"(r[c + 2]), "r"(r[c + 3]), "r"(r[c + 4]), "r"(r[c + 5]), "r"(r[c + 6]), "r"(r[c + 7])
+                 : "memory");
+  asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory");
+}
+
 // d[0 .. 1] = x[0 .. 1] * c + m and acc[0 .. 1] += p[0 .. 1], each one packed fp32 instruction
 __device__ __forceinline__ void fma2(float* d, const float* x, float c, float m) {
   asm("{\n .reg .b64 a, b, e, f;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %4};\n mov.b64 e, {%5, %5};\n"
@@ -131,11 +176,12 @@ __global__ void __launch_bounds__(THREADS, 1) attn_chunk_kernel(const __grid_con
                                                                 const __grid_constant__ CUtensorMap tmTail,
                                                                 const __grid_constant__ ChunkArgs a, float scale_log2) {
   using C = Cfg<D>;
+  constexpr int BKV = C::BKV, PAGES = C::PAGES, KST = C::KST, VST = C::VST;
   extern __shared__ unsigned char smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   unsigned char* smem = smem_raw + ((1024 - (raw & 1023)) & 1023);
-  const uint32_t sQ = smem_u32(smem), sK = sQ + 2 * C::TILE, sV = sK + ST * C::TILE;
-  Ctrl* ctl = reinterpret_cast<Ctrl*>(smem + (2 + 2 * ST) * C::TILE);
+  const uint32_t sQ = smem_u32(smem), sK = sQ + 2 * C::Q_TILE, sV = sK + KST * C::KV_TILE;
+  Ctrl<D>* ctl = reinterpret_cast<Ctrl<D>*>(smem + 2 * C::Q_TILE + (KST + VST) * C::KV_TILE);
   volatile int* abort_flag = &ctl->abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const bool fp8 = a.k_scale != nullptr;
@@ -144,20 +190,23 @@ __global__ void __launch_bounds__(THREADS, 1) attn_chunk_kernel(const __grid_con
   if (threadIdx.x == 0) {
     mbar_init(bar(ctl->q_full), 1);
     mbar_init(bar(ctl->q_empty), 2);
-    for (int i = 0; i < ST; ++i) {
+    for (int i = 0; i < KST; ++i) {
       mbar_init(bar(ctl->k_full[i]), 1);
-      mbar_init(bar(ctl->v_full[i]), 1);
       mbar_init(bar(ctl->k_empty[i]), 2);
+    }
+    for (int i = 0; i < VST; ++i) {
+      mbar_init(bar(ctl->v_full[i]), 1);
       mbar_init(bar(ctl->v_empty[i]), 2);
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(bar(ctl->s_full[t]), 1);
+      mbar_init(bar(ctl->s_empty[t]), 128);
       mbar_init(bar(ctl->p_full[t]), 128);
       mbar_init(bar(ctl->pv_done[t]), 1);
       mbar_init(bar(ctl->o_empty[t]), 128);
       mbar_init(bar(ctl->fin[t]), 1);
     }
-    for (int i = 0; i < 1 + 2 * ST; ++i) ctl->pend[i] = -1;
+    for (int i = 0; i < 1 + KST + VST; ++i) ctl->pend[i] = -1;
     ctl->abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -175,123 +224,146 @@ __global__ void __launch_bounds__(THREADS, 1) attn_chunk_kernel(const __grid_con
 
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_ISSUE));
-    if (warp == 0 && lane == 0) {
-      const int group = a.n_q / a.n_kv, none = a.num_pages * a.n_kv * kPageSize;  // rows past the pool: zeros
-      int kv_i = 0;
-      bool ok = true;
-      for (int it = 0; ok && item_at(it, a, I); ++it) {
-        const int kvh = I.h / group;
-        if (it > 0 && !mbar_wait(bar(ctl->q_empty), (uint32_t)((it - 1) & 1), abort_flag)) break;
-        mbar_expect_tx(bar(ctl->q_full), (I.has_b ? 2 : 1) * C::TILE);
-        ctl->pend[0] = it & 1;
-        for (int t = 0; t < (I.has_b ? 2 : 1); ++t)
+    if ((warp == 0 || warp == 3) && lane == 0) {
+      // warp 0: Q and K, warp 3: V and the scales
+      const bool is_v = warp == 3;
+      const int group = a.n_q / a.n_kv;
+      // page ids of block b of item X (-1: not needed, or outside the pool)
+      auto block_pages = [&](const Item& X, int j, int* pg) {
+        const int w0 = window_begin(X.c0 + X.q0a, a.window), key0 = X.block(j) * BKV;
 #pragma unroll
-          for (int hf = 0; hf < C::HALVES; ++hf)
-            tma_load_2d(sQ + t * C::TILE + hf * C::HALF, &tmQ, (t ? I.hb : I.h) * D + hf * 64,
-                        I.seq0 + (t ? I.q0b : I.q0a), bar(ctl->q_full));
-        const TailPages tail = tail_pages(I.c0, I.n, a.window, a.sinks);
-        const int w0 = window_begin(I.c0 + I.q0a, a.window);
-        for (int j = 0; ok && j < I.nblk; ++j, ++kv_i) {
-          const int st = kv_i % ST;
-          const uint32_t ph = (uint32_t)((kv_i / ST) & 1);
-          const int key0 = I.key0(j);
-          int row[PAGES];
-#pragma unroll
-          for (int p = 0; p < PAGES; ++p) {
-            const int key = key0 + p * kPageSize;
-            row[p] = none;
-            if (key < I.nk && (key + kPageSize > w0 || key < a.sinks)) {
-              const int page = a.bt[(size_t)I.s * a.max_pages + (key >> 4)];
-              if (page >= 0 && page < a.num_pages) row[p] = (page * a.n_kv + kvh) * kPageSize;
-              else atomicOr(a.status, kStatusBadPage);
-            }
+        for (int p = 0; p < PAGES; ++p) {
+          const int key = key0 + p * kPageSize;
+          pg[p] = -1;
+          if (key < X.nk && (key + kPageSize > w0 || key < a.sinks)) {
+            const int page = a.bt[(size_t)X.s * a.max_pages + (key >> 4)];
+            if (page >= 0 && page < a.num_pages) pg[p] = page;
+            else atomicOr(a.status, kStatusBadPage);
           }
-          if (!(ok = mbar_wait(bar(ctl->k_empty[st]), ph ^ 1, abort_flag))) break;
-          mbar_expect_tx(bar(ctl->k_full[st]), C::TILE);
-          ctl->pend[1 + st] = (int)ph;
-#pragma unroll
-          for (int p = 0; p < PAGES; ++p)
+        }
+      };
+      int kv_i = 0, pg[PAGES], next[PAGES];
+      bool ok = true, have = item_at<BKV>(0, a, I);
+      if (have) block_pages(I, 0, pg);
+      for (int it = 0; ok && have; ++it) {
+        Item N;
+        const bool have_next = item_at<BKV>(it + 1, a, N);
+        const int kvh = I.h / group;
+        TailPages tail;
+        if (!is_v) {
+          // Q overwrites the previous item's, once its last S has completed
+          if (it > 0 && !mbar_wait(bar(ctl->q_empty), (uint32_t)((it - 1) & 1), abort_flag)) break;
+          mbar_expect_tx(bar(ctl->q_full), (I.has_b ? 2 : 1) * C::Q_TILE);
+          ctl->pend[0] = it & 1;
+          for (int t = 0; t < (I.has_b ? 2 : 1); ++t)
 #pragma unroll
             for (int hf = 0; hf < C::HALVES; ++hf)
-              tma_load_2d(sK + st * C::TILE + hf * C::HALF + p * 2048, &tmK, hf * 64, row[p], bar(ctl->k_full[st]));
-          if (!(ok = mbar_wait(bar(ctl->v_empty[st]), ph ^ 1, abort_flag))) break;
-          mbar_expect_tx(bar(ctl->v_full[st]), C::TILE + (fp8 ? 2 * BKV * 4 : 0));
-          ctl->pend[1 + ST + st] = (int)ph;
+              tma_load_2d(sQ + t * C::Q_TILE + hf * C::Q_HALF, &tmQ, (t ? I.hb : I.h) * D + hf * 64,
+                          I.seq0 + (t ? I.q0b : I.q0a), bar(ctl->q_full));
+        } else {
+          tail = tail_pages(I.c0, I.n, a.window, a.sinks);
+        }
+        for (int j = 0; j < I.nblk; ++j, ++kv_i) {
+          if (j + 1 < I.nblk) block_pages(I, j + 1, next);
+          else if (have_next) block_pages(N, 0, next);
+          const int st = is_v ? kv_i % VST : kv_i % KST;
+          const uint32_t ph = (uint32_t)((is_v ? kv_i / VST : kv_i / KST) & 1);
+          const uint32_t full = is_v ? bar(ctl->v_full[st]) : bar(ctl->k_full[st]);
+          if (!(ok = mbar_wait(is_v ? bar(ctl->v_empty[st]) : bar(ctl->k_empty[st]), ph ^ 1, abort_flag))) break;
+          mbar_expect_tx(full, C::KV_TILE + (is_v && fp8 ? 2 * BKV * 4 : 0));
+          ctl->pend[is_v ? 1 + KST + st : 1 + st] = (int)ph;
+          const uint32_t dst = (is_v ? sV : sK) + st * C::KV_TILE;
 #pragma unroll
           for (int p = 0; p < PAGES; ++p) {
-            const CUtensorMap* map = &tmV;
-            int vrow = row[p];
-            if (a.v_tail && vrow != none) {
-              const int pidx = key0 / kPageSize + p;
+            // a page that is not needed reads rows past the pool's end: zeros
+            int row = (pg[p] >= 0 ? pg[p] * a.n_kv + kvh : a.num_pages * a.n_kv) * kPageSize;
+            const CUtensorMap* map = is_v ? &tmV : &tmK;
+            if (is_v && fp8) {  // page 0's scales for a page that is not loaded: its keys are masked
+              const size_t sr = pg[p] >= 0 ? (size_t)row : (size_t)kvh * kPageSize;
+              const uint32_t sd = smem_u32(&ctl->scale[st][0][p * kPageSize]);
+              bulk_load(sd, a.k_scale + sr, kPageSize * 4, full);
+              bulk_load(sd + BKV * 4, a.v_scale + sr, kPageSize * 4, full);
+            }
+            if (is_v && a.v_tail && pg[p] >= 0) {
+              const int pidx = I.block(j) * PAGES + p;
 #pragma unroll
               for (int t = 0; t < kTailSlots; ++t)
                 if (pidx == tail.page[t]) {
                   map = &tmTail;
-                  vrow = ((I.s * kTailSlots + t) * a.n_kv + kvh) * kPageSize;
+                  row = ((I.s * kTailSlots + t) * a.n_kv + kvh) * kPageSize;
                 }
             }
 #pragma unroll
-            for (int hf = 0; hf < C::HALVES; ++hf)
-              tma_load_2d(sV + st * C::TILE + hf * C::HALF + p * 2048, map, hf * 64, vrow, bar(ctl->v_full[st]));
-            if (fp8) {  // page 0's scales for a page that is not loaded: its keys are masked
-              const size_t sr = row[p] != none ? (size_t)row[p] : (size_t)kvh * kPageSize;
-              const uint32_t dst = smem_u32(&ctl->scale[st][0][p * kPageSize]);
-              bulk_load(dst, a.k_scale + sr, kPageSize * 4, bar(ctl->v_full[st]));
-              bulk_load(dst + BKV * 4, a.v_scale + sr, kPageSize * 4, bar(ctl->v_full[st]));
-            }
+            for (int hf = 0; hf < C::HALVES; ++hf) tma_load_2d(dst + hf * C::KV_HALF + p * 2048, map, hf * 64, row, full);
           }
+#pragma unroll
+          for (int p = 0; p < PAGES; ++p) pg[p] = next[p];
         }
+        I = N;
+        have = have_next;
       }
     } else if ((warp == 1 || warp == 2) && lane == 0) {
       // tile t's MMAs; g counts its blocks over all items, oi the items that used its O
       const int t = warp - 1;
+      const uint32_t q = sQ + t * C::Q_TILE, base = tmem + t * C::COLS;
       int kv_base = 0, g = 0, oi = 0;
       bool ok = true;
-      for (int it = 0; ok && item_at(it, a, I); ++it) {
+      for (int it = 0; ok && item_at<BKV>(it, a, I); ++it) {
         const int nb = t ? I.nblk_b : I.nblk_a;
         if (!mbar_wait(bar(ctl->q_full), (uint32_t)(it & 1), abort_flag)) break;
         ctl->pend[0] = -1;
         if (nb == 0) mbar_arrive(bar(ctl->q_empty));
-        for (int j = 0; ok && j < I.nblk; ++j) {
-          const int kv = kv_base + j, st = kv % ST;
-          const uint32_t ph = (uint32_t)((kv / ST) & 1);
-          if (!(ok = mbar_wait(bar(ctl->k_full[st]), ph, abort_flag))) break;
+        // S of block j of the item, the tile's block g + j: the softmax has read the one before it
+        auto issue_s = [&](int j) -> bool {
+          const int kv = kv_base + j, st = kv % KST, gj = g + j;
+          if (!mbar_wait(bar(ctl->k_full[st]), (uint32_t)((kv / KST) & 1), abort_flag)) return false;
           ctl->pend[1 + st] = -1;
-          if (j >= nb) {  // a block this tile does not read: only release it, once it has arrived
-            mbar_arrive(bar(ctl->k_empty[st]));
-            if (!(ok = mbar_wait(bar(ctl->v_full[st]), ph, abort_flag))) break;
-            ctl->pend[1 + ST + st] = -1;
-            mbar_arrive(bar(ctl->v_empty[st]));
-            continue;
-          }
-          // the buffer holds P of the previous block until the product that reads it has completed
-          if (g > 0 && !(ok = mbar_wait(bar(ctl->pv_done[t]), (uint32_t)((g - 1) & 1), abort_flag))) break;
+          if (gj > 0 && !mbar_wait(bar(ctl->s_empty[t]), (uint32_t)((gj - 1) & 1), abort_flag)) return false;
           tc_fence_after();
-          const uint32_t k = sK + st * C::TILE, q = sQ + t * C::TILE;
+          const uint32_t k = sK + st * C::KV_TILE;
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t off = (kk >> 2) * C::HALF + (kk & 3) * 32;
-            tc_mma(tmem + t * BKV, sdesc(q + off), sdesc(k + off), C::IDESC_S, kk != 0);
-          }
+          for (int kk = 0; kk < D / 16; ++kk)
+            tc_mma(base, sdesc(q + (kk >> 2) * C::Q_HALF + (kk & 3) * 32),
+                   sdesc(k + (kk >> 2) * C::KV_HALF + (kk & 3) * 32), C::IDESC_S, kk != 0);
           tc_commit(bar(ctl->s_full[t]));
           tc_commit(bar(ctl->k_empty[st]));
           if (j + 1 == nb) tc_commit(bar(ctl->q_empty));
-          if (!(ok = mbar_wait(bar(ctl->v_full[st]), ph, abort_flag))) break;
-          ctl->pend[1 + ST + st] = -1;
-          if (!(ok = mbar_wait(bar(ctl->p_full[t]), (uint32_t)(g & 1), abort_flag))) break;
+          return true;
+        };
+        auto issue_pv = [&](int j) -> bool {
+          const int kv = kv_base + j, st = kv % VST;
+          if (!mbar_wait(bar(ctl->v_full[st]), (uint32_t)((kv / VST) & 1), abort_flag)) return false;
+          ctl->pend[1 + KST + st] = -1;
+          if (!mbar_wait(bar(ctl->p_full[t]), (uint32_t)((g + j) & 1), abort_flag)) return false;
           // the first P V of an item overwrites O: the previous item's output must have left
-          if (j == 0 && oi > 0 && !(ok = mbar_wait(bar(ctl->o_empty[t]), (uint32_t)((oi - 1) & 1), abort_flag))) break;
+          if (j == 0 && oi > 0 && !mbar_wait(bar(ctl->o_empty[t]), (uint32_t)((oi - 1) & 1), abort_flag)) return false;
           tc_fence_after();
-          const uint32_t v = sV + st * C::TILE;
+          const uint32_t v = sV + st * C::KV_TILE;
 #pragma unroll
           for (int kk = 0; kk < BKV / 16; ++kk)  // 16 keys: 8 columns of P, 2 KB of each 64-dim half of V
-            tc_mma_ts(tmem + O_COL + t * 128, tmem + t * BKV + kk * 8, sdesc_sw128(v + kk * 2048, C::HALF, 1024),
-                      C::IDESC_O, (j | kk) != 0);
+            tc_mma_ts(base + C::O_COL, base + C::P_COL + kk * 8, sdesc_sw128(v + kk * 2048, C::KV_HALF, 1024), C::IDESC_O,
+                      (j | kk) != 0);
           tc_commit(bar(ctl->pv_done[t]));
           tc_commit(bar(ctl->v_empty[st]));
-          ++g;
+          return true;
+        };
+        if (nb > 0) ok = issue_s(0);
+        for (int j = 0; ok && j < nb; ++j) {
+          if (j + 1 < nb && !(ok = issue_s(j + 1))) break;
+          ok = issue_pv(j);
+        }
+        // blocks this tile does not read: only released, once they have arrived
+        for (int j = nb; ok && j < I.nblk; ++j) {
+          const int kv = kv_base + j, ks = kv % KST, vs = kv % VST;
+          if (!(ok = mbar_wait(bar(ctl->k_full[ks]), (uint32_t)((kv / KST) & 1), abort_flag))) break;
+          ctl->pend[1 + ks] = -1;
+          mbar_arrive(bar(ctl->k_empty[ks]));
+          if (!(ok = mbar_wait(bar(ctl->v_full[vs]), (uint32_t)((kv / VST) & 1), abort_flag))) break;
+          ctl->pend[1 + KST + vs] = -1;
+          mbar_arrive(bar(ctl->v_empty[vs]));
         }
         kv_base += I.nblk;
+        g += nb;
         if (nb > 0) ++oi;
       }
     }
@@ -299,37 +371,28 @@ __global__ void __launch_bounds__(THREADS, 1) attn_chunk_kernel(const __grid_con
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_SOFTMAX));
     const int t = (warp - 4) >> 2, quarter = warp & 3;
     const int r = quarter * 32 + lane;
-    const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
-    const uint32_t s_addr = tmem + lane_off + t * BKV, o_addr = tmem + lane_off + O_COL + t * 128;
+    const uint32_t s_addr = tmem + ((uint32_t)(quarter * 32) << 16) + t * C::COLS;
     int g = 0, kvb = 0;
     bool ok = true;
-    for (int it = 0; ok && item_at(it, a, I); kvb += I.nblk, ++it) {
+    // a warp leaves a wait as one: what follows is collective
+    auto wait = [&](uint64_t& b, uint32_t phase) { return __all_sync(0xffffffffu, mbar_wait(bar(b), phase, abort_flag)) != 0; };
+    for (int it = 0; ok && item_at<BKV>(it, a, I); kvb += I.nblk, ++it) {
       const int nb = t ? I.nblk_b : I.nblk_a, q0 = t ? I.q0b : I.q0a;
       if (nb == 0) continue;
       const int qrow = q0 + r, qpos = I.c0 + qrow;
       const int first = window_begin(qpos, a.window), last = min(qpos, I.nk - 1), sinks = a.window > 0 ? a.sinks : 0;
       float m = -INFINITY, l = 0.f;
       for (int j = 0; j < nb; ++j, ++g) {
-        // a warp leaves as one: what follows is collective
-        if (!(ok = __all_sync(0xffffffffu, mbar_wait(bar(ctl->s_full[t]), (uint32_t)(g & 1), abort_flag)))) break;
+        if (!(ok = wait(ctl->s_full[t], (uint32_t)(g & 1)))) break;
         tc_fence_after();
         float x[BKV];
-        {
-          uint32_t v[BKV / 32][32];
-#pragma unroll
-          for (int c = 0; c < BKV / 32; ++c) tmem_ld32_async(s_addr + 32 * c, v[c]);
-#pragma unroll
-          for (int c = 0; c < BKV / 32; ++c) {
-            tmem_wait32(v[c]);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) x[32 * c + i] = __uint_as_float(v[c][i]);
-          }
-        }
+        tmem_ld_row<BKV>(s_addr, x);
+        tc_fence_before();
+        mbar_arrive(bar(ctl->s_empty[t]));  // S of the next block may be computed
         const float* scales = nullptr;
         if (fp8) {
-          const int kv = kvb + j, st = kv % ST;
-          if (!(ok = __all_sync(0xffffffffu, mbar_wait(bar(ctl->v_full[st]), (uint32_t)((kv / ST) & 1), abort_flag))))
-            break;
+          const int kv = kvb + j, st = kv % VST;
+          if (!(ok = wait(ctl->v_full[st], (uint32_t)((kv / VST) & 1)))) break;
           scales = ctl->scale[st][0];
 #pragma unroll
           for (int i = 0; i < BKV; i += 4) {
@@ -340,50 +403,36 @@ __global__ void __launch_bounds__(THREADS, 1) attn_chunk_kernel(const __grid_con
             x[i + 3] *= f.w;
           }
         }
-        const int key0 = I.key0(j);
+        const int key0 = I.block(j) * BKV;
         // no key of the block hidden from any row of the tile
         const bool inside = key0 + BKV - 1 <= I.c0 + q0 && key0 + BKV <= I.nk &&
                             (a.window <= 0 || key0 > I.c0 + q0 + BQ - 1 - a.window || key0 + BKV <= a.sinks);
-        if (!inside) {  // the row's visible keys as bits, 32 at a time
+        if (!inside) {  // the row's visible keys as bits, 16 at a time
 #pragma unroll
-          for (int c = 0; c < BKV / 32; ++c) {
-            const int b = key0 + 32 * c;
-            auto upto = [](int n) { return n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1; };  // the first n bits
+          for (int c = 0; c < BKV / 16; ++c) {
+            const int b = key0 + 16 * c;
+            auto upto = [](int n) { return n >= 16 ? 0xffffu : n <= 0 ? 0u : (1u << n) - 1; };  // the first n bits
             const uint32_t in = upto(last + 1 - b) & (~upto(first - b) | upto(sinks - b));
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (!(in >> i & 1u)) x[32 * c + i] = -INFINITY;
+            for (int i = 0; i < 16; ++i)
+              if (!(in >> i & 1u)) x[16 * c + i] = -INFINITY;
           }
         }
-        float mx;
-        {
-          float pm[8];
+        float pm[8];
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            float v = fmax3f(x[k], x[k + 8], x[k + 16]);
+        for (int k = 0; k < 8; ++k) {
+          float v = x[k];
 #pragma unroll
-            for (int e = 24; e < BKV; e += 16) v = fmax3f(v, x[k + e], e + 8 < BKV ? x[k + e + 8] : x[k + e]);
-            pm[k] = v;
-          }
-          mx = fmax3f(fmax3f(pm[0], pm[1], pm[2]), fmax3f(pm[3], pm[4], pm[5]), fmaxf(pm[6], pm[7])) * scale_log2;
+          for (int e = 8; e + 8 < BKV; e += 16) v = fmax3f(v, x[k + e], x[k + e + 8]);
+          pm[k] = BKV % 16 ? v : fmaxf(v, x[k + BKV - 8]);
         }
+        const float mx = fmax3f(fmax3f(pm[0], pm[1], pm[2]), fmax3f(pm[3], pm[4], pm[5]), fmaxf(pm[6], pm[7])) * scale_log2;
         const bool move = mx > m + kLag;
-        if (__any_sync(0xffffffffu, move)) {
-          const float mn = move ? mx : m;
-          const float f = m == -INFINITY ? 0.f : ex2_approx(m - mn);
-          if (j > 0) {  // O holds the blocks before: S of this one was issued after their last product
-#pragma unroll
-            for (int c = 0; c < D; c += 32) {
-              float v[32];
-              tmem_ld32(o_addr + c, v);
-#pragma unroll
-              for (int i = 0; i < 32; ++i) v[i] *= f;
-              tmem_st32(o_addr + c, v);
-            }
-          }
-          l *= f;
-          m = mn;
-        }
+        const bool any = __any_sync(0xffffffffu, move);
+        const float mn = move ? mx : m;
+        const float f = m == -INFINITY ? 0.f : ex2_approx(m - mn);
+        m = mn;
+        l *= move ? f : 1.f;
         const float mneg = m == -INFINITY ? 0.f : -m;  // a row that has seen nothing yet: P = 0
 #pragma unroll
         for (int i = 0; i < BKV; i += 2) fma2(x + i, x + i, scale_log2, mneg);
@@ -400,21 +449,35 @@ __global__ void __launch_bounds__(THREADS, 1) attn_chunk_kernel(const __grid_con
         if (fp8) {
 #pragma unroll
           for (int i = 0; i < BKV; i += 4) {
-            const float4 f = *reinterpret_cast<const float4*>(scales + BKV + i);
-            x[i] *= f.x;
-            x[i + 1] *= f.y;
-            x[i + 2] *= f.z;
-            x[i + 3] *= f.w;
+            const float4 w = *reinterpret_cast<const float4*>(scales + BKV + i);
+            x[i] *= w.x;
+            x[i + 1] *= w.y;
+            x[i + 2] *= w.z;
+            x[i + 3] *= w.w;
           }
         }
         uint32_t p[BKV / 2];
 #pragma unroll
         for (int i = 0; i < BKV / 2; ++i) p[i] = pack_bf16(x[2 * i], x[2 * i + 1]);
-        tmem_st64(s_addr, p);
+        // P and O belong to the previous block's product until it has completed
+        if (g > 0 && !(ok = wait(ctl->pv_done[t], (uint32_t)((g - 1) & 1)))) break;
+        tc_fence_after();
+        if (any && j > 0) {
+          const float k = move ? f : 1.f;
+#pragma unroll
+          for (int c = 0; c < D; c += 32) {
+            float v[32];
+            tmem_ld32(s_addr + C::O_COL + c, v);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] *= k;
+            tmem_st32(s_addr + C::O_COL + c, v);
+          }
+        }
+        tmem_st_row<BKV / 2>(s_addr + C::P_COL, p);
         tc_fence_before();
         mbar_arrive(bar(ctl->p_full[t]));
       }
-      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar(ctl->pv_done[t]), (uint32_t)((g - 1) & 1), abort_flag));
+      if (ok) ok = wait(ctl->pv_done[t], (uint32_t)((g - 1) & 1));
       if (ok) {
         tc_fence_after();
         const float inv = 1.f / l;
@@ -424,7 +487,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_chunk_kernel(const __grid_con
 #pragma unroll
         for (int c = 0; c < D; c += 32) {
           float v[32];
-          tmem_ld32(o_addr + c, v);
+          tmem_ld32(s_addr + C::O_COL + c, v);
           if (qrow < I.n) {
 #pragma unroll
             for (int e = 0; e < 32; e += 8) {
@@ -447,10 +510,10 @@ __global__ void __launch_bounds__(THREADS, 1) attn_chunk_kernel(const __grid_con
   if (*abort_flag) {
     if (threadIdx.x == 0) {
       atomicOr(a.status, kStatusTimeout);
-      for (int i = 0; i < 1 + 2 * ST; ++i) {
+      for (int i = 0; i < 1 + KST + VST; ++i) {
         const int ph = ctl->pend[i];
         if (ph < 0) continue;
-        const uint32_t b = i == 0 ? bar(ctl->q_full) : i <= ST ? bar(ctl->k_full[i - 1]) : bar(ctl->v_full[i - 1 - ST]);
+        const uint32_t b = i == 0 ? bar(ctl->q_full) : i <= KST ? bar(ctl->k_full[i - 1]) : bar(ctl->v_full[i - 1 - KST]);
         const uint64_t t0 = global_ns();
         while (!mbar_try_wait(b, (uint32_t)ph) && global_ns() - t0 < kTimeoutNs) {
         }
@@ -473,8 +536,8 @@ __global__ void __launch_bounds__(THREADS, 1) attn_chunk_kernel(const __grid_con
 template <int D>
 cudaError_t launch_d(const ChunkArgs& a, const bf16* q, int ldq, int T, const bf16* k, const bf16* v, int num_sms,
                      cudaStream_t s) {
-  using C = Cfg<D>;
-  static_assert(C::SMEM <= 227 * 1024, "shared memory");
+  constexpr int smem = smem_bytes<D>();
+  static_assert(smem <= 227 * 1024, "shared memory");
   CUtensorMap mq, mk, mv, mt;
   const int rows = a.num_pages * a.n_kv * kPageSize;
   if (!tma_map_bf16_2d(&mq, q, T, a.n_q * D, ldq, 64, BQ, true) ||
@@ -485,9 +548,9 @@ cudaError_t launch_d(const ChunkArgs& a, const bf16* q, int ldq, int T, const bf
       !tma_map_bf16_2d(&mt, a.v_tail, a.tail_seqs * kTailSlots * a.n_kv * kPageSize, D, D, 64, kPageSize, true))
     return cudaErrorNotSupported;
   static PerDeviceOnce once;
-  cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void*>(attn_chunk_kernel<D>), C::SMEM, once);
+  cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void*>(attn_chunk_kernel<D>), smem, once);
   if (e != cudaSuccess) return e;
-  attn_chunk_kernel<D><<<(int)(a.num_items < num_sms ? a.num_items : num_sms), THREADS, C::SMEM, s>>>(
+  attn_chunk_kernel<D><<<(int)(a.num_items < num_sms ? a.num_items : num_sms), THREADS, smem, s>>>(
       mq, mk, mv, mt, a, 1.4426950408889634f / sqrtf((float)D));
   return cudaGetLastError();
 }
