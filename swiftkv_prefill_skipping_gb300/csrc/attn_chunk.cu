@@ -224,81 +224,81 @@ __global__ void __launch_bounds__(THREADS, 1) attn_chunk_kernel(const __grid_con
 
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_ISSUE));
-    if ((warp == 0 || warp == 3) && lane == 0) {
-      // warp 0: Q and K, warp 3: V and the scales
+    if (warp == 0 || warp == 3) {
+      // warp 0: Q and K, warp 3: V and the scales. Lane p looks after page p of a block (one thread
+      // doing it for all pages, at a dependent instruction every few cycles, took longer than the block)
       const bool is_v = warp == 3;
       const int group = a.n_q / a.n_kv;
-      // page ids of block b of item X (-1: not needed, or outside the pool)
-      auto block_pages = [&](const Item& X, int j, int* pg) {
-        const int w0 = window_begin(X.c0 + X.q0a, a.window), key0 = X.block(j) * BKV;
-#pragma unroll
-        for (int p = 0; p < PAGES; ++p) {
-          const int key = key0 + p * kPageSize;
-          pg[p] = -1;
-          if (key < X.nk && (key + kPageSize > w0 || key < a.sinks)) {
-            const int page = a.bt[(size_t)X.s * a.max_pages + (key >> 4)];
-            if (page >= 0 && page < a.num_pages) pg[p] = page;
-            else atomicOr(a.status, kStatusBadPage);
-          }
-        }
+      // the lane's page id in block j of item X, loaded one block ahead of its use
+      auto load_page = [&](const Item& X, int j) {
+        const int key = X.block(j) * BKV + lane * kPageSize;
+        // not read where no row of the item sees a key of the page
+        const bool need = lane < PAGES && key < X.nk && (key + kPageSize > window_begin(X.c0 + X.q0a, a.window) || key < a.sinks);
+        return make_int2(need, need ? a.bt[(size_t)X.s * a.max_pages + (key >> 4)] : 0);
       };
-      int kv_i = 0, pg[PAGES], next[PAGES];
+      int kv_i = 0;
+      int2 pg = make_int2(0, 0);
       bool ok = true, have = item_at<BKV>(0, a, I);
-      if (have) block_pages(I, 0, pg);
+      if (have) pg = load_page(I, 0);
       for (int it = 0; ok && have; ++it) {
         Item N;
         const bool have_next = item_at<BKV>(it + 1, a, N);
         const int kvh = I.h / group;
-        TailPages tail;
+        const TailPages tail = tail_pages(I.c0, I.n, a.window, a.sinks);
         if (!is_v) {
           // Q overwrites the previous item's, once its last S has completed
           if (it > 0 && !mbar_wait(bar(ctl->q_empty), (uint32_t)((it - 1) & 1), abort_flag)) break;
-          mbar_expect_tx(bar(ctl->q_full), (I.has_b ? 2 : 1) * C::Q_TILE);
-          ctl->pend[0] = it & 1;
-          for (int t = 0; t < (I.has_b ? 2 : 1); ++t)
+          if (lane == 0) {
+            mbar_expect_tx(bar(ctl->q_full), (I.has_b ? 2 : 1) * C::Q_TILE);
+            ctl->pend[0] = it & 1;
+            for (int t = 0; t < (I.has_b ? 2 : 1); ++t)
 #pragma unroll
-            for (int hf = 0; hf < C::HALVES; ++hf)
-              tma_load_2d(sQ + t * C::Q_TILE + hf * C::Q_HALF, &tmQ, (t ? I.hb : I.h) * D + hf * 64,
-                          I.seq0 + (t ? I.q0b : I.q0a), bar(ctl->q_full));
-        } else {
-          tail = tail_pages(I.c0, I.n, a.window, a.sinks);
+              for (int hf = 0; hf < C::HALVES; ++hf)
+                tma_load_2d(sQ + t * C::Q_TILE + hf * C::Q_HALF, &tmQ, (t ? I.hb : I.h) * D + hf * 64,
+                            I.seq0 + (t ? I.q0b : I.q0a), bar(ctl->q_full));
+          }
         }
         for (int j = 0; j < I.nblk; ++j, ++kv_i) {
-          if (j + 1 < I.nblk) block_pages(I, j + 1, next);
-          else if (have_next) block_pages(N, 0, next);
+          int2 next = pg;
+          if (j + 1 < I.nblk) next = load_page(I, j + 1);
+          else if (have_next) next = load_page(N, 0);
           const int st = is_v ? kv_i % VST : kv_i % KST;
           const uint32_t ph = (uint32_t)((is_v ? kv_i / VST : kv_i / KST) & 1);
           const uint32_t full = is_v ? bar(ctl->v_full[st]) : bar(ctl->k_full[st]);
-          if (!(ok = mbar_wait(is_v ? bar(ctl->v_empty[st]) : bar(ctl->k_empty[st]), ph ^ 1, abort_flag))) break;
-          mbar_expect_tx(full, C::KV_TILE + (is_v && fp8 ? 2 * BKV * 4 : 0));
-          ctl->pend[is_v ? 1 + KST + st : 1 + st] = (int)ph;
-          const uint32_t dst = (is_v ? sV : sK) + st * C::KV_TILE;
+          // a page that is not needed, or outside the pool, reads rows past the pool's end: zeros
+          const bool valid = pg.x && pg.y >= 0 && pg.y < a.num_pages;
+          if (pg.x && !valid) atomicOr(a.status, kStatusBadPage);
+          int row = (valid ? pg.y * a.n_kv + kvh : a.num_pages * a.n_kv) * kPageSize;
+          const CUtensorMap* map = is_v ? &tmV : &tmK;
+          const size_t sr = valid ? (size_t)row : (size_t)kvh * kPageSize;  // scales of a masked page: page 0's
+          if (is_v && a.v_tail && valid) {
+            const int pidx = I.block(j) * PAGES + lane;
 #pragma unroll
-          for (int p = 0; p < PAGES; ++p) {
-            // a page that is not needed reads rows past the pool's end: zeros
-            int row = (pg[p] >= 0 ? pg[p] * a.n_kv + kvh : a.num_pages * a.n_kv) * kPageSize;
-            const CUtensorMap* map = is_v ? &tmV : &tmK;
-            if (is_v && fp8) {  // page 0's scales for a page that is not loaded: its keys are masked
-              const size_t sr = pg[p] >= 0 ? (size_t)row : (size_t)kvh * kPageSize;
-              const uint32_t sd = smem_u32(&ctl->scale[st][0][p * kPageSize]);
+            for (int t = 0; t < kTailSlots; ++t)
+              if (pidx == tail.page[t]) {
+                map = &tmTail;
+                row = ((I.s * kTailSlots + t) * a.n_kv + kvh) * kPageSize;
+              }
+          }
+          if (!(ok = mbar_wait(is_v ? bar(ctl->v_empty[st]) : bar(ctl->k_empty[st]), ph ^ 1, abort_flag))) break;
+          if (lane == 0) {
+            mbar_expect_tx(full, C::KV_TILE + (is_v && fp8 ? 2 * BKV * 4 : 0));
+            ctl->pend[is_v ? 1 + KST + st : 1 + st] = (int)ph;
+          }
+          __syncwarp();
+          if (lane < PAGES) {
+            const uint32_t dst = (is_v ? sV : sK) + st * C::KV_TILE + lane * 2048;
+#pragma unroll
+            for (int hf = 0; hf < C::HALVES; ++hf) tma_load_2d(dst + hf * C::KV_HALF, map, hf * 64, row, full);
+            if (is_v && fp8) {
+              const uint32_t sd = smem_u32(&ctl->scale[st][0][lane * kPageSize]);
               bulk_load(sd, a.k_scale + sr, kPageSize * 4, full);
               bulk_load(sd + BKV * 4, a.v_scale + sr, kPageSize * 4, full);
             }
-            if (is_v && a.v_tail && pg[p] >= 0) {
-              const int pidx = I.block(j) * PAGES + p;
-#pragma unroll
-              for (int t = 0; t < kTailSlots; ++t)
-                if (pidx == tail.page[t]) {
-                  map = &tmTail;
-                  row = ((I.s * kTailSlots + t) * a.n_kv + kvh) * kPageSize;
-                }
-            }
-#pragma unroll
-            for (int hf = 0; hf < C::HALVES; ++hf) tma_load_2d(dst + hf * C::KV_HALF + p * 2048, map, hf * 64, row, full);
           }
-#pragma unroll
-          for (int p = 0; p < PAGES; ++p) pg[p] = next[p];
+          pg = next;
         }
+        ok = __all_sync(0xffffffffu, ok);
         I = N;
         have = have_next;
       }
