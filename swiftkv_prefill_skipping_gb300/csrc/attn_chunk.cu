@@ -186,6 +186,8 @@ __global__ void __launch_bounds__(THREADS, 1) attn_chunk_kernel(const __grid_con
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const bool fp8 = a.k_scale != nullptr;
   auto bar = [&](uint64_t& b) { return smem_u32(&b); };
+  // a warp leaves a wait as one: what follows is collective
+  auto wait_all = [&](uint32_t b, uint32_t phase) { return __all_sync(0xffffffffu, mbar_wait(b, phase, abort_flag)) != 0; };
 
   if (threadIdx.x == 0) {
     mbar_init(bar(ctl->q_full), 1);
@@ -247,7 +249,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_chunk_kernel(const __grid_con
         const TailPages tail = tail_pages(I.c0, I.n, a.window, a.sinks);
         if (!is_v) {
           // Q overwrites the previous item's, once its last S has completed
-          if (it > 0 && !mbar_wait(bar(ctl->q_empty), (uint32_t)((it - 1) & 1), abort_flag)) break;
+          if (it > 0 && !(ok = wait_all(bar(ctl->q_empty), (uint32_t)((it - 1) & 1)))) break;
           if (lane == 0) {
             mbar_expect_tx(bar(ctl->q_full), (I.has_b ? 2 : 1) * C::Q_TILE);
             ctl->pend[0] = it & 1;
@@ -280,7 +282,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_chunk_kernel(const __grid_con
                 row = ((I.s * kTailSlots + t) * a.n_kv + kvh) * kPageSize;
               }
           }
-          if (!(ok = mbar_wait(is_v ? bar(ctl->v_empty[st]) : bar(ctl->k_empty[st]), ph ^ 1, abort_flag))) break;
+          if (!(ok = wait_all(is_v ? bar(ctl->v_empty[st]) : bar(ctl->k_empty[st]), ph ^ 1))) break;
           if (lane == 0) {
             mbar_expect_tx(full, C::KV_TILE + (is_v && fp8 ? 2 * BKV * 4 : 0));
             ctl->pend[is_v ? 1 + KST + st : 1 + st] = (int)ph;
@@ -298,14 +300,15 @@ __global__ void __launch_bounds__(THREADS, 1) attn_chunk_kernel(const __grid_con
           }
           pg = next;
         }
-        ok = __all_sync(0xffffffffu, ok);
         I = N;
         have = have_next;
       }
     } else if ((warp == 1 || warp == 2) && lane == 0) {
       // tile t's MMAs; g counts its blocks over all items, oi the items that used its O
       const int t = warp - 1;
-      const uint32_t q = sQ + t * C::Q_TILE, base = tmem + t * C::COLS;
+      // descriptors of the tile's Q and of stage 0; an offset in bytes adds its sixteenth
+      const uint64_t q = sdesc(sQ + t * C::Q_TILE), k0 = sdesc(sK), v0 = sdesc_sw128(sV, C::KV_HALF, 1024);
+      const uint32_t base = tmem + t * C::COLS;
       int kv_base = 0, g = 0, oi = 0;
       bool ok = true;
       for (int it = 0; ok && item_at<BKV>(it, a, I); ++it) {
@@ -320,11 +323,11 @@ __global__ void __launch_bounds__(THREADS, 1) attn_chunk_kernel(const __grid_con
           ctl->pend[1 + st] = -1;
           if (gj > 0 && !mbar_wait(bar(ctl->s_empty[t]), (uint32_t)((gj - 1) & 1), abort_flag)) return false;
           tc_fence_after();
-          const uint32_t k = sK + st * C::KV_TILE;
+          const uint64_t k = k0 + st * (C::KV_TILE / 16);
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk)
-            tc_mma(base, sdesc(q + (kk >> 2) * C::Q_HALF + (kk & 3) * 32),
-                   sdesc(k + (kk >> 2) * C::KV_HALF + (kk & 3) * 32), C::IDESC_S, kk != 0);
+            tc_mma(base, q + ((kk >> 2) * C::Q_HALF + (kk & 3) * 32) / 16,
+                   k + ((kk >> 2) * C::KV_HALF + (kk & 3) * 32) / 16, C::IDESC_S, kk != 0);
           tc_commit(bar(ctl->s_full[t]));
           tc_commit(bar(ctl->k_empty[st]));
           if (j + 1 == nb) tc_commit(bar(ctl->q_empty));
@@ -338,11 +341,10 @@ __global__ void __launch_bounds__(THREADS, 1) attn_chunk_kernel(const __grid_con
           // the first P V of an item overwrites O: the previous item's output must have left
           if (j == 0 && oi > 0 && !mbar_wait(bar(ctl->o_empty[t]), (uint32_t)((oi - 1) & 1), abort_flag)) return false;
           tc_fence_after();
-          const uint32_t v = sV + st * C::KV_TILE;
+          const uint64_t v = v0 + st * (C::KV_TILE / 16);
 #pragma unroll
           for (int kk = 0; kk < BKV / 16; ++kk)  // 16 keys: 8 columns of P, 2 KB of each 64-dim half of V
-            tc_mma_ts(base + C::O_COL, base + C::P_COL + kk * 8, sdesc_sw128(v + kk * 2048, C::KV_HALF, 1024), C::IDESC_O,
-                      (j | kk) != 0);
+            tc_mma_ts(base + C::O_COL, base + C::P_COL + kk * 8, v + kk * 128, C::IDESC_O, (j | kk) != 0);
           tc_commit(bar(ctl->pv_done[t]));
           tc_commit(bar(ctl->v_empty[st]));
           return true;
@@ -374,8 +376,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_chunk_kernel(const __grid_con
     const uint32_t s_addr = tmem + ((uint32_t)(quarter * 32) << 16) + t * C::COLS;
     int g = 0, kvb = 0;
     bool ok = true;
-    // a warp leaves a wait as one: what follows is collective
-    auto wait = [&](uint64_t& b, uint32_t phase) { return __all_sync(0xffffffffu, mbar_wait(bar(b), phase, abort_flag)) != 0; };
+    auto wait = [&](uint64_t& b, uint32_t phase) { return wait_all(bar(b), phase); };
     for (int it = 0; ok && item_at<BKV>(it, a, I); kvb += I.nblk, ++it) {
       const int nb = t ? I.nblk_b : I.nblk_a, q0 = t ? I.q0b : I.q0a;
       if (nb == 0) continue;

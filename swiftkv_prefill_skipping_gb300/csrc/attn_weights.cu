@@ -353,7 +353,7 @@ __global__ void __launch_bounds__(WT, 1) weights_tc_kernel(const __grid_constant
   if (warp == 0) {
     if (lane == 0) {
       bool ok = true;
-      long long g = 0;  // query tiles so far
+      unsigned g = 0;  // query tiles so far (only remainders and low quotient bits are used)
       for (long long it = 0; ok && w_item(it, tiles, n_items, a, I); ++it) {
         const int kb = (int)(it & 1);
         const uint32_t kph = (uint32_t)((it >> 1) & 1);
@@ -395,8 +395,10 @@ __global__ void __launch_bounds__(WT, 1) weights_tc_kernel(const __grid_constant
     }
   } else if (warp == 1) {
     if (lane == 0) {
+      // descriptors of the first K buffer and Q stage; an offset in bytes adds its sixteenth
+      const uint64_t k0 = sdesc(sK), q0 = sdesc(sQ);
       bool ok = true;
-      long long g = 0;
+      unsigned g = 0;  // only its remainders and low quotient bits are used
       for (long long it = 0; ok && w_item(it, tiles, n_items, a, I); ++it) {
         const int kb = (int)(it & 1);
         if (!mbar_wait(bar(ctl->k_full[kb]), (uint32_t)((it >> 1) & 1), abort_flag)) break;
@@ -414,11 +416,11 @@ __global__ void __launch_bounds__(WT, 1) weights_tc_kernel(const __grid_constant
             break;
           }
           tc_fence_after();
-          const uint32_t k = sK + kb * TILE, q = sQ + st * TILE;
+          const uint64_t k = k0 + kb * (TILE / 16), q = q0 + st * (TILE / 16);
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t off = (kk >> 2) * HALF + (kk & 3) * 32;
-            tc_mma(tmem + sb * BQ, sdesc(k + off), sdesc(q + off), IDESC, kk != 0);
+            const int off = ((kk >> 2) * HALF + (kk & 3) * 32) / 16;
+            tc_mma(tmem + sb * BQ, k + off, q + off, IDESC, kk != 0);
           }
           tc_commit(bar(ctl->q_empty[st]));
           tc_commit(bar(ctl->s_full[sb]));
@@ -435,7 +437,7 @@ __global__ void __launch_bounds__(WT, 1) weights_tc_kernel(const __grid_constant
     const int r = quarter * 32 + lane;
     const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
     auto wg_sync = [&]() { asm volatile("bar.sync %0, 128;" ::"r"(1 + wg) : "memory"); };
-    long long g = 0;
+    unsigned g = 0;
     int turn = 0;  // this warpgroup's tiles so far: parity of its lse buffer
     bool ok = true;
     for (long long it = 0; w_item(it, tiles, n_items, a, I); ++it) {
@@ -469,7 +471,7 @@ __global__ void __launch_bounds__(WT, 1) weights_tc_kernel(const __grid_constant
         h += WGS;
         settle();
         next = lse_here();
-        const long long gt = g + t;
+        const unsigned gt = g + t;
         const int sb = (int)(gt % SBUF);
         // after an expired wait the loops run on without work, so that every thread still meets
         // the same barriers
