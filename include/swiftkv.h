@@ -272,6 +272,28 @@ int swiftkv_evict(swiftkv_model* m, int cache, const swiftkv_kv_pages* kv, float
                   const int32_t* seq_lens, int num_seqs, int keep, int sinks, int recent,
                   const int32_t* dst_block_table, int dst_max_pages, int32_t* kept, swiftkv_stream stream);
 
+/* ---- the same in the model's own calls ------------------------------------------------------
+ * Sliding window and sinks for the attention of every layer in later calls of swiftkv_prefill,
+ * _prefill_host, _forward, _forward_at and _decode_step (visibility as above, by cache row); window 0
+ * (default) turns them off. swiftkv_set_attention_impl does not concern calls with a window. */
+int swiftkv_set_attention_window(swiftkv_model* m, int window, int sinks);
+
+/* From now on every layer's attention adds the weights its rows gave to the keys of its cache to
+ * that cache's score pool (swiftkv_attention_weights with this decay after each layer's attention;
+ * layers that share a cache add up, so a decay other than 1 acts once per layer).
+ *   scores  HOST array [swiftkv_cache_count] of device float pools, as for swiftkv_evict, read at
+ *           this call; the pools stay the caller's and must outlive the calls that add to them.
+ *           NULL turns it off (default). */
+int swiftkv_set_score_pools(swiftkv_model* m, float* const* scores, float decay);
+
+/* swiftkv_forward for sequences whose caches were shrunk by swiftkv_evict: chunk token i of sequence
+ * s goes to cache row ctx_lens[s] + i and sees rows up to its own, while its position for RoPE is
+ * ctx_lens[s] + pos_offsets[s] + i. With n keys before an eviction that kept k, the offset grows by
+ * n - k. pos_offsets HOST int32 [num_seqs], none negative; NULL: all 0 (swiftkv_forward). */
+int swiftkv_forward_at(swiftkv_model* m, const int32_t* tokens, const int32_t* cu_seqlens, const int32_t* ctx_lens,
+                       const int32_t* pos_offsets, int num_seqs, int l, int acrosskv_group, const swiftkv_kv_pages* kv,
+                       float* logits, swiftkv_stream stream);
+
 /* How swiftkv_sample draws. Each setting is a device array with one value per row, or NULL and
  * one value for all rows in the *_all field. Order and meaning, with w_i = exp((l_i - max l) / T):
  *   temperature T <= 0 or NaN: the argmax, lowest id on ties (u and the rest are not used)

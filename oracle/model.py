@@ -149,6 +149,43 @@ def swiglu(g: np.ndarray, u: np.ndarray) -> np.ndarray:
     return (silu(g).astype(t) * np.asarray(u).astype(t)).astype(F64)
 
 
+# Attention window of the context manager below: (window, sinks), window 0 = every earlier key.
+_WINDOW = (0, 0)
+_OBSERVERS: List[Callable[[np.ndarray], None]] = []
+
+
+class attention_window:
+    """Inside the context a query at position p sees key positions j <= p with j > p - window or
+    j < sinks (window 0: all j <= p)."""
+
+    def __init__(self, window: int, sinks: int = 0):
+        self.new = (window, sinks)
+
+    def __enter__(self):
+        global _WINDOW
+        self.old, _WINDOW = _WINDOW, self.new
+        return self
+
+    def __exit__(self, *exc):
+        global _WINDOW
+        _WINDOW = self.old
+
+
+class observe_attention:
+    """Inside the context `fn` receives the softmax weights [n_q, n, m] of every attention, in the
+    order in which they are computed (float64 mode)."""
+
+    def __init__(self, fn: Callable[[np.ndarray], None]):
+        self.fn = fn
+
+    def __enter__(self):
+        _OBSERVERS.append(self.fn)
+        return self
+
+    def __exit__(self, *exc):
+        _OBSERVERS.remove(self.fn)
+
+
 def causal_gqa_attention(q: np.ndarray, k: np.ndarray, v: np.ndarray, q_pos: np.ndarray,
                          k_pos: np.ndarray) -> np.ndarray:
     """softmax(q k^T / sqrt(d_h)) v with a causal mask (key position <= query
@@ -156,10 +193,14 @@ def causal_gqa_attention(q: np.ndarray, k: np.ndarray, v: np.ndarray, q_pos: np.
     head h // (n_q / n_kv)."""
     n_q, d_h = q.shape[1], q.shape[2]
     grp = n_q // k.shape[1]
-    allowed = np.asarray(k_pos)[None, :] <= np.asarray(q_pos)[:, None]
+    behind = np.asarray(q_pos)[:, None] - np.asarray(k_pos)[None, :]
+    allowed = behind >= 0
+    if _WINDOW[0] > 0:
+        allowed &= (behind < _WINDOW[0]) | (np.asarray(k_pos)[None, :] < _WINDOW[1])
     out = np.empty(q.shape, dtype=F64)
     scale = 1.0 / np.sqrt(F64(d_h))
     t = _mode()
+    seen = []
     for h in range(n_q):
         kv = h // grp
         if t is F64:
@@ -169,12 +210,16 @@ def causal_gqa_attention(q: np.ndarray, k: np.ndarray, v: np.ndarray, q_pos: np.
             p = np.exp(s)
             p = p / p.sum(axis=1, keepdims=True)
             out[:, h, :] = p @ v[:, kv, :]
+            if _OBSERVERS:
+                seen.append(p)
         else:  # everything in the mode's type; unnormalised weights applied to V, then divided
             s = (q[:, h, :].astype(t) @ k[:, kv, :].T.astype(t)) * t(scale)
             s = np.where(allowed, s, t(-np.inf))
             p = np.exp(s - s.max(axis=1, keepdims=True))
             denom = p.sum(axis=1, keepdims=True, dtype=t)
             out[:, h, :] = ((p @ v[:, kv, :].astype(t)) / denom).astype(F64)
+    for fn in _OBSERVERS:
+        fn(np.stack(seen))
     return out
 
 
@@ -501,15 +546,17 @@ def swiftkv_decode_step(cfg: Config, w: Weights, caches: List[KV], token: int, l
 
 
 def swiftkv_forward_one(cfg: Config, w: Weights, caches: Optional[List[KV]], tokens: Sequence[int], l: int,
-                        g: int = 1) -> Tuple[List[KV], np.ndarray]:
+                        g: int = 1, pos_offset: int = 0) -> Tuple[List[KV], np.ndarray]:
     """One chunk of a sequence whose caches already hold its first ctx tokens (caches None
     or empty for ctx = 0): the serving forward of [S] 3.4 "Inference Implementation in
     Production Serving Frameworks" / [P] 3.5, where every token of the chunk runs layers
     0..l-1 (attending to the cached prefix and to the chunk causally), the caches of every
     skipped layer / AcrossKV group are computed for the chunk's tokens from x_l, and only
     the chunk's last token continues through layers l..L-1. A decode token is a chunk of
-    one token; a prompt may be fed in several chunks. Returns the extended caches and the
-    last token's logits [V]."""
+    one token; a prompt may be fed in several chunks. pos_offset: keys that an eviction removed
+    from the caches; the chunk's tokens then sit that many positions further on for RoPE, while
+    they see cache rows up to their own. Returns the extended caches and the last token's
+    logits [V]."""
     check_lg(cfg.L, l, g)
     tokens = np.asarray(tokens)
     n = len(tokens)
@@ -523,7 +570,8 @@ def swiftkv_forward_one(cfg: Config, w: Weights, caches: Optional[List[KV]], tok
         ctx = 0
         empty = np.zeros((0, cfg.n_kv, cfg.d_h))
         out = [(empty, empty)] * C
-    pos = np.arange(ctx, ctx + n)
+    row = np.arange(ctx, ctx + n)
+    pos = row + pos_offset
     kpos = np.arange(ctx + n)
 
     def append(c: int, kv: KV) -> None:
@@ -534,15 +582,15 @@ def swiftkv_forward_one(cfg: Config, w: Weights, caches: Optional[List[KV]], tok
         lw = w.layer(j)
         q, kv = qkv_proj(cfg, lw, x, pos)
         append(j, kv)
-        x = attn_out(cfg, lw, x, q, out[j], pos, kpos)
+        x = attn_out(cfg, lw, x, q, out[j], row, kpos)
         x = mlp(cfg, lw, x)
     for c in range(l, C):
         append(c, swiftkv_kv(cfg, w.layer(representative(c, l, g)), x, pos))
-    xt, pt = x[n - 1:], pos[n - 1:]
+    xt, pt, rt = x[n - 1:], pos[n - 1:], row[n - 1:]
     for j in range(l, cfg.L):
         lw = w.layer(j)
         q = q_proj(cfg, lw, xt, pt)
-        xt = attn_out(cfg, lw, xt, q, out[cache_of_layer(j, l, g)], pt, kpos)
+        xt = attn_out(cfg, lw, xt, q, out[cache_of_layer(j, l, g)], rt, kpos)
         xt = mlp(cfg, lw, xt)
     return out, lm_head(cfg, w, xt)[0]
 

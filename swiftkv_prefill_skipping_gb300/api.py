@@ -105,6 +105,25 @@ class Model:
     def status(self, clear: bool = True) -> int:
         return B.check(B.lib().swiftkv_status(self.handle, int(clear)))
 
+    def set_attention_window(self, window: int, sinks: int = 0) -> None:
+        """Later calls see the last `window` tokens and the first `sinks` (0: all of them)."""
+        B.check(B.lib().swiftkv_set_attention_window(self.handle, window, sinks))
+
+    def set_score_pools(self, scores: Optional[torch.Tensor], decay: float = 1.0) -> None:
+        """Later calls add every layer's attention weights to scores (float32 [num_caches, num_pages,
+        n_kv, 16], e.g. KVCache.new_scores(); kept alive here); None turns that off."""
+        if scores is None:
+            B.check(B.lib().swiftkv_set_score_pools(self.handle, None, decay))
+        else:
+            s = self.shape
+            if scores.dim() != 4 or scores.shape[0] != self.num_caches or tuple(scores.shape[2:]) != (s.n_kv, 16):
+                raise ValueError(f"scores: float32 [{self.num_caches}, pages, {s.n_kv}, 16]")
+            base = _flat(scores, torch.float32, tuple(scores.shape), scores.device, "scores")
+            step = scores.stride(0) * 4
+            ptrs = (C.c_void_p * self.num_caches)(*[base + c * step for c in range(self.num_caches)])
+            B.check(B.lib().swiftkv_set_score_pools(self.handle, ptrs, decay))
+        self._scores = scores
+
     def memory(self):
         wb, sb = C.c_size_t(), C.c_size_t()
         B.check(B.lib().swiftkv_memory(self.handle, C.byref(wb), C.byref(sb)))
@@ -162,6 +181,11 @@ class KVCache:
     def _set_pages(self, pages: B.KVPages) -> None:
         self.pages, self.pages_ref = pages, C.byref(pages)
         self.num_rows = self.block_table.shape[0]
+
+    def new_scores(self) -> torch.Tensor:
+        """Zeroed accumulated attention weights, one per cached key: [num_caches, num_pages, n_kv, 16]."""
+        return torch.zeros((self.num_caches, self.num_pages, self.k.shape[2], 16), dtype=torch.float32,
+                           device=self.k.device)
 
     def view(self, rows: Sequence[int]) -> "KVCache":
         """The same pools with block table rows `rows` (in that order): a batch that holds
@@ -223,9 +247,11 @@ def prefill_host(model: Model, tokens: np.ndarray, cu_seqlens: Sequence[int], kv
 
 
 def forward(model: Model, tokens: torch.Tensor, cu_seqlens: Sequence[int], ctx_lens: Optional[Sequence[int]],
-            kv: KVCache, logits: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+            kv: KVCache, logits: Optional[torch.Tensor] = None, stream=None,
+            pos_offsets: Optional[Sequence[int]] = None) -> torch.Tensor:
     """Serving forward over prompt chunks and decode tokens: chunk s follows ctx_lens[s]
-    tokens already in kv (None: none); returns [P, V] logits of each chunk's last token."""
+    tokens already in kv (None: none); returns [P, V] logits of each chunk's last token. After an
+    eviction ctx_lens[s] counts the keys that are left and pos_offsets[s] those that are gone."""
     cu = np.ascontiguousarray(cu_seqlens, dtype=np.int32)
     P = len(cu) - 1
     ctx = None if ctx_lens is None else np.ascontiguousarray(ctx_lens, dtype=np.int32)
@@ -234,6 +260,14 @@ def forward(model: Model, tokens: torch.Tensor, cu_seqlens: Sequence[int], ctx_l
     if logits is None:
         logits = torch.empty((P, model.shape.vocab), dtype=torch.float32, device=kv.k.device)
     tokens = tokens.to(torch.int32).contiguous()
+    if pos_offsets is not None:
+        off = np.ascontiguousarray(pos_offsets, dtype=np.int32)
+        if len(off) != P:
+            raise ValueError(f"pos_offsets has {len(off)} entries for {P} chunks")
+        B.check(B.lib().swiftkv_forward_at(model.handle, tokens.data_ptr(), cu.ctypes.data,
+                                           None if ctx is None else ctx.ctypes.data, off.ctypes.data, P, model.l,
+                                           model.g, C.byref(kv.pages), logits.data_ptr(), _stream(stream)))
+        return logits
     B.check(B.lib().swiftkv_forward(model.handle, tokens.data_ptr(), cu.ctypes.data,
                                     None if ctx is None else ctx.ctypes.data, P, model.l, model.g,
                                     C.byref(kv.pages), logits.data_ptr(), _stream(stream)))

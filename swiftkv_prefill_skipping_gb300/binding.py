@@ -27,7 +27,8 @@ STATUS_TIMEOUT = 4
 EXPORTS = ("swiftkv_cache_count", "swiftkv_model_create", "swiftkv_load_layer", "swiftkv_load_globals",
            "swiftkv_load_weights", "swiftkv_prefill", "swiftkv_prefill_host", "swiftkv_forward",
            "swiftkv_decode_step", "swiftkv_sample", "swiftkv_attend",
-           "swiftkv_attention_weights", "swiftkv_evict",
+           "swiftkv_attention_weights", "swiftkv_evict", "swiftkv_set_attention_window",
+           "swiftkv_set_score_pools", "swiftkv_forward_at",
            "swiftkv_status", "swiftkv_memory", "swiftkv_set_gemm_impl", "swiftkv_set_attention_impl",
            "swiftkv_set_norm_fusion", "swiftkv_set_rows_impl", "swiftkv_gemm_bf16",
            "swiftkv_gemm_skinny_noalloc", "swiftkv_selftest_wait_timeout",
@@ -101,6 +102,9 @@ def lib(path: str | None = None):
             L.swiftkv_attention_weights.argtypes = [vp, i, vp, i, vp, vp, vp, i, C.POINTER(KVPages), i, i, C.c_float,
                                                     vp, vp]
             L.swiftkv_evict.argtypes = [vp, i, C.POINTER(KVPages), C.POINTER(vp), vp, i, i, i, i, vp, i, vp, vp]
+            L.swiftkv_set_attention_window.argtypes = [vp, i, i]
+            L.swiftkv_set_score_pools.argtypes = [vp, C.POINTER(vp), C.c_float]
+            L.swiftkv_forward_at.argtypes = [vp, vp, vp, vp, vp, i, i, i, C.POINTER(KVPages), vp, vp]
             L.swiftkv_sample.argtypes = [vp, i, i, C.c_longlong, C.POINTER(Sampling), vp, vp, vp]
             L.swiftkv_status.argtypes = [vp, i]
             L.swiftkv_memory.argtypes = [vp, C.POINTER(sz), C.POINTER(sz)]

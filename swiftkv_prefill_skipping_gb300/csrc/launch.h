@@ -101,8 +101,8 @@ cudaError_t upload_ints(int* dst, const int* src, int n, cudaStream_t stream);
 
 // positions / slots / last index of a packed prefill batch; validates tokens and pages.
 // ctx (device, nullable = all zero): tokens already cached per sequence; chunk row i of
-// sequence s sits at position ctx[s] + i.
-cudaError_t launch_plan_prefill(const int* cu, const int* ctx, int P, int T, const int* tokens, int vocab,
+// sequence s sits in cache row ctx[s] + i, and at that position plus pos_off[s] (nullable) for RoPE.
+cudaError_t launch_plan_prefill(const int* cu, const int* ctx, const int* pos_off, int P, int T, const int* tokens, int vocab,
                                 const int* block_table, int max_pages, int num_pages, int* positions,
                                 int* slots, int* last_idx, int* last_pos, int* status,
                                 cudaStream_t stream);

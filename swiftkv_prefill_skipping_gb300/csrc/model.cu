@@ -15,6 +15,7 @@
 
 #include "launch.h"
 #include "model_state.h"
+#include "serving.h"
 #include "swiftkv.h"
 
 using namespace skv;
@@ -259,11 +260,56 @@ struct Ctx {
   float* const* vs_dev = nullptr;
   bool expand = false;       // FP8: prompt tiles read a bf16 expansion of the layer's cache
   int n_deq = 0;             // FP8: prefix pages to expand per full layer (w.deq_items)
+  const struct ServingPlan* serving = nullptr;  // window, score pools or position offsets: attention by its plans
   // RMSNorm fused into the prompt rows' tcgen05 GEMMs: the O and down epilogues leave
   // bf16(gamma * x) in w.u (gamma: the next norm's gain) and per-tile sums of squares of x in
   // w.ss_attn / w.ss_mlp, which the next GEMM's epilogue turns into the row's 1/rms; no
   // separate norm pass over the prompt rows
   bool fused = false;
+};
+
+// A call's attention where the model has a window or score pools, or the sequences position offsets:
+// the operators' plans for all rows of the call (full layers) and for each chunk's last row (tail),
+// uploaded once and run by every layer. The two may be one (decode: every row is its chunk's last).
+struct ServingPlan {
+  AttendPlan rows, last;
+  WeightsPlan rows_w, last_w;
+  bool has_last = false, scores = false;
+  float *lse_rows = nullptr, *lse_last = nullptr;
+  int* offsets = nullptr;  // device [P] or null
+
+  int make(const swiftkv_model* m, const int32_t* cu, const int32_t* ctx, int P, const swiftkv_kv_pages* kv, bool with_last) {
+    has_last = with_last;
+    scores = !m->score_pools.empty();
+    RET(rows.make(m, cu, ctx, P, kv, m->window, m->sinks));
+    if (scores) RET(rows_w.make(m, cu, ctx, P, kv, m->window, m->sinks));
+    if (!with_last) return SWIFTKV_OK;
+    std::vector<int> one(P + 1), at(P);
+    for (int i = 0; i <= P; ++i) one[i] = i;
+    for (int i = 0; i < P; ++i) at[i] = (ctx ? ctx[i] : 0) + cu[i + 1] - cu[i] - 1;
+    RET(last.make(m, one.data(), at.data(), P, kv, m->window, m->sinks));
+    if (scores) RET(last_w.make(m, one.data(), at.data(), P, kv, m->window, m->sinks));
+    return SWIFTKV_OK;
+  }
+  void place(const swiftkv_model* m, bool with_offsets, Arena* a) {
+    rows.place(m, a);
+    if (has_last) last.place(m, a);
+    if (scores) {
+      rows_w.place(m, a);
+      if (has_last) last_w.place(m, a);
+      lse_rows = a->take<float>((size_t)m->cfg.n_q * rows.b.T);
+      lse_last = has_last ? a->take<float>((size_t)m->cfg.n_q * last.b.T) : lse_rows;
+    }
+    offsets = with_offsets ? a->take<int>(rows.b.P) : nullptr;
+  }
+  int upload(const int32_t* host_offsets, cudaStream_t s) const {
+    RET(rows.upload(s));
+    if (has_last) RET(last.upload(s));
+    if (scores) RET(rows_w.upload(s));
+    if (scores && has_last) RET(last_w.upload(s));
+    if (offsets) CK(upload_ints(offsets, host_offsets, rows.b.P, s));
+    return SWIFTKV_OK;
+  }
 };
 
 // Host side of a key-split plan: units then ubeg in one vector (one upload).
@@ -447,7 +493,24 @@ int layer_rest(Ctx& x, int j, int M, float* xres, bf16* qb, bf16* ab, bf16* ub, 
   const bf16* tvp = x.fp8 ? x.w.exp_v : vp;
   const float* tks = x.fp8 ? static_cast<const float*>(x.kv->k_scale[cidx]) : nullptr;
   const float* tvs = x.fp8 ? static_cast<const float*>(x.kv->v_scale[cidx]) : nullptr;
-  {
+  if (x.serving) {
+    const ServingPlan& sv = *x.serving;
+    const bool is_last = !prefill && sv.has_last;
+    const AttendPlan& ap = is_last ? sv.last : sv.rows;
+    float* lse = sv.scores ? (is_last ? sv.lse_last : sv.lse_rows) : nullptr;
+    {
+      Prof pr(x.m, x.s, prefill ? "attn_prefill" : "attn_decode", ap.kernels(), 4.0 * c.n_q * c.d_head * ap.pairs,
+              ap.keys * kv_bytes_per_key(m, x.fp8) + 2.0 * M * m->Nq * 2);
+      RET(ap.run(m, x.kv, cidx, qb, m->Nq, ab, m->Nq, lse, M, x.s));
+    }
+    if (sv.scores) {
+      const WeightsPlan& wp = is_last ? sv.last_w : sv.rows_w;
+      Prof pr(x.m, x.s, "attn_weights", wp.kernels(), 2.0 * c.n_q * c.d_head * wp.pairs,
+              wp.keys * (kv_bytes_per_key(m, x.fp8) / 2 + 4.0 * c.n_kv) + 1.0 * M * m->Nq * 2);
+      RET(wp.run(m, x.kv, cidx, qb, m->Nq, lse, M, m->score_decay, m->score_pools[cidx], x.s));
+    }
+    e = cudaSuccess;
+  } else {
   Prof pr(x.m, x.s, prefill ? "attn_prefill" : "attn_decode",
           prefill ? (ntiles > 0) + (x.nshort > 0 ? launches(x.sp_short) : 0) : launches(x.sp_rows), attn_flops,
           attn_bytes);
@@ -990,8 +1053,10 @@ int swiftkv_profile_end(swiftkv_model* m, swiftkv_profile_entry* out, int max_en
 
 // Prefill of packed prompt chunks; ctx (host, nullable) = tokens each sequence already has
 // in the cache (0 for a fresh prompt, its length for a decode token).
+// pos_off (host, nullable): added to the positions that RoPE sees, not to the cache rows.
 static int prefill_impl(swiftkv_model* m, const int32_t* tokens, const int32_t* cu, const int32_t* ctx, int P,
-                        int l, int g, const swiftkv_kv_pages* kv, float* logits, cudaStream_t s, bool host_io) {
+                        int l, int g, const swiftkv_kv_pages* kv, float* logits, cudaStream_t s, bool host_io,
+                        const int32_t* pos_off = nullptr) {
   RET(check_ready(m));
   if (l != m->l) return fail(SWIFTKV_EINVAL_L, "l=%d but the model was packed for l=%d", l, m->l);
   if (g != m->g) return fail(SWIFTKV_EINVAL_GROUP, "g=%d but the model was packed for g=%d", g, m->g);
@@ -1008,6 +1073,8 @@ static int prefill_impl(swiftkv_model* m, const int32_t* tokens, const int32_t* 
     if ((long long)c0 + n > (long long)kv->max_pages_per_seq * kPageSize)
       return fail(SWIFTKV_ENO_PAGES, "sequence %d needs %lld pages, block table holds %d", i,
                   ((long long)c0 + n + 15) / 16, kv->max_pages_per_seq);
+    if (pos_off && (pos_off[i] < 0 || (long long)pos_off[i] + c0 + n > (1LL << 30)))
+      return fail(SWIFTKV_EINVAL_SEQLENS, "pos_offsets[%d] = %d: positions outside [0, 2^30)", i, pos_off[i]);
   }
   const int T = cu[P];
   if ((long long)T * std::max(m->Fp, m->cfg.d) >= (1LL << 31)) return fail(SWIFTKV_EUNSUPPORTED, "batch too large");
@@ -1047,7 +1114,17 @@ static int prefill_impl(swiftkv_model* m, const int32_t* tokens, const int32_t* 
   // FP8 cache: prompt tiles attend over a bf16 expansion of the layer's cache (chunk rows
   // written by the quantize pass, cached prefixes expanded page by page before each layer)
   x.fp8 = kv->kv_dtype == 1;
-  x.expand = x.fp8 && !tiles.empty();
+  ServingPlan serving;
+  if (m->window > 0 || !m->score_pools.empty() || pos_off) {
+    RET(serving.make(m, cu, ctx, P, kv, m->l < m->cfg.L));
+    Arena size, arena;
+    serving.place(m, pos_off != nullptr, &size);
+    RET(reserve(m, size.used, s, &arena));
+    serving.place(m, pos_off != nullptr, &arena);
+    RET(serving.upload(pos_off, s));
+    x.serving = &serving;
+  }
+  x.expand = x.fp8 && !tiles.empty() && !x.serving;
   std::vector<int> deq;
   if (x.expand)
     for (int i = 0; i < P; ++i) {
@@ -1113,7 +1190,7 @@ static int prefill_impl(swiftkv_model* m, const int32_t* tokens, const int32_t* 
   RET(upload_split(x, hs_short, x.w.dint, &x.sp_short));
   RET(upload_split(x, hs_tail, x.w.dint + hs_short.ints(), &x.sp_rows));
   RET(upload_pools(x));
-  CK(launch_plan_prefill(x.w.cu, x.ctx, P, T, tok, m->cfg.vocab, kv->block_table, kv->max_pages_per_seq, kv->num_pages,
+  CK(launch_plan_prefill(x.w.cu, x.ctx, serving.offsets, P, T, tok, m->cfg.vocab, kv->block_table, kv->max_pages_per_seq, kv->num_pages,
                          x.w.positions, x.w.slots, x.w.last_idx, x.w.last_pos, m->status, s));
   }
   const auto& c = m->cfg;
@@ -1196,6 +1273,36 @@ int swiftkv_forward(swiftkv_model* m, const int32_t* tokens, const int32_t* cu_s
   return prefill_impl(m, tokens, cu_seqlens, ctx_lens, num_seqs, l, g, kv, logits, (cudaStream_t)stream, false);
 }
 
+int swiftkv_forward_at(swiftkv_model* m, const int32_t* tokens, const int32_t* cu_seqlens, const int32_t* ctx_lens,
+                       const int32_t* pos_offsets, int num_seqs, int l, int g, const swiftkv_kv_pages* kv, float* logits,
+                       swiftkv_stream stream) {
+  return prefill_impl(m, tokens, cu_seqlens, ctx_lens, num_seqs, l, g, kv, logits, (cudaStream_t)stream, false,
+                      pos_offsets);
+}
+
+int swiftkv_set_attention_window(swiftkv_model* m, int window, int sinks) {
+  if (!m) return fail(SWIFTKV_EINVAL, "null model");
+  if (window < 0 || sinks < 0) return fail(SWIFTKV_EINVAL, "negative window or sinks");
+  m->window = window;
+  m->sinks = window > 0 ? sinks : 0;
+  return SWIFTKV_OK;
+}
+
+int swiftkv_set_score_pools(swiftkv_model* m, float* const* scores, float decay) {
+  if (!m) return fail(SWIFTKV_EINVAL, "null model");
+  if (!scores) {
+    m->score_pools.clear();
+    return SWIFTKV_OK;
+  }
+  if (!(std::fabs(decay) <= 3.0e38f)) return fail(SWIFTKV_EINVAL, "decay is not finite");
+  for (int c = 0; c < m->C; ++c)
+    if (!scores[c] || (reinterpret_cast<uintptr_t>(scores[c]) & 15))
+      return fail(SWIFTKV_EINVAL, "null or misaligned score pool for cache %d", c);
+  m->score_pools.assign(scores, scores + m->C);
+  m->score_decay = decay;
+  return SWIFTKV_OK;
+}
+
 int swiftkv_decode_step(swiftkv_model* m, const int32_t* tokens, const int32_t* seq_lens, int B,
                         const swiftkv_kv_pages* kv, float* logits, int32_t* next_tokens, swiftkv_stream stream) {
   RET(check_ready(m));
@@ -1223,6 +1330,18 @@ int swiftkv_decode_step(swiftkv_model* m, const int32_t* tokens, const int32_t* 
   }
   const HostSplit hs = make_split(nk);
   x.fp8 = kv->kv_dtype == 1;
+  ServingPlan serving;
+  if (m->window > 0 || !m->score_pools.empty()) {
+    std::vector<int> one(B + 1);
+    for (int b = 0; b <= B; ++b) one[b] = b;
+    RET(serving.make(m, one.data(), seq_lens, B, kv, false));
+    Arena size, arena;
+    serving.place(m, false, &size);
+    RET(reserve(m, size.used, s, &arena));
+    serving.place(m, false, &arena);
+    RET(serving.upload(nullptr, s));
+    x.serving = &serving;
+  }
   RET(ensure_workspace(m, B, B, m->C, 1, skinny_part_bytes(m, B), &x.w, hs.ints(),
                        split_part_floats(hs.num_units(), m->cfg.n_q, m->cfg.d_head),
                        x.fp8 ? (size_t)B * std::max(2 * m->Nkv, m->Nwide) : 0));

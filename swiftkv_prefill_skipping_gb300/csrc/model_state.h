@@ -66,6 +66,9 @@ struct swiftkv_model {
   int rows_impl = 1;  // tail / decode rows after attention: 0 one chained launch, 1 a launch per GEMM / norm
   unsigned* chain_count = nullptr;  // grid-barrier arrivals of the chained launches (device)
   unsigned chain_base = 0;          // ... and their count so far (host)
+  int window = 0, sinks = 0;          // attention window of the model's layers (0: none)
+  std::vector<float*> score_pools;    // per cache, where the layers' attention weights are added (empty: off)
+  float score_decay = 1.f;
   // profiling (swiftkv_profile_begin/end)
   bool prof_on = false;
   struct Rec {

@@ -21,7 +21,8 @@ __global__ void upload_kernel(int* dst, IntBlob blob) {
     dst[i] = blob.v[i];
 }
 
-__global__ void plan_prefill_kernel(const int* __restrict__ cu, const int* __restrict__ ctx, int P, int T,
+__global__ void plan_prefill_kernel(const int* __restrict__ cu, const int* __restrict__ ctx,
+                                    const int* __restrict__ pos_off, int P, int T,
                                     const int* __restrict__ tokens,
                                     int vocab, const int* __restrict__ bt, int max_pages, int num_pages,
                                     int* positions, int* slots, int* last_idx, int* last_pos, int* status) {
@@ -39,11 +40,12 @@ __global__ void plan_prefill_kernel(const int* __restrict__ cu, const int* __res
     const int page = bt[(size_t)s * max_pages + (pos >> 4)];
     const bool ok = page >= 0 && page < num_pages;
     if (!ok) atomicOr(status, kStatusBadPage);
-    positions[t] = pos;
+    const int rope_pos = pos + (pos_off ? pos_off[s] : 0);
+    positions[t] = rope_pos;
     slots[t] = ok ? page * kPageSize + (pos & 15) : -1;
     if (pos == n - 1) {
       last_idx[s] = t;
-      last_pos[s] = pos;
+      last_pos[s] = rope_pos;
     }
     const int tok = tokens[t];
     if (tok < 0 || tok >= vocab) atomicOr(status, kStatusBadToken);
@@ -456,13 +458,13 @@ cudaError_t launch_v_tail(const bf16* v_pool, const int* block_table, int max_pa
   return cudaGetLastError();
 }
 
-cudaError_t launch_plan_prefill(const int* cu, const int* ctx, int P, int T, const int* tokens, int vocab,
+cudaError_t launch_plan_prefill(const int* cu, const int* ctx, const int* pos_off, int P, int T, const int* tokens, int vocab,
                                 const int* block_table, int max_pages, int num_pages, int* positions,
                                 int* slots, int* last_idx, int* last_pos, int* status,
                                 cudaStream_t stream) {
   if (T <= 0) return cudaSuccess;
   int blocks = (T + 255) / 256;
-  plan_prefill_kernel<<<blocks, 256, 0, stream>>>(cu, ctx, P, T, tokens, vocab, block_table, max_pages,
+  plan_prefill_kernel<<<blocks, 256, 0, stream>>>(cu, ctx, pos_off, P, T, tokens, vocab, block_table, max_pages,
                                                    num_pages, positions, slots, last_idx, last_pos,
                                                    status);
   return cudaGetLastError();
