@@ -7,7 +7,6 @@ libswiftkv.so. Every call checks the library's return code and raises
 from __future__ import annotations
 
 import ctypes as C
-from contextlib import nullcontext
 from dataclasses import dataclass
 from typing import Optional, Sequence
 
@@ -27,14 +26,10 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _stream_of(dev: torch.device, stream) -> int:
+    # dev.index is set: the devices here are those of CUDA tensors
     if stream is None and _raw_stream is not None:
         return _raw_stream(dev.index)
     return (stream if stream is not None else torch.cuda.current_stream(dev)).cuda_stream
-
-
-def _on(dev: torch.device):
-    """Makes dev the current device for a call, at no cost where it already is."""
-    return nullcontext() if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
 
 
 def _ptr(a) -> Optional[int]:
@@ -302,7 +297,7 @@ def _chunks(cu_seqlens, ctx_lens, kv: KVCache):
 def _rows_of(t: torch.Tensor, T: int, model: Model, dev, name: str) -> int:
     """Row stride of bf16 rows [T, n_q, d_h] (or [T, n_q * d_h]) whose heads are contiguous."""
     s, shape, stride = model.shape, t.shape, t.stride()
-    if t.dtype != torch.bfloat16 or t.device != dev or shape[0] != T or not (
+    if t.dtype is not torch.bfloat16 or t.device != dev or shape[0] != T or not (
             len(shape) == 3 and shape[1] == s.n_q and shape[2] == s.d_h and stride[2] == 1 and
             (s.n_q == 1 or stride[1] == s.d_h) or
             len(shape) == 2 and shape[1] == s.n_q * s.d_h and stride[1] == 1):
@@ -312,7 +307,7 @@ def _rows_of(t: torch.Tensor, T: int, model: Model, dev, name: str) -> int:
 
 def _flat(t: torch.Tensor, dtype, shape: tuple, dev, name: str) -> int:
     """Address of a contiguous tensor of this type and shape on dev."""
-    if t.dtype != dtype or tuple(t.shape) != shape or t.device != dev or not t.is_contiguous():
+    if t.dtype is not dtype or t.shape != shape or t.device != dev or not t.is_contiguous():
         raise ValueError(f"{name}: contiguous {dtype} {list(shape)} on {dev}")
     return t.data_ptr()
 
@@ -375,23 +370,22 @@ def evict(model: Model, kv: KVCache, scores: torch.Tensor, seq_lens: Sequence[in
     base = _flat(scores, torch.float32, pool if cache is not None else (n,) + pool, dev, "scores")
     dst, width = None, 0
     if dst_block_table is not None:
-        width = dst_block_table.shape[-1]
-        if dst_block_table.dim() != 2 or dst_block_table.shape[0] < P:
+        rows, width = dst_block_table.shape if dst_block_table.dim() == 2 else (-1, 0)
+        if rows < P:
             raise ValueError(f"dst_block_table: int32 [{P}, pages]")
-        dst = _flat(dst_block_table, torch.int32, tuple(dst_block_table.shape), dev, "dst_block_table")
+        dst = _flat(dst_block_table, torch.int32, (rows, width), dev, "dst_block_table")
+    shape = (n, P, s.n_kv, keep)
     if kept is None:
-        kept = torch.empty((n, P, s.n_kv, keep), dtype=torch.int32, device=dev)
-    kp = _flat(kept, torch.int32, (n, P, s.n_kv, keep), dev, "kept")
+        kept = torch.empty(shape, dtype=torch.int32, device=dev)
+        kp = kept.data_ptr()
+    else:
+        kp = _flat(kept, torch.int32, shape, dev, "kept")
     step, first = 4 * kv.num_pages * s.n_kv * 16, cache or 0
-    ptrs = (C.c_void_p * kv.num_caches)()
-    for c in range(n):
-        ptrs[first + c] = base + c * step
+    ptrs = (C.c_void_p * kv.num_caches)(*[base + (c - first) * step if 0 <= c - first < n else None
+                                          for c in range(kv.num_caches)])
     B.check(B.lib().swiftkv_evict(model.handle, -1 if cache is None else cache, kv.pages_ref, ptrs, B.host(sl), P, keep,
                                   sinks, recent, dst, width, kp, _stream_of(dev, stream)))
     return kept
-
-
-_SAMPLING = (("temperature", torch.float32), ("top_k", torch.int32), ("top_p", torch.float32), ("min_p", torch.float32))
 
 
 def sample(logits: torch.Tensor, u: torch.Tensor, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0,
@@ -400,22 +394,37 @@ def sample(logits: torch.Tensor, u: torch.Tensor, temperature=1.0, top_k=0, top_
     uniform numbers u [P] in [0, 1). temperature, top_k, top_p and min_p are numbers, or one value
     per row as tensors on the same device (float32; top_k int32); temperature <= 0 takes the argmax,
     top_k <= 0, top_p >= 1 and min_p <= 0 are off. Enqueued without synchronising."""
-    if logits.dim() != 2 or logits.dtype != torch.float32 or not logits.is_cuda:
+    if logits.dim() != 2 or logits.dtype is not torch.float32 or not logits.is_cuda:
         raise ValueError("logits: float32 CUDA [P, V]")
     (P, V), (ld, step), dev = logits.shape, logits.stride(), logits.device
     if P <= 1:
         ld = V
     if V < 1 or (V > 1 and step != 1) or ld < V:
         raise ValueError("logits: at least one column, contiguous within a row, rows that do not overlap")
-    s, vec = B.Sampling(None, None, None, None, 1.0, 0, 1.0, 0.0), (P,)
-    for (name, dtype), value in zip(_SAMPLING, (temperature, top_k, top_p, min_p)):
-        if isinstance(value, torch.Tensor):
-            setattr(s, name, _flat(value, dtype, vec, dev, name))
-        else:
-            setattr(s, name + "_all", int(value) if dtype == torch.int32 else float(value))
+    vec, f32, s = (P,), torch.float32, B.Sampling()
+    if isinstance(temperature, torch.Tensor):
+        s.temperature = _flat(temperature, f32, vec, dev, "temperature")
+    else:
+        s.temperature_all = temperature
+    if isinstance(top_k, torch.Tensor):
+        s.top_k = _flat(top_k, torch.int32, vec, dev, "top_k")
+    else:
+        s.top_k_all = int(top_k)
+    if isinstance(top_p, torch.Tensor):
+        s.top_p = _flat(top_p, f32, vec, dev, "top_p")
+    else:
+        s.top_p_all = top_p
+    if isinstance(min_p, torch.Tensor):
+        s.min_p = _flat(min_p, f32, vec, dev, "min_p")
+    else:
+        s.min_p_all = min_p
     if out is None:
         out = torch.empty(vec, dtype=torch.int32, device=dev)
-    with _on(dev):
-        B.check(B.lib().swiftkv_sample(logits.data_ptr(), P, V, ld, C.byref(s), _flat(u, torch.float32, vec, dev, "u"),
-                                       _flat(out, torch.int32, vec, dev, "out"), _stream_of(dev, stream)))
+    args = (logits.data_ptr(), P, V, ld, s, _flat(u, f32, vec, dev, "u"), _flat(out, torch.int32, vec, dev, "out"),
+            _stream_of(dev, stream))
+    if torch.cuda.current_device() == dev.index:
+        B.check(B.lib().swiftkv_sample(*args))
+    else:
+        with torch.cuda.device(dev):
+            B.check(B.lib().swiftkv_sample(*args))
     return out
