@@ -40,6 +40,7 @@ constexpr int ST = 512;            // threads per CTA
 constexpr int SWARPS = ST / 32;
 constexpr int NB = 1024;           // histogram bins
 constexpr int TAB = 256;           // 2^(j / TAB) table
+constexpr int MAXCAND = 2048;      // elements of one bin that one CTA searches (in the room of its bins)
 constexpr int FX = 44;             // fixed-point weights: w * 2^FX (360448 of them, times 2^(1/256), stay below 2^63)
 constexpr int kMaxSlice = 45056;   // floats of a row one CTA holds (176 KB)
 constexpr int kMaxVocab = 8 * kMaxSlice;
@@ -84,6 +85,7 @@ struct alignas(16) Share {  // the slice behind it is written 16 bytes at a time
   unsigned limb[3][NB];         // 16-bit limbs of the bins while they are summed
   u64 warp_mass[SWARPS];
   u64 sums[NB];                 // the cluster's sums of the bins this CTA scans
+  u64 part[SWARPS];
   // the row's settings
   float set_t, set_p, set_m, set_u, set_ch, set_cl;
   int set_k;
@@ -101,7 +103,9 @@ struct alignas(16) Share {  // the slice behind it is written 16 bytes at a time
   u64 x_mass, x_sum;
   // the bin that a search found
   unsigned d_bin;
-  u64 d_before;
+  u64 d_before, d_inside;
+  // a bin's elements on their way to one key: counted and kept by the cluster's first CTA
+  unsigned cand;
 };
 
 __device__ __forceinline__ unsigned cluster_rank() {
@@ -131,6 +135,15 @@ __device__ __forceinline__ u64 ld_remote(const u64* p, unsigned rank) {
   u64 v;
   asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(remote(p, rank)) : "memory");
   return v;
+}
+
+__device__ __forceinline__ unsigned add_remote(unsigned* p, unsigned rank, unsigned v) {
+  unsigned old;
+  asm volatile("atom.shared::cluster.add.u32 %0, [%1], %2;" : "=r"(old) : "r"(remote(p, rank)), "r"(v) : "memory");
+  return old;
+}
+__device__ __forceinline__ void st_remote(float* p, unsigned rank, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(remote(p, rank)), "f"(v) : "memory");
 }
 
 // Order-preserving map of floats to unsigned (no NaN); -0 and +0 share a key.
@@ -295,6 +308,7 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const SampleParams p) {
     }
   }
   if (tid < TAB) sh.tab[tid] = entry;
+  if (tid == 0) sh.cand = 0;
   if (tid == ST - 1) {
     const float t = p.temperature ? p.temperature[r] : p.temperature_all;
     sh.set_t = t;
@@ -387,11 +401,11 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const SampleParams p) {
     sync_all();
   };
   // The first bin, in descending order of the logits, at which the cluster's running sum reaches
-  // `want`; the sum above it is returned in `before`. fraction >= 0: want is that part of all the
+  // `want`; the sum above it is returned in `before`, the bin's own in `inside`. fraction >= 0: want is that part of all the
   // bins (at least 1). Each CTA sums its NB / C bins over the cluster's copies, so a bin crosses
   // between CTAs once (all CTAs reading all bins took 3 us a search), and only the totals and the
   // decision are exchanged after that.
-  auto find = [&](u64& want, float fraction, u64& before) -> int {
+  auto find = [&](u64& want, float fraction, u64& before, u64& inside) -> int {
     constexpr int BPC = NB / C;
     constexpr int PER = ST >= BPC ? ST / BPC : 1;  // threads per bin, each with C / PER copies
 #pragma unroll
@@ -454,6 +468,7 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const SampleParams p) {
           if (want <= x + v) {
             sh.d_bin = (unsigned)(owner * BPC + lane * PL + e);
             sh.d_before = x;
+            sh.d_inside = v;
             break;
           }
           x += v;
@@ -461,16 +476,103 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const SampleParams p) {
     }
     __syncthreads();
     before = sh.d_before;
+    inside = sh.d_inside;
     return (int)sh.d_bin;
   };
-  // "The threshold lies in bin `bin` of a first histogram" to one key; `before` becomes the
-  // count or mass above that key.
-  auto refine = [&](bool by_mass, u64 want, int bin, u64& before) -> unsigned {
+  // "The threshold lies in bin `bin` of a first histogram" to one key; `before` and `inside` become
+  // the count or mass above that key and at it. Lists hold no element below the bin.
+  auto refine = [&](bool by_mass, u64 want, int bin, u64& before, u64& inside) -> unsigned {
     // keys that can fall into the bin: its ends, moved out by more than bin_of can round
     const float width = 1.f / bin_scale, slack = 4e-6f * ((float)(bin + 1) * width + fabsf(mx));
     const float top = mx - (float)bin * width + slack, low = mx - (float)(bin + 1) * width - slack;
     unsigned hi = top < mx ? key_of(top) : key_of(mx);
     unsigned lo = bin < NB - 1 && low > -FLT_MAX ? key_of(low) : 0u;  // NaN and infinite ends: everything
+    // The bin's elements, if they are few, meet in the first CTA, which finishes the search alone: a
+    // round over the cluster costs it two barriers and an exchange of bins.
+    for (int i0 = s0; i0 < s1; i0 += 32) {
+      const int i = i0 + lane;
+      const float l = i < s1 ? row[i] : 0.f;
+      const bool in = i < s1 && bin_of(l) == bin;
+      const unsigned who = __ballot_sync(0xffffffffu, in);
+      if (!who) continue;
+      unsigned at = 0;
+      if (lane == 0) at = add_remote(&sh.cand, 0, __popc(who));
+      at = __shfl_sync(0xffffffffu, at, 0) + __popc(who & ((1u << lane) - 1));
+      if (in && at < MAXCAND) st_remote(reinterpret_cast<float*>(sh.mass) + at, 0, l);
+    }
+    sync_all();
+    const unsigned cands = ld_remote(&sh.cand, 0);
+    if (cands <= MAXCAND) {
+      if (rank == 0) {
+        constexpr int PER = MAXCAND / ST;
+        unsigned k[PER];
+        u64 w[PER];
+#pragma unroll
+        for (int e = 0; e < PER; ++e) {
+          const int i = tid + e * ST;
+          const float l = i < (int)cands ? reinterpret_cast<const float*>(sh.mass)[i] : 0.f;
+          k[e] = i < (int)cands ? key_of(l) : 0u;
+          w[e] = i < (int)cands ? (by_mass ? weight_fx(l, sc, sh.tab) : 1ull) : 0ull;
+        }
+        while (lo < hi) {  // ten bits of the key a round, with this CTA's bins alone
+          const int s = max(0, 22 - __clz(hi - lo));  // (hi - lo) >> s < NB
+          clear();
+#pragma unroll
+          for (int e = 0; e < PER; ++e)
+            if (w[e] && k[e] >= lo && k[e] <= hi) {
+              if (by_mass) add_mass((int)((hi - k[e]) >> s), w[e]);
+              else atomicAdd(&sh.limb[0][(hi - k[e]) >> s], 1u);
+            }
+          __syncthreads();
+          static_assert(NB == 2 * ST, "two bins a thread");
+          u64 v[2], x = 0;
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int b = 2 * tid + e;
+            x += v[e] = (u64)sh.limb[0][b] + ((u64)sh.limb[1][b] << 16) + ((u64)sh.limb[2][b] << 32);
+          }
+          u64 upto = x;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const u64 y = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += y;
+          }
+          if (lane == 31) sh.part[warp] = upto;
+          if (tid == 0) sh.d_bin = 0;
+          __syncthreads();
+          u64 c = before + upto - x;
+#pragma unroll
+          for (int i = 0; i < SWARPS - 1; ++i) c += i < warp ? sh.part[i] : 0ull;
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            if (c < want && want <= c + v[e]) {
+              sh.d_bin = (unsigned)(2 * tid + e);
+              sh.d_before = c;
+              sh.d_inside = v[e];
+            }
+            c += v[e];
+          }
+          __syncthreads();
+          hi -= sh.d_bin << s;
+          lo = max(lo, hi - ((1u << s) - 1));
+          before = sh.d_before;
+          inside = sh.d_inside;
+          __syncthreads();  // read before the next round writes
+        }
+        if (tid == 0) {
+          sh.d_bin = lo;
+          sh.d_before = before;
+          sh.d_inside = inside;
+          sh.cand = 0;
+        }
+      }
+      sync_all();
+      before = ld_remote(&sh.d_before, 0);
+      inside = ld_remote(&sh.d_inside, 0);
+      return ld_remote(&sh.d_bin, 0);
+    }
+    sync_all();  // everyone has read the count
+    if (rank == 0 && tid == 0) sh.cand = 0;
     for (int it = 0; it < 5 && lo < hi; ++it) {  // ten bits of the key a round
       const int s = max(0, 22 - __clz(hi - lo));  // (hi - lo) >> s < NB
       clear();
@@ -484,13 +586,12 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const SampleParams p) {
         }
       }
       publish();
-      const unsigned b = (unsigned)find(want, -1.f, before);
+      const unsigned b = (unsigned)find(want, -1.f, before, inside);
       hi -= b << s;
       lo = max(lo, hi - ((1u << s) - 1));
     }
     return lo;
   };
-
   // Keeps the elements that pass `keep` (all lanes call it), each warp's segment in place.
   auto squeeze = [&](auto keep) {
     int out = s0;
@@ -544,16 +645,17 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const SampleParams p) {
     squeeze([&](bool in, float l) { return in && bin_of(l) <= bin; });
   };
 
+  int list_bin = -1;  // the lists hold the elements of the bins up to this one
   if (use_k) {
     clear();
 #pragma unroll 4
     for (int i = s0 + lane; i < s1; i += 32) atomicAdd(&sh.limb[0][bin_of(row[i])], 1u);
     publish();
-    u64 want = (u64)tk, before = 0;
-    const int bin = find(want, -1.f, before);
+    u64 want = (u64)tk, before = 0, inside = 0;
+    const int bin = find(want, -1.f, before, inside);
     drop_below(bin);
-    pre.key = refine(false, want, bin, before);
-    pre.ties = (unsigned)(want - before);
+    pre.key = refine(false, want, bin, before, inside);
+    pre.ties = want - before < inside ? (unsigned)(want - before) : UINT_MAX;
     compact();
   }
   if (use_p) {
@@ -565,15 +667,18 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const SampleParams p) {
       if (w) add_mass(bin_of(l), w);
     });
     publish();
-    u64 want = 0, before = 0;
-    const int bin = find(want, tp, before);
+    u64 want = 0, before = 0, inside = 0;
+    const int bin = find(want, tp, before, inside);
     drop_below(bin);
     Prefix pp;
-    pp.key = refine(true, want, bin, before);
-    const u64 w = weight_fx(value_of(pp.key), sc, sh.tab);
-    const u64 ties = w ? (want - before + w - 1) / w : UINT_MAX;
-    pp.ties = ties > UINT_MAX ? UINT_MAX : (unsigned)ties;
+    pp.key = refine(true, want, bin, before, inside);
+    pp.ties = UINT_MAX;
+    if (want - before < inside) {  // not all of the key's elements
+      const u64 w = weight_fx(value_of(pp.key), sc, sh.tab), ties = w ? (want - before + w - 1) / w : UINT_MAX;
+      if (ties * w < inside) pp.ties = (unsigned)ties;
+    }
     if (pp.shorter(pre)) pre = pp;
+    if (!use_k) list_bin = bin;
   }
   if (mp > 0.f) {
     // the smallest key, up to the maximum's, whose weight is min_p of the maximum's: weights grow
@@ -602,11 +707,15 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const SampleParams p) {
       pre.ties = UINT_MAX;
     }
   }
-  if (use_p || mp > 0.f) compact();
+  // After top-p alone nearly all that is left is kept: the passes below skip the rest instead of
+  // moving everything once more.
+  const bool listed = list_bin >= 0 && pre.ties == UINT_MAX;
+  if ((use_p || mp > 0.f) && !listed) compact();
 
   // ---- the draw: running sums over the kept ids in ascending order
   u64 sum = 0;
-  each([&](float l, auto weight) { sum += weight(l); });
+  if (listed) each([&](float l, auto weight) { sum += key_of(l) >= pre.key ? weight(l) : 0ull; });
+  else each([&](float l, auto weight) { sum += weight(l); });
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   if (lane == 0) {
@@ -649,9 +758,12 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const SampleParams p) {
   }
   const int w0 = min(n, win * seg), w1 = w0 + sh.len[win];
   const int chunks = (w1 - w0 + 31) / 32;
+  auto mass_at = [&](int i) -> u64 {
+    return i < w1 && (!listed || key_of(row[i]) >= pre.key) ? weight_fx(row[i], sc, sh.tab) : 0ull;
+  };
   for (int c = warp; c < chunks; c += SWARPS) {
     const int i = w0 + 32 * c + lane;
-    u64 x = i < w1 ? weight_fx(row[i], sc, sh.tab) : 0ull;
+    u64 x = mass_at(i);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
     if (lane == 0) sh.chunk_mass[c] = x;
@@ -679,7 +791,7 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const SampleParams p) {
       before = __shfl_sync(0xffffffffu, upto, 31);
     }
     const int i = w0 + 32 * c + lane;
-    const u64 upto = before + scan(i < w1 ? weight_fx(row[i], sc, sh.tab) : 0ull);
+    const u64 upto = before + scan(mass_at(i));
     const unsigned hit = __ballot_sync(0xffffffffu, upto >= target);
     const int at = 32 * c + __ffs(hit) - 1;  // within the segment's kept elements
     if (lane == 0) {
@@ -690,13 +802,17 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const SampleParams p) {
   if (whole) return;
   // the segment was compacted: its pos-th kept element, counted in the logits again
   const int e1 = min(n, win * seg + seg), all = (e1 - w0 + 31) / 32;
+  Prefix in_list = pre;
+  if (listed) in_list = Prefix{1u, UINT_MAX};  // its elements have key 2, the others 0
   auto key_in = [&](int c) {
     const int i = w0 + 32 * c + lane;
-    return i < e1 ? key_of(fmaxf(src[i], -INFINITY)) : 0u;  // 0: below every key
+    if (i >= e1) return 0u;  // below every key
+    const float l = fmaxf(src[i], -INFINITY);
+    return listed ? (bin_of(l) <= list_bin ? 2u : 0u) : key_of(l);
   };
   for (int c = warp; c < all; c += SWARPS) {
     const unsigned k = key_in(c);
-    const unsigned gt = __ballot_sync(0xffffffffu, k > pre.key), eq = __ballot_sync(0xffffffffu, k == pre.key && k);
+    const unsigned gt = __ballot_sync(0xffffffffu, k > in_list.key), eq = __ballot_sync(0xffffffffu, k == in_list.key && k);
     if (lane == 0) {
       sh.chunk_gt[c] = __popc(gt);
       sh.chunk_eq[c] = __popc(eq);
@@ -711,14 +827,14 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const SampleParams p) {
       const bool in = c0 + lane < all;
       const unsigned gt = in ? sh.chunk_gt[c0 + lane] : 0u, eq = in ? sh.chunk_eq[c0 + lane] : 0u;
       const unsigned eq_to = (unsigned)scan(eq) + ties;  // ties up to and with the lane's chunk
-      const unsigned kept_to = (unsigned)scan(gt + min(eq_to, pre.ties) - min(eq_to - eq, pre.ties));
+      const unsigned kept_to = (unsigned)scan(gt + min(eq_to, in_list.ties) - min(eq_to - eq, in_list.ties));
       const unsigned hit = __ballot_sync(0xffffffffu, kept_to > (unsigned)left);
       if (hit) {
         const int who = __ffs(hit) - 1;
         const unsigned skip = who ? __shfl_sync(0xffffffffu, kept_to, who - 1) : 0u;
         unsigned t0 = who ? __shfl_sync(0xffffffffu, eq_to, who - 1) : ties;
         const int i = w0 + 32 * (c0 + who) + lane;
-        unsigned kept = __ballot_sync(0xffffffffu, pre.keeps(i < e1, key_in(c0 + who), t0, lane));
+        unsigned kept = __ballot_sync(0xffffffffu, in_list.keeps(i < e1, key_in(c0 + who), t0, lane));
         for (left -= (int)skip; left > 0; --left) kept &= kept - 1;
         if (lane == 0) p.tokens[r] = base + w0 + 32 * (c0 + who) + __ffs(kept) - 1;
         break;
