@@ -9,9 +9,10 @@
 // of mma.sync m16n8k16 and the chunk's rows x heads its columns, so a key's sum is a sum along
 // the accumulator's row: one register per key and two shuffles a page.
 //
-// weights_tc_kernel (longer chunks): S^T = K Q^T on tcgen05. An item is a 128-key tile of one
+// weights_tc_kernel (longer chunks): S^T = K Q^T on tcgen05. An item is a 256-key tile of one
 // (sequence, KV head); the tile stays in shared memory while 128-row query tiles of every head of
-// the group stream past it. The transposed product gives each of the 128 epilogue threads one
+// the group stream past it, each used for both halves (with 128 keys an item, the query tiles' way from
+// L2, 8 TB/s, was the bound). The transposed product gives each of the 128 epilogue threads one
 // key: it reads its row of S from TMEM, adds exp2(s c - lse_column) over the columns, and keeps
 // the key's sum in a register for the whole item; no score leaves the SM. Three warpgroups take
 // alternate tiles, so one reads TMEM and computes exponentials (the bound: one per score) while
@@ -233,21 +234,21 @@ __global__ void __launch_bounds__(RW * 32, 1) weights_rows_kernel(const WeightsA
 
 using namespace tc;
 
-constexpr int BK = 128;        // keys per item
+constexpr int BK = 128;        // keys per half of an item: an item is kWeightTile = 2 BK keys
 constexpr int BQ = 128;        // query rows per tile
 constexpr int QST = 4;         // query tiles in flight
-constexpr int SBUF = 4;        // S accumulators (128 TMEM columns each)
-constexpr int WGS = 3;         // epilogue warpgroups
-constexpr int WT = 64 + WGS * 128;  // TMA, MMA, epilogue warps
-constexpr int EPI0 = 2;
+constexpr int SBUF = 2;        // S accumulators of a half (128 TMEM columns each)
+constexpr int TMEM_COLS = 2 * SBUF * BQ;
+constexpr int EPI0 = 4;        // warp 0 loads Q, 1 and 2 issue a half's products, 3 loads K; then a warpgroup
+constexpr int WT = 32 * EPI0 + 2 * SBUF * 128;  // for each accumulator
 
 struct WCtrl {
-  uint64_t k_full[2], k_empty[2], q_full[QST], q_empty[QST], s_full[SBUF], s_empty[SBUF], fin;
+  uint64_t k_full[2], k_empty[2], q_full[QST], q_empty[QST], s_full[2][SBUF], s_empty[2][SBUF], fin;
   uint32_t tmem_base;
   int abort;
   int pend_k[2], pend_q[QST];
-  alignas(16) float lse[WGS][2][BQ];  // [warpgroup][parity], read 16 bytes at a time
-  float comb[2][WGS - 1][BK];  // the other warpgroups' sums, by item parity
+  alignas(16) float lse[2 * SBUF][2][BQ];  // [warpgroup][parity], read 16 bytes at a time
+  float comb[2][2][BK];                    // the second warpgroups' sums: [item parity][half]
 };
 
 template <int D>
@@ -281,7 +282,7 @@ __device__ __forceinline__ bool w_item(long long it, const int* __restrict__ til
   const int t = (int)(w / a.n_kv);
   I.kvh = (int)(w - (long long)t * a.n_kv);
   I.s = tiles[2 * t];
-  I.key0 = tiles[2 * t + 1] * BK;
+  I.key0 = tiles[2 * t + 1] * kWeightTile;
   const int *cu = a.lists + a.o_cu, *ctx = a.lists + a.o_ctx;
   I.seq0 = cu[I.s];
   I.n = cu[I.s + 1] - I.seq0;
@@ -291,7 +292,7 @@ __device__ __forceinline__ bool w_item(long long it, const int* __restrict__ til
   const int lo = max(0, I.key0 - I.c0);
   long long hi = I.n;
   I.sink = a.window > 0 && I.key0 < a.sinks;
-  if (a.window > 0 && !I.sink) hi = min(hi, (long long)I.key0 + BK - 1 + a.window - I.c0);
+  if (a.window > 0 && !I.sink) hi = min(hi, (long long)I.key0 + kWeightTile - 1 + a.window - I.c0);
   I.qt0 = lo / BQ;
   I.qt1 = hi > lo ? (int)((hi + BQ - 1) / BQ) : I.qt0;
   return true;
@@ -324,23 +325,23 @@ __global__ void __launch_bounds__(WT, 1) weights_tc_kernel(const __grid_constant
       mbar_init(bar(ctl->k_full[i]), 1);
       mbar_init(bar(ctl->k_empty[i]), 1);
       ctl->pend_k[i] = -1;
+      for (int j = 0; j < SBUF; ++j) {
+        mbar_init(bar(ctl->s_full[i][j]), 1);
+        mbar_init(bar(ctl->s_empty[i][j]), 128);
+      }
     }
     for (int i = 0; i < QST; ++i) {
       mbar_init(bar(ctl->q_full[i]), 1);
-      mbar_init(bar(ctl->q_empty[i]), 1);
+      mbar_init(bar(ctl->q_empty[i]), 2);
       ctl->pend_q[i] = -1;
     }
-    for (int i = 0; i < SBUF; ++i) {
-      mbar_init(bar(ctl->s_full[i]), 1);
-      mbar_init(bar(ctl->s_empty[i]), 128);
-    }
-    mbar_init(bar(ctl->fin), 1);
+    mbar_init(bar(ctl->fin), 2);
     ctl->abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&ctl->tmem_base)),
-                 "r"(SBUF * BQ)
+                 "r"(TMEM_COLS)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
@@ -355,32 +356,11 @@ __global__ void __launch_bounds__(WT, 1) weights_tc_kernel(const __grid_constant
       bool ok = true;
       unsigned g = 0;  // query tiles so far (only remainders and low quotient bits are used)
       for (long long it = 0; ok && w_item(it, tiles, n_items, a, I); ++it) {
-        const int kb = (int)(it & 1);
-        const uint32_t kph = (uint32_t)((it >> 1) & 1);
-        int pg[BK / kPageSize];
-#pragma unroll
-        for (int p = 0; p < BK / kPageSize; ++p) {
-          const int key = I.key0 + p * kPageSize;
-          // pages without a key that some row sees are not read
-          const bool need = key < I.nk && (key + kPageSize > window_begin(I.c0, a.window) || key < a.sinks);
-          pg[p] = need ? bt_k[(size_t)I.s * a.max_pages + (key >> 4)] : -1;
-        }
-        if (!mbar_wait(bar(ctl->k_empty[kb]), kph ^ 1, abort_flag)) break;
-        mbar_expect_tx(bar(ctl->k_full[kb]), TILE);
-        ctl->pend_k[kb] = (int)kph;
-#pragma unroll
-        for (int p = 0; p < BK / kPageSize; ++p) {
-          const bool valid = pg[p] >= 0 && pg[p] < pages_k;
-          const int row = valid ? (pg[p] * a.n_kv + I.kvh) * kPageSize : pages_k * a.n_kv * kPageSize;  // past the end: zeros
-#pragma unroll
-          for (int hf = 0; hf < HALVES; ++hf)
-            tma_load_2d(sK + kb * TILE + hf * HALF + p * 2048, &tmK, hf * 64, row, bar(ctl->k_full[kb]));
-        }
         for (int qt = I.qt0; ok && qt < I.qt1; ++qt)
           for (int h = 0; h < G; ++h, ++g) {
             const int st = (int)(g % QST);
             const uint32_t ph = (uint32_t)((g / QST) & 1);
-            if (!mbar_wait(bar(ctl->q_empty[st]), ph ^ 1, abort_flag)) {
+            if (!mbar_wait_ready(bar(ctl->q_empty[st]), ph ^ 1, abort_flag)) {
               ok = false;
               break;
             }
@@ -393,64 +373,92 @@ __global__ void __launch_bounds__(WT, 1) weights_tc_kernel(const __grid_constant
           }
       }
     }
-  } else if (warp == 1) {
-    if (lane == 0) {
-      // descriptors of the first K buffer and Q stage; an offset in bytes adds its sixteenth
-      const uint64_t k0 = sdesc(sK), q0 = sdesc(sQ);
-      bool ok = true;
-      unsigned g = 0;  // only its remainders and low quotient bits are used
-      for (long long it = 0; ok && w_item(it, tiles, n_items, a, I); ++it) {
-        const int kb = (int)(it & 1);
-        if (!mbar_wait(bar(ctl->k_full[kb]), (uint32_t)((it >> 1) & 1), abort_flag)) break;
-        ctl->pend_k[kb] = -1;
-        const int tiles_here = (I.qt1 - I.qt0) * G;
-        for (int t = 0; t < tiles_here; ++t, ++g) {
-          const int st = (int)(g % QST), sb = (int)(g % SBUF);
-          if (!mbar_wait(bar(ctl->q_full[st]), (uint32_t)((g / QST) & 1), abort_flag)) {
-            ok = false;
-            break;
-          }
+  } else if (warp == 3) {  // a lane a page
+    bool ok = true;
+    for (long long it = 0; ok && w_item(it, tiles, n_items, a, I); ++it) {
+      const int key = I.key0 + lane * kPageSize;
+      // pages without a key that some row sees are not read
+      const bool need = lane < kWeightTile / kPageSize && key < I.nk &&
+                        (key + kPageSize > window_begin(I.c0, a.window) || key < a.sinks);
+      const int page = need ? bt_k[(size_t)I.s * a.max_pages + (key >> 4)] : -1;
+      const int row = page >= 0 && page < pages_k ? (page * a.n_kv + I.kvh) * kPageSize
+                                                  : pages_k * a.n_kv * kPageSize;  // past the end: zeros
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        ok = ok && mbar_wait_ready(bar(ctl->k_empty[half]), (uint32_t)(it & 1) ^ 1, abort_flag);
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        if (lane == 0) {
+          mbar_expect_tx(bar(ctl->k_full[half]), TILE);
+          ctl->pend_k[half] = (int)(it & 1);
+        }
+        __syncwarp();
+        const int p = lane - half * (BK / kPageSize);
+        if (p >= 0 && p < BK / kPageSize) {
+#pragma unroll
+          for (int hf = 0; hf < HALVES; ++hf)
+            tma_load_2d(sK + half * TILE + hf * HALF + p * 2048, &tmK, hf * 64, row, bar(ctl->k_full[half]));
+        }
+        __syncwarp();
+      }
+    }
+  } else if (warp < EPI0) {  // the products of half w: the whole warp waits, one lane issues
+    const int w = warp - 1;
+    // descriptors of this half's keys and of the first Q stage; an offset in bytes adds its sixteenth
+    const uint64_t k0 = sdesc(sK + w * TILE), q0 = sdesc(sQ);
+    bool ok = true;
+    unsigned g = 0;  // query tiles so far
+    for (long long it = 0; ok && w_item(it, tiles, n_items, a, I); ++it) {
+      const int tiles_here = (I.qt1 - I.qt0) * G;
+      const uint32_t kph = (uint32_t)(it & 1);
+      if (!(ok = __all_sync(0xffffffffu, mbar_wait_ready(bar(ctl->k_full[w]), kph, abort_flag)))) break;
+      if (lane == 0) ctl->pend_k[w] = -1;
+      for (int t = 0; t < tiles_here; ++t, ++g) {
+        const int st = (int)(g % QST), sb = (int)(g % SBUF);
+        const uint32_t b0 = bar(ctl->s_empty[w][sb]), b1 = bar(ctl->q_full[st]), p0 = (g / SBUF & 1) ^ 1, p1 = g / QST & 1;
+        const bool free = mbar_test_wait(b0, p0), loaded = mbar_test_wait(b1, p1);  // both tests in flight
+        ok = (free || mbar_wait(b0, p0, abort_flag)) && (loaded || mbar_wait(b1, p1, abort_flag));
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        tc_fence_after();
+        if (elect_lane()) {
           ctl->pend_q[st] = -1;
-          if (!mbar_wait(bar(ctl->s_empty[sb]), (uint32_t)((g / SBUF) & 1) ^ 1, abort_flag)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint64_t k = k0 + kb * (TILE / 16), q = q0 + st * (TILE / 16);
+          const uint32_t d = tmem + (w * SBUF + sb) * BQ;
+          const uint64_t q = q0 + st * (TILE / 16);
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
             const int off = ((kk >> 2) * HALF + (kk & 3) * 32) / 16;
-            tc_mma(tmem + sb * BQ, k + off, q + off, IDESC, kk != 0);
+            tc_mma(d, k0 + off, q + off, IDESC, kk != 0);
           }
+          tc_commit(bar(ctl->s_full[w][sb]));
           tc_commit(bar(ctl->q_empty[st]));
-          tc_commit(bar(ctl->s_full[sb]));
+          if (t + 1 == tiles_here) tc_commit(bar(ctl->k_empty[w]));
         }
-        if (ok) {
-          if (tiles_here > 0) tc_commit(bar(ctl->k_empty[kb]));
-          else mbar_arrive(bar(ctl->k_empty[kb]));
-        }
+        __syncwarp();
       }
+      if (tiles_here == 0 && lane == 0) mbar_arrive(bar(ctl->k_empty[w]));  // nothing sees the keys
     }
   } else {
-    const int wg = (warp - EPI0) >> 2;
+    static_assert(SBUF == 2, "");
+    // this warpgroup's half of the keys, and the parity of its tiles
+    const int wg = (warp - EPI0) >> 2, half = wg >> 1, sb = wg & 1;
     const int quarter = warp & 3;  // the TMEM lanes this warp may access
     const int r = quarter * 32 + lane;
-    const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
+    const uint32_t s_addr = tmem + ((uint32_t)(quarter * 32) << 16) + wg * BQ;
     auto wg_sync = [&]() { asm volatile("bar.sync %0, 128;" ::"r"(1 + wg) : "memory"); };
-    unsigned g = 0;
-    int turn = 0;  // this warpgroup's tiles so far: parity of its lse buffer
+    unsigned g = 0;  // query tiles so far
     bool ok = true;
     for (long long it = 0; w_item(it, tiles, n_items, a, I); ++it) {
-      const int key = I.key0 + r;
-      // whether some row sees the key: the first one's window reaches back furthest
+      // this thread's key: whether some row sees it (the first one's window reaches back furthest),
+      // and the score's scale
+      const int key0 = I.key0 + half * BK, key = key0 + r;
       const bool seen = key < I.nk && (key >= window_begin(I.c0, a.window) || key < a.sinks);
-      const int page = seen ? bt_k[(size_t)I.s * a.max_pages + (key >> 4)] : -1;
       float c = scale_log2;
-      if (kscale) c *= page >= 0 && page < pages_k ? kscale[((size_t)page * a.n_kv + I.kvh) * kPageSize + (key & 15)] : 0.f;
+      if (kscale && seen) {
+        const int page = bt_k[(size_t)I.s * a.max_pages + (key >> 4)];
+        c *= page >= 0 && page < pages_k ? kscale[((size_t)page * a.n_kv + I.kvh) * kPageSize + (key & 15)] : 0.f;
+      }
       const int tiles_here = (I.qt1 - I.qt0) * G;
-      float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      // tiles alternate between the warpgroups over all items; (qt, h): tile t's rows and head
-      int t = (int)((wg + WGS - g % WGS) % WGS), qt = I.qt0, h = t;
+      float acc[4] = {0.f, 0.f, 0.f, 0.f};
+      int t = (int)((sb + g) & 1), qt = I.qt0, h = t;  // the rows and head of the next tile
       auto settle = [&]() {
         while (h >= G) {
           h -= G;
@@ -463,49 +471,50 @@ __global__ void __launch_bounds__(WT, 1) weights_tc_kernel(const __grid_constant
         return qt < I.qt1 && row < I.n ? -a.lse[(size_t)(I.kvh * G + h) * a.ldl + I.seq0 + row] * kLog2e : -INFINITY;
       };
       float next = lse_here();
-      for (; t < tiles_here; t += WGS, ++turn) {
+      for (; t < tiles_here; t += 2) {
+        const unsigned turn = (g + t) >> 1;  // of this warpgroup
         float* lse = ctl->lse[wg][turn & 1];
         lse[r] = next;
         wg_sync();  // written; and everyone has left the buffer of two turns ago
         const int q0 = qt * BQ;
-        h += WGS;
+        h += 2;
         settle();
         next = lse_here();
-        const unsigned gt = g + t;
-        const int sb = (int)(gt % SBUF);
         // after an expired wait the loops run on without work, so that every thread still meets
         // the same barriers
-        ok = ok && mbar_wait(bar(ctl->s_full[sb]), (uint32_t)((gt / SBUF) & 1), abort_flag);
+        ok = ok && mbar_wait_ready(bar(ctl->s_full[half][sb]), turn & 1, abort_flag);
         if (!__all_sync(0xffffffffu, ok)) {
           ok = false;
           continue;
         }
         tc_fence_after();
         // no key of the tile hidden from any row, and no row past the chunk
-        const bool interior = I.key0 + BK - 1 <= I.c0 + q0 && q0 + BQ <= I.n &&
-                              (a.window <= 0 || I.key0 > I.c0 + q0 + BQ - 1 - a.window || I.key0 + BK <= a.sinks);
-        // columns of this tile whose rows see the key: [lo, lo + span)
-        const int first = max(0, key - I.c0 - q0);
+        const bool interior = key0 + BK - 1 <= I.c0 + q0 && q0 + BQ <= I.n &&
+                              (a.window <= 0 || key0 > I.c0 + q0 + BQ - 1 - a.window || key0 + BK <= a.sinks);
+        // columns of this tile whose rows see the key: [lo, hi)
+        const int lo = max(0, key - I.c0 - q0);
         long long last = min(BQ, I.n - q0);
         if (a.window > 0 && key >= a.sinks) last = min(last, (long long)key + a.window - I.c0 - q0);
-        const unsigned lo = (unsigned)first, span = last > first ? (unsigned)(last - first) : 0u;
+        const int hi = (int)max(last, 0LL);
         // two groups of 32 columns in registers; a group is loaded as soon as one has been summed,
         // so that the accumulator is free when half of it has been
         uint32_t v[2][32];
-        tmem_ld32_async(tmem + lane_off + sb * BQ, v[0]);
-        tmem_ld32_async(tmem + lane_off + sb * BQ + 32, v[1]);
-        tmem_wait32(v[0]);
-        tmem_wait32(v[1]);
+        tmem_ld32_async(s_addr, v[0]);
+        tmem_ld32_async(s_addr + 32, v[1]);
 #pragma unroll
         for (int cb = 0; cb < BQ; cb += 32) {
           uint32_t* x = v[(cb / 32) & 1];
-          if (cb == 64) {
+          if (cb % 64 == 0) {
             tmem_wait32(v[0]);
             tmem_wait32(v[1]);
-            tc_fence_before();
-            mbar_arrive(bar(ctl->s_empty[sb]));  // S has been read: the accumulator may be refilled
+            if (cb == 64) {
+              tc_fence_before();
+              mbar_arrive(bar(ctl->s_empty[half][sb]));  // S has been read: the accumulator may be refilled
+            }
           }
-          if (interior) {
+          // whether every key of the warp is seen by every row of these columns, or none by any
+          const bool all = interior || __all_sync(0xffffffffu, lo <= cb && cb + 32 <= hi);
+          if (all) {
             float e[32];  // two columns an instruction, all exponents before the exponentials
 #pragma unroll
             for (int i = 0; i < 32; i += 4) {
@@ -516,28 +525,27 @@ __global__ void __launch_bounds__(WT, 1) weights_tc_kernel(const __grid_constant
 #pragma unroll
             for (int i = 0; i < 32; ++i) e[i] = ex2_approx(e[i]);
 #pragma unroll
-            for (int i = 0; i < 32; i += 2) add2(acc + (i & 7), e[i], e[i + 1]);
-          } else {
+            for (int i = 0; i < 32; i += 2) add2(acc + (i & 3), e[i], e[i + 1]);
+          } else if (__any_sync(0xffffffffu, lo < cb + 32 && cb < hi)) {
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
               const float e = fmaf(__uint_as_float(x[i]), c, lse[cb + i]);
-              acc[i & 7] += ex2_approx((unsigned)(cb + i) - lo < span ? e : -INFINITY);
+              acc[i & 3] += ex2_approx(cb + i >= lo && cb + i < hi ? e : -INFINITY);
             }
           }
-          if (cb < 64) tmem_ld32_async(tmem + lane_off + sb * BQ + cb + 64, x);
+          if (cb < 64) tmem_ld32_async(s_addr + cb + 64, x);
         }
       }
       g += tiles_here;
-      const float sum = ((acc[0] + acc[1]) + (acc[2] + acc[3])) + ((acc[4] + acc[5]) + (acc[6] + acc[7]));
-      if (wg > 0) ctl->comb[it & 1][wg - 1][r] = sum;
-      asm volatile("bar.sync %0, %1;" ::"n"(1 + WGS), "n"(WGS * 128) : "memory");
-      if (wg == 0 && seen && ok) {
+      float w = (acc[0] + acc[1]) + (acc[2] + acc[3]);
+      float* other = &ctl->comb[it & 1][half][r];
+      if (sb == 1) *other = w;
+      asm volatile("bar.sync %0, 256;" ::"r"(5 + half) : "memory");
+      if (sb == 0 && ok && seen) {
+        w += *other;
         const int own = a.bt[(size_t)I.s * a.max_pages + (key >> 4)];
         if (own >= 0 && own < a.num_pages) {
           float* dst = a.scores + ((size_t)own * a.n_kv + I.kvh) * kPageSize + (key & 15);
-          float w = sum;
-#pragma unroll
-          for (int i = 0; i + 1 < WGS; ++i) w += ctl->comb[it & 1][i][r];
           *dst = a.decay != 0.f ? fmaf(a.decay, *dst, w) : w;
         } else {
           atomicOr(a.status, kStatusBadPage);
@@ -559,7 +567,7 @@ __global__ void __launch_bounds__(WT, 1) weights_tc_kernel(const __grid_constant
         }
       }
     }
-    if (threadIdx.x == 32) {  // MMAs in flight
+    if ((warp == 1 || warp == 2) && elect_lane()) {  // products in flight
       tc_commit(bar(ctl->fin));
       const uint64_t t0 = global_ns();
       while (!mbar_try_wait(bar(ctl->fin), 0) && global_ns() - t0 < kTimeoutNs) {
@@ -569,7 +577,7 @@ __global__ void __launch_bounds__(WT, 1) weights_tc_kernel(const __grid_constant
   }
   tc_fence_after();
   if (warp == 1)
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(SBUF * BQ) : "memory");
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(TMEM_COLS) : "memory");
 }
 
 template <int D, bool FP8, int NT>

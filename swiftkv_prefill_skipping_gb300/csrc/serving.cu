@@ -357,11 +357,10 @@ int WeightsPlan::make(const swiftkv_model* m, const int32_t* cu, const int32_t* 
     }
     int next = 0;
     for (int k = 0; k < r.n; ++k)
-      for (int t = std::max(next, r.k0[k] / 128); t < (r.k1[k] + 127) / 128; ++t) {
-        const long long first = std::max(0, t * 128 - c0);
+      for (int t = std::max(next, r.k0[k] / kWeightTile); t < (r.k1[k] + kWeightTile - 1) / kWeightTile; ++t) {
+        const long long key0 = (long long)t * kWeightTile, first = std::max(0LL, key0 - c0);
         long long last = n;
-        if (b.window > 0 && t * 128 >= b.sinks)
-          last = std::min<long long>(n, (long long)t * 128 + 127 + b.window - c0);
+        if (b.window > 0 && key0 >= b.sinks) last = std::min<long long>(n, key0 + kWeightTile - 1 + b.window - c0);
         heavy.push_back({last - first, {i, t}});
         next = t + 1;
       }

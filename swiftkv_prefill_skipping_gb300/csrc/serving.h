@@ -201,11 +201,12 @@ struct WeightsArgs {
 // Chunks of few rows (rows x group <= kWeightCols): units [3 * num_units] = (sequence, first key,
 // keys), one warp per unit and KV head at a time. FP8 cache: codes and scales of K.
 constexpr int kWeightCols = 32;
+constexpr int kWeightTile = 256;  // keys of an item of the tcgen05 kernel
 constexpr int kWeightWarps = 12;  // warps per SM that walk units
 cudaError_t launch_weights_rows(const WeightsArgs& a, const InlineInts& inl, const bf16* k, const uint8_t* k8,
                                 const float* k_scale, int d_head, int max_cols, int num_units, int num_sms,
                                 cudaStream_t s);
-// Longer chunks on tcgen05: tiles [2 * num_tiles] = (sequence, 128-key tile), heaviest first. FP8:
+// Longer chunks on tcgen05: tiles [2 * num_tiles] = (sequence, kWeightTile-key tile), heaviest first. FP8:
 // k / k_scale are an expansion (pages named by a.bt's counterpart `bt_k` of the same shape).
 cudaError_t launch_weights_tc(const WeightsArgs& a, const bf16* k, const float* k_scale, const int* bt_k, int pages_k,
                               int d_head, const int* tiles, int num_tiles, int num_sms, cudaStream_t s);
