@@ -187,7 +187,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_chunk_kernel(const __grid_con
   const bool fp8 = a.k_scale != nullptr;
   auto bar = [&](uint64_t& b) { return smem_u32(&b); };
   // a warp leaves a wait as one: what follows is collective
-  auto wait_all = [&](uint32_t b, uint32_t phase) { return __all_sync(0xffffffffu, mbar_wait(b, phase, abort_flag)) != 0; };
+  auto wait_all = [&](uint32_t b, uint32_t phase) { return __all_sync(0xffffffffu, mbar_wait_ready(b, phase, abort_flag)) != 0; };
 
   if (threadIdx.x == 0) {
     mbar_init(bar(ctl->q_full), 1);
@@ -303,8 +303,8 @@ __global__ void __launch_bounds__(THREADS, 1) attn_chunk_kernel(const __grid_con
         I = N;
         have = have_next;
       }
-    } else if ((warp == 1 || warp == 2) && lane == 0) {
-      // tile t's MMAs; g counts its blocks over all items, oi the items that used its O
+    } else {
+      // tile t's MMAs, the warp waiting as one and one lane issuing; g counts its blocks over all items, oi the items that used its O
       const int t = warp - 1;
       // descriptors of the tile's Q and of stage 0; an offset in bytes adds its sixteenth
       const uint64_t q = sdesc(sQ + t * C::Q_TILE), k0 = sdesc(sK), v0 = sdesc_sw128(sV, C::KV_HALF, 1024);
@@ -313,40 +313,53 @@ __global__ void __launch_bounds__(THREADS, 1) attn_chunk_kernel(const __grid_con
       bool ok = true;
       for (int it = 0; ok && item_at<BKV>(it, a, I); ++it) {
         const int nb = t ? I.nblk_b : I.nblk_a;
-        if (!mbar_wait(bar(ctl->q_full), (uint32_t)(it & 1), abort_flag)) break;
-        ctl->pend[0] = -1;
-        if (nb == 0) mbar_arrive(bar(ctl->q_empty));
+        if (!(ok = wait_all(bar(ctl->q_full), (uint32_t)(it & 1)))) break;
+        if (lane == 0) {
+          ctl->pend[0] = -1;
+          if (nb == 0) mbar_arrive(bar(ctl->q_empty));
+        }
+        // two phases, both tests in flight
+        auto wait2 = [&](uint64_t& b0, uint32_t p0, uint64_t& b1, uint32_t p1) {
+          const bool r0 = mbar_test_wait(bar(b0), p0), r1 = mbar_test_wait(bar(b1), p1);
+          const bool done = (r0 || mbar_wait(bar(b0), p0, abort_flag)) && (r1 || mbar_wait(bar(b1), p1, abort_flag));
+          return __all_sync(0xffffffffu, done) != 0;
+        };
         // S of block j of the item, the tile's block g + j: the softmax has read the one before it
         auto issue_s = [&](int j) -> bool {
           const int kv = kv_base + j, st = kv % KST, gj = g + j;
-          if (!mbar_wait(bar(ctl->k_full[st]), (uint32_t)((kv / KST) & 1), abort_flag)) return false;
-          ctl->pend[1 + st] = -1;
-          if (gj > 0 && !mbar_wait(bar(ctl->s_empty[t]), (uint32_t)((gj - 1) & 1), abort_flag)) return false;
+          // s_empty's phase before its first is complete from the start
+          if (!wait2(ctl->k_full[st], (uint32_t)((kv / KST) & 1), ctl->s_empty[t], (uint32_t)((gj - 1) & 1))) return false;
           tc_fence_after();
-          const uint64_t k = k0 + st * (C::KV_TILE / 16);
+          if (elect_lane()) {
+            ctl->pend[1 + st] = -1;
+            const uint64_t k = k0 + st * (C::KV_TILE / 16);
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-            tc_mma(base, q + ((kk >> 2) * C::Q_HALF + (kk & 3) * 32) / 16,
-                   k + ((kk >> 2) * C::KV_HALF + (kk & 3) * 32) / 16, C::IDESC_S, kk != 0);
-          tc_commit(bar(ctl->s_full[t]));
-          tc_commit(bar(ctl->k_empty[st]));
-          if (j + 1 == nb) tc_commit(bar(ctl->q_empty));
+            for (int kk = 0; kk < D / 16; ++kk)
+              tc_mma(base, q + ((kk >> 2) * C::Q_HALF + (kk & 3) * 32) / 16,
+                     k + ((kk >> 2) * C::KV_HALF + (kk & 3) * 32) / 16, C::IDESC_S, kk != 0);
+            tc_commit(bar(ctl->s_full[t]));
+            tc_commit(bar(ctl->k_empty[st]));
+            if (j + 1 == nb) tc_commit(bar(ctl->q_empty));
+          }
+          __syncwarp();
           return true;
         };
         auto issue_pv = [&](int j) -> bool {
           const int kv = kv_base + j, st = kv % VST;
-          if (!mbar_wait(bar(ctl->v_full[st]), (uint32_t)((kv / VST) & 1), abort_flag)) return false;
-          ctl->pend[1 + KST + st] = -1;
-          if (!mbar_wait(bar(ctl->p_full[t]), (uint32_t)((g + j) & 1), abort_flag)) return false;
+          if (!wait2(ctl->v_full[st], (uint32_t)((kv / VST) & 1), ctl->p_full[t], (uint32_t)((g + j) & 1))) return false;
           // the first P V of an item overwrites O: the previous item's output must have left
-          if (j == 0 && oi > 0 && !mbar_wait(bar(ctl->o_empty[t]), (uint32_t)((oi - 1) & 1), abort_flag)) return false;
+          if (j == 0 && oi > 0 && !wait_all(bar(ctl->o_empty[t]), (uint32_t)((oi - 1) & 1))) return false;
           tc_fence_after();
-          const uint64_t v = v0 + st * (C::KV_TILE / 16);
+          if (elect_lane()) {
+            ctl->pend[1 + KST + st] = -1;
+            const uint64_t v = v0 + st * (C::KV_TILE / 16);
 #pragma unroll
-          for (int kk = 0; kk < BKV / 16; ++kk)  // 16 keys: 8 columns of P, 2 KB of each 64-dim half of V
-            tc_mma_ts(base + C::O_COL, base + C::P_COL + kk * 8, v + kk * 128, C::IDESC_O, (j | kk) != 0);
-          tc_commit(bar(ctl->pv_done[t]));
-          tc_commit(bar(ctl->v_empty[st]));
+            for (int kk = 0; kk < BKV / 16; ++kk)  // 16 keys: 8 columns of P, 2 KB of each 64-dim half of V
+              tc_mma_ts(base + C::O_COL, base + C::P_COL + kk * 8, v + kk * 128, C::IDESC_O, (j | kk) != 0);
+            tc_commit(bar(ctl->pv_done[t]));
+            tc_commit(bar(ctl->v_empty[st]));
+          }
+          __syncwarp();
           return true;
         };
         if (nb > 0) ok = issue_s(0);
@@ -357,12 +370,13 @@ __global__ void __launch_bounds__(THREADS, 1) attn_chunk_kernel(const __grid_con
         // blocks this tile does not read: only released, once they have arrived
         for (int j = nb; ok && j < I.nblk; ++j) {
           const int kv = kv_base + j, ks = kv % KST, vs = kv % VST;
-          if (!(ok = mbar_wait(bar(ctl->k_full[ks]), (uint32_t)((kv / KST) & 1), abort_flag))) break;
-          ctl->pend[1 + ks] = -1;
-          mbar_arrive(bar(ctl->k_empty[ks]));
-          if (!(ok = mbar_wait(bar(ctl->v_full[vs]), (uint32_t)((kv / VST) & 1), abort_flag))) break;
-          ctl->pend[1 + KST + vs] = -1;
-          mbar_arrive(bar(ctl->v_empty[vs]));
+          if (!(ok = wait2(ctl->k_full[ks], (uint32_t)((kv / KST) & 1), ctl->v_full[vs], (uint32_t)((kv / VST) & 1)))) break;
+          if (lane == 0) {
+            ctl->pend[1 + ks] = -1;
+            mbar_arrive(bar(ctl->k_empty[ks]));
+            ctl->pend[1 + KST + vs] = -1;
+            mbar_arrive(bar(ctl->v_empty[vs]));
+          }
         }
         kv_base += I.nblk;
         g += nb;
@@ -520,8 +534,8 @@ __global__ void __launch_bounds__(THREADS, 1) attn_chunk_kernel(const __grid_con
         }
       }
     }
-    if (threadIdx.x == 32 || threadIdx.x == 64) {  // MMAs each issuing thread has in flight
-      const uint32_t f = bar(ctl->fin[threadIdx.x == 64]);
+    if ((warp == 1 || warp == 2) && elect_lane()) {  // MMAs each issuing lane has in flight
+      const uint32_t f = bar(ctl->fin[warp - 1]);
       tc_commit(f);
       const uint64_t t0 = global_ns();
       while (!mbar_try_wait(f, 0) && global_ns() - t0 < kTimeoutNs) {
