@@ -386,7 +386,6 @@ __global__ void __launch_bounds__(THREADS, 1) attn_chunk_kernel(const __grid_con
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_SOFTMAX));
     const int t = (warp - 4) >> 2, quarter = warp & 3;
-    const int r = quarter * 32 + lane;
     const uint32_t s_addr = tmem + ((uint32_t)(quarter * 32) << 16) + t * C::COLS;
     int g = 0, kvb = 0;
     bool ok = true;
@@ -394,7 +393,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_chunk_kernel(const __grid_con
     for (int it = 0; ok && item_at<BKV>(it, a, I); kvb += I.nblk, ++it) {
       const int nb = t ? I.nblk_b : I.nblk_a, q0 = t ? I.q0b : I.q0a;
       if (nb == 0) continue;
-      const int qrow = q0 + r, qpos = I.c0 + qrow;
+      const int qw = q0 + quarter * 32, qrow = qw + lane, qpos = I.c0 + qrow;  // the warp's first row, this thread's
       const int first = window_begin(qpos, a.window), last = min(qpos, I.nk - 1), sinks = a.window > 0 ? a.sinks : 0;
       float m = -INFINITY, l = 0.f;
       for (int j = 0; j < nb; ++j, ++g) {
@@ -419,9 +418,9 @@ __global__ void __launch_bounds__(THREADS, 1) attn_chunk_kernel(const __grid_con
           }
         }
         const int key0 = I.block(j) * BKV;
-        // no key of the block hidden from any row of the tile
-        const bool inside = key0 + BKV - 1 <= I.c0 + q0 && key0 + BKV <= I.nk &&
-                            (a.window <= 0 || key0 > I.c0 + q0 + BQ - 1 - a.window || key0 + BKV <= a.sinks);
+        // no key of the block hidden from any row of the warp
+        const bool inside = key0 + BKV - 1 <= I.c0 + qw && key0 + BKV <= I.nk &&
+                            (a.window <= 0 || key0 > I.c0 + qw + 31 - a.window || key0 + BKV <= a.sinks);
         if (!inside) {  // the row's visible keys as bits, 16 at a time
 #pragma unroll
           for (int c = 0; c < BKV / 16; ++c) {
