@@ -283,8 +283,10 @@ int swiftkv_set_attention_window(swiftkv_model* m, int window, int sinks);
  * layers that share a cache add up, so a decay other than 1 acts once per layer).
  *   scores  HOST array [swiftkv_cache_count] of device float pools, as for swiftkv_evict, read at
  *           this call; the pools stay the caller's and must outlive the calls that add to them.
- *           NULL turns it off (default). */
-int swiftkv_set_score_pools(swiftkv_model* m, float* const* scores, float decay);
+ *           NULL turns it off (default).
+ *   num_pages  pages of each pool: later calls whose caches have more are refused (SWIFTKV_EINVAL)
+ * Sequences of one call must not share pages (a common prefix) while it is on. */
+int swiftkv_set_score_pools(swiftkv_model* m, float* const* scores, int num_pages, float decay);
 
 /* swiftkv_forward for sequences whose caches were shrunk by swiftkv_evict: chunk token i of sequence
  * s goes to cache row ctx_lens[s] + i and sees rows up to its own, while its position for RoPE is

@@ -106,9 +106,10 @@ class Model:
 
     def set_score_pools(self, scores: Optional[torch.Tensor], decay: float = 1.0) -> None:
         """Later calls add every layer's attention weights to scores (float32 [num_caches, num_pages,
-        n_kv, 16], e.g. KVCache.new_scores(); kept alive here); None turns that off."""
+        n_kv, 16], e.g. KVCache.new_scores(); kept alive here); None turns that off. Sequences of a
+        call must not share pages while it is on."""
         if scores is None:
-            B.check(B.lib().swiftkv_set_score_pools(self.handle, None, decay))
+            B.check(B.lib().swiftkv_set_score_pools(self.handle, None, 0, decay))
         else:
             s = self.shape
             if scores.dim() != 4 or scores.shape[0] != self.num_caches or tuple(scores.shape[2:]) != (s.n_kv, 16):
@@ -116,7 +117,7 @@ class Model:
             base = _flat(scores, torch.float32, tuple(scores.shape), scores.device, "scores")
             step = scores.stride(0) * 4
             ptrs = (C.c_void_p * self.num_caches)(*[base + c * step for c in range(self.num_caches)])
-            B.check(B.lib().swiftkv_set_score_pools(self.handle, ptrs, decay))
+            B.check(B.lib().swiftkv_set_score_pools(self.handle, ptrs, scores.shape[1], decay))
         self._scores = scores
 
     def memory(self):
@@ -149,6 +150,7 @@ class KVCache:
         s = model.shape
         dev = device or torch.device("cuda", torch.cuda.current_device())
         self.num_pages, self.dtype = num_pages, dtype
+        self.heads = (s.n_kv, s.d_h)
         shape = (model.num_caches, num_pages, s.n_kv, 16, s.d_h)
         elem = torch.bfloat16 if dtype == "bf16" else torch.uint8
         self.k = torch.zeros(shape, dtype=elem, device=dev)
@@ -282,8 +284,14 @@ def decode_step(model: Model, tokens: torch.Tensor, seq_lens: Sequence[int], kv:
     return logits, nxt
 
 
-def _chunks(cu_seqlens, ctx_lens, kv: KVCache):
+def _fits(model: Model, kv: KVCache) -> None:
+    if kv.heads != (model.shape.n_kv, model.shape.d_h):
+        raise ValueError(f"a cache of (n_kv, d_h) {kv.heads} for a model of {(model.shape.n_kv, model.shape.d_h)}")
+
+
+def _chunks(cu_seqlens, ctx_lens, kv: KVCache, model: Model):
     """Host int32 arrays of a ragged batch, checked against the block table: (cu, ctx, P, T)."""
+    _fits(model, kv)
     cu = np.ascontiguousarray(cu_seqlens, dtype=np.int32)
     ctx = None if ctx_lens is None else np.ascontiguousarray(ctx_lens, dtype=np.int32)
     P = cu.shape[0] - 1 if cu.ndim == 1 else -1
@@ -320,7 +328,7 @@ def attend(model: Model, q: torch.Tensor, cu_seqlens: Sequence[int], ctx_lens: O
     position p sees positions <= p; with window > 0 only those above p - window, and the first
     `sinks`. Returns out [T, n_q, d_h] bf16; lse (float32 [n_q, T]), if given, receives each row's
     log-sum-exp, which attention_weights takes."""
-    cu, ctx, P, T = _chunks(cu_seqlens, ctx_lens, kv)
+    cu, ctx, P, T = _chunks(cu_seqlens, ctx_lens, kv, model)
     dev = kv.k.device
     ldq = _rows_of(q, T, model, dev, "q")
     if out is None:
@@ -339,7 +347,7 @@ def attention_weights(model: Model, q: torch.Tensor, lse: torch.Tensor, cu_seqle
     and the query heads of its KV head, to scores (float32 [num_pages, n_kv, 16], one per key of the
     cache): scores = decay * scores + weight for every key some token sees, the others unchanged.
     q and lse are those of the attend call before. Returns scores."""
-    cu, ctx, P, T = _chunks(cu_seqlens, ctx_lens, kv)
+    cu, ctx, P, T = _chunks(cu_seqlens, ctx_lens, kv, model)
     dev, s = kv.k.device, model.shape
     ldq = _rows_of(q, T, model, dev, "q")
     lp = _flat(lse, torch.float32, (s.n_q, T), dev, "lse")
@@ -359,6 +367,7 @@ def evict(model: Model, kv: KVCache, scores: torch.Tensor, seq_lens: Sequence[in
     pages no sequence uses now; the source is then only read). Returns kept, the former indices
     [caches, P, n_kv, keep] int32, -1 behind a shorter list; sequence s then holds
     min(seq_lens[s], keep) keys."""
+    _fits(model, kv)
     sl = np.ascontiguousarray(seq_lens, dtype=np.int32)
     P, dev, s = sl.shape[0], kv.k.device, model.shape
     if P > kv.num_rows:

@@ -103,7 +103,7 @@ def lib(path: str | None = None):
                                                     vp, vp]
             L.swiftkv_evict.argtypes = [vp, i, C.POINTER(KVPages), C.POINTER(vp), vp, i, i, i, i, vp, i, vp, vp]
             L.swiftkv_set_attention_window.argtypes = [vp, i, i]
-            L.swiftkv_set_score_pools.argtypes = [vp, C.POINTER(vp), C.c_float]
+            L.swiftkv_set_score_pools.argtypes = [vp, C.POINTER(vp), C.c_int, C.c_float]
             L.swiftkv_forward_at.argtypes = [vp, vp, vp, vp, vp, i, i, i, C.POINTER(KVPages), vp, vp]
             L.swiftkv_sample.argtypes = [vp, i, i, C.c_longlong, C.POINTER(Sampling), vp, vp, vp]
             L.swiftkv_status.argtypes = [vp, i]

@@ -279,8 +279,14 @@ struct ServingPlan {
   int* offsets = nullptr;  // device [P] or null
 
   int make(const swiftkv_model* m, const int32_t* cu, const int32_t* ctx, int P, const swiftkv_kv_pages* kv, bool with_last) {
+    return guarded([&] { return make_lists(m, cu, ctx, P, kv, with_last); });
+  }
+  int make_lists(const swiftkv_model* m, const int32_t* cu, const int32_t* ctx, int P, const swiftkv_kv_pages* kv,
+                 bool with_last) {
     has_last = with_last;
     scores = !m->score_pools.empty();
+    if (scores && kv->num_pages > m->score_pages)
+      return fail(SWIFTKV_EINVAL, "the caches have %d pages, the score pools %d", kv->num_pages, m->score_pages);
     RET(rows.make(m, cu, ctx, P, kv, m->window, m->sinks));
     if (scores) RET(rows_w.make(m, cu, ctx, P, kv, m->window, m->sinks));
     if (!with_last) return SWIFTKV_OK;
@@ -914,7 +920,7 @@ int swiftkv_load_weights(const swiftkv_model_config* cfg, const swiftkv_host_wei
 int swiftkv_memory(const swiftkv_model* m, size_t* weight_bytes, size_t* workspace_bytes) {
   if (!m) return fail(SWIFTKV_EINVAL, "null model");
   if (weight_bytes) *weight_bytes = m->weight_bytes;
-  if (workspace_bytes) *workspace_bytes = m->ws_bytes;
+  if (workspace_bytes) *workspace_bytes = m->ws_bytes + m->ops_bytes;
   return SWIFTKV_OK;
 }
 
@@ -1288,7 +1294,7 @@ int swiftkv_set_attention_window(swiftkv_model* m, int window, int sinks) {
   return SWIFTKV_OK;
 }
 
-int swiftkv_set_score_pools(swiftkv_model* m, float* const* scores, float decay) {
+int swiftkv_set_score_pools(swiftkv_model* m, float* const* scores, int num_pages, float decay) {
   if (!m) return fail(SWIFTKV_EINVAL, "null model");
   if (!scores) {
     m->score_pools.clear();
@@ -1298,9 +1304,13 @@ int swiftkv_set_score_pools(swiftkv_model* m, float* const* scores, float decay)
   for (int c = 0; c < m->C; ++c)
     if (!scores[c] || (reinterpret_cast<uintptr_t>(scores[c]) & 15))
       return fail(SWIFTKV_EINVAL, "null or misaligned score pool for cache %d", c);
-  m->score_pools.assign(scores, scores + m->C);
-  m->score_decay = decay;
-  return SWIFTKV_OK;
+  if (num_pages < 1) return fail(SWIFTKV_EINVAL, "num_pages %d < 1", num_pages);
+  return guarded([&] {
+    m->score_pools.assign(scores, scores + m->C);
+    m->score_pages = num_pages;
+    m->score_decay = decay;
+    return (int)SWIFTKV_OK;
+  });
 }
 
 int swiftkv_decode_step(swiftkv_model* m, const int32_t* tokens, const int32_t* seq_lens, int B,

@@ -3,6 +3,7 @@
 
 #include <cuda_runtime.h>
 
+#include <new>
 #include <string>
 #include <vector>
 
@@ -68,6 +69,7 @@ struct swiftkv_model {
   unsigned chain_base = 0;          // ... and their count so far (host)
   int window = 0, sinks = 0;          // attention window of the model's layers (0: none)
   std::vector<float*> score_pools;    // per cache, where the layers' attention weights are added (empty: off)
+  int score_pages = 0;                // pages of each
   float score_decay = 1.f;
   // profiling (swiftkv_profile_begin/end)
   bool prof_on = false;
@@ -83,6 +85,18 @@ struct swiftkv_model {
 };
 
 namespace skv {
+
+// f() for a C entry: host lists that do not fit the memory become an error code.
+template <typename F>
+int guarded(F f) {
+  try {
+    return f();
+  } catch (const std::bad_alloc&) {
+    return fail(SWIFTKV_EOOM, "host memory");
+  } catch (const std::exception& e) {  // std::length_error
+    return fail(SWIFTKV_EUNSUPPORTED, "%s", e.what());
+  }
+}
 
 // The caches a call names: counts, page size and pointers against the model's.
 int check_kv(const swiftkv_model* m, const swiftkv_kv_pages* kv);

@@ -28,6 +28,8 @@ int check_batch(const swiftkv_model* m, const int32_t* cu, const int32_t* ctx, i
     if (n > 65535LL * 64) return fail(SWIFTKV_EUNSUPPORTED, "chunk %d has more than 4194240 tokens", i);
   }
   if (window < 0 || sinks < 0) return fail(SWIFTKV_EINVAL, "negative window or sinks");
+  if ((long long)kv->num_pages * m->cfg.n_kv * kPageSize >= 1LL << 31)
+    return fail(SWIFTKV_EUNSUPPORTED, "a pool of 2^31 rows or more");
   if (kv->max_pages_per_seq > (1 << 26)) return fail(SWIFTKV_EUNSUPPORTED, "max_pages_per_seq above 2^26");
   b->P = P;
   b->T = cu[P];
@@ -226,9 +228,11 @@ int AttendPlan::make(const swiftkv_model* m, const int32_t* cu, const int32_t* c
     cut_units(ids, seen, c.n_kv, (long long)m->num_sms * (b.fp8 ? kRowsWarps8 : kRowsWarps), &units, &ubeg);
   num_tiles = (int)tiles.size();
   num_items = (int)ids.size();
-  num_units = (int)units.size() / 3;
-  num_exp = (int)exp_items.size() / 2;
-  if ((long long)num_units * c.n_kv >= (1LL << 31) || (long long)num_tiles * c.n_q >= (1LL << 31))
+  num_units = (int)(units.size() / 3);
+  num_exp = (int)(exp_items.size() / 2);
+  // offsets into the lists and the kernels' item counts are ints
+  if (std::max({units.size(), tiles.size(), exp_items.size()}) >= (size_t)1 << 28 ||
+      (long long)num_units * c.n_kv >= (1LL << 31) || (long long)num_tiles * c.n_q >= (1LL << 31))
     return fail(SWIFTKV_EUNSUPPORTED, "batch too large");
   o_cu = put(&ints, cuv);
   o_ctx = put(&ints, ctxv);
@@ -372,10 +376,11 @@ int WeightsPlan::make(const swiftkv_model* m, const int32_t* cu, const int32_t* 
     tiles.push_back(h.second.first);
     tiles.push_back(h.second.second);
   }
-  num_units = (int)units.size() / 3;
-  num_tiles = (int)tiles.size() / 2;
-  num_exp = (int)exp_items.size() / 2;
-  if ((long long)num_units * c.n_kv >= (1LL << 31) || (long long)num_tiles * c.n_kv >= (1LL << 31))
+  num_units = (int)(units.size() / 3);
+  num_tiles = (int)(tiles.size() / 2);
+  num_exp = (int)(exp_items.size() / 2);
+  if (std::max({units.size(), tiles.size(), exp_items.size()}) >= (size_t)1 << 28 ||
+      (long long)num_units * c.n_kv >= (1LL << 31) || (long long)num_tiles * c.n_kv >= (1LL << 31))
     return fail(SWIFTKV_EUNSUPPORTED, "batch too large");
   o_cu = put(&ints, cuv);
   o_ctx = put(&ints, ctxv);
@@ -474,127 +479,133 @@ extern "C" {
 int swiftkv_attend(swiftkv_model* m, int cache, const void* q, int ldq, const int32_t* cu, const int32_t* ctx, int P,
                    const swiftkv_kv_pages* kv, int window, int sinks, void* out, int ldo, float* lse,
                    swiftkv_stream stream) {
-  RET(check_call(m, cache, P, kv));
-  if (P == 0) return SWIFTKV_OK;
-  if (!cu) return fail(SWIFTKV_EINVAL, "null cu_seqlens");
-  AttendPlan p;
-  RET(p.make(m, cu, ctx, P, kv, window, sinks));
-  if (p.b.T == 0) return SWIFTKV_OK;
-  RET(check_rows(m, q, ldq, "q"));
-  RET(check_rows(m, out, ldo, "out"));
-  const char *qa = static_cast<const char*>(q), *oa = static_cast<const char*>(out);
-  const size_t qn = ((size_t)(p.b.T - 1) * ldq + m->Nq) * 2, on = ((size_t)(p.b.T - 1) * ldo + m->Nq) * 2;
-  if (qa < oa + on && oa < qa + qn) return fail(SWIFTKV_EINVAL, "out overlaps q");
-  if (reinterpret_cast<uintptr_t>(lse) & 3) return fail(SWIFTKV_EINVAL, "misaligned lse");
-  OnDevice on_device(m);
-  cudaStream_t s = (cudaStream_t)stream;
-  Arena size, arena;
-  p.place(m, &size);
-  RET(reserve(m, size.used, s, &arena));
-  p.place(m, &arena);
-  RET(p.upload(s));
-  return p.run(m, kv, cache, static_cast<const bf16*>(q), ldq, static_cast<bf16*>(out), ldo, lse, p.b.T, s);
+  return guarded([&]() -> int {
+    RET(check_call(m, cache, P, kv));
+    if (P == 0) return SWIFTKV_OK;
+    if (!cu) return fail(SWIFTKV_EINVAL, "null cu_seqlens");
+    AttendPlan p;
+    RET(p.make(m, cu, ctx, P, kv, window, sinks));
+    if (p.b.T == 0) return SWIFTKV_OK;
+    RET(check_rows(m, q, ldq, "q"));
+    RET(check_rows(m, out, ldo, "out"));
+    const char *qa = static_cast<const char*>(q), *oa = static_cast<const char*>(out);
+    const size_t qn = ((size_t)(p.b.T - 1) * ldq + m->Nq) * 2, on = ((size_t)(p.b.T - 1) * ldo + m->Nq) * 2;
+    if (qa < oa + on && oa < qa + qn) return fail(SWIFTKV_EINVAL, "out overlaps q");
+    if (reinterpret_cast<uintptr_t>(lse) & 3) return fail(SWIFTKV_EINVAL, "misaligned lse");
+    OnDevice on_device(m);
+    cudaStream_t s = (cudaStream_t)stream;
+    Arena size, arena;
+    p.place(m, &size);
+    RET(reserve(m, size.used, s, &arena));
+    p.place(m, &arena);
+    RET(p.upload(s));
+    return p.run(m, kv, cache, static_cast<const bf16*>(q), ldq, static_cast<bf16*>(out), ldo, lse, p.b.T, s);
+  });
 }
 
 int swiftkv_attention_weights(swiftkv_model* m, int cache, const void* q, int ldq, const float* lse, const int32_t* cu,
                               const int32_t* ctx, int P, const swiftkv_kv_pages* kv, int window, int sinks, float decay,
                               float* scores, swiftkv_stream stream) {
-  RET(check_call(m, cache, P, kv));
-  if (P == 0) return SWIFTKV_OK;
-  if (!cu) return fail(SWIFTKV_EINVAL, "null cu_seqlens");
-  if (!(std::fabs(decay) <= 3.0e38f)) return fail(SWIFTKV_EINVAL, "decay is not finite");
-  WeightsPlan p;
-  RET(p.make(m, cu, ctx, P, kv, window, sinks));
-  if (p.b.T == 0) return SWIFTKV_OK;
-  RET(check_rows(m, q, ldq, "q"));
-  if (!lse || !scores) return fail(SWIFTKV_EINVAL, "null lse / scores");
-  if ((reinterpret_cast<uintptr_t>(lse) & 3) || (reinterpret_cast<uintptr_t>(scores) & 15))
-    return fail(SWIFTKV_EINVAL, "misaligned lse (4 bytes) or scores (16 bytes)");
-  OnDevice on_device(m);
-  cudaStream_t s = (cudaStream_t)stream;
-  Arena size, arena;
-  p.place(m, &size);
-  RET(reserve(m, size.used, s, &arena));
-  p.place(m, &arena);
-  RET(p.upload(s));
-  return p.run(m, kv, cache, static_cast<const bf16*>(q), ldq, lse, p.b.T, decay, scores, s);
+  return guarded([&]() -> int {
+    RET(check_call(m, cache, P, kv));
+    if (P == 0) return SWIFTKV_OK;
+    if (!cu) return fail(SWIFTKV_EINVAL, "null cu_seqlens");
+    if (!(std::fabs(decay) <= 3.0e38f)) return fail(SWIFTKV_EINVAL, "decay is not finite");
+    WeightsPlan p;
+    RET(p.make(m, cu, ctx, P, kv, window, sinks));
+    if (p.b.T == 0) return SWIFTKV_OK;
+    RET(check_rows(m, q, ldq, "q"));
+    if (!lse || !scores) return fail(SWIFTKV_EINVAL, "null lse / scores");
+    if ((reinterpret_cast<uintptr_t>(lse) & 3) || (reinterpret_cast<uintptr_t>(scores) & 15))
+      return fail(SWIFTKV_EINVAL, "misaligned lse (4 bytes) or scores (16 bytes)");
+    OnDevice on_device(m);
+    cudaStream_t s = (cudaStream_t)stream;
+    Arena size, arena;
+    p.place(m, &size);
+    RET(reserve(m, size.used, s, &arena));
+    p.place(m, &arena);
+    RET(p.upload(s));
+    return p.run(m, kv, cache, static_cast<const bf16*>(q), ldq, lse, p.b.T, decay, scores, s);
+  });
 }
 
 int swiftkv_evict(swiftkv_model* m, int cache, const swiftkv_kv_pages* kv, float* const* scores,
                   const int32_t* seq_lens, int P, int keep, int sinks, int recent, const int32_t* dst_block_table,
                   int dst_max_pages, int32_t* kept, swiftkv_stream stream) {
-  RET(check_call(m, cache < 0 ? 0 : cache, P, kv));
-  if (P == 0) return SWIFTKV_OK;
-  if (cache < -1) return fail(SWIFTKV_EINVAL, "cache %d outside [-1, %d)", cache, m->C);
-  if (!scores || !seq_lens || !kept) return fail(SWIFTKV_EINVAL, "null scores / seq_lens / kept");
-  const int first = cache < 0 ? 0 : cache, C = cache < 0 ? m->C : 1;
-  for (int c = first; c < first + C; ++c)
-    if (!scores[c] || (reinterpret_cast<uintptr_t>(scores[c]) & 15))
-      return fail(SWIFTKV_EINVAL, "null or misaligned score pool for cache %d", c);
-  if (keep < 1 || sinks < 0 || recent < 0 || (long long)sinks + recent > keep)
-    return fail(SWIFTKV_EINVAL, "need keep >= 1, sinks >= 0, recent >= 0 and sinks + recent <= keep");
-  const int dst_width = dst_block_table ? dst_max_pages : kv->max_pages_per_seq;
-  if (dst_block_table && dst_max_pages < 1) return fail(SWIFTKV_EINVAL, "empty destination block table");
-  int longest = 0;
-  for (int i = 0; i < P; ++i) {
-    const long long n = seq_lens[i];
-    if (n < 0) return fail(SWIFTKV_EINVAL_SEQLENS, "seq_lens[%d] < 0", i);
-    if (n > (long long)kv->max_pages_per_seq * kPageSize)
-      return fail(SWIFTKV_ENO_PAGES, "sequence %d needs %lld pages, block table holds %d", i, (n + 15) / 16,
-                  kv->max_pages_per_seq);
-    const long long left = std::min<long long>(n, keep);
-    if (left > (long long)dst_width * kPageSize)
-      return fail(SWIFTKV_ENO_PAGES, "sequence %d keeps %lld pages, destination block table holds %d", i,
-                  (left + 15) / 16, dst_width);
-    longest = std::max(longest, (int)n);
-  }
-  OnDevice on_device(m);
-  cudaStream_t s = (cudaStream_t)stream;
-  // lengths and the caches' pool pointers in one list
-  const bool fp8 = kv->kv_dtype == 1;
-  std::vector<int> ints(seq_lens, seq_lens + P);
-  if (ints.size() % 2) ints.push_back(0);
-  const size_t at = ints.size();
-  std::vector<const void*> ptrs;
-  for (int c = 0; c < m->C; ++c) ptrs.push_back(kv->k_pool[c]);
-  for (int c = 0; c < m->C; ++c) ptrs.push_back(kv->v_pool[c]);
-  for (int c = 0; c < m->C; ++c) ptrs.push_back(c >= first && c < first + C ? scores[c] : nullptr);
-  for (int c = 0; fp8 && c < m->C; ++c) ptrs.push_back(kv->k_scale[c]);
-  for (int c = 0; fp8 && c < m->C; ++c) ptrs.push_back(kv->v_scale[c]);
-  ints.resize(at + 2 * ptrs.size());
-  memcpy(ints.data() + at, ptrs.data(), ptrs.size() * 8);
-  int* dev = nullptr;
-  if (ints.size() > kInlineInts) {
-    Arena arena;
-    RET(reserve(m, ints.size() * 4, s, &arena));
-    dev = arena.take<int>(ints.size());
-    CK(upload_ints(dev, ints.data(), (int)ints.size(), s));
-  }
-  EvictArgs a;
-  a.lists = dev;
-  a.o_ptrs = (int)at;
-  a.num_ptrs = m->C;
-  a.fp8 = fp8;
-  a.P = P;
-  a.first_cache = first;
-  a.num_caches = C;
-  a.n_kv = m->cfg.n_kv;
-  a.row_bytes = m->cfg.d_head * (fp8 ? 1 : 2);
-  a.src_bt = kv->block_table;
-  a.src_pages = kv->max_pages_per_seq;
-  a.dst_bt = dst_block_table ? dst_block_table : kv->block_table;
-  a.dst_pages = dst_width;
-  a.num_pages = kv->num_pages;
-  a.keep = keep;
-  a.sinks = sinks;
-  a.recent = recent;
-  a.kept = kept;
-  a.status = m->status;
-  a.in_place = !dst_block_table;
-  const cudaError_t e = launch_evict(a, inline_of(ints, dev), longest, s);
-  if (e != cudaSuccess)
-    return fail(e == cudaErrorNotSupported ? SWIFTKV_EUNSUPPORTED : SWIFTKV_ECUDA, "evict: %s", cudaGetErrorString(e));
-  return SWIFTKV_OK;
+  return guarded([&]() -> int {
+    RET(check_call(m, cache < 0 ? 0 : cache, P, kv));
+    if (P == 0) return SWIFTKV_OK;
+    if (cache < -1) return fail(SWIFTKV_EINVAL, "cache %d outside [-1, %d)", cache, m->C);
+    if (!scores || !seq_lens || !kept) return fail(SWIFTKV_EINVAL, "null scores / seq_lens / kept");
+    const int first = cache < 0 ? 0 : cache, C = cache < 0 ? m->C : 1;
+    for (int c = first; c < first + C; ++c)
+      if (!scores[c] || (reinterpret_cast<uintptr_t>(scores[c]) & 15))
+        return fail(SWIFTKV_EINVAL, "null or misaligned score pool for cache %d", c);
+    if (keep < 1 || sinks < 0 || recent < 0 || (long long)sinks + recent > keep)
+      return fail(SWIFTKV_EINVAL, "need keep >= 1, sinks >= 0, recent >= 0 and sinks + recent <= keep");
+    const int dst_width = dst_block_table ? dst_max_pages : kv->max_pages_per_seq;
+    if (dst_block_table && dst_max_pages < 1) return fail(SWIFTKV_EINVAL, "empty destination block table");
+    int longest = 0;
+    for (int i = 0; i < P; ++i) {
+      const long long n = seq_lens[i];
+      if (n < 0) return fail(SWIFTKV_EINVAL_SEQLENS, "seq_lens[%d] < 0", i);
+      if (n > (long long)kv->max_pages_per_seq * kPageSize)
+        return fail(SWIFTKV_ENO_PAGES, "sequence %d needs %lld pages, block table holds %d", i, (n + 15) / 16,
+                    kv->max_pages_per_seq);
+      const long long left = std::min<long long>(n, keep);
+      if (left > (long long)dst_width * kPageSize)
+        return fail(SWIFTKV_ENO_PAGES, "sequence %d keeps %lld pages, destination block table holds %d", i,
+                    (left + 15) / 16, dst_width);
+      longest = std::max(longest, (int)n);
+    }
+    OnDevice on_device(m);
+    cudaStream_t s = (cudaStream_t)stream;
+    // lengths and the caches' pool pointers in one list
+    const bool fp8 = kv->kv_dtype == 1;
+    std::vector<int> ints(seq_lens, seq_lens + P);
+    if (ints.size() % 2) ints.push_back(0);
+    const size_t at = ints.size();
+    std::vector<const void*> ptrs;
+    for (int c = 0; c < m->C; ++c) ptrs.push_back(kv->k_pool[c]);
+    for (int c = 0; c < m->C; ++c) ptrs.push_back(kv->v_pool[c]);
+    for (int c = 0; c < m->C; ++c) ptrs.push_back(c >= first && c < first + C ? scores[c] : nullptr);
+    for (int c = 0; fp8 && c < m->C; ++c) ptrs.push_back(kv->k_scale[c]);
+    for (int c = 0; fp8 && c < m->C; ++c) ptrs.push_back(kv->v_scale[c]);
+    ints.resize(at + 2 * ptrs.size());
+    memcpy(ints.data() + at, ptrs.data(), ptrs.size() * 8);
+    int* dev = nullptr;
+    if (ints.size() > kInlineInts) {
+      Arena arena;
+      RET(reserve(m, ints.size() * 4, s, &arena));
+      dev = arena.take<int>(ints.size());
+      CK(upload_ints(dev, ints.data(), (int)ints.size(), s));
+    }
+    EvictArgs a;
+    a.lists = dev;
+    a.o_ptrs = (int)at;
+    a.num_ptrs = m->C;
+    a.fp8 = fp8;
+    a.P = P;
+    a.first_cache = first;
+    a.num_caches = C;
+    a.n_kv = m->cfg.n_kv;
+    a.row_bytes = m->cfg.d_head * (fp8 ? 1 : 2);
+    a.src_bt = kv->block_table;
+    a.src_pages = kv->max_pages_per_seq;
+    a.dst_bt = dst_block_table ? dst_block_table : kv->block_table;
+    a.dst_pages = dst_width;
+    a.num_pages = kv->num_pages;
+    a.keep = keep;
+    a.sinks = sinks;
+    a.recent = recent;
+    a.kept = kept;
+    a.status = m->status;
+    a.in_place = !dst_block_table;
+    const cudaError_t e = launch_evict(a, inline_of(ints, dev), longest, s);
+    if (e != cudaSuccess)
+      return fail(e == cudaErrorNotSupported ? SWIFTKV_EUNSUPPORTED : SWIFTKV_ECUDA, "evict: %s", cudaGetErrorString(e));
+    return SWIFTKV_OK;
+  });
 }
 
 }  // extern "C"

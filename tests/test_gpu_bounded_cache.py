@@ -228,4 +228,18 @@ def test_refusals():
         api.forward(m, tok, [0, 20], None, kv, pos_offsets=[1 << 30])
     with pytest.raises(ValueError):
         api.forward(m, tok, [0, 20], None, kv, pos_offsets=[0, 0])
+    # pools of fewer pages than the cache, in each of the model's calls
+    small = torch.zeros_like(sc[:, :-1].contiguous())
+    m.set_score_pools(small)
+    for call in (lambda: api.prefill(m, tok, [0, 20], kv), lambda: api.forward(m, tok, [0, 20], [0], kv),
+                 lambda: api.forward(m, tok, [0, 20], [0], kv, pos_offsets=[3]),
+                 lambda: api.decode_step(m, tok[:1], [20], kv)):
+        with pytest.raises(B.SwiftKVError, match="score pools"):
+            call()
+    torch.cuda.synchronize()
+    assert not small.any() and m.status() == 0
+    m.set_score_pools(None)
+    before = m.memory()[1]
+    api.attend(m, torch.zeros(300, m.shape.n_q, m.shape.d_h, dtype=torch.bfloat16, device="cuda")[:20], [0, 20], None, kv)
+    assert m.memory()[1] > before  # the operators' workspace counts
     m.free()

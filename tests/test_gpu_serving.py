@@ -346,8 +346,6 @@ def test_capture_replays_on_new_values():
     lse = torch.empty(c.n_q, c.T, device="cuda")
     out = torch.empty_like(q)
     sc = torch.zeros(c.total, c.n_kv, 16, device="cuda")
-    kept = torch.empty(1, 3, c.n_kv, 24, dtype=torch.int32, device="cuda")
-    lens = [91, 301, 50]
 
     def step():
         api.attend(c.model, q, c.cu, c.ctx, c.kv, cache=1, window=64, sinks=4, out=out, lse=lse)
@@ -373,7 +371,102 @@ def test_capture_replays_on_new_values():
         step()
         torch.cuda.synchronize()
         assert all(bool((a == b).all()) for a, b in zip(got, (out, lse, sc)))
-    del kept, lens
+
+
+@pytest.mark.gpu
+def test_two_graphs_share_a_workspace():
+    """Graphs of different batches, captured on one model, replayed in turn on one stream."""
+    import torch
+    from swiftkv_prefill_skipping_gb300 import api
+    cases = [Case("gqa4", [1, 200], [90, 10], 64, 4, seed=21), Case("gqa4", [150, 3, 6], [700, 30, 1], seed=22)]
+    model, calls = cases[0].model, []
+    for c in cases:
+        q = c.q.cuda()
+        lse, sc = torch.empty(c.n_q, c.T, device="cuda"), torch.zeros(c.total, c.n_kv, 16, device="cuda")
+        out = torch.empty_like(q)
+
+        def call(c=c, q=q, lse=lse, sc=sc, out=out):
+            api.attend(model, q, c.cu, c.ctx, c.kv, cache=1, window=c.window, sinks=c.sinks, out=out, lse=lse)
+            api.attention_weights(model, q, lse, c.cu, c.ctx, c.kv, sc, cache=1, window=c.window, sinks=c.sinks, decay=0.0)
+
+        call()
+        torch.cuda.synchronize()
+        calls.append((call, (out, lse, sc), [t.clone() for t in (out, lse, sc)]))
+    graphs = []
+    for call, _, _ in calls:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            call()
+        graphs.append(g)
+    for _, got, _ in calls:
+        for t in got:
+            t.zero_()
+    for i in (0, 1, 0, 1, 1, 0):
+        graphs[i].replay()
+        torch.cuda.synchronize()
+        _, got, ref = calls[i]
+        assert all(bool((a == b).all()) for a, b in zip(got, ref))
+        got[0].zero_()
+    assert model.status() == 0
+
+
+@pytest.mark.gpu
+def test_pages_far_into_the_pool():
+    """Elements past 2^32 of a pool: the same bits as in a pool of a few pages."""
+    import torch
+    from swiftkv_prefill_skipping_gb300 import api
+    model = model_of("gqa8", 1)
+    n_q, n_kv, d = HEADS["gqa8"]
+    new, ctx, keep = [1, 3, 140], [90, 400, 33], 30
+    cu, lens = np.concatenate([[0], np.cumsum(new)]), [a + b for a, b in zip(new, ctx)]
+    pages = [(n + 15) // 16 for n in lens]
+    table = np.zeros((3, max(pages)), np.int32)
+    at = 0
+    for i, n in enumerate(pages):
+        table[i, :n] = at + np.arange(n)
+        at += n
+    dst = at + np.arange(3 * 2, dtype=np.int32).reshape(3, 2)
+    base = (1 << 32) // (n_kv * 16 * d)
+    g = torch.Generator().manual_seed(3)
+    k, v = (torch.randn(at + 6, n_kv, 16, d, generator=g).bfloat16() for _ in range(2))
+    q = torch.randn(int(cu[-1]), n_q, d, generator=g).bfloat16().cuda()
+    results = []
+    for first in (0, base):
+        kv = api.KVCache(model, first + at + 6, table + first)
+        kv.k[0, first:], kv.v[0, first:] = k.cuda(), v.cuda()
+        lse, sc = torch.empty(n_q, int(cu[-1]), device="cuda"), kv.new_scores()
+        out = api.attend(model, q, cu, ctx, kv, window=100, sinks=4, lse=lse)
+        api.attention_weights(model, q, lse, cu, ctx, kv, sc[0], window=100, sinks=4)
+        to = torch.as_tensor(dst + first, device="cuda", dtype=torch.int32)
+        kept = api.evict(model, kv, sc, lens, keep, sinks=2, recent=5, dst_block_table=to)
+        moved = [t[0, first:].clone() for t in (kv.k, kv.v, sc)]
+        api.evict(model, kv, sc, lens, keep, sinks=2, recent=5)
+        results.append([out, lse, kept] + moved + [t[0, first:].clone() for t in (kv.k, kv.v, sc)])
+        assert model.status() == 0
+        del kv, sc
+    for a, b in zip(*results):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.gpu
+def test_captured_eviction_replays_on_new_scores():
+    import torch
+    from swiftkv_prefill_skipping_gb300 import api
+    c = EvictCase("gqa4", [200, 40], 32, 2, 8, seed=4)
+    sc, dst = torch.rand_like(c.kv.new_scores()), c.dst.cuda()
+    kept = torch.empty(2, 2, c.n_kv, 32, dtype=torch.int32, device="cuda")
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        api.evict(c.model, c.kv, sc, [200, 40], 32, sinks=2, recent=8, dst_block_table=dst, kept=kept)
+    for seed in (1, 2):
+        sc.copy_(torch.rand(sc.shape, generator=torch.Generator().manual_seed(seed)))
+        before = sc.clone()
+        g.replay()
+        torch.cuda.synchronize()
+        got = kept.clone()
+        sc.copy_(before)
+        ref = api.evict(c.model, c.kv, sc, [200, 40], 32, sinks=2, recent=8, dst_block_table=dst)
+        assert torch.equal(got, ref)
 
 
 # ---------------------------------------------------------------- eviction
@@ -550,6 +643,12 @@ def test_refusals_on_the_gpu():
         api.evict(c.model, c.kv, all_sc, [-1, 5], 8)
     with pytest.raises(B.SwiftKVError):  # a destination too narrow
         api.evict(c.model, c.kv, all_sc, [13, 60], 40, dst_block_table=torch.zeros(2, 2, dtype=torch.int32, device="cuda"))
+    other = model_of("d64")  # a cache of other heads
+    for call in (lambda: api.attend(other, q, c.cu, c.ctx, c.kv),
+                 lambda: api.attention_weights(other, q, lse, c.cu, c.ctx, c.kv, sc),
+                 lambda: api.evict(other, c.kv, all_sc, [13, 60], 8)):
+        with pytest.raises(ValueError, match="a cache of"):
+            call()
     torch.cuda.synchronize()
     assert c.model.status() == 0
     assert api.attend(c.model, q[:0], [0], None, c.kv).shape == (0, c.n_q, c.d)
