@@ -12,17 +12,22 @@
 // Both products are transposed: S^T = K Q^T and O^T = V^T P^T with mma.sync m16n8k16, keys or
 // dimensions as the 16 rows of A and the columns as the 8 of B. A group of 8 columns then fills an
 // instruction; with the heads as rows of A (attention_split.cu) half of every instruction and half
-// of the accumulators are padding, and the 90 registers it takes less let 12 warps instead of 7 hide
-// one another's latency. P^T becomes a B operand by one movmatrix per 8 keys. The
-// running maximum may lag behind by 2^8 before O is rescaled, so no reduction over the keys is
-// needed while it holds.
+// of the accumulators are padding, and the registers they took let more warps run (8 on a bf16 cache,
+// where the rings fill shared memory, 12 on FP8) and hide one another's latency. P^T becomes a B
+// operand by one movmatrix per 8 keys. The running maximum may lag behind by 2^8 before O is rescaled,
+// so no reduction over the keys is needed while it holds.
 //
-// bf16: P enters P V as two bf16 parts (about 17 bits). FP8: K and V codes enter as f16 (exact, times 2^-8), the
-// key's scale multiplies the score in float32, and the value's scale rides on P against a
+// bf16: P enters P V as two bf16 parts (about 17 bits). FP8: K and V codes enter as f16 (exact, times
+// 2^-8), the key's scale multiplies the score in float32, and the value's scale rides on P against a
 // reference, P' = p s_v / S_ref in f16; O and S_ref are rescaled when a scale exceeds 128 S_ref.
 //
 // A unit that covers its item writes the output, others (max, sum, unnormalised O) records that
 // attn_rows_merge joins, one warp per column.
+//
+// 24 rows of ~1100 keys, 40 / 8 heads x 128, bf16: 25.6 us, 4.3 TB/s; 16 windows of 4096 keys and 4
+// sinks, 32 / 8 heads, FP8: 37 us, 3.7 TB/s. With one or two units a warp the rings' start, the last
+// round and the merge (3 us) do not overlap anything; on FP8 the unpacking and the products take
+// as long as the reads. 4 rows of up to 64 keys: 7.5 us, the launches' latency.
 #include <cfloat>
 
 #include "common.cuh"

@@ -4,14 +4,18 @@
 // order, to rows 0 .. of the destination pages, K, V, FP8 scales and scores alike.
 //
 // evict_select_kernel: one CTA per list. Scores become order-preserving 32-bit keys in shared
-// memory (protected keys the largest); four rounds of 256-bin histograms find the keep-th largest
-// key, and one ordered pass writes the kept indices, ties by index. The floats of a kept key (its
-// score, FP8 scales) move here.
-// evict_move_kernel: the bound, HBM: kept rows are read once and written once. To other pages, CTAs
-// split the kept list freely. In place every destination row lies at or below its source, so a CTA
-// walks one list in order: a chunk is loaded whole before any of it is written, and the next chunk
-// is loaded before that, which only reads rows that no earlier write reaches. Rows of a list are
-// cut into 64-byte columns, each its own CTA, so that one sequence still fills the GPU.
+// memory (protected keys the largest); three rounds of histograms over 11, 11 and 10 bits find the
+// keep-th largest key, and one ordered pass writes the kept indices, ties by index. The floats of a
+// kept key (its score, FP8 scales) move here. Bound by latency: every round is a pass over shared
+// memory and three barriers. 512 lists of 7000 keys: 39 us.
+//
+// evict_copy_kernel, evict_shift_kernel: the bound, HBM: kept rows are read once and written once.
+// To other pages (copy), CTAs split the kept list freely. In place (shift) every destination row lies
+// at or below its source, so a CTA walks one list in order: a chunk is loaded whole before any of it
+// is written, and the next chunk is loaded before that, which only reads rows that no earlier write
+// reaches. Rows of a list are cut into 64-byte columns, each its own CTA, so that one sequence still
+// fills the GPU. 16 sequences of ~7000 keys to 2048, 4 caches of 8 heads x 128, bf16, to other pages:
+// 1.07 GB in 172 us, 6.2 TB/s of a copy's 6.8; 215-220 us with the selection.
 #include <climits>
 
 #include "common.cuh"

@@ -18,8 +18,14 @@
 // One thread-block cluster per row: each CTA keeps its slice of the row in shared memory (one
 // read of the logits from HBM), and the CTAs exchange maxima, histograms and prefix sums
 // through distributed shared memory. A threshold is found by a histogram over 1024 bins that
-// are linear in (m - l) / T (masses as three 16-bit limbs, 32-bit shared atomics), then by
-// histograms over the key range of the one bin that holds it until a single key is left.
+// are linear in (m - l) / T (masses as three 16-bit limbs, 32-bit shared atomics). The elements of
+// the one bin that holds it meet in the cluster's first CTA, if they are at most 2048, which narrows
+// their keys ten bits a round; more of them are narrowed by histograms over the cluster.
+//
+// Bound by latency for few rows (a cluster barrier is 1 us) and by instructions for many: a weight is
+// some 45 of them and its histogram up to three shared atomics. 128256 logits, us for 1 / 64 / 256 rows
+// (131 MB, 19 us of reading): argmax 4.2 / 12 / 47, no filter 9.4 / 31 / 106, top-k 50 16 / 41 / 146, top-p 0.95
+// 25 / 69 / 235, both 23 / 58 / 212, min-p 0.1 11 / 27 / 95.
 #include <cfloat>
 #include <climits>
 #include <cmath>
@@ -401,8 +407,8 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const SampleParams p) {
     sync_all();
   };
   // The first bin, in descending order of the logits, at which the cluster's running sum reaches
-  // `want`; the sum above it is returned in `before`, the bin's own in `inside`. fraction >= 0: want is that part of all the
-  // bins (at least 1). Each CTA sums its NB / C bins over the cluster's copies, so a bin crosses
+  // `want`; the sum above it is returned in `before`, the bin's own in `inside`. fraction >= 0: want is
+  // that part of all the bins (at least 1). Each CTA sums its NB / C bins over the cluster's copies, so a bin crosses
   // between CTAs once (all CTAs reading all bins took 3 us a search), and only the totals and the
   // decision are exchanged after that.
   auto find = [&](u64& want, float fraction, u64& before, u64& inside) -> int {

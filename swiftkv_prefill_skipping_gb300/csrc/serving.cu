@@ -61,8 +61,8 @@ int pages_of(int k0, int k1) { return k1 > k0 ? (k1 - 1) / kPageSize - k0 / kPag
 
 // Cuts the items' key ranges into units (item, first key, keys) of whole pages and about the same
 // length, so that each of `warps` warps gets one per KV head: units of a fixed 128 or 256 keys left
-// the last round of warps half empty (attention of 24 rows of ~1100 keys, 40 / 8 heads: 22 against
-// 25 us; 16 windows of 4100 FP8 keys: 60 against 83 us). The rounding of a row split this way
+// the last round of warps half empty (with the row kernel as it then was, attention of 24 rows of
+// ~1100 keys, 40 / 8 heads: 22 against 25 us; 16 windows of 4100 FP8 keys: 60 against 83 us). The rounding of a row split this way
 // depends on the call it is part of. ubeg [items + 1]: each item's first unit.
 constexpr int kMinUnitPages = 4;   // below this a unit's partial result costs more than it spreads
 constexpr int kMaxUnitPages = 64;  // with more items than warps: the last round stays short

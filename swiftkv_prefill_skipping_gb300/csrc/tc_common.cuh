@@ -70,8 +70,10 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
 __device__ __forceinline__ bool mbar_wait_ready(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
   return mbar_test_wait(bar, parity) || mbar_wait(bar, parity, abort_flag);
 }
-// One lane of a converged warp. Inside `if (elect_lane())` the compiler knows of one active thread and
-// issues a tcgen05.mma every 32 cycles; under `if (lane == 0)` it takes 44 to 52.
+// One lane of a converged warp. Inside `if (elect_lane())` the compiler knows of one active thread: a
+// product of N = 64 with A in tensor memory issues every 32 cycles (its own time), under `if (lane == 0)`
+// every 44. With A in shared memory N = 64 / 80 / 96 / 128 take 48 / 52 / 56 / 64 either way: 4 KB of A and
+// 32 N bytes of B at 128 bytes a cycle.
 __device__ __forceinline__ bool elect_lane() {
   uint32_t p;
   asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
