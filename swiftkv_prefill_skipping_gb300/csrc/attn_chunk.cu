@@ -57,7 +57,7 @@ using namespace tc;
 constexpr int BQ = 128;                // query rows per tile
 constexpr int THREADS = 384;
 constexpr int REGS_ISSUE = 72, REGS_SOFTMAX = 216;  // 72 + 2 x 216 = 3 x 168, the registers at launch
-constexpr float kLag = 8.f;            // log2 headroom of the running maximum
+constexpr float kGrown = 65536.f;      // a block's row sum from which the running maximum is moved
 constexpr float kLn2 = 0.69314718055994531f;
 
 template <int D>
@@ -181,7 +181,7 @@ __device__ __forceinline__ void add2(float* acc, const float* p) {
       : "f"(p[0]), "f"(p[1]));
 }
 
-template <int D>
+template <int D, bool FP8>
 __global__ void __launch_bounds__(THREADS, 1) attn_chunk_kernel(const __grid_constant__ CUtensorMap tmQ,
                                                                 const __grid_constant__ CUtensorMap tmK,
                                                                 const __grid_constant__ CUtensorMap tmV,
@@ -196,7 +196,6 @@ __global__ void __launch_bounds__(THREADS, 1) attn_chunk_kernel(const __grid_con
   Ctrl<D>* ctl = reinterpret_cast<Ctrl<D>*>(smem + 2 * C::Q_TILE + (KST + VST) * C::KV_TILE);
   volatile int* abort_flag = &ctl->abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const bool fp8 = a.k_scale != nullptr;
   auto bar = [&](uint64_t& b) { return smem_u32(&b); };
   // a warp leaves a wait as one: what follows is collective
   auto wait_all = [&](uint32_t b, uint32_t phase) { return __all_sync(0xffffffffu, mbar_wait_ready(b, phase, abort_flag)) != 0; };
@@ -296,7 +295,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_chunk_kernel(const __grid_con
           }
           if (!(ok = wait_all(is_v ? bar(ctl->v_empty[st]) : bar(ctl->k_empty[st]), ph ^ 1))) break;
           if (lane == 0) {
-            mbar_expect_tx(full, C::KV_TILE + (is_v && fp8 ? 2 * BKV * 4 : 0));
+            mbar_expect_tx(full, C::KV_TILE + (is_v && FP8 ? 2 * BKV * 4 : 0));
             ctl->pend[is_v ? 1 + KST + st : 1 + st] = (int)ph;
           }
           __syncwarp();
@@ -304,7 +303,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_chunk_kernel(const __grid_con
             const uint32_t dst = (is_v ? sV : sK) + st * C::KV_TILE + lane * 2048;
 #pragma unroll
             for (int hf = 0; hf < C::HALVES; ++hf) tma_load_2d(dst + hf * C::KV_HALF, map, hf * 64, row, full);
-            if (is_v && fp8) {
+            if (is_v && FP8) {
               const uint32_t sd = smem_u32(&ctl->scale[st][0][lane * kPageSize]);
               bulk_load(sd, a.k_scale + sr, kPageSize * 4, full);
               bulk_load(sd + BKV * 4, a.v_scale + sr, kPageSize * 4, full);
@@ -406,7 +405,8 @@ __global__ void __launch_bounds__(THREADS, 1) attn_chunk_kernel(const __grid_con
     for (int it = 0; ok && item_at<BKV>(it, a, I); kvb += I.nblk, ++it) {
       const int nb = t ? I.nblk_b : I.nblk_a, q0 = t ? I.q0b : I.q0a;
       if (nb == 0) continue;
-      const int qw = q0 + quarter * 32, qrow = qw + lane, qpos = I.c0 + qrow;  // the warp's first row, this thread's
+// rows past the chunk see what its last row sees
+      const int qw = q0 + quarter * 32, qrow = qw + lane, qpos = I.c0 + min(qrow, I.n - 1);
       const int first = window_begin(qpos, a.window), last = min(qpos, I.nk - 1), sinks = a.window > 0 ? a.sinks : 0;
       float m = -INFINITY, l = 0.f;
       for (int j = 0; j < nb; ++j, ++g) {
@@ -417,7 +417,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_chunk_kernel(const __grid_con
         tc_fence_before();
         mbar_arrive(bar(ctl->s_empty[t]));  // S of the next block may be computed
         const float* scales = nullptr;
-        if (fp8) {
+        if (FP8) {
           const int kv = kvb + j, st = kv % VST;
           if (!(ok = wait(ctl->v_full[st], (uint32_t)((kv / VST) & 1)))) break;
           scales = ctl->scale[st][0];
@@ -445,58 +445,70 @@ __global__ void __launch_bounds__(THREADS, 1) attn_chunk_kernel(const __grid_con
               if (!(in >> i & 1u)) x[16 * c + i] = -INFINITY;
           }
         }
-        float pm[8];
+        // P against the running maximum as it is. The block's own maximum is sought only for rows that have
+        // none yet (the first block), or, with P computed again, where a row's sum has outgrown the old
+        // one: seeking it every time costs 40 us of 400.
+        uint32_t p[BKV / 2];
+        float add, f = 1.f;
+        bool seek = __any_sync(0xffffffffu, m == -INFINITY), any = false;
+#pragma unroll 1
+        while (true) {
+          if (seek) {
+            float pm[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          float v = x[k];
+            for (int k = 0; k < 8; ++k) {
+              float v = x[k];
 #pragma unroll
-          for (int e = 8; e + 8 < BKV; e += 16) v = fmax3f(v, x[k + e], x[k + e + 8]);
-          pm[k] = BKV % 16 ? v : fmaxf(v, x[k + BKV - 8]);
-        }
-        const float mx = fmax3f(fmax3f(pm[0], pm[1], pm[2]), fmax3f(pm[3], pm[4], pm[5]), fmaxf(pm[6], pm[7])) * scale_log2;
-        const bool move = mx > m + kLag;
-        const bool any = __any_sync(0xffffffffu, move);
-        const float mn = move ? mx : m;
-        const float f = m == -INFINITY ? 0.f : ex2_approx(m - mn);
-        m = mn;
-        l *= move ? f : 1.f;
-        const float mneg = m == -INFINITY ? 0.f : -m;  // a row that has seen nothing yet: P = 0
+              for (int e = 8; e + 8 < BKV; e += 16) v = fmax3f(v, x[k + e], x[k + e + 8]);
+              pm[k] = BKV % 16 ? v : fmaxf(v, x[k + BKV - 8]);
+            }
+            const float mx = fmax3f(fmax3f(pm[0], pm[1], pm[2]), fmax3f(pm[3], pm[4], pm[5]), fmaxf(pm[6], pm[7])) * scale_log2;
+            const bool move = mx > m;
+            any = __any_sync(0xffffffffu, move);
+            if (move) {
+              f = m == -INFINITY ? 0.f : ex2_approx(m - mx);
+              m = mx;
+              l *= f;
+            }
+          }
+          const float mneg = m == -INFINITY ? 0.f : -m;  // a row that has seen nothing yet: P = 0
+          float sum[8];
 #pragma unroll
-        for (int i = 0; i < BKV; i += 2) fma2(x + i, x + i, scale_log2, mneg);
-        float sum[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) sum[i] = 0.f;
-#pragma unroll
-        for (int i = 0; i < BKV; i += 2) {
-          x[i] = ex2_approx(x[i]);
-          x[i + 1] = ex2_approx(x[i + 1]);
-          add2(sum + (i & 7), x + i);
-        }
-        l += ((sum[0] + sum[1]) + (sum[2] + sum[3])) + ((sum[4] + sum[5]) + (sum[6] + sum[7]));
-        if (fp8) {
+          for (int i = 0; i < 8; ++i) sum[i] = 0.f;
 #pragma unroll
           for (int i = 0; i < BKV; i += 4) {
-            const float4 w = *reinterpret_cast<const float4*>(scales + BKV + i);
-            x[i] *= w.x;
-            x[i + 1] *= w.y;
-            x[i + 2] *= w.z;
-            x[i + 3] *= w.w;
-          }
-        }
-        uint32_t p[BKV / 2];
+            float e[4];
 #pragma unroll
-        for (int i = 0; i < BKV / 2; ++i) p[i] = pack_bf16(x[2 * i], x[2 * i + 1]);
+            for (int k = 0; k < 4; k += 2) fma2(e + k, x + i + k, scale_log2, mneg);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) e[k] = ex2_approx(e[k]);
+#pragma unroll
+            for (int k = 0; k < 4; k += 2) add2(sum + ((i + k) & 7), e + k);
+            if (FP8) {
+              const float4 w = *reinterpret_cast<const float4*>(scales + BKV + i);
+              e[0] *= w.x;
+              e[1] *= w.y;
+              e[2] *= w.z;
+              e[3] *= w.w;
+            }
+            p[i / 2] = pack_bf16(e[0], e[1]);
+            p[i / 2 + 1] = pack_bf16(e[2], e[3]);
+          }
+          add = ((sum[0] + sum[1]) + (sum[2] + sum[3])) + ((sum[4] + sum[5]) + (sum[6] + sum[7]));
+          if (seek || !__any_sync(0xffffffffu, add > kGrown)) break;
+          seek = true;
+        }
+        l += add;
         // P and O belong to the previous block's product until it has completed
         if (g > 0 && !(ok = wait(ctl->pv_done[t], (uint32_t)((g - 1) & 1)))) break;
         tc_fence_after();
         if (any && j > 0) {
-          const float k = move ? f : 1.f;
 #pragma unroll
           for (int c = 0; c < D; c += 32) {
             float v[32];
             tmem_ld32(s_addr + C::O_COL + c, v);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] *= k;
+            for (int i = 0; i < 32; ++i) v[i] *= f;
             tmem_st32(s_addr + C::O_COL + c, v);
           }
         }
@@ -560,7 +572,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_chunk_kernel(const __grid_con
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
 }
 
-template <int D>
+template <int D, bool FP8>
 cudaError_t launch_d(const ChunkArgs& a, const bf16* q, int ldq, int T, const bf16* k, const bf16* v, int num_sms,
                      cudaStream_t s) {
   constexpr int smem = smem_bytes<D>();
@@ -575,9 +587,9 @@ cudaError_t launch_d(const ChunkArgs& a, const bf16* q, int ldq, int T, const bf
       !tma_map_bf16_2d(&mt, a.v_tail, a.tail_seqs * kTailSlots * a.n_kv * kPageSize, D, D, 64, kPageSize, true))
     return cudaErrorNotSupported;
   static PerDeviceOnce once;
-  cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void*>(attn_chunk_kernel<D>), smem, once);
+  cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void*>(attn_chunk_kernel<D, FP8>), smem, once);
   if (e != cudaSuccess) return e;
-  attn_chunk_kernel<D><<<(int)(a.num_items < num_sms ? a.num_items : num_sms), THREADS, smem, s>>>(
+  attn_chunk_kernel<D, FP8><<<(int)(a.num_items < num_sms ? a.num_items : num_sms), THREADS, smem, s>>>(
       mq, mk, mv, mt, a, 1.4426950408889634f / sqrtf((float)D));
   return cudaGetLastError();
 }
@@ -589,8 +601,10 @@ cudaError_t launch_attn_chunk(const ChunkArgs& a, const bf16* q, int ldq, int T,
   if (a.num_items <= 0) return cudaSuccess;
   if (a.head_pairs && (a.n_q / a.n_kv) % 2) return cudaErrorNotSupported;
   if (!a.k_scale != !a.v_scale) return cudaErrorNotSupported;
-  if (d_head == 128) return launch_d<128>(a, q, ldq, T, k, v, num_sms, s);
-  if (d_head == 64) return launch_d<64>(a, q, ldq, T, k, v, num_sms, s);
+  if (d_head == 128)
+    return a.k_scale ? launch_d<128, true>(a, q, ldq, T, k, v, num_sms, s) : launch_d<128, false>(a, q, ldq, T, k, v, num_sms, s);
+  if (d_head == 64)
+    return a.k_scale ? launch_d<64, true>(a, q, ldq, T, k, v, num_sms, s) : launch_d<64, false>(a, q, ldq, T, k, v, num_sms, s);
   return cudaErrorNotSupported;
 }
 

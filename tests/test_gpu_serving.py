@@ -43,7 +43,7 @@ def seen_mask(n, c0, window, sinks):
 class Case:
     """A ragged batch over poisoned pools; K and V of visible keys are finite, all else is NaN."""
 
-    def __init__(self, heads, new, ctx, window=0, sinks=0, fp8=False, seed=0, caches=2, cache=1, scale=1.0):
+    def __init__(self, heads, new, ctx, window=0, sinks=0, fp8=False, seed=0, caches=2, cache=1, scale=1.0, ramp=None):
         import torch
         from swiftkv_prefill_skipping_gb300 import api
         self.n_q, self.n_kv, self.d = HEADS[heads]
@@ -75,6 +75,9 @@ class Case:
             self.seen.append(some)
             kk = torch.randn(c0 + n, self.n_kv, self.d, generator=g) * scale
             vv = torch.randn(c0 + n, self.n_kv, self.d, generator=g)
+            if ramp:  # scores near ramp[0] at the first key, ramp[1] at the last
+                at = torch.linspace(ramp[0], ramp[1], c0 + n)[:, None, None]
+                kk = kk + at / math.sqrt(self.d)
             for p in range(need[s]):
                 if some[16 * p:16 * p + 16].any():
                     table[s, p] = perm[first + p]
@@ -109,7 +112,7 @@ class Case:
         else:
             self.kv.k[cache] = pool.bfloat16().cuda()
             self.kv.v[cache] = vpool.bfloat16().cuda()
-        self.q = (torch.randn(T, self.n_q, self.d, generator=g) * scale).bfloat16()
+        self.q = (torch.randn(T, self.n_q, self.d, generator=g) * scale + (1.0 if ramp else 0.0)).bfloat16()
         self.T, self.P, self.total = T, P, total
 
     def logits(self, s, h):
@@ -231,6 +234,19 @@ def test_attend_large_scores():
         for fp8 in (False, True):
             c = Case("gqa4", new, ctx, 150, 2, fp8, seed=3, scale=3.0)
             c.check_attend(*c.attend())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("heads", ["gqa4", "d64"])
+@pytest.mark.parametrize("ramp", [(-500, -500), (-500, 0), (0, 500), (500, -500), (-900, 900), (300, 300)])
+def test_attend_scores_far_from_zero(ramp, heads):
+    """Weights that would underflow or overflow against any maximum but the row's own, and maxima that
+    rise by more than a block's range from one block to the next or fall after the first."""
+    for new, ctx in (([1, 3], [300, 64]), ([200, 5], [100, 400])):
+        for fp8, window in ((False, 0), (False, 150), (True, 0), (True, 90)):
+            c = Case(heads, new, ctx, window, 2, fp8, seed=4, ramp=ramp)
+            out, lse = c.attend()
+            c.check_attend(out, lse)
 
 
 @pytest.mark.gpu
