@@ -26,16 +26,19 @@
 // mbarrier waits are bounded; when one expires the CTA flags kStatusTimeout, drains its copies and
 // MMAs, frees tensor memory and exits.
 //
-// 4 chunks of ~1960 rows after 0 - 6048 keys, 32 / 8 heads x 128: 434 us, 1.18 PFLOP/s, the tensor pipe
-// active 61 % of the time; the same rows through a window of 1024 and 4 sinks: 174 us. Bound by the
-// softmax: a warp takes some 2400 cycles for a block of 80 keys, 400 instructions at one every six cycles
-// (dependent latencies, exponentials, the waits' fixed cost; without the exponentials 365 us, without
-// the maximum 380). S of an 80-key block reads 6.5 KB
-// of shared memory per 16 dims, 52 cycles where the product takes 40: with that the tensor core alone
-// would take 307 us. Measured and not kept: four softmax warpgroups on alternate 64-key blocks with P over
-// S, 504 us (S waits for the product of two blocks before); two threads a row, half of a block's columns
-// each, 509 us (a block's fixed instructions double); P with the old maximum and a second try where it
-// moved, 468 us.
+// The softmax computes P against the running maximum as it is. Only where a row has none yet, or where
+// its sum of a block passes 2^16, does a warp look for the block's own maximum, before it computes P
+// (again): seeking it in every block stood in the chain with 370 of its 2400 cycles. Exponentials, sums and
+// the rounding of P go four columns at a time, and FP8 is a template parameter, so that no branch
+// parts them (436 us with all three undone).
+//
+// 4 chunks of ~1960 rows after 0 - 6048 keys, 32 / 8 heads x 128: 360 us, 1.43 PFLOP/s; the same rows
+// through a window of 1024 and 4 sinks: 153 us. Bound by the tensor core and the hand-overs to it: 337 us
+// without any softmax. S of an 80-key block reads 6.5 KB of shared memory per 16 dims, 52 cycles
+// where the product takes 40, and a wider block does not fit beside P and O: with that the products
+// alone take 307 us. Measured and not kept: four softmax warpgroups on alternate 64-key blocks with P
+// over S (504 us, where this form took 434: S waits for the product of two blocks before); two threads a
+// row, half of a block's columns each (509).
 //
 // Pages without a visible key are not loaded (zeros instead), and pages of V that the chunk sees in
 // part come from zero-padded copies (launch_v_tail). FP8: K and V are an expansion to bf16 codes;
