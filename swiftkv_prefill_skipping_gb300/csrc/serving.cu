@@ -84,6 +84,7 @@ void cut_units(const std::vector<int>& item_ids, const std::vector<Ranges>& seen
     if (count(mid) <= budget) hi = mid;
     else lo = mid + 1;
   }
+  units->reserve(3 * count(lo));
   if (ubeg) ubeg->assign(1, 0);
   for (size_t b = 0; b < seen.size(); ++b) {
     for (int i = 0; i < seen[b].n; ++i) {
@@ -200,6 +201,9 @@ int AttendPlan::make(const swiftkv_model* m, const int32_t* cu, const int32_t* c
   const int tile_rows = head_pairs ? 128 : 256;
   std::vector<int> cuv(cu, cu + P + 1), ctxv(P, 0), tiles, items, ids, exp_items;
   std::vector<Ranges> seen;
+  items.reserve(4 * P);
+  ids.reserve(P);
+  seen.reserve(P);
   const int G = c.n_q / c.n_kv, group = kRowsCols / G;  // rows of an item of the row kernel
   for (int i = 0; i < P; ++i) {
     const int n = cu[i + 1] - cu[i], c0 = ctx ? ctx[i] : 0;
@@ -234,6 +238,7 @@ int AttendPlan::make(const swiftkv_model* m, const int32_t* cu, const int32_t* c
   if (std::max({units.size(), tiles.size(), exp_items.size()}) >= (size_t)1 << 28 ||
       (long long)num_units * c.n_kv >= (1LL << 31) || (long long)num_tiles * c.n_q >= (1LL << 31))
     return fail(SWIFTKV_EUNSUPPORTED, "batch too large");
+  ints.reserve(2 * cuv.size() + tiles.size() + units.size() + exp_items.size() + ubeg.size() + items.size());
   o_cu = put(&ints, cuv);
   o_ctx = put(&ints, ctxv);
   o_tiles = put(&ints, tiles);
@@ -241,7 +246,7 @@ int AttendPlan::make(const swiftkv_model* m, const int32_t* cu, const int32_t* c
   o_units = put(&ints, units);
   o_ubeg = put(&ints, ubeg);
   o_exp = put(&ints, exp_items);
-  count_work(cu, ctx, b, &keys, &pairs);
+  if (m->prof_on) count_work(cu, ctx, b, &keys, &pairs);
   return SWIFTKV_OK;
 }
 
@@ -382,12 +387,13 @@ int WeightsPlan::make(const swiftkv_model* m, const int32_t* cu, const int32_t* 
   if (std::max({units.size(), tiles.size(), exp_items.size()}) >= (size_t)1 << 28 ||
       (long long)num_units * c.n_kv >= (1LL << 31) || (long long)num_tiles * c.n_kv >= (1LL << 31))
     return fail(SWIFTKV_EUNSUPPORTED, "batch too large");
+  ints.reserve(2 * cuv.size() + tiles.size() + units.size() + exp_items.size());
   o_cu = put(&ints, cuv);
   o_ctx = put(&ints, ctxv);
   o_units = put(&ints, units);
   o_tiles = put(&ints, tiles);
   o_exp = put(&ints, exp_items);
-  count_work(cu, ctx, b, &keys, &pairs);
+  if (m->prof_on) count_work(cu, ctx, b, &keys, &pairs);
   return SWIFTKV_OK;
 }
 
