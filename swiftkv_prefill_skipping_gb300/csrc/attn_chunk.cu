@@ -32,8 +32,8 @@
 // the rounding of P go four columns at a time, and FP8 is a template parameter, so that no branch
 // parts them (436 us with all three undone).
 //
-// 4 chunks of ~1960 rows after 0 - 6048 keys, 32 / 8 heads x 128: 360 us, 1.43 PFLOP/s; the same rows
-// through a window of 1024 and 4 sinks: 153 us. Bound by the tensor core and the hand-overs to it: 337 us
+// 4 chunks of ~1960 rows after 0 - 6048 keys, 32 / 8 heads x 128: 355 us, 1.45 PFLOP/s; the same rows
+// through a window of 1024 and 4 sinks: 148 us. Bound by the tensor core and the hand-overs to it: 337 us
 // without any softmax. S of an 80-key block reads 6.5 KB of shared memory per 16 dims, 52 cycles
 // where the product takes 40, and a wider block does not fit beside P and O: with that the products
 // alone take 307 us. Measured and not kept: four softmax warpgroups on alternate 64-key blocks with P
@@ -48,6 +48,7 @@
 
 #include "attn_common.cuh"
 #include "common.cuh"
+#include "pdl.cuh"
 #include "serving.h"
 #include "tc_common.cuh"
 
@@ -237,6 +238,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_chunk_kernel(const __grid_con
   tc_fence_after();
   const uint32_t tmem = ctl->tmem_base;
   Item I;
+  griddep_wait();  // launched as a dependent of the kernel that writes the tail copies (or the expansion)
 
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_ISSUE));
@@ -592,9 +594,8 @@ cudaError_t launch_d(const ChunkArgs& a, const bf16* q, int ldq, int T, const bf
   static PerDeviceOnce once;
   cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void*>(attn_chunk_kernel<D, FP8>), smem, once);
   if (e != cudaSuccess) return e;
-  attn_chunk_kernel<D, FP8><<<(int)(a.num_items < num_sms ? a.num_items : num_sms), THREADS, smem, s>>>(
-      mq, mk, mv, mt, a, 1.4426950408889634f / sqrtf((float)D));
-  return cudaGetLastError();
+  return launch_pdl(attn_chunk_kernel<D, FP8>, dim3(a.num_items < num_sms ? a.num_items : num_sms), dim3(THREADS), smem,
+                    s, mq, mk, mv, mt, a, 1.4426950408889634f / sqrtf((float)D));
 }
 
 }  // namespace

@@ -357,6 +357,7 @@ __global__ void __launch_bounds__(WT, 1) weights_tc_kernel(const __grid_constant
   tc_fence_after();
   const uint32_t tmem = ctl->tmem_base;
   WItem I;
+  griddep_wait();  // launched as a dependent of the kernel before it
 
   if (warp == 0) {
     if (lane == 0) {
@@ -622,9 +623,8 @@ cudaError_t tc_launch(const WeightsArgs& a, const bf16* k, const float* ks, cons
   cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void*>(weights_tc_kernel<D>), smem, once);
   if (e != cudaSuccess) return e;
   const long long n_items = (long long)num_tiles * a.n_kv;
-  weights_tc_kernel<D><<<(int)(n_items < num_sms ? n_items : num_sms), WT, smem, s>>>(
-      mq, mk, a, ks, bt_k, pages_k, tiles, n_items, kLog2e / sqrtf((float)D));
-  return cudaGetLastError();
+  return launch_pdl(weights_tc_kernel<D>, dim3((unsigned)(n_items < num_sms ? n_items : num_sms)), dim3(WT), smem, s, mq, mk,
+                    a, ks, bt_k, pages_k, tiles, n_items, kLog2e / sqrtf((float)D));
 }
 
 }  // namespace

@@ -396,6 +396,8 @@ __global__ void v_tail_kernel(const bf16* __restrict__ v_pool, const int* __rest
                               const int* __restrict__ cu, const int* __restrict__ ctx, int n_kv, int dh, int window,
                               int sinks, bf16* __restrict__ out) {
   const int s = blockIdx.x, slot = blockIdx.y;
+  griddep_launch_dependents();
+  griddep_wait();
   const int n = cu[s + 1] - cu[s];
   if (n < 1) return;
   const TailPages t = tail_pages(ctx ? ctx[s] : 0, n, window, sinks);
@@ -403,13 +405,13 @@ __global__ void v_tail_kernel(const bf16* __restrict__ v_pool, const int* __rest
   if (pidx < 0) return;
   const int page = bt[(size_t)s * max_pages + pidx];
   const bool ok = page >= 0 && page < num_pages;
-  const int per_page = n_kv * kPageSize * dh;
-  bf16* dst = out + ((size_t)s * kTailSlots + slot) * per_page;
-  for (int e = threadIdx.x * 8; e < per_page; e += blockDim.x * 8) {
-    const bool seen = ok && t.seen(pidx * kPageSize + e / dh % kPageSize);
-    *reinterpret_cast<uint4*>(dst + e) =
-        seen ? *reinterpret_cast<const uint4*>(v_pool + (size_t)page * per_page + e) : make_uint4(0, 0, 0, 0);
-  }
+  // a KV head's rows of the page, 16 bytes a thread
+  const int per_head = kPageSize * dh, e = threadIdx.x * 8;
+  if (e >= per_head) return;
+  bf16* dst = out + (((size_t)s * kTailSlots + slot) * n_kv + blockIdx.z) * per_head;
+  const bool seen = ok && t.seen(pidx * kPageSize + e / dh);
+  *reinterpret_cast<uint4*>(dst + e) =
+      seen ? *reinterpret_cast<const uint4*>(v_pool + ((size_t)page * n_kv + blockIdx.z) * per_head + e) : make_uint4(0, 0, 0, 0);
 }
 
 }  // namespace
@@ -453,9 +455,9 @@ cudaError_t launch_v_tail(const bf16* v_pool, const int* block_table, int max_pa
                           const int* ctx, int P, int n_kv, int d_head, int window, int sinks, bf16* out,
                           cudaStream_t stream) {
   if (P <= 0) return cudaSuccess;
-  v_tail_kernel<<<dim3(P, kTailSlots), 256, 0, stream>>>(v_pool, block_table, max_pages, num_pages, cu, ctx, n_kv,
-                                                         d_head, window, sinks, out);
-  return cudaGetLastError();
+  if (kPageSize * d_head > 8 * 256) return cudaErrorNotSupported;
+  return launch_pdl(v_tail_kernel, dim3(P, kTailSlots, n_kv), dim3(256), 0, stream, v_pool, block_table, max_pages,
+                    num_pages, cu, ctx, n_kv, d_head, window, sinks, out);
 }
 
 cudaError_t launch_plan_prefill(const int* cu, const int* ctx, const int* pos_off, int P, int T, const int* tokens, int vocab,
