@@ -17,15 +17,18 @@
 // operand by one movmatrix per 8 keys. The running maximum may lag behind by 2^8 before O is rescaled,
 // so no reduction over the keys is needed while it holds.
 //
-// bf16: P enters P V as two bf16 parts (about 17 bits). FP8: K and V codes enter as f16 (exact, times
-// 2^-8), the key's scale multiplies the score in float32, and the value's scale rides on P against a
-// reference, P' = p s_v / S_ref in f16; O and S_ref are rescaled when a scale exceeds 128 S_ref.
+// P enters P V as two bf16 parts (about 17 bits). FP8: K's codes enter as f16 (exact, times 2^-8) and
+// the key's scale multiplies the score in float32; V's codes enter as bf16 (exact) and the value's
+// scale rides on P, P' = 2^16 p s_v, which has float32's range in bf16: keys whose value scales are any
+// factor apart keep their bits. (P' in f16 against the largest scale so far lost those far below it.)
+// The 2^16, undone at the end, keeps P' above bf16's subnormals for value scales down to float32's;
+// scales have to stay below 2^100.
 //
 // A unit that covers its item writes the output, others (max, sum, unnormalised O) records that
 // attn_rows_merge joins, one warp per column.
 //
 // 24 rows of ~1100 keys, 40 / 8 heads x 128, bf16: 25.6 us, 4.3 TB/s; 16 windows of 4096 keys and 4
-// sinks, 32 / 8 heads, FP8: 37 us, 3.7 TB/s. With one or two units a warp the rings' start, the last
+// sinks, 32 / 8 heads, FP8: 38 us, 3.6 TB/s. With one or two units a warp the rings' start, the last
 // round and the merge (3 us) do not overlap anything; on FP8 the unpacking and the products take
 // as long as the reads. 4 rows of up to 64 keys: 7.5 us, the launches' latency.
 #include <cfloat>
@@ -67,9 +70,23 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
 // and f16's subnormals cover e4m3's): the even and the odd bytes. Cheaper than two conversions and
 // the moves that line their inputs up, and part of it runs on the multiply pipe.
 constexpr float kCodeScale = 256.f;
+constexpr float kValueShift = 65536.f;
 __device__ __forceinline__ void unpack4(uint32_t r, uint32_t& even, uint32_t& odd) {
   even = ((r * 128u) & 0x3f803f80u) | ((r * 256u) & 0x80008000u);
   odd = ((r >> 1) & 0x3f803f80u) | (r & 0x80008000u);
+}
+// The same as two bf16 pairs with the values themselves: the shifted bits are 2^-120 of them, subnormal
+// for e4m3's subnormals, and the product (which keeps subnormals) is exact.
+__device__ __forceinline__ void unpack4_bf16(uint32_t r, uint32_t& even, uint32_t& odd) {
+  uint32_t x[2] = {((r << 4) & 0x07f007f0u) | ((r << 8) & 0x80008000u), ((r >> 4) & 0x07f007f0u) | (r & 0x80008000u)};
+  const uint32_t up = 0x7b807b80u;  // 2^120 twice
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const __nv_bfloat162 y = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&x[i]), *reinterpret_cast<const __nv_bfloat162*>(&up));
+    x[i] = *reinterpret_cast<const uint32_t*>(&y);
+  }
+  even = x[0];
+  odd = x[1];
 }
 
 // NT: columns in groups of 8.
@@ -165,7 +182,6 @@ __global__ void __launch_bounds__(Rg<D, FP8>::WARPS * 32, 1) attn_rows_kernel(
   float m[NT][2], l[NT][2];         // of columns 2 qd, 2 qd + 1
   int qpos[NT][2];                  // their positions, -1: no such column
   int row0 = 0, cols = 0, pos_lo = 0, pos_hi = 0;
-  float sref = 0.f, isref = 0.f;
   long long cv = gw;
   int cp = 0, cslot = 0;
   Geo cg;
@@ -211,7 +227,6 @@ __global__ void __launch_bounds__(Rg<D, FP8>::WARPS * 32, 1) attn_rows_kernel(
 #pragma unroll
           for (int e = 0; e < 4; ++e) o[t][i][e] = 0.f;
       }
-      sref = isref = 0.f;
     }
 
     // S^T = K Q^T: keys g0, g0 + 8 (rows) x columns 2 qd, 2 qd + 1, in two independent chains
@@ -269,29 +284,17 @@ __global__ void __launch_bounds__(Rg<D, FP8>::WARPS * 32, 1) attn_rows_kernel(
           if (!(ok && key >= cg.k0 && key < cg.k1 && attn_visible(key, qpos[t][e & 1], a.window, a.sinks))) z[t][e] = -INFINITY;
         }
     }
-    float v_lo = 0.f, v_hi = 0.f;  // FP8: the value scales of keys g0, g0 + 8 (0 outside the unit)
-    bool move = false;
+    float v_lo = 1.f, v_hi = 1.f;  // FP8: the shifted value scales of keys g0, g0 + 8 (0 outside the unit)
     if (FP8) {
-      v_lo = key0 + g0 >= cg.k0 && key0 + g0 < cg.k1 ? sc[kPageSize + g0] : 0.f;
-      v_hi = key0 + g0 + 8 >= cg.k0 && key0 + g0 + 8 < cg.k1 ? sc[kPageSize + g0 + 8] : 0.f;
-      move = fmaxf(v_lo, v_hi) > 128.f * sref;
+      v_lo = key0 + g0 >= cg.k0 && key0 + g0 < cg.k1 ? kValueShift * sc[kPageSize + g0] : 0.f;
+      v_hi = key0 + g0 + 8 >= cg.k0 && key0 + g0 + 8 < cg.k1 ? kValueShift * sc[kPageSize + g0 + 8] : 0.f;
     }
+    bool move = false;
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
       for (int e = 0; e < 2; ++e) move |= fmaxf(z[t][e], z[t][e + 2]) > m[t][e] + kLag;
     if (__any_sync(0xffffffffu, move)) {
-      float f8 = 1.f;
-      if (FP8) {
-        float v = fmaxf(v_lo, v_hi);
-#pragma unroll
-        for (int o2 = 4; o2 <= 16; o2 <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o2));
-        if (v > 128.f * sref) {
-          f8 = sref / v;  // 0 the first time
-          sref = v;
-          isref = 1.f / v;
-        }
-      }
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         float al[2];
@@ -304,7 +307,6 @@ __global__ void __launch_bounds__(Rg<D, FP8>::WARPS * 32, 1) attn_rows_kernel(
           al[e] = mn == m[t][e] ? 1.f : exp2f(m[t][e] - mn);  // 0 the first time
           m[t][e] = mn;
           l[t][e] *= al[e];
-          al[e] *= f8;
         }
 #pragma unroll
         for (int i = 0; i < D / 16; ++i)
@@ -321,18 +323,13 @@ __global__ void __launch_bounds__(Rg<D, FP8>::WARPS * 32, 1) attn_rows_kernel(
       for (int e = 0; e < 4; ++e) p[e] = ex2_approx(z[t][e] - (m[t][e & 1] == -INFINITY ? 0.f : m[t][e & 1]));
       l[t][0] += p[0] + p[2];
       l[t][1] += p[1] + p[3];
-      if (FP8) {
-        ph[t][0] = transpose8(pack_f16(p[0] * (v_lo * isref), p[1] * (v_lo * isref)));
-        ph[t][1] = transpose8(pack_f16(p[2] * (v_hi * isref), p[3] * (v_hi * isref)));
-      } else {
-        uint32_t h0, l0, h1, l1;
-        split_pair_bf16(p[0], p[1], h0, l0);
-        split_pair_bf16(p[2], p[3], h1, l1);
-        ph[t][0] = transpose8(h0);
-        ph[t][1] = transpose8(h1);
-        pl[t][0] = transpose8(l0);
-        pl[t][1] = transpose8(l1);
-      }
+      uint32_t h0, l0, h1, l1;
+      split_pair_bf16(p[0] * v_lo, p[1] * v_lo, h0, l0);
+      split_pair_bf16(p[2] * v_hi, p[3] * v_hi, h1, l1);
+      ph[t][0] = transpose8(h0);
+      ph[t][1] = transpose8(h1);
+      pl[t][0] = transpose8(l0);
+      pl[t][1] = transpose8(l1);
     }
     // O^T += V^T P^T. bf16: tile i holds dims 16 i + row. FP8: ldmatrix.trans yields two keys x two
     // neighbouring dims, so rows 0-7 are the even dims of the chunk and rows 8-15 the odd ones
@@ -345,10 +342,13 @@ __global__ void __launch_bounds__(Rg<D, FP8>::WARPS * 32, 1) attn_rows_kernel(
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           uint32_t va[4];
-          unpack4(r[2 * h], va[0], va[1]);
-          unpack4(r[2 * h + 1], va[2], va[3]);
+          unpack4_bf16(r[2 * h], va[0], va[1]);
+          unpack4_bf16(r[2 * h + 1], va[2], va[3]);
 #pragma unroll
-          for (int t = 0; t < NT; ++t) mma_f16_16816(o[t][c + h], va, ph[t]);
+          for (int t = 0; t < NT; ++t) {
+            mma_bf16_16816(o[t][c + h], va, ph[t]);
+            mma_bf16_16816(o[t][c + h], va, pl[t]);
+          }
         }
       }
     } else {
@@ -382,7 +382,7 @@ __global__ void __launch_bounds__(Rg<D, FP8>::WARPS * 32, 1) attn_rows_kernel(
           // dims this thread holds of tile i: bf16 16 i + g0 and + 8; FP8 16 i + 2 g0 and + 1
           if (whole) {
             const int row = row0 + col / G, h = cg.kvh * G + col % G;
-            const float f = (FP8 ? kCodeScale * sref : 1.f) / sum;
+            const float f = (FP8 ? 1.f / kValueShift : 1.f) / sum;
             if (a.lse && g0 == 0) a.lse[(size_t)h * a.ldl + row] = (m[t][e] + log2f(sum)) * kLn2;
             bf16* dst = a.out + (size_t)row * a.ldo + (size_t)h * D;
 #pragma unroll
@@ -400,8 +400,7 @@ __global__ void __launch_bounds__(Rg<D, FP8>::WARPS * 32, 1) attn_rows_kernel(
 #pragma unroll
             for (int i = 0; i < D / 16; ++i) {
               if (FP8) {
-                *reinterpret_cast<float2*>(pp + 4 + 16 * i + 2 * g0) =
-                    make_float2(o[t][i][e] * (kCodeScale * sref), o[t][i][2 + e] * (kCodeScale * sref));
+                *reinterpret_cast<float2*>(pp + 4 + 16 * i + 2 * g0) = make_float2(o[t][i][e] * (1.f / kValueShift), o[t][i][2 + e] * (1.f / kValueShift));
               } else {
                 pp[4 + 16 * i + g0] = o[t][i][e];
                 pp[4 + 16 * i + 8 + g0] = o[t][i][2 + e];
