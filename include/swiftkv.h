@@ -235,9 +235,9 @@ int swiftkv_decode_step(swiftkv_model* m, const int32_t* tokens, const int32_t* 
  *   out  device bf16, rows ldo apart (same rules); must not overlap q
  *   lse  device float [n_q][T] or NULL: natural log of sum_j exp(q . k_j / sqrt(d_head))
  * P, over an FP8 cache times the value's scale, enters the product with V rounded to bf16 (chunks of
- * more than 4 rows) or as two bf16 parts (shorter ones); q enters as f16 for shorter ones over an FP8
- * cache and must stay below 65504 there; scores, sums and the output accumulate in float32. FP8 value
- * scales have to stay below 2^95. swiftkv_set_attention_impl does not concern this call. */
+ * more than 4 rows) or as two bf16 parts (shorter ones); scores, sums and the output accumulate in
+ * float32. FP8 value scales have to stay below 2^95. swiftkv_set_attention_impl does not concern this
+ * call. */
 int swiftkv_attend(swiftkv_model* m, int cache, const void* q, int ldq, const int32_t* cu_seqlens,
                    const int32_t* ctx_lens, int num_seqs, const swiftkv_kv_pages* kv, int window, int sinks,
                    void* out, int ldo, float* lse, swiftkv_stream stream);

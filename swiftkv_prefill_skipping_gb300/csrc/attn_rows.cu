@@ -18,7 +18,7 @@
 // so no reduction over the keys is needed while it holds.
 //
 // P enters P V as two bf16 parts (about 17 bits). FP8: K's codes enter as f16 (exact, times 2^-8) and
-// the key's scale multiplies the score in float32; V's codes enter as bf16 (exact) and the value's
+// the key's scale multiplies the score in float32, q as f16 under a power of two per column; V's codes enter as bf16 (exact) and the value's
 // scale rides on P, P' = 2^16 p s_v, which has float32's range in bf16: keys whose value scales are any
 // factor apart keep their bits. (P' in f16 against the largest scale so far lost those far below it.)
 // The 2^16, undone at the end, keeps P' above bf16's subnormals for value scales down to float32's;
@@ -28,7 +28,7 @@
 // attn_rows_merge joins, one warp per column.
 //
 // 24 rows of ~1100 keys, 40 / 8 heads x 128, bf16: 25.6 us, 4.3 TB/s; 16 windows of 4096 keys and 4
-// sinks, 32 / 8 heads, FP8: 38 us, 3.6 TB/s. With one or two units a warp the rings' start, the last
+// sinks, 32 / 8 heads, FP8: 39 us, 3.5 TB/s (167 registers; with 16 columns a few of them spill). With one or two units a warp the rings' start, the last
 // round and the merge (3 us) do not overlap anything; on FP8 the unpacking and the products take
 // as long as the reads. 4 rows of up to 64 keys: 7.5 us, the launches' latency.
 #include <cfloat>
@@ -87,6 +87,37 @@ __device__ __forceinline__ void unpack4_bf16(uint32_t r, uint32_t& even, uint32_
   }
   even = x[0];
   odd = x[1];
+}
+
+// A column of q (held by the 4 lanes of a group, dims 16 ks + 4 qd .. + 3 each) as f16, times the power
+// of two that takes its largest element to [2^14, 2^15), and the inverse power. Exact for elements down
+// to 2^-31 of the largest (below, off by 2^-39 of it), whatever q's size, where f16 alone ends at 65504.
+template <int D>
+__device__ __forceinline__ void load_q_f16(const bf16* src, bool in, int qd, uint32_t (*qf)[2], float& back) {
+  float top = 0.f;
+#pragma unroll
+  for (int ks = 0; ks < D / 16; ++ks) {
+    const uint2 w = in ? *reinterpret_cast<const uint2*>(src + ks * 16 + 4 * qd) : make_uint2(0u, 0u);
+    qf[ks][0] = w.x;
+    qf[ks][1] = w.y;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const float2 x = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&qf[ks][e]));
+      top = fmaxf(top, fmaxf(fabsf(x.x), fabsf(x.y)));
+    }
+  }
+  top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+  top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+  const int ex = max(__float_as_int(top) >> 23, 15);  // biased; both powers stay normal
+  const float to = __int_as_float((268 - ex) << 23);
+  back = __int_as_float((ex - 14) << 23);
+#pragma unroll
+  for (int ks = 0; ks < D / 16; ++ks) {
+    const float2 x = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&qf[ks][0]));
+    const float2 y = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&qf[ks][1]));
+    qf[ks][0] = pack_f16(x.x * to, y.x * to);
+    qf[ks][1] = pack_f16(x.y * to, y.y * to);
+  }
 }
 
 // NT: columns in groups of 8.
@@ -180,6 +211,7 @@ __global__ void __launch_bounds__(Rg<D, FP8>::WARPS * 32, 1) attn_rows_kernel(
   uint32_t qf[NT][D / 16][2];
   float o[NT][D / 16][4];           // O^T: 16 dimensions x 8 columns a tile
   float m[NT][2], l[NT][2];         // of columns 2 qd, 2 qd + 1
+  float qback[NT][2];               // FP8: what undoes their q's power of two
   int qpos[NT][2];                  // their positions, -1: no such column
   int row0 = 0, cols = 0, pos_lo = 0, pos_hi = 0;
   long long cv = gw;
@@ -202,15 +234,14 @@ __global__ void __launch_bounds__(Rg<D, FP8>::WARPS * 32, 1) attn_rows_kernel(
         const int cb = t * 8 + g0;
         const bool in = cb < cols;
         const bf16* src = a.q + (size_t)(row0 + (in ? cb / G : 0)) * a.ldq + (cg.kvh * G + (in ? cb % G : 0)) * D;
+        if (FP8) {  // f16, dims 16 ks + 4 qd + {0, 2} and {1, 3}: the order in which K's codes arrive
+          float back;
+          load_q_f16<D>(src, in, qd, qf[t], back);
 #pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) {
-          if (FP8) {  // f16, dims 16 ks + 4 qd + {0, 2} and {1, 3}: the order in which K's codes arrive
-            const uint2 w = in ? *reinterpret_cast<const uint2*>(src + ks * 16 + 4 * qd) : make_uint2(0u, 0u);
-            const float2 x = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w.x));
-            const float2 y = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w.y));
-            qf[t][ks][0] = pack_f16(x.x, y.x);
-            qf[t][ks][1] = pack_f16(x.y, y.y);
-          } else {
+          for (int e = 0; e < 2; ++e) qback[t][e] = __shfl_sync(0xffffffffu, back, (2 * qd + e) * 4);
+        } else {
+#pragma unroll
+          for (int ks = 0; ks < D / 16; ++ks) {
             qf[t][ks][0] = in ? *reinterpret_cast<const uint32_t*>(src + ks * 16 + 2 * qd) : 0u;
             qf[t][ks][1] = in ? *reinterpret_cast<const uint32_t*>(src + ks * 16 + 8 + 2 * qd) : 0u;
           }
@@ -273,7 +304,7 @@ __global__ void __launch_bounds__(Rg<D, FP8>::WARPS * 32, 1) attn_rows_kernel(
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) z[t][e] = (s[t][0][e] + s[t][1][e]) * (e < 2 ? c_lo : c_hi);
+      for (int e = 0; e < 4; ++e) z[t][e] = (s[t][0][e] + s[t][1][e]) * ((e < 2 ? c_lo : c_hi) * (FP8 ? qback[t][e & 1] : 1.f));
     if (!inside) {
       const bool ok = *reinterpret_cast<const int*>(st + S::STAGE - 16);
 #pragma unroll

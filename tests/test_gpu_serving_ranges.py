@@ -137,3 +137,11 @@ def test_values_far_below_their_vectors_largest(heads, n):
 def test_value_vectors_near_the_ends_of_the_range(heads, n):
     for size in (1e-36, 1e-30, 1e30):
         Fp8Batch(heads, n, 100, vmul=np.full(100 + n, size), seed=4).check_attend()
+
+
+@pytest.mark.parametrize("heads,n", ROWS)
+@pytest.mark.parametrize("power", [20, 60, -30, -60])
+def test_queries_of_any_size(heads, n, power):
+    """q 2^power times as large and K as much smaller: the same scores."""
+    for c0 in (100, 2000):
+        Fp8Batch(heads, n, c0, qmul=2.0 ** power, kmul=2.0 ** -power, seed=5).check_attend()
