@@ -32,6 +32,7 @@
 #include "attn_common.cuh"
 #include "common.cuh"
 #include "pdl.cuh"
+#include "rows_common.cuh"
 #include "serving.h"
 #include "tc_common.cuh"
 
@@ -125,6 +126,7 @@ __global__ void __launch_bounds__(RW * 32, 1) weights_rows_kernel(const WeightsA
 
   const int g0 = lane >> 2, qd = lane & 3;
   uint32_t qf[NT][D / 16][2];
+  float qback[NT][2];  // FP8: what undoes the power of two of a column's q
   float lse2[NT][2];
   int qpos[NT][2];
   long long cv = gw;
@@ -145,15 +147,14 @@ __global__ void __launch_bounds__(RW * 32, 1) weights_rows_kernel(const WeightsA
         const int cb = t * 8 + g0;
         const bool in = cb < M;
         const bf16* src = a.q + (size_t)(seq0 + (in ? cb / G : 0)) * a.ldq + (cg.kvh * G + (in ? cb % G : 0)) * D;
+        if (FP8) {  // f16, dims 16 ks + 4 qd .. + 3: the order in which K's codes arrive
+          float back;
+          load_q_f16<D, false>(src, in, qd, qf[t], back);
 #pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) {
-          if (FP8) {  // f16, dims 16 ks + 4 qd .. + 3: the order in which K's codes arrive
-            uint2 w = in ? *reinterpret_cast<const uint2*>(src + ks * 16 + 4 * qd) : make_uint2(0u, 0u);
-            const float2 x = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w.x));
-            const float2 y = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w.y));
-            qf[t][ks][0] = pack_f16(x.x, x.y);
-            qf[t][ks][1] = pack_f16(y.x, y.y);
-          } else {
+          for (int e = 0; e < 2; ++e) qback[t][e] = __shfl_sync(0xffffffffu, back, (2 * qd + e) * 4);
+        } else {
+#pragma unroll
+          for (int ks = 0; ks < D / 16; ++ks) {
             qf[t][ks][0] = in ? *reinterpret_cast<const uint32_t*>(src + ks * 16 + 2 * qd) : 0u;
             qf[t][ks][1] = in ? *reinterpret_cast<const uint32_t*>(src + ks * 16 + 8 + 2 * qd) : 0u;
           }
@@ -210,7 +211,8 @@ __global__ void __launch_bounds__(RW * 32, 1) weights_rows_kernel(const WeightsA
       for (int t = 0; t < NT; ++t)
 #pragma unroll
         for (int e = 0; e < 2; ++e)
-          w += attn_visible(key, qpos[t][e], a.window, a.sinks) ? exp2f(fmaf(s[t][2 * half + e], c, -lse2[t][e])) : 0.f;
+          w += attn_visible(key, qpos[t][e], a.window, a.sinks)
+                   ? exp2f(fmaf(s[t][2 * half + e], FP8 ? c * qback[t][e] : c, -lse2[t][e])) : 0.f;
       w += __shfl_xor_sync(0xffffffffu, w, 1);
       w += __shfl_xor_sync(0xffffffffu, w, 2);
       sum[half] = w;

@@ -6,7 +6,7 @@ Tolerances, for each element (row i, head h, dimension e) with its own mass M = 
 the scores' errors as in test_gpu_serving (2 ds + 2^-12 of M, ds the bound of a d-term fp32 sum), P's
 rounding (2^-8 of M in chunks of more than 4 rows; two bf16 parts, 2^-8 of 2^-8, in shorter ones) and
 the output's own rounding to bf16, 2^-8 of its value. Nothing scales with the largest value of the
-cache."""
+cache. Weights: as in test_gpu_serving."""
 import math
 
 import numpy as np
@@ -86,6 +86,28 @@ class Fp8Batch:
             assert bool((err <= tol).all()), (h, float((err / tol).max()))
             assert bool(((lse[h] - ref_lse).abs() <= ds + 2.0 ** -12 + 2.0 ** -21 * ref_lse.abs()).all()), h
 
+    def check_weights(self):
+        import torch
+        from swiftkv_prefill_skipping_gb300 import api
+        zs = [self.logits(h) for h in range(self.n_q)]
+        lse = torch.stack([torch.logsumexp(z, 1) for z, _ in zs]).float()
+        sc = api.attention_weights(self.model, self.q.cuda(), lse.cuda(), [0, self.n], [self.c0], self.kv,
+                                   torch.zeros(self.pages, self.n_kv, 16, device="cuda"), window=self.window,
+                                   sinks=self.sinks, decay=0.0)
+        assert self.model.status() == 0
+        got = sc.cpu().double()[self.pg, :, self.sl]
+        G = self.n_q // self.n_kv
+        for kh in range(self.n_kv):
+            ref, tol = 0, 0
+            for h in range(kh * G, kh * G + G):
+                z, ds = zs[h]
+                l = lse[h].double()[:, None]
+                p = torch.exp(z - l)
+                rel = ds + 2.0 ** -22 * (z.masked_fill(z == -math.inf, 0).abs() + l.abs()) + 2.0 ** -12
+                ref, tol = ref + p.sum(0), tol + (p * rel).sum(0)
+            err = (got[:, kh] - ref).abs()
+            assert bool((err <= tol + 2.0 ** -22 * ref).all()), (kh, float(err.max()))
+
 
 ROWS = [("gqa4", 1), ("gqa4", 3), ("gqa8", 4), ("d64", 2), ("gqa4", 40), ("d64", 70)]
 
@@ -145,3 +167,10 @@ def test_queries_of_any_size(heads, n, power):
     """q 2^power times as large and K as much smaller: the same scores."""
     for c0 in (100, 2000):
         Fp8Batch(heads, n, c0, qmul=2.0 ** power, kmul=2.0 ** -power, seed=5).check_attend()
+
+
+@pytest.mark.parametrize("heads,n", ROWS + [("gqa4", 7)])
+@pytest.mark.parametrize("power", [20, 60, -30, -60])
+def test_weights_of_queries_of_any_size(heads, n, power):
+    for c0 in (100, 2000):
+        Fp8Batch(heads, n, c0, qmul=2.0 ** power, kmul=2.0 ** -power, seed=6).check_weights()
