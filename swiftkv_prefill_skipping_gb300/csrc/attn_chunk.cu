@@ -42,7 +42,8 @@
 //
 // Pages without a visible key are not loaded (zeros instead), and pages of V that the chunk sees in
 // part come from zero-padded copies (launch_v_tail). FP8: K and V are an expansion to bf16 codes;
-// the block's key and value scales travel with V, scores take the key's and P the value's.
+// the block's key and value scales travel with V, scores take the key's and P the value's (times
+// kValueShift).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -524,7 +525,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_chunk_kernel(const __grid_con
       if (ok) ok = wait(ctl->pv_done[t], (uint32_t)((g - 1) & 1));
       if (ok) {
         tc_fence_after();
-        const float inv = 1.f / l;
+        const float inv = (FP8 ? 1.f / kValueShift : 1.f) / l;
         const int head = t ? I.hb : I.h;
         if (a.lse && qrow < I.n) a.lse[(size_t)head * a.ldl + I.seq0 + qrow] = (m + log2f(l)) * kLn2;
         bf16* dst = a.out + (size_t)(I.seq0 + min(qrow, I.n - 1)) * a.ldo + (size_t)head * D;

@@ -71,7 +71,6 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
 // and f16's subnormals cover e4m3's): the even and the odd bytes. Cheaper than two conversions and
 // the moves that line their inputs up, and part of it runs on the multiply pipe.
 constexpr float kCodeScale = 256.f;
-constexpr float kValueShift = 65536.f;
 __device__ __forceinline__ void unpack4(uint32_t r, uint32_t& even, uint32_t& odd) {
   even = ((r * 128u) & 0x3f803f80u) | ((r * 256u) & 0x80008000u);
   odd = ((r >> 1) & 0x3f803f80u) | (r & 0x80008000u);

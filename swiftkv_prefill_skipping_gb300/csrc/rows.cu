@@ -388,7 +388,7 @@ __global__ void kv_expand_seen_kernel(const int* __restrict__ items, const KVPoo
     if (kvsel && !dst.v) break;
     const bool seen = ok && t.seen(pidx * kPageSize + e % kPageSize);
     (kvsel ? dst.v_scale : dst.k_scale)[(size_t)i * rows + e] =
-        seen ? (kvsel ? src.v_scale : src.k_scale)[(size_t)page * rows + e] : 0.f;
+        !seen ? 0.f : kvsel ? kValueShift * src.v_scale[(size_t)page * rows + e] : src.k_scale[(size_t)page * rows + e];
   }
 }
 

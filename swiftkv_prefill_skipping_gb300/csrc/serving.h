@@ -46,6 +46,9 @@ cudaError_t launch_v_tail(const bf16* v_pool, const int* block_table, int max_pa
 // beside them, rows that no row of the sequence's chunk sees as zeros): item i = (sequence, page
 // index) becomes page i, which `dst.block_table`, of the same shape as src's, then names. Dense
 // and per sequence, so that sequences may share pages and the copy is no larger than what is read.
+// Value scales are copied times kValueShift, which whoever multiplies P by them takes back: P times a
+// scale goes to bf16, and value scales near float32's smallest would end up among bf16's subnormals.
+constexpr float kValueShift = 65536.f;
 struct KVPool8 {
   const uint8_t *k, *v;
   const float *k_scale, *v_scale;
