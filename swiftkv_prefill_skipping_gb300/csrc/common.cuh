@@ -45,7 +45,7 @@ struct EpiParams {
   const int* slots;          // [M] page*16 + row, or -1 (invalid page: write skipped)
   const float2* rope_tab;    // [rope_len][d_head/2] (cos, sin) for positions < rope_len
   int rope_len;
-  const float* inv_freq;     // [d_head/2]
+  const unsigned long long* rope_turn;  // [d_head/2] turns per position, in units of 2^-64 of one
   bf16* const* k_pools;      // device array [num_caches] of K pools
   bf16* const* v_pools;      // device array [num_caches] of V pools
   int cache_base;            // EPI_QKV: the layer's cache; EPI_WIDE_KV: first skipped cache
@@ -93,6 +93,9 @@ __host__ __device__ __forceinline__ int pair_half(const EpiParams& p) {
 // Column of the lo member of pair index `u` (0 <= u < ncols/2) in a block-aligned range.
 __device__ __forceinline__ int pair_lo(int u, int half) { return (u / half) * (2 * half) + (u % half); }
 
+// Rotates (a, b) by pos times the pair's frequency. Past the table the angle is a whole number of
+// 2^-64 turns, whose product with pos wraps at a full turn: exact but for the frequency's own rounding
+// (2^-53 of it, 2^-22 radians at position 2^30). A float32 product is off by pos 2^-24 radians.
 __device__ __forceinline__ void rope_rotate(const EpiParams& p, int pos, int i, float& a, float& b) {
   float c, s;
   if (pos < p.rope_len) {
@@ -100,7 +103,8 @@ __device__ __forceinline__ void rope_rotate(const EpiParams& p, int pos, int i, 
     c = cs.x;
     s = cs.y;
   } else {
-    sincosf((float)pos * p.inv_freq[i], &s, &c);
+    const int turn = (int)((p.rope_turn[i] * (unsigned long long)pos) >> 32);  // 2^-32 turns in [-1/2, 1/2)
+    sincospif((float)turn * 4.6566128730773926e-10f, &s, &c);                  // 2^-31: half turns
   }
   float a2 = a * c - b * s;
   float b2 = b * c + a * s;

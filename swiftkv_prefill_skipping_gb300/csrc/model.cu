@@ -419,7 +419,7 @@ EpiParams epi_base(Ctx& x, int kind, int M, int N) {
   p.n_kv = x.m->cfg.n_kv;
   p.rope_tab = x.m->rope_tab;
   p.rope_len = kRopeLen;
-  p.inv_freq = x.m->inv_freq;
+  p.rope_turn = x.m->rope_turn;
   p.k_pools = x.k_dev;
   p.v_pools = x.v_dev;
   return p;
@@ -808,13 +808,14 @@ int swiftkv_model_create(const swiftkv_model_config* cfg, int l, int g, swiftkv_
       (r = dalloc_t(m, &m->chain_count, 1)))
     return bail(r);
   const int half = cfg->d_head / 2;
-  if ((r = dalloc_t(m, &m->inv_freq, half)) || (r = dalloc_t(m, &m->rope_tab, (size_t)kRopeLen * half)))
+  if ((r = dalloc_t(m, &m->rope_turn, half)) || (r = dalloc_t(m, &m->rope_tab, (size_t)kRopeLen * half)))
     return bail(r);
-  std::vector<float> inv(half);
+  std::vector<unsigned long long> turn(half);
   std::vector<double> invd(half);
   for (int i = 0; i < half; ++i) {
     invd[i] = std::pow((double)cfg->rope_theta, -2.0 * i / cfg->d_head);
-    inv[i] = (float)invd[i];
+    const double turns = invd[i] / 6.283185307179586476925;
+    turn[i] = (unsigned long long)((turns - std::floor(turns)) * 18446744073709551616.0);
   }
   std::vector<float2> tab((size_t)kRopeLen * half);
   for (int p = 0; p < kRopeLen; ++p)
@@ -822,7 +823,7 @@ int swiftkv_model_create(const swiftkv_model_config* cfg, int l, int g, swiftkv_
       double a = p * invd[i];
       tab[(size_t)p * half + i] = make_float2((float)std::cos(a), (float)std::sin(a));
     }
-  if (cudaMemcpy(m->inv_freq, inv.data(), half * 4, cudaMemcpyHostToDevice) != cudaSuccess ||
+  if (cudaMemcpy(m->rope_turn, turn.data(), half * 8, cudaMemcpyHostToDevice) != cudaSuccess ||
       cudaMemcpy(m->rope_tab, tab.data(), tab.size() * sizeof(float2), cudaMemcpyHostToDevice) != cudaSuccess ||
       cudaMemset(m->status, 0, 4) != cudaSuccess || cudaMemset(m->chain_count, 0, 4) != cudaSuccess)
     return bail(fail(SWIFTKV_ECUDA, "rope table upload"));

@@ -52,7 +52,7 @@ struct swiftkv_model {
   skv::bf16* w_wide = nullptr;
   float* b_wide = nullptr;
   float2* rope_tab = nullptr;
-  float* inv_freq = nullptr;
+  unsigned long long* rope_turn = nullptr;
   int* status = nullptr;
   std::vector<void*> allocs;
   size_t weight_bytes = 0;
