@@ -76,6 +76,7 @@ class Model:
         h = C.c_void_p()
         B.check(B.lib().swiftkv_model_create(C.byref(self._cfg), l, g, C.byref(h)))
         self.handle = h
+        self.device = torch.device("cuda", torch.cuda.current_device())
 
     def load_layer(self, j: int, w: dict, stream=None) -> None:
         lw = B.LayerWeights(*[_ptr(w.get(k)) for k in (
@@ -106,15 +107,15 @@ class Model:
 
     def set_score_pools(self, scores: Optional[torch.Tensor], decay: float = 1.0) -> None:
         """Later calls add every layer's attention weights to scores (float32 [num_caches, num_pages,
-        n_kv, 16], e.g. KVCache.new_scores(); kept alive here); None turns that off. Sequences of a
-        call must not share pages while it is on."""
+        n_kv, 16] on the model's device, e.g. KVCache.new_scores(); kept alive here); None turns that
+        off. Sequences of a call must not share pages while it is on."""
         if scores is None:
             B.check(B.lib().swiftkv_set_score_pools(self.handle, None, 0, decay))
         else:
             s = self.shape
             if scores.dim() != 4 or scores.shape[0] != self.num_caches or tuple(scores.shape[2:]) != (s.n_kv, 16):
                 raise ValueError(f"scores: float32 [{self.num_caches}, pages, {s.n_kv}, 16]")
-            base = _flat(scores, torch.float32, tuple(scores.shape), scores.device, "scores")
+            base = _flat(scores, torch.float32, tuple(scores.shape), self.device, "scores")
             step = scores.stride(0) * 4
             ptrs = (C.c_void_p * self.num_caches)(*[base + c * step for c in range(self.num_caches)])
             B.check(B.lib().swiftkv_set_score_pools(self.handle, ptrs, scores.shape[1], decay))

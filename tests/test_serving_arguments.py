@@ -1,0 +1,24 @@
+"""Checks of the operators' arguments that need no GPU: nothing here reaches a kernel."""
+import ctypes as C
+
+import pytest
+import torch
+
+from swiftkv_prefill_skipping_gb300 import api
+
+
+def model_on(device="cuda:0", n_kv=2, d_h=64, caches=2):
+    """A Model without its handle: every call that gets past the checks fails on it."""
+    m = object.__new__(api.Model)
+    m.shape = api.Shape(L=caches, d=128, n_q=4, n_kv=n_kv, d_h=d_h, ffn=64, vocab=128, rope_theta=1e4)
+    m.l, m.g, m.num_caches, m.handle = caches, 1, caches, C.c_void_p()
+    m.device = torch.device(device)
+    return m
+
+
+@pytest.mark.parametrize("device", ["cuda:0", "cuda:1"])
+def test_score_pools_have_to_be_on_the_models_device(device):
+    m = model_on(device)
+    with pytest.raises(ValueError, match=f"on {device}"):
+        m.set_score_pools(torch.zeros(2, 5, 2, 16))
+    assert getattr(m, "_scores", None) is None
