@@ -156,6 +156,7 @@ class KVCache:
         elem = torch.bfloat16 if dtype == "bf16" else torch.uint8
         self.k = torch.zeros(shape, dtype=elem, device=dev)
         self.v = torch.zeros(shape, dtype=elem, device=dev)
+        self.device = self.k.device
         self.k_scale = self.v_scale = None
         if dtype == "fp8":
             self.k_scale = torch.zeros(shape[:-1], dtype=torch.float32, device=dev)
@@ -276,7 +277,7 @@ def decode_step(model: Model, tokens: torch.Tensor, seq_lens: Sequence[int], kv:
     """One decode token per sequence; returns (logits [B, V], next token ids [B])."""
     sl = np.ascontiguousarray(seq_lens, dtype=np.int32)
     Bsz = len(sl)
-    dev = kv.k.device
+    dev = kv.device
     logits = torch.empty((Bsz, model.shape.vocab), dtype=torch.float32, device=dev)
     nxt = torch.empty((Bsz,), dtype=torch.int32, device=dev)
     tokens = tokens.to(torch.int32).contiguous()
@@ -288,6 +289,8 @@ def decode_step(model: Model, tokens: torch.Tensor, seq_lens: Sequence[int], kv:
 def _fits(model: Model, kv: KVCache) -> None:
     if kv.heads != (model.shape.n_kv, model.shape.d_h):
         raise ValueError(f"a cache of (n_kv, d_h) {kv.heads} for a model of {(model.shape.n_kv, model.shape.d_h)}")
+    if kv.device != model.device:
+        raise ValueError(f"a cache on {kv.device} for a model on {model.device}")
 
 
 def _chunks(cu_seqlens, ctx_lens, kv: KVCache, model: Model):
@@ -330,7 +333,7 @@ def attend(model: Model, q: torch.Tensor, cu_seqlens: Sequence[int], ctx_lens: O
     `sinks`. Returns out [T, n_q, d_h] bf16; lse (float32 [n_q, T]), if given, receives each row's
     log-sum-exp, which attention_weights takes."""
     cu, ctx, P, T = _chunks(cu_seqlens, ctx_lens, kv, model)
-    dev = kv.k.device
+    dev = kv.device
     ldq = _rows_of(q, T, model, dev, "q")
     if out is None:
         out = torch.empty((T, model.shape.n_q, model.shape.d_h), dtype=torch.bfloat16, device=dev)
@@ -349,7 +352,7 @@ def attention_weights(model: Model, q: torch.Tensor, lse: torch.Tensor, cu_seqle
     cache): scores = decay * scores + weight for every key some token sees, the others unchanged.
     q and lse are those of the attend call before. Returns scores."""
     cu, ctx, P, T = _chunks(cu_seqlens, ctx_lens, kv, model)
-    dev, s = kv.k.device, model.shape
+    dev, s = kv.device, model.shape
     ldq = _rows_of(q, T, model, dev, "q")
     lp = _flat(lse, torch.float32, (s.n_q, T), dev, "lse")
     sp = _flat(scores, torch.float32, (kv.num_pages, s.n_kv, 16), dev, "scores")
@@ -370,7 +373,7 @@ def evict(model: Model, kv: KVCache, scores: torch.Tensor, seq_lens: Sequence[in
     min(seq_lens[s], keep) keys."""
     _fits(model, kv)
     sl = np.ascontiguousarray(seq_lens, dtype=np.int32)
-    P, dev, s = sl.shape[0], kv.k.device, model.shape
+    P, dev, s = sl.shape[0], kv.device, model.shape
     if P > kv.num_rows:
         raise ValueError(f"{P} sequences, but the block table has {kv.num_rows} rows")
     if keep < 1 or (cache is not None and not 0 <= cache < kv.num_caches):

@@ -1,6 +1,7 @@
 """Checks of the operators' arguments that need no GPU: nothing here reaches a kernel."""
 import ctypes as C
 
+import numpy as np
 import pytest
 import torch
 
@@ -22,3 +23,14 @@ def test_score_pools_have_to_be_on_the_models_device(device):
     with pytest.raises(ValueError, match=f"on {device}"):
         m.set_score_pools(torch.zeros(2, 5, 2, 16))
     assert getattr(m, "_scores", None) is None
+
+
+def test_operators_refuse_a_cache_on_another_device():
+    m = model_on()
+    kv = api.KVCache(m, 4, np.zeros((1, 2), np.int32), device=torch.device("cpu"))
+    q, lse = torch.zeros(1, 4, 64, dtype=torch.bfloat16), torch.zeros(4, 1)
+    for call in (lambda: api.attend(m, q, [0, 1], None, kv),
+                 lambda: api.attention_weights(m, q, lse, [0, 1], None, kv, kv.new_scores()[0]),
+                 lambda: api.evict(m, kv, kv.new_scores(), [5], 2)):
+        with pytest.raises(ValueError, match="model on cuda:0"):
+            call()
