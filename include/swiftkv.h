@@ -267,6 +267,7 @@ int swiftkv_attention_weights(swiftkv_model* m, int cache, const void* q, int ld
  *              be pages of any sequence's first seq_lens[s] keys; source pages are only read then,
  *              so they may be shared (a common prefix). In place, no two sequences may share pages.
  *   kept       device int32 [caches][num_seqs][n_kv][keep]: former indices, ascending, -1 behind them
+ * keep and seq_lens go up to 2^30, else SWIFTKV_EUNSUPPORTED.
  * A block-table entry outside the pools among those a sequence needs sets SWIFTKV_STATUS_BAD_PAGE,
  * leaves that sequence's rows as they are and its `kept` at -1. */
 int swiftkv_evict(swiftkv_model* m, int cache, const swiftkv_kv_pages* kv, float* const* scores,

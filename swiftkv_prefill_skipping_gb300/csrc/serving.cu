@@ -475,6 +475,9 @@ int check_call(const swiftkv_model* m, int cache, int P, const swiftkv_kv_pages*
   return SWIFTKV_OK;
 }
 
+// Keys of a sequence, and of its kept list: the kernels step through them in ints, past the end.
+constexpr int kMaxKeys = 1 << 30;
+
 int check_rows(const swiftkv_model* m, const void* p, int ld, const char* name) {
   if (!p) return fail(SWIFTKV_EINVAL, "null %s", name);
   if (ld < m->Nq || ld % 8 || (reinterpret_cast<uintptr_t>(p) & 15))
@@ -554,12 +557,14 @@ int swiftkv_evict(swiftkv_model* m, int cache, const swiftkv_kv_pages* kv, float
         return fail(SWIFTKV_EINVAL, "null or misaligned score pool for cache %d", c);
     if (keep < 1 || sinks < 0 || recent < 0 || (long long)sinks + recent > keep)
       return fail(SWIFTKV_EINVAL, "need keep >= 1, sinks >= 0, recent >= 0 and sinks + recent <= keep");
+    if (keep > kMaxKeys) return fail(SWIFTKV_EUNSUPPORTED, "keep above 2^30");
     const int dst_width = dst_block_table ? dst_max_pages : kv->max_pages_per_seq;
     if (dst_block_table && dst_max_pages < 1) return fail(SWIFTKV_EINVAL, "empty destination block table");
     int longest = 0;
     for (int i = 0; i < P; ++i) {
       const long long n = seq_lens[i];
       if (n < 0) return fail(SWIFTKV_EINVAL_SEQLENS, "seq_lens[%d] < 0", i);
+      if (n > kMaxKeys) return fail(SWIFTKV_EUNSUPPORTED, "seq_lens[%d] above 2^30", i);
       if (n > (long long)kv->max_pages_per_seq * kPageSize)
         return fail(SWIFTKV_ENO_PAGES, "sequence %d needs %lld pages, block table holds %d", i, (n + 15) / 16,
                     kv->max_pages_per_seq);

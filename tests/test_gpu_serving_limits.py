@@ -1,0 +1,26 @@
+"""Limits and ownership of the operators over the paged cache: what is refused before a launch, what
+memory they hold, which stream their outputs belong to."""
+import ctypes as C
+
+import numpy as np
+import pytest
+
+from swiftkv_prefill_skipping_gb300 import binding as B
+from test_gpu_serving import EvictCase
+
+pytestmark = pytest.mark.gpu
+
+
+def test_evict_refuses_lists_past_what_its_kernels_count():
+    """Refused on the host: nothing is launched, so the pointers are never used."""
+    c = EvictCase("d64", [40], 8, 0, 0)
+    lib, fake = B.lib(), 1 << 20
+    scores = (C.c_void_p * 2)(c.scores[0].data_ptr(), c.scores[1].data_ptr())
+    lens = np.array([40], np.int32)
+    for keep in ((1 << 30) + 1, 2 ** 31 - 1):
+        assert lib.swiftkv_evict(c.model.handle, -1, c.kv.pages_ref, scores, B.host(lens), 1, keep, 0, 0, None, 0, fake, None) == -9
+    wide = B.KVPages.from_buffer_copy(c.kv.pages)
+    wide.max_pages_per_seq = 1 << 27
+    lens = np.array([(1 << 30) + 1], np.int32)
+    assert lib.swiftkv_evict(c.model.handle, -1, C.byref(wide), scores, B.host(lens), 1, 8, 0, 0, None, 0, fake, None) == -9
+    assert b"2^30" in lib.swiftkv_last_error()
