@@ -108,6 +108,7 @@ typedef struct {
  * belong to the full layers, cache l + i to the i-th group of skipped layers.
  * Each cache has a K pool and a V pool of [num_pages][n_kv][page_size][d_head]
  * elements: one (page, head) block of page_size * d_head elements is contiguous.
+ * Pools start on 16 bytes.
  * Token at position p of sequence s lives in page block_table[s][p / page_size],
  * row p % page_size.
  * kv_dtype 0: bf16 elements. kv_dtype 1: per-token FP8 ("SwiftKV" summary, AcrossKV,

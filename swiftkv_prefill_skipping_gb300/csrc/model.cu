@@ -50,6 +50,12 @@ int check_kv(const swiftkv_model* m, const swiftkv_kv_pages* kv) {
     if (m->cfg.n_q / m->cfg.n_kv > 8)
       return fail(SWIFTKV_EUNSUPPORTED, "fp8 cache needs at most 8 query heads per KV head");
   }
+  if (reinterpret_cast<uintptr_t>(kv->block_table) & 3) return fail(SWIFTKV_EINVAL, "misaligned block table");
+  for (int c = 0; c < m->C; ++c) {  // the kernels copy 16 bytes at a time
+    uintptr_t bits = reinterpret_cast<uintptr_t>(kv->k_pool[c]) | reinterpret_cast<uintptr_t>(kv->v_pool[c]);
+    if (kv->kv_dtype == 1) bits |= reinterpret_cast<uintptr_t>(kv->k_scale[c]) | reinterpret_cast<uintptr_t>(kv->v_scale[c]);
+    if (bits & 15) return fail(SWIFTKV_EINVAL, "pools of cache %d are not 16-byte aligned", c);
+  }
   return SWIFTKV_OK;
 }
 

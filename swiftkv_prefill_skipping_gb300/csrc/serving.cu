@@ -467,11 +467,6 @@ int check_call(const swiftkv_model* m, int cache, int P, const swiftkv_kv_pages*
   if (P < 0 || P > 32767) return fail(SWIFTKV_EINVAL, "num_seqs %d outside [0, 32767]", P);
   RET(check_kv(m, kv));
   if (cache < 0 || cache >= m->C) return fail(SWIFTKV_EINVAL, "cache %d outside [0, %d)", cache, m->C);
-  for (int c = 0; c < m->C; ++c) {  // the kernels copy 16 bytes at a time
-    uintptr_t bits = reinterpret_cast<uintptr_t>(kv->k_pool[c]) | reinterpret_cast<uintptr_t>(kv->v_pool[c]);
-    if (kv->kv_dtype == 1) bits |= reinterpret_cast<uintptr_t>(kv->k_scale[c]) | reinterpret_cast<uintptr_t>(kv->v_scale[c]);
-    if (bits & 15) return fail(SWIFTKV_EINVAL, "pools of cache %d are not 16-byte aligned", c);
-  }
   return SWIFTKV_OK;
 }
 

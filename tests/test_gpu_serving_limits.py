@@ -6,6 +6,7 @@ import numpy as np
 import pytest
 
 from swiftkv_prefill_skipping_gb300 import binding as B
+from test_gpu_bounded_cache import setup
 from test_gpu_serving import EvictCase
 
 pytestmark = pytest.mark.gpu
@@ -24,3 +25,29 @@ def test_evict_refuses_lists_past_what_its_kernels_count():
     lens = np.array([(1 << 30) + 1], np.int32)
     assert lib.swiftkv_evict(c.model.handle, -1, C.byref(wide), scores, B.host(lens), 1, 8, 0, 0, None, 0, fake, None) == -9
     assert b"2^30" in lib.swiftkv_last_error()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp8"])
+@pytest.mark.parametrize("mode", ["plain", "window", "scores"])
+def test_the_models_calls_refuse_pools_off_16_bytes(mode, dtype):
+    """Refused on the host, as by the operators: the kernels would read such a pool 16 bytes at a time."""
+    import torch
+    from swiftkv_prefill_skipping_gb300 import api
+    m, kv, batch, *_ = setup("tiny", [20], dtype=dtype)
+    if mode == "window":
+        m.set_attention_window(8, 1)
+    if mode == "scores":
+        m.set_score_pools(kv.new_scores())
+    tok = torch.as_tensor(batch.tokens, device="cuda")
+    for name, step in (("_kp", 2), ("_vp", 8)) + ((("_ks", 4), ("_vs", 8)) if dtype == "fp8" else ()):
+        pools = getattr(kv, name)
+        for c in range(m.num_caches):
+            was, pools[c] = pools[c], pools[c] + step
+            for call in (lambda: api.prefill(m, tok, [0, 20], kv), lambda: api.forward(m, tok, [0, 20], [0], kv),
+                         lambda: api.forward(m, tok, [0, 20], [0], kv, pos_offsets=[3]),
+                         lambda: api.decode_step(m, tok[:1], [20], kv)):
+                with pytest.raises(B.SwiftKVError, match="16-byte"):
+                    call()
+            pools[c] = was
+    assert m.status() == 0
+    m.free()
