@@ -885,8 +885,9 @@ extern "C" int swiftkv_sample(const float* logits, int rows, int vocab, long lon
   if (rows == 0) return SWIFTKV_OK;
   if (!logits || !s || !u || !tokens) return set_error(SWIFTKV_EINVAL, "null logits / settings / u / tokens");
   if (ld < vocab) return set_error(SWIFTKV_EINVAL, "row stride smaller than vocab");
-  if ((reinterpret_cast<uintptr_t>(logits) & 3) || (reinterpret_cast<uintptr_t>(u) & 3))
-    return set_error(SWIFTKV_EINVAL, "misaligned logits / u");
+  const void* const arrays[] = {logits, u, tokens, s->temperature, s->top_k, s->top_p, s->min_p};
+  for (const void* a : arrays)
+    if (reinterpret_cast<uintptr_t>(a) & 3) return set_error(SWIFTKV_EINVAL, "misaligned logits / u / tokens / settings");
   if (vocab > kMaxVocab) return set_error(SWIFTKV_EUNSUPPORTED, "vocab above 360448");
   if (rows > (1 << 27)) return set_error(SWIFTKV_EUNSUPPORTED, "more than 2^27 rows");
   SampleParams p;

@@ -546,6 +546,8 @@ int swiftkv_evict(swiftkv_model* m, int cache, const swiftkv_kv_pages* kv, float
     if (P == 0) return SWIFTKV_OK;
     if (cache < -1) return fail(SWIFTKV_EINVAL, "cache %d outside [-1, %d)", cache, m->C);
     if (!scores || !seq_lens || !kept) return fail(SWIFTKV_EINVAL, "null scores / seq_lens / kept");
+    if ((reinterpret_cast<uintptr_t>(kept) | reinterpret_cast<uintptr_t>(dst_block_table)) & 3)
+      return fail(SWIFTKV_EINVAL, "misaligned kept or destination block table");
     const int first = cache < 0 ? 0 : cache, C = cache < 0 ? m->C : 1;
     for (int c = first; c < first + C; ++c)
       if (!scores[c] || (reinterpret_cast<uintptr_t>(scores[c]) & 15))

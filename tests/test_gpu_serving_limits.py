@@ -51,3 +51,14 @@ def test_the_models_calls_refuse_pools_off_16_bytes(mode, dtype):
             pools[c] = was
     assert m.status() == 0
     m.free()
+
+
+def test_evict_refuses_misaligned_lists():
+    """Refused on the host: nothing is launched."""
+    c = EvictCase("d64", [40], 8, 0, 0)
+    scores = (C.c_void_p * 2)(c.scores[0].data_ptr(), c.scores[1].data_ptr())
+    lens = np.array([40], np.int32)
+    for kept, dst in ((4098, None), (4096, 4097), (4096, 4098)):
+        assert B.lib().swiftkv_evict(c.model.handle, -1, c.kv.pages_ref, scores, B.host(lens), 1, 8, 0, 0, dst,
+                                     1 if dst else 0, kept, None) == -1
+        assert b"misaligned" in B.lib().swiftkv_last_error()

@@ -6,6 +6,7 @@ import pytest
 import torch
 
 from swiftkv_prefill_skipping_gb300 import api
+from swiftkv_prefill_skipping_gb300 import binding as B
 
 
 def model_on(device="cuda:0", n_kv=2, d_h=64, caches=2):
@@ -34,3 +35,15 @@ def test_operators_refuse_a_cache_on_another_device():
                  lambda: api.evict(m, kv, kv.new_scores(), [5], 2)):
         with pytest.raises(ValueError, match="model on cuda:0"):
             call()
+
+
+@pytest.mark.parametrize("which", ["tokens", "u", "temperature", "top_k", "top_p", "min_p"])
+def test_sample_refuses_misaligned_arrays(which):
+    s, at = B.Sampling(), dict(tokens=256, u=256)  # addresses that are never used: refused first
+    if which in at:
+        at[which] += 2
+    else:
+        setattr(s, which, 258)
+    vocab = 360449  # refused later on, so that no kernel runs where the check is missing
+    assert B.lib().swiftkv_sample(256, 1, vocab, vocab, C.byref(s), at["u"], at["tokens"], None) == -1
+    assert b"misaligned" in B.lib().swiftkv_last_error()
