@@ -32,6 +32,15 @@ def _stream_of(dev: torch.device, stream) -> int:
     return (stream if stream is not None else torch.cuda.current_stream(dev)).cuda_stream
 
 
+def _empty(shape, dtype, dev: torch.device, stream) -> torch.Tensor:
+    """An output that work on `stream` (None: the current one) will write. Its memory is that stream's:
+    a block of the current stream may still be in use by what was enqueued there before."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
 def _ptr(a) -> Optional[int]:
     if a is None:
         return None
@@ -336,7 +345,7 @@ def attend(model: Model, q: torch.Tensor, cu_seqlens: Sequence[int], ctx_lens: O
     dev = kv.device
     ldq = _rows_of(q, T, model, dev, "q")
     if out is None:
-        out = torch.empty((T, model.shape.n_q, model.shape.d_h), dtype=torch.bfloat16, device=dev)
+        out = _empty((T, model.shape.n_q, model.shape.d_h), torch.bfloat16, dev, stream)
     ldo = _rows_of(out, T, model, dev, "out")
     lp = None if lse is None else _flat(lse, torch.float32, (model.shape.n_q, T), dev, "lse")
     B.check(B.lib().swiftkv_attend(model.handle, cache, q.data_ptr(), ldq, B.host(cu), B.host(ctx), P, kv.pages_ref,
@@ -389,7 +398,7 @@ def evict(model: Model, kv: KVCache, scores: torch.Tensor, seq_lens: Sequence[in
         dst = _flat(dst_block_table, torch.int32, (rows, width), dev, "dst_block_table")
     shape = (n, P, s.n_kv, keep)
     if kept is None:
-        kept = torch.empty(shape, dtype=torch.int32, device=dev)
+        kept = _empty(shape, torch.int32, dev, stream)
         kp = kept.data_ptr()
     else:
         kp = _flat(kept, torch.int32, shape, dev, "kept")
@@ -432,7 +441,7 @@ def sample(logits: torch.Tensor, u: torch.Tensor, temperature=1.0, top_k=0, top_
     else:
         s.min_p_all = min_p
     if out is None:
-        out = torch.empty(vec, dtype=torch.int32, device=dev)
+        out = _empty(vec, torch.int32, dev, stream)
     args = (logits.data_ptr(), P, V, ld, s, _flat(u, f32, vec, dev, "u"), _flat(out, torch.int32, vec, dev, "out"),
             _stream_of(dev, stream))
     if torch.cuda.current_device() == dev.index:

@@ -7,7 +7,7 @@ import pytest
 
 from swiftkv_prefill_skipping_gb300 import binding as B
 from test_gpu_bounded_cache import setup
-from test_gpu_serving import EvictCase
+from test_gpu_serving import Case, EvictCase
 
 pytestmark = pytest.mark.gpu
 
@@ -62,3 +62,37 @@ def test_evict_refuses_misaligned_lists():
         assert B.lib().swiftkv_evict(c.model.handle, -1, c.kv.pages_ref, scores, B.host(lens), 1, 8, 0, 0, dst,
                                      1 if dst else 0, kept, None) == -1
         assert b"misaligned" in B.lib().swiftkv_last_error()
+
+
+def test_outputs_belong_to_the_stream_they_are_written_on():
+    """A call on another stream takes no memory that the current stream's work still writes: a block that
+    was freed while a fill was waiting on the current stream is not handed out as the output."""
+    import torch
+    from swiftkv_prefill_skipping_gb300 import api
+    c = Case("gqa4", [140, 1], [20, 70], seed=5)
+    e = EvictCase("gqa4", [200, 40], 32, 2, 8, seed=4)
+    q, dst, x, u = c.q.cuda(), e.dst.cuda(), torch.randn(300, 1000, device="cuda"), torch.rand(300, device="cuda")
+    scores = e.scores.clone()
+    side = torch.cuda.Stream()
+
+    def attend(**kw):
+        return api.attend(c.model, q, c.cu, c.ctx, c.kv, cache=1, **kw)
+
+    def evict(**kw):  # to other pages: the source and its scores stay
+        return api.evict(e.model, e.kv, scores, e.lens, 32, sinks=2, recent=8, dst_block_table=dst, **kw)
+
+    def sample(**kw):
+        return api.sample(x, u, top_p=0.9, **kw)
+
+    for call in (attend, evict, sample):
+        ref = call()
+        torch.cuda.synchronize()
+        block = torch.empty_like(ref)
+        was = block.data_ptr()
+        torch.cuda._sleep(100_000_000)
+        block.fill_(7)
+        del block
+        got = call(stream=side)
+        assert got.data_ptr() != was
+        torch.cuda.synchronize()
+        assert torch.equal(got, ref)
