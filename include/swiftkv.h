@@ -217,8 +217,10 @@ int swiftkv_decode_step(swiftkv_model* m, const int32_t* tokens, const int32_t* 
  * loaded. As every call on a model, calls that share one must be ordered on the GPU (one stream,
  * or events between streams), graph replays among them. They can be captured into a CUDA graph:
  * host arrays are read at the call and stay fixed in the graph, and a call whose workspace would
- * have to grow is refused during a capture (SWIFTKV_ESTATE) - make one like it before. The model's
- * device need not be the current one. num_seqs == 0 and chunks of no tokens are allowed.
+ * have to grow is refused during a capture (SWIFTKV_ESTATE) - make one like it before. A workspace that
+ * a captured graph uses stays when a later call outgrows it, and counts in swiftkv_memory, until the
+ * model is freed. The model's device need not be the current one. num_seqs == 0 and chunks of no tokens
+ * are allowed.
  *
  * Visibility: chunk row i of sequence s sits at position p = ctx_lens[s] + i and sees the cached
  * keys j <= p if window == 0; else those with j > p - window (the last `window` of them, its own
@@ -336,7 +338,8 @@ int swiftkv_sample(const float* logits, int rows, int vocab, long long ld, const
  * Returns the swiftkv_status_bits that are set, or a negative swiftkv_error. */
 int swiftkv_status(swiftkv_model* m, int clear);
 
-/* Bytes of device memory the model holds for weights and for workspace. */
+/* Bytes of device memory the model holds for weights and for workspace, blocks kept for captured graphs
+ * included. */
 int swiftkv_memory(const swiftkv_model* m, size_t* weight_bytes, size_t* workspace_bytes);
 
 /* Kernel family for GEMMs with more than 64 rows: 0 = tcgen05 on CTA pairs (cta_group::2,

@@ -763,6 +763,7 @@ void swiftkv_free(swiftkv_model* m) {
   if (!m) return;
   for (void* p : m->allocs) cudaFree(p);
   if (m->ws) cudaFree(m->ws);
+  if (m->ops_ws) cudaFree(m->ops_ws);
   for (cudaEvent_t e : m->ev_pool) cudaEventDestroy(e);
   delete m;
 }
@@ -927,7 +928,7 @@ int swiftkv_load_weights(const swiftkv_model_config* cfg, const swiftkv_host_wei
 int swiftkv_memory(const swiftkv_model* m, size_t* weight_bytes, size_t* workspace_bytes) {
   if (!m) return fail(SWIFTKV_EINVAL, "null model");
   if (weight_bytes) *weight_bytes = m->weight_bytes;
-  if (workspace_bytes) *workspace_bytes = m->ws_bytes + m->ops_bytes;
+  if (workspace_bytes) *workspace_bytes = m->ws_bytes + m->ops_bytes + m->ops_kept_bytes;
   return SWIFTKV_OK;
 }
 

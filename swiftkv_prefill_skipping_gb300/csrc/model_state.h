@@ -58,8 +58,10 @@ struct swiftkv_model {
   size_t weight_bytes = 0;
   char* ws = nullptr;
   size_t ws_bytes = 0;
-  char* ops_ws = nullptr;  // workspace of the operators of serving.h; one that was outgrown stays in
-  size_t ops_bytes = 0;    // `allocs`, since a captured graph may still use it
+  char* ops_ws = nullptr;  // workspace of the operators of serving.h
+  size_t ops_bytes = 0;
+  bool ops_captured = false;   // a captured graph uses ops_ws: when outgrown it stays, in `allocs`
+  size_t ops_kept_bytes = 0;   // of the blocks that stayed so
   bool globals_loaded = false;
   int gemm_impl = 0;  // 0 tcgen05 CTA pairs, 1 mma.sync tiles, 2 tcgen05 single CTA (GEMMs with > 64 rows)
   int attn_impl = 0;  // 0 tcgen05 when d_head == 128, 1 mma.sync

@@ -167,14 +167,23 @@ int expand(swiftkv_model* m, const swiftkv_kv_pages* kv, int c, const Batch& b, 
   return SWIFTKV_OK;
 }
 
-}  // namespace
-
-int reserve(swiftkv_model* m, size_t bytes, cudaStream_t stream, Arena* arena) {
+// The model's operator workspace holds `bytes`. One that a captured graph uses stays when it is outgrown.
+int hold(swiftkv_model* m, size_t bytes, cudaStream_t stream) {
+  cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+  CK(cudaStreamIsCapturing(stream, &cap));
+  const bool capturing = cap != cudaStreamCaptureStatusNone;
   if (bytes > m->ops_bytes) {
-    cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
-    CK(cudaStreamIsCapturing(stream, &cap));
-    if (cap != cudaStreamCaptureStatusNone)
+    if (capturing)
       return fail(SWIFTKV_ESTATE, "the workspace must grow to %zu bytes: make one such call before the capture", bytes);
+    if (m->ops_ws && m->ops_captured) {
+      m->allocs.push_back(m->ops_ws);
+      m->ops_kept_bytes += m->ops_bytes;
+    } else if (m->ops_ws) {
+      CK(cudaFree(m->ops_ws));  // synchronises the device: no enqueued work still uses it
+    }
+    m->ops_ws = nullptr;
+    m->ops_bytes = 0;
+    m->ops_captured = false;
     const size_t want = std::max(bytes + bytes / 4, (size_t)1 << 20);
     void* p = nullptr;
     const cudaError_t e = cudaMalloc(&p, want);
@@ -182,10 +191,17 @@ int reserve(swiftkv_model* m, size_t bytes, cudaStream_t stream, Arena* arena) {
       cudaGetLastError();
       return fail(SWIFTKV_EOOM, "workspace cudaMalloc(%zu): %s", want, cudaGetErrorString(e));
     }
-    m->allocs.push_back(p);
     m->ops_ws = static_cast<char*>(p);
     m->ops_bytes = want;
   }
+  m->ops_captured |= capturing;
+  return SWIFTKV_OK;
+}
+
+}  // namespace
+
+int reserve(swiftkv_model* m, size_t bytes, cudaStream_t stream, Arena* arena) {
+  if (bytes > 0) RET(guarded([&] { return hold(m, bytes, stream); }));
   arena->base = m->ops_ws;
   arena->used = 0;
   return SWIFTKV_OK;

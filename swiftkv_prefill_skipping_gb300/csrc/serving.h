@@ -84,7 +84,8 @@ struct Arena {
   }
 };
 // Gives the arena `bytes` of the model's operator workspace, growing it where needed: refused
-// (SWIFTKV_ESTATE) while `stream` is being captured, since that would need an allocation.
+// (SWIFTKV_ESTATE) while `stream` is being captured, since that would need an allocation. One call of
+// the library makes at most one reservation: a larger one later on would free what it uses.
 int reserve(swiftkv_model* m, size_t bytes, cudaStream_t stream, Arena* arena);
 
 // A ragged batch: chunk s is rows [cu[s], cu[s + 1]) at positions ctx[s] .. of sequence s.

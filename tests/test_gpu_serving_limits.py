@@ -7,7 +7,7 @@ import pytest
 
 from swiftkv_prefill_skipping_gb300 import binding as B
 from test_gpu_bounded_cache import setup
-from test_gpu_serving import Case, EvictCase
+from test_gpu_serving import HEADS, Case, EvictCase, model_of
 
 pytestmark = pytest.mark.gpu
 
@@ -96,3 +96,53 @@ def test_outputs_belong_to_the_stream_they_are_written_on():
         assert got.data_ptr() != was
         torch.cuda.synchronize()
         assert torch.equal(got, ref)
+
+
+@pytest.mark.parametrize("captured", [False, True])
+def test_workspace_that_was_outgrown(captured):
+    """Over an FP8 cache a chunk's workspace holds a bf16 copy of its keys. After growing step by step
+    swiftkv_memory gives what the device has lost, and without a graph that is the last block alone."""
+    import torch
+    from swiftkv_prefill_skipping_gb300 import api
+    n_q, n_kv, d = HEADS["gqa8"]
+    steps, new = (2000, 16000, 32000, 64000), 8
+    pages = steps[-1] // 16 + 1
+
+    def make():
+        m = model_of("gqa8", 1)
+        return m, api.KVCache(m, pages, np.arange(pages, dtype=np.int32)[None], dtype="fp8")
+
+    q = torch.randn(new, n_q, d, device="cuda").bfloat16()
+    out = torch.empty_like(q)
+
+    def call(m, kv, keys):
+        api.attend(m, q, [0, new], [keys - new], kv, out=out)
+
+    other = make()
+    call(*other, steps[-1])
+    m, kv = make()
+    call(m, kv, 500)
+    torch.cuda.synchronize()
+    held, free = m.memory()[1], torch.cuda.mem_get_info()[0]
+    graphs = []
+    for keys in steps:
+        call(m, kv, keys)
+        if captured:
+            graphs.append(torch.cuda.CUDAGraph())
+            with torch.cuda.graph(graphs[-1]):
+                call(m, kv, keys)
+        torch.cuda.synchronize()
+        lost = free - torch.cuda.mem_get_info()[0]
+        assert abs(m.memory()[1] - held - lost) <= (8 << 20), (keys, m.memory()[1] - held, lost)
+    if captured:
+        ref = []
+        for keys in steps:
+            call(m, kv, keys)
+            ref.append(out.clone())
+        for g, r in zip(graphs, ref):
+            out.zero_()
+            g.replay()
+            assert torch.equal(out, r)
+    else:
+        assert m.memory() == other[0].memory()
+    assert m.status() == 0
