@@ -251,7 +251,8 @@ int swiftkv_attend(swiftkv_model* m, int cache, const void* q, int ldq, const in
  *       + sum over the rows that see it and the group's query heads of exp(q . k / sqrt(d_head) - lse)
  * and every other entry stays as it is (decay 0 does not read the old value).
  *   q, lse  as swiftkv_attend took and wrote them
- *   scores  device float [num_pages][n_kv][16], the layout of the FP8 scale pools; 16-byte aligned
+ *   scores  device float [num_pages][n_kv][16], the layout of the FP8 scale pools; 16-byte aligned.
+ *           A key that is new to the cache needs an entry of 0 (or decay 0) in its first call.
  * Sequences of one call must not share pages they see. */
 int swiftkv_attention_weights(swiftkv_model* m, int cache, const void* q, int ldq, const float* lse,
                               const int32_t* cu_seqlens, const int32_t* ctx_lens, int num_seqs,
@@ -285,7 +286,9 @@ int swiftkv_set_attention_window(swiftkv_model* m, int window, int sinks);
 
 /* From now on every layer's attention adds the weights its rows gave to the keys of its cache to
  * that cache's score pool (swiftkv_attention_weights with this decay after each layer's attention;
- * layers that share a cache add up, so a decay other than 1 acts once per layer).
+ * layers that share a cache add up, so a decay other than 1 acts once per layer). The entries of rows
+ * that a call writes start from 0, whatever they held: a page's former owner's scores, or those behind
+ * the keys that an eviction kept.
  *   scores  HOST array [swiftkv_cache_count] of device float pools, as for swiftkv_evict, read at
  *           this call; the pools stay the caller's and must outlive the calls that add to them.
  *           NULL turns it off (default).

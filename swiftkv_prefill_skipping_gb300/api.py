@@ -117,7 +117,8 @@ class Model:
     def set_score_pools(self, scores: Optional[torch.Tensor], decay: float = 1.0) -> None:
         """Later calls add every layer's attention weights to scores (float32 [num_caches, num_pages,
         n_kv, 16] on the model's device, e.g. KVCache.new_scores(); kept alive here); None turns that
-        off. Sequences of a call must not share pages while it is on."""
+        off. Rows that a call writes start from 0. Sequences of a call must not share pages while it
+        is on."""
         if scores is None:
             B.check(B.lib().swiftkv_set_score_pools(self.handle, None, 0, decay))
         else:
@@ -358,7 +359,8 @@ def attention_weights(model: Model, q: torch.Tensor, lse: torch.Tensor, cu_seqle
                       window: int = 0, sinks: int = 0, decay: float = 1.0, stream=None) -> torch.Tensor:
     """Adds the attention weight that each cached key received from these tokens, summed over them
     and the query heads of its KV head, to scores (float32 [num_pages, n_kv, 16], one per key of the
-    cache): scores = decay * scores + weight for every key some token sees, the others unchanged.
+    cache): scores = decay * scores + weight for every key some token sees, the others unchanged. The
+    entry of a key that is new to the cache has to be 0.
     q and lse are those of the attend call before. Returns scores."""
     cu, ctx, P, T = _chunks(cu_seqlens, ctx_lens, kv, model)
     dev, s = kv.device, model.shape

@@ -110,6 +110,10 @@ cudaError_t launch_plan_prefill(const int* cu, const int* ctx, const int* pos_of
 cudaError_t launch_plan_decode(const int* seq_lens, int B, const int* tokens, int vocab,
                                const int* block_table, int max_pages, int num_pages, int* positions,
                                int* slots, int* status, cudaStream_t stream);
+// Score entries of the rows (slots, -1: none) that a call writes, zero in every pool [pages][n_kv][16]:
+// a key's score starts with the key. pools: host array of num_pools device pointers.
+cudaError_t launch_clear_scores(float* const* pools, int num_pools, const int* slots, int T, int n_kv,
+                                cudaStream_t stream);
 
 // ---- FP8 KV cache -------------------------------------------------------------------------
 // Quantizes staged K/V rows (stage [M][ld]: per group [K heads | V heads] of d_head bf16

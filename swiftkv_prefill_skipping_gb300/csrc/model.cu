@@ -1187,7 +1187,7 @@ static int prefill_impl(swiftkv_model* m, const int32_t* tokens, const int32_t* 
           (4 * m->C + kBlobInts - 1) / kBlobInts + (ctx ? (P + kBlobInts - 1) / kBlobInts : 0) +
           2 * (((int)srow.size() + kBlobInts - 1) / kBlobInts) +
           ((int)hs_short.ints() + kBlobInts - 1) / kBlobInts + ((int)hs_tail.ints() + kBlobInts - 1) / kBlobInts +
-          ((int)deq.size() + kBlobInts - 1) / kBlobInts,
+          ((int)deq.size() + kBlobInts - 1) / kBlobInts + (m->score_pools.empty() ? 0 : (m->C + 63) / 64),
           0.0, 0.0);
   if (!deq.empty()) CK(upload_ints(x.w.deq_items, deq.data(), (int)deq.size(), s));
   CK(upload_ints(x.w.cu, cu, P + 1, s));
@@ -1206,6 +1206,7 @@ static int prefill_impl(swiftkv_model* m, const int32_t* tokens, const int32_t* 
   RET(upload_pools(x));
   CK(launch_plan_prefill(x.w.cu, x.ctx, serving.offsets, P, T, tok, m->cfg.vocab, kv->block_table, kv->max_pages_per_seq, kv->num_pages,
                          x.w.positions, x.w.slots, x.w.last_idx, x.w.last_pos, m->status, s));
+  if (!m->score_pools.empty()) CK(launch_clear_scores(m->score_pools.data(), m->C, x.w.slots, T, m->cfg.n_kv, s));
   }
   const auto& c = m->cfg;
   // more than 64 prompt rows run on the tcgen05 GEMMs, which take the RMSNorm in their epilogues
@@ -1369,6 +1370,7 @@ int swiftkv_decode_step(swiftkv_model* m, const int32_t* tokens, const int32_t* 
   const auto& c = m->cfg;
   CK(launch_plan_decode(x.w.cu, B, tokens, c.vocab, kv->block_table, kv->max_pages_per_seq, kv->num_pages,
                         x.w.positions, x.w.slots, m->status, s));
+  if (!m->score_pools.empty()) CK(launch_clear_scores(m->score_pools.data(), m->C, x.w.slots, B, c.n_kv, s));
   CK(launch_embed_rmsnorm(tokens, B, m->embed, c.vocab, c.d, m->layers[0].g_attn, c.rms_eps, x.w.x, x.w.u, nullptr,
                           0, s));
   bool q_ready = false;  // the previous chained launch already computed this layer's Q/K/V

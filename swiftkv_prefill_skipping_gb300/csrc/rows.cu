@@ -67,6 +67,16 @@ __global__ void plan_decode_kernel(const int* __restrict__ seq_lens, int B, cons
   }
 }
 
+struct PoolBlob {
+  float* v[64];
+};
+__global__ void clear_scores_kernel(const PoolBlob pools, const int* __restrict__ slots, int T, int n_kv) {
+  const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x;
+  if (i >= (long long)T * n_kv) return;
+  const int slot = slots[i / n_kv], h = (int)(i % n_kv);
+  if (slot >= 0) pools.v[blockIdx.y][((size_t)(slot / kPageSize) * n_kv + h) * kPageSize + slot % kPageSize] = 0.f;
+}
+
 constexpr int RN_THREADS = 128;
 constexpr int RN_MAXV = 16;  // float4 per thread: d <= 8192
 
@@ -478,6 +488,20 @@ cudaError_t launch_plan_decode(const int* seq_lens, int B, const int* tokens, in
   if (B <= 0) return cudaSuccess;
   plan_decode_kernel<<<(B + 255) / 256, 256, 0, stream>>>(seq_lens, B, tokens, vocab, block_table,
                                                           max_pages, num_pages, positions, slots, status);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_clear_scores(float* const* pools, int num_pools, const int* slots, int T, int n_kv,
+                                cudaStream_t stream) {
+  if (T <= 0) return cudaSuccess;
+  constexpr int N = sizeof(PoolBlob) / sizeof(float*);
+  const long long blocks = ((long long)T * n_kv + 255) / 256;
+  for (int c = 0; c < num_pools; c += N) {
+    PoolBlob b;
+    const int n = num_pools - c < N ? num_pools - c : N;
+    for (int i = 0; i < n; ++i) b.v[i] = pools[c + i];
+    clear_scores_kernel<<<dim3((unsigned)blocks, n), 256, 0, stream>>>(b, slots, T, n_kv);
+  }
   return cudaGetLastError();
 }
 
