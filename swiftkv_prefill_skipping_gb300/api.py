@@ -41,6 +41,28 @@ def _empty(shape, dtype, dev: torch.device, stream) -> torch.Tensor:
         return torch.empty(shape, dtype=dtype, device=dev)
 
 
+_I32 = np.dtype(np.int32)
+
+
+def _int32(*values: int) -> None:
+    """ctypes takes a number's low 32 bits without a word."""
+    for x in values:
+        if not -0x80000000 <= x <= 0x7fffffff:
+            raise ValueError(f"{x} does not fit 32 bits")
+
+
+def _ints(a) -> np.ndarray:
+    """A call's host list as int32. (NumPy refuses Python numbers past 32 bits by itself, but wraps an
+    array's.)"""
+    if type(a) is np.ndarray and a.dtype is _I32:
+        return a
+    if type(a) not in (list, tuple):
+        a = np.asarray(a)
+        if not np.array_equal(a.astype(np.int32), a):
+            raise ValueError("a list with numbers that do not fit 32 bits")
+    return np.ascontiguousarray(a, dtype=np.int32)
+
+
 def _ptr(a) -> Optional[int]:
     if a is None:
         return None
@@ -112,6 +134,7 @@ class Model:
 
     def set_attention_window(self, window: int, sinks: int = 0) -> None:
         """Later calls see the last `window` tokens and the first `sinks` (0: all of them)."""
+        _int32(window, sinks)
         B.check(B.lib().swiftkv_set_attention_window(self.handle, window, sinks))
 
     def set_score_pools(self, scores: Optional[torch.Tensor], decay: float = 1.0) -> None:
@@ -270,7 +293,7 @@ def forward(model: Model, tokens: torch.Tensor, cu_seqlens: Sequence[int], ctx_l
         logits = torch.empty((P, model.shape.vocab), dtype=torch.float32, device=kv.k.device)
     tokens = tokens.to(torch.int32).contiguous()
     if pos_offsets is not None:
-        off = np.ascontiguousarray(pos_offsets, dtype=np.int32)
+        off = np.ascontiguousarray(_ints(pos_offsets))
         if len(off) != P:
             raise ValueError(f"pos_offsets has {len(off)} entries for {P} chunks")
         B.check(B.lib().swiftkv_forward_at(model.handle, tokens.data_ptr(), cu.ctypes.data,
@@ -306,8 +329,8 @@ def _fits(model: Model, kv: KVCache) -> None:
 def _chunks(cu_seqlens, ctx_lens, kv: KVCache, model: Model):
     """Host int32 arrays of a ragged batch, checked against the block table: (cu, ctx, P, T)."""
     _fits(model, kv)
-    cu = np.ascontiguousarray(cu_seqlens, dtype=np.int32)
-    ctx = None if ctx_lens is None else np.ascontiguousarray(ctx_lens, dtype=np.int32)
+    cu = _ints(cu_seqlens)
+    ctx = None if ctx_lens is None else _ints(ctx_lens)
     P = cu.shape[0] - 1 if cu.ndim == 1 else -1
     if P < 0 or (ctx is not None and ctx.shape != (P,)):
         raise ValueError("cu_seqlens: [P + 1], ctx_lens: [P]")
@@ -343,6 +366,8 @@ def attend(model: Model, q: torch.Tensor, cu_seqlens: Sequence[int], ctx_lens: O
     `sinks`. Returns out [T, n_q, d_h] bf16; lse (float32 [n_q, T]), if given, receives each row's
     log-sum-exp, which attention_weights takes."""
     cu, ctx, P, T = _chunks(cu_seqlens, ctx_lens, kv, model)
+    if cache or window or sinks:
+        _int32(cache, window, sinks)
     dev = kv.device
     ldq = _rows_of(q, T, model, dev, "q")
     if out is None:
@@ -363,6 +388,8 @@ def attention_weights(model: Model, q: torch.Tensor, lse: torch.Tensor, cu_seqle
     entry of a key that is new to the cache has to be 0.
     q and lse are those of the attend call before. Returns scores."""
     cu, ctx, P, T = _chunks(cu_seqlens, ctx_lens, kv, model)
+    if cache or window or sinks:
+        _int32(cache, window, sinks)
     dev, s = kv.device, model.shape
     ldq = _rows_of(q, T, model, dev, "q")
     lp = _flat(lse, torch.float32, (s.n_q, T), dev, "lse")
@@ -383,7 +410,8 @@ def evict(model: Model, kv: KVCache, scores: torch.Tensor, seq_lens: Sequence[in
     [caches, P, n_kv, keep] int32, -1 behind a shorter list; sequence s then holds
     min(seq_lens[s], keep) keys."""
     _fits(model, kv)
-    sl = np.ascontiguousarray(seq_lens, dtype=np.int32)
+    sl = _ints(seq_lens)
+    _int32(keep, sinks, recent)
     P, dev, s = sl.shape[0], kv.device, model.shape
     if P > kv.num_rows:
         raise ValueError(f"{P} sequences, but the block table has {kv.num_rows} rows")
@@ -433,7 +461,7 @@ def sample(logits: torch.Tensor, u: torch.Tensor, temperature=1.0, top_k=0, top_
     if isinstance(top_k, torch.Tensor):
         s.top_k = _flat(top_k, torch.int32, vec, dev, "top_k")
     else:
-        s.top_k_all = int(top_k)
+        s.top_k_all = max(0, min(int(top_k), 0x7fffffff))
     if isinstance(top_p, torch.Tensor):
         s.top_p = _flat(top_p, f32, vec, dev, "top_p")
     else:

@@ -146,3 +146,14 @@ def test_workspace_that_was_outgrown(captured):
     else:
         assert m.memory() == other[0].memory()
     assert m.status() == 0
+
+
+def test_sample_takes_any_number_as_top_k():
+    """From vocab on it is off, 2^32 + 5 as well, and so is anything below 1."""
+    import torch
+    from swiftkv_prefill_skipping_gb300 import api
+    x, u = torch.randn(200, 3000, device="cuda"), torch.rand(200, device="cuda")
+    ref = api.sample(x, u)
+    assert not torch.equal(ref, api.sample(x, u, top_k=5))
+    for k in (3000, (1 << 31) - 1, 1 << 31, (1 << 32) + 5, (1 << 63) + 5, -1, -(1 << 31), 5 - (1 << 32)):
+        assert torch.equal(ref, api.sample(x, u, top_k=k))

@@ -47,3 +47,25 @@ def test_sample_refuses_misaligned_arrays(which):
     vocab = 360449  # refused later on, so that no kernel runs where the check is missing
     assert B.lib().swiftkv_sample(256, 1, vocab, vocab, C.byref(s), at["u"], at["tokens"], None) == -1
     assert b"misaligned" in B.lib().swiftkv_last_error()
+
+
+@pytest.mark.parametrize("big", [1 << 31, (1 << 32) + 5, -(1 << 31) - 1])
+def test_numbers_past_32_bits_are_refused(big):
+    """They would wrap on their way into the call: 2^32 + 5 would be a window of 5."""
+    m = model_on("cpu")
+    kv = api.KVCache(m, 4, np.zeros((1, 2), np.int32), device=torch.device("cpu"))
+    q, lse, sc = torch.zeros(1, 4, 64, dtype=torch.bfloat16), torch.zeros(4, 1), kv.new_scores()
+    wide = np.array([big], np.int64)
+    calls = [lambda: m.set_attention_window(big), lambda: m.set_attention_window(4, big),
+             lambda: api.attend(m, q, [0, 1], None, kv, window=big), lambda: api.attend(m, q, [0, 1], None, kv, window=2, sinks=big),
+             lambda: api.attend(m, q, [0, 1], None, kv, cache=big),
+             lambda: api.attend(m, q, [0, 1], wide, kv), lambda: api.attend(m, q, [0, 1], torch.tensor(wide), kv),
+             lambda: api.attend(m, q, np.array([0, big]), None, kv),
+             lambda: api.attention_weights(m, q, lse, [0, 1], None, kv, sc[0], window=big),
+             lambda: api.attention_weights(m, q, lse, [0, 1], wide, kv, sc[0]),
+             lambda: api.evict(m, kv, sc, wide, 2), lambda: api.evict(m, kv, sc, [5], 2, sinks=big),
+             lambda: api.evict(m, kv, sc, [5], 2, recent=big), lambda: api.evict(m, kv, sc, [5], big),
+             lambda: api.forward(m, torch.zeros(1, dtype=torch.int32), [0, 1], [0], kv, pos_offsets=wide)]
+    for call in calls:
+        with pytest.raises((ValueError, OverflowError), match="32 bits"):
+            call()
