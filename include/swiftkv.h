@@ -269,7 +269,8 @@ int swiftkv_attention_weights(swiftkv_model* m, int cache, const void* q, int ld
  *   seq_lens   HOST int32 [num_seqs]: keys held now
  *   dst_block_table  device int32 [num_seqs][dst_max_pages], or NULL: in place. Its pages must not
  *              be pages of any sequence's first seq_lens[s] keys; source pages are only read then,
- *              so they may be shared (a common prefix). In place, no two sequences may share pages.
+ *              so they may be shared (a common prefix). In place, no two sequences may share pages,
+ *              and no two may share destination pages.
  *   kept       device int32 [caches][num_seqs][n_kv][keep]: former indices, ascending, -1 behind them
  * keep and seq_lens go up to 2^30, else SWIFTKV_EUNSUPPORTED.
  * A block-table entry outside the pools among those a sequence needs sets SWIFTKV_STATUS_BAD_PAGE,
@@ -279,6 +280,11 @@ int swiftkv_evict(swiftkv_model* m, int cache, const swiftkv_kv_pages* kv, float
                   const int32_t* dst_block_table, int dst_max_pages, int32_t* kept, swiftkv_stream stream);
 
 /* ---- the same in the model's own calls ------------------------------------------------------
+ * With a window, score pools or position offsets every layer's attention runs swiftkv_attend's kernels
+ * and rounds as they do. For prompt chunks of more than 4 rows that is P as one bf16, where the ordinary
+ * path takes two parts (an attention output is then off by 2.3e-3 instead of 1.7e-3 of its norm, most of
+ * it the output's own rounding to bf16): turning one of them on moves the logits by that.
+ *
  * Sliding window and sinks for the attention of every layer in later calls of swiftkv_prefill,
  * _prefill_host, _forward, _forward_at and _decode_step (visibility as above, by cache row); window 0
  * (default) turns them off. swiftkv_set_attention_impl does not concern calls with a window. */

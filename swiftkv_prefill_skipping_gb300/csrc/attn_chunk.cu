@@ -32,8 +32,10 @@
 // the rounding of P go four columns at a time, and FP8 is a template parameter, so that no branch
 // parts them (436 us with all three undone).
 //
-// 4 chunks of ~1960 rows after 0 - 6048 keys, 32 / 8 heads x 128: 355 us, 1.45 PFLOP/s; the same rows
-// through a window of 1024 and 4 sinks: 148 us. Bound by the tensor core and the hand-overs to it: 337 us
+// 4 chunks of ~1960 rows after 0 - 6048 keys, 32 / 8 heads x 128: 361 us, 1.42 PFLOP/s (392 called without
+// a pause, where the power cap lowers the clock); the same rows through a window of 1024 and 4 sinks:
+// 150 us. Those scores are nearly flat; with q 16 times as large, where sums outgrow the running maximum
+// more often, 454 us. FP8: 547 and 207 us, of which the expansion to bf16 is the difference. Bound by the tensor core and the hand-overs to it: 337 us
 // without any softmax. S of an 80-key block reads 6.5 KB of shared memory per 16 dims, 52 cycles
 // where the product takes 40, and a wider block does not fit beside P and O: with that the products
 // alone take 307 us. Measured and not kept: four softmax warpgroups on alternate 64-key blocks with P
@@ -402,6 +404,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_chunk_kernel(const __grid_con
       }
     }
   } else {
+    // (216 registers; 12 to 116 bytes of them spill, at d_head 64 most)
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_SOFTMAX));
     const int t = (warp - 4) >> 2, quarter = warp & 3;
     const uint32_t s_addr = tmem + ((uint32_t)(quarter * 32) << 16) + t * C::COLS;
@@ -411,7 +414,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_chunk_kernel(const __grid_con
     for (int it = 0; ok && item_at<BKV>(it, a, I); kvb += I.nblk, ++it) {
       const int nb = t ? I.nblk_b : I.nblk_a, q0 = t ? I.q0b : I.q0a;
       if (nb == 0) continue;
-// rows past the chunk see what its last row sees
+      // rows past the chunk see what its last row sees
       const int qw = q0 + quarter * 32, qrow = qw + lane, qpos = I.c0 + min(qrow, I.n - 1);
       const int first = window_begin(qpos, a.window), last = min(qpos, I.nk - 1), sinks = a.window > 0 ? a.sinks : 0;
       float m = -INFINITY, l = 0.f;

@@ -27,10 +27,13 @@
 // A unit that covers its item writes the output, others (max, sum, unnormalised O) records that
 // attn_rows_merge joins, one warp per column.
 //
-// 24 rows of ~1100 keys, 40 / 8 heads x 128, bf16: 25.6 us, 4.3 TB/s; 16 windows of 4096 keys and 4
-// sinks, 32 / 8 heads, FP8: 39 us, 3.5 TB/s (167 registers; with 16 columns a few of them spill). With one or two units a warp the rings' start, the last
-// round and the merge (3 us) do not overlap anything; on FP8 the unpacking and the products take
-// as long as the reads. 4 rows of up to 64 keys: 7.5 us, the launches' latency.
+// 24 rows of ~1100 keys, 40 / 8 heads x 128, bf16: 27.4 us, 4.1 TB/s; 16 windows of 4096 keys and 4
+// sinks, 32 / 8 heads, FP8: 39.7 us, 3.5 TB/s, and bf16 53 us, 5.0 TB/s. With one or two units a warp the
+// rings' start, the last round and the merge (3 us) do not overlap anything. On FP8 no unit is full
+// either (2.0 instructions a cycle and SM, 45 % of the ALU, 18 % of the tensor pipe, DRAM 51 %): 12 warps
+// do not cover the chain from a page's codes to its weights and back. 167 registers; with 16 columns 60
+// bytes spill. 64 rows of 3000 FP8 keys: 94 us, 4.3 TB/s. 4 rows of up to 64 keys: 7.3 us, the launches'
+// latency.
 #include <cfloat>
 
 #include "common.cuh"

@@ -9,7 +9,7 @@
 // of mma.sync m16n8k16 and the chunk's rows x heads its columns, so a key's sum is a sum along
 // the accumulator's row: one register per key and two shuffles a page.
 //
-// 24 rows of ~1100 keys, 40 / 8 heads x 128: 11.1 us, 5.1 TB/s.
+// 24 rows of ~1100 keys, 40 / 8 heads x 128: 15.3 us, 3.7 TB/s (11.1 with K still in L2); FP8 13.2 us.
 //
 // weights_tc_kernel (longer chunks): S^T = K Q^T on tcgen05. An item is a 256-key tile of one
 // (sequence, KV head); the tile stays in shared memory while 128-row query tiles of every head of
@@ -20,8 +20,9 @@
 //
 // Each half has two accumulators, a warpgroup for each, and a warp that issues its products: one
 // issuing warp for all spent 1000 cycles a tile on waits and issue where the product takes 512.
-// 4 chunks of ~1960 rows after 0 - 4032 keys, 32 / 8 heads x 128: 208 us, 920 TFLOP/s. Bound by the
-// epilogue: without its sums 138 us, without the exponentials alone 170 (they are one per score, 32 a
+// 4 chunks of ~1960 rows after 0 - 4032 keys, 32 / 8 heads x 128: 213 us, 903 TFLOP/s (FP8 227, with the
+// expansion of K; 0 - 6048 keys through a window of 1024: 138). A key's sum is off by 2e-7 of itself: four
+// float32 sums and ex2.approx (2^-22) for each of thousands of weights. Bound by the epilogue: without its sums 138 us, without the exponentials alone 170 (they are one per score, 32 a
 // cycle and SM, as many cycles as the product). Masks are decided for a warp's 32 keys by 32 rows:
 // all seen, none, or by element, which costs twice as much (218 us when decided by tile).
 #include <cuda.h>

@@ -12,7 +12,9 @@ namespace skv {
 namespace {
 
 // Chunks of at most this many rows go to the row kernel, split along their keys; a 128-row query
-// tile would be nearly empty (the serving forward's rule).
+// tile would be nearly empty (the serving forward's rule). Tiles are not split along the keys, so few
+// short chunks after a long prefix leave SMs idle: one sequence, 32 / 8 heads x 128, bf16, 4 rows after
+// 16000 keys 37 us, 5 rows 176; 8 sequences 98 and 179.
 constexpr int kRowChunk = 4;
 
 int check_batch(const swiftkv_model* m, const int32_t* cu, const int32_t* ctx, int P, const swiftkv_kv_pages* kv,
