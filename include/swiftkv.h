@@ -239,8 +239,9 @@ int swiftkv_decode_step(swiftkv_model* m, const int32_t* tokens, const int32_t* 
  *   lse  device float [n_q][T] or NULL: natural log of sum_j exp(q . k_j / sqrt(d_head))
  * P, over an FP8 cache times the value's scale, enters the product with V rounded to bf16 (chunks of
  * more than 4 rows) or as two bf16 parts (shorter ones); scores, sums and the output accumulate in
- * float32. FP8 value scales have to stay below 2^95. swiftkv_set_attention_impl does not concern this
- * call. */
+ * float32. The order in which a shorter chunk's keys are summed depends on the call's other chunks, so
+ * its last bits may; a longer one's do not. FP8 value scales have to stay below 2^95.
+ * swiftkv_set_attention_impl does not concern this call. */
 int swiftkv_attend(swiftkv_model* m, int cache, const void* q, int ldq, const int32_t* cu_seqlens,
                    const int32_t* ctx_lens, int num_seqs, const swiftkv_kv_pages* kv, int window, int sinks,
                    void* out, int ldo, float* lse, swiftkv_stream stream);
