@@ -108,14 +108,20 @@ typedef struct {
  * belong to the full layers, cache l + i to the i-th group of skipped layers.
  * Each cache has a K pool and a V pool of [num_pages][n_kv][page_size][d_head]
  * elements: one (page, head) block of page_size * d_head elements is contiguous.
- * Pools start on 16 bytes.
+ * Pools start on 16 bytes (the scale pools of kv_dtype 2 on 4).
  * Token at position p of sequence s lives in page block_table[s][p / page_size],
  * row p % page_size.
  * kv_dtype 0: bf16 elements. kv_dtype 1: per-token FP8 ("SwiftKV" summary, AcrossKV,
  * complementarity with KV quantization, Appendix B.1 / Table B.1): uint8 float8-e4m3
  * codes, and for every (page, head, row) one float32 scale in k_scale / v_scale pools of
  * [num_pages][n_kv][page_size]; the value is code * scale, scale = max|v| / 448 over the
- * token's d_head values of that head (K after RoPE). */
+ * token's d_head values of that head (K after RoPE).
+ * kv_dtype 2: int8 codes with one float32 scale for each (page, head), in k_scale / v_scale pools of
+ * [num_pages][n_kv]; the value is code * scale, codes in [-127, 127]: steps of 1/127 of the block's largest
+ * value, where FP8 has 1/14 of the token's for its largest values. How a block's scale grows: swiftkv_append. The
+ * model's calls take such caches too; their attention then runs swiftkv_attend's kernels.
+ * swiftkv_attention_weights, swiftkv_evict and score pools do not (SWIFTKV_EUNSUPPORTED).
+ * kv_dtype 1 and 2 take at most 8 query heads for each KV head. */
 typedef struct {
   void* const* k_pool;        /* host array [num_caches] of device pointers */
   void* const* v_pool;        /* host array [num_caches] of device pointers */
@@ -124,8 +130,8 @@ typedef struct {
   int page_size;              /* must be 16 */
   const int32_t* block_table; /* device int32 [num_seqs][max_pages_per_seq] */
   int max_pages_per_seq;
-  int kv_dtype;               /* 0 bf16, 1 fp8 e4m3 + per-token scales */
-  void* const* k_scale;       /* kv_dtype 1: host array [num_caches] of device float pools; else NULL */
+  int kv_dtype;               /* 0 bf16, 1 fp8 e4m3 + per-token scales, 2 int8 + per-page scales */
+  void* const* k_scale;       /* kv_dtype 1, 2: host array [num_caches] of device float pools; else NULL */
   void* const* v_scale;
 } swiftkv_kv_pages;
 
@@ -237,14 +243,46 @@ int swiftkv_decode_step(swiftkv_model* m, const int32_t* tokens, const int32_t* 
  *   cu_seqlens, ctx_lens  HOST int32, as for swiftkv_forward
  *   out  device bf16, rows ldo apart (same rules); must not overlap q
  *   lse  device float [n_q][T] or NULL: natural log of sum_j exp(q . k_j / sqrt(d_head))
- * P, over an FP8 cache times the value's scale, enters the product with V rounded to bf16 (chunks of
+ * P, over an FP8 or int8 cache times the value's scale, enters the product with V rounded to bf16 (chunks of
  * more than 4 rows) or as two bf16 parts (shorter ones); scores, sums and the output accumulate in
  * float32. The order in which a shorter chunk's keys are summed depends on the call's other chunks, so
- * its last bits may; a longer one's do not. FP8 value scales have to stay below 2^95.
+ * its last bits may; a longer one's do not. Value scales have to stay below 2^95. Over an int8 cache a page's
+ * scales have to be finite where any of its rows is visible.
  * swiftkv_set_attention_impl does not concern this call. */
 int swiftkv_attend(swiftkv_model* m, int cache, const void* q, int ldq, const int32_t* cu_seqlens,
                    const int32_t* ctx_lens, int num_seqs, const swiftkv_kv_pages* kv, int window, int sinks,
                    void* out, int ldo, float* lse, swiftkv_stream stream);
+
+/* New rows of one or several caches, device bf16, rows a multiple of 8 elements apart and 16-byte aligned. */
+typedef struct {
+  const void* k;    /* [T] rows of n_kv*d_head, ldk elements apart; cache i of the call k_step * i elements on */
+  const void* v;
+  int ldk, ldv;
+  long long k_step, v_step; /* multiples of 8; not used for one cache */
+  const void* q;    /* [T] rows of n_q*d_head, ldq elements apart, to be rotated as well, or NULL */
+  void* q_out;      /* where they go (rows ldq_out apart): q itself, or memory apart from it, k and v */
+  int ldq, ldq_out;
+} swiftkv_new_rows;
+
+/* Writes the K and V rows of a ragged batch of new tokens into caches cache .. cache + caches - 1, with the
+ * rotation of their positions on the way: what swiftkv_attend expects to have been done. Row i of chunk s
+ * goes to cache row p = ctx_lens[s] + i, and with rotate != 0 its K heads and its q turn to position
+ * p + pos_offsets[s] (pairs (i, i + d_head/2), the model's rope_theta, angles exact up to position 2^30, the
+ * rotation in float32 and rounded to bf16 once). With rotate 0 they are stored as they are.
+ *   cu_seqlens, ctx_lens  HOST int32, as for swiftkv_attend; pos_offsets HOST int32 [num_seqs] or NULL (all 0),
+ *                         none negative and no position above 2^30 - 1 (SWIFTKV_EINVAL_SEQLENS)
+ * An FP8 cache takes the scale and codes of the bf16 values, as in the model's own calls. On an int8 cache
+ * a page's scale is max|x| / 127 over the new rows, NaN left out and infinities as the largest bf16; where
+ * the page holds rows before them, it is the larger of that and the page's, and if it grows the earlier rows'
+ * codes become round(code * old / new), half a step of the new scale off at most. Codes are round(x / scale), 0
+ * for NaN. The codes thus depend on how a page's tokens were split into calls. What is in a page behind
+ * the new rows is not kept up: its codes stay and its scale may change.
+ * No two chunks of a call may write to the same row; on an int8 cache not to the same page. Rows before and behind
+ * a chunk's own stay as they are. An entry outside [0, num_pages) sets SWIFTKV_STATUS_BAD_PAGE, and its rows are
+ * skipped (their q is rotated all the same). */
+int swiftkv_append(swiftkv_model* m, int cache, int caches, const swiftkv_new_rows* rows, const int32_t* cu_seqlens,
+                   const int32_t* ctx_lens, const int32_t* pos_offsets, int num_seqs, const swiftkv_kv_pages* kv,
+                   int rotate, swiftkv_stream stream);
 
 /* Attention weight that each cached key received from the chunks' rows, per KV head: for every key
  * that some row sees
@@ -343,6 +381,37 @@ typedef struct {
  * (the arrays are read at each replay). vocab up to 360448, else SWIFTKV_EUNSUPPORTED. */
 int swiftkv_sample(const float* logits, int rows, int vocab, long long ld, const swiftkv_sampling* settings,
                    const float* u, int32_t* tokens, swiftkv_stream stream);
+
+/* Changes to logits before a token is drawn. Device arrays with one value (or row) for each row of the
+ * logits; NULL: the *_all value, or none of the kind. */
+typedef struct {
+  const int32_t* tokens;      /* [rows] histories, prompt first, ld_tokens apart: the first lens[r] of row r, ids */
+  long long ld_tokens;        /*   outside [0, vocab) ignored */
+  int max_tokens;             /* columns of tokens, up to 1048575; 0: no histories */
+  const int32_t* lens;        /* [rows], taken as within [0, max_tokens]; NULL: max_tokens */
+  const int32_t* prompt_lens; /* [rows] how many of them are the prompt's; NULL: 0 */
+  const float* repetition;    /* [rows] <= 0 or NaN: 1 (off) */
+  const float* presence;      /* [rows] 0: off */
+  const float* frequency;     /* [rows] 0: off */
+  float repetition_all, presence_all, frequency_all;
+  const int32_t* bias_ids;    /* [rows][num_bias], ids outside [0, vocab) unused; the last entry of an id counts */
+  const float* bias;          /* [rows][num_bias] */
+  int num_bias;               /* up to 2046; 0: none */
+  const uint32_t* mask;       /* [rows] of (vocab + 31) / 32 words, ld_mask apart: bit i % 32 of word i / 32 allows id i */
+  long long ld_mask;
+} swiftkv_adjustments;
+
+/* Penalties, biases and masks on logits, between the model's calls and swiftkv_sample. For id i of row r, s the
+ * ids in its history and c[i] how often i stands behind the prompt:
+ *   x = i in s ? (l > 0 ? l / repetition : l * repetition) : l
+ *   out = allowed by the mask ? x - frequency * c[i] - presence * (c[i] > 0) + bias[i] : -inf
+ *   logits  device float [rows][ld], the first `vocab` of each row
+ *   out     device float [rows][ld_out]: the logits themselves, or memory apart from them
+ * A row whose mask allows nothing becomes -inf throughout (swiftkv_sample then gives id 0). Needs no model and no
+ * workspace: calls on several streams may overlap, and a call can be captured into a CUDA graph (the arrays,
+ * lens among them, are read at each replay). In place, logits that nothing concerns are not read. vocab up to 2^30. */
+int swiftkv_adjust_logits(const float* logits, int rows, int vocab, long long ld, const swiftkv_adjustments* a,
+                          float* out, long long ld_out, swiftkv_stream stream);
 
 /* Reads (synchronously) the device status word; clears it when clear != 0.
  * Returns the swiftkv_status_bits that are set, or a negative swiftkv_error. */

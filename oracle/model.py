@@ -329,6 +329,62 @@ class kv_cache_fp8:
         return False
 
 
+PAGE = 16
+_KV_INT8 = [False]
+
+
+class kv_cache_int8:
+    """Context manager: the KV cache stores int8 codes with one float32 scale for each page of 16 rows
+    and head; every cache write goes through int8_append, which needs the rows before it."""
+
+    def __enter__(self):
+        _KV_INT8.append(True)
+        return self
+
+    def __exit__(self, *exc):
+        _KV_INT8.pop()
+        return False
+
+
+class Int8Rows(np.ndarray):
+    """Cached values [rows, n_kv, d_h] with the codes (the same shape) and scales [pages, n_kv] they come from."""
+    codes: np.ndarray
+    scales: np.ndarray
+
+
+def int8_append(old, rows: np.ndarray) -> Int8Rows:
+    """A cache of rows `old` (an Int8Rows or None) with the bfloat16 `rows` behind them. Page by page: scale =
+    float32(max |new rows|) / 127 in float32, or the page's own where that is larger; a page's earlier
+    codes become rint(code * (old / new)), new ones rint(float32(x) / scale), all in float32."""
+    rows = np.asarray(rows, np.float32)
+    n, h, d = rows.shape
+    ctx = 0 if old is None else old.shape[0]
+    codes = np.concatenate([np.zeros((0, h, d)) if old is None else old.codes, np.zeros((n, h, d))])
+    pages = (ctx + n + PAGE - 1) // PAGE
+    scales = np.zeros((pages, h), np.float32)
+    if ctx:
+        scales[:old.scales.shape[0]] = old.scales
+    for p in range(ctx // PAGE, pages):
+        lo, hi = max(PAGE * p, ctx), min(PAGE * p + PAGE, ctx + n)
+        x = rows[lo - ctx:hi - ctx]
+        was = scales[p].copy()
+        scales[p] = np.maximum(was, np.abs(x).max(axis=(0, 2)) / np.float32(127))
+        some = np.where(scales[p] > 0, scales[p], np.float32(1))
+        grown = scales[p] > was
+        codes[PAGE * p:lo, grown] = np.rint(codes[PAGE * p:lo, grown].astype(np.float32) * (was / some)[grown][:, None])
+        codes[lo:hi] = np.rint(x / some[:, None])
+    out = (codes * scales.astype(F64)[np.arange(ctx + n) // PAGE][..., None]).view(Int8Rows)
+    out.codes, out.scales = codes, scales
+    return out
+
+
+def _extended(old, new):
+    """The cache of rows `old` (a KV, or None) with the KV `new` behind them."""
+    if _KV_INT8[-1]:
+        return tuple(int8_append(None if old is None or not len(old[t]) else old[t], new[t]) for t in (0, 1))
+    return new if old is None else (np.concatenate([old[0], new[0]]), np.concatenate([old[1], new[1]]))
+
+
 def _cache_values(t: np.ndarray) -> np.ndarray:
     """What the cache holds for the bfloat16 K or V rows t[tokens, n_kv, d_h]."""
     return fp8_dequantize(*fp8_quantize(t)) if _KV_FP8[-1] else t
@@ -483,11 +539,11 @@ def swiftkv_prefill_one(cfg: Config, w: Weights, tokens: Sequence[int], l: int,
     for j in range(l):
         lw = w.layer(j)
         q, kv = qkv_proj(cfg, lw, x, pos)
-        caches[j] = kv
-        x = attn_out(cfg, lw, x, q, kv, pos, pos)
+        caches[j] = _extended(None, kv)
+        x = attn_out(cfg, lw, x, q, caches[j], pos, pos)
         x = mlp(cfg, lw, x)
     for c in range(l, len(caches)):
-        caches[c] = swiftkv_kv(cfg, w.layer(representative(c, l, g)), x, pos)
+        caches[c] = _extended(None, swiftkv_kv(cfg, w.layer(representative(c, l, g)), x, pos))
     xt, pt = x[n - 1:], pos[n - 1:]
     for j in range(l, cfg.L):
         lw = w.layer(j)
@@ -528,7 +584,7 @@ def swiftkv_decode_step(cfg: Config, w: Weights, caches: List[KV], token: int, l
     out: List[KV] = list(caches)
 
     def append(c: int, kv: KV) -> None:
-        out[c] = (np.concatenate([out[c][0], kv[0]]), np.concatenate([out[c][1], kv[1]]))
+        out[c] = _extended(out[c], kv)
 
     for j in range(cfg.L):
         lw = w.layer(j)
@@ -575,7 +631,7 @@ def swiftkv_forward_one(cfg: Config, w: Weights, caches: Optional[List[KV]], tok
     kpos = np.arange(ctx + n)
 
     def append(c: int, kv: KV) -> None:
-        out[c] = (np.concatenate([out[c][0], kv[0]]), np.concatenate([out[c][1], kv[1]]))
+        out[c] = _extended(out[c], kv)
 
     x = w.embed(tokens)
     for j in range(l):

@@ -172,34 +172,39 @@ def load_synthetic(shape, l: int, g: int = 1, seed: int = 0, gain_std: float = 0
     return m
 
 
+_KV_DTYPES = {"bf16": torch.bfloat16, "fp8": torch.uint8, "int8": torch.int8}  # in the order of kv_dtype
+
+
 class KVCache:
     """Caller-owned paged KV cache: num_caches x (K, V) pools of [num_pages][n_kv][16][d_h]
     elements plus a device block table. dtype "bf16": bfloat16 elements; dtype "fp8":
     uint8 float8-e4m3 codes with float32 scales [num_pages][n_kv][16] per pool (per-token
-    FP8)."""
+    FP8); dtype "int8": int8 codes with float32 scales [num_pages][n_kv], one for each page and
+    head."""
 
     def __init__(self, model: Model, num_pages: int, block_table: np.ndarray, device=None, dtype: str = "bf16"):
-        if dtype not in ("bf16", "fp8"):
+        if dtype not in _KV_DTYPES:
             raise ValueError(f"KV cache dtype {dtype!r}")
         s = model.shape
         dev = device or torch.device("cuda", torch.cuda.current_device())
         self.num_pages, self.dtype = num_pages, dtype
         self.heads = (s.n_kv, s.d_h)
         shape = (model.num_caches, num_pages, s.n_kv, 16, s.d_h)
-        elem = torch.bfloat16 if dtype == "bf16" else torch.uint8
+        elem = _KV_DTYPES[dtype]
         self.k = torch.zeros(shape, dtype=elem, device=dev)
         self.v = torch.zeros(shape, dtype=elem, device=dev)
         self.device = self.k.device
         self.k_scale = self.v_scale = None
-        if dtype == "fp8":
-            self.k_scale = torch.zeros(shape[:-1], dtype=torch.float32, device=dev)
-            self.v_scale = torch.zeros(shape[:-1], dtype=torch.float32, device=dev)
+        if dtype != "bf16":
+            per = shape[:-1] if dtype == "fp8" else shape[:-2]
+            self.k_scale = torch.zeros(per, dtype=torch.float32, device=dev)
+            self.v_scale = torch.zeros(per, dtype=torch.float32, device=dev)
         self.block_table = torch.as_tensor(np.ascontiguousarray(block_table, dtype=np.int32), device=dev)
         n = model.num_caches
         self._kp = (C.c_void_p * n)(*[self.k[c].data_ptr() for c in range(n)])
         self._vp = (C.c_void_p * n)(*[self.v[c].data_ptr() for c in range(n)])
         self._ks = self._vs = None
-        if dtype == "fp8":
+        if dtype != "bf16":
             self._ks = (C.c_void_p * n)(*[self.k_scale[c].data_ptr() for c in range(n)])
             self._vs = (C.c_void_p * n)(*[self.v_scale[c].data_ptr() for c in range(n)])
         self.num_caches = n
@@ -208,7 +213,7 @@ class KVCache:
     def _pages(self, block_table: torch.Tensor) -> B.KVPages:
         ptr = lambda a: C.cast(a, C.POINTER(C.c_void_p)) if a is not None else None  # noqa: E731
         return B.KVPages(ptr(self._kp), ptr(self._vp), self.num_caches, self.num_pages, 16, block_table.data_ptr(),
-                         block_table.shape[1], 1 if self.dtype == "fp8" else 0, ptr(self._ks), ptr(self._vs))
+                         block_table.shape[1], list(_KV_DTYPES).index(self.dtype), ptr(self._ks), ptr(self._vs))
 
     def _set_pages(self, pages: B.KVPages) -> None:
         self.pages, self.pages_ref = pages, C.byref(pages)
@@ -236,20 +241,23 @@ class KVCache:
 
     def gather(self, c: int, s: int, n: int, which: str = "k") -> torch.Tensor:
         """Cache c's first n rows of sequence s, [n, n_kv, d_h] (test/inspection helper);
-        for an fp8 cache the values code * scale in float32."""
+        for an fp8 or int8 cache the values code * scale in float32."""
         pool = self.k[c] if which == "k" else self.v[c]
         if self.dtype == "bf16":
             return self._rows(pool, s, n)
         return self.codes(c, s, n, which) * self.scales(c, s, n, which)[..., None]
 
     def codes(self, c: int, s: int, n: int, which: str = "k") -> torch.Tensor:
-        """fp8 cache: the e4m3 codes of cache c's first n rows of sequence s, as float32."""
+        """fp8 or int8 cache: the codes of cache c's first n rows of sequence s, as float32."""
         pool = self.k[c] if which == "k" else self.v[c]
-        return self._rows(pool, s, n).view(torch.float8_e4m3fn).float()
+        rows = self._rows(pool, s, n)
+        return (rows.view(torch.float8_e4m3fn) if self.dtype == "fp8" else rows).float()
 
     def scales(self, c: int, s: int, n: int, which: str = "k") -> torch.Tensor:
-        """fp8 cache: the float32 scales [n, n_kv] of cache c's first n rows of sequence s."""
+        """fp8 or int8 cache: the float32 scales [n, n_kv] of cache c's first n rows of sequence s."""
         pool = self.k_scale[c] if which == "k" else self.v_scale[c]
+        if self.dtype == "int8":
+            return pool[self.block_table[s][torch.arange(n, device=pool.device) // 16].long()]
         return self._rows(pool, s, n)
 
 
@@ -357,6 +365,52 @@ def _flat(t: torch.Tensor, dtype, shape: tuple, dev, name: str) -> int:
     return t.data_ptr()
 
 
+def _new_rows(t: torch.Tensor, T: int, heads: int, caches: int, d_h: int, dev, name: str):
+    """Row stride and the stride between caches of bf16 rows [T, heads, d_h], or [T, caches, heads, d_h]."""
+    shape, stride = t.shape, t.stride()
+    many = len(shape) == 4
+    if t.dtype is not torch.bfloat16 or t.device != dev or tuple(shape) != ((T, caches, heads, d_h) if many else
+                                                                           (T, heads, d_h)):
+        raise ValueError(f"{name}: bfloat16 [{T}, {heads}, {d_h}] or, for several caches, [{T}, {caches}, {heads}, {d_h}] on {dev}")
+    if T and (stride[-1] != 1 or heads > 1 and stride[-2] != d_h):
+        raise ValueError(f"{name}: the heads of a row have to be contiguous")
+    step = stride[1] if many and caches > 1 else heads * d_h
+    return (stride[0] if T > 1 else max(0, (caches - 1) * step) + heads * d_h), step
+
+
+def append(model: Model, k: torch.Tensor, v: torch.Tensor, cu_seqlens: Sequence[int], ctx_lens: Optional[Sequence[int]],
+           kv: KVCache, cache: int = 0, q: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None,
+           pos_offsets: Optional[Sequence[int]] = None, rotate: bool = True, stream=None) -> Optional[torch.Tensor]:
+    """Writes the keys and values of chunks of new tokens, k and v [T, n_kv, d_h] bf16 (rows may be strided:
+    parts of one projection), into cache `cache` of kv, ahead of attend. Chunk s follows ctx_lens[s] cached
+    tokens (None: none). Keys, and q [T, n_q, d_h] if given, are rotated to their positions, pos_offsets[s]
+    ahead of the cache's rows (after an eviction: the tokens that are gone); with rotate=False nothing is.
+    k and v of shape [T, n, n_kv, d_h] fill the n caches from `cache` on. Returns the rotated q: q_out, which may
+    be q itself, or a new tensor; None without q."""
+    cu, ctx, P, T = _chunks(cu_seqlens, ctx_lens, kv, model)
+    _int32(cache)
+    dev, s = kv.device, model.shape
+    off = None if pos_offsets is None else _ints(pos_offsets)
+    if off is not None and off.shape != (P,):
+        raise ValueError("pos_offsets: [P]")
+    n = k.shape[1] if k.dim() == 4 else 1
+    r = B.NewRows()
+    r.ldk, r.k_step = _new_rows(k, T, s.n_kv, n, s.d_h, dev, "k")
+    r.ldv, r.v_step = _new_rows(v, T, s.n_kv, n, s.d_h, dev, "v")
+    r.k, r.v = k.data_ptr(), v.data_ptr()
+    if q is not None:
+        r.ldq = _rows_of(q, T, model, dev, "q")
+        if q_out is None:
+            q_out = _empty((T, s.n_q, s.d_h), torch.bfloat16, dev, stream)
+        r.ldq_out = _rows_of(q_out, T, model, dev, "q_out")
+        r.q, r.q_out = q.data_ptr(), q_out.data_ptr()
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    B.check(B.lib().swiftkv_append(model.handle, cache, n, r, B.host(cu), B.host(ctx), B.host(off), P, kv.pages_ref,
+                                   int(rotate), _stream_of(dev, stream)))
+    return q_out
+
+
 def attend(model: Model, q: torch.Tensor, cu_seqlens: Sequence[int], ctx_lens: Optional[Sequence[int]], kv: KVCache,
            cache: int = 0, window: int = 0, sinks: int = 0, out: Optional[torch.Tensor] = None,
            lse: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
@@ -438,6 +492,68 @@ def evict(model: Model, kv: KVCache, scores: torch.Tensor, seq_lens: Sequence[in
     B.check(B.lib().swiftkv_evict(model.handle, -1 if cache is None else cache, kv.pages_ref, ptrs, B.host(sl), P, keep,
                                   sinks, recent, dst, width, kp, _stream_of(dev, stream)))
     return kept
+
+
+def _matrix(t: torch.Tensor, dtype, rows: int, cols: Optional[int], dev, name: str):
+    """Address, row stride and columns of a matrix [rows, cols] whose rows are contiguous."""
+    if t.dim() != 2 or t.dtype is not dtype or t.device != dev or t.shape[0] != rows or (
+            cols is not None and t.shape[1] != cols) or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name}: {dtype} [{rows}, {'n' if cols is None else cols}] on {dev}, contiguous within a row")
+    return t.data_ptr(), t.stride(0) if rows > 1 else t.shape[1], t.shape[1]
+
+
+def adjust_logits(logits: torch.Tensor, tokens: Optional[torch.Tensor] = None, lens: Optional[torch.Tensor] = None,
+                  prompt_lens: Optional[torch.Tensor] = None, repetition=1.0, presence=0.0, frequency=0.0,
+                  bias_ids: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
+                  mask: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Penalties, biases and grammar masks on float32 logits [P, V] (rows may be strided), ahead of sample.
+    tokens int32 [P, N] are the rows' histories, the first lens[r] of row r (None: all N), of which the first
+    prompt_lens[r] are its prompt (None: none). Ids in the history have their logit divided by `repetition` where
+    it is positive and multiplied by it elsewhere; `frequency` for each time behind the prompt and `presence`
+    once are subtracted; all three are numbers or float32 [P]. bias [P, B] float32 is added to the ids bias_ids
+    [P, B] int32 (-1: unused; the last entry of an id counts). mask int32 [P, (V + 31) // 32] allows id i of row r
+    by bit i % 32 of mask[r, i // 32]; the others become -inf. Returns out, which may be logits itself, or a
+    new tensor. Enqueued without synchronising."""
+    if logits.dim() != 2 or logits.dtype is not torch.float32 or not logits.is_cuda:
+        raise ValueError("logits: float32 CUDA [P, V]")
+    (P, V), (ld, step), dev = logits.shape, logits.stride(), logits.device
+    if P <= 1:
+        ld = V
+    if V < 1 or (V > 1 and step != 1) or ld < V:
+        raise ValueError("logits: at least one column, contiguous within a row, rows that do not overlap")
+    i32, f32, vec, a = torch.int32, torch.float32, (P,), B.Adjustments()
+    a.repetition_all, a.presence_all, a.frequency_all = 1.0, 0.0, 0.0
+    if tokens is not None:
+        a.tokens, a.ld_tokens, a.max_tokens = _matrix(tokens, i32, P, None, dev, "tokens")
+        if lens is not None:
+            a.lens = _flat(lens, i32, vec, dev, "lens")
+        if prompt_lens is not None:
+            a.prompt_lens = _flat(prompt_lens, i32, vec, dev, "prompt_lens")
+        for name, x in (("repetition", repetition), ("presence", presence), ("frequency", frequency)):
+            if isinstance(x, torch.Tensor):
+                setattr(a, name, _flat(x, f32, vec, dev, name))
+            else:
+                setattr(a, name + "_all", x)
+    elif lens is not None or prompt_lens is not None:
+        raise ValueError("lens and prompt_lens belong to tokens")
+    if (bias_ids is None) != (bias is None):
+        raise ValueError("bias_ids and bias go together")
+    if bias is not None:
+        n = bias.shape[1] if bias.dim() == 2 else -1
+        a.bias_ids, a.bias, a.num_bias = (_flat(bias_ids, i32, (P, n), dev, "bias_ids"),
+                                          _flat(bias, f32, (P, n), dev, "bias"), n)
+    if mask is not None:
+        a.mask, a.ld_mask, _ = _matrix(mask, i32, P, (V + 31) // 32, dev, "mask")
+    if out is None:
+        out = _empty((P, V), f32, dev, stream)
+    op, ldo, _ = _matrix(out, f32, P, V, dev, "out")
+    args = (logits.data_ptr(), P, V, ld, a, op, ldo, _stream_of(dev, stream))
+    if torch.cuda.current_device() == dev.index:
+        B.check(B.lib().swiftkv_adjust_logits(*args))
+    else:
+        with torch.cuda.device(dev):
+            B.check(B.lib().swiftkv_adjust_logits(*args))
+    return out
 
 
 def sample(logits: torch.Tensor, u: torch.Tensor, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0,

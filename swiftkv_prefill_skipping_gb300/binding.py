@@ -26,7 +26,7 @@ STATUS_TIMEOUT = 4
 # every symbol include/swiftkv.h declares
 EXPORTS = ("swiftkv_cache_count", "swiftkv_model_create", "swiftkv_load_layer", "swiftkv_load_globals",
            "swiftkv_load_weights", "swiftkv_prefill", "swiftkv_prefill_host", "swiftkv_forward",
-           "swiftkv_decode_step", "swiftkv_sample", "swiftkv_attend",
+           "swiftkv_decode_step", "swiftkv_sample", "swiftkv_adjust_logits", "swiftkv_append", "swiftkv_attend",
            "swiftkv_attention_weights", "swiftkv_evict", "swiftkv_set_attention_window",
            "swiftkv_set_score_pools", "swiftkv_forward_at",
            "swiftkv_status", "swiftkv_memory", "swiftkv_set_gemm_impl", "swiftkv_set_attention_impl",
@@ -73,6 +73,19 @@ class Sampling(C.Structure):
                 ("min_p_all", C.c_float)]
 
 
+class NewRows(C.Structure):
+    _fields_ = [("k", C.c_void_p), ("v", C.c_void_p), ("ldk", C.c_int), ("ldv", C.c_int), ("k_step", C.c_longlong),
+                ("v_step", C.c_longlong), ("q", C.c_void_p), ("q_out", C.c_void_p), ("ldq", C.c_int), ("ldq_out", C.c_int)]
+
+
+class Adjustments(C.Structure):
+    _fields_ = [("tokens", C.c_void_p), ("ld_tokens", C.c_longlong), ("max_tokens", C.c_int), ("lens", C.c_void_p),
+                ("prompt_lens", C.c_void_p), ("repetition", C.c_void_p), ("presence", C.c_void_p),
+                ("frequency", C.c_void_p), ("repetition_all", C.c_float), ("presence_all", C.c_float),
+                ("frequency_all", C.c_float), ("bias_ids", C.c_void_p), ("bias", C.c_void_p), ("num_bias", C.c_int),
+                ("mask", C.c_void_p), ("ld_mask", C.c_longlong)]
+
+
 class ProfileEntry(C.Structure):
     _fields_ = [("name", C.c_char * 32), ("calls", C.c_int), ("kernels", C.c_int), ("ms", C.c_double),
                 ("flops", C.c_double), ("bytes", C.c_double)]
@@ -99,6 +112,8 @@ def lib(path: str | None = None):
             L.swiftkv_forward.argtypes = [vp, vp, vp, vp, i, i, i, C.POINTER(KVPages), vp, vp]
             L.swiftkv_decode_step.argtypes = [vp, vp, vp, i, C.POINTER(KVPages), vp, vp, vp]
             L.swiftkv_attend.argtypes = [vp, i, vp, i, vp, vp, i, C.POINTER(KVPages), i, i, vp, i, vp, vp]
+            L.swiftkv_append.argtypes = [vp, i, i, C.POINTER(NewRows), vp, vp, vp, i, C.POINTER(KVPages), i, vp]
+            L.swiftkv_adjust_logits.argtypes = [vp, i, i, C.c_longlong, C.POINTER(Adjustments), vp, C.c_longlong, vp]
             L.swiftkv_attention_weights.argtypes = [vp, i, vp, i, vp, vp, vp, i, C.POINTER(KVPages), i, i, C.c_float,
                                                     vp, vp]
             L.swiftkv_evict.argtypes = [vp, i, C.POINTER(KVPages), C.POINTER(vp), vp, i, i, i, i, vp, i, vp, vp]

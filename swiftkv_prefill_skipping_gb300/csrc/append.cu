@@ -1,0 +1,316 @@
+// New keys and values into the paged cache, with the rotation of their positions on the way
+// (swiftkv_append, and the model's own calls on an int8 cache).
+//
+//   k' = R(pos) k, q' = R(pos) q: pairs (i, i + d/2) turned by pos theta^(-2i/d), in float32, rounded
+//   to bf16 once. Cache row ctx + i of the sequence takes
+//     bf16   k' and v
+//     FP8    per row and head the scale s = max|x| / 448 and the e4m3 codes of x / s
+//     int8   per page and head one scale and codes round(x / s) in [-127, 127]. The scale is that of the
+//            new rows, max|x| / 127, or, on a page that holds earlier rows, the larger of that and what the
+//            page has; where it grows the earlier rows' codes become round(code * old / new), off by half a
+//            step of the new scale each time.
+//
+// Bound by HBM: every row is read and written once. A lane owns 8 neighbouring dimensions and their
+// partners half a head on, so a pair turns within a lane, all accesses are 16 bytes (8 for codes), and a
+// head is 8 lanes (4 at d_head 64).
+//   Rows (q; K and V of a bf16 or FP8 cache): a warp takes one token and steps through its heads with the
+//   token's angles in registers, 4 heads in flight per lane. Few tokens are split among several warps.
+//   Pages (K and V of an int8 cache): a warp takes one (page, cache, K or V, head): its new rows stay in
+//   registers between the maximum and the codes. One warp owns the block, so a repeated call repeats its bits.
+#include <algorithm>
+
+#include "common.cuh"
+#include "pdl.cuh"
+#include "serving.h"
+
+namespace skv {
+
+namespace {
+
+constexpr int AWARPS = 8;
+constexpr int UNROLL = 4;  // heads in flight per lane
+
+// The last of n entries of the ascending f with f(s) <= v (f(0) <= v), searched by the whole warp.
+template <typename F>
+__device__ __forceinline__ int find_last(int n, long long v, F f) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, len = n;
+  while (len > 1) {
+    const int step = (len + 31) / 32, at = lane * step;
+    const unsigned in = __ballot_sync(0xffffffffu, at < len && f(lo + at) <= v);
+    const int k = (31 - __clz(in)) * step;
+    lo += k;
+    len = min(step, len - k);
+  }
+  return lo;
+}
+
+// 16 values of a lane: dims 8 j .. + 7 and their partners.
+struct Piece {
+  uint4 a, b;
+};
+__device__ __forceinline__ void turn_piece(Piece& p, const float2* cs) {
+  uint32_t* a = &p.a.x;
+  uint32_t* b = &p.b.x;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float x0 = __uint_as_float(a[i] << 16), x1 = __uint_as_float(a[i] & 0xffff0000u);
+    float y0 = __uint_as_float(b[i] << 16), y1 = __uint_as_float(b[i] & 0xffff0000u);
+    rope_turn_pair(cs[2 * i], x0, y0);
+    rope_turn_pair(cs[2 * i + 1], x1, y1);
+    a[i] = pack_bf16(x0, x1);
+    b[i] = pack_bf16(y0, y1);
+  }
+}
+__device__ __forceinline__ float largest(const Piece& p) {
+  const uint32_t* w = &p.a.x;
+  const uint32_t* u = &p.b.x;
+  float m = 0.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    m = fmaxf(m, fmaxf(fabsf(__uint_as_float(w[i] << 16)), fabsf(__uint_as_float(w[i] & 0xffff0000u))));
+    m = fmaxf(m, fmaxf(fabsf(__uint_as_float(u[i] << 16)), fabsf(__uint_as_float(u[i] & 0xffff0000u))));
+  }
+  return m;
+}
+template <int D>
+__device__ __forceinline__ void load_angles(const AppendArgs& a, int pos, int j, float2* cs) {
+  if (pos < a.rope_len) {
+    const float4* t = reinterpret_cast<const float4*>(a.rope_tab + (size_t)pos * (D / 2) + 8 * j);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float4 f = t[i];
+      cs[2 * i] = make_float2(f.x, f.y);
+      cs[2 * i + 1] = make_float2(f.z, f.w);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) cs[i] = rope_angle(a.rope_tab, a.rope_len, a.rope_turn, D / 2, pos, 8 * j + i);
+  }
+}
+
+// x / scale as an int8 code; NaN becomes 0.
+__device__ __forceinline__ uint32_t code8(float x, float scale) {
+  return (uint32_t)(max(-127, min(127, __float2int_rn(x / scale))) & 255);
+}
+__device__ __forceinline__ uint2 codes8(uint4 v, float scale) {
+  const uint32_t* w = &v.x;
+  uint32_t c[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    c[2 * i] = code8(__uint_as_float(w[i] << 16), scale);
+    c[2 * i + 1] = code8(__uint_as_float(w[i] & 0xffff0000u), scale);
+  }
+  return make_uint2(c[0] | c[1] << 8 | c[2] << 16 | c[3] << 24, c[4] | c[5] << 8 | c[6] << 16 | c[7] << 24);
+}
+__device__ __forceinline__ uint2 rescale8(uint2 v, float ratio) {
+  uint32_t out[2] = {v.x, v.y};
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t r = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int code = (int)(out[h] << (24 - 8 * i)) >> 24;
+      r |= (uint32_t)(__float2int_rn((float)code * ratio) & 255) << (8 * i);
+    }
+    out[h] = r;
+  }
+  return make_uint2(out[0], out[1]);
+}
+
+template <int D, int KIND>
+__global__ void __launch_bounds__(AWARPS * 32) append_kernel(const AppendArgs a, const __grid_constant__ InlineInts inl) {
+  constexpr int LPV = D / 16, VPW = 32 / LPV;  // lanes of a head, heads (or rows) of a warp's step
+  griddep_launch_dependents();
+  griddep_wait();
+  const int* const lists = list_base(a.lists, inl);
+  const int *cu = lists + a.o_cu, *ctx = lists + a.o_ctx, *off = lists + a.o_off;
+  const long long* const pools = a.pools ? a.pools : reinterpret_cast<const long long*>(lists + a.o_pools);
+  const int lane = threadIdx.x & 31, sub = lane / LPV, j = lane % LPV;
+  long long w = (long long)blockIdx.x * AWARPS + (threadIdx.x >> 5);
+  if (w < a.row_warps) {
+    const int t = (int)(w / a.splits), split = (int)(w - (long long)t * a.splits);
+    const int s = find_last(a.P, t, [&](int i) { return (long long)cu[i]; });
+    const int row = ctx[s] + t - cu[s], pos = row + (a.o_off >= 0 ? off[s] : 0);
+    const int page = KIND == kKvInt8 ? 0 : a.bt[(size_t)s * a.max_pages + (row >> 4)];
+    const bool ok = page >= 0 && page < a.num_pages;
+    if (!ok && lane == 0 && split == 0) atomicOr(a.status, kStatusBadPage);
+    float2 cs[8];
+    if (a.rotate) load_angles<D>(a, pos, j, cs);
+    const int nq = a.q ? a.n_q : 0, nvec = nq + (KIND == kKvInt8 ? 0 : a.caches * 2 * a.n_kv);
+    // vectors in order: the query heads, then K heads and V heads of each cache
+    for (int v0 = split * UNROLL * VPW; v0 < nvec; v0 += a.splits * UNROLL * VPW) {
+      Piece p[UNROLL];
+      int cache[UNROLL], head[UNROLL];  // head: -1 nothing, then query heads, K heads, V heads
+#pragma unroll
+      for (int u = 0; u < UNROLL; ++u) {
+        const int vec = v0 + u * VPW + sub;
+        p[u].a = p[u].b = make_uint4(0, 0, 0, 0);
+        cache[u] = 0;
+        head[u] = -1;
+        const bf16* src = nullptr;
+        if (vec < nq) {
+          head[u] = vec;
+          src = a.q + (size_t)t * a.ldq + (size_t)vec * D;
+        } else if (vec < nvec && ok) {
+          const int r = vec - nq, c = (int)__umulhi((uint32_t)r, a.per_cache), h = r - c * 2 * a.n_kv;
+          cache[u] = c;
+          head[u] = a.n_q + h;
+          src = h < a.n_kv ? a.k + (size_t)t * a.ldk + (size_t)c * a.k_step + (size_t)h * D
+                           : a.v + (size_t)t * a.ldv + (size_t)c * a.v_step + (size_t)(h - a.n_kv) * D;
+        }
+        if (src) {
+          p[u].a = *reinterpret_cast<const uint4*>(src + 8 * j);
+          p[u].b = *reinterpret_cast<const uint4*>(src + D / 2 + 8 * j);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < UNROLL; ++u) {
+        const bool is_q = head[u] < a.n_q, is_v = head[u] >= a.n_q + a.n_kv;
+        if (a.rotate && !is_v) turn_piece(p[u], cs);
+        if (is_q) {
+          if (head[u] >= 0) {
+            bf16* dst = a.q_out + (size_t)t * a.ldq_out + (size_t)head[u] * D + 8 * j;
+            *reinterpret_cast<uint4*>(dst) = p[u].a;
+            *reinterpret_cast<uint4*>(dst + D / 2) = p[u].b;
+          }
+        }
+        if (KIND == kKvInt8) continue;
+        const int h = head[u] - a.n_q - (is_v ? a.n_kv : 0);
+        const size_t at = ((size_t)page * a.n_kv + (is_q ? 0 : h)) * kPageSize + (row & 15);
+        const long long* pool = pools + (is_v ? a.pool_step : 0) + cache[u];
+        if (KIND == kKvBf16) {
+          if (!is_q) {
+            bf16* dst = reinterpret_cast<bf16*>(*pool) + at * D + 8 * j;
+            *reinterpret_cast<uint4*>(dst) = p[u].a;
+            *reinterpret_cast<uint4*>(dst + D / 2) = p[u].b;
+          }
+        } else {
+          float top = largest(p[u]);
+#pragma unroll
+          for (int o = 1; o < LPV; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+          if (!is_q) {
+            const float scale = top / 448.f;
+            const uint32_t* x = &p[u].a.x;
+            const uint32_t* y = &p[u].b.x;
+            uint16_t c[8];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float x0 = __uint_as_float(x[i] << 16), x1 = __uint_as_float(x[i] & 0xffff0000u);
+              const float y0 = __uint_as_float(y[i] << 16), y1 = __uint_as_float(y[i] & 0xffff0000u);
+              c[i] = scale > 0.f ? e4m3x2_from_f32(x0 / scale, x1 / scale) : (uint16_t)0;
+              c[4 + i] = scale > 0.f ? e4m3x2_from_f32(y0 / scale, y1 / scale) : (uint16_t)0;
+            }
+            uint8_t* dst = reinterpret_cast<uint8_t*>(*pool) + at * D + 8 * j;
+            *reinterpret_cast<uint2*>(dst) = make_uint2(c[0] | (uint32_t)c[1] << 16, c[2] | (uint32_t)c[3] << 16);
+            *reinterpret_cast<uint2*>(dst + D / 2) = make_uint2(c[4] | (uint32_t)c[5] << 16, c[6] | (uint32_t)c[7] << 16);
+            if (j == 0) reinterpret_cast<float*>(pool[2 * a.pool_step])[at] = scale;
+          }
+        }
+      }
+    }
+    return;
+  }
+  if (KIND != kKvInt8) return;
+  // int8: virtual page x of sequence s, those of a sequence starting at cu[s] / 16 + 2 s: n rows touch at
+  // most floor(n / 16) + 2 pages, which is no more than the distance to the next sequence's
+  w -= (a.row_warps + AWARPS - 1) / AWARPS * AWARPS;
+  if (w < 0) return;  // the last block of rows
+  const int per = a.caches * 2 * a.n_kv;
+  const long long x = w / per;
+  if (x >= a.pages) return;
+  const int r = (int)(w - x * per), c = (int)__umulhi((uint32_t)r, a.per_cache), h2 = r - c * 2 * a.n_kv;
+  const bool is_v = h2 >= a.n_kv;
+  const int h = is_v ? h2 - a.n_kv : h2;
+  const int s = find_last(a.P, x, [&](int i) { return (long long)(cu[i] >> 4) + 2LL * i; });
+  const int r0 = cu[s], n = cu[s + 1] - r0, c0 = ctx[s];
+  const long long pidx = (c0 >> 4) + (x - (r0 >> 4) - 2LL * s);
+  const int key0 = (int)(pidx << 4);
+  if (n < 1 || pidx << 4 >= (long long)c0 + n) return;
+  const int page = a.bt[(size_t)s * a.max_pages + pidx];
+  if (page < 0 || page >= a.num_pages) {
+    if (lane == 0) atomicOr(a.status, kStatusBadPage);
+    return;
+  }
+  const int first = max(0, c0 - key0), last = min(kPageSize, c0 + n - key0);  // the page's new rows
+  const bf16* src = (is_v ? a.v + (size_t)c * a.v_step : a.k + (size_t)c * a.k_step) + (size_t)h * D + 8 * j;
+  const int ld = is_v ? a.ldv : a.ldk;
+  constexpr int STEPS = kPageSize / VPW;
+  Piece p[STEPS];
+#pragma unroll
+  for (int i = 0; i < STEPS; ++i) {
+    const int row = i * VPW + sub;
+    p[i].a = p[i].b = make_uint4(0, 0, 0, 0);
+    if (row >= first && row < last) {
+      const bf16* from = src + (size_t)(r0 + key0 + row - c0) * ld;
+      p[i].a = *reinterpret_cast<const uint4*>(from);
+      p[i].b = *reinterpret_cast<const uint4*>(from + D / 2);
+    }
+  }
+  const long long* pool = pools + (is_v ? a.pool_step : 0) + c;
+  float* scale_at = reinterpret_cast<float*>(pool[2 * a.pool_step]) + (size_t)page * a.n_kv + h;
+  const float old = first > 0 ? *scale_at : 0.f;
+  float top = 0.f;
+#pragma unroll
+  for (int i = 0; i < STEPS; ++i) {
+    const int row = i * VPW + sub;
+    if (!is_v && a.rotate && row >= first && row < last) {
+      float2 cs[8];
+      load_angles<D>(a, key0 + row + (a.o_off >= 0 ? off[s] : 0), j, cs);
+      turn_piece(p[i], cs);
+    }
+    top = fmaxf(top, largest(p[i]));
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  const float mine = fminf(top, 3.3895314e38f) / 127.f;  // an infinity counts as the largest bf16
+  const float scale = fmaxf(mine, old), by = scale > 0.f ? scale : 1.f;
+  uint8_t* dst = reinterpret_cast<uint8_t*>(*pool) + ((size_t)page * a.n_kv + h) * kPageSize * D + 8 * j;
+#pragma unroll
+  for (int i = 0; i < STEPS; ++i) {
+    const int row = i * VPW + sub;
+    uint2* lo = reinterpret_cast<uint2*>(dst + (size_t)row * D);
+    uint2* hi = reinterpret_cast<uint2*>(dst + (size_t)row * D + D / 2);
+    if (row >= first && row < last) {
+      *lo = codes8(p[i].a, by);
+      *hi = codes8(p[i].b, by);
+    } else if (row < first && scale > old) {
+      const float ratio = old / scale;
+      *lo = rescale8(*lo, ratio);
+      *hi = rescale8(*hi, ratio);
+    }
+  }
+  if (lane == 0 && (first == 0 || scale > old)) *scale_at = scale;
+}
+
+template <int D, int KIND>
+cudaError_t launch_kind(const AppendArgs& a, const InlineInts& inl, cudaStream_t s) {
+  const long long rows = (a.row_warps + AWARPS - 1) / AWARPS;
+  const long long pages = KIND == kKvInt8 ? (a.pages * a.caches * 2 * a.n_kv + AWARPS - 1) / AWARPS : 0;
+  if (rows + pages <= 0) return cudaSuccess;
+  if (rows + pages >= 1LL << 31) return cudaErrorNotSupported;
+  return launch_pdl(append_kernel<D, KIND>, dim3((unsigned)(rows + pages)), dim3(AWARPS * 32), 0, s, a, inl);
+}
+
+template <int D>
+cudaError_t launch_d(const AppendArgs& a, int kind, const InlineInts& inl, cudaStream_t s) {
+  return kind == kKvBf16 ? launch_kind<D, kKvBf16>(a, inl, s)
+         : kind == kKvFp8 ? launch_kind<D, kKvFp8>(a, inl, s) : launch_kind<D, kKvInt8>(a, inl, s);
+}
+
+}  // namespace
+
+cudaError_t launch_append(AppendArgs a, int kind, int d_head, const InlineInts& inl, int num_sms, cudaStream_t s) {
+  if (a.T <= 0) return cudaSuccess;
+  if (d_head != 64 && d_head != 128) return cudaErrorNotSupported;
+  a.per_cache = (uint32_t)((1ULL << 32) / (2 * a.n_kv)) + 1;  // r * this >> 32 = r / (2 n_kv) for r < 2^16
+  const int vecs = (a.q ? a.n_q : 0) + (kind == kKvInt8 ? 0 : a.caches * 2 * a.n_kv);
+  const int steps = (vecs + UNROLL * (512 / d_head) - 1) / (UNROLL * (512 / d_head));
+  // a token's heads go to several warps until every SM has 16 of them
+  a.splits = (int)std::max(1LL, std::min<long long>(steps, (16LL * num_sms + a.T - 1) / a.T));
+  a.row_warps = steps ? (long long)a.T * a.splits : 0;
+  a.pages = kind == kKvInt8 ? (a.T >> 4) + 2LL * a.P : 0;
+  return d_head == 128 ? launch_d<128>(a, kind, inl, s) : launch_d<64>(a, kind, inl, s);
+}
+
+}  // namespace skv

@@ -90,7 +90,7 @@ struct Ctrl {
   uint32_t tmem_base;
   int abort;
   int pend[1 + C::KST + C::VST];                  // phases of copies in flight: Q, K stages, V stages
-  alignas(16) float scale[C::VST][2][C::BKV];      // FP8: key scales, value scales
+  alignas(16) float scale[C::VST][2][C::BKV];      // FP8: key scales, value scales; int8: a float4 a page
 };
 template <int D>
 constexpr int smem_bytes() {
@@ -181,6 +181,12 @@ __device__ __forceinline__ void fma2(float* d, const float* x, float c, float m)
       : "=f"(d[0]), "=f"(d[1])
       : "f"(x[0]), "f"(x[1]), "f"(c), "f"(m));
 }
+__device__ __forceinline__ void mul2(float* d, float c) {
+  asm("{\n .reg .b64 a, b;\n mov.b64 a, {%0, %1};\n mov.b64 b, {%2, %2};\n mul.rn.f32x2 a, a, b;\n"
+      " mov.b64 {%0, %1}, a;\n}\n"
+      : "+f"(d[0]), "+f"(d[1])
+      : "f"(c));
+}
 __device__ __forceinline__ void add2(float* acc, const float* p) {
   asm("{\n .reg .b64 a, b;\n mov.b64 a, {%0, %1};\n mov.b64 b, {%2, %3};\n add.rn.f32x2 a, a, b;\n"
       " mov.b64 {%0, %1}, a;\n}\n"
@@ -188,7 +194,7 @@ __device__ __forceinline__ void add2(float* acc, const float* p) {
       : "f"(p[0]), "f"(p[1]));
 }
 
-template <int D, bool FP8>
+template <int D, int KIND>
 __global__ void __launch_bounds__(THREADS, 1) attn_chunk_kernel(const __grid_constant__ CUtensorMap tmQ,
                                                                 const __grid_constant__ CUtensorMap tmK,
                                                                 const __grid_constant__ CUtensorMap tmV,
@@ -196,6 +202,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_chunk_kernel(const __grid_con
                                                                 const __grid_constant__ ChunkArgs a, float scale_log2) {
   using C = Cfg<D>;
   constexpr int BKV = C::BKV, PAGES = C::PAGES, KST = C::KST, VST = C::VST;
+  constexpr bool FP8 = KIND == kKvFp8, INT8 = KIND == kKvInt8;
   extern __shared__ unsigned char smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   unsigned char* smem = smem_raw + ((1024 - (raw & 1023)) & 1023);
@@ -303,7 +310,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_chunk_kernel(const __grid_con
           }
           if (!(ok = wait_all(is_v ? bar(ctl->v_empty[st]) : bar(ctl->k_empty[st]), ph ^ 1))) break;
           if (lane == 0) {
-            mbar_expect_tx(full, C::KV_TILE + (is_v && FP8 ? 2 * BKV * 4 : 0));
+            mbar_expect_tx(full, C::KV_TILE + (!is_v ? 0 : FP8 ? 2 * BKV * 4 : INT8 ? PAGES * 16 : 0));
             ctl->pend[is_v ? 1 + KST + st : 1 + st] = (int)ph;
           }
           __syncwarp();
@@ -316,6 +323,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_chunk_kernel(const __grid_con
               bulk_load(sd, a.k_scale + sr, kPageSize * 4, full);
               bulk_load(sd + BKV * 4, a.v_scale + sr, kPageSize * 4, full);
             }
+            if (is_v && INT8) bulk_load(smem_u32(&ctl->scale[st][0][lane * 4]), a.k_scale + sr / kPageSize * 4, 16, full);
           }
           pg = next;
         }
@@ -426,6 +434,11 @@ __global__ void __launch_bounds__(THREADS, 1) attn_chunk_kernel(const __grid_con
         tc_fence_before();
         mbar_arrive(bar(ctl->s_empty[t]));  // S of the next block may be computed
         const float* scales = nullptr;
+        if (INT8) {
+          const int kv = kvb + j, st = kv % VST;
+          if (!(ok = wait(ctl->v_full[st], (uint32_t)((kv / VST) & 1)))) break;
+          scales = ctl->scale[st][0];
+        }
         if (FP8) {
           const int kv = kvb + j, st = kv % VST;
           if (!(ok = wait(ctl->v_full[st], (uint32_t)((kv / VST) & 1)))) break;
@@ -463,6 +476,17 @@ __global__ void __launch_bounds__(THREADS, 1) attn_chunk_kernel(const __grid_con
 #pragma unroll 1
         while (true) {
           if (seek) {
+            float mx;
+            if (INT8) {  // page by page: each has a scale of its own
+              mx = -INFINITY;
+#pragma unroll
+              for (int c = 0; c < PAGES; ++c) {
+                float v = x[16 * c];
+#pragma unroll
+                for (int i = 1; i < 15; i += 2) v = fmax3f(v, x[16 * c + i], x[16 * c + i + 1]);
+                mx = fmaxf(mx, fmaxf(v, x[16 * c + 15]) * scales[4 * c]);
+              }
+            } else {
             float pm[8];
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
@@ -471,7 +495,8 @@ __global__ void __launch_bounds__(THREADS, 1) attn_chunk_kernel(const __grid_con
               for (int e = 8; e + 8 < BKV; e += 16) v = fmax3f(v, x[k + e], x[k + e + 8]);
               pm[k] = BKV % 16 ? v : fmaxf(v, x[k + BKV - 8]);
             }
-            const float mx = fmax3f(fmax3f(pm[0], pm[1], pm[2]), fmax3f(pm[3], pm[4], pm[5]), fmaxf(pm[6], pm[7])) * scale_log2;
+            mx = fmax3f(fmax3f(pm[0], pm[1], pm[2]), fmax3f(pm[3], pm[4], pm[5]), fmaxf(pm[6], pm[7])) * scale_log2;
+            }
             const bool move = mx > m;
             any = __any_sync(0xffffffffu, move);
             if (move) {
@@ -488,7 +513,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_chunk_kernel(const __grid_con
           for (int i = 0; i < BKV; i += 4) {
             float e[4];
 #pragma unroll
-            for (int k = 0; k < 4; k += 2) fma2(e + k, x + i + k, scale_log2, mneg);
+            for (int k = 0; k < 4; k += 2) fma2(e + k, x + i + k, INT8 ? scales[i / 16 * 4] : scale_log2, mneg);
 #pragma unroll
             for (int k = 0; k < 4; ++k) e[k] = ex2_approx(e[k]);
 #pragma unroll
@@ -499,6 +524,11 @@ __global__ void __launch_bounds__(THREADS, 1) attn_chunk_kernel(const __grid_con
               e[1] *= w.y;
               e[2] *= w.z;
               e[3] *= w.w;
+            }
+            if (INT8) {
+              const float w = scales[i / 16 * 4 + 1];
+#pragma unroll
+              for (int k = 0; k < 4; k += 2) mul2(e + k, w);
             }
             p[i / 2] = pack_bf16(e[0], e[1]);
             p[i / 2 + 1] = pack_bf16(e[2], e[3]);
@@ -528,7 +558,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_chunk_kernel(const __grid_con
       if (ok) ok = wait(ctl->pv_done[t], (uint32_t)((g - 1) & 1));
       if (ok) {
         tc_fence_after();
-        const float inv = (FP8 ? 1.f / kValueShift : 1.f) / l;
+        const float inv = (FP8 || INT8 ? 1.f / kValueShift : 1.f) / l;
         const int head = t ? I.hb : I.h;
         if (a.lse && qrow < I.n) a.lse[(size_t)head * a.ldl + I.seq0 + qrow] = (m + log2f(l)) * kLn2;
         bf16* dst = a.out + (size_t)(I.seq0 + min(qrow, I.n - 1)) * a.ldo + (size_t)head * D;
@@ -581,7 +611,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_chunk_kernel(const __grid_con
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
 }
 
-template <int D, bool FP8>
+template <int D, int KIND>
 cudaError_t launch_d(const ChunkArgs& a, const bf16* q, int ldq, int T, const bf16* k, const bf16* v, int num_sms,
                      cudaStream_t s) {
   constexpr int smem = smem_bytes<D>();
@@ -596,9 +626,9 @@ cudaError_t launch_d(const ChunkArgs& a, const bf16* q, int ldq, int T, const bf
       !tma_map_bf16_2d(&mt, a.v_tail, a.tail_seqs * kTailSlots * a.n_kv * kPageSize, D, D, 64, kPageSize, true))
     return cudaErrorNotSupported;
   static PerDeviceOnce once;
-  cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void*>(attn_chunk_kernel<D, FP8>), smem, once);
+  cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void*>(attn_chunk_kernel<D, KIND>), smem, once);
   if (e != cudaSuccess) return e;
-  return launch_pdl(attn_chunk_kernel<D, FP8>, dim3(a.num_items < num_sms ? a.num_items : num_sms), dim3(THREADS), smem,
+  return launch_pdl(attn_chunk_kernel<D, KIND>, dim3(a.num_items < num_sms ? a.num_items : num_sms), dim3(THREADS), smem,
                     s, mq, mk, mv, mt, a, 1.4426950408889634f / sqrtf((float)D));
 }
 
@@ -608,11 +638,15 @@ cudaError_t launch_attn_chunk(const ChunkArgs& a, const bf16* q, int ldq, int T,
                               int num_sms, cudaStream_t s) {
   if (a.num_items <= 0) return cudaSuccess;
   if (a.head_pairs && (a.n_q / a.n_kv) % 2) return cudaErrorNotSupported;
-  if (!a.k_scale != !a.v_scale) return cudaErrorNotSupported;
+  if (a.kind != kKvBf16 && !a.k_scale) return cudaErrorNotSupported;
   if (d_head == 128)
-    return a.k_scale ? launch_d<128, true>(a, q, ldq, T, k, v, num_sms, s) : launch_d<128, false>(a, q, ldq, T, k, v, num_sms, s);
+    return a.kind == kKvBf16 ? launch_d<128, kKvBf16>(a, q, ldq, T, k, v, num_sms, s)
+           : a.kind == kKvFp8 ? launch_d<128, kKvFp8>(a, q, ldq, T, k, v, num_sms, s)
+                              : launch_d<128, kKvInt8>(a, q, ldq, T, k, v, num_sms, s);
   if (d_head == 64)
-    return a.k_scale ? launch_d<64, true>(a, q, ldq, T, k, v, num_sms, s) : launch_d<64, false>(a, q, ldq, T, k, v, num_sms, s);
+    return a.kind == kKvBf16 ? launch_d<64, kKvBf16>(a, q, ldq, T, k, v, num_sms, s)
+           : a.kind == kKvFp8 ? launch_d<64, kKvFp8>(a, q, ldq, T, k, v, num_sms, s)
+                              : launch_d<64, kKvInt8>(a, q, ldq, T, k, v, num_sms, s);
   return cudaErrorNotSupported;
 }
 

@@ -48,12 +48,12 @@ namespace {
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr float kLag = 8.f;  // log2 headroom of the running maximum
 
-template <int D, bool FP8>
+template <int D, int KIND>
 struct Rg {
-  static constexpr int RB = D * (FP8 ? 1 : 2);        // bytes of a key's K or V row
+  static constexpr int RB = D * (KIND ? 1 : 2);       // bytes of a key's K or V row
   static constexpr int PAGE = kPageSize * RB;
-  static constexpr int STAGE = 2 * PAGE + (FP8 ? 2 * kPageSize * 4 : 0) + 16;  // K, V, scales, validity
-  static constexpr int WARPS = FP8 ? kRowsWarps8 : kRowsWarps;
+  static constexpr int STAGE = 2 * PAGE + (KIND == kKvFp8 ? 2 * kPageSize * 4 : 0) + 16;  // K, V, keys' scales; validity, page's scales
+  static constexpr int WARPS = KIND ? kRowsWarps8 : kRowsWarps;
   static constexpr int SLOTS = (227 * 1024) / (WARPS * STAGE) < 6 ? (227 * 1024) / (WARPS * STAGE) : 6;
   static constexpr int SMEM = WARPS * SLOTS * STAGE;
   static_assert(SLOTS >= 2 && SMEM <= 227 * 1024, "ring");
@@ -92,13 +92,40 @@ __device__ __forceinline__ void unpack4_bf16(uint32_t r, uint32_t& even, uint32_
   odd = x[1];
 }
 
+// Four int8 codes as two f16 pairs, the even and the odd bytes: code + 128 under the exponent of 1024 (whose
+// last bit is 1), less 1152.
+__device__ __forceinline__ void unpack4_int8(uint32_t r, uint32_t& even, uint32_t& odd) {
+  const uint32_t u = r ^ 0x80808080u, less = 0x64806480u;
+  uint32_t x[2] = {__byte_perm(u, 0x64646464u, 0x4240), __byte_perm(u, 0x64646464u, 0x4341)};
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const __half2 y = __hsub2(*reinterpret_cast<const __half2*>(&x[i]), *reinterpret_cast<const __half2*>(&less));
+    x[i] = *reinterpret_cast<const uint32_t*>(&y);
+  }
+  even = x[0];
+  odd = x[1];
+}
+// The same as bf16 pairs: 128 + the code's low seven bits, less 128 or, for negative codes, 256.
+__device__ __forceinline__ void unpack4_int8_bf16(uint32_t r, uint32_t& even, uint32_t& odd) {
+  uint32_t x[2] = {__byte_perm(r, 0x43434343u, 0x4240), __byte_perm(r, 0x43434343u, 0x4341)};
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t low = x[i] & 0xff7fff7fu, sign = x[i] & 0xff80ff80u;
+    const __nv_bfloat162 y = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&low), *reinterpret_cast<const __nv_bfloat162*>(&sign));
+    x[i] = *reinterpret_cast<const uint32_t*>(&y);
+  }
+  even = x[0];
+  odd = x[1];
+}
+
 // NT: columns in groups of 8.
-template <int D, bool FP8, int NT>
-__global__ void __launch_bounds__(Rg<D, FP8>::WARPS * 32, 1) attn_rows_kernel(
+template <int D, int KIND, int NT>
+__global__ void __launch_bounds__(Rg<D, KIND>::WARPS * 32, 1) attn_rows_kernel(
     const RowsArgs a, const __grid_constant__ InlineInts inl, const unsigned char* __restrict__ kpool,
     const unsigned char* __restrict__ vpool, const float* __restrict__ kscale, const float* __restrict__ vscale,
     float scale_log2) {
-  using S = Rg<D, FP8>;
+  using S = Rg<D, KIND>;
+  constexpr bool FP8 = KIND == kKvFp8, INT8 = KIND == kKvInt8, CODES = FP8 || INT8;
   extern __shared__ __align__(128) unsigned char smem[];
   griddep_launch_dependents();
   griddep_wait();
@@ -163,6 +190,8 @@ __global__ void __launch_bounds__(Rg<D, FP8>::WARPS * 32, 1) attn_rows_kernel(
       if (FP8 && lane < 8)  // 16 K scales, then 16 V scales
         cp_async16(smem_u32(st + 2 * S::PAGE + lane * 16), (lane < 4 ? kscale : vscale) + blk * kPageSize + (lane & 3) * 4,
                    ok ? 16 : 0);
+      if (INT8 && lane < 2)  // the page's K scale, its V scale
+        cp_async4(smem_u32(st + S::STAGE - 12 + lane * 4), (lane ? vscale : kscale) + blk, ok ? 4 : 0);
       if (lane == 0) {
         *reinterpret_cast<int*>(st + S::STAGE - 16) = ok;
         if (!ok) atomicOr(a.status, kStatusBadPage);
@@ -183,7 +212,7 @@ __global__ void __launch_bounds__(Rg<D, FP8>::WARPS * 32, 1) attn_rows_kernel(
   uint32_t qf[NT][D / 16][2];
   float o[NT][D / 16][4];           // O^T: 16 dimensions x 8 columns a tile
   float m[NT][2], l[NT][2];         // of columns 2 qd, 2 qd + 1
-  float qback[NT][2];               // FP8: what undoes their q's power of two
+  float qback[NT][2];               // codes: what undoes their q's power of two
   int qpos[NT][2];                  // their positions, -1: no such column
   int row0 = 0, cols = 0, pos_lo = 0, pos_hi = 0;
   long long cv = gw;
@@ -206,7 +235,7 @@ __global__ void __launch_bounds__(Rg<D, FP8>::WARPS * 32, 1) attn_rows_kernel(
         const int cb = t * 8 + g0;
         const bool in = cb < cols;
         const bf16* src = a.q + (size_t)(row0 + (in ? cb / G : 0)) * a.ldq + (cg.kvh * G + (in ? cb % G : 0)) * D;
-        if (FP8) {  // f16, dims 16 ks + 4 qd + {0, 2} and {1, 3}: the order in which K's codes arrive
+        if (CODES) {  // f16, dims 16 ks + 4 qd + {0, 2} and {1, 3}: the order in which K's codes arrive
           float back;
           load_q_f16<D, true>(src, in, qd, qf[t], back);
 #pragma unroll
@@ -241,7 +270,7 @@ __global__ void __launch_bounds__(Rg<D, FP8>::WARPS * 32, 1) attn_rows_kernel(
 #pragma unroll
         for (int e = 0; e < 4; ++e) s[t][c][e] = 0.f;
     const int krow = (lane & 7) + ((lane >> 3) & 1) * 8;
-    if (FP8) {
+    if (CODES) {
 #pragma unroll
       for (int ks = 0; ks < D / 16; ks += 2) {
         uint32_t r[4];  // keys 0-7 and 8-15 of chunk ks, then of chunk ks + 1
@@ -249,8 +278,13 @@ __global__ void __launch_bounds__(Rg<D, FP8>::WARPS * 32, 1) attn_rows_kernel(
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           uint32_t ka[4];
-          unpack4(r[2 * h], ka[0], ka[2]);
-          unpack4(r[2 * h + 1], ka[1], ka[3]);
+          if (INT8) {
+            unpack4_int8(r[2 * h], ka[0], ka[2]);
+            unpack4_int8(r[2 * h + 1], ka[1], ka[3]);
+          } else {
+            unpack4(r[2 * h], ka[0], ka[2]);
+            unpack4(r[2 * h + 1], ka[1], ka[3]);
+          }
 #pragma unroll
           for (int t = 0; t < NT; ++t) mma_f16_16816(s[t][h], ka, qf[t][ks + h]);
         }
@@ -266,8 +300,9 @@ __global__ void __launch_bounds__(Rg<D, FP8>::WARPS * 32, 1) attn_rows_kernel(
     }
     const int key0 = (cg.p0 + cp) * kPageSize;
     const float* sc = reinterpret_cast<const float*>(st + 2 * S::PAGE);  // FP8: 16 key, 16 value scales
-    const float c_lo = FP8 ? kCodeScale * scale_log2 * sc[g0] : scale_log2;
-    const float c_hi = FP8 ? kCodeScale * scale_log2 * sc[g0 + 8] : scale_log2;
+    const float* page_sc = reinterpret_cast<const float*>(st + S::STAGE - 12);  // int8: the page's
+    const float c_lo = FP8 ? kCodeScale * scale_log2 * sc[g0] : INT8 ? scale_log2 * page_sc[0] : scale_log2;
+    const float c_hi = FP8 ? kCodeScale * scale_log2 * sc[g0 + 8] : c_lo;
     // every key of the page visible to every column
     const bool inside = *reinterpret_cast<const int*>(st + S::STAGE - 16) && key0 >= cg.k0 && key0 + kPageSize <= cg.k1 &&
                         key0 + kPageSize - 1 <= pos_lo &&
@@ -276,7 +311,7 @@ __global__ void __launch_bounds__(Rg<D, FP8>::WARPS * 32, 1) attn_rows_kernel(
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) z[t][e] = (s[t][0][e] + s[t][1][e]) * ((e < 2 ? c_lo : c_hi) * (FP8 ? qback[t][e & 1] : 1.f));
+      for (int e = 0; e < 4; ++e) z[t][e] = (s[t][0][e] + s[t][1][e]) * ((e < 2 ? c_lo : c_hi) * (CODES ? qback[t][e & 1] : 1.f));
     if (!inside) {
       const bool ok = *reinterpret_cast<const int*>(st + S::STAGE - 16);
 #pragma unroll
@@ -292,6 +327,7 @@ __global__ void __launch_bounds__(Rg<D, FP8>::WARPS * 32, 1) attn_rows_kernel(
       v_lo = key0 + g0 >= cg.k0 && key0 + g0 < cg.k1 ? kValueShift * sc[kPageSize + g0] : 0.f;
       v_hi = key0 + g0 + 8 >= cg.k0 && key0 + g0 + 8 < cg.k1 ? kValueShift * sc[kPageSize + g0 + 8] : 0.f;
     }
+    if (INT8) v_lo = v_hi = kValueShift * page_sc[1];
     bool move = false;
 #pragma unroll
     for (int t = 0; t < NT; ++t)
@@ -337,7 +373,7 @@ __global__ void __launch_bounds__(Rg<D, FP8>::WARPS * 32, 1) attn_rows_kernel(
     // O^T += V^T P^T. bf16: tile i holds dims 16 i + row. FP8: ldmatrix.trans yields two keys x two
     // neighbouring dims, so rows 0-7 are the even dims of the chunk and rows 8-15 the odd ones
     const unsigned char* vb = st + S::PAGE;
-    if (FP8) {
+    if (CODES) {
 #pragma unroll
       for (int c = 0; c < D / 16; c += 2) {
         uint32_t r[4];  // keys 0-7 and 8-15 of chunk c, then of chunk c + 1
@@ -345,8 +381,13 @@ __global__ void __launch_bounds__(Rg<D, FP8>::WARPS * 32, 1) attn_rows_kernel(
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           uint32_t va[4];
-          unpack4_bf16(r[2 * h], va[0], va[1]);
-          unpack4_bf16(r[2 * h + 1], va[2], va[3]);
+          if (INT8) {
+            unpack4_int8_bf16(r[2 * h], va[0], va[1]);
+            unpack4_int8_bf16(r[2 * h + 1], va[2], va[3]);
+          } else {
+            unpack4_bf16(r[2 * h], va[0], va[1]);
+            unpack4_bf16(r[2 * h + 1], va[2], va[3]);
+          }
 #pragma unroll
           for (int t = 0; t < NT; ++t) {
             mma_bf16_16816(o[t][c + h], va, ph[t]);
@@ -382,15 +423,15 @@ __global__ void __launch_bounds__(Rg<D, FP8>::WARPS * 32, 1) attn_rows_kernel(
           for (int o2 = 4; o2 <= 16; o2 <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o2);
           const int col = t * 8 + 2 * qd + e;
           if (col >= cols) continue;
-          // dims this thread holds of tile i: bf16 16 i + g0 and + 8; FP8 16 i + 2 g0 and + 1
+          // dims this thread holds of tile i: bf16 16 i + g0 and + 8; codes 16 i + 2 g0 and + 1
           if (whole) {
             const int row = row0 + col / G, h = cg.kvh * G + col % G;
-            const float f = (FP8 ? 1.f / kValueShift : 1.f) / sum;
+            const float f = (CODES ? 1.f / kValueShift : 1.f) / sum;
             if (a.lse && g0 == 0) a.lse[(size_t)h * a.ldl + row] = (m[t][e] + log2f(sum)) * kLn2;
             bf16* dst = a.out + (size_t)row * a.ldo + (size_t)h * D;
 #pragma unroll
             for (int i = 0; i < D / 16; ++i) {
-              if (FP8) {
+              if (CODES) {
                 *reinterpret_cast<uint32_t*>(dst + 16 * i + 2 * g0) = pack_bf16(o[t][i][e] * f, o[t][i][2 + e] * f);
               } else {
                 dst[16 * i + g0] = __float2bfloat16_rn(o[t][i][e] * f);
@@ -402,7 +443,7 @@ __global__ void __launch_bounds__(Rg<D, FP8>::WARPS * 32, 1) attn_rows_kernel(
             if (g0 == 0) *reinterpret_cast<float2*>(pp) = make_float2(m[t][e], sum);
 #pragma unroll
             for (int i = 0; i < D / 16; ++i) {
-              if (FP8) {
+              if (CODES) {
                 *reinterpret_cast<float2*>(pp + 4 + 16 * i + 2 * g0) = make_float2(o[t][i][e] * (1.f / kValueShift), o[t][i][2 + e] * (1.f / kValueShift));
               } else {
                 pp[4 + 16 * i + g0] = o[t][i][e];
@@ -488,15 +529,15 @@ __global__ void __launch_bounds__(MERGE_WARPS * 32) attn_rows_merge(const RowsAr
   if (a.lse && lane == 0) a.lse[(size_t)h * a.ldl + row] = (m + log2f(den)) * kLn2;
 }
 
-template <int D, bool FP8, int NT>
+template <int D, int KIND, int NT>
 cudaError_t launch_nt(const RowsArgs& a, const InlineInts& inl, const void* k, const void* v, const float* ks, const float* vs, int num_items,
                       int num_sms, cudaStream_t s) {
-  using S = Rg<D, FP8>;
+  using S = Rg<D, KIND>;
   static PerDeviceOnce once;
-  cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void*>(attn_rows_kernel<D, FP8, NT>), S::SMEM, once);
+  cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void*>(attn_rows_kernel<D, KIND, NT>), S::SMEM, once);
   if (e != cudaSuccess) return e;
   const long long total = (long long)a.num_units * a.n_kv;
-  e = launch_pdl(attn_rows_kernel<D, FP8, NT>, dim3((unsigned)(total < num_sms ? total : num_sms)), dim3(S::WARPS * 32),
+  e = launch_pdl(attn_rows_kernel<D, KIND, NT>, dim3((unsigned)(total < num_sms ? total : num_sms)), dim3(S::WARPS * 32),
                  S::SMEM, s, a, inl, static_cast<const unsigned char*>(k), static_cast<const unsigned char*>(v), ks, vs,
                  1.4426950408889634f / sqrtf((float)D));
   if (e != cudaSuccess || a.num_units == num_items) return e;
@@ -505,24 +546,28 @@ cudaError_t launch_nt(const RowsArgs& a, const InlineInts& inl, const void* k, c
                     0, s, a, inl, num_items);
 }
 
-template <int D, bool FP8>
+template <int D, int KIND>
 cudaError_t launch_cols(const RowsArgs& a, const InlineInts& inl, const void* k, const void* v, const float* ks, const float* vs, int num_items,
                         int num_sms, cudaStream_t s) {
-  return a.max_cols <= 8 ? launch_nt<D, FP8, 1>(a, inl, k, v, ks, vs, num_items, num_sms, s)
-                         : launch_nt<D, FP8, 2>(a, inl, k, v, ks, vs, num_items, num_sms, s);
+  return a.max_cols <= 8 ? launch_nt<D, KIND, 1>(a, inl, k, v, ks, vs, num_items, num_sms, s)
+                         : launch_nt<D, KIND, 2>(a, inl, k, v, ks, vs, num_items, num_sms, s);
+}
+
+template <int D>
+cudaError_t launch_d(const RowsArgs& a, int kind, const InlineInts& inl, const void* k, const void* v, const float* ks, const float* vs, int num_items,
+                     int num_sms, cudaStream_t s) {
+  return kind == kKvBf16 ? launch_cols<D, kKvBf16>(a, inl, k, v, ks, vs, num_items, num_sms, s)
+         : kind == kKvFp8 ? launch_cols<D, kKvFp8>(a, inl, k, v, ks, vs, num_items, num_sms, s)
+                          : launch_cols<D, kKvInt8>(a, inl, k, v, ks, vs, num_items, num_sms, s);
 }
 
 }  // namespace
 
-cudaError_t launch_attn_rows(const RowsArgs& a, const InlineInts& inl, const void* k, const void* v, const float* ks, const float* vs, int d_head,
+cudaError_t launch_attn_rows(const RowsArgs& a, int kind, const InlineInts& inl, const void* k, const void* v, const float* ks, const float* vs, int d_head,
                              int num_items, int num_sms, cudaStream_t s) {
-  if (a.max_cols > kRowsCols || (!ks != !vs)) return cudaErrorNotSupported;
-  if (d_head == 128)
-    return ks ? launch_cols<128, true>(a, inl, k, v, ks, vs, num_items, num_sms, s)
-              : launch_cols<128, false>(a, inl, k, v, ks, vs, num_items, num_sms, s);
-  if (d_head == 64)
-    return ks ? launch_cols<64, true>(a, inl, k, v, ks, vs, num_items, num_sms, s)
-              : launch_cols<64, false>(a, inl, k, v, ks, vs, num_items, num_sms, s);
+  if (a.max_cols > kRowsCols || (kind != kKvBf16 && (!ks || !vs))) return cudaErrorNotSupported;
+  if (d_head == 128) return launch_d<128>(a, kind, inl, k, v, ks, vs, num_items, num_sms, s);
+  if (d_head == 64) return launch_d<64>(a, kind, inl, k, v, ks, vs, num_items, num_sms, s);
   return cudaErrorNotSupported;
 }
 

@@ -93,23 +93,25 @@ __host__ __device__ __forceinline__ int pair_half(const EpiParams& p) {
 // Column of the lo member of pair index `u` (0 <= u < ncols/2) in a block-aligned range.
 __device__ __forceinline__ int pair_lo(int u, int half) { return (u / half) * (2 * half) + (u % half); }
 
-// Rotates (a, b) by pos times the pair's frequency. Past the table the angle is a whole number of
+// (cos, sin) of pos times pair i's frequency, of `half` pairs. Past the table the angle is a whole number of
 // 2^-64 turns, whose product with pos wraps at a full turn: exact but for the frequency's own rounding
 // (2^-53 of it, 2^-22 radians at position 2^30). A float32 product is off by pos 2^-24 radians.
-__device__ __forceinline__ void rope_rotate(const EpiParams& p, int pos, int i, float& a, float& b) {
+__device__ __forceinline__ float2 rope_angle(const float2* tab, int len, const unsigned long long* turns, int half, int pos,
+                                             int i) {
+  if (pos < len) return tab[(size_t)pos * half + i];
+  const int turn = (int)((turns[i] * (unsigned long long)pos) >> 32);  // 2^-32 turns in [-1/2, 1/2)
   float c, s;
-  if (pos < p.rope_len) {
-    float2 cs = p.rope_tab[(size_t)pos * (p.d_head >> 1) + i];
-    c = cs.x;
-    s = cs.y;
-  } else {
-    const int turn = (int)((p.rope_turn[i] * (unsigned long long)pos) >> 32);  // 2^-32 turns in [-1/2, 1/2)
-    sincospif((float)turn * 4.6566128730773926e-10f, &s, &c);                  // 2^-31: half turns
-  }
-  float a2 = a * c - b * s;
-  float b2 = b * c + a * s;
+  sincospif((float)turn * 4.6566128730773926e-10f, &s, &c);            // 2^-31: half turns
+  return make_float2(c, s);
+}
+__device__ __forceinline__ void rope_turn_pair(float2 cs, float& a, float& b) {
+  const float a2 = a * cs.x - b * cs.y;
+  const float b2 = b * cs.x + a * cs.y;
   a = a2;
   b = b2;
+}
+__device__ __forceinline__ void rope_rotate(const EpiParams& p, int pos, int i, float& a, float& b) {
+  rope_turn_pair(rope_angle(p.rope_tab, p.rope_len, p.rope_turn, p.d_head >> 1, pos, i), a, b);
 }
 
 __device__ __forceinline__ void paged_store_pair(bf16* pool, int slot, int n_kv, int head, int d_head,
@@ -471,6 +473,9 @@ __device__ __forceinline__ uint32_t smem_u32(const void* p) {
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int src_bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(src_bytes));
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, int src_bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;\n" ::"r"(dst), "l"(src), "r"(src_bytes));
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;\n" ::); }
 template <int N>

@@ -42,19 +42,22 @@ int check_kv(const swiftkv_model* m, const swiftkv_kv_pages* kv) {
   if (kv->num_pages < 1 || kv->max_pages_per_seq < 1) return fail(SWIFTKV_EINVAL, "empty page pool");
   for (int c = 0; c < m->C; ++c)
     if (!kv->k_pool[c] || !kv->v_pool[c]) return fail(SWIFTKV_EINVAL, "null pool pointer for cache %d", c);
-  if (kv->kv_dtype != 0 && kv->kv_dtype != 1) return fail(SWIFTKV_EINVAL, "kv_dtype %d", kv->kv_dtype);
-  if (kv->kv_dtype == 1) {
-    if (!kv->k_scale || !kv->v_scale) return fail(SWIFTKV_EINVAL, "fp8 cache without scale pools");
+  if (kv->kv_dtype < 0 || kv->kv_dtype > 2) return fail(SWIFTKV_EINVAL, "kv_dtype %d", kv->kv_dtype);
+  if (kv->kv_dtype != 0) {
+    const char* name = kv->kv_dtype == 1 ? "fp8" : "int8";
+    if (!kv->k_scale || !kv->v_scale) return fail(SWIFTKV_EINVAL, "%s cache without scale pools", name);
     for (int c = 0; c < m->C; ++c)
       if (!kv->k_scale[c] || !kv->v_scale[c]) return fail(SWIFTKV_EINVAL, "null scale pool for cache %d", c);
     if (m->cfg.n_q / m->cfg.n_kv > 8)
-      return fail(SWIFTKV_EUNSUPPORTED, "fp8 cache needs at most 8 query heads per KV head");
+      return fail(SWIFTKV_EUNSUPPORTED, "%s cache needs at most 8 query heads per KV head", name);
   }
   if (reinterpret_cast<uintptr_t>(kv->block_table) & 3) return fail(SWIFTKV_EINVAL, "misaligned block table");
   for (int c = 0; c < m->C; ++c) {  // the kernels copy 16 bytes at a time
     uintptr_t bits = reinterpret_cast<uintptr_t>(kv->k_pool[c]) | reinterpret_cast<uintptr_t>(kv->v_pool[c]);
     if (kv->kv_dtype == 1) bits |= reinterpret_cast<uintptr_t>(kv->k_scale[c]) | reinterpret_cast<uintptr_t>(kv->v_scale[c]);
     if (bits & 15) return fail(SWIFTKV_EINVAL, "pools of cache %d are not 16-byte aligned", c);
+    if (kv->kv_dtype == 2 && ((reinterpret_cast<uintptr_t>(kv->k_scale[c]) | reinterpret_cast<uintptr_t>(kv->v_scale[c])) & 3))
+      return fail(SWIFTKV_EINVAL, "scale pools of cache %d are not 4-byte aligned", c);
   }
   return SWIFTKV_OK;
 }
@@ -63,13 +66,11 @@ int check_kv(const swiftkv_model* m, const swiftkv_kv_pages* kv) {
 
 namespace {
 
-constexpr int kRopeLen = 32768;
-
 struct Workspace {
   int *cu, *tiles, *pools, *positions, *slots, *last_idx, *last_pos, *tokens, *ctx, *srow, *sseq, *dint;
   float *x, *xt, *part, *logits, *dpart;
   bf16 *u, *q, *attn, *h, *ut, *qt, *at, *ht;
-  bf16 *kv_stage;         // FP8 cache: staged K/V rows before quantization
+  bf16 *kv_stage;         // 8-bit caches: staged K/V rows before quantization
   bf16 *exp_k, *exp_v;    // FP8 cache: bf16 expansion of one cache for the prompt-tile attention
   int* deq_items;         // FP8 cache: (sequence, page) pairs of cached prefixes to expand
   float *ss_attn, *ss_mlp;  // fused RMSNorm: per-256-column sums of squares of x after the O / down GEMM
@@ -262,11 +263,12 @@ struct Ctx {
   SplitPlan sp_short{};      // key-split plan of those rows
   SplitPlan sp_rows{};       // key-split plan of the single-row attention (tail / decode rows)
   bool fp8 = false;          // the caches hold e4m3 codes + per-token scales
+  bool int8 = false;         // the caches hold int8 codes + a scale for each page and head (serving is set)
   float* const* ks_dev = nullptr;  // device arrays of scale pools
   float* const* vs_dev = nullptr;
   bool expand = false;       // FP8: prompt tiles read a bf16 expansion of the layer's cache
   int n_deq = 0;             // FP8: prefix pages to expand per full layer (w.deq_items)
-  const struct ServingPlan* serving = nullptr;  // window, score pools or position offsets: attention by its plans
+  const struct ServingPlan* serving = nullptr;  // window, score pools, position offsets or an int8 cache: attention by its plans
   // RMSNorm fused into the prompt rows' tcgen05 GEMMs: the O and down epilogues leave
   // bf16(gamma * x) in w.u (gamma: the next norm's gain) and per-tile sums of squares of x in
   // w.ss_attn / w.ss_mlp, which the next GEMM's epilogue turns into the row's 1/rms; no
@@ -291,6 +293,7 @@ struct ServingPlan {
                  bool with_last) {
     has_last = with_last;
     scores = !m->score_pools.empty();
+    if (scores && kv->kv_dtype == kKvInt8) return fail(SWIFTKV_EUNSUPPORTED, "attention weights over an int8 cache");
     if (scores && kv->num_pages > m->score_pages)
       return fail(SWIFTKV_EINVAL, "the caches have %d pages, the score pools %d", kv->num_pages, m->score_pages);
     RET(rows.make(m, cu, ctx, P, kv, m->window, m->sinks));
@@ -353,8 +356,9 @@ int upload_split(Ctx& x, const HostSplit& h, int* dst, SplitPlan* p) {
 }
 
 // Bytes of one key's K and V vectors over every KV head in a cache (codes + scales for FP8).
-double kv_bytes_per_key(const swiftkv_model* m, bool fp8) {
-  return 2.0 * m->cfg.n_kv * (fp8 ? m->cfg.d_head + 4.0 : 2.0 * m->cfg.d_head);
+double kv_bytes_per_key(const swiftkv_model* m, int kind) {
+  const double d = m->cfg.d_head;
+  return 2.0 * m->cfg.n_kv * (kind == kKvFp8 ? d + 4.0 : kind == kKvInt8 ? d + 4.0 / kPageSize : 2.0 * d);
 }
 
 cudaEvent_t prof_event(swiftkv_model* m) {
@@ -512,13 +516,13 @@ int layer_rest(Ctx& x, int j, int M, float* xres, bf16* qb, bf16* ab, bf16* ub, 
     float* lse = sv.scores ? (is_last ? sv.lse_last : sv.lse_rows) : nullptr;
     {
       Prof pr(x.m, x.s, prefill ? "attn_prefill" : "attn_decode", ap.kernels(), 4.0 * c.n_q * c.d_head * ap.pairs,
-              ap.keys * kv_bytes_per_key(m, x.fp8) + 2.0 * M * m->Nq * 2);
+              ap.keys * kv_bytes_per_key(m, x.kv->kv_dtype) + 2.0 * M * m->Nq * 2);
       RET(ap.run(m, x.kv, cidx, qb, m->Nq, ab, m->Nq, lse, M, x.s));
     }
     if (sv.scores) {
       const WeightsPlan& wp = is_last ? sv.last_w : sv.rows_w;
       Prof pr(x.m, x.s, "attn_weights", wp.kernels(), 2.0 * c.n_q * c.d_head * wp.pairs,
-              wp.keys * (kv_bytes_per_key(m, x.fp8) / 2 + 4.0 * c.n_kv) + 1.0 * M * m->Nq * 2);
+              wp.keys * (kv_bytes_per_key(m, x.kv->kv_dtype) / 2 + 4.0 * c.n_kv) + 1.0 * M * m->Nq * 2);
       RET(wp.run(m, x.kv, cidx, qb, m->Nq, lse, M, m->score_decay, m->score_pools[cidx], x.s));
     }
     e = cudaSuccess;
@@ -577,6 +581,32 @@ int quantize(Ctx& x, int M, const int* slots, int groups, int cache_base, int ld
   return SWIFTKV_OK;
 }
 
+// Int8 cache: staged K/V rows of `groups` consecutive caches from cache_base -> pages of the call's rows.
+int append_staged(Ctx& x, int groups, int cache_base, int ld) {
+  swiftkv_model* m = x.m;
+  const AttendPlan& p = x.serving->rows;
+  AppendArgs a = {};
+  a.k = x.w.kv_stage;
+  a.v = x.w.kv_stage + m->Nkv;
+  a.ldk = a.ldv = ld;
+  a.k_step = a.v_step = 2 * m->Nkv;
+  a.caches = groups;
+  a.P = p.b.P;
+  a.T = p.b.T;
+  a.lists = p.dev;
+  a.o_cu = p.o_cu;
+  a.o_ctx = p.o_ctx;
+  a.o_off = -1;
+  a.pools = reinterpret_cast<const long long*>(x.w.pools) + cache_base;
+  a.pool_step = m->C;
+  a.bt = x.kv->block_table;
+  a.max_pages = x.kv->max_pages_per_seq;
+  a.num_pages = x.kv->num_pages;
+  Prof pr(m, x.s, "kv_quantize", 1, 0.0, (double)a.T * groups * 2 * m->Nkv * 3);
+  CK(launch_append_on(m, a, kKvInt8, inline_of(p.ints, p.dev), x.s));
+  return SWIFTKV_OK;
+}
+
 // Epilogue of layer j's Q/K/V (full layer: cache_base = j) or Q only (skipped layer)
 // projection with RoPE.
 EpiParams qkv_epi(Ctx& x, int j, int M, bf16* qb, const int* pos, const int* slots) {
@@ -598,6 +628,9 @@ EpiParams qkv_epi(Ctx& x, int j, int M, bf16* qb, const int* pos, const int* slo
       e.kv_stage = x.w.kv_stage;
       e.kv_stage_ld = 2 * m->Nkv;
     }
+  } else if (full && x.int8) {
+    e.kv_stage = x.w.kv_stage;
+    e.kv_stage_ld = 2 * m->Nkv;
   }
   return e;
 }
@@ -610,6 +643,7 @@ int qkv(Ctx& x, int j, int M, const bf16* ub, bf16* qb, const int* pos, const in
   if (fused) fuse_input(x, e, x.w.ss_mlp);
   RET(gemm(x, gname, ub, m->cfg.d, m->layers[j].wqkv, m->cfg.d, e, 2.0 * M * e.N * m->cfg.d));
   if (full && x.fp8 && !fp8_in_epilogue(x, M)) RET(quantize(x, M, slots, 1, j, 2 * m->Nkv, x.expand));
+  if (full && x.int8) RET(append_staged(x, 1, j, 2 * m->Nkv));
   return SWIFTKV_OK;
 }
 
@@ -706,12 +740,13 @@ int wide_kv(Ctx& x, int M, const float* xres, bf16* ub, const int* pos, const in
   const bool in_epi = fp8_in_epilogue(x, M);
   if (x.fp8 && in_epi) {
     set_fp8_epilogue(x, e, false);  // skipped caches are read only by the single-row attention
-  } else if (x.fp8) {
+  } else if (x.fp8 || x.int8) {
     e.kv_stage = x.w.kv_stage;
     e.kv_stage_ld = m->Nwide;
   }
   RET(gemm(x, "gemm_wide_kv", ub, m->cfg.d, m->w_wide, m->cfg.d, e, 2.0 * M * m->Nwide * m->cfg.d));
   if (x.fp8 && !in_epi) RET(quantize(x, M, slots, m->G, m->l, m->Nwide, false));
+  if (x.int8) RET(append_staged(x, m->G, m->l, m->Nwide));
   return SWIFTKV_OK;
 }
 
@@ -725,12 +760,12 @@ int check_ready(const swiftkv_model* m) {
 
 int upload_pools(Ctx& x) {
   const int C = x.m->C;
-  const int n = x.fp8 ? 4 * C : 2 * C;
+  const int n = x.fp8 || x.int8 ? 4 * C : 2 * C;
   std::vector<void*> ptrs(n);
   for (int c = 0; c < C; ++c) {
     ptrs[c] = x.kv->k_pool[c];
     ptrs[C + c] = x.kv->v_pool[c];
-    if (x.fp8) {
+    if (x.fp8 || x.int8) {
       ptrs[2 * C + c] = x.kv->k_scale[c];
       ptrs[3 * C + c] = x.kv->v_scale[c];
     }
@@ -1127,9 +1162,10 @@ static int prefill_impl(swiftkv_model* m, const int32_t* tokens, const int32_t* 
   x.tc_attn = tc_attn;
   // FP8 cache: prompt tiles attend over a bf16 expansion of the layer's cache (chunk rows
   // written by the quantize pass, cached prefixes expanded page by page before each layer)
-  x.fp8 = kv->kv_dtype == 1;
+  x.fp8 = kv->kv_dtype == kKvFp8;
+  x.int8 = kv->kv_dtype == kKvInt8;
   ServingPlan serving;
-  if (m->window > 0 || !m->score_pools.empty() || pos_off) {
+  if (m->window > 0 || !m->score_pools.empty() || pos_off || x.int8) {
     RET(serving.make(m, cu, ctx, P, kv, m->l < m->cfg.L));
     Arena size, arena;
     serving.place(m, pos_off != nullptr, &size);
@@ -1150,7 +1186,7 @@ static int prefill_impl(swiftkv_model* m, const int32_t* tokens, const int32_t* 
       }
     }
   x.n_deq = (int)deq.size() / 2;
-  const size_t stage_elems = x.fp8 ? (size_t)T * std::max(2 * m->Nkv, m->Nwide) : 0;
+  const size_t stage_elems = x.fp8 || x.int8 ? (size_t)T * std::max(2 * m->Nkv, m->Nwide) : 0;
   const size_t exp_elems = x.expand ? (size_t)kv->num_pages * m->cfg.n_kv * kPageSize * m->cfg.d_head : 0;
   size_t part = std::max(skinny_part_bytes(m, P), skinny_part_bytes(m, T));
   std::vector<int> nk_short, nk_tail(P);
@@ -1178,7 +1214,7 @@ static int prefill_impl(swiftkv_model* m, const int32_t* tokens, const int32_t* 
     attn_flops += 4.0 * m->cfg.n_q * m->cfg.d_head * (n * c0 + n * (n + 1) / 2);
     tail_keys += c0 + n;
   }
-  const double kv_key_bytes = kv_bytes_per_key(m, x.fp8);
+  const double kv_key_bytes = kv_bytes_per_key(m, x.kv->kv_dtype);
   const double attn_bytes = tail_keys * kv_key_bytes + 2.0 * T * m->Nq * 2;
   const double tail_bytes = tail_keys * kv_key_bytes + 2.0 * P * m->Nq * 2;
   {
@@ -1348,9 +1384,10 @@ int swiftkv_decode_step(swiftkv_model* m, const int32_t* tokens, const int32_t* 
     dec_keys += nk[b];
   }
   const HostSplit hs = make_split(nk);
-  x.fp8 = kv->kv_dtype == 1;
+  x.fp8 = kv->kv_dtype == kKvFp8;
+  x.int8 = kv->kv_dtype == kKvInt8;
   ServingPlan serving;
-  if (m->window > 0 || !m->score_pools.empty()) {
+  if (m->window > 0 || !m->score_pools.empty() || x.int8) {
     std::vector<int> one(B + 1);
     for (int b = 0; b <= B; ++b) one[b] = b;
     RET(serving.make(m, one.data(), seq_lens, B, kv, false));
@@ -1363,7 +1400,7 @@ int swiftkv_decode_step(swiftkv_model* m, const int32_t* tokens, const int32_t* 
   }
   RET(ensure_workspace(m, B, B, m->C, 1, skinny_part_bytes(m, B), &x.w, hs.ints(),
                        split_part_floats(hs.num_units(), m->cfg.n_q, m->cfg.d_head),
-                       x.fp8 ? (size_t)B * std::max(2 * m->Nkv, m->Nwide) : 0));
+                       x.fp8 || x.int8 ? (size_t)B * std::max(2 * m->Nkv, m->Nwide) : 0));
   CK(upload_ints(x.w.cu, seq_lens, B, s));
   RET(upload_pools(x));
   RET(upload_split(x, hs, x.w.dint, &x.sp_rows));
@@ -1381,7 +1418,7 @@ int swiftkv_decode_step(swiftkv_model* m, const int32_t* tokens, const int32_t* 
     }
     if (!q_ready) RET(qkv(x, j, B, x.w.u, x.w.q, x.w.positions, x.w.slots, "gemm_decode"));
     RET(layer_rest(x, j, B, x.w.x, x.w.q, x.w.attn, x.w.u, x.w.h, false, x.w.positions, 0, "gemm_decode",
-                   4.0 * c.n_q * c.d_head * dec_keys, dec_keys * kv_bytes_per_key(m, x.fp8) + 2.0 * B * m->Nq * 2,
+                   4.0 * c.n_q * c.d_head * dec_keys, dec_keys * kv_bytes_per_key(m, x.kv->kv_dtype) + 2.0 * B * m->Nq * 2,
                    true));
     // the chained launch also runs the next layer's input norm and Q/K/V projection, except
     // before the SwiftKV boundary (the wide KV GEMM normalises x_l itself)
@@ -1398,8 +1435,9 @@ int swiftkv_decode_step(swiftkv_model* m, const int32_t* tokens, const int32_t* 
       RET(norm(x, x.w.x, nullptr, B, g_next, x.w.u, nullptr));
     } else {
       RET(r);
-      // K/V of the next full layer went to the staging rows: quantize them into the FP8 cache
+      // K/V of the next full layer went to the staging rows: quantize them into the cache
       if (q_ready && x.fp8 && j + 1 < m->l) RET(quantize(x, B, x.w.slots, 1, j + 1, 2 * m->Nkv, x.expand));
+      if (q_ready && x.int8 && j + 1 < m->l) RET(append_staged(x, 1, j + 1, 2 * m->Nkv));
     }
   }
   EpiParams el = epi_base(x, EPI_STORE_F32, B, c.vocab);

@@ -88,6 +88,8 @@ struct swiftkv_model {
 
 namespace skv {
 
+constexpr int kRopeLen = 32768;  // positions of rope_tab
+
 // f() for a C entry: host lists that do not fit the memory become an error code.
 template <typename F>
 int guarded(F f) {

@@ -368,7 +368,22 @@ __global__ void kv_dequant_pages_kernel(const int* __restrict__ items, const int
   }
 }
 
+// 16 int8 codes as bf16 values (exact).
+__device__ __forceinline__ void expand_int8x16(uint4 raw, uint32_t* o) {
+  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      // 128 + the low seven bits, less 128 or, for negative codes, 256
+      const uint32_t x = __byte_perm(w[i], 0x43434343u, h ? 0x4342 : 0x4140), low = x & 0xff7fff7fu, sign = x & 0xff80ff80u;
+      const __nv_bfloat162 y = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&low), *reinterpret_cast<const __nv_bfloat162*>(&sign));
+      o[2 * i + h] = *reinterpret_cast<const uint32_t*>(&y);
+    }
+}
+
 // Item i = (sequence, page index) becomes page i of the expansion.
+template <bool INT8>
 __global__ void kv_expand_seen_kernel(const int* __restrict__ items, const KVPool8 src, int max_pages, int num_pages,
                                       const int* __restrict__ cu, const int* __restrict__ ctx, int n_kv, int dh,
                                       int window, int sinks, const KVExpansion dst, int* status) {
@@ -387,11 +402,23 @@ __global__ void kv_expand_seen_kernel(const int* __restrict__ items, const KVPoo
     if (kvsel && !dst.v) break;  // K alone
     const int e = (c - kvsel * (per_page / 16)) * 16;
     uint32_t o[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    if (ok && t.seen(pidx * kPageSize + e / dh % kPageSize))
-      expand_codes16(*reinterpret_cast<const uint4*>((kvsel ? src.v : src.k) + from + e), o);
+    if (ok && t.seen(pidx * kPageSize + e / dh % kPageSize)) {
+      const uint4 codes = *reinterpret_cast<const uint4*>((kvsel ? src.v : src.k) + from + e);
+      if (INT8) expand_int8x16(codes, o);
+      else expand_codes16(codes, o);
+    }
     bf16* d = (kvsel ? dst.v : dst.k) + to + e;
     *reinterpret_cast<uint4*>(d) = make_uint4(o[0], o[1], o[2], o[3]);
     *reinterpret_cast<uint4*>(d + 8) = make_uint4(o[4], o[5], o[6], o[7]);
+  }
+  if (INT8) {
+    // no scale is 0: it would turn scores of -inf into NaN (where the page's is, all codes are 0 and any scale does)
+    for (int h = threadIdx.x; h < n_kv; h += blockDim.x) {
+      const float ks = ok ? src.k_scale[(size_t)page * n_kv + h] : 0.f, vs = ok ? src.v_scale[(size_t)page * n_kv + h] : 0.f;
+      reinterpret_cast<float4*>(dst.k_scale)[(size_t)i * n_kv + h] =
+          make_float4(fmaxf(ks * (1.4426950408889634f / sqrtf((float)dh)), 1.4e-45f), vs * kValueShift, 0.f, 0.f);
+    }
+    return;
   }
   for (int c = threadIdx.x; c < 2 * rows; c += blockDim.x) {
     const int kvsel = c >= rows, e = c - kvsel * rows;
@@ -452,12 +479,16 @@ cudaError_t launch_kv_dequant_pages(const int* items, int num_items, const int* 
   return cudaGetLastError();
 }
 
-cudaError_t launch_kv_expand_seen(const int* items, int num_items, const KVPool8& src, int max_pages, int num_pages,
+cudaError_t launch_kv_expand_seen(const int* items, int num_items, int kind, const KVPool8& src, int max_pages, int num_pages,
                                   const int* cu, const int* ctx, int n_kv, int d_head, int window, int sinks,
                                   const KVExpansion& dst, int* status, cudaStream_t stream) {
   if (num_items <= 0) return cudaSuccess;
-  kv_expand_seen_kernel<<<num_items, 256, 0, stream>>>(items, src, max_pages, num_pages, cu, ctx, n_kv, d_head, window,
-                                                       sinks, dst, status);
+  if (kind == kKvInt8)
+    kv_expand_seen_kernel<true><<<num_items, 256, 0, stream>>>(items, src, max_pages, num_pages, cu, ctx, n_kv, d_head,
+                                                               window, sinks, dst, status);
+  else
+    kv_expand_seen_kernel<false><<<num_items, 256, 0, stream>>>(items, src, max_pages, num_pages, cu, ctx, n_kv, d_head,
+                                                                window, sinks, dst, status);
   return cudaGetLastError();
 }
 

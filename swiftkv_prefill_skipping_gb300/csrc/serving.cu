@@ -35,7 +35,7 @@ int check_batch(const swiftkv_model* m, const int32_t* cu, const int32_t* ctx, i
   if (kv->max_pages_per_seq > (1 << 26)) return fail(SWIFTKV_EUNSUPPORTED, "max_pages_per_seq above 2^26");
   b->P = P;
   b->T = cu[P];
-  b->fp8 = kv->kv_dtype == 1;
+  b->kind = kv->kv_dtype;
   b->window = window;
   b->sinks = window > 0 ? std::min(sinks, 1 << 30) : 0;
   b->max_pages = kv->max_pages_per_seq;
@@ -139,20 +139,14 @@ int put(std::vector<int>* ints, const std::vector<int>& v) {
   return at;
 }
 
-// The lists for the kernels' parameters (nothing of them where they were uploaded).
-InlineInts inline_of(const std::vector<int>& ints, const int* dev) {
-  InlineInts r;
-  if (!dev) memcpy(r.v, ints.data(), ints.size() * 4);
-  return r;
-}
-
 void place_expansion(const swiftkv_model* m, Arena* a, int pages, const Batch& b, bool with_v, KVExpansion* e) {
   if (pages <= 0) return;
   const size_t rows = (size_t)pages * m->cfg.n_kv * kPageSize;
   e->k = a->take<bf16>(rows * m->cfg.d_head);
   e->v = with_v ? a->take<bf16>(rows * m->cfg.d_head) : nullptr;
-  e->k_scale = a->take<float>(rows);
-  e->v_scale = with_v ? a->take<float>(rows) : nullptr;
+  // int8: a float4 for each page and head in place of a key's scales
+  e->k_scale = a->take<float>(b.kind == kKvInt8 ? rows / kPageSize * 4 : rows);
+  e->v_scale = with_v && b.kind == kKvFp8 ? a->take<float>(rows) : nullptr;
   e->block_table = a->take<int>((size_t)b.P * b.max_pages);
 }
 
@@ -164,7 +158,7 @@ int expand(swiftkv_model* m, const swiftkv_kv_pages* kv, int c, const Batch& b, 
   src.k_scale = static_cast<const float*>(kv->k_scale[c]);
   src.v_scale = static_cast<const float*>(kv->v_scale[c]);
   src.block_table = kv->block_table;
-  CK(launch_kv_expand_seen(items, num, src, b.max_pages, kv->num_pages, cu, ctx, m->cfg.n_kv, m->cfg.d_head, b.window,
+  CK(launch_kv_expand_seen(items, num, b.kind, src, b.max_pages, kv->num_pages, cu, ctx, m->cfg.n_kv, m->cfg.d_head, b.window,
                            b.sinks, e, m->status, s));
   return SWIFTKV_OK;
 }
@@ -202,11 +196,27 @@ int hold(swiftkv_model* m, size_t bytes, cudaStream_t stream) {
 
 }  // namespace
 
+InlineInts inline_of(const std::vector<int>& ints, const int* dev) {
+  InlineInts r;
+  if (!dev) memcpy(r.v, ints.data(), ints.size() * 4);
+  return r;
+}
+
 int reserve(swiftkv_model* m, size_t bytes, cudaStream_t stream, Arena* arena) {
   if (bytes > 0) RET(guarded([&] { return hold(m, bytes, stream); }));
   arena->base = m->ops_ws;
   arena->used = 0;
   return SWIFTKV_OK;
+}
+
+cudaError_t launch_append_on(const swiftkv_model* m, AppendArgs a, int kind, const InlineInts& inl, cudaStream_t s) {
+  a.n_q = m->cfg.n_q;
+  a.n_kv = m->cfg.n_kv;
+  a.rope_tab = m->rope_tab;
+  a.rope_len = kRopeLen;
+  a.rope_turn = m->rope_turn;
+  a.status = m->status;
+  return launch_append(a, kind, m->cfg.d_head, inl, m->num_sms, s);
 }
 
 // ---------------------------------------------------------------------------- attention
@@ -237,7 +247,7 @@ int AttendPlan::make(const swiftkv_model* m, const int32_t* cu, const int32_t* c
       continue;
     }
     for (int t = 0; t < (n + tile_rows - 1) / tile_rows; ++t) tiles.push_back((i << 16) | t);
-    if (b.fp8) list_pages(i, c0, n, b.window, b.sinks, &exp_items);
+    if (b.kind != kKvBf16) list_pages(i, c0, n, b.window, b.sinks, &exp_items);
   }
   // heaviest first: the keys that a tile's last row sees
   auto keys_of = [&](int tl) {
@@ -247,7 +257,7 @@ int AttendPlan::make(const swiftkv_model* m, const int32_t* cu, const int32_t* c
   std::stable_sort(tiles.begin(), tiles.end(), [&](int x, int y) { return keys_of(x) > keys_of(y); });
   std::vector<int> units, ubeg;
   if (!ids.empty())
-    cut_units(ids, seen, c.n_kv, (long long)m->num_sms * (b.fp8 ? kRowsWarps8 : kRowsWarps), &units, &ubeg);
+    cut_units(ids, seen, c.n_kv, (long long)m->num_sms * (b.kind != kKvBf16 ? kRowsWarps8 : kRowsWarps), &units, &ubeg);
   num_tiles = (int)tiles.size();
   num_items = (int)ids.size();
   num_units = (int)(units.size() / 3);
@@ -273,7 +283,7 @@ void AttendPlan::place(const swiftkv_model* m, Arena* a) {
   dev = num_tiles > 0 || ints.size() > kInlineInts ? a->take<int>(ints.size()) : nullptr;
   part = a->take<float>(num_units > num_items ? (size_t)num_units * c.n_kv * max_cols * (c.d_head + 4) : 0);
   v_tail = nullptr;
-  if (num_tiles > 0 && !b.fp8)
+  if (num_tiles > 0 && b.kind == kKvBf16)
     v_tail = a->take<bf16>((size_t)b.P * kTailSlots * c.n_kv * kPageSize * c.d_head);
   place_expansion(m, a, num_exp, b, true, &exp);
 }
@@ -291,6 +301,7 @@ int AttendPlan::run(swiftkv_model* m, const swiftkv_kv_pages* kv, int c, const b
     ChunkArgs t;
     const bf16* k = static_cast<const bf16*>(kv->k_pool[c]);
     const bf16* v = static_cast<const bf16*>(kv->v_pool[c]);
+    t.kind = b.kind;
     t.k_scale = t.v_scale = nullptr;
     t.bt = kv->block_table;
     t.num_pages = kv->num_pages;
@@ -298,7 +309,7 @@ int AttendPlan::run(swiftkv_model* m, const swiftkv_kv_pages* kv, int c, const b
     t.tail_seqs = b.P;
     t.cu = dev + o_cu;
     t.ctx = dev + o_ctx;
-    if (b.fp8) {
+    if (b.kind != kKvBf16) {
       RET(expand(m, kv, c, b, dev + o_exp, num_exp, t.cu, t.ctx, exp, s));
       k = exp.k;
       v = exp.v;
@@ -348,8 +359,9 @@ int AttendPlan::run(swiftkv_model* m, const swiftkv_kv_pages* kv, int c, const b
     r.ldl = ldl;
     r.part = part;
     r.status = m->status;
-    e = launch_attn_rows(r, inline_of(ints, dev), kv->k_pool[c], kv->v_pool[c], b.fp8 ? static_cast<const float*>(kv->k_scale[c]) : nullptr,
-                         b.fp8 ? static_cast<const float*>(kv->v_scale[c]) : nullptr, g.d_head, num_items, m->num_sms, s);
+    e = launch_attn_rows(r, b.kind, inline_of(ints, dev), kv->k_pool[c], kv->v_pool[c],
+                         b.kind != kKvBf16 ? static_cast<const float*>(kv->k_scale[c]) : nullptr,
+                         b.kind != kKvBf16 ? static_cast<const float*>(kv->v_scale[c]) : nullptr, g.d_head, num_items, m->num_sms, s);
   }
   if (e != cudaSuccess)
     return fail(e == cudaErrorNotSupported ? SWIFTKV_EUNSUPPORTED : SWIFTKV_ECUDA, "attention: %s", cudaGetErrorString(e));
@@ -391,7 +403,7 @@ int WeightsPlan::make(const swiftkv_model* m, const int32_t* cu, const int32_t* 
         heavy.push_back({last - first, {i, t}});
         next = t + 1;
       }
-    if (b.fp8) list_pages(i, c0, n, b.window, b.sinks, &exp_items);
+    if (b.kind != kKvBf16) list_pages(i, c0, n, b.window, b.sinks, &exp_items);
   }
   if (!ids.empty()) cut_units(ids, seen, c.n_kv, (long long)m->num_sms * kWeightWarps, &units, nullptr);
   std::stable_sort(heavy.begin(), heavy.end(), [](const auto& x, const auto& y) { return x.first > y.first; });
@@ -450,12 +462,12 @@ int WeightsPlan::run(swiftkv_model* m, const swiftkv_kv_pages* kv, int c, const 
   a.status = m->status;
   cudaError_t e = cudaSuccess;
   if (num_units > 0)
-    e = launch_weights_rows(a, inline_of(ints, dev), b.fp8 ? nullptr : static_cast<const bf16*>(kv->k_pool[c]),
-                            b.fp8 ? static_cast<const uint8_t*>(kv->k_pool[c]) : nullptr,
-                            b.fp8 ? static_cast<const float*>(kv->k_scale[c]) : nullptr, g.d_head, max_cols,
+    e = launch_weights_rows(a, inline_of(ints, dev), (b.kind == kKvFp8) ? nullptr : static_cast<const bf16*>(kv->k_pool[c]),
+                            (b.kind == kKvFp8) ? static_cast<const uint8_t*>(kv->k_pool[c]) : nullptr,
+                            (b.kind == kKvFp8) ? static_cast<const float*>(kv->k_scale[c]) : nullptr, g.d_head, max_cols,
                             num_units, m->num_sms, s);
   if (e == cudaSuccess && num_tiles > 0) {
-    if (b.fp8) {
+    if ((b.kind == kKvFp8)) {
       RET(expand(m, kv, c, b, dev + o_exp, num_exp, dev + o_cu, dev + o_ctx, exp, s));
       e = launch_weights_tc(a, exp.k, exp.k_scale, exp.block_table, num_exp, g.d_head, dev + o_tiles, num_tiles,
                             m->num_sms, s);
@@ -470,7 +482,7 @@ int WeightsPlan::run(swiftkv_model* m, const swiftkv_kv_pages* kv, int c, const 
   return SWIFTKV_OK;
 }
 
-int WeightsPlan::kernels() const { return (num_units > 0) + (num_tiles > 0 ? 1 + b.fp8 : 0); }
+int WeightsPlan::kernels() const { return (num_units > 0) + (num_tiles > 0 ? 1 + (b.kind == kKvFp8) : 0); }
 
 }  // namespace skv
 
@@ -488,16 +500,22 @@ int check_call(const swiftkv_model* m, int cache, int P, const swiftkv_kv_pages*
   return SWIFTKV_OK;
 }
 
+// The caches' operators that know no block scales: weights by the key, and moves between pages.
+int check_no_blocks(const swiftkv_kv_pages* kv, const char* name) {
+  return kv->kv_dtype == kKvInt8 ? fail(SWIFTKV_EUNSUPPORTED, "%s over an int8 cache", name) : (int)SWIFTKV_OK;
+}
+
 // Keys of a sequence, and of its kept list: the kernels step through them in ints, past the end.
 constexpr int kMaxKeys = 1 << 30;
 
-int check_rows(const swiftkv_model* m, const void* p, int ld, const char* name) {
+int check_width(const void* p, int ld, long long width, const char* name) {
   if (!p) return fail(SWIFTKV_EINVAL, "null %s", name);
-  if (ld < m->Nq || ld % 8 || (reinterpret_cast<uintptr_t>(p) & 15))
-    return fail(SWIFTKV_EINVAL, "%s: rows need a stride of at least %d, a multiple of 8, and 16-byte alignment", name,
-                m->Nq);
+  if (ld < width || ld % 8 || (reinterpret_cast<uintptr_t>(p) & 15))
+    return fail(SWIFTKV_EINVAL, "%s: rows need a stride of at least %lld, a multiple of 8, and 16-byte alignment", name,
+                width);
   return SWIFTKV_OK;
 }
+int check_rows(const swiftkv_model* m, const void* p, int ld, const char* name) { return check_width(p, ld, m->Nq, name); }
 
 }  // namespace
 
@@ -530,6 +548,87 @@ int swiftkv_attend(swiftkv_model* m, int cache, const void* q, int ldq, const in
   });
 }
 
+int swiftkv_append(swiftkv_model* m, int cache, int caches, const swiftkv_new_rows* rows, const int32_t* cu,
+                   const int32_t* ctx, const int32_t* pos_off, int P, const swiftkv_kv_pages* kv, int rotate,
+                   swiftkv_stream stream) {
+  return guarded([&]() -> int {
+    RET(check_call(m, cache, P, kv));
+    if (caches < 1 || caches > m->C - cache)
+      return fail(SWIFTKV_EINVAL, "caches %d .. %lld of %d", cache, (long long)cache + caches - 1, m->C);
+    if (P == 0) return SWIFTKV_OK;
+    if (!cu || !rows) return fail(SWIFTKV_EINVAL, "null cu_seqlens / rows");
+    Batch b;
+    RET(check_batch(m, cu, ctx, P, kv, 0, 0, &b));
+    for (int i = 0; i < P; ++i) {
+      const long long end = (ctx ? ctx[i] : 0) + (long long)(cu[i + 1] - cu[i]), off = pos_off ? pos_off[i] : 0;
+      if (off < 0 || off + end > (1LL << 30))
+        return fail(SWIFTKV_EINVAL_SEQLENS, "sequence %d: positions outside [0, 2^30)", i);
+    }
+    if (b.T == 0) return SWIFTKV_OK;
+    const long long Nkv = m->Nkv, k_width = (caches - 1) * rows->k_step + Nkv, v_width = (caches - 1) * rows->v_step + Nkv;
+    if (caches > 1 && (rows->k_step < Nkv || rows->v_step < Nkv || rows->k_step % 8 || rows->v_step % 8))
+      return fail(SWIFTKV_EINVAL, "k_step, v_step: at least %lld and a multiple of 8", Nkv);
+    RET(check_width(rows->k, rows->ldk, k_width, "k"));
+    RET(check_width(rows->v, rows->ldv, v_width, "v"));
+    if (rows->q) {
+      RET(check_rows(m, rows->q, rows->ldq, "q"));
+      RET(check_rows(m, rows->q_out, rows->ldq_out, "q_out"));
+      const char *qa = static_cast<const char*>(rows->q), *oa = static_cast<const char*>(rows->q_out);
+      const size_t qn = ((size_t)(b.T - 1) * rows->ldq + m->Nq) * 2, on = ((size_t)(b.T - 1) * rows->ldq_out + m->Nq) * 2;
+      if (qa < oa + on && oa < qa + qn && !(qa == oa && (rows->ldq == rows->ldq_out || b.T == 1)))
+        return fail(SWIFTKV_EINVAL, "q_out overlaps q without being it");
+    }
+    OnDevice on_device(m);
+    cudaStream_t s = (cudaStream_t)stream;
+    AppendArgs a;
+    std::vector<int> ints;
+    ints.reserve(3 * (size_t)P + 4 + 8 * (size_t)caches);
+    a.o_cu = put(&ints, std::vector<int>(cu, cu + P + 1));
+    a.o_ctx = put(&ints, ctx ? std::vector<int>(ctx, ctx + P) : std::vector<int>(P, 0));
+    a.o_off = pos_off ? put(&ints, std::vector<int>(pos_off, pos_off + P)) : -1;
+    if (ints.size() % 2) ints.push_back(0);
+    a.o_pools = (int)ints.size();
+    std::vector<const void*> ptrs;
+    for (int c = 0; c < caches; ++c) ptrs.push_back(kv->k_pool[cache + c]);
+    for (int c = 0; c < caches; ++c) ptrs.push_back(kv->v_pool[cache + c]);
+    for (int c = 0; b.kind != kKvBf16 && c < caches; ++c) ptrs.push_back(kv->k_scale[cache + c]);
+    for (int c = 0; b.kind != kKvBf16 && c < caches; ++c) ptrs.push_back(kv->v_scale[cache + c]);
+    ints.resize(ints.size() + 2 * ptrs.size());
+    memcpy(ints.data() + a.o_pools, ptrs.data(), ptrs.size() * 8);
+    int* dev = nullptr;
+    if (ints.size() > kInlineInts) {
+      Arena arena;
+      RET(reserve(m, ints.size() * 4, s, &arena));
+      dev = arena.take<int>(ints.size());
+      CK(upload_ints(dev, ints.data(), (int)ints.size(), s));
+    }
+    a.lists = dev;
+    a.pools = nullptr;
+    a.pool_step = caches;
+    a.q = static_cast<const bf16*>(rows->q);
+    a.ldq = rows->ldq;
+    a.q_out = static_cast<bf16*>(rows->q_out);
+    a.ldq_out = rows->ldq_out;
+    a.k = static_cast<const bf16*>(rows->k);
+    a.v = static_cast<const bf16*>(rows->v);
+    a.ldk = rows->ldk;
+    a.ldv = rows->ldv;
+    a.k_step = rows->k_step;
+    a.v_step = rows->v_step;
+    a.caches = caches;
+    a.P = P;
+    a.T = b.T;
+    a.bt = kv->block_table;
+    a.max_pages = kv->max_pages_per_seq;
+    a.num_pages = kv->num_pages;
+    a.rotate = rotate != 0;
+    const cudaError_t e = launch_append_on(m, a, b.kind, inline_of(ints, dev), s);
+    if (e != cudaSuccess)
+      return fail(e == cudaErrorNotSupported ? SWIFTKV_EUNSUPPORTED : SWIFTKV_ECUDA, "append: %s", cudaGetErrorString(e));
+    return SWIFTKV_OK;
+  });
+}
+
 int swiftkv_attention_weights(swiftkv_model* m, int cache, const void* q, int ldq, const float* lse, const int32_t* cu,
                               const int32_t* ctx, int P, const swiftkv_kv_pages* kv, int window, int sinks, float decay,
                               float* scores, swiftkv_stream stream) {
@@ -538,6 +637,7 @@ int swiftkv_attention_weights(swiftkv_model* m, int cache, const void* q, int ld
     if (P == 0) return SWIFTKV_OK;
     if (!cu) return fail(SWIFTKV_EINVAL, "null cu_seqlens");
     if (!(std::fabs(decay) <= 3.0e38f)) return fail(SWIFTKV_EINVAL, "decay is not finite");
+    RET(check_no_blocks(kv, "attention weights"));
     WeightsPlan p;
     RET(p.make(m, cu, ctx, P, kv, window, sinks));
     if (p.b.T == 0) return SWIFTKV_OK;
@@ -563,6 +663,7 @@ int swiftkv_evict(swiftkv_model* m, int cache, const swiftkv_kv_pages* kv, float
     RET(check_call(m, cache < 0 ? 0 : cache, P, kv));
     if (P == 0) return SWIFTKV_OK;
     if (cache < -1) return fail(SWIFTKV_EINVAL, "cache %d outside [-1, %d)", cache, m->C);
+    RET(check_no_blocks(kv, "eviction"));
     if (!scores || !seq_lens || !kept) return fail(SWIFTKV_EINVAL, "null scores / seq_lens / kept");
     if ((reinterpret_cast<uintptr_t>(kept) | reinterpret_cast<uintptr_t>(dst_block_table)) & 3)
       return fail(SWIFTKV_EINVAL, "misaligned kept or destination block table");

@@ -49,6 +49,8 @@ cudaError_t launch_v_tail(const bf16* v_pool, const int* block_table, int max_pa
 // Value scales are copied times kValueShift, which whoever multiplies P by them takes back: P times a
 // scale goes to bf16, and value scales near float32's smallest would end up among bf16's subnormals.
 constexpr float kValueShift = 65536.f;
+// int8: k_scale alone, a float4 for every (page, head): the key scale times log2(e) / sqrt(d_head), the
+// value scale times kValueShift, 0, 0.
 struct KVPool8 {
   const uint8_t *k, *v;
   const float *k_scale, *v_scale;
@@ -59,9 +61,12 @@ struct KVExpansion {
   float *k_scale, *v_scale;
   int* block_table;
 };
-cudaError_t launch_kv_expand_seen(const int* items, int num_items, const KVPool8& src, int max_pages, int num_pages,
+cudaError_t launch_kv_expand_seen(const int* items, int num_items, int kind, const KVPool8& src, int max_pages, int num_pages,
                                   const int* cu, const int* ctx, int n_kv, int d_head, int window, int sinks,
                                   const KVExpansion& dst, int* status, cudaStream_t stream);
+
+// kv_dtype of a cache
+constexpr int kKvBf16 = 0, kKvFp8 = 1, kKvInt8 = 2;
 
 // Host lists of a small call travel in the kernels' parameters instead of an upload of their own
 // (which costs a launch: 2 us of a 26 us decode attention, a third of a tiny one). A kernel that may
@@ -70,6 +75,8 @@ constexpr int kInlineInts = 1000;
 struct alignas(16) InlineInts {
   int v[kInlineInts];
 };
+// The lists for the kernels' parameters (nothing of them where they were uploaded).
+InlineInts inline_of(const std::vector<int>& ints, const int* dev);
 __device__ __forceinline__ const int* list_base(const int* dev, const InlineInts& inl) { return dev ? dev : inl.v; }
 
 // Bump allocator over the model's operator workspace: sized by a first pass without a base.
@@ -91,7 +98,7 @@ int reserve(swiftkv_model* m, size_t bytes, cudaStream_t stream, Arena* arena);
 // A ragged batch: chunk s is rows [cu[s], cu[s + 1]) at positions ctx[s] .. of sequence s.
 struct Batch {
   int P = 0, T = 0;
-  bool fp8 = false;
+  int kind = 0;  // kv_dtype
   int window = 0, sinks = 0;
   int max_pages = 0;
 };
@@ -145,7 +152,8 @@ struct WeightsPlan {
 // an item is a tile for two query heads of one KV head, num_items = tiles * n_q / 2) or of 256 rows
 // (an item is a tile for one head, num_items = tiles * n_q).
 struct ChunkArgs {
-  const float *k_scale, *v_scale;  // FP8: the expansion's scales; else null
+  int kind;                        // kv_dtype
+  const float *k_scale, *v_scale;  // FP8: the expansion's scales; int8: k_scale alone, its float4 a block
   const int* bt;
   int max_pages, num_pages;
   const int *cu, *ctx, *tiles;
@@ -167,7 +175,7 @@ cudaError_t launch_attn_chunk(const ChunkArgs& a, const bf16* q, int ldq, int T,
 // kRowsCols; units [3 * num_units] = (item, first key, keys) of keys some row sees, item-major; ubeg
 // [n + 1]; part: num_units * n_kv * max_cols records of d_head + 4 floats (several units an item).
 constexpr int kRowsCols = 16;
-constexpr int kRowsWarps = 8, kRowsWarps8 = 12;  // warps per SM that walk units: bf16, FP8
+constexpr int kRowsWarps = 8, kRowsWarps8 = 12;  // warps per SM that walk units: bf16, 8-bit codes
 struct RowsArgs {
   const bf16* q;
   int ldq;
@@ -185,7 +193,7 @@ struct RowsArgs {
   float* part;
   int* status;
 };
-cudaError_t launch_attn_rows(const RowsArgs& a, const InlineInts& inl, const void* k, const void* v, const float* k_scale, const float* v_scale,
+cudaError_t launch_attn_rows(const RowsArgs& a, int kind, const InlineInts& inl, const void* k, const void* v, const float* k_scale, const float* v_scale,
                              int d_head, int num_items, int num_sms, cudaStream_t s);
 struct WeightsArgs {
   const bf16* q;
@@ -214,6 +222,40 @@ cudaError_t launch_weights_rows(const WeightsArgs& a, const InlineInts& inl, con
 // k / k_scale are an expansion (pages named by a.bt's counterpart `bt_k` of the same shape).
 cudaError_t launch_weights_tc(const WeightsArgs& a, const bf16* k, const float* k_scale, const int* bt_k, int pages_k,
                               int d_head, const int* tiles, int num_tiles, int num_sms, cudaStream_t s);
+
+// New rows of `caches` caches (append.cu): k and v [T] rows, ldk / ldv elements apart, a cache's heads k_step /
+// v_step elements behind the one before; q [T] rows or null. Lists (null: inline): cu [P + 1], ctx [P], o_off
+// (-1: none) [P] added to the positions of the rotation.
+struct AppendArgs {
+  const bf16* q;
+  int ldq;
+  bf16* q_out;
+  int ldq_out;
+  const bf16 *k, *v;
+  int ldk, ldv;
+  long long k_step, v_step;
+  int caches, n_q, n_kv;
+  int P, T;
+  const int* lists;
+  int o_cu, o_ctx, o_off;
+  // addresses of the caches' K pools, and pool_step entries on of V's, of K's scales and of V's
+  const long long* pools;  // null: in the lists, at o_pools
+  int o_pools, pool_step;
+  const int* bt;
+  int max_pages, num_pages;
+  bool rotate;
+  const float2* rope_tab;
+  int rope_len;
+  const unsigned long long* rope_turn;
+  int* status;
+  // set by launch_append
+  uint32_t per_cache;
+  int splits;
+  long long row_warps, pages;
+};
+// launch_append with the model's shape, rotation and status word.
+cudaError_t launch_append_on(const swiftkv_model* m, AppendArgs a, int kind, const InlineInts& inl, cudaStream_t s);
+cudaError_t launch_append(AppendArgs a, int kind, int d_head, const InlineInts& inl, int num_sms, cudaStream_t s);
 
 struct EvictArgs {
   const int* lists;         // null: inline; [0, P): keys each sequence holds, then at o_ptrs the
