@@ -403,7 +403,7 @@ typedef struct {
 
 /* Penalties, biases and masks on logits, between the model's calls and swiftkv_sample. For id i of row r, s the
  * ids in its history and c[i] how often i stands behind the prompt:
- *   x = i in s ? (l > 0 ? l / repetition : l * repetition) : l
+ *   x = i in s ? (l > 0 ? l * (1 / repetition) : l * repetition) : l
  *   out = allowed by the mask ? x - frequency * c[i] - presence * (c[i] > 0) + bias[i] : -inf
  *   logits  device float [rows][ld], the first `vocab` of each row
  *   out     device float [rows][ld_out]: the logits themselves, or memory apart from them

@@ -1,13 +1,14 @@
 // Penalties for repeated tokens, biases and grammar masks on logits, before swiftkv_sample.
 //
 //   s_i: id i is in the row's history; c_i: how often in the part after the prompt
-//   x = s_i ? (l_i > 0 ? l_i / rep : l_i * rep) : l_i
+//   x = s_i ? (l_i > 0 ? l_i * (1 / rep) : l_i * rep) : l_i
 //   x = x - frequency * c_i - presence * (c_i > 0) + bias_i;  x = -inf where the mask forbids i
 //
-// Bound by HBM: the row is read and written once. A CTA owns a slice of one row's ids and reads the
-// row's whole history itself, keeping what concerns its slice: one 32-bit word an id in shared memory,
-// count, prompt bit and place in the bias list. No CTA waits for another, and integer counts make the order of
-// the atomics irrelevant. The slice's logits are requested before the history is walked.
+// Bound by HBM: the row is read and written once. A CTA owns a slice of one row's ids and copies it through shared
+// memory. While the copy arrives it walks the row's whole history and keeps what concerns its slice, one 32-bit
+// word an id: count, prompt bit and place in the bias list. Then it looks at its words; only ids that are named cost
+// arithmetic. No CTA waits for another, and counts are integers: the order of the atomics
+// changes nothing.
 #include <algorithm>
 #include <cmath>
 
@@ -21,6 +22,8 @@ namespace skv {
 namespace {
 
 constexpr int AT = 512;                 // threads
+constexpr int kMaxSlice = 8192;         // ids of a CTA: 64 KB of logits and words, three CTAs an SM
+constexpr int kTargetBlocks = 456;      // CTAs that fill the GPU
 constexpr unsigned kCount = 0xfffff;    // how often the id was generated
 constexpr unsigned kPrompt = 1u << 20;  // it is in the prompt
 constexpr int kBiasShift = 21;          // 1 + its last place in the bias list
@@ -31,10 +34,11 @@ struct AdjustParams {
   long long ld;
   float* out;
   long long ldo;
-  int V, slices;
+  int V, slice, slices;  // slice: ids of a CTA, a multiple of 4
   const int* tokens;
   long long ld_tokens;
   int max_tokens;
+  bool tokens16;  // histories start on 16 bytes
   const int *lens, *prompt_lens;
   const float *repetition, *presence, *frequency;
   float repetition_all, presence_all, frequency_all;
@@ -45,141 +49,165 @@ struct AdjustParams {
   long long ld_mask;
 };
 
-// N: groups of four ids a thread owns. VEC: rows start on 16 bytes; a thread's four ids are neighbours, else they
-// lie AT apart.
-template <int N, bool VEC>
+// VEC: rows start on 16 bytes.
+template <bool VEC>
 __global__ void __launch_bounds__(AT) adjust_kernel(const AdjustParams p) {
-  constexpr int SLICE = 4 * N * AT;
-  extern __shared__ __align__(16) unsigned word[];
+  extern __shared__ __align__(16) unsigned char smem[];
   griddep_launch_dependents();
   griddep_wait();
-  const int row = blockIdx.x / p.slices, base = (blockIdx.x - row * p.slices) * SLICE, tid = threadIdx.x;
-  const int size = min(SLICE, p.V - base);
+  const int row = blockIdx.x / p.slices, base = (blockIdx.x - row * p.slices) * p.slice, tid = threadIdx.x;
+  const int size = min(p.slice, p.V - base);
   const float* src = p.logits + (size_t)row * p.ld + base;
   float* dst = p.out + (size_t)row * p.ldo + base;
-  auto at = [&](int g, int e) { return VEC ? (g * AT + tid) * 4 + e : (g * 4 + e) * AT + tid; };
-  const bool in_place = src == dst;
-  float x[N][4];
-  auto load = [&](int g) {
-    if (VEC && at(g, 3) < size) {
-      const float4 f = *reinterpret_cast<const float4*>(src + at(g, 0));
-      x[g][0] = f.x;
-      x[g][1] = f.y;
-      x[g][2] = f.z;
-      x[g][3] = f.w;
-    } else {
+  const bool in_place = src == dst, lists = p.tokens || p.num_bias > 0;
+  unsigned* word = reinterpret_cast<unsigned*>(smem);                                // [slice], with lists
+  float* x = reinterpret_cast<float*>(smem + (lists ? (size_t)p.slice * 4 : 0));     // [slice], not in place
+  uint32_t* allow = reinterpret_cast<uint32_t*>(x + (in_place ? 0 : p.slice));       // [slice / 32], with a mask
+  // Everything that the CTA reads is asked for here, the lists beyond their ends too (as far as the arrays go):
+  // one trip to memory and not one after another, which took most of a CTA's time
+  constexpr int B = 4;  // fours of ids in flight
+  const int* ids = p.tokens ? p.tokens + (size_t)row * p.ld_tokens : nullptr;
+  auto fetch = [&](int i0, int end, int4* id) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) x[g][e] = at(g, e) < size ? src[at(g, e)] : 0.f;
+    for (int b = 0; b < B; ++b) {
+      const int i = i0 + b * 4 * AT;
+      id[b] = make_int4(-1, -1, -1, -1);
+      if (p.tokens16 && i + 3 < end) {
+        id[b] = *reinterpret_cast<const int4*>(ids + i);
+      } else {
+        if (i < end) id[b].x = ids[i];
+        if (i + 1 < end) id[b].y = ids[i + 1];
+        if (i + 2 < end) id[b].z = ids[i + 2];
+        if (i + 3 < end) id[b].w = ids[i + 3];
+      }
     }
   };
-  // in place a group that nothing concerns is not read either
-  if (!in_place)
-#pragma unroll
-    for (int g = 0; g < N; ++g) load(g);
-  const int* ids = p.tokens ? p.tokens + (size_t)row * p.ld_tokens : nullptr;
-  const int len = ids ? max(0, min(p.max_tokens, p.lens ? p.lens[row] : p.max_tokens)) : 0;
-  const int prompt = p.prompt_lens ? p.prompt_lens[row] : 0;
-  const bool listed = ids || p.num_bias > 0;
-  if (listed) {
-#pragma unroll
-    for (int g = 0; g < N; ++g) reinterpret_cast<uint4*>(word)[g * AT + tid] = make_uint4(0, 0, 0, 0);
+  int4 id[B];
+  int len = 0, prompt = 0;
+  float rep = 1.f, presence = 0.f, frequency = 0.f;
+  if (ids) {
+    fetch(tid * 4, p.max_tokens, id);
+    len = p.lens ? p.lens[row] : p.max_tokens;
+    prompt = p.prompt_lens ? p.prompt_lens[row] : 0;
+    rep = p.repetition ? p.repetition[row] : p.repetition_all;
+    presence = p.presence ? p.presence[row] : p.presence_all;
+    frequency = p.frequency ? p.frequency[row] : p.frequency_all;
+  }
+  const int* bias_ids = p.bias_ids + (size_t)row * p.num_bias;
+  const unsigned bias_id = tid < p.num_bias ? (unsigned)bias_ids[tid] : 0xffffffffu;
+  const uint32_t* mask = p.mask ? p.mask + (size_t)row * p.ld_mask + (base >> 5) : nullptr;
+  if (mask)
+    for (int i = tid; i * 32 < size; i += AT) cp_async4(smem_u32(allow + i), mask + i, 4);
+  if (!in_place) {
+    if (VEC) {
+      for (int i = tid * 4; i < size; i += 4 * AT)  // the bytes past the row's end become zeros
+        cp_async16(smem_u32(x + i), src + i, min(16, (size - i) * 4));
+    } else {
+      for (int i = tid; i < size; i += AT) cp_async4(smem_u32(x + i), src + i, 4);
+    }
+  }
+  cp_async_commit();
+  if (lists) {
+    for (int i = tid * 4; i < p.slice; i += 4 * AT) *reinterpret_cast<uint4*>(word + i) = make_uint4(0, 0, 0, 0);
     __syncthreads();
+    // an id less base, as unsigned: ids outside the slice, negative ones among them, are at least `size`
     if (p.num_bias > 0) {  // an id named twice takes its last entry: the words hold nothing else yet
       for (int i = tid; i < p.num_bias; i += AT) {
-        const long long u = (long long)p.bias_ids[(size_t)row * p.num_bias + i] - base;
-        if (u >= 0 && u < size) atomicMax(word + u, (unsigned)(i + 1) << kBiasShift);
+        const unsigned u = (i == tid ? bias_id : (unsigned)bias_ids[i]) - (unsigned)base;
+        if (u < (unsigned)size) atomicMax(word + u, (unsigned)(i + 1) << kBiasShift);
       }
       __syncthreads();
     }
-    constexpr int B = 4;
-    for (int i0 = tid; i0 < len; i0 += B * AT) {
-      int id[B];
-#pragma unroll
-      for (int b = 0; b < B; ++b) id[b] = i0 + b * AT < len ? ids[i0 + b * AT] : -1;
+    if (ids) len = min(len, p.max_tokens);
+    for (int i1 = 0; i1 < len; i1 += 4 * AT * B) {
+      const int i0 = i1 + tid * 4;
+      if (i1 > 0) fetch(i0, len, id);
 #pragma unroll
       for (int b = 0; b < B; ++b) {
-        const long long u = (long long)id[b] - base;
-        if (u < 0 || u >= size || id[b] < 0) continue;
-        if (i0 + b * AT < prompt) atomicOr(word + u, kPrompt);
-        else atomicAdd(word + u, 1u);
-      }
-    }
-    __syncthreads();
-  }
-  float rep = p.repetition ? p.repetition[row] : p.repetition_all;
-  if (!(rep > 0.f)) rep = 1.f;
-  const float presence = p.presence ? p.presence[row] : p.presence_all;
-  const float frequency = p.frequency ? p.frequency[row] : p.frequency_all;
-  const uint32_t* mask = p.mask ? p.mask + (size_t)row * p.ld_mask : nullptr;
-  const float* bias = p.bias + (size_t)row * p.num_bias;
+        unsigned u[4] = {(unsigned)id[b].x - (unsigned)base, (unsigned)id[b].y - (unsigned)base,
+                         (unsigned)id[b].z - (unsigned)base, (unsigned)id[b].w - (unsigned)base};
+        // the warp's 128 neighbours: all the prompt's, all behind it (both without a look at the single one), or neither
+        const int w0 = i1 + b * 4 * AT + (tid >> 5) * 128, i = i0 + b * 4 * AT;
+        if (w0 + 128 <= min(prompt, len)) {
 #pragma unroll
-  for (int g = 0; g < N; ++g) {
-    unsigned w[4] = {0, 0, 0, 0}, allowed = 15;
-    if (listed) {
-      if (VEC) {
-        const uint4 q = reinterpret_cast<const uint4*>(word)[g * AT + tid];
-        w[0] = q.x;
-        w[1] = q.y;
-        w[2] = q.z;
-        w[3] = q.w;
-      } else {
+          for (int e = 0; e < 4; ++e)
+            if (u[e] < (unsigned)size) atomicOr(word + u[e], kPrompt);
+        } else if (w0 >= prompt && w0 + 128 <= len) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) w[e] = word[at(g, e)];
-      }
-    }
-    if (mask) {
-      if (VEC) {
-        const int i = base + at(g, 0);
-        if (at(g, 0) < size) allowed = mask[i >> 5] >> (i & 31) & 15;
-      } else {
-        allowed = 0;
+          for (int e = 0; e < 4; ++e)
+            if (u[e] < (unsigned)size) atomicAdd(word + u[e], 1u);
+        } else if (w0 < len) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int i = base + at(g, e);
-          if (at(g, e) < size) allowed |= (mask[i >> 5] >> (i & 31) & 1) << e;
+          for (int e = 0; e < 4; ++e)
+            if (i + e < len && u[e] < (unsigned)size) {
+              if (i + e < prompt) atomicOr(word + u[e], kPrompt);
+              else atomicAdd(word + u[e], 1u);
+            }
         }
       }
     }
-    if (in_place) {
-      if (!(w[0] | w[1] | w[2] | w[3]) && allowed == 15) continue;
-      load(g);
-    }
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      float v = x[g][e];
-      if (w[e]) {
-        const unsigned count = w[e] & kCount, place = w[e] >> kBiasShift;
-        if (w[e] & (kCount | kPrompt)) v = v > 0.f ? v / rep : v * rep;
-        if (count) v = v - frequency * (float)count - presence;
-        if (place) v += bias[place - 1];
+  }
+  if (!(rep > 0.f)) rep = 1.f;
+  const float* bias = p.bias + (size_t)row * p.num_bias;
+  const float per = 1.f / rep;
+  auto adjust = [&](unsigned w, float v) {
+    if (w & (kCount | kPrompt)) v *= v > 0.f ? per : rep;
+    if (w & kCount) v = v - frequency * (float)(w & kCount) - presence;
+    if (w >> kBiasShift) v += bias[(w >> kBiasShift) - 1];
+    return v;
+  };
+  cp_async_wait<0>();
+  __syncthreads();
+  if (VEC && !in_place) {
+    for (int u = tid * 4; u < size; u += 4 * AT) {
+      float4 v = *reinterpret_cast<const float4*>(x + u);
+      if (lists) {
+        const uint4 w = *reinterpret_cast<const uint4*>(word + u);
+        if (w.x) v.x = adjust(w.x, v.x);
+        if (w.y) v.y = adjust(w.y, v.y);
+        if (w.z) v.z = adjust(w.z, v.z);
+        if (w.w) v.w = adjust(w.w, v.w);
       }
-      x[g][e] = allowed >> e & 1 ? v : -INFINITY;
+      if (mask) {
+        const unsigned a = allow[u >> 5] >> (u & 31);
+        if (!(a & 1)) v.x = -INFINITY;
+        if (!(a & 2)) v.y = -INFINITY;
+        if (!(a & 4)) v.z = -INFINITY;
+        if (!(a & 8)) v.w = -INFINITY;
+      }
+      if (u + 3 < size) {
+        *reinterpret_cast<float4*>(dst + u) = v;
+      } else {
+        dst[u] = v.x;
+        if (u + 1 < size) dst[u + 1] = v.y;
+        if (u + 2 < size) dst[u + 2] = v.z;
+      }
     }
-    if (VEC && at(g, 3) < size) {
-      *reinterpret_cast<float4*>(dst + at(g, 0)) = make_float4(x[g][0], x[g][1], x[g][2], x[g][3]);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (at(g, e) < size) dst[at(g, e)] = x[g][e];
+  } else {
+    for (int u = tid; u < size; u += AT) {
+      const unsigned w = lists ? word[u] : 0u;
+      const bool ok = !mask || (allow[u >> 5] >> (u & 31) & 1);
+      if (in_place) {  // what nothing concerns is neither read nor written
+        if (!ok) dst[u] = -INFINITY;
+        else if (w) dst[u] = adjust(w, src[u]);
+      } else {
+        dst[u] = !ok ? -INFINITY : w ? adjust(w, x[u]) : x[u];
+      }
     }
   }
 }
 
-template <int N, bool VEC>
-cudaError_t launch_n(AdjustParams p, int rows, cudaStream_t s) {
-  constexpr int slice = 4 * N * AT;
+template <bool VEC>
+cudaError_t launch_vec(const AdjustParams& p, int rows, cudaStream_t s) {
+  const bool lists = p.tokens || p.num_bias > 0, in_place = p.logits == p.out;
+  constexpr int most = kMaxSlice * 8 + kMaxSlice / 8;
   static PerDeviceOnce once;
-  cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void*>(adjust_kernel<N, VEC>), slice * 4, once);
+  cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void*>(adjust_kernel<VEC>), most, once);
   if (e != cudaSuccess) return e;
-  p.slices = (int)(((long long)p.V + slice - 1) / slice);
+  const int smem = (lists ? p.slice * 4 : 0) + (in_place ? 0 : p.slice * 4) + (p.mask ? p.slice / 8 : 0);
   const long long blocks = (long long)rows * p.slices;
   if (blocks >= 1LL << 31) return cudaErrorNotSupported;
-  return launch_pdl(adjust_kernel<N, VEC>, dim3((unsigned)blocks), dim3(AT), slice * 4, s, p);
-}
-
-template <int N>
-cudaError_t launch_vec(const AdjustParams& p, bool vec, int rows, cudaStream_t s) {
-  return vec ? launch_n<N, true>(p, rows, s) : launch_n<N, false>(p, rows, s);
+  return launch_pdl(adjust_kernel<VEC>, dim3((unsigned)blocks), dim3(AT), smem, s, p);
 }
 
 }  // namespace
@@ -220,10 +248,10 @@ extern "C" int swiftkv_adjust_logits(const float* logits, int rows, int vocab, l
   p.out = out;
   p.ldo = ld_out;
   p.V = vocab;
-  p.slices = 0;
   p.tokens = hist ? a->tokens : nullptr;
   p.ld_tokens = a->ld_tokens;
   p.max_tokens = a->max_tokens;
+  p.tokens16 = (reinterpret_cast<uintptr_t>(a->tokens) & 15) == 0 && (rows == 1 || a->ld_tokens % 4 == 0);
   p.lens = a->lens;
   p.prompt_lens = a->prompt_lens;
   p.repetition = a->repetition;
@@ -239,11 +267,11 @@ extern "C" int swiftkv_adjust_logits(const float* logits, int rows, int vocab, l
   p.ld_mask = a->ld_mask;
   const bool vec = ((i0 | o0) & 15) == 0 && (rows == 1 || (ld % 4 == 0 && ld_out % 4 == 0));
   // Short slices while there are few rows, so that every SM has work; long ones walk a history less often.
-  const long long ids = (long long)rows * vocab;
+  const long long ids = (long long)rows * vocab, want = (ids / kTargetBlocks + 1023) / 1024 * 1024;
+  p.slice = (int)std::max(1024LL, std::min<long long>(kMaxSlice, want));
+  p.slices = (vocab + p.slice - 1) / p.slice;
   cudaStream_t s = (cudaStream_t)stream;
-  const cudaError_t e = ids < (1 << 20) ? launch_vec<1>(p, vec, rows, s)
-                        : ids < (1 << 22) ? launch_vec<2>(p, vec, rows, s)
-                        : ids < (1 << 23) ? launch_vec<4>(p, vec, rows, s) : launch_vec<8>(p, vec, rows, s);
+  const cudaError_t e = vec ? launch_vec<true>(p, rows, s) : launch_vec<false>(p, rows, s);
   if (e != cudaSuccess)
     return set_error(e == cudaErrorNotSupported ? SWIFTKV_EUNSUPPORTED : SWIFTKV_ECUDA, cudaGetErrorString(e));
   return SWIFTKV_OK;
