@@ -23,7 +23,7 @@ namespace {
 
 constexpr int AT = 512;                 // threads
 constexpr int kMaxSlice = 8192;         // ids of a CTA: 64 KB of logits and words, three CTAs an SM
-constexpr int kTargetBlocks = 456;      // CTAs that fill the GPU
+constexpr int kTargetBlocks = 304;      // CTAs that fill the GPU
 constexpr unsigned kCount = 0xfffff;    // how often the id was generated
 constexpr unsigned kPrompt = 1u << 20;  // it is in the prompt
 constexpr int kBiasShift = 21;          // 1 + its last place in the bias list
@@ -65,7 +65,7 @@ __global__ void __launch_bounds__(AT) adjust_kernel(const AdjustParams p) {
   uint32_t* allow = reinterpret_cast<uint32_t*>(x + (in_place ? 0 : p.slice));       // [slice / 32], with a mask
   // Everything that the CTA reads is asked for here, the lists beyond their ends too (as far as the arrays go):
   // one trip to memory and not one after another, which took most of a CTA's time
-  constexpr int B = 4;  // fours of ids in flight
+  constexpr int B = 2;  // fours of ids in flight
   const int* ids = p.tokens ? p.tokens + (size_t)row * p.ld_tokens : nullptr;
   auto fetch = [&](int i0, int end, int4* id) {
 #pragma unroll
