@@ -62,14 +62,30 @@ __device__ __forceinline__ void turn_piece(Piece& p, const float2* cs) {
     b[i] = pack_bf16(y0, y1);
   }
 }
-__device__ __forceinline__ float largest(const Piece& p) {
-  const uint32_t* w = &p.a.x;
-  const uint32_t* u = &p.b.x;
+// The largest magnitude of a lane's values as a bf16's bits, in which NaN is above infinity and that above the rest.
+__device__ __forceinline__ uint32_t largest(const Piece& p) {
+  const uint32_t w[8] = {p.a.x, p.a.y, p.a.z, p.a.w, p.b.x, p.b.y, p.b.z, p.b.w};
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = __vmaxu2(m, w[i] & 0x7fff7fffu);
+  return max(m & 0xffffu, m >> 16);
+}
+__device__ __forceinline__ float bits_to_f32(uint32_t bf16_bits) { return __uint_as_float(bf16_bits << 16); }
+__device__ __noinline__ float largest_number(uint4 a, uint4 b) {  // NaN left out
+  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
   float m = 0.f;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    m = fmaxf(m, fmaxf(fabsf(__uint_as_float(w[i] << 16)), fabsf(__uint_as_float(w[i] & 0xffff0000u))));
-    m = fmaxf(m, fmaxf(fabsf(__uint_as_float(u[i] << 16)), fabsf(__uint_as_float(u[i] & 0xffff0000u))));
+  for (int i = 0; i < 8; ++i) m = fmaxf(m, fmaxf(fabsf(bits_to_f32(w[i] & 0xffffu)), fabsf(bits_to_f32(w[i] >> 16))));
+  return m;
+}
+// The same without NaN, and with infinities as the largest finite number.
+__device__ __noinline__ uint32_t largest_finite(uint4 a, uint4 b) {
+  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t lo = w[i] & 0x7fffu, hi = w[i] >> 16 & 0x7fffu;
+    m = max(m, max(lo > 0x7f80u ? 0u : min(lo, 0x7f7fu), hi > 0x7f80u ? 0u : min(hi, 0x7f7fu)));
   }
   return m;
 }
@@ -89,17 +105,44 @@ __device__ __forceinline__ void load_angles(const AppendArgs& a, int pos, int j,
   }
 }
 
-// x / scale as an int8 code; NaN becomes 0.
-__device__ __forceinline__ uint32_t code8(float x, float scale) {
-  return (uint32_t)(max(-127, min(127, __float2int_rn(x / scale))) & 255);
+// Two quotients x / scale rounded to float32, from the reciprocal (itself rounded): the quotient's remainder, exact
+// in a fused multiply-add, corrects it (P. Markstein, "Computation of elementary functions on the IBM RISC System/6000",
+// 1990). For scales at which no remainder is subnormal. A division by itself is some five times as long.
+__device__ __forceinline__ void quotients(float2& x, float scale, float recip) {
+  asm("{\n .reg .b64 a, b, c, q, r;\n mov.b64 a, {%0, %1};\n mov.b64 b, {%2, %2};\n mov.b64 c, {%3, %3};\n"
+      " mul.rn.f32x2 q, a, b;\n fma.rn.f32x2 r, q, c, a;\n fma.rn.f32x2 q, r, b, q;\n mov.b64 {%0, %1}, q;\n}\n"
+      : "+f"(x.x), "+f"(x.y)
+      : "f"(recip), "f"(-scale));
 }
-__device__ __forceinline__ uint2 codes8(uint4 v, float scale) {
-  const uint32_t* w = &v.x;
+__device__ __forceinline__ bool plain_scale(float scale) { return scale > 1e-20f && scale < 1e30f; }
+__device__ __forceinline__ float2 pair_of(uint32_t w) { return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)); }
+
+// x / scale as int8 codes: with 1.5 2^23 added the integer next to a quotient (ties to even) is the sum's last byte.
+__device__ __forceinline__ uint2 codes8(uint4 v, float scale, float recip) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
   uint32_t c[8];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    c[2 * i] = code8(__uint_as_float(w[i] << 16), scale);
-    c[2 * i + 1] = code8(__uint_as_float(w[i] & 0xffff0000u), scale);
+    float2 x = pair_of(w[i]);
+    quotients(x, scale, recip);
+    c[2 * i] = __float_as_uint(x.x + 12582912.f);
+    c[2 * i + 1] = __float_as_uint(x.y + 12582912.f);
+  }
+  return make_uint2(__byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410),
+                    __byte_perm(__byte_perm(c[4], c[5], 0x0040), __byte_perm(c[6], c[7], 0x0040), 0x5410));
+}
+// The same for values and scales of any kind; NaN becomes 0.
+__device__ __forceinline__ uint32_t code8_any(float x, float scale) {
+  return (uint32_t)(max(-127, min(127, __float2int_rn(x / scale))) & 255);
+}
+__device__ __noinline__ uint2 codes8_any(uint4 v, float scale) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t c[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 x = pair_of(w[i]);
+    c[2 * i] = code8_any(x.x, scale);
+    c[2 * i + 1] = code8_any(x.y, scale);
   }
   return make_uint2(c[0] | c[1] << 8 | c[2] << 16 | c[3] << 24, c[4] | c[5] << 8 | c[6] << 16 | c[7] << 24);
 }
@@ -152,7 +195,7 @@ __global__ void __launch_bounds__(AWARPS * 32) append_kernel(const AppendArgs a,
         if (vec < nq) {
           head[u] = vec;
           src = a.q + (size_t)t * a.ldq + (size_t)vec * D;
-        } else if (vec < nvec && ok) {
+        } else if (vec < nvec) {
           const int r = vec - nq, c = (int)__umulhi((uint32_t)r, a.per_cache), h = r - c * 2 * a.n_kv;
           cache[u] = c;
           head[u] = a.n_q + h;
@@ -180,26 +223,44 @@ __global__ void __launch_bounds__(AWARPS * 32) append_kernel(const AppendArgs a,
         const size_t at = ((size_t)page * a.n_kv + (is_q ? 0 : h)) * kPageSize + (row & 15);
         const long long* pool = pools + (is_v ? a.pool_step : 0) + cache[u];
         if (KIND == kKvBf16) {
-          if (!is_q) {
+          if (!is_q && ok) {
             bf16* dst = reinterpret_cast<bf16*>(*pool) + at * D + 8 * j;
             *reinterpret_cast<uint4*>(dst) = p[u].a;
             *reinterpret_cast<uint4*>(dst + D / 2) = p[u].b;
           }
         } else {
-          float top = largest(p[u]);
+          // (as the model's epilogues: the largest but NaN, infinities among them)
+          uint32_t most = largest(p[u]);
 #pragma unroll
-          for (int o = 1; o < LPV; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-          if (!is_q) {
+          for (int o = 1; o < LPV; o <<= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
+          float top = bits_to_f32(most);
+          if (__any_sync(0xffffffffu, most > 0x7f80u)) {
+            top = largest_number(p[u].a, p[u].b);
+#pragma unroll
+            for (int o = 1; o < LPV; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+          }
+          if (!is_q && ok) {
             const float scale = top / 448.f;
             const uint32_t* x = &p[u].a.x;
             const uint32_t* y = &p[u].b.x;
             uint16_t c[8];
+            if (plain_scale(scale)) {
+              const float recip = 1.f / scale;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float x0 = __uint_as_float(x[i] << 16), x1 = __uint_as_float(x[i] & 0xffff0000u);
-              const float y0 = __uint_as_float(y[i] << 16), y1 = __uint_as_float(y[i] & 0xffff0000u);
-              c[i] = scale > 0.f ? e4m3x2_from_f32(x0 / scale, x1 / scale) : (uint16_t)0;
-              c[4 + i] = scale > 0.f ? e4m3x2_from_f32(y0 / scale, y1 / scale) : (uint16_t)0;
+              for (int i = 0; i < 4; ++i) {
+                float2 f = pair_of(x[i]), g = pair_of(y[i]);
+                quotients(f, scale, recip);
+                quotients(g, scale, recip);
+                c[i] = e4m3x2_from_f32(f.x, f.y);
+                c[4 + i] = e4m3x2_from_f32(g.x, g.y);
+              }
+            } else {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const float2 f = pair_of(x[i]), g = pair_of(y[i]);
+                c[i] = scale > 0.f ? e4m3x2_from_f32(f.x / scale, f.y / scale) : (uint16_t)0;
+                c[4 + i] = scale > 0.f ? e4m3x2_from_f32(g.x / scale, g.y / scale) : (uint16_t)0;
+              }
             }
             uint8_t* dst = reinterpret_cast<uint8_t*>(*pool) + at * D + 8 * j;
             *reinterpret_cast<uint2*>(dst) = make_uint2(c[0] | (uint32_t)c[1] << 16, c[2] | (uint32_t)c[3] << 16);
@@ -228,10 +289,6 @@ __global__ void __launch_bounds__(AWARPS * 32) append_kernel(const AppendArgs a,
   const int key0 = (int)(pidx << 4);
   if (n < 1 || pidx << 4 >= (long long)c0 + n) return;
   const int page = a.bt[(size_t)s * a.max_pages + pidx];
-  if (page < 0 || page >= a.num_pages) {
-    if (lane == 0) atomicOr(a.status, kStatusBadPage);
-    return;
-  }
   const int first = max(0, c0 - key0), last = min(kPageSize, c0 + n - key0);  // the page's new rows
   const bf16* src = (is_v ? a.v + (size_t)c * a.v_step : a.k + (size_t)c * a.k_step) + (size_t)h * D + 8 * j;
   const int ld = is_v ? a.ldv : a.ldk;
@@ -247,10 +304,14 @@ __global__ void __launch_bounds__(AWARPS * 32) append_kernel(const AppendArgs a,
       p[i].b = *reinterpret_cast<const uint4*>(from + D / 2);
     }
   }
+  if (page < 0 || page >= a.num_pages) {
+    if (lane == 0) atomicOr(a.status, kStatusBadPage);
+    return;
+  }
   const long long* pool = pools + (is_v ? a.pool_step : 0) + c;
   float* scale_at = reinterpret_cast<float*>(pool[2 * a.pool_step]) + (size_t)page * a.n_kv + h;
   const float old = first > 0 ? *scale_at : 0.f;
-  float top = 0.f;
+  uint32_t most = 0;
 #pragma unroll
   for (int i = 0; i < STEPS; ++i) {
     const int row = i * VPW + sub;
@@ -259,12 +320,18 @@ __global__ void __launch_bounds__(AWARPS * 32) append_kernel(const AppendArgs a,
       load_angles<D>(a, key0 + row + (a.o_off >= 0 ? off[s] : 0), j, cs);
       turn_piece(p[i], cs);
     }
-    top = fmaxf(top, largest(p[i]));
+    most = max(most, largest(p[i]));
   }
+  most = __reduce_max_sync(0xffffffffu, most);
+  const bool finite = most < 0x7f80u;
+  if (!finite) {  // an infinity counts as the largest bf16, NaN not at all
+    most = 0;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  const float mine = fminf(top, 3.3895314e38f) / 127.f;  // an infinity counts as the largest bf16
-  const float scale = fmaxf(mine, old), by = scale > 0.f ? scale : 1.f;
+    for (int i = 0; i < STEPS; ++i) most = max(most, largest_finite(p[i].a, p[i].b));
+    most = __reduce_max_sync(0xffffffffu, most);
+  }
+  const float scale = fmaxf(bits_to_f32(most) / 127.f, old), by = scale > 0.f ? scale : 1.f, recip = 1.f / by;
+  const bool plain = finite && plain_scale(by);
   uint8_t* dst = reinterpret_cast<uint8_t*>(*pool) + ((size_t)page * a.n_kv + h) * kPageSize * D + 8 * j;
 #pragma unroll
   for (int i = 0; i < STEPS; ++i) {
@@ -272,8 +339,8 @@ __global__ void __launch_bounds__(AWARPS * 32) append_kernel(const AppendArgs a,
     uint2* lo = reinterpret_cast<uint2*>(dst + (size_t)row * D);
     uint2* hi = reinterpret_cast<uint2*>(dst + (size_t)row * D + D / 2);
     if (row >= first && row < last) {
-      *lo = codes8(p[i].a, by);
-      *hi = codes8(p[i].b, by);
+      *lo = plain ? codes8(p[i].a, by, recip) : codes8_any(p[i].a, by);
+      *hi = plain ? codes8(p[i].b, by, recip) : codes8_any(p[i].b, by);
     } else if (row < first && scale > old) {
       const float ratio = old / scale;
       *lo = rescale8(*lo, ratio);
