@@ -32,7 +32,7 @@ constexpr int UNROLL = 4;  // heads in flight per lane
 
 // The last of n entries of the ascending f with f(s) <= v (f(0) <= v), searched by the whole warp.
 template <typename F>
-__device__ __forceinline__ int find_last(int n, long long v, F f) {
+__device__ __forceinline__ int find_last(int n, int v, F f) {
   const int lane = threadIdx.x & 31;
   int lo = 0, len = n;
   while (len > 1) {
@@ -89,6 +89,9 @@ __device__ __noinline__ uint32_t largest_finite(uint4 a, uint4 b) {
   }
   return m;
 }
+__device__ __noinline__ float2 far_angle(const unsigned long long* turns, int pos, int i) {
+  return rope_angle(nullptr, 0, turns, 0, pos, i);
+}
 template <int D>
 __device__ __forceinline__ void load_angles(const AppendArgs& a, int pos, int j, float2* cs) {
   if (pos < a.rope_len) {
@@ -101,7 +104,7 @@ __device__ __forceinline__ void load_angles(const AppendArgs& a, int pos, int j,
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) cs[i] = rope_angle(a.rope_tab, a.rope_len, a.rope_turn, D / 2, pos, 8 * j + i);
+    for (int i = 0; i < 8; ++i) cs[i] = far_angle(a.rope_turn, pos, 8 * j + i);
   }
 }
 
@@ -162,7 +165,7 @@ __device__ __forceinline__ uint2 rescale8(uint2 v, float ratio) {
 }
 
 template <int D, int KIND>
-__global__ void __launch_bounds__(AWARPS * 32) append_kernel(const AppendArgs a, const __grid_constant__ InlineInts inl) {
+__global__ void __launch_bounds__(AWARPS * 32, KIND == kKvInt8 ? 4 : 3) append_kernel(const AppendArgs a, const __grid_constant__ InlineInts inl) {
   constexpr int LPV = D / 16, VPW = 32 / LPV;  // lanes of a head, heads (or rows) of a warp's step
   griddep_launch_dependents();
   griddep_wait();
@@ -170,10 +173,10 @@ __global__ void __launch_bounds__(AWARPS * 32) append_kernel(const AppendArgs a,
   const int *cu = lists + a.o_cu, *ctx = lists + a.o_ctx, *off = lists + a.o_off;
   const long long* const pools = a.pools ? a.pools : reinterpret_cast<const long long*>(lists + a.o_pools);
   const int lane = threadIdx.x & 31, sub = lane / LPV, j = lane % LPV;
-  long long w = (long long)blockIdx.x * AWARPS + (threadIdx.x >> 5);
+  unsigned w = blockIdx.x * AWARPS + (threadIdx.x >> 5);  // fewer than 2^31 warps
   if (w < a.row_warps) {
-    const int t = (int)(w / a.splits), split = (int)(w - (long long)t * a.splits);
-    const int s = find_last(a.P, t, [&](int i) { return (long long)cu[i]; });
+    const int t = (int)(w / (unsigned)a.splits), split = (int)(w - (unsigned)(t * a.splits));
+    const int s = find_last(a.P, t, [&](int i) { return cu[i]; });
     const int row = ctx[s] + t - cu[s], pos = row + (a.o_off >= 0 ? off[s] : 0);
     const int page = KIND == kKvInt8 ? 0 : a.bt[(size_t)s * a.max_pages + (row >> 4)];
     const bool ok = page >= 0 && page < a.num_pages;
@@ -275,19 +278,19 @@ __global__ void __launch_bounds__(AWARPS * 32) append_kernel(const AppendArgs a,
   if (KIND != kKvInt8) return;
   // int8: virtual page x of sequence s, those of a sequence starting at cu[s] / 16 + 2 s: n rows touch at
   // most floor(n / 16) + 2 pages, which is no more than the distance to the next sequence's
-  w -= (a.row_warps + AWARPS - 1) / AWARPS * AWARPS;
-  if (w < 0) return;  // the last block of rows
-  const int per = a.caches * 2 * a.n_kv;
-  const long long x = w / per;
+  const unsigned rows = (a.row_warps + AWARPS - 1) / AWARPS * AWARPS;
+  if (w < rows) return;  // of the last block of rows
+  w -= rows;
+  const unsigned per = (unsigned)(a.caches * 2 * a.n_kv);
+  const int x = (int)(w / per);
   if (x >= a.pages) return;
   const int r = (int)(w - x * per), c = (int)__umulhi((uint32_t)r, a.per_cache), h2 = r - c * 2 * a.n_kv;
   const bool is_v = h2 >= a.n_kv;
   const int h = is_v ? h2 - a.n_kv : h2;
-  const int s = find_last(a.P, x, [&](int i) { return (long long)(cu[i] >> 4) + 2LL * i; });
+  const int s = find_last(a.P, x, [&](int i) { return (cu[i] >> 4) + 2 * i; });
   const int r0 = cu[s], n = cu[s + 1] - r0, c0 = ctx[s];
-  const long long pidx = (c0 >> 4) + (x - (r0 >> 4) - 2LL * s);
-  const int key0 = (int)(pidx << 4);
-  if (n < 1 || pidx << 4 >= (long long)c0 + n) return;
+  const int pidx = (c0 >> 4) + (x - (r0 >> 4) - 2 * s), key0 = pidx << 4;
+  if (n < 1 || key0 >= c0 + n) return;
   const int page = a.bt[(size_t)s * a.max_pages + pidx];
   const int first = max(0, c0 - key0), last = min(kPageSize, c0 + n - key0);  // the page's new rows
   const bf16* src = (is_v ? a.v + (size_t)c * a.v_step : a.k + (size_t)c * a.k_step) + (size_t)h * D + 8 * j;
@@ -352,10 +355,10 @@ __global__ void __launch_bounds__(AWARPS * 32) append_kernel(const AppendArgs a,
 
 template <int D, int KIND>
 cudaError_t launch_kind(const AppendArgs& a, const InlineInts& inl, cudaStream_t s) {
-  const long long rows = (a.row_warps + AWARPS - 1) / AWARPS;
-  const long long pages = KIND == kKvInt8 ? (a.pages * a.caches * 2 * a.n_kv + AWARPS - 1) / AWARPS : 0;
+  const long long rows = ((long long)a.row_warps + AWARPS - 1) / AWARPS;
+  const long long pages = KIND == kKvInt8 ? ((long long)a.pages * a.caches * 2 * a.n_kv + AWARPS - 1) / AWARPS : 0;
   if (rows + pages <= 0) return cudaSuccess;
-  if (rows + pages >= 1LL << 31) return cudaErrorNotSupported;
+  if ((rows + pages) * AWARPS >= 1LL << 31) return cudaErrorNotSupported;
   return launch_pdl(append_kernel<D, KIND>, dim3((unsigned)(rows + pages)), dim3(AWARPS * 32), 0, s, a, inl);
 }
 
@@ -375,8 +378,9 @@ cudaError_t launch_append(AppendArgs a, int kind, int d_head, const InlineInts& 
   const int steps = (vecs + UNROLL * (512 / d_head) - 1) / (UNROLL * (512 / d_head));
   // a token's heads go to several warps until every SM has 16 of them
   a.splits = (int)std::max(1LL, std::min<long long>(steps, (16LL * num_sms + a.T - 1) / a.T));
-  a.row_warps = steps ? (long long)a.T * a.splits : 0;
-  a.pages = kind == kKvInt8 ? (a.T >> 4) + 2LL * a.P : 0;
+  if ((long long)a.T * a.splits >= 1LL << 31) return cudaErrorNotSupported;
+  a.row_warps = steps ? (unsigned)(a.T * a.splits) : 0;
+  a.pages = kind == kKvInt8 ? (a.T >> 4) + 2 * a.P : 0;
   return d_head == 128 ? launch_d<128>(a, kind, inl, s) : launch_d<64>(a, kind, inl, s);
 }
 

@@ -250,8 +250,8 @@ struct AppendArgs {
   int* status;
   // set by launch_append
   uint32_t per_cache;
-  int splits;
-  long long row_warps, pages;
+  int splits, pages;
+  unsigned row_warps;
 };
 // launch_append with the model's shape, rotation and status word.
 cudaError_t launch_append_on(const swiftkv_model* m, AppendArgs a, int kind, const InlineInts& inl, cudaStream_t s);
