@@ -27,8 +27,8 @@ namespace skv {
 
 namespace {
 
-constexpr int AWARPS = 8;
-constexpr int UNROLL = 4;  // heads in flight per lane
+constexpr int AWARPS = 4;
+constexpr int UNROLL = 2;  // heads in flight per lane
 
 // The last of n entries of the ascending f with f(s) <= v (f(0) <= v), searched by the whole warp.
 template <typename F>
@@ -165,7 +165,7 @@ __device__ __forceinline__ uint2 rescale8(uint2 v, float ratio) {
 }
 
 template <int D, int KIND>
-__global__ void __launch_bounds__(AWARPS * 32, KIND == kKvInt8 ? 4 : 3) append_kernel(const AppendArgs a, const __grid_constant__ InlineInts inl) {
+__global__ void __launch_bounds__(AWARPS * 32, 8) append_kernel(const AppendArgs a, const __grid_constant__ InlineInts inl) {
   constexpr int LPV = D / 16, VPW = 32 / LPV;  // lanes of a head, heads (or rows) of a warp's step
   griddep_launch_dependents();
   griddep_wait();
