@@ -67,9 +67,11 @@ constexpr int REGS_ISSUE = 72, REGS_SOFTMAX = 216;  // 72 + 2 x 216 = 3 x 168, t
 constexpr float kGrown = 65536.f;      // a block's row sum from which the running maximum is moved
 constexpr float kLn2 = 0.69314718055994531f;
 
+constexpr int kScaleStages = 8;        // blocks whose scales fit
+
 template <int D>
 struct Cfg {
-  static constexpr int BKV = D == 128 ? 80 : 128;  // keys per block
+  static constexpr int BKV = chunk_block(D);       // keys per block
   static constexpr int PAGES = BKV / kPageSize;
   static constexpr int KST = 3, VST = 3;           // K and V stages
   static constexpr int HALVES = D / 64;
@@ -85,12 +87,17 @@ struct Cfg {
 template <int D>
 struct Ctrl {
   using C = Cfg<D>;
+  static_assert(C::KST + 5 <= kScaleStages, "see the copies of the scales");
   uint64_t q_full, q_empty, k_full[C::KST], k_empty[C::KST], v_full[C::VST], v_empty[C::VST];
   uint64_t s_full[2], s_empty[2], p_full[2], pv_done[2], o_empty[2], fin[2];
   uint32_t tmem_base;
   int abort;
-  int pend[1 + C::KST + C::VST];                  // phases of copies in flight: Q, K stages, V stages
-  alignas(16) float scale[C::VST][2][C::BKV];      // FP8: key scales, value scales; int8: a float4 a page
+  int pend[1 + C::KST + C::VST + kScaleStages];   // phases of copies in flight: Q, K stages, V stages, scales
+  uint64_t sc_full[kScaleStages];
+  union {
+    alignas(16) float scale[kScaleStages][2][C::BKV];  // FP8: a block's key scales, value scales
+    alignas(16) float4 page[kScaleStages][C::PAGES];   // int8: its pages' records
+  };
 };
 template <int D>
 constexpr int smem_bytes() {
@@ -181,11 +188,22 @@ __device__ __forceinline__ void fma2(float* d, const float* x, float c, float m)
       : "=f"(d[0]), "=f"(d[1])
       : "f"(x[0]), "f"(x[1]), "f"(c), "f"(m));
 }
-__device__ __forceinline__ void mul2(float* d, float c) {
-  asm("{\n .reg .b64 a, b;\n mov.b64 a, {%0, %1};\n mov.b64 b, {%2, %2};\n mul.rn.f32x2 a, a, b;\n"
+// the same with both halves of c and m given, and acc[0 .. 1] += p[0 .. 1] * c
+__device__ __forceinline__ void fma2_pair(float* d, const float* x, uint64_t c, uint64_t m) {
+  asm("{\n .reg .b64 a;\n mov.b64 a, {%2, %3};\n fma.rn.f32x2 a, a, %4, %5;\n mov.b64 {%0, %1}, a;\n}\n"
+      : "=f"(d[0]), "=f"(d[1])
+      : "f"(x[0]), "f"(x[1]), "l"(c), "l"(m));
+}
+__device__ __forceinline__ void add2_pair(float* acc, const float* p, uint64_t c) {
+  asm("{\n .reg .b64 a, b;\n mov.b64 a, {%0, %1};\n mov.b64 b, {%2, %3};\n fma.rn.f32x2 a, b, %4, a;\n"
       " mov.b64 {%0, %1}, a;\n}\n"
-      : "+f"(d[0]), "+f"(d[1])
-      : "f"(c));
+      : "+f"(acc[0]), "+f"(acc[1])
+      : "f"(p[0]), "f"(p[1]), "l"(c));
+}
+__device__ __forceinline__ uint64_t both(float x) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %1};" : "=l"(r) : "f"(x));
+  return r;
 }
 __device__ __forceinline__ void add2(float* acc, const float* p) {
   asm("{\n .reg .b64 a, b;\n mov.b64 a, {%0, %1};\n mov.b64 b, {%2, %3};\n add.rn.f32x2 a, a, b;\n"
@@ -202,7 +220,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_chunk_kernel(const __grid_con
                                                                 const __grid_constant__ ChunkArgs a, float scale_log2) {
   using C = Cfg<D>;
   constexpr int BKV = C::BKV, PAGES = C::PAGES, KST = C::KST, VST = C::VST;
-  constexpr bool FP8 = KIND == kKvFp8, INT8 = KIND == kKvInt8;
+  constexpr bool FP8 = KIND == kKvFp8, INT8 = KIND == kKvInt8, CODES = FP8 || INT8;
   extern __shared__ unsigned char smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   unsigned char* smem = smem_raw + ((1024 - (raw & 1023)) & 1023);
@@ -233,7 +251,8 @@ __global__ void __launch_bounds__(THREADS, 1) attn_chunk_kernel(const __grid_con
       mbar_init(bar(ctl->o_empty[t]), 128);
       mbar_init(bar(ctl->fin[t]), 1);
     }
-    for (int i = 0; i < 1 + KST + VST; ++i) ctl->pend[i] = -1;
+    for (int i = 0; i < kScaleStages; ++i) mbar_init(bar(ctl->sc_full[i]), 1);
+    for (int i = 0; i < 1 + KST + VST + kScaleStages; ++i) ctl->pend[i] = -1;
     ctl->abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -267,7 +286,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_chunk_kernel(const __grid_con
       int kv_i = 0;
       int2 pg = make_int2(0, 0);
       bool ok = true, have = item_at<BKV>(0, a, I);
-      if (have) pg = load_page(I, 0);
+      if (have && !CODES) pg = load_page(I, 0);
       for (int it = 0; ok && have; ++it) {
         Item N;
         const bool have_next = item_at<BKV>(it + 1, a, N);
@@ -286,6 +305,45 @@ __global__ void __launch_bounds__(THREADS, 1) attn_chunk_kernel(const __grid_con
                             I.seq0 + (t ? I.q0b : I.q0a), bar(ctl->q_full));
           }
         }
+        if (CODES) {  // a block is one stretch of the expansion
+          const BlockOrder order(I.c0, I.n, a.window, a.sinks, BKV);
+          const int page0 = kvh * a.num_pages + a.exp_first[I.s];
+          for (int j = 0; j < I.nblk; ++j, ++kv_i) {
+            const int st = is_v ? kv_i % VST : kv_i % KST, page = page0 + order.place(I.block(j)) * PAGES;
+            const uint32_t ph = (uint32_t)((is_v ? kv_i / VST : kv_i / KST) & 1);
+            const uint32_t full = is_v ? bar(ctl->v_full[st]) : bar(ctl->k_full[st]);
+            if (!(ok = wait_all(is_v ? bar(ctl->v_empty[st]) : bar(ctl->k_empty[st]), ph ^ 1))) break;
+            // The block's scales come ahead of K, kScaleStages blocks deep. No barrier says that a place is free: K of block kv is asked for once both tiles' S of block kv - KST have been issued, each after
+            // its softmax took S of its block before that into registers, and so was through with the one before.
+            // A place's phases are never two ahead of a reader: the copies of four blocks ago have arrived
+            const int ss = kv_i % kScaleStages, old = kv_i - 4;
+            if (!is_v && old >= 0 &&
+                !(ok = wait_all(bar(ctl->sc_full[old % kScaleStages]), (uint32_t)(old / kScaleStages & 1)))) break;
+            if (elect_lane()) {
+              if (!is_v) {
+                const uint32_t sf = bar(ctl->sc_full[ss]);
+                mbar_expect_tx(sf, FP8 ? 2 * BKV * 4 : PAGES * 16);
+                ctl->pend[1 + KST + VST + ss] = kv_i / kScaleStages & 1;
+                if (FP8) {
+                  bulk_load(smem_u32(&ctl->scale[ss][0][0]), a.k_scale + (size_t)page * kPageSize, BKV * 4, sf);
+                  bulk_load(smem_u32(&ctl->scale[ss][1][0]), a.v_scale + (size_t)page * kPageSize, BKV * 4, sf);
+                } else {
+                  bulk_load(smem_u32(&ctl->page[ss][0]), reinterpret_cast<const float4*>(a.k_scale) + page, PAGES * 16, sf);
+                }
+              }
+              mbar_expect_tx(full, C::KV_TILE);
+              ctl->pend[is_v ? 1 + KST + st : 1 + st] = (int)ph;
+              const uint32_t dst = (is_v ? sV : sK) + st * C::KV_TILE;
+#pragma unroll
+              for (int hf = 0; hf < C::HALVES; ++hf)
+                tma_load_2d(dst + hf * C::KV_HALF, is_v ? &tmV : &tmK, hf * 64, page * kPageSize, full);
+            }
+            __syncwarp();
+          }
+          I = N;
+          have = have_next;
+          continue;
+        }
         for (int j = 0; j < I.nblk; ++j, ++kv_i) {
           int2 next = pg;
           if (j + 1 < I.nblk) next = load_page(I, j + 1);
@@ -298,7 +356,6 @@ __global__ void __launch_bounds__(THREADS, 1) attn_chunk_kernel(const __grid_con
           if (pg.x && !valid) atomicOr(a.status, kStatusBadPage);
           int row = (valid ? pg.y * a.n_kv + kvh : a.num_pages * a.n_kv) * kPageSize;
           const CUtensorMap* map = is_v ? &tmV : &tmK;
-          const size_t sr = valid ? (size_t)row : (size_t)kvh * kPageSize;  // scales of a masked page: page 0's
           if (is_v && a.v_tail && valid) {
             const int pidx = I.block(j) * PAGES + lane;
 #pragma unroll
@@ -310,7 +367,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_chunk_kernel(const __grid_con
           }
           if (!(ok = wait_all(is_v ? bar(ctl->v_empty[st]) : bar(ctl->k_empty[st]), ph ^ 1))) break;
           if (lane == 0) {
-            mbar_expect_tx(full, C::KV_TILE + (!is_v ? 0 : FP8 ? 2 * BKV * 4 : INT8 ? PAGES * 16 : 0));
+            mbar_expect_tx(full, C::KV_TILE);
             ctl->pend[is_v ? 1 + KST + st : 1 + st] = (int)ph;
           }
           __syncwarp();
@@ -318,12 +375,6 @@ __global__ void __launch_bounds__(THREADS, 1) attn_chunk_kernel(const __grid_con
             const uint32_t dst = (is_v ? sV : sK) + st * C::KV_TILE + lane * 2048;
 #pragma unroll
             for (int hf = 0; hf < C::HALVES; ++hf) tma_load_2d(dst + hf * C::KV_HALF, map, hf * 64, row, full);
-            if (is_v && FP8) {
-              const uint32_t sd = smem_u32(&ctl->scale[st][0][lane * kPageSize]);
-              bulk_load(sd, a.k_scale + sr, kPageSize * 4, full);
-              bulk_load(sd + BKV * 4, a.v_scale + sr, kPageSize * 4, full);
-            }
-            if (is_v && INT8) bulk_load(smem_u32(&ctl->scale[st][0][lane * 4]), a.k_scale + sr / kPageSize * 4, 16, full);
           }
           pg = next;
         }
@@ -427,22 +478,31 @@ __global__ void __launch_bounds__(THREADS, 1) attn_chunk_kernel(const __grid_con
       const int first = window_begin(qpos, a.window), last = min(qpos, I.nk - 1), sinks = a.window > 0 ? a.sinks : 0;
       float m = -INFINITY, l = 0.f;
       for (int j = 0; j < nb; ++j, ++g) {
-        if (!(ok = wait(ctl->s_full[t], (uint32_t)(g & 1)))) break;
+        // 8-bit caches: S first and then its scales, both tests in flight (a second wait behind this one cost 65 us of
+        // 455; before S is there the scales' phase says nothing: a tile may run ahead by items that it has no part in)
+        const int ss = (kvb + j) % kScaleStages;
+        if (CODES) {
+          const uint32_t sp = (uint32_t)((kvb + j) / kScaleStages & 1);
+          const bool r0 = mbar_test_wait(bar(ctl->s_full[t]), (uint32_t)(g & 1)), r1 = mbar_test_wait(bar(ctl->sc_full[ss]), sp);
+          const bool done = (r0 && r1) || (mbar_wait(bar(ctl->s_full[t]), (uint32_t)(g & 1), abort_flag) &&
+                                           mbar_wait(bar(ctl->sc_full[ss]), sp, abort_flag));
+          ok = __all_sync(0xffffffffu, done) != 0;
+        } else {
+          ok = wait(ctl->s_full[t], (uint32_t)(g & 1));
+        }
+        if (!ok) break;
         tc_fence_after();
         float x[BKV];
         tmem_ld_row<BKV>(s_addr, x);
         tc_fence_before();
         mbar_arrive(bar(ctl->s_empty[t]));  // S of the next block may be computed
         const float* scales = nullptr;
-        if (INT8) {
-          const int kv = kvb + j, st = kv % VST;
-          if (!(ok = wait(ctl->v_full[st], (uint32_t)((kv / VST) & 1)))) break;
-          scales = ctl->scale[st][0];
+        const float4* pages = nullptr;
+        if (CODES) {
+          scales = ctl->scale[ss][0];
+          pages = ctl->page[ss];
         }
         if (FP8) {
-          const int kv = kvb + j, st = kv % VST;
-          if (!(ok = wait(ctl->v_full[st], (uint32_t)((kv / VST) & 1)))) break;
-          scales = ctl->scale[st][0];
 #pragma unroll
           for (int i = 0; i < BKV; i += 4) {
             const float4 f = *reinterpret_cast<const float4*>(scales + i);
@@ -484,7 +544,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_chunk_kernel(const __grid_con
                 float v = x[16 * c];
 #pragma unroll
                 for (int i = 1; i < 15; i += 2) v = fmax3f(v, x[16 * c + i], x[16 * c + i + 1]);
-                mx = fmaxf(mx, fmaxf(v, x[16 * c + 15]) * scales[4 * c]);
+                mx = fmaxf(mx, fmaxf(v, x[16 * c + 15]) * pages[c].x);
               }
             } else {
             float pm[8];
@@ -509,26 +569,35 @@ __global__ void __launch_bounds__(THREADS, 1) attn_chunk_kernel(const __grid_con
           float sum[8];
 #pragma unroll
           for (int i = 0; i < 8; ++i) sum[i] = 0.f;
+          // int8: the key's scale, the exponent's rest with the value's scale, and what takes that out of the sums
+          uint64_t kc = 0, m2 = 0, out_of_sum = 0;
 #pragma unroll
           for (int i = 0; i < BKV; i += 4) {
+            if (INT8 && i % 16 == 0) {
+              const float4 page = pages[i / 16];
+              kc = both(page.x);
+              m2 = both(mneg + page.y);
+              out_of_sum = both(page.z);
+            }
             float e[4];
 #pragma unroll
-            for (int k = 0; k < 4; k += 2) fma2(e + k, x + i + k, INT8 ? scales[i / 16 * 4] : scale_log2, mneg);
+            for (int k = 0; k < 4; k += 2) {
+              if (INT8) fma2_pair(e + k, x + i + k, kc, m2);
+              else fma2(e + k, x + i + k, scale_log2, mneg);
+            }
 #pragma unroll
             for (int k = 0; k < 4; ++k) e[k] = ex2_approx(e[k]);
 #pragma unroll
-            for (int k = 0; k < 4; k += 2) add2(sum + ((i + k) & 7), e + k);
+            for (int k = 0; k < 4; k += 2) {
+              if (INT8) add2_pair(sum + ((i + k) & 7), e + k, out_of_sum);
+              else add2(sum + ((i + k) & 7), e + k);
+            }
             if (FP8) {
               const float4 w = *reinterpret_cast<const float4*>(scales + BKV + i);
               e[0] *= w.x;
               e[1] *= w.y;
               e[2] *= w.z;
               e[3] *= w.w;
-            }
-            if (INT8) {
-              const float w = scales[i / 16 * 4 + 1];
-#pragma unroll
-              for (int k = 0; k < 4; k += 2) mul2(e + k, w);
             }
             p[i / 2] = pack_bf16(e[0], e[1]);
             p[i / 2 + 1] = pack_bf16(e[2], e[3]);
@@ -558,7 +627,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_chunk_kernel(const __grid_con
       if (ok) ok = wait(ctl->pv_done[t], (uint32_t)((g - 1) & 1));
       if (ok) {
         tc_fence_after();
-        const float inv = (FP8 || INT8 ? 1.f / kValueShift : 1.f) / l;
+        const float inv = (FP8 ? 1.f / kValueShift : INT8 ? 1.f / kPageShift : 1.f) / l;
         const int head = t ? I.hb : I.h;
         if (a.lse && qrow < I.n) a.lse[(size_t)head * a.ldl + I.seq0 + qrow] = (m + log2f(l)) * kLn2;
         bf16* dst = a.out + (size_t)(I.seq0 + min(qrow, I.n - 1)) * a.ldo + (size_t)head * D;
@@ -588,10 +657,11 @@ __global__ void __launch_bounds__(THREADS, 1) attn_chunk_kernel(const __grid_con
   if (*abort_flag) {
     if (threadIdx.x == 0) {
       atomicOr(a.status, kStatusTimeout);
-      for (int i = 0; i < 1 + KST + VST; ++i) {
+      for (int i = 0; i < 1 + KST + VST + kScaleStages; ++i) {
         const int ph = ctl->pend[i];
         if (ph < 0) continue;
-        const uint32_t b = i == 0 ? bar(ctl->q_full) : i <= KST ? bar(ctl->k_full[i - 1]) : bar(ctl->v_full[i - 1 - KST]);
+        const uint32_t b = i == 0 ? bar(ctl->q_full) : i <= KST ? bar(ctl->k_full[i - 1])
+                           : i <= KST + VST ? bar(ctl->v_full[i - 1 - KST]) : bar(ctl->sc_full[i - 1 - KST - VST]);
         const uint64_t t0 = global_ns();
         while (!mbar_try_wait(b, (uint32_t)ph) && global_ns() - t0 < kTimeoutNs) {
         }
@@ -617,9 +687,9 @@ cudaError_t launch_d(const ChunkArgs& a, const bf16* q, int ldq, int T, const bf
   constexpr int smem = smem_bytes<D>();
   static_assert(smem <= 227 * 1024, "shared memory");
   CUtensorMap mq, mk, mv, mt;
-  const int rows = a.num_pages * a.n_kv * kPageSize;
+  const int rows = a.num_pages * a.n_kv * kPageSize, box = KIND == kKvBf16 ? kPageSize : chunk_block(D);
   if (!tma_map_bf16_2d(&mq, q, T, a.n_q * D, ldq, 64, BQ, true) ||
-      !tma_map_bf16_2d(&mk, k, rows, D, D, 64, kPageSize, true) || !tma_map_bf16_2d(&mv, v, rows, D, D, 64, kPageSize, true))
+      !tma_map_bf16_2d(&mk, k, rows, D, D, 64, box, true) || !tma_map_bf16_2d(&mv, v, rows, D, D, 64, box, true))
     return cudaErrorNotSupported;
   mt = mv;
   if (a.v_tail &&

@@ -368,55 +368,74 @@ __global__ void kv_dequant_pages_kernel(const int* __restrict__ items, const int
   }
 }
 
-// 16 int8 codes as bf16 values (exact).
-__device__ __forceinline__ void expand_int8x16(uint4 raw, uint32_t* o) {
-  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+// 8 codes as bf16 values (exact).
+__device__ __forceinline__ void expand_codes8(uint2 raw, uint32_t* o) {
+  uint32_t all[8];
+  expand_codes16(make_uint4(raw.x, raw.y, 0, 0), all);
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < 4; ++i) o[i] = all[i];
+}
+__device__ __forceinline__ void expand_int8x8(uint2 raw, uint32_t* o) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      // 128 + the low seven bits, less 128 or, for negative codes, 256
-      const uint32_t x = __byte_perm(w[i], 0x43434343u, h ? 0x4342 : 0x4140), low = x & 0xff7fff7fu, sign = x & 0xff80ff80u;
-      const __nv_bfloat162 y = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&low), *reinterpret_cast<const __nv_bfloat162*>(&sign));
-      o[2 * i + h] = *reinterpret_cast<const uint32_t*>(&y);
-    }
+  for (int i = 0; i < 4; ++i) {
+    // 128 + the low seven bits, less 128 or, for negative codes, 256
+    const uint32_t x = __byte_perm(i < 2 ? raw.x : raw.y, 0x43434343u, i & 1 ? 0x4342 : 0x4140);
+    const uint32_t low = x & 0xff7fff7fu, sign = x & 0xff80ff80u;
+    const __nv_bfloat162 y = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&low), *reinterpret_cast<const __nv_bfloat162*>(&sign));
+    o[i] = *reinterpret_cast<const uint32_t*>(&y);
+  }
 }
 
-// Item i = (sequence, page index) becomes page i of the expansion.
-template <bool INT8>
-__global__ void kv_expand_seen_kernel(const int* __restrict__ items, const KVPool8 src, int max_pages, int num_pages,
-                                      const int* __restrict__ cu, const int* __restrict__ ctx, int n_kv, int dh,
-                                      int window, int sinks, const KVExpansion dst, int* status) {
+// Item i = (sequence, page index) becomes page i of the expansion, `head_rows` rows a head and `page_rows` a page on.
+// 8 codes a thread and step, so that a warp's store fills its sectors (16 codes with two stores: 28 us for 20000 keys of
+// 8 heads x 128, 41 MB in and 82 out, where this takes 22), eight steps in flight.
+template <int dh, bool INT8>
+__global__ void __launch_bounds__(256) kv_expand_seen_kernel(const int* __restrict__ items, const KVPool8 src, int max_pages,
+                                                             int num_pages, const int* __restrict__ cu,
+                                                             const int* __restrict__ ctx, int n_kv, int window, int sinks,
+                                                             const KVExpansion dst, int head_rows, int page_rows, int* status) {
+  griddep_launch_dependents();
+  griddep_wait();
   const int i = blockIdx.x, s = items[2 * i], pidx = items[2 * i + 1];
-  const int page = src.block_table[(size_t)s * max_pages + pidx];
+  const int page = pidx >= 0 ? src.block_table[(size_t)s * max_pages + pidx] : -1;
   const bool ok = page >= 0 && page < num_pages;
-  if (threadIdx.x == 0) {
-    dst.block_table[(size_t)s * max_pages + pidx] = i;
+  if (threadIdx.x == 0 && pidx >= 0) {
+    if (dst.block_table) dst.block_table[(size_t)s * max_pages + pidx] = i;
     if (!ok) atomicOr(status, kStatusBadPage);
   }
   const TailPages t = tail_pages(ctx[s], cu[s + 1] - cu[s], window, sinks);
-  const int rows = n_kv * kPageSize, per_page = rows * dh;
-  const size_t from = ok ? (size_t)page * per_page : 0, to = (size_t)i * per_page;
-  for (int c = threadIdx.x; c < 2 * per_page / 16; c += blockDim.x) {
-    const int kvsel = c >= per_page / 16;
-    if (kvsel && !dst.v) break;  // K alone
-    const int e = (c - kvsel * (per_page / 16)) * 16;
-    uint32_t o[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    if (ok && t.seen(pidx * kPageSize + e / dh % kPageSize)) {
-      const uint4 codes = *reinterpret_cast<const uint4*>((kvsel ? src.v : src.k) + from + e);
-      if (INT8) expand_int8x16(codes, o);
-      else expand_codes16(codes, o);
+  constexpr int per_row = dh / 8;
+  const int rows = n_kv * kPageSize, chunks = rows * per_row;
+  const uint8_t *k = src.k + (ok ? (size_t)page * rows * dh : 0), *v = src.v + (ok ? (size_t)page * rows * dh : 0);
+  const int total = dst.v ? 2 * chunks : chunks;  // K alone without
+  constexpr int U = 8;
+  for (int c0 = threadIdx.x; c0 < total; c0 += U * 256) {
+    uint2 codes[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int c = c0 + u * 256, e = c < chunks ? c : c - chunks;
+      codes[u] = make_uint2(0, 0);
+      if (c < total && ok && t.seen(pidx * kPageSize + e / per_row % kPageSize))
+        codes[u] = *reinterpret_cast<const uint2*>((c < chunks ? k : v) + (size_t)e * 8);
     }
-    bf16* d = (kvsel ? dst.v : dst.k) + to + e;
-    *reinterpret_cast<uint4*>(d) = make_uint4(o[0], o[1], o[2], o[3]);
-    *reinterpret_cast<uint4*>(d + 8) = make_uint4(o[4], o[5], o[6], o[7]);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int c = c0 + u * 256, e = c < chunks ? c : c - chunks, row = e / per_row;
+      if (c >= total) break;
+      uint32_t o[4];  // (codes of 0 are zeros in both)
+      if (INT8) expand_int8x8(codes[u], o);
+      else expand_codes8(codes[u], o);
+      const size_t to = (size_t)(row / kPageSize) * head_rows + (size_t)i * page_rows + row % kPageSize;
+      *reinterpret_cast<uint4*>((c < chunks ? dst.k : dst.v) + to * dh + e % per_row * 8) = make_uint4(o[0], o[1], o[2], o[3]);
+    }
   }
   if (INT8) {
-    // no scale is 0: it would turn scores of -inf into NaN (where the page's is, all codes are 0 and any scale does)
+    // no key scale is 0: it would turn scores of -inf into NaN (where the page's is, all codes are 0 and any scale does)
     for (int h = threadIdx.x; h < n_kv; h += blockDim.x) {
       const float ks = ok ? src.k_scale[(size_t)page * n_kv + h] : 0.f, vs = ok ? src.v_scale[(size_t)page * n_kv + h] : 0.f;
-      reinterpret_cast<float4*>(dst.k_scale)[(size_t)i * n_kv + h] =
-          make_float4(fmaxf(ks * (1.4426950408889634f / sqrtf((float)dh)), 1.4e-45f), vs * kValueShift, 0.f, 0.f);
+      const float kc = fmaxf(ks * (1.4426950408889634f / sqrtf((float)dh)), 1.4e-45f), vc = vs * kPageShift;
+      const float lv = vc > 0.f ? log2f(vc) : 0.f;
+      reinterpret_cast<float4*>(dst.k_scale)[(size_t)h * (head_rows / kPageSize) + i] = make_float4(kc, lv, exp2f(-lv), 0.f);
     }
     return;
   }
@@ -424,7 +443,8 @@ __global__ void kv_expand_seen_kernel(const int* __restrict__ items, const KVPoo
     const int kvsel = c >= rows, e = c - kvsel * rows;
     if (kvsel && !dst.v) break;
     const bool seen = ok && t.seen(pidx * kPageSize + e % kPageSize);
-    (kvsel ? dst.v_scale : dst.k_scale)[(size_t)i * rows + e] =
+    const size_t to = (size_t)(e / kPageSize) * head_rows + (size_t)i * page_rows + e % kPageSize;
+    (kvsel ? dst.v_scale : dst.k_scale)[to] =
         !seen ? 0.f : kvsel ? kValueShift * src.v_scale[(size_t)page * rows + e] : src.k_scale[(size_t)page * rows + e];
   }
 }
@@ -479,17 +499,19 @@ cudaError_t launch_kv_dequant_pages(const int* items, int num_items, const int* 
   return cudaGetLastError();
 }
 
-cudaError_t launch_kv_expand_seen(const int* items, int num_items, int kind, const KVPool8& src, int max_pages, int num_pages,
-                                  const int* cu, const int* ctx, int n_kv, int d_head, int window, int sinks,
+cudaError_t launch_kv_expand_seen(const int* items, int num_items, int kind, bool by_head, const KVPool8& src, int max_pages,
+                                  int num_pages, const int* cu, const int* ctx, int n_kv, int d_head, int window, int sinks,
                                   const KVExpansion& dst, int* status, cudaStream_t stream) {
   if (num_items <= 0) return cudaSuccess;
-  if (kind == kKvInt8)
-    kv_expand_seen_kernel<true><<<num_items, 256, 0, stream>>>(items, src, max_pages, num_pages, cu, ctx, n_kv, d_head,
-                                                               window, sinks, dst, status);
-  else
-    kv_expand_seen_kernel<false><<<num_items, 256, 0, stream>>>(items, src, max_pages, num_pages, cu, ctx, n_kv, d_head,
-                                                                window, sinks, dst, status);
-  return cudaGetLastError();
+  if (kind == kKvInt8 && !by_head) return cudaErrorNotSupported;
+  const int head_rows = by_head ? num_items * kPageSize : kPageSize, page_rows = by_head ? kPageSize : n_kv * kPageSize;
+  if (d_head != 64 && d_head != 128) return cudaErrorNotSupported;
+  auto run = [&](auto kernel) {
+    return launch_pdl(kernel, dim3(num_items), dim3(256), 0, stream, items, src, max_pages, num_pages, cu, ctx, n_kv, window,
+                      sinks, dst, head_rows, page_rows, status);
+  };
+  if (d_head == 128) return kind == kKvInt8 ? run(kv_expand_seen_kernel<128, true>) : run(kv_expand_seen_kernel<128, false>);
+  return kind == kKvInt8 ? run(kv_expand_seen_kernel<64, true>) : run(kv_expand_seen_kernel<64, false>);
 }
 
 cudaError_t launch_v_tail(const bf16* v_pool, const int* block_table, int max_pages, int num_pages, const int* cu,

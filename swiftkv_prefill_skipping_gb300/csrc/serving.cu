@@ -114,6 +114,22 @@ void list_pages(int s, int c0, int n, int window, int sinks, std::vector<int>* o
     }
 }
 
+// (sequence, page) pairs of the blocks of `bkv` keys that hold a page some row of the chunk sees, in BlockOrder's order;
+// pages nobody sees as -1.
+void list_blocks(int s, int c0, int n, int window, int sinks, int bkv, std::vector<int>* out) {
+  const BlockOrder o(c0, n, window, sinks, bkv);
+  const TailPages t = tail_pages(c0, n, window, sinks);
+  auto put_block = [&](int b) {
+    for (int p = b * (bkv / kPageSize); p < (b + 1) * (bkv / kPageSize); ++p) {
+      const int k0 = p * kPageSize;
+      out->push_back(s);
+      out->push_back(k0 < t.sinks || (k0 + kPageSize > t.first && k0 < t.end) ? p : -1);
+    }
+  };
+  for (int b = 0; b < o.sinks; ++b) put_block(b);
+  for (int b = o.rest; b < o.end; ++b) put_block(b);
+}
+
 void count_work(const int32_t* cu, const int32_t* ctx, const Batch& b, double* keys, double* pairs) {
   for (int i = 0; i < b.P; ++i) {
     const int n = cu[i + 1] - cu[i], c0 = ctx ? ctx[i] : 0;
@@ -144,21 +160,20 @@ void place_expansion(const swiftkv_model* m, Arena* a, int pages, const Batch& b
   const size_t rows = (size_t)pages * m->cfg.n_kv * kPageSize;
   e->k = a->take<bf16>(rows * m->cfg.d_head);
   e->v = with_v ? a->take<bf16>(rows * m->cfg.d_head) : nullptr;
-  // int8: a float4 for each page and head in place of a key's scales
-  e->k_scale = a->take<float>(b.kind == kKvInt8 ? rows / kPageSize * 4 : rows);
+  e->k_scale = a->take<float>(b.kind == kKvInt8 ? rows / kPageSize * 4 : rows);  // int8: a record a page and head
   e->v_scale = with_v && b.kind == kKvFp8 ? a->take<float>(rows) : nullptr;
-  e->block_table = a->take<int>((size_t)b.P * b.max_pages);
+  e->block_table = with_v ? nullptr : a->take<int>((size_t)b.P * b.max_pages);
 }
 
 int expand(swiftkv_model* m, const swiftkv_kv_pages* kv, int c, const Batch& b, const int* items, int num,
-           const int* cu, const int* ctx, const KVExpansion& e, cudaStream_t s) {
+           const int* cu, const int* ctx, bool by_head, const KVExpansion& e, cudaStream_t s) {
   KVPool8 src;
   src.k = static_cast<const uint8_t*>(kv->k_pool[c]);
   src.v = static_cast<const uint8_t*>(kv->v_pool[c]);
   src.k_scale = static_cast<const float*>(kv->k_scale[c]);
   src.v_scale = static_cast<const float*>(kv->v_scale[c]);
   src.block_table = kv->block_table;
-  CK(launch_kv_expand_seen(items, num, b.kind, src, b.max_pages, kv->num_pages, cu, ctx, m->cfg.n_kv, m->cfg.d_head, b.window,
+  CK(launch_kv_expand_seen(items, num, b.kind, by_head, src, b.max_pages, kv->num_pages, cu, ctx, m->cfg.n_kv, m->cfg.d_head, b.window,
                            b.sinks, e, m->status, s));
   return SWIFTKV_OK;
 }
@@ -227,7 +242,8 @@ int AttendPlan::make(const swiftkv_model* m, const int32_t* cu, const int32_t* c
   const auto& c = m->cfg;
   head_pairs = (c.n_q / c.n_kv) % 2 == 0;
   const int tile_rows = head_pairs ? 128 : 256;
-  std::vector<int> cuv(cu, cu + P + 1), ctxv(P, 0), tiles, items, ids, exp_items;
+  std::vector<int> cuv(cu, cu + P + 1), ctxv(P, 0), tiles, items, ids, exp_items, first;
+  if (b.kind != kKvBf16) first.assign(P, 0);
   std::vector<Ranges> seen;
   items.reserve(4 * P);
   ids.reserve(P);
@@ -247,7 +263,10 @@ int AttendPlan::make(const swiftkv_model* m, const int32_t* cu, const int32_t* c
       continue;
     }
     for (int t = 0; t < (n + tile_rows - 1) / tile_rows; ++t) tiles.push_back((i << 16) | t);
-    if (b.kind != kKvBf16) list_pages(i, c0, n, b.window, b.sinks, &exp_items);
+    if (b.kind != kKvBf16) {
+      first[i] = (int)(exp_items.size() / 2);
+      list_blocks(i, c0, n, b.window, b.sinks, chunk_block(c.d_head), &exp_items);
+    }
   }
   // heaviest first: the keys that a tile's last row sees
   auto keys_of = [&](int tl) {
@@ -266,14 +285,17 @@ int AttendPlan::make(const swiftkv_model* m, const int32_t* cu, const int32_t* c
   if (std::max({units.size(), tiles.size(), exp_items.size()}) >= (size_t)1 << 28 ||
       (long long)num_units * c.n_kv >= (1LL << 31) || (long long)num_tiles * c.n_q >= (1LL << 31))
     return fail(SWIFTKV_EUNSUPPORTED, "batch too large");
-  ints.reserve(2 * cuv.size() + tiles.size() + units.size() + exp_items.size() + ubeg.size() + items.size());
+  ints.reserve(3 * cuv.size() + tiles.size() + units.size() + exp_items.size() + ubeg.size() + items.size());
   o_cu = put(&ints, cuv);
   o_ctx = put(&ints, ctxv);
   o_tiles = put(&ints, tiles);
   o_items = put(&ints, items);
   o_units = put(&ints, units);
   o_ubeg = put(&ints, ubeg);
-  o_exp = put(&ints, exp_items);
+  if (num_exp > 0) {
+    o_exp = put(&ints, exp_items);
+    o_first = put(&ints, first);
+  }
   if (m->prof_on) count_work(cu, ctx, b, &keys, &pairs);
   return SWIFTKV_OK;
 }
@@ -303,6 +325,7 @@ int AttendPlan::run(swiftkv_model* m, const swiftkv_kv_pages* kv, int c, const b
     const bf16* v = static_cast<const bf16*>(kv->v_pool[c]);
     t.kind = b.kind;
     t.k_scale = t.v_scale = nullptr;
+    t.exp_first = nullptr;
     t.bt = kv->block_table;
     t.num_pages = kv->num_pages;
     t.v_tail = nullptr;
@@ -310,12 +333,13 @@ int AttendPlan::run(swiftkv_model* m, const swiftkv_kv_pages* kv, int c, const b
     t.cu = dev + o_cu;
     t.ctx = dev + o_ctx;
     if (b.kind != kKvBf16) {
-      RET(expand(m, kv, c, b, dev + o_exp, num_exp, t.cu, t.ctx, exp, s));
+      RET(expand(m, kv, c, b, dev + o_exp, num_exp, t.cu, t.ctx, true, exp, s));
+      t.exp_first = dev + o_first;
       k = exp.k;
       v = exp.v;
       t.k_scale = exp.k_scale;
       t.v_scale = exp.v_scale;
-      t.bt = exp.block_table;
+      t.bt = nullptr;
       t.num_pages = num_exp;
     } else {
       CK(launch_v_tail(v, t.bt, b.max_pages, t.num_pages, t.cu, t.ctx, b.P, g.n_kv, g.d_head, b.window, b.sinks, v_tail, s));
@@ -468,7 +492,7 @@ int WeightsPlan::run(swiftkv_model* m, const swiftkv_kv_pages* kv, int c, const 
                             num_units, m->num_sms, s);
   if (e == cudaSuccess && num_tiles > 0) {
     if ((b.kind == kKvFp8)) {
-      RET(expand(m, kv, c, b, dev + o_exp, num_exp, dev + o_cu, dev + o_ctx, exp, s));
+      RET(expand(m, kv, c, b, dev + o_exp, num_exp, dev + o_cu, dev + o_ctx, false, exp, s));
       e = launch_weights_tc(a, exp.k, exp.k_scale, exp.block_table, num_exp, g.d_head, dev + o_tiles, num_tiles,
                             m->num_sms, s);
     } else {

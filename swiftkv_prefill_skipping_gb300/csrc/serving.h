@@ -42,15 +42,19 @@ __host__ __device__ __forceinline__ TailPages tail_pages(int c0, int n, int wind
 cudaError_t launch_v_tail(const bf16* v_pool, const int* block_table, int max_pages, int num_pages, const int* cu,
                           const int* ctx, int P, int n_kv, int d_head, int window, int sinks, bf16* out,
                           cudaStream_t stream);
-// One FP8 cache, and a dense bf16 copy of the pages a call needs (codes as bf16 values, scales
-// beside them, rows that no row of the sequence's chunk sees as zeros): item i = (sequence, page
-// index) becomes page i, which `dst.block_table`, of the same shape as src's, then names. Dense
-// and per sequence, so that sequences may share pages and the copy is no larger than what is read.
-// Value scales are copied times kValueShift, which whoever multiplies P by them takes back: P times a
-// scale goes to bf16, and value scales near float32's smallest would end up among bf16's subnormals.
+// An 8-bit cache, and a dense bf16 copy of the pages a call needs: codes as bf16 values, scales beside them,
+// rows that no row of the sequence's chunk sees as zeros. Item i = (sequence, page index), page -1: zeros,
+// becomes page i of the copy. Dense and per sequence, so that sequences may share pages and the copy is no larger than
+// what is read. by_head: the copy is [n_kv][items][16][d_head], a head's pages neighbours, so that one TMA copy takes
+// a block of them; else [items][n_kv][16][d_head], and `block_table`, of the same shape as src's, names its pages.
+// FP8: scales [...][16] likewise. Value scales are copied times kValueShift, which whoever multiplies P by them takes
+// back: P times a scale goes to bf16, and value scales near float32's smallest would end up among bf16's subnormals.
+// int8 (by_head): k_scale alone, [n_kv][items] records of a float4: the key scale times log2(e) / sqrt(d_head); lv,
+// the binary logarithm of the value scale times kPageShift, by which exp2's argument rises so that P carries the
+// value scale; 2^-lv; 0. This shift keeps P above float32's smallest for scales down to theirs; scales have to
+// stay below 2^64.
 constexpr float kValueShift = 65536.f;
-// int8: k_scale alone, a float4 for every (page, head): the key scale times log2(e) / sqrt(d_head), the
-// value scale times kValueShift, 0, 0.
+constexpr float kPageShift = 268435456.f;
 struct KVPool8 {
   const uint8_t *k, *v;
   const float *k_scale, *v_scale;
@@ -61,9 +65,24 @@ struct KVExpansion {
   float *k_scale, *v_scale;
   int* block_table;
 };
-cudaError_t launch_kv_expand_seen(const int* items, int num_items, int kind, const KVPool8& src, int max_pages, int num_pages,
-                                  const int* cu, const int* ctx, int n_kv, int d_head, int window, int sinks,
+cudaError_t launch_kv_expand_seen(const int* items, int num_items, int kind, bool by_head, const KVPool8& src, int max_pages,
+                                  int num_pages, const int* cu, const int* ctx, int n_kv, int d_head, int window, int sinks,
                                   const KVExpansion& dst, int* status, cudaStream_t stream);
+
+// Keys of a block of the tcgen05 attention, and where a sequence's blocks are in the expansion, behind its first:
+// those of the sinks, then the others.
+__host__ __device__ constexpr int chunk_block(int d_head) { return d_head == 128 ? 80 : 128; }
+struct BlockOrder {
+  int sinks, rest, end;  // blocks of the sinks alone; first of the others; past the last
+  __host__ __device__ BlockOrder(int c0, int n, int window, int num_sinks, int bkv) {
+    const TailPages t = tail_pages(c0, n, window, num_sinks);
+    sinks = t.sinks > 0 && t.sinks < t.first ? (t.sinks + bkv - 1) / bkv : 0;
+    rest = t.sinks >= t.first ? 0 : t.first / bkv > sinks ? t.first / bkv : sinks;
+    end = (t.end + bkv - 1) / bkv;
+  }
+  __host__ __device__ int place(int block) const { return block < sinks ? block : block - rest + sinks; }
+  __host__ __device__ int count() const { return place(end); }
+};
 
 // kv_dtype of a cache
 constexpr int kKvBf16 = 0, kKvFp8 = 1, kKvInt8 = 2;
@@ -108,7 +127,7 @@ struct AttendPlan {
   bool head_pairs = false;
   // host lists, and their places in one device upload
   std::vector<int> ints;
-  int o_cu = 0, o_ctx = 0, o_tiles = 0, o_items = 0, o_units = 0, o_ubeg = 0, o_exp = 0;
+  int o_cu = 0, o_ctx = 0, o_tiles = 0, o_items = 0, o_units = 0, o_ubeg = 0, o_exp = 0, o_first = 0;
   int num_tiles = 0, num_items = 0, max_cols = 0, num_units = 0, num_exp = 0;
   // device (lists: null where the kernels take them inline)
   int* dev = nullptr;
@@ -153,8 +172,9 @@ struct WeightsPlan {
 // (an item is a tile for one head, num_items = tiles * n_q).
 struct ChunkArgs {
   int kind;                        // kv_dtype
-  const float *k_scale, *v_scale;  // FP8: the expansion's scales; int8: k_scale alone, its float4 a block
-  const int* bt;
+  const float *k_scale, *v_scale;  // 8-bit caches: the expansion's
+  const int* exp_first;            // 8-bit caches: [P] each sequence's first page in the expansion of num_pages pages
+  const int* bt;                   // bf16 cache
   int max_pages, num_pages;
   const int *cu, *ctx, *tiles;
   int num_items;
