@@ -132,6 +132,14 @@ def test_pages_of_any_size(heads, new, ctx):
     Case(heads, new, ctx, seed=36, kmul=(0.0,)).check()
 
 
+@pytest.mark.parametrize("heads", ["gqa5", "gqa4", "d64"])
+def test_more_items_than_ctas(heads):
+    """CTAs walk several items, of which the second tile takes part in some only (odd groups)."""
+    n = {"gqa5": 44, "gqa4": 24, "d64": 48}[heads]
+    Case(heads, [100, 300, 5, 260] * (n // 4), [(37 * i) % 500 for i in range(n)], seed=50).check()
+    Case(heads, [100, 300, 5, 260] * (n // 4), [(37 * i) % 500 for i in range(n)], 90, 20, seed=51).check()
+
+
 @pytest.mark.parametrize("heads", ["gqa4", "d64"])
 def test_queries_of_any_size(heads):
     for new, ctx in (([1, 2], [300, 64]), ([70], [100])):
@@ -266,6 +274,25 @@ def test_window_and_chained_rows(impl):
         for s in range(2):
             _, ref = OM.swiftkv_decode_step(cfg, w, refs[s][0], toks[s], l, g)
             assert np.abs(lg[s].cpu().numpy() - ref).max() <= LOGIT_ABS_TOL
+    assert m.status() == 0
+    m.free()
+
+
+@pytest.mark.parametrize("gemm,fused", [(1, 0), (2, 0), (0, 1)])
+def test_other_gemm_families(gemm, fused):
+    """Every family hands its rows to the same pages; the fused norm rounds elsewhere (one more bf16 step)."""
+    import torch
+    from swiftkv_prefill_skipping_gb300 import api
+    m, kv, batch, prompts, cfg, w, l, g = setup("d128", [150, 30])
+    B.check(B.lib().swiftkv_set_gemm_impl(m.handle, gemm))
+    B.check(B.lib().swiftkv_set_norm_fusion(m.handle, fused))
+    logits = api.prefill(m, torch.as_tensor(batch.tokens, device="cuda"), batch.cu_seqlens, kv)
+    with OM.kv_cache_int8():
+        for s, p in enumerate(prompts):
+            caches, ref = OM.swiftkv_prefill_one(cfg, w, p, l, g)
+            assert np.abs(logits[s].cpu().numpy() - ref).max() <= LOGIT_ABS_TOL
+            got = kv.gather(0, s, len(p), "v").cpu().numpy()
+            assert np.linalg.norm(got - caches[0][1]) <= 2e-2 * np.linalg.norm(caches[0][1])
     assert m.status() == 0
     m.free()
 
