@@ -125,6 +125,9 @@ __global__ void __launch_bounds__(Rg<D, KIND>::WARPS * 32, 1) attn_rows_kernel(
     const unsigned char* __restrict__ vpool, const float* __restrict__ kscale, const float* __restrict__ vscale,
     float scale_log2) {
   using S = Rg<D, KIND>;
+  // pages a step: two int8 pages for 8 columns (64 rows of 3000 keys 88.6 -> 86.1 us; with 16 columns 39 -> 43, they spill)
+  constexpr int PG = KIND == kKvInt8 && NT == 1 ? 2 : 1;
+  static_assert(S::SLOTS >= 2 * PG, "ring");
   constexpr bool FP8 = KIND == kKvFp8, INT8 = KIND == kKvInt8, CODES = FP8 || INT8;
   extern __shared__ __align__(128) unsigned char smem[];
   griddep_launch_dependents();
@@ -206,7 +209,7 @@ __global__ void __launch_bounds__(Rg<D, KIND>::WARPS * 32, 1) attn_rows_kernel(
     cp_async_commit();  // possibly empty: keeps the group count uniform
   };
 #pragma unroll
-  for (int i = 0; i < S::SLOTS - 1; ++i) issue();
+  for (int i = 0; i < S::SLOTS - PG; ++i) issue();
 
   const int g0 = lane >> 2, qd = lane & 3;
   uint32_t qf[NT][D / 16][2];
@@ -220,10 +223,19 @@ __global__ void __launch_bounds__(Rg<D, KIND>::WARPS * 32, 1) attn_rows_kernel(
   Geo cg;
   if (cv < total) cg = geo(cv);
   while (cv < total) {
-    issue();
-    cp_async_wait<S::SLOTS - 1>();
+    // as far as the unit goes; a page that is not there repeats the first, hidden
+    const int np = PG == 1 ? 1 : min(PG, cg.npages - cp);
+#pragma unroll
+    for (int p = 0; p < PG; ++p)
+      if (p < np) issue();
+    cp_async_wait<S::SLOTS - PG>();
     __syncwarp();
-    const unsigned char* st = ring + cslot * S::STAGE;
+    const unsigned char* sp[PG];
+#pragma unroll
+    for (int p = 0; p < PG; ++p) {
+      const int slot = cslot + (p < np ? p : 0);
+      sp[p] = ring + (slot >= S::SLOTS ? slot - S::SLOTS : slot) * S::STAGE;
+    }
     if (cp == 0) {  // a new unit: Q as B operands straight from memory, fresh softmax state
       const int* it = items + 4 * cg.item;
       row0 = it[0];
@@ -261,85 +273,94 @@ __global__ void __launch_bounds__(Rg<D, KIND>::WARPS * 32, 1) attn_rows_kernel(
       }
     }
 
-    // S^T = K Q^T: keys g0, g0 + 8 (rows) x columns 2 qd, 2 qd + 1, in two independent chains
-    float s[NT][2][4];
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-      for (int c = 0; c < 2; ++c)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[t][c][e] = 0.f;
+    // S^T = K Q^T: keys g0, g0 + 8 (rows) x columns 2 qd, 2 qd + 1, in two independent chains a page
+    float z[PG][NT][4];  // scaled scores: [0] key g0 col 0, [1] key g0 col 1, [2], [3] key g0 + 8
+    float v_lo[PG], v_hi[PG];  // codes: the shifted value scales of keys g0, g0 + 8 (0 outside the unit)
     const int krow = (lane & 7) + ((lane >> 3) & 1) * 8;
-    if (CODES) {
 #pragma unroll
-      for (int ks = 0; ks < D / 16; ks += 2) {
-        uint32_t r[4];  // keys 0-7 and 8-15 of chunk ks, then of chunk ks + 1
-        ldmatrix_x4(smem_u32(st + swz(krow, ks + (lane >> 4))), r[0], r[1], r[2], r[3]);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t ka[4];
-          if (INT8) {
-            unpack4_int8(r[2 * h], ka[0], ka[2]);
-            unpack4_int8(r[2 * h + 1], ka[1], ka[3]);
-          } else {
-            unpack4(r[2 * h], ka[0], ka[2]);
-            unpack4(r[2 * h + 1], ka[1], ka[3]);
-          }
-#pragma unroll
-          for (int t = 0; t < NT; ++t) mma_f16_16816(s[t][h], ka, qf[t][ks + h]);
-        }
-      }
-    } else {
-#pragma unroll
-      for (int ks = 0; ks < D / 16; ++ks) {
-        uint32_t ka[4];
-        ldmatrix_x4(smem_u32(st + swz(krow, ks * 2 + (lane >> 4))), ka[0], ka[1], ka[2], ka[3]);
-#pragma unroll
-        for (int t = 0; t < NT; ++t) mma_bf16_16816(s[t][ks & 1], ka, qf[t][ks]);
-      }
-    }
-    const int key0 = (cg.p0 + cp) * kPageSize;
-    const float* sc = reinterpret_cast<const float*>(st + 2 * S::PAGE);  // FP8: 16 key, 16 value scales
-    const float* page_sc = reinterpret_cast<const float*>(st + S::STAGE - 12);  // int8: the page's
-    const float c_lo = FP8 ? kCodeScale * scale_log2 * sc[g0] : INT8 ? scale_log2 * page_sc[0] : scale_log2;
-    const float c_hi = FP8 ? kCodeScale * scale_log2 * sc[g0 + 8] : c_lo;
-    // every key of the page visible to every column
-    const bool inside = *reinterpret_cast<const int*>(st + S::STAGE - 16) && key0 >= cg.k0 && key0 + kPageSize <= cg.k1 &&
-                        key0 + kPageSize - 1 <= pos_lo &&
-                        (a.window <= 0 || key0 > pos_hi - a.window || key0 + kPageSize <= a.sinks);
-    float z[NT][4];  // scaled scores: [0] key g0 col 0, [1] key g0 col 1, [2], [3] key g0 + 8
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) z[t][e] = (s[t][0][e] + s[t][1][e]) * ((e < 2 ? c_lo : c_hi) * (CODES ? qback[t][e & 1] : 1.f));
-    if (!inside) {
-      const bool ok = *reinterpret_cast<const int*>(st + S::STAGE - 16);
+    for (int p = 0; p < PG; ++p) {
+      const unsigned char* st = sp[p];
+      float s[NT][2][4];
 #pragma unroll
       for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int key = key0 + g0 + (e < 2 ? 0 : 8);
-          if (!(ok && key >= cg.k0 && key < cg.k1 && attn_visible(key, qpos[t][e & 1], a.window, a.sinks))) z[t][e] = -INFINITY;
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[t][c][e] = 0.f;
+      if (CODES) {
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ks += 2) {
+          uint32_t r[4];  // keys 0-7 and 8-15 of chunk ks, then of chunk ks + 1
+          ldmatrix_x4(smem_u32(st + swz(krow, ks + (lane >> 4))), r[0], r[1], r[2], r[3]);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t ka[4];
+            if (INT8) {
+              unpack4_int8(r[2 * h], ka[0], ka[2]);
+              unpack4_int8(r[2 * h + 1], ka[1], ka[3]);
+            } else {
+              unpack4(r[2 * h], ka[0], ka[2]);
+              unpack4(r[2 * h + 1], ka[1], ka[3]);
+            }
+#pragma unroll
+            for (int t = 0; t < NT; ++t) mma_f16_16816(s[t][h], ka, qf[t][ks + h]);
+          }
         }
+      } else {
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+          uint32_t ka[4];
+          ldmatrix_x4(smem_u32(st + swz(krow, ks * 2 + (lane >> 4))), ka[0], ka[1], ka[2], ka[3]);
+#pragma unroll
+          for (int t = 0; t < NT; ++t) mma_bf16_16816(s[t][ks & 1], ka, qf[t][ks]);
+        }
+      }
+      const int key0 = (cg.p0 + cp + p) * kPageSize;
+      const float* sc = reinterpret_cast<const float*>(st + 2 * S::PAGE);  // FP8: 16 key, 16 value scales
+      const float* page_sc = reinterpret_cast<const float*>(st + S::STAGE - 12);  // int8: the page's
+      const float c_lo = FP8 ? kCodeScale * scale_log2 * sc[g0] : INT8 ? scale_log2 * page_sc[0] : scale_log2;
+      const float c_hi = FP8 ? kCodeScale * scale_log2 * sc[g0 + 8] : c_lo;
+      const bool ok = *reinterpret_cast<const int*>(st + S::STAGE - 16) && p < np;
+      // every key of the page visible to every column
+      const bool inside = ok && key0 >= cg.k0 && key0 + kPageSize <= cg.k1 && key0 + kPageSize - 1 <= pos_lo &&
+                          (a.window <= 0 || key0 > pos_hi - a.window || key0 + kPageSize <= a.sinks);
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          z[p][t][e] = (s[t][0][e] + s[t][1][e]) * ((e < 2 ? c_lo : c_hi) * (CODES ? qback[t][e & 1] : 1.f));
+      if (!inside) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int key = key0 + g0 + (e < 2 ? 0 : 8);
+            if (!(ok && key >= cg.k0 && key < cg.k1 && attn_visible(key, qpos[t][e & 1], a.window, a.sinks))) z[p][t][e] = -INFINITY;
+          }
+      }
+      v_lo[p] = v_hi[p] = 1.f;
+      if (FP8) {
+        v_lo[p] = key0 + g0 >= cg.k0 && key0 + g0 < cg.k1 && p < np ? kValueShift * sc[kPageSize + g0] : 0.f;
+        v_hi[p] = key0 + g0 + 8 >= cg.k0 && key0 + g0 + 8 < cg.k1 && p < np ? kValueShift * sc[kPageSize + g0 + 8] : 0.f;
+      }
+      if (INT8) v_lo[p] = v_hi[p] = kValueShift * page_sc[1];
     }
-    float v_lo = 1.f, v_hi = 1.f;  // FP8: the shifted value scales of keys g0, g0 + 8 (0 outside the unit)
-    if (FP8) {
-      v_lo = key0 + g0 >= cg.k0 && key0 + g0 < cg.k1 ? kValueShift * sc[kPageSize + g0] : 0.f;
-      v_hi = key0 + g0 + 8 >= cg.k0 && key0 + g0 + 8 < cg.k1 ? kValueShift * sc[kPageSize + g0 + 8] : 0.f;
-    }
-    if (INT8) v_lo = v_hi = kValueShift * page_sc[1];
     bool move = false;
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
+    for (int p = 0; p < PG; ++p)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) move |= fmaxf(z[t][e], z[t][e + 2]) > m[t][e] + kLag;
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) move |= fmaxf(z[p][t][e], z[p][t][e + 2]) > m[t][e] + kLag;
     if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         float al[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          float mx = fmaxf(z[t][e], z[t][e + 2]);
+          float mx = fmaxf(z[0][t][e], z[0][t][e + 2]);
+#pragma unroll
+          for (int p = 1; p < PG; ++p) mx = fmaxf(mx, fmaxf(z[p][t][e], z[p][t][e + 2]));
 #pragma unroll
           for (int o2 = 4; o2 <= 16; o2 <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o2));
           const float mn = mx > m[t][e] + kLag ? mx : m[t][e];
@@ -354,64 +375,69 @@ __global__ void __launch_bounds__(Rg<D, KIND>::WARPS * 32, 1) attn_rows_kernel(
       }
     }
     // P^T as B operands: rows of 8 keys become columns by a transpose within the warp
-    uint32_t ph[NT][2], pl[NT][2];
+    uint32_t ph[PG][NT][2], pl[PG][NT][2];
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      float p[4];
+    for (int p = 0; p < PG; ++p)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) p[e] = ex2_approx(z[t][e] - (m[t][e & 1] == -INFINITY ? 0.f : m[t][e & 1]));
-      l[t][0] += p[0] + p[2];
-      l[t][1] += p[1] + p[3];
-      uint32_t h0, l0, h1, l1;
-      split_pair_bf16(p[0] * v_lo, p[1] * v_lo, h0, l0);
-      split_pair_bf16(p[2] * v_hi, p[3] * v_hi, h1, l1);
-      ph[t][0] = transpose8(h0);
-      ph[t][1] = transpose8(h1);
-      pl[t][0] = transpose8(l0);
-      pl[t][1] = transpose8(l1);
-    }
-    // O^T += V^T P^T. bf16: tile i holds dims 16 i + row. FP8: ldmatrix.trans yields two keys x two
+      for (int t = 0; t < NT; ++t) {
+        float w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w[e] = ex2_approx(z[p][t][e] - (m[t][e & 1] == -INFINITY ? 0.f : m[t][e & 1]));
+        l[t][0] += w[0] + w[2];
+        l[t][1] += w[1] + w[3];
+        uint32_t h0, l0, h1, l1;
+        split_pair_bf16(w[0] * v_lo[p], w[1] * v_lo[p], h0, l0);
+        split_pair_bf16(w[2] * v_hi[p], w[3] * v_hi[p], h1, l1);
+        ph[p][t][0] = transpose8(h0);
+        ph[p][t][1] = transpose8(h1);
+        pl[p][t][0] = transpose8(l0);
+        pl[p][t][1] = transpose8(l1);
+      }
+    // O^T += V^T P^T. bf16: tile i holds dims 16 i + row. Codes: ldmatrix.trans yields two keys x two
     // neighbouring dims, so rows 0-7 are the even dims of the chunk and rows 8-15 the odd ones
-    const unsigned char* vb = st + S::PAGE;
     if (CODES) {
 #pragma unroll
-      for (int c = 0; c < D / 16; c += 2) {
-        uint32_t r[4];  // keys 0-7 and 8-15 of chunk c, then of chunk c + 1
-        ldmatrix_x4_trans(smem_u32(vb + swz(krow, c + (lane >> 4))), r[0], r[1], r[2], r[3]);
+      for (int c = 0; c < D / 16; c += 2)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t va[4];
-          if (INT8) {
-            unpack4_int8_bf16(r[2 * h], va[0], va[1]);
-            unpack4_int8_bf16(r[2 * h + 1], va[2], va[3]);
-          } else {
-            unpack4_bf16(r[2 * h], va[0], va[1]);
-            unpack4_bf16(r[2 * h + 1], va[2], va[3]);
-          }
+        for (int p = 0; p < PG; ++p) {
+          uint32_t r[4];  // keys 0-7 and 8-15 of chunk c, then of chunk c + 1
+          ldmatrix_x4_trans(smem_u32(sp[p] + S::PAGE + swz(krow, c + (lane >> 4))), r[0], r[1], r[2], r[3]);
 #pragma unroll
-          for (int t = 0; t < NT; ++t) {
-            mma_bf16_16816(o[t][c + h], va, ph[t]);
-            mma_bf16_16816(o[t][c + h], va, pl[t]);
+          for (int h = 0; h < 2; ++h) {
+            uint32_t va[4];
+            if (INT8) {
+              unpack4_int8_bf16(r[2 * h], va[0], va[1]);
+              unpack4_int8_bf16(r[2 * h + 1], va[2], va[3]);
+            } else {
+              unpack4_bf16(r[2 * h], va[0], va[1]);
+              unpack4_bf16(r[2 * h + 1], va[2], va[3]);
+            }
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+              mma_bf16_16816(o[t][c + h], va, ph[p][t]);
+              mma_bf16_16816(o[t][c + h], va, pl[p][t]);
+            }
           }
         }
-      }
     } else {
       const int vrow = (lane & 7) + ((lane >> 4) & 1) * 8;
 #pragma unroll
       for (int i = 0; i < D / 16; ++i) {
         uint32_t va[4];  // (dims 0-7, keys 0-7), (dims 8-15, keys 0-7), (dims 0-7, keys 8-15), ...
-        ldmatrix_x4_trans(smem_u32(vb + swz(vrow, i * 2 + ((lane >> 3) & 1))), va[0], va[1], va[2], va[3]);
+        ldmatrix_x4_trans(smem_u32(sp[0] + S::PAGE + swz(vrow, i * 2 + ((lane >> 3) & 1))), va[0], va[1], va[2], va[3]);
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-          mma_bf16_16816(o[t][i], va, ph[t]);
-          mma_bf16_16816(o[t][i], va, pl[t]);
+          mma_bf16_16816(o[t][i], va, ph[0][t]);
+          mma_bf16_16816(o[t][i], va, pl[0][t]);
         }
       }
     }
-    __syncwarp();  // the slot is refilled by a later issue()
-    if (++cslot == S::SLOTS) cslot = 0;
+    __syncwarp();  // the slots are refilled by later issues
+    cslot += np;
+    if (cslot >= S::SLOTS) cslot -= S::SLOTS;
 
-    if (++cp == cg.npages) {
+    cp += np;
+    if (cp == cg.npages) {
       const bool whole = ubeg[cg.item + 1] - ubeg[cg.item] == 1;
       const int u = (int)(cv / a.n_kv);
 #pragma unroll
