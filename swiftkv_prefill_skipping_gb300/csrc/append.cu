@@ -18,6 +18,7 @@
 //   Pages (K and V of an int8 cache): a warp takes one (page, cache, K or V, head): its new rows stay in
 //   registers between the maximum and the codes. One warp owns the block, so a repeated call repeats its bits.
 #include <algorithm>
+#include <type_traits>
 
 #include "common.cuh"
 #include "pdl.cuh"
@@ -92,9 +93,9 @@ __device__ __noinline__ uint32_t largest_finite(uint4 a, uint4 b) {
 __device__ __noinline__ float2 far_angle(const unsigned long long* turns, int pos, int i) {
   return rope_angle(nullptr, 0, turns, 0, pos, i);
 }
-template <int D>
+template <int D, bool NEAR>
 __device__ __forceinline__ void load_angles(const AppendArgs& a, int pos, int j, float2* cs) {
-  if (pos < a.rope_len) {
+  if (NEAR || pos < a.rope_len) {
     const float4* t = reinterpret_cast<const float4*>(a.rope_tab + (size_t)pos * (D / 2) + 8 * j);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -182,7 +183,7 @@ __global__ void __launch_bounds__(AWARPS * 32, 8) append_kernel(const AppendArgs
     const bool ok = page >= 0 && page < a.num_pages;
     if (!ok && lane == 0 && split == 0) atomicOr(a.status, kStatusBadPage);
     float2 cs[8];
-    if (a.rotate) load_angles<D>(a, pos, j, cs);
+    if (a.rotate) load_angles<D, false>(a, pos, j, cs);
     const int nq = a.q ? a.n_q : 0, nvec = nq + (KIND == kKvInt8 ? 0 : a.caches * 2 * a.n_kv);
     // vectors in order: the query heads, then K heads and V heads of each cache
     for (int v0 = split * UNROLL * VPW; v0 < nvec; v0 += a.splits * UNROLL * VPW) {
@@ -294,63 +295,85 @@ __global__ void __launch_bounds__(AWARPS * 32, 8) append_kernel(const AppendArgs
   const int page = a.bt[(size_t)s * a.max_pages + pidx];
   const int first = max(0, c0 - key0), last = min(kPageSize, c0 + n - key0);  // the page's new rows
   const bf16* src = (is_v ? a.v + (size_t)c * a.v_step : a.k + (size_t)c * a.k_step) + (size_t)h * D + 8 * j;
-  const int ld = is_v ? a.ldv : a.ldk;
-  constexpr int STEPS = kPageSize / VPW;
-  Piece p[STEPS];
-#pragma unroll
-  for (int i = 0; i < STEPS; ++i) {
-    const int row = i * VPW + sub;
-    p[i].a = p[i].b = make_uint4(0, 0, 0, 0);
-    if (row >= first && row < last) {
-      const bf16* from = src + (size_t)(r0 + key0 + row - c0) * ld;
-      p[i].a = *reinterpret_cast<const uint4*>(from);
-      p[i].b = *reinterpret_cast<const uint4*>(from + D / 2);
-    }
-  }
-  if (page < 0 || page >= a.num_pages) {
-    if (lane == 0) atomicOr(a.status, kStatusBadPage);
-    return;
-  }
+  const long long ld = is_v ? a.ldv : a.ldk;
+  src += (r0 + key0 - c0) * ld;  // of the page's first row, which may lie before the batch's
   const long long* pool = pools + (is_v ? a.pool_step : 0) + c;
-  float* scale_at = reinterpret_cast<float*>(pool[2 * a.pool_step]) + (size_t)page * a.n_kv + h;
-  const float old = first > 0 ? *scale_at : 0.f;
-  uint32_t most = 0;
+  const bool turned = !is_v && a.rotate;
+  const int pos0 = key0 + (a.o_off >= 0 ? off[s] : 0);
+  // all 16 rows new, near and plain (most pages of a prompt): no row needs a look of its own
+  auto block = [&](auto whole_) {
+    constexpr bool WHOLE = decltype(whole_)::value;
+    constexpr int STEPS = kPageSize / VPW;
+    Piece p[STEPS];
 #pragma unroll
-  for (int i = 0; i < STEPS; ++i) {
-    const int row = i * VPW + sub;
-    if (!is_v && a.rotate && row >= first && row < last) {
-      float2 cs[8];
-      load_angles<D>(a, key0 + row + (a.o_off >= 0 ? off[s] : 0), j, cs);
-      turn_piece(p[i], cs);
+    for (int i = 0; i < STEPS; ++i) {
+      const int row = i * VPW + sub;
+      p[i].a = p[i].b = make_uint4(0, 0, 0, 0);
+      if (WHOLE || (row >= first && row < last)) {
+        const bf16* from = src + row * ld;
+        p[i].a = *reinterpret_cast<const uint4*>(from);
+        p[i].b = *reinterpret_cast<const uint4*>(from + D / 2);
+      }
     }
-    most = max(most, largest(p[i]));
-  }
-  most = __reduce_max_sync(0xffffffffu, most);
-  const bool finite = most < 0x7f80u;
-  if (!finite) {  // an infinity counts as the largest bf16, NaN not at all
-    most = 0;
+    if (page < 0 || page >= a.num_pages) {
+      if (lane == 0) atomicOr(a.status, kStatusBadPage);
+      return;
+    }
+    float* scale_at = reinterpret_cast<float*>(pool[2 * a.pool_step]) + (size_t)page * a.n_kv + h;
+    const float old = !WHOLE && first > 0 ? *scale_at : 0.f;
+    uint32_t most = 0;
 #pragma unroll
-    for (int i = 0; i < STEPS; ++i) most = max(most, largest_finite(p[i].a, p[i].b));
+    for (int i = 0; i < STEPS; ++i) {
+      const int row = i * VPW + sub;
+      if (turned && (WHOLE || (row >= first && row < last))) {
+        float2 cs[8];
+        load_angles<D, WHOLE>(a, pos0 + row, j, cs);
+        turn_piece(p[i], cs);
+      }
+      most = max(most, largest(p[i]));
+    }
     most = __reduce_max_sync(0xffffffffu, most);
-  }
-  const float scale = fmaxf(bits_to_f32(most) / 127.f, old), by = scale > 0.f ? scale : 1.f, recip = 1.f / by;
-  const bool plain = finite && plain_scale(by);
-  uint8_t* dst = reinterpret_cast<uint8_t*>(*pool) + ((size_t)page * a.n_kv + h) * kPageSize * D + 8 * j;
+    const bool finite = most < 0x7f80u;
+    if (!finite) {  // an infinity counts as the largest bf16, NaN not at all
+      most = 0;
 #pragma unroll
-  for (int i = 0; i < STEPS; ++i) {
-    const int row = i * VPW + sub;
-    uint2* lo = reinterpret_cast<uint2*>(dst + (size_t)row * D);
-    uint2* hi = reinterpret_cast<uint2*>(dst + (size_t)row * D + D / 2);
-    if (row >= first && row < last) {
-      *lo = plain ? codes8(p[i].a, by, recip) : codes8_any(p[i].a, by);
-      *hi = plain ? codes8(p[i].b, by, recip) : codes8_any(p[i].b, by);
-    } else if (row < first && scale > old) {
-      const float ratio = old / scale;
-      *lo = rescale8(*lo, ratio);
-      *hi = rescale8(*hi, ratio);
+      for (int i = 0; i < STEPS; ++i) most = max(most, largest_finite(p[i].a, p[i].b));
+      most = __reduce_max_sync(0xffffffffu, most);
     }
-  }
-  if (lane == 0 && (first == 0 || scale > old)) *scale_at = scale;
+    const float scale = fmaxf(bits_to_f32(most) / 127.f, old), by = scale > 0.f ? scale : 1.f, recip = 1.f / by;
+    uint8_t* dst = reinterpret_cast<uint8_t*>(*pool) + ((size_t)page * a.n_kv + h) * kPageSize * D + 8 * j;
+    if (finite && plain_scale(by)) {
+#pragma unroll
+      for (int i = 0; i < STEPS; ++i) {
+        const int row = i * VPW + sub;
+        if (WHOLE || (row >= first && row < last)) {
+          *reinterpret_cast<uint2*>(dst + row * D) = codes8(p[i].a, by, recip);
+          *reinterpret_cast<uint2*>(dst + row * D + D / 2) = codes8(p[i].b, by, recip);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < STEPS; ++i) {
+        const int row = i * VPW + sub;
+        if (WHOLE || (row >= first && row < last)) {
+          *reinterpret_cast<uint2*>(dst + row * D) = codes8_any(p[i].a, by);
+          *reinterpret_cast<uint2*>(dst + row * D + D / 2) = codes8_any(p[i].b, by);
+        }
+      }
+    }
+    if (!WHOLE && scale > old) {
+      const float ratio = old / scale;
+      for (int row = sub; row < first; row += VPW) {
+        uint2* lo = reinterpret_cast<uint2*>(dst + row * D);
+        uint2* hi = reinterpret_cast<uint2*>(dst + row * D + D / 2);
+        *lo = rescale8(*lo, ratio);
+        *hi = rescale8(*hi, ratio);
+      }
+    }
+    if (lane == 0 && (WHOLE || first == 0 || scale > old)) *scale_at = scale;
+  };
+  if (first == 0 && last == kPageSize && (!turned || pos0 + kPageSize <= a.rope_len)) block(std::true_type());
+  else block(std::false_type());
 }
 
 template <int D, int KIND>
