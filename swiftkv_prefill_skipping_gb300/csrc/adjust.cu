@@ -6,9 +6,15 @@
 //
 // Bound by HBM: the row is read and written once. A CTA owns a slice of one row's ids and copies it through shared
 // memory. While the copy arrives it walks the row's whole history and keeps what concerns its slice, one 32-bit
-// word an id: count, prompt bit and place in the bias list. Then it looks at its words; only ids that are named cost
-// arithmetic. No CTA waits for another, and counts are integers: the order of the atomics
-// changes nothing.
+// word an id: count, prompt bit and place in the bias list; the words meet the logits on their way out. No CTA waits
+// for another, and counts are integers: the order of the atomics changes nothing. Everything that a CTA
+// reads is asked for at its start: with lengths, ids, settings and mask one after another the same took 94 us.
+//
+// 256 rows of 128256 with a mask, 262 MB: 37 us without histories (7.1 TB/s), 62 with 4000 - 8064 tokens each, of which
+// reading them in every slice is 6, putting them on their words 12 and the arithmetic 8 us, in series with the copy in
+// each CTA and overlapped across three an SM. Measured and not kept: the touched ids on a list (118 us with one place
+// asked for at a time, 94 with one for a warp), each id computed by whoever takes its word (134), slices of 4096 and
+// 12288 ids. 24 rows of 152064: 12.4 us, one row 6.7 to 8.6, latency.
 #include <algorithm>
 #include <cmath>
 

@@ -29,23 +29,27 @@
 // The softmax computes P against the running maximum as it is. Only where a row has none yet, or where
 // its sum of a block passes 2^16, does a warp look for the block's own maximum, before it computes P
 // (again): seeking it in every block stood in the chain with 370 of its 2400 cycles. Exponentials, sums and
-// the rounding of P go four columns at a time, and FP8 is a template parameter, so that no branch
+// the rounding of P go four columns at a time, and the cache's type is a template parameter, so that no branch
 // parts them (436 us with all three undone).
 //
 // 4 chunks of ~1960 rows after 0 - 6048 keys, 32 / 8 heads x 128: 361 us, 1.42 PFLOP/s (392 called without
 // a pause, where the power cap lowers the clock); the same rows through a window of 1024 and 4 sinks:
 // 150 us. Those scores are nearly flat; with q 16 times as large, where sums outgrow the running maximum
-// more often, 454 us. FP8: 547 and 207 us, of which the expansion to bf16 is the difference. Bound by the tensor core and the hand-overs to it: 337 us
-// without any softmax. S of an 80-key block reads 6.5 KB of shared memory per 16 dims, 52 cycles
+// more often, 454 us. FP8: 527 and 205 us, int8: 405 and 170 us, the expansion to bf16 among them (22 us of the 405).
+// Bound by the tensor core and the hand-overs to it: 337 us without any softmax. S of an 80-key block reads 6.5 KB of shared memory per 16 dims, 52 cycles
 // where the product takes 40, and a wider block does not fit beside P and O: with that the products
 // alone take 307 us. Measured and not kept: four softmax warpgroups on alternate 64-key blocks with P
 // over S (504 us, where this form took 434: S waits for the product of two blocks before); two threads a
 // row, half of a block's columns each (509).
 //
 // Pages without a visible key are not loaded (zeros instead), and pages of V that the chunk sees in
-// part come from zero-padded copies (launch_v_tail). FP8: K and V are an expansion to bf16 codes;
-// the block's key and value scales travel with V, scores take the key's and P the value's (times
-// kValueShift).
+// part come from zero-padded copies (launch_v_tail). 8-bit caches: K and V are an expansion to bf16 codes, in which a
+// block of a sequence is one stretch per head, so that K or V of a block are two TMA copies and not two a page.
+// Scores take the keys' scales and P the values' (times a power of two), both in float32. FP8 has one for each key: 80
+// products for each. int8 has one for each page: the key's goes into the multiply-add that every exponent needs
+// anyway, the value's logarithm into its addend, and the row sums, fused multiply-adds then, take it out again. What
+// is left of a softmax warp's time is the chain of its instructions, some five cycles each: a second wait behind that
+// for S, for the scales, cost 65 us of 455 by itself.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -87,7 +91,7 @@ struct Cfg {
 template <int D>
 struct Ctrl {
   using C = Cfg<D>;
-  static_assert(C::KST + 5 <= kScaleStages, "see the copies of the scales");
+  static_assert(C::KST + 2 <= kScaleStages, "see the copies of the scales");
   uint64_t q_full, q_empty, k_full[C::KST], k_empty[C::KST], v_full[C::VST], v_empty[C::VST];
   uint64_t s_full[2], s_empty[2], p_full[2], pv_done[2], o_empty[2], fin[2];
   uint32_t tmem_base;
@@ -313,9 +317,11 @@ __global__ void __launch_bounds__(THREADS, 1) attn_chunk_kernel(const __grid_con
             const uint32_t ph = (uint32_t)((is_v ? kv_i / VST : kv_i / KST) & 1);
             const uint32_t full = is_v ? bar(ctl->v_full[st]) : bar(ctl->k_full[st]);
             if (!(ok = wait_all(is_v ? bar(ctl->v_empty[st]) : bar(ctl->k_empty[st]), ph ^ 1))) break;
-            // The block's scales come ahead of K, kScaleStages blocks deep. No barrier says that a place is free: K of block kv is asked for once both tiles' S of block kv - KST have been issued, each after
-            // its softmax took S of its block before that into registers, and so was through with the one before.
-            // A place's phases are never two ahead of a reader: the copies of four blocks ago have arrived
+            // The block's scales come ahead of K, kScaleStages blocks deep. No barrier says that a place is free: K
+            // of block kv is asked for once both tiles' S of block kv - KST have been issued, each after its softmax
+            // took S of the tile's block before that, p <= kv - KST - 1, into registers. It may still read the scales
+            // of p, none before them. And a place's phases are never two ahead of a reader: before the copies for kv
+            // go out, those of kv - 4 have arrived
             const int ss = kv_i % kScaleStages, old = kv_i - 4;
             if (!is_v && old >= 0 &&
                 !(ok = wait_all(bar(ctl->sc_full[old % kScaleStages]), (uint32_t)(old / kScaleStages & 1)))) break;

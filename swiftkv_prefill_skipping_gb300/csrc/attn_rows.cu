@@ -24,6 +24,9 @@
 // The 2^16, undone at the end, keeps P' above bf16's subnormals for value scales down to float32's;
 // scales have to stay below 2^100.
 //
+// int8 with a scale for each page and head: codes enter as f16 and bf16 by byte permutes and one subtraction, exactly, and
+// the page's scales take the places of the key's and the value's.
+//
 // A unit that covers its item writes the output, others (max, sum, unnormalised O) records that
 // attn_rows_merge joins, one warp per column.
 //
@@ -33,7 +36,8 @@
 // either (2.0 instructions a cycle and SM, 45 % of the ALU, 18 % of the tensor pipe, DRAM 51 %): 12 warps
 // do not cover the chain from a page's codes to its weights and back. 167 registers; with 16 columns 60
 // bytes spill. 64 rows of 3000 FP8 keys: 94 us, 4.3 TB/s. 4 rows of up to 64 keys: 7.3 us, the launches'
-// latency.
+// latency. int8: 24 rows of ~1100 keys 25 us, 16 rows of ~14200 keys 90 us, 5.2 TB/s (14 or 16 warps an SM with 128
+// registers: 97 and 90; two pages a step: as one), 16 windows 40 us, 64 rows of 3000 keys 86 us.
 #include <cfloat>
 
 #include "common.cuh"
