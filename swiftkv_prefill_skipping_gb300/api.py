@@ -369,8 +369,7 @@ def _new_rows(t: torch.Tensor, T: int, heads: int, caches: int, d_h: int, dev, n
     """Row stride and the stride between caches of bf16 rows [T, heads, d_h], or [T, caches, heads, d_h]."""
     shape, stride = t.shape, t.stride()
     many = len(shape) == 4
-    if t.dtype is not torch.bfloat16 or t.device != dev or tuple(shape) != ((T, caches, heads, d_h) if many else
-                                                                           (T, heads, d_h)):
+    if t.dtype is not torch.bfloat16 or t.device != dev or shape != ((T, caches, heads, d_h) if many else (T, heads, d_h)):
         raise ValueError(f"{name}: bfloat16 [{T}, {heads}, {d_h}] or, for several caches, [{T}, {caches}, {heads}, {d_h}] on {dev}")
     if T and (stride[-1] != 1 or heads > 1 and stride[-2] != d_h):
         raise ValueError(f"{name}: the heads of a row have to be contiguous")
@@ -388,15 +387,19 @@ def append(model: Model, k: torch.Tensor, v: torch.Tensor, cu_seqlens: Sequence[
     k and v of shape [T, n, n_kv, d_h] fill the n caches from `cache` on. Returns the rotated q: q_out, which may
     be q itself, or a new tensor; None without q."""
     cu, ctx, P, T = _chunks(cu_seqlens, ctx_lens, kv, model)
-    _int32(cache)
+    if cache:
+        _int32(cache)
     dev, s = kv.device, model.shape
     off = None if pos_offsets is None else _ints(pos_offsets)
     if off is not None and off.shape != (P,):
         raise ValueError("pos_offsets: [P]")
-    n = k.shape[1] if k.dim() == 4 else 1
+    shape = k.shape
+    n = shape[1] if len(shape) == 4 else 1
     r = B.NewRows()
-    r.ldk, r.k_step = _new_rows(k, T, s.n_kv, n, s.d_h, dev, "k")
-    r.ldv, r.v_step = _new_rows(v, T, s.n_kv, n, s.d_h, dev, "v")
+    r.ldk, r.k_step = ld = _new_rows(k, T, s.n_kv, n, s.d_h, dev, "k")
+    if v.shape != shape or v.dtype is not torch.bfloat16 or v.device != dev or v.stride() != k.stride():
+        ld = _new_rows(v, T, s.n_kv, n, s.d_h, dev, "v")
+    r.ldv, r.v_step = ld
     r.k, r.v = k.data_ptr(), v.data_ptr()
     if q is not None:
         r.ldq = _rows_of(q, T, model, dev, "q")
@@ -496,10 +499,11 @@ def evict(model: Model, kv: KVCache, scores: torch.Tensor, seq_lens: Sequence[in
 
 def _matrix(t: torch.Tensor, dtype, rows: int, cols: Optional[int], dev, name: str):
     """Address, row stride and columns of a matrix [rows, cols] whose rows are contiguous."""
-    if t.dim() != 2 or t.dtype is not dtype or t.device != dev or t.shape[0] != rows or (
-            cols is not None and t.shape[1] != cols) or (t.shape[1] > 1 and t.stride(1) != 1):
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 2 or t.dtype is not dtype or t.device != dev or shape[0] != rows or (
+            cols is not None and shape[1] != cols) or (shape[1] > 1 and stride[1] != 1):
         raise ValueError(f"{name}: {dtype} [{rows}, {'n' if cols is None else cols}] on {dev}, contiguous within a row")
-    return t.data_ptr(), t.stride(0) if rows > 1 else t.shape[1], t.shape[1]
+    return t.data_ptr(), stride[0] if rows > 1 else shape[1], shape[1]
 
 
 def adjust_logits(logits: torch.Tensor, tokens: Optional[torch.Tensor] = None, lens: Optional[torch.Tensor] = None,
@@ -522,18 +526,24 @@ def adjust_logits(logits: torch.Tensor, tokens: Optional[torch.Tensor] = None, l
     if V < 1 or (V > 1 and step != 1) or ld < V:
         raise ValueError("logits: at least one column, contiguous within a row, rows that do not overlap")
     i32, f32, vec, a = torch.int32, torch.float32, (P,), B.Adjustments()
-    a.repetition_all, a.presence_all, a.frequency_all = 1.0, 0.0, 0.0
     if tokens is not None:
         a.tokens, a.ld_tokens, a.max_tokens = _matrix(tokens, i32, P, None, dev, "tokens")
         if lens is not None:
             a.lens = _flat(lens, i32, vec, dev, "lens")
         if prompt_lens is not None:
             a.prompt_lens = _flat(prompt_lens, i32, vec, dev, "prompt_lens")
-        for name, x in (("repetition", repetition), ("presence", presence), ("frequency", frequency)):
-            if isinstance(x, torch.Tensor):
-                setattr(a, name, _flat(x, f32, vec, dev, name))
-            else:
-                setattr(a, name + "_all", x)
+        if isinstance(repetition, torch.Tensor):
+            a.repetition = _flat(repetition, f32, vec, dev, "repetition")
+        else:
+            a.repetition_all = repetition
+        if isinstance(presence, torch.Tensor):
+            a.presence = _flat(presence, f32, vec, dev, "presence")
+        else:
+            a.presence_all = presence
+        if isinstance(frequency, torch.Tensor):
+            a.frequency = _flat(frequency, f32, vec, dev, "frequency")
+        else:
+            a.frequency_all = frequency
     elif lens is not None or prompt_lens is not None:
         raise ValueError("lens and prompt_lens belong to tokens")
     if (bias_ids is None) != (bias is None):

@@ -309,7 +309,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_chunk_kernel(const __grid_con
                             I.seq0 + (t ? I.q0b : I.q0a), bar(ctl->q_full));
           }
         }
-        if (CODES) {  // a block is one stretch of the expansion
+        if constexpr (CODES) {  // a block is one stretch of the expansion
           const BlockOrder order(I.c0, I.n, a.window, a.sinks, BKV);
           const int page0 = kvh * a.num_pages + a.exp_first[I.s];
           for (int j = 0; j < I.nblk; ++j, ++kv_i) {
@@ -346,43 +346,41 @@ __global__ void __launch_bounds__(THREADS, 1) attn_chunk_kernel(const __grid_con
             }
             __syncwarp();
           }
-          I = N;
-          have = have_next;
-          continue;
-        }
-        for (int j = 0; j < I.nblk; ++j, ++kv_i) {
-          int2 next = pg;
-          if (j + 1 < I.nblk) next = load_page(I, j + 1);
-          else if (have_next) next = load_page(N, 0);
-          const int st = is_v ? kv_i % VST : kv_i % KST;
-          const uint32_t ph = (uint32_t)((is_v ? kv_i / VST : kv_i / KST) & 1);
-          const uint32_t full = is_v ? bar(ctl->v_full[st]) : bar(ctl->k_full[st]);
-          // a page that is not needed, or outside the pool, reads rows past the pool's end: zeros
-          const bool valid = pg.x && pg.y >= 0 && pg.y < a.num_pages;
-          if (pg.x && !valid) atomicOr(a.status, kStatusBadPage);
-          int row = (valid ? pg.y * a.n_kv + kvh : a.num_pages * a.n_kv) * kPageSize;
-          const CUtensorMap* map = is_v ? &tmV : &tmK;
-          if (is_v && a.v_tail && valid) {
-            const int pidx = I.block(j) * PAGES + lane;
-#pragma unroll
-            for (int t = 0; t < kTailSlots; ++t)
-              if (pidx == tail.page[t]) {
-                map = &tmTail;
-                row = ((I.s * kTailSlots + t) * a.n_kv + kvh) * kPageSize;
-              }
+        } else {
+          for (int j = 0; j < I.nblk; ++j, ++kv_i) {
+            int2 next = pg;
+            if (j + 1 < I.nblk) next = load_page(I, j + 1);
+            else if (have_next) next = load_page(N, 0);
+            const int st = is_v ? kv_i % VST : kv_i % KST;
+            const uint32_t ph = (uint32_t)((is_v ? kv_i / VST : kv_i / KST) & 1);
+            const uint32_t full = is_v ? bar(ctl->v_full[st]) : bar(ctl->k_full[st]);
+            // a page that is not needed, or outside the pool, reads rows past the pool's end: zeros
+            const bool valid = pg.x && pg.y >= 0 && pg.y < a.num_pages;
+            if (pg.x && !valid) atomicOr(a.status, kStatusBadPage);
+            int row = (valid ? pg.y * a.n_kv + kvh : a.num_pages * a.n_kv) * kPageSize;
+            const CUtensorMap* map = is_v ? &tmV : &tmK;
+            if (is_v && a.v_tail && valid) {
+              const int pidx = I.block(j) * PAGES + lane;
+  #pragma unroll
+              for (int t = 0; t < kTailSlots; ++t)
+                if (pidx == tail.page[t]) {
+                  map = &tmTail;
+                  row = ((I.s * kTailSlots + t) * a.n_kv + kvh) * kPageSize;
+                }
+            }
+            if (!(ok = wait_all(is_v ? bar(ctl->v_empty[st]) : bar(ctl->k_empty[st]), ph ^ 1))) break;
+            if (lane == 0) {
+              mbar_expect_tx(full, C::KV_TILE);
+              ctl->pend[is_v ? 1 + KST + st : 1 + st] = (int)ph;
+            }
+            __syncwarp();
+            if (lane < PAGES) {
+              const uint32_t dst = (is_v ? sV : sK) + st * C::KV_TILE + lane * 2048;
+  #pragma unroll
+              for (int hf = 0; hf < C::HALVES; ++hf) tma_load_2d(dst + hf * C::KV_HALF, map, hf * 64, row, full);
+            }
+            pg = next;
           }
-          if (!(ok = wait_all(is_v ? bar(ctl->v_empty[st]) : bar(ctl->k_empty[st]), ph ^ 1))) break;
-          if (lane == 0) {
-            mbar_expect_tx(full, C::KV_TILE);
-            ctl->pend[is_v ? 1 + KST + st : 1 + st] = (int)ph;
-          }
-          __syncwarp();
-          if (lane < PAGES) {
-            const uint32_t dst = (is_v ? sV : sK) + st * C::KV_TILE + lane * 2048;
-#pragma unroll
-            for (int hf = 0; hf < C::HALVES; ++hf) tma_load_2d(dst + hf * C::KV_HALF, map, hf * 64, row, full);
-          }
-          pg = next;
         }
         I = N;
         have = have_next;

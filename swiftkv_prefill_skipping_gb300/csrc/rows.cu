@@ -429,7 +429,7 @@ __global__ void __launch_bounds__(256) kv_expand_seen_kernel(const int* __restri
       *reinterpret_cast<uint4*>((c < chunks ? dst.k : dst.v) + to * dh + e % per_row * 8) = make_uint4(o[0], o[1], o[2], o[3]);
     }
   }
-  if (INT8) {
+  if constexpr (INT8) {
     // no key scale is 0: it would turn scores of -inf into NaN (where the page's is, all codes are 0 and any scale does)
     for (int h = threadIdx.x; h < n_kv; h += blockDim.x) {
       const float ks = ok ? src.k_scale[(size_t)page * n_kv + h] : 0.f, vs = ok ? src.v_scale[(size_t)page * n_kv + h] : 0.f;
@@ -437,15 +437,15 @@ __global__ void __launch_bounds__(256) kv_expand_seen_kernel(const int* __restri
       const float lv = vc > 0.f ? log2f(vc) : 0.f;
       reinterpret_cast<float4*>(dst.k_scale)[(size_t)h * (head_rows / kPageSize) + i] = make_float4(kc, lv, exp2f(-lv), 0.f);
     }
-    return;
-  }
-  for (int c = threadIdx.x; c < 2 * rows; c += blockDim.x) {
-    const int kvsel = c >= rows, e = c - kvsel * rows;
-    if (kvsel && !dst.v) break;
-    const bool seen = ok && t.seen(pidx * kPageSize + e % kPageSize);
-    const size_t to = (size_t)(e / kPageSize) * head_rows + (size_t)i * page_rows + e % kPageSize;
-    (kvsel ? dst.v_scale : dst.k_scale)[to] =
-        !seen ? 0.f : kvsel ? kValueShift * src.v_scale[(size_t)page * rows + e] : src.k_scale[(size_t)page * rows + e];
+  } else {
+    for (int c = threadIdx.x; c < 2 * rows; c += blockDim.x) {
+      const int kvsel = c >= rows, e = c - kvsel * rows;
+      if (kvsel && !dst.v) break;
+      const bool seen = ok && t.seen(pidx * kPageSize + e % kPageSize);
+      const size_t to = (size_t)(e / kPageSize) * head_rows + (size_t)i * page_rows + e % kPageSize;
+      (kvsel ? dst.v_scale : dst.k_scale)[to] =
+          !seen ? 0.f : kvsel ? kValueShift * src.v_scale[(size_t)page * rows + e] : src.k_scale[(size_t)page * rows + e];
+    }
   }
 }
 

@@ -605,26 +605,29 @@ int swiftkv_append(swiftkv_model* m, int cache, int caches, const swiftkv_new_ro
     OnDevice on_device(m);
     cudaStream_t s = (cudaStream_t)stream;
     AppendArgs a;
-    std::vector<int> ints;
-    ints.reserve(3 * (size_t)P + 4 + 8 * (size_t)caches);
-    a.o_cu = put(&ints, std::vector<int>(cu, cu + P + 1));
-    a.o_ctx = put(&ints, ctx ? std::vector<int>(ctx, ctx + P) : std::vector<int>(P, 0));
-    a.o_off = pos_off ? put(&ints, std::vector<int>(pos_off, pos_off + P)) : -1;
-    if (ints.size() % 2) ints.push_back(0);
-    a.o_pools = (int)ints.size();
-    std::vector<const void*> ptrs;
-    for (int c = 0; c < caches; ++c) ptrs.push_back(kv->k_pool[cache + c]);
-    for (int c = 0; c < caches; ++c) ptrs.push_back(kv->v_pool[cache + c]);
-    for (int c = 0; b.kind != kKvBf16 && c < caches; ++c) ptrs.push_back(kv->k_scale[cache + c]);
-    for (int c = 0; b.kind != kKvBf16 && c < caches; ++c) ptrs.push_back(kv->v_scale[cache + c]);
-    ints.resize(ints.size() + 2 * ptrs.size());
-    memcpy(ints.data() + a.o_pools, ptrs.data(), ptrs.size() * 8);
+    // lists and pool addresses: in the kernel's parameters where they fit, straight from here
+    const int planes = b.kind != kKvBf16 ? 4 : 2;
+    a.o_cu = 0;
+    a.o_ctx = P + 1;
+    a.o_off = pos_off ? 2 * P + 1 : -1;
+    a.o_pools = ((pos_off ? 3 : 2) * P + 2) & ~1;
+    const size_t total = (size_t)a.o_pools + 2 * (size_t)planes * caches;
+    InlineInts inl;
+    std::vector<int> many(total > kInlineInts ? total : 0);
+    int* to = many.empty() ? inl.v : many.data();
+    memcpy(to, cu, (size_t)(P + 1) * 4);
+    if (ctx) memcpy(to + a.o_ctx, ctx, (size_t)P * 4);
+    else memset(to + a.o_ctx, 0, (size_t)P * 4);
+    if (pos_off) memcpy(to + a.o_off, pos_off, (size_t)P * 4);
+    void* const* const pools[4] = {kv->k_pool, kv->v_pool, kv->k_scale, kv->v_scale};
+    for (int i = 0; i < planes; ++i)
+      memcpy(to + a.o_pools + 2 * (size_t)i * caches, pools[i] + cache, (size_t)caches * sizeof(void*));
     int* dev = nullptr;
-    if (ints.size() > kInlineInts) {
+    if (!many.empty()) {
       Arena arena;
-      RET(reserve(m, ints.size() * 4, s, &arena));
-      dev = arena.take<int>(ints.size());
-      CK(upload_ints(dev, ints.data(), (int)ints.size(), s));
+      RET(reserve(m, total * 4, s, &arena));
+      dev = arena.take<int>(total);
+      CK(upload_ints(dev, to, (int)total, s));
     }
     a.lists = dev;
     a.pools = nullptr;
@@ -646,7 +649,7 @@ int swiftkv_append(swiftkv_model* m, int cache, int caches, const swiftkv_new_ro
     a.max_pages = kv->max_pages_per_seq;
     a.num_pages = kv->num_pages;
     a.rotate = rotate != 0;
-    const cudaError_t e = launch_append_on(m, a, b.kind, inline_of(ints, dev), s);
+    const cudaError_t e = launch_append_on(m, a, b.kind, inl, s);
     if (e != cudaSuccess)
       return fail(e == cudaErrorNotSupported ? SWIFTKV_EUNSUPPORTED : SWIFTKV_ECUDA, "append: %s", cudaGetErrorString(e));
     return SWIFTKV_OK;
