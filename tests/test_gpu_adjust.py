@@ -124,6 +124,23 @@ def test_rows_of_a_wider_buffer(pad, offset):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("first,more", [(0, 1), (1, 3), (4, 4), (3, 1)])
+def test_lists_that_are_parts_of_wider_ones(first, more):
+    """Histories and masks whose rows start anywhere and have other words before and behind them."""
+    import torch
+    for rows, vocab, hist in ((3, 5000, 70), (50, 40000, 2100)):
+        c = Case(rows, vocab, hist, 0, 0.6, seed=9)
+        kw = {}
+        for name, fill in (("tokens", 17), ("mask", -1)):
+            t = c.kw[name]
+            wide = torch.full((rows, t.shape[1] + first + more), fill, dtype=torch.int32)
+            wide[:, first:first + t.shape[1]] = t
+            kw[name] = wide.cuda()[:, first:first + t.shape[1]]
+        c.check(c.run(**kw))
+        c.check(c.run(out="in place", **kw))
+
+
+@pytest.mark.gpu
 def test_many_rows_and_long_histories():
     for rows, vocab, hist, bias in ((300, 32000, 90, 3), (70, 151669, 5000, 2046), (2, 128256, 200000, 0), (1, 700000, 100, 9)):
         c = Case(rows, vocab, hist, bias, 0.6, seed=2)

@@ -304,6 +304,58 @@ def test_captured_and_replayed(kind):
 
 
 @pytest.mark.gpu
+def test_two_graphs_that_share_the_workspace():
+    """Batches whose lists do not fit the parameters are uploaded: two captured ones, replayed in turn, and a larger call
+    between them, which makes the workspace grow."""
+    import torch
+    from swiftkv_prefill_skipping_gb300 import api
+    cases = [Case("d64", [(s * i) % 3 + 1 for i in range(400)], [(5 * s * i) % 40 for i in range(400)], "int8", seed=s)
+             for s in (1, 2)]
+    m = cases[0].model
+    big = Case("d64", [1] * 9000, [0] * 9000, "bf16", seed=3)
+    graphs, outs = [], []
+    for c in cases:
+        c.model = m
+        c.run()                    # the workspace holds it
+        k, v = (x.contiguous() for x in c.args())
+        q, out = c.q.cuda(), torch.empty_like(c.q, device="cuda")
+        c.keep = (k, v, q)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            api.append(m, k, v, c.cu, c.ctx, c.kv, q=q, q_out=out)
+        graphs.append(g)
+        outs.append(out)
+    big.model = m
+    big.check(big.run())
+    for _ in range(2):
+        for c, g, out in zip(cases, graphs, outs):
+            for name in c.names():
+                getattr(c.kv, name).copy_(c.before[name].cuda())
+            out.zero_()
+            g.replay()
+        torch.cuda.synchronize()
+        for c, out in zip(cases, outs):
+            c.check(out)
+    assert m.status() == 0
+
+
+@pytest.mark.gpu
+def test_calls_on_two_streams():
+    """Appends to two models' caches at once."""
+    import torch
+    from swiftkv_prefill_skipping_gb300 import api
+    cases = [Case("gqa4", [300, 1, 7], [5, 15, 0], kind, seed=30 + i) for i, kind in enumerate(("bf16", "int8", "fp8"))]
+    streams = [torch.cuda.Stream() for _ in cases]
+    data = [(c.args(), c.q.cuda()) for c in cases]
+    torch.cuda.synchronize()
+    outs = [api.append(c.model, *kv, c.cu, c.ctx, c.kv, q=q, stream=st) for c, (kv, q), st in zip(cases, data, streams)]
+    torch.cuda.synchronize()
+    for c, out in zip(cases, outs):
+        assert c.model.status() == 0
+        c.check(out)
+
+
+@pytest.mark.gpu
 def test_refusals():
     import torch
     from swiftkv_prefill_skipping_gb300 import api

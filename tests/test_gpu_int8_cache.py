@@ -179,6 +179,51 @@ def test_captured_and_on_another_stream():
         assert torch.equal(got.cpu(), ref)
 
 
+def test_two_graphs_that_share_the_workspace():
+    """Expansions and lists of two captured calls in one workspace, which a larger call outgrows between them."""
+    import torch
+    from swiftkv_prefill_skipping_gb300 import api
+    cases = [Case("gqa4", [70, 3, 200], [100, 40, 0], seed=60), Case("gqa4", [5, 33], [900, 20], 64, 3, seed=61)]
+    big = Case("gqa4", [900, 900], [3000, 2000], seed=62)
+    m = cases[0].model
+    graphs = []
+    for c in cases:
+        c.model = m
+        c.want = c.attend()
+        q, out = c.q.cuda(), torch.zeros_like(c.q, device="cuda")
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            api.attend(m, q, c.cu, c.ctx, c.kv, cache=1, window=c.window, sinks=c.sinks, out=out)
+        graphs.append((g, q, out))
+    big.model = m
+    big.check()
+    for _ in range(2):
+        for c, (g, q, out) in zip(cases, graphs):
+            out.zero_()
+            g.replay()
+        torch.cuda.synchronize()
+        for c, (g, q, out) in zip(cases, graphs):
+            assert torch.equal(out.cpu(), c.want[0])
+    assert m.status() == 0
+
+
+def test_sequences_that_share_pages():
+    """A common prefix in two sequences' tables, and one sequence named twice."""
+    import torch
+    c = Case("gqa5", [40, 2, 40], [80, 80, 80], seed=63)
+    table = c.kv.block_table.clone()
+    for s in (1, 2):
+        c.kv.block_table[s, :5] = table[0, :5]       # 80 rows
+        for x in "kv":
+            c.ref[s][x][:80] = c.ref[0][x][:80]
+    c.check()
+    rows = c.kv.view([0, 0])
+    from swiftkv_prefill_skipping_gb300 import api
+    q = torch.cat([c.q[:40], c.q[:40]]).cuda()
+    out = api.attend(c.model, q, [0, 40, 80], [80, 80], rows, cache=1)
+    assert torch.equal(out[:40], out[40:])
+
+
 def test_bad_pages_are_flagged():
     c = Case("gqa4", [2, 60], [40, 50], seed=43)
     import torch
