@@ -16,6 +16,11 @@ namespace {
 // short chunks after a long prefix leave SMs idle: one sequence, 32 / 8 heads x 128, bf16, 4 rows after
 // 16000 keys 37 us, 5 rows 176; 8 sequences 98 and 179.
 constexpr int kRowChunk = 4;
+// Over an int8 cache, by the same measure (us as rows / as tiles; 32 / 8 heads): 1 sequence, 5 / 8 / 16 rows after 16000 keys
+// 45 / 47 / 56 where tiles take 203; 8 sequences 139 / 140 / 258 against 325; 32 sequences, 5 / 8 / 16 rows after 4000 keys
+// 158 / 160 / 352 against 338, 16 rows after 300 keys 55 against 45. Past 16 rows rows win for few sequences only (32
+// rows: one 82 / 203, four 141 / 136), and the rule would have to look at the batch.
+constexpr int kRowChunkInt8 = 16;
 
 int check_batch(const swiftkv_model* m, const int32_t* cu, const int32_t* ctx, int P, const swiftkv_kv_pages* kv,
                 int window, int sinks, Batch* b) {
@@ -252,7 +257,7 @@ int AttendPlan::make(const swiftkv_model* m, const int32_t* cu, const int32_t* c
   for (int i = 0; i < P; ++i) {
     const int n = cu[i + 1] - cu[i], c0 = ctx ? ctx[i] : 0;
     ctxv[i] = c0;
-    if (n <= kRowChunk) {
+    if (n <= (b.kind == kKvInt8 ? kRowChunkInt8 : kRowChunk)) {
       for (int r = 0; r < n; r += group) {
         const int rows = std::min(group, n - r);
         ids.push_back((int)ids.size());
