@@ -6,7 +6,9 @@
 // [256 p, 256 p + 128) and the next 128 of one head (the second absent past the chunk's end). The
 // blocks of an item are those of the sinks and those from its first row's window to its last row's
 // position, one ascending list of which tile A needs a prefix. Persistent: one CTA per SM walks its
-// share of the items, heaviest first, alternate rounds reversed.
+// share of the items, heaviest first, alternate rounds reversed. Over an int8 cache an item may be a part of such a list,
+// where a call has too few tiles for the SMs (cut_tiles): it leaves O unnormalised with its rows' maxima and sums, which
+// attn_chunk_merge joins.
 //
 // A block is 80 keys at d_head 128 and 128 keys at 64: per tile, tensor memory then holds the scores S
 // of one block, the weights P of another (bf16, two a column) and O, and both tiles fill its 512
@@ -52,6 +54,8 @@
 // for S, for the scales, cost 65 us of 455 by itself.
 #include <cuda.h>
 #include <cudaTypedefs.h>
+
+#include <type_traits>
 
 #include "attn_common.cuh"
 #include "common.cuh"
@@ -110,18 +114,36 @@ constexpr int smem_bytes() {
 
 struct Item {
   int s, h, hb, seq0, n, c0, nk, q0a, q0b, nblk_a, nblk_b, nblk, nsink, nwin;
+  int from;   // entry of the tile's list at which the item begins
+  int slot;   // its place among the partial results, -1: it is a whole tile
   bool has_b;
   // block of list entry j
-  __device__ __forceinline__ int block(int j) const { return j < nsink ? j : nwin + j - nsink; }
+  template <bool PARTS>
+  __device__ __forceinline__ int block(int j) const {
+    if (PARTS) j += from;
+    return j < nsink ? j : nwin + j - nsink;
+  }
 };
 
-template <int BKV>
+// PARTS: the list holds parts of tiles.
+template <int BKV, bool PARTS>
 __device__ __forceinline__ bool item_at(int it, const ChunkArgs& a, Item& I) {
   const int G = gridDim.x, c = blockIdx.x;
   const long long w = (long long)it * G + ((it & 1) ? (G - 1 - c) : c);
   if (w >= a.num_items) return false;
-  const int per = a.head_pairs ? a.n_q / 2 : a.n_q;
-  const int tile = a.tiles[w / per], k = (int)(w % per);
+  const int per = a.head_pairs ? a.n_q / 2 : a.n_q, k = (int)(w % per);
+  int tile, count = 0x7fffffff;
+  I.from = 0;
+  I.slot = -1;
+  if (PARTS) {
+    const int4 e = reinterpret_cast<const int4*>(a.tiles)[w / per];
+    tile = e.x;
+    I.from = e.y;
+    count = e.z;
+    if (e.w >= 0) I.slot = e.w * per + k;
+  } else {
+    tile = a.tiles[w / per];
+  }
   I.s = tile >> 16;
   const int qp = tile & 0xffff;
   I.seq0 = a.cu[I.s];
@@ -139,17 +161,23 @@ __device__ __forceinline__ bool item_at(int it, const ChunkArgs& a, Item& I) {
     I.q0b = I.q0a + BQ;
     I.has_b = I.q0b < I.n;
   }
-  const int end_a = (min(I.nk, I.c0 + I.q0a + BQ) + BKV - 1) / BKV;
-  const int end_b = I.has_b ? (min(I.nk, I.c0 + I.q0b + BQ) + BKV - 1) / BKV : 0;
-  const int end = I.has_b ? end_b : end_a, w0 = window_begin(I.c0 + I.q0a, a.window);
-  I.nsink = w0 > 0 ? min(end, (min(a.sinks, w0) + BKV - 1) / BKV) : 0;
-  I.nwin = max(I.nsink, w0 / BKV);
-  auto entries = [&](int last) { return min(I.nsink, last) + max(0, last - I.nwin); };
-  I.nblk_a = entries(end_a);
-  I.nblk_b = entries(end_b);
+  const TileBlocks blocks(I.c0, I.n, I.q0a, I.has_b ? I.q0b : I.q0a, a.window, a.sinks, BKV);
+  I.nsink = blocks.sinks;
+  I.nwin = blocks.rest;
+  auto entries = [&](int q0) {
+    const int n = blocks.entries((min(I.nk, I.c0 + q0 + BQ) + BKV - 1) / BKV);
+    return PARTS ? max(0, min(count, n - I.from)) : n;
+  };
+  I.nblk_a = entries(I.q0a);
+  I.nblk_b = I.has_b ? entries(I.q0b) : 0;
   I.nblk = I.has_b ? I.nblk_b : I.nblk_a;
   return true;
 }
+
+// A tile's partial results at Item::slot: O unnormalised, 4 dims of every row after the other, then the rows' maxima and
+// sums.
+template <int D>
+constexpr int kPartFloats = BQ * (D + 2);
 
 // 16 columns of this thread's tensor-memory lane; a load's registers hold values after tmem_wait16
 __device__ __forceinline__ void tmem_ld16_async(uint32_t addr, float* r) {
@@ -216,7 +244,8 @@ __device__ __forceinline__ void add2(float* acc, const float* p) {
       : "f"(p[0]), "f"(p[1]));
 }
 
-template <int D, int KIND>
+// PARTS: items may be parts of tiles (int8).
+template <int D, int KIND, bool PARTS>
 __global__ void __launch_bounds__(THREADS, 1) attn_chunk_kernel(const __grid_constant__ CUtensorMap tmQ,
                                                                 const __grid_constant__ CUtensorMap tmK,
                                                                 const __grid_constant__ CUtensorMap tmV,
@@ -282,18 +311,18 @@ __global__ void __launch_bounds__(THREADS, 1) attn_chunk_kernel(const __grid_con
       const int group = a.n_q / a.n_kv;
       // the lane's page id in block j of item X, loaded one block ahead of its use
       auto load_page = [&](const Item& X, int j) {
-        const int key = X.block(j) * BKV + lane * kPageSize;
+        const int key = X.template block<PARTS>(j) * BKV + lane * kPageSize;
         // not read where no row of the item sees a key of the page
         const bool need = lane < PAGES && key < X.nk && (key + kPageSize > window_begin(X.c0 + X.q0a, a.window) || key < a.sinks);
         return make_int2(need, need ? a.bt[(size_t)X.s * a.max_pages + (key >> 4)] : 0);
       };
       int kv_i = 0;
       int2 pg = make_int2(0, 0);
-      bool ok = true, have = item_at<BKV>(0, a, I);
+      bool ok = true, have = item_at<BKV, PARTS>(0, a, I);
       if (have && !CODES) pg = load_page(I, 0);
       for (int it = 0; ok && have; ++it) {
         Item N;
-        const bool have_next = item_at<BKV>(it + 1, a, N);
+        const bool have_next = item_at<BKV, PARTS>(it + 1, a, N);
         const int kvh = I.h / group;
         const TailPages tail = tail_pages(I.c0, I.n, a.window, a.sinks);
         if (!is_v) {
@@ -313,7 +342,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_chunk_kernel(const __grid_con
           const BlockOrder order(I.c0, I.n, a.window, a.sinks, BKV);
           const int page0 = kvh * a.num_pages + a.exp_first[I.s];
           for (int j = 0; j < I.nblk; ++j, ++kv_i) {
-            const int st = is_v ? kv_i % VST : kv_i % KST, page = page0 + order.place(I.block(j)) * PAGES;
+            const int st = is_v ? kv_i % VST : kv_i % KST, page = page0 + order.place(I.template block<PARTS>(j)) * PAGES;
             const uint32_t ph = (uint32_t)((is_v ? kv_i / VST : kv_i / KST) & 1);
             const uint32_t full = is_v ? bar(ctl->v_full[st]) : bar(ctl->k_full[st]);
             if (!(ok = wait_all(is_v ? bar(ctl->v_empty[st]) : bar(ctl->k_empty[st]), ph ^ 1))) break;
@@ -360,7 +389,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_chunk_kernel(const __grid_con
             int row = (valid ? pg.y * a.n_kv + kvh : a.num_pages * a.n_kv) * kPageSize;
             const CUtensorMap* map = is_v ? &tmV : &tmK;
             if (is_v && a.v_tail && valid) {
-              const int pidx = I.block(j) * PAGES + lane;
+              const int pidx = I.template block<PARTS>(j) * PAGES + lane;
   #pragma unroll
               for (int t = 0; t < kTailSlots; ++t)
                 if (pidx == tail.page[t]) {
@@ -394,7 +423,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_chunk_kernel(const __grid_con
       const uint32_t base = tmem + t * C::COLS;
       int kv_base = 0, g = 0, oi = 0;
       bool ok = true;
-      for (int it = 0; ok && item_at<BKV>(it, a, I); ++it) {
+      for (int it = 0; ok && item_at<BKV, PARTS>(it, a, I); ++it) {
         const int nb = t ? I.nblk_b : I.nblk_a;
         if (!(ok = wait_all(bar(ctl->q_full), (uint32_t)(it & 1)))) break;
         if (lane == 0) {
@@ -474,9 +503,16 @@ __global__ void __launch_bounds__(THREADS, 1) attn_chunk_kernel(const __grid_con
     int g = 0, kvb = 0;
     bool ok = true;
     auto wait = [&](uint64_t& b, uint32_t phase) { return wait_all(bar(b), phase); };
-    for (int it = 0; ok && item_at<BKV>(it, a, I); kvb += I.nblk, ++it) {
+    for (int it = 0; ok && item_at<BKV, PARTS>(it, a, I); kvb += I.nblk, ++it) {
       const int nb = t ? I.nblk_b : I.nblk_a, q0 = t ? I.q0b : I.q0a;
-      if (nb == 0) continue;
+      if (nb == 0) {
+        if (PARTS && I.slot >= 0 && (t == 0 || I.has_b)) {  // a part behind what the tile sees
+          float* ml = a.part + ((size_t)I.slot * 2 + t) * kPartFloats<D> + BQ * D + quarter * 32 + lane;
+          ml[0] = -INFINITY;
+          ml[BQ] = 0.f;
+        }
+        continue;
+      }
       // rows past the chunk see what its last row sees
       const int qw = q0 + quarter * 32, qrow = qw + lane, qpos = I.c0 + min(qrow, I.n - 1);
       const int first = window_begin(qpos, a.window), last = min(qpos, I.nk - 1), sinks = a.window > 0 ? a.sinks : 0;
@@ -516,7 +552,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_chunk_kernel(const __grid_con
             x[i + 3] *= f.w;
           }
         }
-        const int key0 = I.block(j) * BKV;
+        const int key0 = I.template block<PARTS>(j) * BKV;
         // no key of the block hidden from any row of the warp
         const bool inside = key0 + BKV - 1 <= I.c0 + qw && key0 + BKV <= I.nk &&
                             (a.window <= 0 || key0 > I.c0 + qw + 31 - a.window || key0 + BKV <= a.sinks);
@@ -631,6 +667,23 @@ __global__ void __launch_bounds__(THREADS, 1) attn_chunk_kernel(const __grid_con
       if (ok) ok = wait(ctl->pv_done[t], (uint32_t)((g - 1) & 1));
       if (ok) {
         tc_fence_after();
+        if (PARTS && I.slot >= 0) {
+          float* to = a.part + ((size_t)I.slot * 2 + t) * kPartFloats<D>;
+          const int r = quarter * 32 + lane;
+#pragma unroll
+          for (int c = 0; c < D; c += 32) {
+            float v[32];
+            tmem_ld32(s_addr + C::O_COL + c, v);
+#pragma unroll
+            for (int e = 0; e < 32; e += 4)
+              reinterpret_cast<float4*>(to)[(c + e) / 4 * BQ + r] = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+          }
+          to[BQ * D + r] = m;
+          to[BQ * D + BQ + r] = l;
+          tc_fence_before();
+          mbar_arrive(bar(ctl->o_empty[t]));
+          continue;
+        }
         const float inv = (FP8 ? 1.f / kValueShift : INT8 ? 1.f / kPageShift : 1.f) / l;
         const int head = t ? I.hb : I.h;
         if (a.lse && qrow < I.n) a.lse[(size_t)head * a.ldl + I.seq0 + qrow] = (m + log2f(l)) * kLn2;
@@ -685,7 +738,53 @@ __global__ void __launch_bounds__(THREADS, 1) attn_chunk_kernel(const __grid_con
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
 }
 
-template <int D, int KIND>
+// Joins the parts of split tiles (INT8's): a CTA per tile, query head and 16 dims, a thread a row. merges [3 * n] = (tile,
+// first slot, parts).
+template <int D>
+__global__ void __launch_bounds__(BQ) attn_chunk_merge(const __grid_constant__ ChunkArgs a) {
+  griddep_launch_dependents();
+  griddep_wait();
+  const int per = a.head_pairs ? a.n_q / 2 : a.n_q;
+  const int t = blockIdx.x & 1, w = blockIdx.x >> 1, k = w % per;
+  const int *e = a.merges + 3 * (w / per), tile = e[0], first = e[1], parts = e[2];
+  const int s = tile >> 16, n = a.cu[s + 1] - a.cu[s], r = threadIdx.x;
+  const int row = (tile & 0xffff) * (a.head_pairs ? BQ : 2 * BQ) + (a.head_pairs ? 0 : t * BQ) + r;
+  if (row >= n) return;
+  const size_t step = (size_t)per * 2 * kPartFloats<D>;
+  const float* p = a.part + (((size_t)first * per + k) * 2 + t) * kPartFloats<D>;
+  float m = -INFINITY, l = 0.f;
+  for (int i = 0; i < parts; ++i) m = fmaxf(m, p[i * step + BQ * D + r]);
+  float4 o[4];
+#pragma unroll
+  for (int c = 0; c < 4; ++c) o[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+  const int c0 = blockIdx.y * 4;
+  for (int i = 0; i < parts; ++i) {
+    const float* q = p + i * step;
+    const float li = q[BQ * D + BQ + r];
+    if (li == 0.f) continue;  // the row saw nothing there
+    const float f = exp2f(q[BQ * D + r] - m);
+    l = fmaf(li, f, l);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const float4 v = reinterpret_cast<const float4*>(q)[(c0 + c) * BQ + r];
+      o[c].x = fmaf(v.x, f, o[c].x);
+      o[c].y = fmaf(v.y, f, o[c].y);
+      o[c].z = fmaf(v.z, f, o[c].z);
+      o[c].w = fmaf(v.w, f, o[c].w);
+    }
+  }
+  const float inv = 1.f / (kPageShift * l);
+  const int head = a.head_pairs ? 2 * k + t : k;
+  const size_t at = a.cu[s] + row;
+  uint4* dst = reinterpret_cast<uint4*>(a.out + at * a.ldo + (size_t)head * D + 16 * blockIdx.y);
+#pragma unroll
+  for (int c = 0; c < 4; c += 2)
+    dst[c / 2] = make_uint4(pack_bf16(o[c].x * inv, o[c].y * inv), pack_bf16(o[c].z * inv, o[c].w * inv),
+                            pack_bf16(o[c + 1].x * inv, o[c + 1].y * inv), pack_bf16(o[c + 1].z * inv, o[c + 1].w * inv));
+  if (a.lse && blockIdx.y == 0) a.lse[(size_t)head * a.ldl + at] = (m + log2f(l)) * kLn2;
+}
+
+template <int D, int KIND, bool PARTS>
 cudaError_t launch_d(const ChunkArgs& a, const bf16* q, int ldq, int T, const bf16* k, const bf16* v, int num_sms,
                      cudaStream_t s) {
   constexpr int smem = smem_bytes<D>();
@@ -700,10 +799,12 @@ cudaError_t launch_d(const ChunkArgs& a, const bf16* q, int ldq, int T, const bf
       !tma_map_bf16_2d(&mt, a.v_tail, a.tail_seqs * kTailSlots * a.n_kv * kPageSize, D, D, 64, kPageSize, true))
     return cudaErrorNotSupported;
   static PerDeviceOnce once;
-  cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void*>(attn_chunk_kernel<D, KIND>), smem, once);
+  cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void*>(attn_chunk_kernel<D, KIND, PARTS>), smem, once);
   if (e != cudaSuccess) return e;
-  return launch_pdl(attn_chunk_kernel<D, KIND>, dim3(a.num_items < num_sms ? a.num_items : num_sms), dim3(THREADS), smem,
-                    s, mq, mk, mv, mt, a, 1.4426950408889634f / sqrtf((float)D));
+  e = launch_pdl(attn_chunk_kernel<D, KIND, PARTS>, dim3(a.num_items < num_sms ? a.num_items : num_sms), dim3(THREADS), smem,
+                 s, mq, mk, mv, mt, a, 1.4426950408889634f / sqrtf((float)D));
+  if (e != cudaSuccess || !PARTS) return e;
+  return launch_pdl(attn_chunk_merge<D>, dim3(a.num_merges * (a.head_pairs ? a.n_q / 2 : a.n_q) * 2, D / 16), dim3(BQ), 0, s, a);
 }
 
 }  // namespace
@@ -713,14 +814,15 @@ cudaError_t launch_attn_chunk(const ChunkArgs& a, const bf16* q, int ldq, int T,
   if (a.num_items <= 0) return cudaSuccess;
   if (a.head_pairs && (a.n_q / a.n_kv) % 2) return cudaErrorNotSupported;
   if (a.kind != kKvBf16 && !a.k_scale) return cudaErrorNotSupported;
-  if (d_head == 128)
-    return a.kind == kKvBf16 ? launch_d<128, kKvBf16>(a, q, ldq, T, k, v, num_sms, s)
-           : a.kind == kKvFp8 ? launch_d<128, kKvFp8>(a, q, ldq, T, k, v, num_sms, s)
-                              : launch_d<128, kKvInt8>(a, q, ldq, T, k, v, num_sms, s);
-  if (d_head == 64)
-    return a.kind == kKvBf16 ? launch_d<64, kKvBf16>(a, q, ldq, T, k, v, num_sms, s)
-           : a.kind == kKvFp8 ? launch_d<64, kKvFp8>(a, q, ldq, T, k, v, num_sms, s)
-                              : launch_d<64, kKvInt8>(a, q, ldq, T, k, v, num_sms, s);
+  auto run = [&](auto d) {
+    constexpr int D = decltype(d)::value;
+    return a.kind == kKvBf16  ? launch_d<D, kKvBf16, false>(a, q, ldq, T, k, v, num_sms, s)
+           : a.kind == kKvFp8 ? launch_d<D, kKvFp8, false>(a, q, ldq, T, k, v, num_sms, s)
+           : a.num_merges > 0 ? launch_d<D, kKvInt8, true>(a, q, ldq, T, k, v, num_sms, s)
+                              : launch_d<D, kKvInt8, false>(a, q, ldq, T, k, v, num_sms, s);
+  };
+  if (d_head == 128) return run(std::integral_constant<int, 128>());
+  if (d_head == 64) return run(std::integral_constant<int, 64>());
   return cudaErrorNotSupported;
 }
 

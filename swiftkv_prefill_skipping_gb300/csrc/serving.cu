@@ -12,7 +12,7 @@ namespace skv {
 namespace {
 
 // Chunks of at most this many rows go to the row kernel, split along their keys; a 128-row query
-// tile would be nearly empty (the serving forward's rule). Tiles are not split along the keys, so few
+// tile would be nearly empty (the serving forward's rule). Tiles over bf16 and FP8 are not split along the keys, so few
 // short chunks after a long prefix leave SMs idle: one sequence, 32 / 8 heads x 128, bf16, 4 rows after
 // 16000 keys 37 us, 5 rows 176; 8 sequences 98 and 179.
 constexpr int kRowChunk = 4;
@@ -154,6 +154,68 @@ void count_work(const int32_t* cu, const int32_t* ctx, const Batch& b, double* k
   }
 }
 
+// Cuts tiles (seq << 16 | tile, of so many blocks each, heaviest first) along their lists of blocks where there are too
+// few to keep the SMs busy: entries of ChunkArgs::tiles, heaviest first, and its merges; none of the two where whole tiles
+// are as good. `per` items run for each. Parts fill the rounds that whole tiles take, the last of which would be half
+// empty, and are no shorter than kMinPart blocks. Whether that pays is counted as the kernel deals items out, with
+// kStart blocks' time for an item's start and end, twice that for a part's, and kMerge for the join.
+// int8, 32 / 8 heads x 128, us whole / cut: 1 sequence, 24 and 64 rows after 16000 keys 206 / 62, 128 after 6048 93 / 41, 512
+// 98 / 70, 2016 191 / 185 (2016 after none 49 / 55: left whole); 2 and 4 sequences, 32 rows after 8000 121 / 64 and 140 / 103.
+constexpr int kMinPart = 8, kStart = 2, kMerge = 6, kFullRounds = 4;
+void cut_tiles(const std::vector<int>& tiles, const std::vector<int>& blocks, int per, int num_sms, std::vector<int>* out,
+               std::vector<int>* merges, int* num_slots) {
+  struct Part {
+    int tile, from, n, slot;
+  };
+  const long long items = (long long)tiles.size() * per, rounds = (items + num_sms - 1) / num_sms;
+  if (items >= (long long)kFullRounds * num_sms) return;
+  auto longest = [&](const std::vector<Part>& parts) {  // blocks of the SM that has most
+    std::vector<long long> load(num_sms, 0);
+    long long w = 0, most = 0;
+    for (const Part& p : parts)
+      for (int k = 0; k < per; ++k, ++w) {
+        const long long it = w / num_sms, c = w % num_sms;
+        most = std::max(most, load[it & 1 ? num_sms - 1 - c : c] += p.n + (p.slot < 0 ? kStart : 2 * kStart));
+      }
+    return most;
+  };
+  std::vector<Part> whole, parts;
+  long long most = 1;
+  for (size_t i = 0; i < tiles.size(); ++i) {
+    whole.push_back({tiles[i], 0, blocks[i], -1});
+    most = std::max<long long>(most, blocks[i]);
+  }
+  int lo = (int)std::min<long long>(kMinPart, most), len = (int)most;
+  while (lo < len) {  // the shortest length that keeps to the rounds
+    const int mid = (lo + len) / 2;
+    long long n = 0;
+    for (int b : blocks) n += (b + mid - 1) / mid;
+    if (n * per <= rounds * num_sms) len = mid;
+    else lo = mid + 1;
+  }
+  std::vector<int> joins;
+  int slots = 0;
+  for (size_t i = 0; i < tiles.size(); ++i) {
+    const int n = blocks[i], p = (n + len - 1) / len;
+    if (p <= 1) {
+      parts.push_back(whole[i]);
+      continue;
+    }
+    joins.insert(joins.end(), {tiles[i], slots, p});
+    for (int k = 0; k < p; ++k) {
+      const int a = (int)((long long)n * k / p), e = (int)((long long)n * (k + 1) / p);
+      parts.push_back({tiles[i], a, e - a, slots++});
+    }
+  }
+  auto heavier = [](const Part& x, const Part& y) { return x.n > y.n; };
+  std::stable_sort(whole.begin(), whole.end(), heavier);
+  std::stable_sort(parts.begin(), parts.end(), heavier);
+  if (joins.empty() || longest(parts) + kMerge >= longest(whole)) return;
+  for (const Part& p : parts) out->insert(out->end(), {p.tile, p.from, p.n, p.slot});
+  merges->swap(joins);
+  *num_slots = slots;
+}
+
 int put(std::vector<int>* ints, const std::vector<int>& v) {
   const int at = (int)ints->size();
   ints->insert(ints->end(), v.begin(), v.end());
@@ -279,10 +341,26 @@ int AttendPlan::make(const swiftkv_model* m, const int32_t* cu, const int32_t* c
     return b.window > 0 ? std::min((long long)p, (long long)b.window + b.sinks + tile_rows) : (long long)p;
   };
   std::stable_sort(tiles.begin(), tiles.end(), [&](int x, int y) { return keys_of(x) > keys_of(y); });
+  num_tiles = (int)tiles.size();
+  std::vector<int> merges;
+  if (b.kind == kKvInt8 && num_tiles > 0) {
+    std::vector<int> blocks, cut;
+    for (int tl : tiles) {
+      const int i = tl >> 16, n = cu[i + 1] - cu[i], q0 = (tl & 0xffff) * tile_rows;
+      const int q1 = !head_pairs && q0 + 128 < n ? q0 + 128 : q0;
+      const TileBlocks t(ctxv[i], n, q0, q1, b.window, b.sinks, chunk_block(c.d_head));
+      blocks.push_back(t.entries(t.end));
+    }
+    cut_tiles(tiles, blocks, head_pairs ? c.n_q / 2 : c.n_q, m->num_sms, &cut, &merges, &num_slots);
+    num_merges = (int)(merges.size() / 3);
+    if (num_merges > 0) {
+      num_tiles = (int)(cut.size() / 4);
+      tiles.swap(cut);
+    }
+  }
   std::vector<int> units, ubeg;
   if (!ids.empty())
     cut_units(ids, seen, c.n_kv, (long long)m->num_sms * (b.kind != kKvBf16 ? kRowsWarps8 : kRowsWarps), &units, &ubeg);
-  num_tiles = (int)tiles.size();
   num_items = (int)ids.size();
   num_units = (int)(units.size() / 3);
   num_exp = (int)(exp_items.size() / 2);
@@ -290,10 +368,12 @@ int AttendPlan::make(const swiftkv_model* m, const int32_t* cu, const int32_t* c
   if (std::max({units.size(), tiles.size(), exp_items.size()}) >= (size_t)1 << 28 ||
       (long long)num_units * c.n_kv >= (1LL << 31) || (long long)num_tiles * c.n_q >= (1LL << 31))
     return fail(SWIFTKV_EUNSUPPORTED, "batch too large");
-  ints.reserve(3 * cuv.size() + tiles.size() + units.size() + exp_items.size() + ubeg.size() + items.size());
+  ints.reserve(3 * cuv.size() + tiles.size() + merges.size() + 8 + units.size() + exp_items.size() + ubeg.size() + items.size());
   o_cu = put(&ints, cuv);
   o_ctx = put(&ints, ctxv);
+  while (num_merges > 0 && ints.size() % 4) ints.push_back(0);  // entries of 16 bytes
   o_tiles = put(&ints, tiles);
+  o_merges = put(&ints, merges);
   o_items = put(&ints, items);
   o_units = put(&ints, units);
   o_ubeg = put(&ints, ubeg);
@@ -309,6 +389,7 @@ void AttendPlan::place(const swiftkv_model* m, Arena* a) {
   const auto& c = m->cfg;
   dev = num_tiles > 0 || ints.size() > kInlineInts ? a->take<int>(ints.size()) : nullptr;
   part = a->take<float>(num_units > num_items ? (size_t)num_units * c.n_kv * max_cols * (c.d_head + 4) : 0);
+  tile_part = a->take<float>((size_t)num_slots * (head_pairs ? c.n_q / 2 : c.n_q) * 2 * 128 * (c.d_head + 2));
   v_tail = nullptr;
   if (num_tiles > 0 && b.kind == kKvBf16)
     v_tail = a->take<bf16>((size_t)b.P * kTailSlots * c.n_kv * kPageSize * c.d_head);
@@ -352,6 +433,9 @@ int AttendPlan::run(swiftkv_model* m, const swiftkv_kv_pages* kv, int c, const b
     }
     t.max_pages = b.max_pages;
     t.tiles = dev + o_tiles;
+    t.merges = dev + o_merges;
+    t.num_merges = num_merges;
+    t.part = tile_part;
     t.num_items = num_tiles * (head_pairs ? g.n_q / 2 : g.n_q);
     t.head_pairs = head_pairs;
     t.n_q = g.n_q;
@@ -398,7 +482,7 @@ int AttendPlan::run(swiftkv_model* m, const swiftkv_kv_pages* kv, int c, const b
 }
 
 int AttendPlan::kernels() const {
-  return (num_tiles > 0 ? 2 : 0) + (num_items > 0 ? 1 + (num_units > num_items) : 0);
+  return (num_tiles > 0 ? 2 + (num_merges > 0) : 0) + (num_items > 0 ? 1 + (num_units > num_items) : 0);
 }
 
 // ---------------------------------------------------------------------------- attention weights

@@ -84,6 +84,22 @@ struct BlockOrder {
   __host__ __device__ int count() const { return place(end); }
 };
 
+// The blocks of a query tile, or of two, that starts at row q0 of its chunk and whose last starts at q1: those of the
+// sinks [0, sinks), then [rest, end), one list of which a tile that ends before needs a prefix.
+struct TileBlocks {
+  int sinks, rest, end;
+  __host__ __device__ TileBlocks(int c0, int n, int q0, int q1, int window, int num_sinks, int bkv) {
+    const int seen = c0 + n < c0 + q1 + 128 ? c0 + n : c0 + q1 + 128, w0 = window_begin(c0 + q0, window);
+    const int near = num_sinks < w0 ? num_sinks : w0;
+    end = (seen + bkv - 1) / bkv;
+    sinks = (near + bkv - 1) / bkv < end ? (near + bkv - 1) / bkv : end;
+    rest = w0 / bkv > sinks ? w0 / bkv : sinks;
+  }
+  __host__ __device__ int entries(int last) const {
+    return (sinks < last ? sinks : last) + (last > rest ? last - rest : 0);
+  }
+};
+
 // kv_dtype of a cache
 constexpr int kKvBf16 = 0, kKvFp8 = 1, kKvInt8 = 2;
 
@@ -127,11 +143,12 @@ struct AttendPlan {
   bool head_pairs = false;
   // host lists, and their places in one device upload
   std::vector<int> ints;
-  int o_cu = 0, o_ctx = 0, o_tiles = 0, o_items = 0, o_units = 0, o_ubeg = 0, o_exp = 0, o_first = 0;
+  int o_cu = 0, o_ctx = 0, o_tiles = 0, o_items = 0, o_units = 0, o_ubeg = 0, o_exp = 0, o_first = 0, o_merges = 0;
+  int num_slots = 0, num_merges = 0;
   int num_tiles = 0, num_items = 0, max_cols = 0, num_units = 0, num_exp = 0;
   // device (lists: null where the kernels take them inline)
   int* dev = nullptr;
-  float* part = nullptr;
+  float *part = nullptr, *tile_part = nullptr;
   bf16* v_tail = nullptr;
   KVExpansion exp{};
   double keys = 0, pairs = 0;  // cached keys some row sees, and (row, key) pairs, for profiling
@@ -169,7 +186,9 @@ struct WeightsPlan {
 // ---- kernels (attn_chunk.cu, attn_rows.cu, attn_weights.cu, evict.cu) --------------------------------------
 // Query tiles of longer chunks: tiles (seq << 16 | tile), heaviest first, of 128 rows (head_pairs:
 // an item is a tile for two query heads of one KV head, num_items = tiles * n_q / 2) or of 256 rows
-// (an item is a tile for one head, num_items = tiles * n_q).
+// (an item is a tile for one head, num_items = tiles * n_q). int8 with num_merges > 0: tiles [4 * n] = (seq << 16 | tile,
+// first entry of its list of blocks, entries, slot of its partial result or -1), merges [3 * num_merges] = (tile, first
+// slot, parts).
 struct ChunkArgs {
   int kind;                        // kv_dtype
   const float *k_scale, *v_scale;  // 8-bit caches: the expansion's
@@ -178,6 +197,9 @@ struct ChunkArgs {
   int max_pages, num_pages;
   const int *cu, *ctx, *tiles;
   int num_items;
+  const int* merges;
+  int num_merges;
+  float* part;             // [slots][items of a tile][2][128 * (d_head + 2)]
   bool head_pairs;
   int n_q, n_kv;
   int window, sinks;

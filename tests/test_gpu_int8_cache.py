@@ -139,6 +139,35 @@ def test_chunks_around_the_border_between_rows_and_tiles(heads):
         Case(heads, [15, 16, 17, 9, 18], [300, 1, 40, 0, 500], window, sinks, seed=71).check()
 
 
+@pytest.mark.parametrize("heads", list(HEADS))
+@pytest.mark.parametrize("window,sinks", [(0, 0), (900, 30), (2500, 0), (300, 1500)])
+def test_tiles_cut_along_their_keys(heads, window, sinks):
+    """Few tiles after long prefixes run in parts: rows that see nothing of a part, tiles that end before one, second tiles
+    that are absent."""
+    Case(heads, [40], [3000], window, sinks, seed=80).check()
+    Case(heads, [300], [2500], window, sinks, seed=81, kmul=(1.0, 4.0, 0.1)).check()
+    Case(heads, [17, 2, 500], [4000, 100, 1000], window, sinks, seed=82, vmul=(1.0, 2.0 ** 30, 1e-6)).check()
+
+
+def test_cut_tiles_repeat_their_bits_and_replay():
+    import torch
+    from swiftkv_prefill_skipping_gb300 import api
+    c = Case("gqa4", [100, 3], [5000, 40], seed=83)
+    out, lse = c.attend()
+    assert all(torch.equal(x, y) for x, y in zip((out, lse), c.attend()))
+    q, got, l = c.q.cuda(), torch.zeros_like(c.q, device="cuda"), torch.zeros_like(lse, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        api.attend(c.model, q, c.cu, c.ctx, c.kv, cache=1, out=got, lse=l)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(got.cpu(), out) and torch.equal(l.cpu(), lse)
+    # rows of a wider buffer, and no log-sum-exp
+    wide = torch.full((c.T, c.n_q + 1, c.d), 5.0, dtype=torch.bfloat16, device="cuda")
+    api.attend(c.model, q, c.cu, c.ctx, c.kv, cache=1, out=wide[:, 1:])
+    assert torch.equal(wide[:, 1:].cpu(), out) and bool((wide[:, 0] == 5).all())
+
+
 @pytest.mark.parametrize("heads", ["gqa5", "gqa4", "d64"])
 def test_more_items_than_ctas(heads):
     """CTAs walk several items, of which the second tile takes part in some only (odd groups)."""
