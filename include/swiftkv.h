@@ -246,8 +246,9 @@ int swiftkv_decode_step(swiftkv_model* m, const int32_t* tokens, const int32_t* 
  * Chunks of at most 4 rows (16 over an int8 cache) are short. P, over an FP8 or int8 cache times the value's scale,
  * enters the product with V rounded to bf16, in short chunks as two bf16 parts; scores, sums and the output
  * accumulate in float32. The order in which a short chunk's keys are summed depends on the call's other chunks, so
- * its last bits may; a longer one's do not, but over an int8 cache in calls of few of them. Value scales have to stay below 2^95 (FP8) or 2^64 (int8), q over an 8-bit
- * cache below 2^100 in longer chunks, and a page's int8 scales finite where any of its rows is visible.
+ * its last bits may; a longer one's do not, but over an int8 cache in calls of few of them. Value scales have
+ * to stay below 2^95 (FP8) or 2^64 (int8), q over an 8-bit cache below 2^100 in longer chunks, and a page's
+ * int8 scales finite where any of its rows is visible.
  * swiftkv_set_attention_impl does not concern this call. */
 int swiftkv_attend(swiftkv_model* m, int cache, const void* q, int ldq, const int32_t* cu_seqlens,
                    const int32_t* ctx_lens, int num_seqs, const swiftkv_kv_pages* kv, int window, int sinks,

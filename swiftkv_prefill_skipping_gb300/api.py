@@ -355,7 +355,10 @@ def _rows_of(t: torch.Tensor, T: int, model: Model, dev, name: str) -> int:
             (s.n_q == 1 or stride[1] == s.d_h) or
             len(shape) == 2 and shape[1] == s.n_q * s.d_h and stride[1] == 1):
         raise ValueError(f"{name}: bfloat16 [{T}, {s.n_q}, {s.d_h}] on {dev}, the heads of a row contiguous")
-    return stride[0] if T > 1 else s.n_q * s.d_h
+    ld = stride[0] if T > 1 else s.n_q * s.d_h
+    if ld > 0x7fffffff:
+        _int32(ld)
+    return ld
 
 
 def _flat(t: torch.Tensor, dtype, shape: tuple, dev, name: str) -> int:
@@ -374,7 +377,10 @@ def _new_rows(t: torch.Tensor, T: int, heads: int, caches: int, d_h: int, dev, n
     if T and (stride[-1] != 1 or heads > 1 and stride[-2] != d_h):
         raise ValueError(f"{name}: the heads of a row have to be contiguous")
     step = stride[1] if many and caches > 1 else heads * d_h
-    return (stride[0] if T > 1 else max(0, (caches - 1) * step) + heads * d_h), step
+    ld = stride[0] if T > 1 else max(0, (caches - 1) * step) + heads * d_h
+    if ld > 0x7fffffff:
+        _int32(ld)
+    return ld, step
 
 
 def append(model: Model, k: torch.Tensor, v: torch.Tensor, cu_seqlens: Sequence[int], ctx_lens: Optional[Sequence[int]],
@@ -526,8 +532,13 @@ def adjust_logits(logits: torch.Tensor, tokens: Optional[torch.Tensor] = None, l
     if V < 1 or (V > 1 and step != 1) or ld < V:
         raise ValueError("logits: at least one column, contiguous within a row, rows that do not overlap")
     i32, f32, vec, a = torch.int32, torch.float32, (P,), B.Adjustments()
+    if P > 0x7fffffff or V > 0x7fffffff:
+        _int32(P, V)
     if tokens is not None:
-        a.tokens, a.ld_tokens, a.max_tokens = _matrix(tokens, i32, P, None, dev, "tokens")
+        a.tokens, a.ld_tokens, n = _matrix(tokens, i32, P, None, dev, "tokens")
+        if n > 0x7fffffff:
+            _int32(n)
+        a.max_tokens = n
         if lens is not None:
             a.lens = _flat(lens, i32, vec, dev, "lens")
         if prompt_lens is not None:
@@ -550,6 +561,8 @@ def adjust_logits(logits: torch.Tensor, tokens: Optional[torch.Tensor] = None, l
         raise ValueError("bias_ids and bias go together")
     if bias is not None:
         n = bias.shape[1] if bias.dim() == 2 else -1
+        if n > 0x7fffffff:
+            _int32(n)
         a.bias_ids, a.bias, a.num_bias = (_flat(bias_ids, i32, (P, n), dev, "bias_ids"),
                                           _flat(bias, f32, (P, n), dev, "bias"), n)
     if mask is not None:

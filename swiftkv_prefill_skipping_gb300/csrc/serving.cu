@@ -678,9 +678,12 @@ int swiftkv_append(swiftkv_model* m, int cache, int caches, const swiftkv_new_ro
         return fail(SWIFTKV_EINVAL_SEQLENS, "sequence %d: positions outside [0, 2^30)", i);
     }
     if (b.T == 0) return SWIFTKV_OK;
-    const long long Nkv = m->Nkv, k_width = (caches - 1) * rows->k_step + Nkv, v_width = (caches - 1) * rows->v_step + Nkv;
-    if (caches > 1 && (rows->k_step < Nkv || rows->v_step < Nkv || rows->k_step % 8 || rows->v_step % 8))
-      return fail(SWIFTKV_EINVAL, "k_step, v_step: at least %lld and a multiple of 8", Nkv);
+    const long long Nkv = m->Nkv, most = 0x7fffffff;  // no step is longer than a row
+    if (caches > 1 && (rows->k_step < Nkv || rows->v_step < Nkv || rows->k_step > most || rows->v_step > most ||
+                       rows->k_step % 8 || rows->v_step % 8))
+      return fail(SWIFTKV_EINVAL, "k_step, v_step: from %lld to a row's stride and a multiple of 8", Nkv);
+    const long long k_width = caches > 1 ? (caches - 1) * rows->k_step + Nkv : Nkv;
+    const long long v_width = caches > 1 ? (caches - 1) * rows->v_step + Nkv : Nkv;
     RET(check_width(rows->k, rows->ldk, k_width, "k"));
     RET(check_width(rows->v, rows->ldv, v_width, "v"));
     if (rows->q) {

@@ -293,3 +293,15 @@ def test_arguments_without_gpu():
     assert call(rows=2) == -1
     a.ld_tokens, a.num_bias = 5, 3
     assert call() == -1 and b"null bias" in lib.swiftkv_last_error()
+
+
+@pytest.mark.gpu
+def test_sizes_past_32_bits_are_refused():
+    """Sizes whose low 32 bits would pass."""
+    import torch
+    from swiftkv_prefill_skipping_gb300 import api
+    big, x = torch.empty(1, (1 << 32) + 4, device="cuda"), torch.zeros(1, 100, device="cuda")
+    ids = big.view(torch.int32)
+    for a, kw in ((big, {}), (big.view(-1, 1), {}), (x, dict(tokens=ids)), (x, dict(bias_ids=ids, bias=big))):
+        with pytest.raises(ValueError, match="32 bits"):
+            api.adjust_logits(a, out=x, **kw)

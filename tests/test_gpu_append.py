@@ -406,6 +406,30 @@ def test_int8_caches_elsewhere_are_refused():
             call()
 
 
+@pytest.mark.gpu
+def test_strides_past_32_bits_are_refused():
+    """A step between caches whose multiple wraps around to a row's width, and row strides whose low 32 bits would pass."""
+    import torch
+    from swiftkv_prefill_skipping_gb300 import api
+    c = Case("gqa4", [3], [0], caches=5, total_caches=5)
+    (k, v), q = c.args(), c.q.cuda()
+    r = B.NewRows()
+    r.k, r.v, r.ldk, r.ldv, r.k_step, r.v_step = k.data_ptr(), v.data_ptr(), 1280, 1280, 1 << 62, 256
+    for r.k_step, r.v_step in ((1 << 62, 256), (256, 1 << 62)):
+        assert B.lib().swiftkv_append(c.model.handle, 0, 5, r, B.host(c.cu), None, None, 1, c.kv.pages_ref, 1, None) == -1
+        assert b"k_step" in B.lib().swiftkv_last_error()
+    wide = torch.empty(2 * ((1 << 32) + 1280) + 4096, dtype=torch.bfloat16, device="cuda")
+
+    def rows(t):
+        return wide.as_strided(t.shape, ((1 << 32) + 1280, *t.stride()[1:]))
+
+    for kk, vv, qq in ((rows(k), v, q), (k, rows(v), q), (k, v, rows(q))):
+        with pytest.raises(ValueError, match="32 bits"):
+            api.append(c.model, kk, vv, c.cu, c.ctx, c.kv, q=qq)
+    torch.cuda.synchronize()
+    assert all(torch.equal(getattr(c.kv, n).cpu(), c.before[n]) for n in c.names())
+
+
 def test_arguments_without_gpu():
     lib = B.lib()
     r = B.NewRows()
