@@ -9,12 +9,16 @@
 // word an id: count, prompt bit and place in the bias list; the words meet the logits on their way out. No CTA waits
 // for another, and counts are integers: the order of the atomics changes nothing. Everything that a CTA
 // reads is asked for at its start: with lengths, ids, settings and mask one after another the same took 94 us.
+// Without biases, and with histories that a count of 15 bits holds, a word has 16 bits. Slices are then half as long
+// again, a history is walked less often, and three CTAs of 640 threads share an SM: 50 us where 32-bit words take 62 (16-bit
+// ones with 512 threads 53, with slices of 8192 55, of 16384 55, two CTAs).
 //
-// 256 rows of 128256 with a mask, 262 MB: 37 us without histories (7.1 TB/s), 62 with 4000 - 8064 tokens each, of which
-// reading them in every slice is 6, putting them on their words 12 and the arithmetic 8 us, in series with the copy in
-// each CTA and overlapped across three an SM. Measured and not kept: the touched ids on a list (118 us with one place
+// 256 rows of 128256 with a mask, 262 MB: 37 us without histories (7.1 TB/s), 50 with 4000 - 8064 tokens each, of which
+// the walk in every slice and the arithmetic on the words are 13, in series with the copy in each CTA and overlapped across
+// three an SM. Measured with 32-bit words and not kept: the touched ids on a list (118 us with one place
 // asked for at a time, 94 with one for a warp), each id computed by whoever takes its word (134), slices of 4096 and
-// 12288 ids, a history walked once by a cluster of 2 / 4 / 8 CTAs with atomics on one another's words (74 / 80 / 93). 24 rows of 152064: 12.4 us, one row 6.7 to 8.6, latency.
+// 12288 ids, a history walked once by a cluster of 2 / 4 / 8 CTAs with atomics on one another's words (74 / 80 / 93).
+// 24 rows of 152064: 12.4 us, one row 6.7 to 8.6, latency.
 #include <algorithm>
 #include <cmath>
 
@@ -27,12 +31,13 @@ namespace skv {
 
 namespace {
 
-constexpr int AT = 512;                 // threads
-constexpr int kMaxSlice = 8192;         // ids of a CTA: 64 KB of logits and words, three CTAs an SM
+constexpr int kThreads = 512, kMaxSlice = 8192;           // ids of a CTA: 64 KB of logits and words, three CTAs an SM
+constexpr int kThreadsHalf = 640, kMaxSliceHalf = 12288;  // with 16-bit words: 72 KB, three as well
 constexpr int kTargetBlocks = 304;      // CTAs that fill the GPU
 constexpr unsigned kCount = 0xfffff;    // how often the id was generated
 constexpr unsigned kPrompt = 1u << 20;  // it is in the prompt
 constexpr int kBiasShift = 21;          // 1 + its last place in the bias list
+constexpr unsigned kHalfCount = 0x7fff, kHalfPrompt = 0x8000;  // the same in 16 bits
 constexpr int kMaxHistory = kCount, kMaxBias = (1 << (32 - kBiasShift)) - 2;
 
 struct AdjustParams {
@@ -55,9 +60,10 @@ struct AdjustParams {
   long long ld_mask;
 };
 
-// VEC: rows start on 16 bytes.
-template <bool VEC>
-__global__ void __launch_bounds__(AT) adjust_kernel(const AdjustParams p) {
+// VEC: rows start on 16 bytes. HALF: histories that fit 16-bit words, two of them a word of memory, and no biases.
+template <bool VEC, bool HALF>
+__global__ void __launch_bounds__(HALF ? kThreadsHalf : kThreads) adjust_kernel(const AdjustParams p) {
+  constexpr int AT = HALF ? kThreadsHalf : kThreads;
   extern __shared__ __align__(16) unsigned char smem[];
   griddep_launch_dependents();
   griddep_wait();
@@ -66,8 +72,9 @@ __global__ void __launch_bounds__(AT) adjust_kernel(const AdjustParams p) {
   const float* src = p.logits + (size_t)row * p.ld + base;
   float* dst = p.out + (size_t)row * p.ldo + base;
   const bool in_place = src == dst, lists = p.tokens || p.num_bias > 0;
-  unsigned* word = reinterpret_cast<unsigned*>(smem);                                // [slice], with lists
-  float* x = reinterpret_cast<float*>(smem + (lists ? (size_t)p.slice * 4 : 0));     // [slice], not in place
+  unsigned* word = reinterpret_cast<unsigned*>(smem);                                // [slice] words, with lists
+  const unsigned word_bytes = lists ? p.slice * (HALF ? 2 : 4) : 0;
+  float* x = reinterpret_cast<float*>(smem + word_bytes);                            // [slice], not in place
   uint32_t* allow = reinterpret_cast<uint32_t*>(x + (in_place ? 0 : p.slice));       // [slice / 32], with a mask
   // Everything that the CTA reads is asked for here, the lists beyond their ends too (as far as the arrays go):
   // one trip to memory and not one after another, which took most of a CTA's time
@@ -114,10 +121,18 @@ __global__ void __launch_bounds__(AT) adjust_kernel(const AdjustParams p) {
   }
   cp_async_commit();
   if (lists) {
-    for (int i = tid * 4; i < p.slice; i += 4 * AT) *reinterpret_cast<uint4*>(word + i) = make_uint4(0, 0, 0, 0);
+    for (unsigned i = tid * 16; i < word_bytes; i += 16 * AT) *reinterpret_cast<uint4*>(smem + i) = make_uint4(0, 0, 0, 0);
+    auto in_prompt = [&](unsigned u) {
+      if (HALF) atomicOr(word + (u >> 1), kHalfPrompt << (u & 1) * 16);
+      else atomicOr(word + u, kPrompt);
+    };
+    auto generated = [&](unsigned u) {
+      if (HALF) atomicAdd(word + (u >> 1), 1u << (u & 1) * 16);
+      else atomicAdd(word + u, 1u);
+    };
     __syncthreads();
     // an id less base, as unsigned: ids outside the slice, negative ones among them, are at least `size`
-    if (p.num_bias > 0) {  // an id named twice takes its last entry: the words hold nothing else yet
+    if (!HALF && p.num_bias > 0) {  // an id named twice takes its last entry: the words hold nothing else yet
       for (int i = tid; i < p.num_bias; i += AT) {
         const unsigned u = (i == tid ? bias_id : (unsigned)bias_ids[i]) - (unsigned)base;
         if (u < (unsigned)size) atomicMax(word + u, (unsigned)(i + 1) << kBiasShift);
@@ -137,17 +152,17 @@ __global__ void __launch_bounds__(AT) adjust_kernel(const AdjustParams p) {
         if (w0 + 128 <= min(prompt, len)) {
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            if (u[e] < (unsigned)size) atomicOr(word + u[e], kPrompt);
+            if (u[e] < (unsigned)size) in_prompt(u[e]);
         } else if (w0 >= prompt && w0 + 128 <= len) {
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            if (u[e] < (unsigned)size) atomicAdd(word + u[e], 1u);
+            if (u[e] < (unsigned)size) generated(u[e]);
         } else if (w0 < len) {
 #pragma unroll
           for (int e = 0; e < 4; ++e)
             if (i + e < len && u[e] < (unsigned)size) {
-              if (i + e < prompt) atomicOr(word + u[e], kPrompt);
-              else atomicAdd(word + u[e], 1u);
+              if (i + e < prompt) in_prompt(u[e]);
+              else generated(u[e]);
             }
         }
       }
@@ -156,10 +171,11 @@ __global__ void __launch_bounds__(AT) adjust_kernel(const AdjustParams p) {
   if (!(rep > 0.f)) rep = 1.f;
   const float* bias = p.bias + (size_t)row * p.num_bias;
   const float per = 1.f / rep;
+  constexpr unsigned count = HALF ? kHalfCount : kCount, in_list = HALF ? kHalfCount | kHalfPrompt : kCount | kPrompt;
   auto adjust = [&](unsigned w, float v) {
-    if (w & (kCount | kPrompt)) v *= v > 0.f ? per : rep;
-    if (w & kCount) v = v - frequency * (float)(w & kCount) - presence;
-    if (w >> kBiasShift) v += bias[(w >> kBiasShift) - 1];
+    if (w & in_list) v *= v > 0.f ? per : rep;
+    if (w & count) v = v - frequency * (float)(w & count) - presence;
+    if (!HALF && w >> kBiasShift) v += bias[(w >> kBiasShift) - 1];
     return v;
   };
   cp_async_wait<0>();
@@ -168,7 +184,13 @@ __global__ void __launch_bounds__(AT) adjust_kernel(const AdjustParams p) {
     for (int u = tid * 4; u < size; u += 4 * AT) {
       float4 v = *reinterpret_cast<const float4*>(x + u);
       if (lists) {
-        const uint4 w = *reinterpret_cast<const uint4*>(word + u);
+        uint4 w;
+        if (HALF) {
+          const uint2 h = *reinterpret_cast<const uint2*>(word + u / 2);
+          w = make_uint4(h.x & 0xffff, h.x >> 16, h.y & 0xffff, h.y >> 16);
+        } else {
+          w = *reinterpret_cast<const uint4*>(word + u);
+        }
         if (w.x) v.x = adjust(w.x, v.x);
         if (w.y) v.y = adjust(w.y, v.y);
         if (w.z) v.z = adjust(w.z, v.z);
@@ -191,7 +213,7 @@ __global__ void __launch_bounds__(AT) adjust_kernel(const AdjustParams p) {
     }
   } else {
     for (int u = tid; u < size; u += AT) {
-      const unsigned w = lists ? word[u] : 0u;
+      const unsigned w = !lists ? 0u : HALF ? reinterpret_cast<const uint16_t*>(word)[u] : word[u];
       const bool ok = !mask || (allow[u >> 5] >> (u & 31) & 1);
       if (in_place) {  // what nothing concerns is neither read nor written
         if (!ok) dst[u] = -INFINITY;
@@ -203,17 +225,17 @@ __global__ void __launch_bounds__(AT) adjust_kernel(const AdjustParams p) {
   }
 }
 
-template <bool VEC>
+template <bool VEC, bool HALF>
 cudaError_t launch_vec(const AdjustParams& p, int rows, cudaStream_t s) {
   const bool lists = p.tokens || p.num_bias > 0, in_place = p.logits == p.out;
-  constexpr int most = kMaxSlice * 8 + kMaxSlice / 8;
+  constexpr int most = HALF ? kMaxSliceHalf * 6 + kMaxSliceHalf / 8 : kMaxSlice * 8 + kMaxSlice / 8;
   static PerDeviceOnce once;
-  cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void*>(adjust_kernel<VEC>), most, once);
+  cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void*>(adjust_kernel<VEC, HALF>), most, once);
   if (e != cudaSuccess) return e;
-  const int smem = (lists ? p.slice * 4 : 0) + (in_place ? 0 : p.slice * 4) + (p.mask ? p.slice / 8 : 0);
+  const int smem = (lists ? p.slice * (HALF ? 2 : 4) : 0) + (in_place ? 0 : p.slice * 4) + (p.mask ? p.slice / 8 : 0);
   const long long blocks = (long long)rows * p.slices;
   if (blocks >= 1LL << 31) return cudaErrorNotSupported;
-  return launch_pdl(adjust_kernel<VEC>, dim3((unsigned)blocks), dim3(AT), smem, s, p);
+  return launch_pdl(adjust_kernel<VEC, HALF>, dim3((unsigned)blocks), dim3(HALF ? kThreadsHalf : kThreads), smem, s, p);
 }
 
 }  // namespace
@@ -273,11 +295,13 @@ extern "C" int swiftkv_adjust_logits(const float* logits, int rows, int vocab, l
   p.ld_mask = a->ld_mask;
   const bool vec = ((i0 | o0) & 15) == 0 && (rows == 1 || (ld % 4 == 0 && ld_out % 4 == 0));
   // Short slices while there are few rows, so that every SM has work; long ones walk a history less often.
+  const bool half = hist && !bias && a->max_tokens <= (int)kHalfCount;
   const long long ids = (long long)rows * vocab, want = (ids / kTargetBlocks + 1023) / 1024 * 1024;
-  p.slice = (int)std::max(1024LL, std::min<long long>(kMaxSlice, want));
+  p.slice = (int)std::max(1024LL, std::min<long long>(half ? kMaxSliceHalf : kMaxSlice, want));
   p.slices = (vocab + p.slice - 1) / p.slice;
   cudaStream_t s = (cudaStream_t)stream;
-  const cudaError_t e = vec ? launch_vec<true>(p, rows, s) : launch_vec<false>(p, rows, s);
+  const cudaError_t e = vec ? (half ? launch_vec<true, true>(p, rows, s) : launch_vec<true, false>(p, rows, s))
+                            : (half ? launch_vec<false, true>(p, rows, s) : launch_vec<false, false>(p, rows, s));
   if (e != cudaSuccess)
     return set_error(e == cudaErrorNotSupported ? SWIFTKV_EUNSUPPORTED : SWIFTKV_ECUDA, cudaGetErrorString(e));
   return SWIFTKV_OK;

@@ -148,6 +148,23 @@ def test_many_rows_and_long_histories():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("hist", [32766, 32767, 32768, 70000])
+def test_one_id_throughout_a_history(hist):
+    """The largest counts, beside neighbours in the prompt alone, in both, and in none, on even and odd ids."""
+    import torch
+    for rows, vocab in ((2, 301), (80, 40000)):
+        c = Case(rows, vocab, hist, mask=0.9, seed=8)
+        t = c.kw["tokens"]
+        for r in range(rows):
+            t[r, :] = 4 + r % 2
+            c.kw["prompt_lens"][r] = 0
+        t[1, :3], c.kw["prompt_lens"][1] = torch.tensor([4, 6, 5]), 3
+        c.kw["lens"][:] = hist
+        c.check(c.run())
+        c.check(c.run(out="in place"))
+
+
+@pytest.mark.gpu
 def test_settings_that_are_off_and_lengths_out_of_range():
     import torch
     nan = float("nan")
