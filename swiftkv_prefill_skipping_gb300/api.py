@@ -371,7 +371,7 @@ def _flat(t: torch.Tensor, dtype, shape: tuple, dev, name: str) -> int:
 def _new_rows(t: torch.Tensor, T: int, heads: int, caches: int, d_h: int, dev, name: str):
     """Row stride and the stride between caches of bf16 rows [T, heads, d_h], or [T, caches, heads, d_h]."""
     shape, stride = t.shape, t.stride()
-    many = len(shape) == 4
+    many = len(shape) == 4 or caches > 1
     if t.dtype is not torch.bfloat16 or t.device != dev or shape != ((T, caches, heads, d_h) if many else (T, heads, d_h)):
         raise ValueError(f"{name}: bfloat16 [{T}, {heads}, {d_h}] or, for several caches, [{T}, {caches}, {heads}, {d_h}] on {dev}")
     if T and (stride[-1] != 1 or heads > 1 and stride[-2] != d_h):

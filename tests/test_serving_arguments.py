@@ -69,3 +69,19 @@ def test_numbers_past_32_bits_are_refused(big):
     for call in calls:
         with pytest.raises((ValueError, OverflowError), match="32 bits"):
             call()
+
+
+@pytest.mark.parametrize("T", [1, 3])
+def test_append_refuses_values_of_one_cache_for_keys_of_several(T):
+    """v of one cache beside k of two: its rows end, or another part of the projection begins, where the second's would be."""
+    m = model_on("cpu")
+    kv = api.KVCache(m, 4, np.zeros((1, 2), np.int32), device=torch.device("cpu"))
+    wide = torch.zeros(T, 2, 2, 2, 64, dtype=torch.bfloat16)  # K and V of the first cache, then of the second
+    k, v = wide[:, :, 0], wide[:, :, 1]
+    for one in (v[:, 0], v[:, 0].contiguous(), wide.flatten(1, 3)[:, 2:4]):
+        with pytest.raises(ValueError, match="v: bfloat16"):
+            api.append(m, k, one, [0, T], None, kv)
+        with pytest.raises(ValueError, match="v: bfloat16"):
+            api.append(m, k.contiguous(), one, [0, T], None, kv)
+        with pytest.raises(ValueError, match="v: bfloat16"):
+            api.append(m, one, v, [0, T], None, kv)
