@@ -411,18 +411,23 @@ __global__ void __launch_bounds__(256) kv_expand_seen_kernel(const int* __restri
   constexpr int U = 8;
   for (int c0 = threadIdx.x; c0 < total; c0 += U * 256) {
     uint2 codes[U];
+    float value_scale[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int c = c0 + u * 256, e = c < chunks ? c : c - chunks;
       codes[u] = make_uint2(0, 0);
-      if (c < total && ok && t.seen(pidx * kPageSize + e / per_row % kPageSize))
+      value_scale[u] = 1.f;
+      if (c < total && ok && t.seen(pidx * kPageSize + e / per_row % kPageSize)) {
         codes[u] = *reinterpret_cast<const uint2*>((c < chunks ? k : v) + (size_t)e * 8);
+        if (INT8 && c >= chunks) value_scale[u] = src.v_scale[(size_t)page * n_kv + e / per_row / kPageSize];
+      }
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int c = c0 + u * 256, e = c < chunks ? c : c - chunks, row = e / per_row;
       if (c >= total) break;
       uint32_t o[4];  // (codes of 0 are zeros in both)
+      if (value_scale[u] == 0.f) codes[u] = make_uint2(0, 0);  // its logarithm below is 0: P does not carry it
       if (INT8) expand_int8x8(codes[u], o);
       else expand_codes8(codes[u], o);
       const size_t to = (size_t)(row / kPageSize) * head_rows + (size_t)i * page_rows + row % kPageSize;
@@ -430,7 +435,7 @@ __global__ void __launch_bounds__(256) kv_expand_seen_kernel(const int* __restri
     }
   }
   if constexpr (INT8) {
-    // no key scale is 0: it would turn scores of -inf into NaN (where the page's is, all codes are 0 and any scale does)
+    // no key scale is 0: it would turn scores of -inf into NaN (for a page's of 0 the smallest, whose scores round away)
     for (int h = threadIdx.x; h < n_kv; h += blockDim.x) {
       const float ks = ok ? src.k_scale[(size_t)page * n_kv + h] : 0.f, vs = ok ? src.v_scale[(size_t)page * n_kv + h] : 0.f;
       const float kc = fmaxf(ks * (1.4426950408889634f / sqrtf((float)dh)), 1.4e-45f), vc = vs * kPageShift;

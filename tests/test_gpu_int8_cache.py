@@ -132,6 +132,22 @@ def test_pages_of_any_size(heads, new, ctx):
     Case(heads, new, ctx, seed=36, kmul=(0.0,)).check()
 
 
+@pytest.mark.parametrize("heads", ["gqa4", "gqa5", "d64"])
+@pytest.mark.parametrize("new", [[16], [17], [300, 3]])
+def test_pages_cleared_by_a_scale_of_zero(heads, new):
+    """Codes under a scale of 0 stand for zeros, in chunks of either kind and beside values of any size."""
+    for vmul in (1.0, 1e-30):
+        c = Case(heads, new, [70 + 10 * i for i in range(len(new))], seed=37, vmul=(vmul,))
+        for s in range(c.P):
+            for p in (1, 3):
+                page = int(c.kv.block_table[s, p])
+                c.kv.v_scale[1, page, 0] = 0
+                c.ref[s]["v"][16 * p:16 * p + 16, 0] = 0
+                c.kv.k_scale[1, page, -1] = 0
+                c.ref[s]["k"][16 * p:16 * p + 16, -1] = 0
+        c.check()
+
+
 @pytest.mark.parametrize("heads", list(HEADS))
 def test_chunks_around_the_border_between_rows_and_tiles(heads):
     for window, sinks in ((0, 0), (37, 5)):
