@@ -342,7 +342,11 @@ __global__ void __launch_bounds__(THREADS, 1) attn_chunk_kernel(const __grid_con
           const BlockOrder order(I.c0, I.n, a.window, a.sinks, BKV);
           const int page0 = kvh * a.num_pages + a.exp_first[I.s];
           for (int j = 0; j < I.nblk; ++j, ++kv_i) {
-            const int st = is_v ? kv_i % VST : kv_i % KST, page = page0 + order.place(I.template block<PARTS>(j)) * PAGES;
+            const int block = I.template block<PARTS>(j);
+            const int st = is_v ? kv_i % VST : kv_i % KST, page = page0 + order.place(block) * PAGES;
+            // Pages that no row sees have a place in the expansion, but nothing in it: K of such a page may be anything,
+            // its scores are masked, and V of a block with some comes page by page, zeros from past the end for them
+            const bool seen = lane >= PAGES || tail.page_seen(block * PAGES + lane), whole = !is_v || __all_sync(0xffffffffu, seen);
             const uint32_t ph = (uint32_t)((is_v ? kv_i / VST : kv_i / KST) & 1);
             const uint32_t full = is_v ? bar(ctl->v_full[st]) : bar(ctl->k_full[st]);
             if (!(ok = wait_all(is_v ? bar(ctl->v_empty[st]) : bar(ctl->k_empty[st]), ph ^ 1))) break;
@@ -368,12 +372,20 @@ __global__ void __launch_bounds__(THREADS, 1) attn_chunk_kernel(const __grid_con
               }
               mbar_expect_tx(full, C::KV_TILE);
               ctl->pend[is_v ? 1 + KST + st : 1 + st] = (int)ph;
-              const uint32_t dst = (is_v ? sV : sK) + st * C::KV_TILE;
+              if (whole) {
+                const uint32_t dst = (is_v ? sV : sK) + st * C::KV_TILE;
 #pragma unroll
-              for (int hf = 0; hf < C::HALVES; ++hf)
-                tma_load_2d(dst + hf * C::KV_HALF, is_v ? &tmV : &tmK, hf * 64, page * kPageSize, full);
+                for (int hf = 0; hf < C::HALVES; ++hf)
+                  tma_load_2d(dst + hf * C::KV_HALF, is_v ? &tmV : &tmK, hf * 64, page * kPageSize, full);
+              }
             }
             __syncwarp();
+            if (!whole && lane < PAGES) {
+              const int row = (seen ? page + lane : a.num_pages * a.n_kv) * kPageSize;
+#pragma unroll
+              for (int hf = 0; hf < C::HALVES; ++hf)
+                tma_load_2d(sV + st * C::KV_TILE + hf * C::KV_HALF + lane * 2048, &tmTail, hf * 64, row, full);
+            }
           }
         } else {
           for (int j = 0; j < I.nblk; ++j, ++kv_i) {
@@ -794,9 +806,11 @@ cudaError_t launch_d(const ChunkArgs& a, const bf16* q, int ldq, int T, const bf
   if (!tma_map_bf16_2d(&mq, q, T, a.n_q * D, ldq, 64, BQ, true) ||
       !tma_map_bf16_2d(&mk, k, rows, D, D, 64, box, true) || !tma_map_bf16_2d(&mv, v, rows, D, D, 64, box, true))
     return cudaErrorNotSupported;
+  // V by pages: the tail copies, or the expansion's
+  const bf16* by_page = KIND == kKvBf16 ? a.v_tail : v;
   mt = mv;
-  if (a.v_tail &&
-      !tma_map_bf16_2d(&mt, a.v_tail, a.tail_seqs * kTailSlots * a.n_kv * kPageSize, D, D, 64, kPageSize, true))
+  if (by_page && !tma_map_bf16_2d(&mt, by_page, KIND == kKvBf16 ? a.tail_seqs * kTailSlots * a.n_kv * kPageSize : rows, D, D, 64,
+                                  kPageSize, true))
     return cudaErrorNotSupported;
   static PerDeviceOnce once;
   cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void*>(attn_chunk_kernel<D, KIND, PARTS>), smem, once);

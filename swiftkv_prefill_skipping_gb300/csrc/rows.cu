@@ -386,20 +386,24 @@ __device__ __forceinline__ void expand_int8x8(uint2 raw, uint32_t* o) {
   }
 }
 
-// Item i = (sequence, page index) becomes page i of the expansion, `head_rows` rows a head and `page_rows` a page on.
+// Item (sequence, page index, place) becomes the page at its place of the expansion, `head_rows` rows a head and
+// `page_rows` a page on; the scales of the places since the item before (for the last, to the end) are its CTA's to write.
 // 8 codes a thread and step, so that a warp's store fills its sectors (16 codes with two stores: 28 us for 20000 keys of
 // 8 heads x 128, 41 MB in and 82 out, where this takes 22), eight steps in flight.
 template <int dh, bool INT8>
 __global__ void __launch_bounds__(256) kv_expand_seen_kernel(const int* __restrict__ items, const KVPool8 src, int max_pages,
                                                              int num_pages, const int* __restrict__ cu,
                                                              const int* __restrict__ ctx, int n_kv, int window, int sinks,
-                                                             const KVExpansion dst, int head_rows, int page_rows, int* status) {
+                                                             const KVExpansion dst, int head_rows, int page_rows, int places,
+                                                             int* status) {
   griddep_launch_dependents();
   griddep_wait();
-  const int i = blockIdx.x, s = items[2 * i], pidx = items[2 * i + 1];
-  const int page = pidx >= 0 ? src.block_table[(size_t)s * max_pages + pidx] : -1;
+  const int* const item = items + 3 * blockIdx.x;
+  const int s = item[0], pidx = item[1], i = item[2];
+  const int from = blockIdx.x ? item[-1] + 1 : 0, until = blockIdx.x + 1 == gridDim.x ? places : i + 1;
+  const int page = src.block_table[(size_t)s * max_pages + pidx];
   const bool ok = page >= 0 && page < num_pages;
-  if (threadIdx.x == 0 && pidx >= 0) {
+  if (threadIdx.x == 0) {
     if (dst.block_table) dst.block_table[(size_t)s * max_pages + pidx] = i;
     if (!ok) atomicOr(status, kStatusBadPage);
   }
@@ -436,18 +440,20 @@ __global__ void __launch_bounds__(256) kv_expand_seen_kernel(const int* __restri
   }
   if constexpr (INT8) {
     // no key scale is 0: it would turn scores of -inf into NaN (for a page's of 0 the smallest, whose scores round away)
-    for (int h = threadIdx.x; h < n_kv; h += blockDim.x) {
-      const float ks = ok ? src.k_scale[(size_t)page * n_kv + h] : 0.f, vs = ok ? src.v_scale[(size_t)page * n_kv + h] : 0.f;
+    for (int c = threadIdx.x; c < (until - from) * n_kv; c += blockDim.x) {
+      const int at = from + c / n_kv, h = c % n_kv;
+      const bool mine = ok && at == i;
+      const float ks = mine ? src.k_scale[(size_t)page * n_kv + h] : 0.f, vs = mine ? src.v_scale[(size_t)page * n_kv + h] : 0.f;
       const float kc = fmaxf(ks * (1.4426950408889634f / sqrtf((float)dh)), 1.4e-45f), vc = vs * kPageShift;
       const float lv = vc > 0.f ? log2f(vc) : 0.f;
-      reinterpret_cast<float4*>(dst.k_scale)[(size_t)h * (head_rows / kPageSize) + i] = make_float4(kc, lv, exp2f(-lv), 0.f);
+      reinterpret_cast<float4*>(dst.k_scale)[(size_t)h * (head_rows / kPageSize) + at] = make_float4(kc, lv, exp2f(-lv), 0.f);
     }
   } else {
-    for (int c = threadIdx.x; c < 2 * rows; c += blockDim.x) {
-      const int kvsel = c >= rows, e = c - kvsel * rows;
-      if (kvsel && !dst.v) break;
-      const bool seen = ok && t.seen(pidx * kPageSize + e % kPageSize);
-      const size_t to = (size_t)(e / kPageSize) * head_rows + (size_t)i * page_rows + e % kPageSize;
+    const int scales = dst.v ? 2 * rows : rows;
+    for (int c = threadIdx.x; c < (until - from) * scales; c += blockDim.x) {
+      const int at = from + c / scales, x = c % scales, kvsel = x >= rows, e = x - kvsel * rows;
+      const bool seen = ok && at == i && t.seen(pidx * kPageSize + e % kPageSize);
+      const size_t to = (size_t)(e / kPageSize) * head_rows + (size_t)at * page_rows + e % kPageSize;
       (kvsel ? dst.v_scale : dst.k_scale)[to] =
           !seen ? 0.f : kvsel ? kValueShift * src.v_scale[(size_t)page * rows + e] : src.k_scale[(size_t)page * rows + e];
     }
@@ -504,16 +510,16 @@ cudaError_t launch_kv_dequant_pages(const int* items, int num_items, const int* 
   return cudaGetLastError();
 }
 
-cudaError_t launch_kv_expand_seen(const int* items, int num_items, int kind, bool by_head, const KVPool8& src, int max_pages,
+cudaError_t launch_kv_expand_seen(const int* items, int num_items, int places, int kind, bool by_head, const KVPool8& src, int max_pages,
                                   int num_pages, const int* cu, const int* ctx, int n_kv, int d_head, int window, int sinks,
                                   const KVExpansion& dst, int* status, cudaStream_t stream) {
   if (num_items <= 0) return cudaSuccess;
-  if (kind == kKvInt8 && !by_head) return cudaErrorNotSupported;
-  const int head_rows = by_head ? num_items * kPageSize : kPageSize, page_rows = by_head ? kPageSize : n_kv * kPageSize;
+  if (!by_head && (kind == kKvInt8 || places != num_items)) return cudaErrorNotSupported;
+  const int head_rows = by_head ? places * kPageSize : kPageSize, page_rows = by_head ? kPageSize : n_kv * kPageSize;
   if (d_head != 64 && d_head != 128) return cudaErrorNotSupported;
   auto run = [&](auto kernel) {
     return launch_pdl(kernel, dim3(num_items), dim3(256), 0, stream, items, src, max_pages, num_pages, cu, ctx, n_kv, window,
-                      sinks, dst, head_rows, page_rows, status);
+                      sinks, dst, head_rows, page_rows, places, status);
   };
   if (d_head == 128) return kind == kKvInt8 ? run(kv_expand_seen_kernel<128, true>) : run(kv_expand_seen_kernel<128, false>);
   return kind == kKvInt8 ? run(kv_expand_seen_kernel<64, true>) : run(kv_expand_seen_kernel<64, false>);

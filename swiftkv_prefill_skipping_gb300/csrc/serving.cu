@@ -107,29 +107,24 @@ void cut_units(const std::vector<int>& item_ids, const std::vector<Ranges>& seen
   }
 }
 
-// (sequence, page) pairs of the pages some row of the chunk sees.
+// (sequence, page, place) of the pages some row of the chunk sees.
 void list_pages(int s, int c0, int n, int window, int sinks, std::vector<int>* out) {
   const Ranges r = seen_ranges(c0, n, window, sinks);
   int next = 0;
   for (int i = 0; i < r.n; ++i)
     for (int p = std::max(next, r.k0[i] / kPageSize); p < (r.k1[i] + kPageSize - 1) / kPageSize; ++p) {
-      out->push_back(s);
-      out->push_back(p);
+      out->insert(out->end(), {s, p, (int)(out->size() / 3)});
       next = p + 1;
     }
 }
 
-// (sequence, page) pairs of the blocks of `bkv` keys that hold a page some row of the chunk sees, in BlockOrder's order;
-// pages nobody sees as -1.
-void list_blocks(int s, int c0, int n, int window, int sinks, int bkv, std::vector<int>* out) {
+// The same in blocks of `bkv` keys that hold such a page, in BlockOrder's order: all pages of a block take a place.
+void list_blocks(int s, int c0, int n, int window, int sinks, int bkv, int* places, std::vector<int>* out) {
   const BlockOrder o(c0, n, window, sinks, bkv);
   const TailPages t = tail_pages(c0, n, window, sinks);
   auto put_block = [&](int b) {
-    for (int p = b * (bkv / kPageSize); p < (b + 1) * (bkv / kPageSize); ++p) {
-      const int k0 = p * kPageSize;
-      out->push_back(s);
-      out->push_back(k0 < t.sinks || (k0 + kPageSize > t.first && k0 < t.end) ? p : -1);
-    }
+    for (int p = b * (bkv / kPageSize); p < (b + 1) * (bkv / kPageSize); ++p, ++*places)
+      if (t.page_seen(p)) out->insert(out->end(), {s, p, *places});
   };
   for (int b = 0; b < o.sinks; ++b) put_block(b);
   for (int b = o.rest; b < o.end; ++b) put_block(b);
@@ -233,14 +228,14 @@ void place_expansion(const swiftkv_model* m, Arena* a, int pages, const Batch& b
 }
 
 int expand(swiftkv_model* m, const swiftkv_kv_pages* kv, int c, const Batch& b, const int* items, int num,
-           const int* cu, const int* ctx, bool by_head, const KVExpansion& e, cudaStream_t s) {
+           int places, const int* cu, const int* ctx, bool by_head, const KVExpansion& e, cudaStream_t s) {
   KVPool8 src;
   src.k = static_cast<const uint8_t*>(kv->k_pool[c]);
   src.v = static_cast<const uint8_t*>(kv->v_pool[c]);
   src.k_scale = static_cast<const float*>(kv->k_scale[c]);
   src.v_scale = static_cast<const float*>(kv->v_scale[c]);
   src.block_table = kv->block_table;
-  CK(launch_kv_expand_seen(items, num, b.kind, by_head, src, b.max_pages, kv->num_pages, cu, ctx, m->cfg.n_kv, m->cfg.d_head, b.window,
+  CK(launch_kv_expand_seen(items, num, places, b.kind, by_head, src, b.max_pages, kv->num_pages, cu, ctx, m->cfg.n_kv, m->cfg.d_head, b.window,
                            b.sinks, e, m->status, s));
   return SWIFTKV_OK;
 }
@@ -331,8 +326,9 @@ int AttendPlan::make(const swiftkv_model* m, const int32_t* cu, const int32_t* c
     }
     for (int t = 0; t < (n + tile_rows - 1) / tile_rows; ++t) tiles.push_back((i << 16) | t);
     if (b.kind != kKvBf16) {
-      first[i] = (int)(exp_items.size() / 2);
-      list_blocks(i, c0, n, b.window, b.sinks, chunk_block(c.d_head), &exp_items);
+      first[i] = places;
+      list_blocks(i, c0, n, b.window, b.sinks, chunk_block(c.d_head), &places, &exp_items);
+      if (places >= 1 << 27) return fail(SWIFTKV_EUNSUPPORTED, "batch too large");
     }
   }
   // heaviest first: the keys that a tile's last row sees
@@ -363,7 +359,7 @@ int AttendPlan::make(const swiftkv_model* m, const int32_t* cu, const int32_t* c
     cut_units(ids, seen, c.n_kv, (long long)m->num_sms * (b.kind != kKvBf16 ? kRowsWarps8 : kRowsWarps), &units, &ubeg);
   num_items = (int)ids.size();
   num_units = (int)(units.size() / 3);
-  num_exp = (int)(exp_items.size() / 2);
+  num_exp = (int)(exp_items.size() / 3);
   // offsets into the lists and the kernels' item counts are ints
   if (std::max({units.size(), tiles.size(), exp_items.size()}) >= (size_t)1 << 28 ||
       (long long)num_units * c.n_kv >= (1LL << 31) || (long long)num_tiles * c.n_q >= (1LL << 31))
@@ -393,7 +389,7 @@ void AttendPlan::place(const swiftkv_model* m, Arena* a) {
   v_tail = nullptr;
   if (num_tiles > 0 && b.kind == kKvBf16)
     v_tail = a->take<bf16>((size_t)b.P * kTailSlots * c.n_kv * kPageSize * c.d_head);
-  place_expansion(m, a, num_exp, b, true, &exp);
+  place_expansion(m, a, places, b, true, &exp);
 }
 
 int AttendPlan::upload(cudaStream_t s) const {
@@ -419,14 +415,14 @@ int AttendPlan::run(swiftkv_model* m, const swiftkv_kv_pages* kv, int c, const b
     t.cu = dev + o_cu;
     t.ctx = dev + o_ctx;
     if (b.kind != kKvBf16) {
-      RET(expand(m, kv, c, b, dev + o_exp, num_exp, t.cu, t.ctx, true, exp, s));
+      RET(expand(m, kv, c, b, dev + o_exp, num_exp, places, t.cu, t.ctx, true, exp, s));
       t.exp_first = dev + o_first;
       k = exp.k;
       v = exp.v;
       t.k_scale = exp.k_scale;
       t.v_scale = exp.v_scale;
       t.bt = nullptr;
-      t.num_pages = num_exp;
+      t.num_pages = places;
     } else {
       CK(launch_v_tail(v, t.bt, b.max_pages, t.num_pages, t.cu, t.ctx, b.P, g.n_kv, g.d_head, b.window, b.sinks, v_tail, s));
       t.v_tail = v_tail;
@@ -526,7 +522,7 @@ int WeightsPlan::make(const swiftkv_model* m, const int32_t* cu, const int32_t* 
   }
   num_units = (int)(units.size() / 3);
   num_tiles = (int)(tiles.size() / 2);
-  num_exp = (int)(exp_items.size() / 2);
+  num_exp = (int)(exp_items.size() / 3);
   if (std::max({units.size(), tiles.size(), exp_items.size()}) >= (size_t)1 << 28 ||
       (long long)num_units * c.n_kv >= (1LL << 31) || (long long)num_tiles * c.n_kv >= (1LL << 31))
     return fail(SWIFTKV_EUNSUPPORTED, "batch too large");
@@ -581,7 +577,7 @@ int WeightsPlan::run(swiftkv_model* m, const swiftkv_kv_pages* kv, int c, const 
                             num_units, m->num_sms, s);
   if (e == cudaSuccess && num_tiles > 0) {
     if ((b.kind == kKvFp8)) {
-      RET(expand(m, kv, c, b, dev + o_exp, num_exp, dev + o_cu, dev + o_ctx, false, exp, s));
+      RET(expand(m, kv, c, b, dev + o_exp, num_exp, num_exp, dev + o_cu, dev + o_ctx, false, exp, s));
       e = launch_weights_tc(a, exp.k, exp.k_scale, exp.block_table, num_exp, g.d_head, dev + o_tiles, num_tiles,
                             m->num_sms, s);
     } else {

@@ -28,6 +28,10 @@ struct TailPages {
   int page[kTailSlots];  // page index within the sequence, -1: none
   int first, end, sinks;
   __host__ __device__ bool seen(int key) const { return key < end && (key >= first || key < sinks); }
+  __host__ __device__ bool page_seen(int p) const {  // page p holds a key that some row sees
+    const int k0 = p * kPageSize;
+    return k0 < sinks || (k0 + kPageSize > first && k0 < end);
+  }
 };
 __host__ __device__ __forceinline__ TailPages tail_pages(int c0, int n, int window, int sinks) {
   TailPages t;
@@ -43,13 +47,14 @@ cudaError_t launch_v_tail(const bf16* v_pool, const int* block_table, int max_pa
                           const int* ctx, int P, int n_kv, int d_head, int window, int sinks, bf16* out,
                           cudaStream_t stream);
 // An 8-bit cache, and a dense bf16 copy of the pages a call needs: codes as bf16 values, scales beside them,
-// rows that no row of the sequence's chunk sees as zeros. Item i = (sequence, page index), page -1: zeros,
-// becomes page i of the copy. Dense and per sequence, so that sequences may share pages and the copy is no larger than
-// what is read. by_head: the copy is [n_kv][items][16][d_head], a head's pages neighbours, so that one TMA copy takes
-// a block of them; else [items][n_kv][16][d_head], and `block_table`, of the same shape as src's, names its pages.
+// rows that no row of the sequence's chunk sees as zeros. An item (sequence, page index, place)
+// becomes the page at that place of the copy; places ascend, and those of `places` that no item names get scales that
+// do no harm and nothing else. Dense and per sequence, so that sequences may share pages and the copy is no larger than
+// what is read. by_head: the copy is [n_kv][places][16][d_head], a head's pages neighbours, so that one TMA copy takes
+// a block of them; else [places][n_kv][16][d_head], every place an item's, and `block_table`, of the same shape as src's, names its pages.
 // FP8: scales [...][16] likewise. Value scales are copied times kValueShift, which whoever multiplies P by them takes
 // back: P times a scale goes to bf16, and value scales near float32's smallest would end up among bf16's subnormals.
-// int8 (by_head): k_scale alone, [n_kv][items] records of a float4: the key scale times log2(e) / sqrt(d_head); lv,
+// int8 (by_head): k_scale alone, [n_kv][places] records of a float4: the key scale times log2(e) / sqrt(d_head); lv,
 // the binary logarithm of the value scale times kPageShift, by which exp2's argument rises so that P carries the
 // value scale; 2^-lv; 0. This shift keeps P above float32's smallest for scales down to theirs; scales have to
 // stay below 2^64.
@@ -65,7 +70,7 @@ struct KVExpansion {
   float *k_scale, *v_scale;
   int* block_table;
 };
-cudaError_t launch_kv_expand_seen(const int* items, int num_items, int kind, bool by_head, const KVPool8& src, int max_pages,
+cudaError_t launch_kv_expand_seen(const int* items, int num_items, int places, int kind, bool by_head, const KVPool8& src, int max_pages,
                                   int num_pages, const int* cu, const int* ctx, int n_kv, int d_head, int window, int sinks,
                                   const KVExpansion& dst, int* status, cudaStream_t stream);
 
@@ -145,7 +150,8 @@ struct AttendPlan {
   std::vector<int> ints;
   int o_cu = 0, o_ctx = 0, o_tiles = 0, o_items = 0, o_units = 0, o_ubeg = 0, o_exp = 0, o_first = 0, o_merges = 0;
   int num_slots = 0, num_merges = 0;
-  int num_tiles = 0, num_items = 0, max_cols = 0, num_units = 0, num_exp = 0;
+  int num_tiles = 0, num_items = 0, max_cols = 0, num_units = 0;
+  int num_exp = 0, places = 0;  // pages of the expansion, and places for them
   // device (lists: null where the kernels take them inline)
   int* dev = nullptr;
   float *part = nullptr, *tile_part = nullptr;
