@@ -375,6 +375,8 @@ __device__ __forceinline__ void expand_codes8(uint2 raw, uint32_t* o) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) o[i] = all[i];
 }
+// The largest power of two that is no larger than x (x >= float32's smallest normal number; 0: 0).
+__device__ __forceinline__ float power_below(float x) { return __uint_as_float(__float_as_uint(x) & 0x7f800000u); }
 __device__ __forceinline__ void expand_int8x8(uint2 raw, uint32_t* o) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -415,23 +417,18 @@ __global__ void __launch_bounds__(256) kv_expand_seen_kernel(const int* __restri
   constexpr int U = 8;
   for (int c0 = threadIdx.x; c0 < total; c0 += U * 256) {
     uint2 codes[U];
-    float value_scale[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int c = c0 + u * 256, e = c < chunks ? c : c - chunks;
       codes[u] = make_uint2(0, 0);
-      value_scale[u] = 1.f;
-      if (c < total && ok && t.seen(pidx * kPageSize + e / per_row % kPageSize)) {
+      if (c < total && ok && t.seen(pidx * kPageSize + e / per_row % kPageSize))
         codes[u] = *reinterpret_cast<const uint2*>((c < chunks ? k : v) + (size_t)e * 8);
-        if (INT8 && c >= chunks) value_scale[u] = src.v_scale[(size_t)page * n_kv + e / per_row / kPageSize];
-      }
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int c = c0 + u * 256, e = c < chunks ? c : c - chunks, row = e / per_row;
       if (c >= total) break;
       uint32_t o[4];  // (codes of 0 are zeros in both)
-      if (value_scale[u] == 0.f) codes[u] = make_uint2(0, 0);  // its logarithm below is 0: P does not carry it
       if (INT8) expand_int8x8(codes[u], o);
       else expand_codes8(codes[u], o);
       const size_t to = (size_t)(row / kPageSize) * head_rows + (size_t)i * page_rows + row % kPageSize;
@@ -440,13 +437,35 @@ __global__ void __launch_bounds__(256) kv_expand_seen_kernel(const int* __restri
   }
   if constexpr (INT8) {
     // no key scale is 0: it would turn scores of -inf into NaN (for a page's of 0 the smallest, whose scores round away)
+    bool small = false;
     for (int c = threadIdx.x; c < (until - from) * n_kv; c += blockDim.x) {
       const int at = from + c / n_kv, h = c % n_kv;
       const bool mine = ok && at == i;
       const float ks = mine ? src.k_scale[(size_t)page * n_kv + h] : 0.f, vs = mine ? src.v_scale[(size_t)page * n_kv + h] : 0.f;
       const float kc = fmaxf(ks * (1.4426950408889634f / sqrtf((float)dh)), 1.4e-45f), vc = vs * kPageShift;
-      const float lv = vc > 0.f ? log2f(vc) : 0.f;
+      small |= mine && vc < 1.f;
+      const float lv = vc >= 1.f ? log2f(vc) : vc > 0.f ? log2f(vc / power_below(vc)) : 0.f;
       reinterpret_cast<float4*>(dst.k_scale)[(size_t)h * (head_rows / kPageSize) + at] = make_float4(kc, lv, exp2f(-lv), 0.f);
+    }
+    // Value scales below 1 / kPageShift, 0 among them: P carries what is above a power of two, the copy's values that
+    // power (exactly; 0 makes them zeros). With all of it on P, weights would fall below float32's smallest, out of
+    // their sum as well. The same page's values are written again, after the loop above.
+    if (__syncthreads_or(small)) {
+      for (int c = threadIdx.x; c < chunks; c += blockDim.x) {
+        const int row = c / per_row;
+        const float vc = src.v_scale[(size_t)page * n_kv + row / kPageSize] * kPageShift;
+        if (vc >= 1.f || !t.seen(pidx * kPageSize + row % kPageSize)) continue;
+        const __nv_bfloat162 by = __float2bfloat162_rn(power_below(vc));
+        uint32_t o[4];
+        expand_int8x8(*reinterpret_cast<const uint2*>(v + (size_t)c * 8), o);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const __nv_bfloat162 y = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&o[e]), by);
+          o[e] = *reinterpret_cast<const uint32_t*>(&y);
+        }
+        const size_t to = (size_t)(row / kPageSize) * head_rows + (size_t)i * page_rows + row % kPageSize;
+        *reinterpret_cast<uint4*>(dst.v + to * dh + c % per_row * 8) = make_uint4(o[0], o[1], o[2], o[3]);
+      }
     }
   } else {
     const int scales = dst.v ? 2 * rows : rows;

@@ -56,8 +56,9 @@ cudaError_t launch_v_tail(const bf16* v_pool, const int* block_table, int max_pa
 // back: P times a scale goes to bf16, and value scales near float32's smallest would end up among bf16's subnormals.
 // int8 (by_head): k_scale alone, [n_kv][places] records of a float4: the key scale times log2(e) / sqrt(d_head); lv,
 // the binary logarithm of the value scale times kPageShift, by which exp2's argument rises so that P carries the
-// value scale; 2^-lv; 0. This shift keeps P above float32's smallest for scales down to theirs; scales have to
-// stay below 2^64.
+// value scale; 2^-lv; 0. Where that product is below 1, lv is what it has above a power of two and the copy's values
+// carry that power, so that lv is never negative and P as far from float32's smallest as it is without it. Scales have
+// to stay below 2^64.
 constexpr float kValueShift = 65536.f;
 constexpr float kPageShift = 268435456.f;
 struct KVPool8 {

@@ -132,6 +132,16 @@ def test_pages_of_any_size(heads, new, ctx):
     Case(heads, new, ctx, seed=36, kmul=(0.0,)).check()
 
 
+@pytest.mark.parametrize("mul", [2.0 ** -60, 2.0 ** -100, 2.0 ** -126, 2.0 ** -135])
+@pytest.mark.parametrize("heads", ["gqa4", "gqa5", "d64"])
+@pytest.mark.parametrize("new", [[16], [17], [130]])
+def test_weights_of_pages_with_tiny_values_count(heads, new, mul):
+    """Thousands of keys whose weights are small and whose values are next to nothing, behind a page of ordinary ones: their
+    share of the sum is not lost, whatever their scale."""
+    n = 600
+    Case(heads, new, [16 * n], seed=38, vmul=(1.0,) + (mul,) * (n + 20), low=range(1, n + 20)).check()
+
+
 @pytest.mark.parametrize("heads", ["gqa4", "gqa5", "d64"])
 @pytest.mark.parametrize("new", [[16], [17], [300, 3]])
 def test_pages_cleared_by_a_scale_of_zero(heads, new):
