@@ -346,7 +346,8 @@ __global__ void __launch_bounds__(THREADS, 1) attn_chunk_kernel(const __grid_con
             const int st = is_v ? kv_i % VST : kv_i % KST, page = page0 + order.place(block) * PAGES;
             // Pages that no row sees have a place in the expansion, but nothing in it: K of such a page may be anything,
             // its scores are masked, and V of a block with some comes page by page, zeros from past the end for them
-            const bool seen = lane >= PAGES || tail.page_seen(block * PAGES + lane), whole = !is_v || __all_sync(0xffffffffu, seen);
+            // (told from the block's ends: a vote of the lanes cost 4 of 404 us)
+            const bool whole = !is_v || tail.pages_seen(block * PAGES, block * PAGES + PAGES - 1);
             const uint32_t ph = (uint32_t)((is_v ? kv_i / VST : kv_i / KST) & 1);
             const uint32_t full = is_v ? bar(ctl->v_full[st]) : bar(ctl->k_full[st]);
             if (!(ok = wait_all(is_v ? bar(ctl->v_empty[st]) : bar(ctl->k_empty[st]), ph ^ 1))) break;
@@ -381,7 +382,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_chunk_kernel(const __grid_con
             }
             __syncwarp();
             if (!whole && lane < PAGES) {
-              const int row = (seen ? page + lane : a.num_pages * a.n_kv) * kPageSize;
+              const int row = (tail.page_seen(block * PAGES + lane) ? page + lane : a.num_pages * a.n_kv) * kPageSize;
 #pragma unroll
               for (int hf = 0; hf < C::HALVES; ++hf)
                 tma_load_2d(sV + st * C::KV_TILE + hf * C::KV_HALF + lane * 2048, &tmTail, hf * 64, row, full);

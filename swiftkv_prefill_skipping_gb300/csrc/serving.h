@@ -28,10 +28,10 @@ struct TailPages {
   int page[kTailSlots];  // page index within the sequence, -1: none
   int first, end, sinks;
   __host__ __device__ bool seen(int key) const { return key < end && (key >= first || key < sinks); }
-  __host__ __device__ bool page_seen(int p) const {  // page p holds a key that some row sees
-    const int k0 = p * kPageSize;
-    return k0 < sinks || (k0 + kPageSize > first && k0 < end);
+  __host__ __device__ bool pages_seen(int p, int q) const {  // pages p .. q all hold such keys, all of the sinks or all behind them
+    return q * kPageSize < sinks || ((p + 1) * kPageSize > first && q * kPageSize < end);
   }
+  __host__ __device__ bool page_seen(int p) const { return pages_seen(p, p); }  // page p holds a key that some row sees
 };
 __host__ __device__ __forceinline__ TailPages tail_pages(int c0, int n, int window, int sinks) {
   TailPages t;
