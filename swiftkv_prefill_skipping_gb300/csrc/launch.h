@@ -31,6 +31,18 @@ inline cudaError_t set_max_dynamic_smem(const void* func, int bytes, PerDeviceOn
   return e;
 }
 
+// Whether `rows` rows of wa bytes, lda bytes apart (no less than wa), share a byte with rows of wb, ldb apart: parts
+// of one wider buffer's rows do not. Rows of different strides count as meeting where their ranges do.
+inline bool rows_meet(const void* a, long long lda, long long wa, const void* b, long long ldb, long long wb, long long rows) {
+  const long long d = (long long)(reinterpret_cast<uintptr_t>(b) - reinterpret_cast<uintptr_t>(a));
+  if (rows < 1 || d >= (rows - 1) * lda + wa || -d >= (rows - 1) * ldb + wb) return false;
+  if (lda != ldb || rows == 1) return true;
+  // b's row i starts `rest` bytes into a's row i + down, and may reach into the next
+  const long long down = d >= 0 ? d / lda : -((-d + lda - 1) / lda), rest = d - down * lda;
+  const long long next = down + 1;
+  return (down < rows && -down < rows && rest < wa) || (next < rows && -next < rows && rest + wb > lda);
+}
+
 // Records `msg` as the calling thread's swiftkv_last_error() and returns `code`.
 int set_error(int code, const char* msg);
 

@@ -689,6 +689,12 @@ int swiftkv_append(swiftkv_model* m, int cache, int caches, const swiftkv_new_ro
       const size_t qn = ((size_t)(b.T - 1) * rows->ldq + m->Nq) * 2, on = ((size_t)(b.T - 1) * rows->ldq_out + m->Nq) * 2;
       if (qa < oa + on && oa < qa + qn && !(qa == oa && (rows->ldq == rows->ldq_out || b.T == 1)))
         return fail(SWIFTKV_EINVAL, "q_out overlaps q without being it");
+      for (int i = 0; i < caches; ++i) {  // other warps read them while these are written
+        const bf16 *ki = static_cast<const bf16*>(rows->k) + i * rows->k_step, *vi = static_cast<const bf16*>(rows->v) + i * rows->v_step;
+        if (rows_meet(rows->q_out, 2LL * rows->ldq_out, 2LL * m->Nq, ki, 2LL * rows->ldk, 2 * Nkv, b.T) ||
+            rows_meet(rows->q_out, 2LL * rows->ldq_out, 2LL * m->Nq, vi, 2LL * rows->ldv, 2 * Nkv, b.T))
+          return fail(SWIFTKV_EINVAL, "q_out overlaps k or v");
+      }
     }
     OnDevice on_device(m);
     cudaStream_t s = (cudaStream_t)stream;

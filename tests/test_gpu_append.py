@@ -395,6 +395,41 @@ def test_refusals():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("T", [1, 3])
+def test_q_out_over_k_or_v_is_refused(T):
+    """Rows of q_out are written while other warps read K and V: a view that reaches into theirs, by one head at
+    either end or in another token's row, is refused; parts beside them are not."""
+    import torch
+    from swiftkv_prefill_skipping_gb300 import api
+    c = Case("gqa4", [T], [0], "int8", caches=2)
+    Q, K = c.n_q, c.n_kv
+    W = 2 * Q + 4 * K
+    # a row: room for q, K of both caches, V of both, room for q again
+    wide = torch.zeros(T + 2, W, c.d, dtype=torch.bfloat16, device="cuda")
+    rows = wide[1:-1]
+    k, v = rows[:, Q:Q + 2 * K].unflatten(1, (2, K)), rows[:, Q + 2 * K:Q + 4 * K].unflatten(1, (2, K))
+    k.copy_(c.k)
+    v.copy_(c.v)
+    q = c.q.cuda()
+    flat, row = wide.flatten(), wide.stride(0)
+
+    def at(head):  # q_out that starts `head` heads into the rows
+        return flat.as_strided((T, Q, c.d), (row, c.d, 1), row + head * c.d)
+
+    apart, over = [0, Q + 4 * K], [1, Q, Q + K + 1, Q + 4 * K - 1]
+    (over if T > 1 else apart).extend((W + 1, 1 - W))  # over the neighbouring tokens' rows
+    for head in over:
+        with pytest.raises(B.SwiftKVError, match="q_out overlaps k or v"):
+            api.append(c.model, k, v, c.cu, c.ctx, c.kv, q=q, q_out=at(head))
+    torch.cuda.synchronize()
+    assert all(torch.equal(getattr(c.kv, n).cpu(), c.before[n]) for n in c.names())
+    for head in apart:
+        out = api.append(c.model, k, v, c.cu, c.ctx, c.kv, q=q, q_out=at(head))
+        c.check(out)
+        assert torch.equal(k.cpu(), c.k) and torch.equal(v.cpu(), c.v)
+
+
+@pytest.mark.gpu
 def test_int8_caches_elsewhere_are_refused():
     import torch
     from swiftkv_prefill_skipping_gb300 import api
