@@ -685,9 +685,8 @@ int swiftkv_append(swiftkv_model* m, int cache, int caches, const swiftkv_new_ro
     if (rows->q) {
       RET(check_rows(m, rows->q, rows->ldq, "q"));
       RET(check_rows(m, rows->q_out, rows->ldq_out, "q_out"));
-      const char *qa = static_cast<const char*>(rows->q), *oa = static_cast<const char*>(rows->q_out);
-      const size_t qn = ((size_t)(b.T - 1) * rows->ldq + m->Nq) * 2, on = ((size_t)(b.T - 1) * rows->ldq_out + m->Nq) * 2;
-      if (qa < oa + on && oa < qa + qn && !(qa == oa && (rows->ldq == rows->ldq_out || b.T == 1)))
+      if (!(rows->q == rows->q_out && (rows->ldq == rows->ldq_out || b.T == 1)) &&
+          rows_meet(rows->q, 2LL * rows->ldq, 2LL * m->Nq, rows->q_out, 2LL * rows->ldq_out, 2LL * m->Nq, b.T))
         return fail(SWIFTKV_EINVAL, "q_out overlaps q without being it");
       for (int i = 0; i < caches; ++i) {  // other warps read them while these are written
         const bf16 *ki = static_cast<const bf16*>(rows->k) + i * rows->k_step, *vi = static_cast<const bf16*>(rows->v) + i * rows->v_step;

@@ -218,6 +218,25 @@ def test_strided_rows_q_in_place_and_another_stream(kind):
 
 
 @pytest.mark.gpu
+def test_q_out_beside_q_in_wider_rows():
+    """The turned q in the same rows as q itself, before or behind it."""
+    import torch
+    from swiftkv_prefill_skipping_gb300 import api
+    c = Case("gqa5", [5, 1, 17], [14, 15, 0], "bf16", seed=17)
+    for first, second in ((0, c.n_q), (c.n_q + 1, 1)):
+        rows = torch.full((c.T, 2 * c.n_q + 1, c.d), 9.0, dtype=torch.bfloat16, device="cuda")
+        q, out = rows[:, first:first + c.n_q], rows[:, second:second + c.n_q]
+        q.copy_(c.q)
+        k, v = c.args()
+        assert api.append(c.model, k, v, c.cu, c.ctx, c.kv, q=q, q_out=out) is out
+        torch.cuda.synchronize()
+        c.check(out)
+        assert torch.equal(q.cpu(), c.q)
+        with pytest.raises(B.SwiftKVError, match="overlaps q"):
+            api.append(c.model, k, v, c.cu, c.ctx, c.kv, q=q, q_out=rows[:, 1:1 + c.n_q] if first == 0 else rows[:, 2:2 + c.n_q])
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("kind", ["bf16", "int8"])
 def test_more_sequences_than_the_parameters_hold(kind):
     new = [(7 * i) % 4 for i in range(700)]
