@@ -266,9 +266,7 @@ extern "C" int swiftkv_adjust_logits(const float* logits, int rows, int vocab, l
   if (a->num_bias > kMaxBias) return set_error(SWIFTKV_EUNSUPPORTED, "more than 2046 biases a row");
   if (vocab > (1 << 30)) return set_error(SWIFTKV_EUNSUPPORTED, "vocab above 2^30");
   if (rows > (1 << 27)) return set_error(SWIFTKV_EUNSUPPORTED, "more than 2^27 rows");
-  const uintptr_t i0 = reinterpret_cast<uintptr_t>(logits), i1 = i0 + ((size_t)(rows - 1) * ld + vocab) * 4;
-  const uintptr_t o0 = reinterpret_cast<uintptr_t>(out), o1 = o0 + ((size_t)(rows - 1) * ld_out + vocab) * 4;
-  if (i0 < o1 && o0 < i1 && !(i0 == o0 && (ld == ld_out || rows == 1)))
+  if (!(logits == out && (ld == ld_out || rows == 1)) && rows_meet(logits, 4 * ld, 4LL * vocab, out, 4 * ld_out, 4LL * vocab, rows))
     return set_error(SWIFTKV_EINVAL, "out overlaps logits without being them");
   AdjustParams p;
   p.logits = logits;
@@ -293,7 +291,8 @@ extern "C" int swiftkv_adjust_logits(const float* logits, int rows, int vocab, l
   p.num_bias = a->num_bias;
   p.mask = a->mask;
   p.ld_mask = a->ld_mask;
-  const bool vec = ((i0 | o0) & 15) == 0 && (rows == 1 || (ld % 4 == 0 && ld_out % 4 == 0));
+  const bool vec = ((reinterpret_cast<uintptr_t>(logits) | reinterpret_cast<uintptr_t>(out)) & 15) == 0 &&
+                   (rows == 1 || (ld % 4 == 0 && ld_out % 4 == 0));
   // Short slices while there are few rows, so that every SM has work; long ones walk a history less often.
   const bool half = hist && !bias && a->max_tokens <= (int)kHalfCount;
   const long long ids = (long long)rows * vocab, want = (ids / kTargetBlocks + 1023) / 1024 * 1024;

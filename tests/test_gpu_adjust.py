@@ -124,6 +124,24 @@ def test_rows_of_a_wider_buffer(pad, offset):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("vocab,gap", [(4099, 0), (4100, 0), (70001, 3)])
+def test_out_beside_the_logits_in_wider_rows(vocab, gap):
+    """Logits and results as parts of the same rows: apart from each other, though their ranges are not."""
+    import torch
+    from swiftkv_prefill_skipping_gb300 import api
+    c = Case(5, vocab, 60, 5, 0.7, seed=3)
+    args = {k: v.cuda() for k, v in c.kw.items()}
+    for x_at, out_at in ((0, vocab + gap), (vocab + gap, 0)):
+        wide = torch.full((5, 2 * vocab + gap), 7.0, device="cuda")
+        x, out = wide[:, x_at:x_at + vocab], wide[:, out_at:out_at + vocab]
+        x.copy_(c.logits)
+        c.check(api.adjust_logits(x, out=out, **args).cpu().numpy())
+        assert torch.equal(x.cpu(), c.logits) and bool((wide[:, vocab:vocab + gap] == 7).all())
+        with pytest.raises(B.SwiftKVError, match="overlaps"):
+            api.adjust_logits(x, out=wide[:, gap + 1:gap + 1 + vocab], **args)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("first,more", [(0, 1), (1, 3), (4, 4), (3, 1)])
 def test_lists_that_are_parts_of_wider_ones(first, more):
     """Histories and masks whose rows start anywhere and have other words before and behind them."""
