@@ -248,7 +248,8 @@ int swiftkv_decode_step(swiftkv_model* m, const int32_t* tokens, const int32_t* 
  * accumulate in float32. The order in which a short chunk's keys are summed depends on the call's other chunks, so
  * its last bits may; a longer one's do not, but over an int8 cache in calls of few of them. Value scales have
  * to stay below 2^95 (FP8) or 2^64 (int8), q over an 8-bit cache below 2^100 in longer chunks, and a page's
- * int8 scales finite where any of its rows is visible.
+ * int8 scales finite and not negative where any of its rows is visible (0: the page's rows are zeros, whatever
+ * their codes).
  * swiftkv_set_attention_impl does not concern this call. */
 int swiftkv_attend(swiftkv_model* m, int cache, const void* q, int ldq, const int32_t* cu_seqlens,
                    const int32_t* ctx_lens, int num_seqs, const swiftkv_kv_pages* kv, int window, int sinks,
@@ -275,11 +276,12 @@ typedef struct {
  * An FP8 cache takes the scale and codes of the bf16 values, as in the model's own calls. On an int8 cache
  * a page's scale is max|x| / 127 over the new rows, NaN left out and infinities as the largest bf16; where
  * the page holds rows before them, it is the larger of that and the page's, and if it grows the earlier rows'
- * codes become round(code * old / new), half a step of the new scale off at most. Codes are round(x / scale), 0
- * for NaN. The codes thus depend on how a page's tokens were split into calls. What is in a page behind
+ * codes become round(code * old / new). Each growth rounds the codes of the one before: half a step of the new
+ * scale at most, which adds up over later ones, up to 15 on a page that is filled a token at a time. Codes are
+ * round(x / scale), 0 for NaN, and thus depend on how a page's tokens were split into calls. What is in a page behind
  * the new rows is not kept up: its codes stay and its scale may change.
  * No two chunks of a call may write to the same row; on an int8 cache not to the same page. Rows before and behind
- * a chunk's own stay as they are. An entry outside [0, num_pages) sets SWIFTKV_STATUS_BAD_PAGE, and its rows are
+ * a chunk's own stay as they are, on an int8 cache but for those of its first and last page, as above. An entry outside [0, num_pages) sets SWIFTKV_STATUS_BAD_PAGE, and its rows are
  * skipped (their q is rotated all the same). */
 int swiftkv_append(swiftkv_model* m, int cache, int caches, const swiftkv_new_rows* rows, const int32_t* cu_seqlens,
                    const int32_t* ctx_lens, const int32_t* pos_offsets, int num_seqs, const swiftkv_kv_pages* kv,

@@ -11,9 +11,11 @@
 //            step of the new scale each time.
 //
 // Bound by HBM: every row is read and written once, 4 chunks of ~1960 rows with q, 32 / 8 heads x 128, 193 MB, in 33 us;
-// 11703 rows of 8 caches, 767 MB, in 123; 24 tokens in 8.5, which is the launch and two trips to memory. Codes are bound
-// by instructions where there are few rows: K and V of 11703 rows, 72 MB, into FP8 or int8 in 23 us, into int8 of 8
-// caches, 575 MB, in 115. With a division for each value those were 41, 43 and 258. A lane owns 8 neighbouring dimensions and their
+// 11703 rows of 8 caches, 767 MB, in 123; 24 tokens in 8.5, which is the launch and two trips to memory. One cache's
+// codes are bound by latency: K and V of 11703 rows, 72 MB, go into FP8 or int8 in 23 us, 2.3 TB/s inside the kernel with
+// 0.55 instructions a cycle and scheduler and its warps waiting for loads: a warp reads its block, turns it, finds its
+// maximum and writes in series, and 2.4 rounds of warps hide little of that. Into int8 of 8 caches, 575 MB, the same
+// takes 115, 5.1 TB/s. With a division for each value those were 41, 43 and 258. A lane owns 8 neighbouring dimensions and their
 // partners half a head on, so a pair turns within a lane, all accesses are 16 bytes (8 for codes), and a
 // head is 8 lanes (4 at d_head 64).
 //   Rows (q; K and V of a bf16 or FP8 cache): a warp takes one token and steps through its heads with the

@@ -22,8 +22,8 @@
 // with 2^-8 of its value); a second product with the remainders would add half of the tensor work.
 // Row sums use the unrounded weights, in float32.
 //
-// 12 warps: 0 loads Q and K and 3 loads V by TMA, each with the page ids of a block read one block
-// ahead; 1 and 2 issue the tiles' MMAs (the warp converged, one elected lane); 4-7 and 8-11 are the
+// 12 warps: 0 loads Q and K (and the scales of 8-bit caches) and 3 loads V by TMA, over bf16 each with the page ids
+// of a block read one block ahead; 1 and 2 issue the tiles' MMAs (the warp converged, one elected lane); 4-7 and 8-11 are the
 // softmax of tile A and B, one thread per row, with the registers that the first four give up. All
 // mbarrier waits are bounded; when one expires the CTA flags kStatusTimeout, drains its copies and
 // MMAs, frees tensor memory and exits.
@@ -46,7 +46,9 @@
 //
 // Pages without a visible key are not loaded (zeros instead), and pages of V that the chunk sees in
 // part come from zero-padded copies (launch_v_tail). 8-bit caches: K and V are an expansion to bf16 codes, in which a
-// block of a sequence is one stretch per head, so that K or V of a block are two TMA copies and not two a page.
+// block of a sequence is one stretch per head, so that K or V of a block are two TMA copies and not two a page (V of a
+// block with pages that no row sees, the last of a short sequence for one, is two a page all the same: with zeros for
+// them in the expansion 200 FP8 chunks of 24 rows took 100 us, without 93).
 // Scores take the keys' scales and P the values' (times a power of two), both in float32. FP8 has one for each key: 80
 // products for each. int8 has one for each page: the key's goes into the multiply-add that every exponent needs
 // anyway, the value's logarithm into its addend, and the row sums, fused multiply-adds then, take it out again. What
@@ -305,8 +307,9 @@ __global__ void __launch_bounds__(THREADS, 1) attn_chunk_kernel(const __grid_con
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_ISSUE));
     if (warp == 0 || warp == 3) {
-      // warp 0: Q and K, warp 3: V and the scales. Lane p looks after page p of a block (one thread
-      // doing it for all pages, at a dependent instruction every few cycles, took longer than the block)
+      // warp 0: Q, K and, over an 8-bit cache, the blocks' scales, warp 3: V. Over bf16 lane p looks after page p of a
+      // block (one thread doing it for all pages, at a dependent instruction every few cycles, took longer than the
+      // block); over an 8-bit cache one lane copies a block, but for blocks of V with pages that no row sees
       const bool is_v = warp == 3;
       const int group = a.n_q / a.n_kv;
       // the lane's page id in block j of item X, loaded one block ahead of its use

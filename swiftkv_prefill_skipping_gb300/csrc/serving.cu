@@ -16,10 +16,17 @@ namespace {
 // short chunks after a long prefix leave SMs idle: one sequence, 32 / 8 heads x 128, bf16, 4 rows after
 // 16000 keys 37 us, 5 rows 176; 8 sequences 98 and 179.
 constexpr int kRowChunk = 4;
-// Over an int8 cache, by the same measure (us as rows / as tiles; 32 / 8 heads): 1 sequence, 5 / 8 / 16 rows after 16000 keys
-// 45 / 47 / 56 where tiles take 203; 8 sequences 139 / 140 / 258 against 325; 32 sequences, 5 / 8 / 16 rows after 4000 keys
-// 158 / 160 / 352 against 338, 16 rows after 300 keys 55 against 45. Past 16 rows rows win for few sequences only (32
-// rows: one 82 / 203, four 141 / 136), and the rule would have to look at the batch.
+// Over an int8 cache, where tiles are cut along their keys (cut_tiles), by the same measure. us as rows for 5 / 8 / 12 / 16
+// rows, and as tiles, for which these are all one:
+//                            32 / 8 heads               40 / 8 heads               64 / 8 heads
+//   1 sequence after 300     17 / 19 / 19 / 19    21    19 / 19 / 19 / 19    19    19 / 19 / 19 / 19    21
+//   1 after 16000            46 / 46 / 52 / 56    64    47 / 51 / 56 / 68    82    48 / 56 / 68 / 82    88
+//   8 after 300              19 / 21 / 21 / 23    23    21 / 21 / 23 / 27    29    21 / 23 / 27 / 31    29
+//   8 after 16000            138 / 140 / 207 / 259 328  139 / 205 / 259 / 430 580  203 / 259 / 431 / 570 504
+//   32 after 300             31 / 31 / 41 / 54    45    31 / 41 / 53 / 47    62    41 / 52 / 48 / 76    64
+//   32 after 4000            158 / 160 / 234 / 352 340  160 / 232 / 351 / 426 489  230 / 353 / 429 / 565 479
+// Rows take a pass over the keys for each 16 query heads and rows, so that the last of these 16 rows are dearer than a
+// tile at 4 heads a KV head with many short sequences (by 4 to 18 %) and at 8 with several sequences (7 to 23 %).
 constexpr int kRowChunkInt8 = 16;
 
 int check_batch(const swiftkv_model* m, const int32_t* cu, const int32_t* ctx, int P, const swiftkv_kv_pages* kv,
