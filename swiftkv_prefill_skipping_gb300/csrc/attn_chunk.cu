@@ -37,7 +37,7 @@
 // 4 chunks of ~1960 rows after 0 - 6048 keys, 32 / 8 heads x 128: 361 us, 1.42 PFLOP/s (392 called without
 // a pause, where the power cap lowers the clock); the same rows through a window of 1024 and 4 sinks:
 // 150 us. Those scores are nearly flat; with q 16 times as large, where sums outgrow the running maximum
-// more often, 454 us. FP8: 527 and 205 us, int8: 405 and 170 us, the expansion to bf16 among them (22 us of the 405).
+// more often, 454 us. FP8: 527 and 207 us, int8: 404 and 172 us, the expansion to bf16 among them (22 us of the 404).
 // Bound by the tensor core and the hand-overs to it: 337 us without any softmax. S of an 80-key block reads 6.5 KB of shared memory per 16 dims, 52 cycles
 // where the product takes 40, and a wider block does not fit beside P and O: with that the products
 // alone take 307 us. Measured and not kept: four softmax warpgroups on alternate 64-key blocks with P
