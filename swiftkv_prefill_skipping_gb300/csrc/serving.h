@@ -51,7 +51,8 @@ cudaError_t launch_v_tail(const bf16* v_pool, const int* block_table, int max_pa
 // becomes the page at that place of the copy; places ascend, and those of `places` that no item names get scales that
 // do no harm and nothing else. Dense and per sequence, so that sequences may share pages and the copy is no larger than
 // what is read. by_head: the copy is [n_kv][places][16][d_head], a head's pages neighbours, so that one TMA copy takes
-// a block of them; else [places][n_kv][16][d_head], every place an item's, and `block_table`, of the same shape as src's, names its pages.
+// a block of them; else [places][n_kv][16][d_head], every place an item's, and `block_table`, of the same shape as
+// src's, names its pages.
 // FP8: scales [...][16] likewise. Value scales are copied times kValueShift, which whoever multiplies P by them takes
 // back: P times a scale goes to bf16, and value scales near float32's smallest would end up among bf16's subnormals.
 // int8 (by_head): k_scale alone, [n_kv][places] records of a float4: the key scale times log2(e) / sqrt(d_head); lv,
